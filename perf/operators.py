@@ -171,8 +171,9 @@ def _run_own(st):
     form.update(key_lens=st["key_lens"], prefix_lens=st["prefix_lens"], doc_ids=st["doc_ids"])
     if c["op"] == "forward":
         return mha.sdpa_scored_forward(st["q"], st["k"], st["v"], **form)
-    o, lse = mha.sdpa_scored_forward_lse(st["q"], st["k"], st["v"], **form)
-    dq, dk, dv, dtable = mha.sdpa_scored_backward(st["q"], st["k"], st["v"], o, st["dout"], lse, **form)
+    o_lo = torch.empty_like(st["q"])
+    o, lse = mha.sdpa_scored_forward_lse(st["q"], st["k"], st["v"], out_lo=o_lo, **form)
+    dq, dk, dv, dtable = mha.sdpa_scored_backward(st["q"], st["k"], st["v"], o, st["dout"], lse, o_lo=o_lo, **form)
     return {"o": o, "dq": dq, "dk": dk, "dv": dv, "dtable": dtable}
 
 
