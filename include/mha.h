@@ -271,6 +271,124 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
                                const int32_t *cache_lens, cudaStream_t stream);
 
 /*
+ * Scored attention (bf16): attention whose scores are more than scale q.k,
+ *
+ *   z = scale q_i.k_j,  s = cap tanh(z / cap)  (cap > 0; else s = z),
+ *   s += bias_h(j - i),
+ *   o_i = sum_j softmax_j(s_ij) v_j   over the keys j that query i sees.
+ *
+ * The members of mha_score_form, each off when 0 / NULL (a NULL form: all
+ * off; the call is then sdpa_forward with shared K/V heads):
+ *   cap             caps |s| smoothly; >= 0, finite.
+ *   slopes          DEVICE fp32 (h): bias_h(d) = -slopes[h] |d|.
+ *   table           DEVICE bf16 (num_buckets, h), or (2 num_buckets, h) with
+ *                   `bidirectional`: bias_h(d) = table[bucket(d), h], a learned
+ *                   relative position bias.  At most one of slopes and table.
+ *   bucket_starts   HOST int32 (num_buckets), read during the call: the first
+ *                   distance of each bucket, [0] = 0, strictly ascending, the
+ *                   last at most 65536.  bucket(d) = the largest u with
+ *                   bucket_starts[u] <= |d| (plus num_buckets for d > 0) with
+ *                   `bidirectional`, else of max(-d, 0): a key past its query
+ *                   is in bucket 0.  1 <= num_buckets <= 64.
+ *   prefix_lens     DEVICE int32 (B), with a causal mask: keys
+ *                   j < prefix_lens[b] are seen by every query (a prompt read
+ *                   in both directions).  Any value; <= 0 is no prefix.
+ *   doc_ids         DEVICE int32 (B, T), T_q == T_k == T: a query sees only
+ *                   keys of its own id (documents packed into one row).  Ids
+ *                   do not decrease along a row (for ids that do, which keys
+ *                   are seen is unspecified; nothing is read or written out of
+ *                   range).
+ * All of them meet with `mask` and key_lens: a key must pass every one.  A query
+ * that sees no key outputs 0 (lse -inf, no gradient).
+ *
+ *   q, o (B, h, T_q, 64); k, v (B, h_kv, T_k, 64), h a multiple of h_kv: query
+ *   head i reads K/V head i / (h / h_kv).  16-byte aligned.  T_q, T_k < 2^24.
+ *   lse: fp32 (B, h, T_q), the log-sum-exp of the row's scores (natural log,
+ *   -inf for a query that sees no key), or NULL.  Unlike sdpa_forward_lse's it
+ *   sums the unrounded weights: an fp32 result.
+ *   o_lo: bf16 like o, what rounding took from o, or NULL; needs lse.  The
+ *   backward takes it so that its row terms carry no bf16 rounding, which
+ *   matters where a few keys dominate their rows.
+ *   workspace: >= sdpa_scored_workspace_bytes() bytes, 256-byte aligned (0
+ *   bytes, and NULL allowed, without table and doc_ids).
+ * K and V rows at or past key_lens[b] are never used, whatever they hold.
+ * One launch, and one before it that expands the table and finds the
+ * documents' ends where the form has them.  Two calls at once, in two streams
+ * or two captured graphs, need a workspace each.
+ */
+typedef struct {
+    float cap;
+    const float *slopes;
+    const void *table;
+    const int32_t *bucket_starts;
+    int num_buckets;
+    int bidirectional;
+    const int32_t *prefix_lens;
+    const int32_t *doc_ids;
+} mha_score_form;
+
+/* 0 for negative sizes or invalid buckets. */
+size_t sdpa_scored_workspace_bytes(int B, int h, int T_q, int T_k, const mha_score_form *form);
+mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const void *k, const void *v, void *o,
+                               float *lse, void *o_lo, void *workspace, size_t workspace_bytes,
+                               int B, int h, int h_kv, int T_q, int T_k, int d_k, int d_v, float scale,
+                               mha_mask mask, const int32_t *key_lens, const mha_score_form *form,
+                               int *status_dev, cudaStream_t stream);
+
+/*
+ * Gradients of sdpa_scored_forward from its output o (and o_lo, or NULL) and
+ * log-sum-exp lse:
+ *   dS = P (.) (dout v^T - rowsum(dout (.) (o + o_lo))),  P = exp(s - lse),
+ *   dz = dS (.) (1 - tanh^2(z / cap))  (dz = dS uncapped),
+ *   dv = P^T dout,  dq = scale dz k,  dk = scale dz^T q  (dk, dv summed over the
+ *   query heads of a K/V head),  dtable[u, h] = sum of dS over the pairs of
+ *   bucket u and all batch entries, bf16 like the table, or NULL.
+ * Shapes as the forward's; the same mask, lengths and form.  dk, dv and dtable
+ * are summed in a fixed order; dq adds key blocks by fp32 reductions in
+ * global memory whose order is not fixed, as sdpa_backward does, so equal calls
+ * may differ in dq's last bit.  workspace:
+ * >= sdpa_scored_backward_workspace_bytes() bytes, 256-byte aligned.
+ */
+size_t sdpa_scored_backward_workspace_bytes(int B, int h, int T_q, int T_k,
+                                            const mha_score_form *form);
+mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, const void *v,
+                                const void *o, const void *o_lo, const void *dout,
+                                const float *lse, void *dq, void *dk, void *dv, void *dtable, void *workspace,
+                                size_t workspace_bytes, int B, int h, int h_kv, int T_q, int T_k,
+                                int d_k, int d_v, float scale, mha_mask mask,
+                                const int32_t *key_lens, const mha_score_form *form,
+                                int *status_dev, cudaStream_t stream);
+
+/*
+ * A decoding step (bf16) of a batch whose requests all start with the same
+ * T_p tokens: keys are the shared prefix's, read once for the whole batch, and
+ * then each request's own cache,
+ *   o = softmax(scores of [k_prefix; k_cache[b, 0:len_b]]) [v_prefix; v_cache].
+ *   q, o (B, h, T_q, 64), 1 <= T_q <= 8; k_prefix, v_prefix (h_kv, T_p, 64);
+ *   k_cache, v_cache (B, h_kv, T_k, 64), T_k the capacity; cache_lens DEVICE
+ *   int32 (B), clamped to [0, T_k], or NULL for T_k everywhere.
+ * The new rows are the last T_q of the cache: for a distance bias, prefix row
+ * j is at position j, cache row j at T_p + j, query row t at
+ * T_p + len_b - T_q + t.  Every query row sees len_b cache rows; with a causal
+ * mask row t sees the first len_b - T_q + 1 + t of them (and all of the
+ * prefix).  form: cap, slopes, table; prefix_lens and doc_ids must be NULL.
+ * T_p == 0 and T_k == 0 are allowed; a row without any key outputs 0.
+ * Two launches (the prefix on the tensor cores, split by key ranges into
+ * partial sums; the caches, merged with them), and one before them that
+ * expands the table.  workspace: >= sdpa_decode_shared_workspace_bytes()
+ * bytes, 256-byte aligned; one per call in flight.
+ */
+size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p,
+                                          const mha_score_form *form);
+mha_status sdpa_decode_shared_forward(const void *q, const void *k_prefix, const void *v_prefix,
+                                      const void *k_cache, const void *v_cache, void *o,
+                                      void *workspace, size_t workspace_bytes, int B, int h,
+                                      int h_kv, int T_q, int T_p, int T_k, int d_k, int d_v,
+                                      float scale, mha_mask mask, const int32_t *cache_lens,
+                                      const mha_score_form *form, int *status_dev,
+                                      cudaStream_t stream);
+
+/*
  * Bytes of device workspace mha_forward needs: the projected Q, K, V in
  * head-split layout (B, h, T, d) and the merged attention output
  * (B, T_q, h * d_v), all bf16, each region 256-byte aligned.

@@ -10,6 +10,8 @@ library's CUDA kernels.  PyTorch supplies device memory and the stream.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 import math
 
 from . import _native
@@ -18,7 +20,9 @@ from ._native import (MHA_BF16, MHA_F32, MHA_MASK_CAUSAL, MHA_MASK_CAUSAL_KEY_PA
 
 __all__ = ["sdpa_forward", "sdpa_forward_lse", "sdpa_forward_host", "sdpa_forward_host_workspace_bytes",
            "sdpa_bf16_key_split", "sdpa_backward", "positional_encoding_add",
-           "encoder_layer_forward", "ENCODER_PARAMS", "sdpa_decode_forward", "mha_forward", "mha_forward_add_layernorm", "mha_workspace_bytes", "status_string", "MhaError",
+           "encoder_layer_forward", "ENCODER_PARAMS", "sdpa_decode_forward",
+           "sdpa_scored_forward", "sdpa_scored_forward_lse", "sdpa_scored_backward",
+           "sdpa_decode_shared_forward", "relative_bucket_starts", "mha_forward", "mha_forward_add_layernorm", "mha_workspace_bytes", "status_string", "MhaError",
            "MASKS", "lib"]
 
 MASKS = {"none": MHA_MASK_NONE, "causal": MHA_MASK_CAUSAL, "key_padding": MHA_MASK_KEY_PADDING,
@@ -300,6 +304,236 @@ def sdpa_decode_forward(q, k_cache, v_cache, cache_lens=None, out=None, *, scale
                                  _stream_handle(stream))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_decode_forward")
+    return out
+
+
+# ------------------------------------------------------------------ scored attention
+def relative_bucket_starts(num_buckets, max_distance) -> tuple:
+    """First distances of `num_buckets` relative position buckets (per
+    direction): one bucket for each distance below num_buckets // 2, then
+    logarithmically wider ones, bucket m + u (m = num_buckets // 2) starting at
+    the first distance d with d / m >= (max_distance / m) ** (u / (num_buckets - m)).
+    Computed in whole numbers, so no border depends on a rounding."""
+    n, far = int(num_buckets), int(max_distance)
+    near = n // 2
+    if n < 2 or far < n:
+        raise ValueError("num_buckets must be at least 2 and max_distance at least num_buckets")
+    starts, d = list(range(near)), near
+    for u in range(n - near):
+        while d ** (n - near) < near ** (n - near - u) * far ** u:
+            d += 1
+        starts.append(max(d, starts[-1] + 1))
+    return tuple(starts)
+
+
+@functools.lru_cache(maxsize=64)
+def _starts_array(starts):
+    return (ctypes.c_int32 * len(starts))(*starts)
+
+
+def _check_same(name, t, dtype, shape, device):
+    _check_dev(name, t, dtype)
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have the shape %s" % (name, shape))
+
+
+def _check_current(device):
+    if device.index != _torch().cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _score_form(h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens, doc_ids):
+    """(ScoreForm, the bucket starts' array it points into)."""
+    torch = _torch()
+    f = _native.ScoreForm()
+    keep = None
+    f.cap = 0.0 if cap is None else float(cap)
+    if slopes is not None:
+        _check_same("slopes", slopes, torch.float32, (h,), device)
+        f.slopes = slopes.data_ptr()
+    if (table is None) != (bucket_starts is None):
+        raise ValueError("table and bucket_starts go together")
+    if table is not None:
+        starts = tuple(bucket_starts)
+        n = len(starts)
+        if n == 0 or not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[0] not in (n, 2 * n):
+            raise ValueError("table must have one row per bucket, or two (bidirectional)")
+        _check_same("table", table, torch.bfloat16, (table.shape[0], h), device)
+        keep = _starts_array(starts)
+        f.table = table.data_ptr()
+        f.bucket_starts = ctypes.addressof(keep)
+        f.num_buckets = n
+        f.bidirectional = int(table.shape[0] == 2 * n)
+    if prefix_lens is not None:
+        _check_same("prefix_lens", prefix_lens, torch.int32, (B,), device)
+        f.prefix_lens = prefix_lens.data_ptr()
+    if doc_ids is not None:
+        _check_same("doc_ids", doc_ids, torch.int32, (B, T), device)
+        f.doc_ids = doc_ids.data_ptr()
+    return f, keep
+
+
+def _check_heads(q, k, v, names=("q", "k", "v")):
+    """Shapes (B, h, T_q, 64) and (B, h_kv, T_k, 64) of q, k, v."""
+    bf = _torch().bfloat16
+    _check_dev(names[0], q, bf)
+    if q.dim() != 4 or not hasattr(k, "dim") or k.dim() != 4:
+        raise ValueError("%s and %s must have four dimensions" % names[:2])
+    B, h, T_q, d = q.shape
+    h_kv, T_k = k.shape[1], k.shape[2]
+    for n, t in zip(names[1:], (k, v)):
+        _check_same(n, t, bf, (B, h_kv, T_k, d), q.device)
+    _check_current(q.device)
+    return B, h, h_kv, T_q, T_k, d
+
+
+def _scratch(workspace, need, device):
+    if workspace is None:
+        return _torch().empty(max(need, 1), dtype=_torch().uint8, device=device)
+    _check_dev("workspace", workspace)
+    if workspace.device != device:
+        raise ValueError("workspace must be on %s" % device)
+    return workspace
+
+
+def _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask, key_lens,
+                 prefix_lens, doc_ids, status, stream):
+    torch = _torch()
+    B, h, h_kv, T_q, T_k, d = _check_heads(q, k, v)
+    dev = q.device
+    out = torch.empty_like(q) if out is None else out
+    _check_same("out", out, torch.bfloat16, (B, h, T_q, d), dev)
+    if lse is not None:
+        _check_same("lse", lse, torch.float32, (B, h, T_q), dev)
+    if out_lo is not None:
+        _check_same("out_lo", out_lo, torch.bfloat16, (B, h, T_q, d), dev)
+    if key_lens is not None:
+        _check_same("key_lens", key_lens, torch.int32, (B,), dev)
+    if status is not None:
+        _check_dev("status", status, torch.int32)
+    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
+    pf = ctypes.addressof(form)
+    need = lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf)
+    if need or workspace is not None:
+        workspace = _scratch(workspace, need, dev)
+    rc = lib.sdpa_scored_forward(MHA_BF16, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(out_lo), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 B, h, h_kv, T_q, T_k, d, d,
+                                 1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
+                                 _ptr(key_lens), pf, _ptr(status), _stream_handle(stream))
+    if rc != MHA_OK:
+        raise MhaError(rc, "sdpa_scored_forward")
+    return out
+
+
+def sdpa_scored_forward(q, k, v, out=None, workspace=None, *, scale=None, cap=None, slopes=None,
+                        table=None, bucket_starts=None, mask="none", key_lens=None,
+                        prefix_lens=None, doc_ids=None, status=None, stream=None):
+    """Attention whose scores are scale q k^T, capped to cap tanh(./cap), plus a
+    bias by distance (slopes: fp32 (h,), -slope |j - i|; or a learned table,
+    bf16 (num_buckets [* 2], h), with the host sequence bucket_starts, see
+    relative_bucket_starts), over the keys that mask, key_lens, prefix_lens
+    (int32 (B,), with a causal mask) and doc_ids (int32 (B, T), not
+    decreasing) leave.  q (B,h,T_q,64), k and v (B,h_kv,T_k,64) with h a
+    multiple of h_kv; bf16.  Returns out (B,h,T_q,64)."""
+    return _scored_call(q, k, v, out, None, None, workspace, scale, cap, slopes, table, bucket_starts, mask,
+                        key_lens, prefix_lens, doc_ids, status, stream)
+
+
+def sdpa_scored_forward_lse(q, k, v, out=None, lse=None, workspace=None, *, out_lo=None,
+                            scale=None, cap=None, slopes=None, table=None, bucket_starts=None,
+                            mask="none", key_lens=None, prefix_lens=None, doc_ids=None, status=None, stream=None):
+    """sdpa_scored_forward that also returns the rows' log-sum-exp, lse
+    (B,h,T_q) fp32, which sdpa_scored_backward takes.  out_lo: a tensor like
+    out to receive what rounding took from it, for the backward's o_lo.
+    Returns (out, lse)."""
+    torch = _torch()
+    if lse is None:
+        _check_dev("q", q, torch.bfloat16)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    out = _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
+                       key_lens, prefix_lens, doc_ids, status, stream)
+    return out, lse
+
+
+def sdpa_scored_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, dtable=None,
+                         workspace=None, *, o_lo=None, scale=None, cap=None, slopes=None,
+                         table=None, bucket_starts=None, mask="none", key_lens=None,
+                         prefix_lens=None, doc_ids=None, status=None, stream=None):
+    """Gradients of sdpa_scored_forward from its output o (and the forward's
+    out_lo, for exact row terms), log-sum-exp lse and the output gradient
+    dout; every other argument as in the forward.  Returns
+    (dq, dk, dv, dtable), dtable None without a table."""
+    torch = _torch()
+    bf = torch.bfloat16
+    B, h, h_kv, T_q, T_k, d = _check_heads(q, k, v)
+    dev = q.device
+    _check_same("o", o, bf, (B, h, T_q, d), dev)
+    _check_same("dout", dout, bf, (B, h, T_q, d), dev)
+    _check_same("lse", lse, torch.float32, (B, h, T_q), dev)
+    if o_lo is not None:
+        _check_same("o_lo", o_lo, bf, (B, h, T_q, d), dev)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_same(n, t, bf, tuple(like.shape), dev)
+    if key_lens is not None:
+        _check_same("key_lens", key_lens, torch.int32, (B,), dev)
+    if status is not None:
+        _check_dev("status", status, torch.int32)
+    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
+    if table is not None:
+        dtable = torch.empty_like(table) if dtable is None else dtable
+        _check_same("dtable", dtable, bf, tuple(table.shape), dev)
+    elif dtable is not None:
+        raise ValueError("dtable needs a table")
+    pf = ctypes.addressof(form)
+    workspace = _scratch(workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, T_q, T_k, pf), dev)
+    rc = lib.sdpa_scored_backward(MHA_BF16, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_lo), _ptr(dout),
+                                  _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dtable), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), B, h, h_kv, T_q, T_k, d, d,
+                                  1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
+                                  _ptr(key_lens), pf, _ptr(status), _stream_handle(stream))
+    if rc != MHA_OK:
+        raise MhaError(rc, "sdpa_scored_backward")
+    return dq, dk, dv, dtable
+
+
+def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_lens=None, out=None,
+                               workspace=None, *, scale=None, cap=None, slopes=None, table=None,
+                               bucket_starts=None, mask="none", status=None, stream=None):
+    """Decoding step of a batch that shares a prefix: the T_q (<= 8) query rows
+    of q (B,h,T_q,64) attend to every row of k_prefix / v_prefix (h_kv,T_p,64)
+    and to the first cache_lens[b] rows of k_cache / v_cache (B,h_kv,T_k,64),
+    whose last T_q they are; with a causal mask row t sees the cache up to its
+    own row.  Scores as sdpa_scored_forward.  Returns out (B,h,T_q,64)."""
+    torch = _torch()
+    B, h, h_kv, T_q, T_k, d = _check_heads(q, k_cache, v_cache, ("q", "k_cache", "v_cache"))
+    dev = q.device
+    if not hasattr(k_prefix, "dim") or k_prefix.dim() != 3:
+        raise ValueError("k_prefix must have three dimensions")
+    T_p = k_prefix.shape[1]
+    for n, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+        _check_same(n, t, torch.bfloat16, (h_kv, T_p, d), dev)
+    out = torch.empty_like(q) if out is None else out
+    _check_same("out", out, torch.bfloat16, (B, h, T_q, d), dev)
+    if cache_lens is not None:
+        _check_same("cache_lens", cache_lens, torch.int32, (B,), dev)
+    if status is not None:
+        _check_dev("status", status, torch.int32)
+    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
+    pf = ctypes.addressof(form)
+    workspace = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, pf), dev)
+    rc = lib.sdpa_decode_shared_forward(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache),
+                                        _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                        B, h, h_kv, T_q, T_p, T_k, d, d,
+                                        1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
+                                        _ptr(cache_lens), pf, _ptr(status), _stream_handle(stream))
+    if rc != MHA_OK:
+        raise MhaError(rc, "sdpa_decode_shared_forward")
     return out
 
 

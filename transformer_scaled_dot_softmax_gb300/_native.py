@@ -18,6 +18,16 @@ MHA_F32, MHA_BF16 = 0, 1
 MHA_STATIC_WORKSPACE_BYTES = 32 << 20
 MHA_MASK_NONE, MHA_MASK_CAUSAL, MHA_MASK_KEY_PADDING, MHA_MASK_CAUSAL_KEY_PADDING = 0, 1, 2, 3
 
+
+
+class ScoreForm(ctypes.Structure):
+    """mha_score_form of include/mha.h."""
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("bucket_starts", ctypes.c_void_p), ("num_buckets", ctypes.c_int),
+                ("bidirectional", ctypes.c_int), ("prefix_lens", ctypes.c_void_p),
+                ("doc_ids", ctypes.c_void_p)]
+
+
 # Every symbol include/mha.h declares, with its ctypes signature.
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 SIGNATURES = {
@@ -40,6 +50,15 @@ SIGNATURES = {
                                                 _ci, _vp, _vp, _vp]),
     "sdpa_decode_forward": (_ci, [_vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _ci, _cf, _vp,
                                   _vp]),
+    "sdpa_scored_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _vp]),
+    "sdpa_scored_forward": (_ci, [_ci] + [_vp] * 7 + [_sz] + [_ci] * 7 +
+                            [_cf, _ci, _vp, _vp, _vp, _vp]),
+    "sdpa_scored_backward_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _vp]),
+    "sdpa_scored_backward": (_ci, [_ci] + [_vp] * 12 + [_sz] + [_ci] * 7 +
+                             [_cf, _ci, _vp, _vp, _vp, _vp]),
+    "sdpa_decode_shared_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _vp]),
+    "sdpa_decode_shared_forward": (_ci, [_vp] * 7 + [_sz] + [_ci] * 8 +
+                                   [_cf, _ci, _vp, _vp, _vp, _vp]),
     "mha_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
     "mha_forward": (_ci, [_ci, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _ci, _ci, _ci, _ci,
                           _ci, _ci, _ci, _cf, _ci, _vp, _vp, _vp]),

@@ -201,6 +201,17 @@ MHA_EXPORT const char *mha_last_error(void) { return g_last_error; }
 
 namespace mha {
 mha_status record_cuda_failure(const char *what, const char *detail) { return cuda_fail(what, detail); }
+mha_status encode_heads_map(CUtensorMap *m, const void *base, long long BH, int T) {
+    return encode_heads(m, base, BH, T);
+}
+mha_status encode_stacked_rows_map(CUtensorMap *m, const void *base, int B, int Hkv, int rows, const DecodeRows &dr) {
+    const uint64_t row = kAttnHeadDim * 2;
+    const uint64_t dims[4] = {kAttnHeadDim, static_cast<uint64_t>(rows), static_cast<uint64_t>(B),
+                              static_cast<uint64_t>(Hkv)};
+    const uint64_t strides[3] = {row, static_cast<uint64_t>(Hkv) * rows * row, static_cast<uint64_t>(rows) * row};
+    const uint32_t box[4] = {kAttnHeadDim, static_cast<uint32_t>(dr.per), static_cast<uint32_t>(dr.nb), 1};
+    return encode_bf16(m, base, 4, dims, strides, box);
+}
 }  // namespace mha
 
 namespace {

@@ -1,0 +1,406 @@
+// api_scored.cu -- the scored attention entry points of include/mha.h:
+// argument checks, workspace layout, tensor maps and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/mha.h"
+#include "kernels.h"
+
+#define MHA_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace mha;
+
+constexpr int kMaxFar = 1 << 16;      // last bucket's first distance
+constexpr int kMaxLength = 1 << 24;   // distances are exact in fp32
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+mha_status launched(cudaError_t e, const char *what) {
+    return e == cudaSuccess ? MHA_OK : record_cuda_failure(what, cudaGetErrorName(e));
+}
+
+// A checked form.
+struct Form {
+    bool capped = false;
+    int bias = kBiasNone;
+    ScoreParams f{};
+    BucketParams bk{};
+    const int32_t *prefix_lens = nullptr, *doc_ids = nullptr;
+    size_t vec_bytes(int h) const {
+        return bias == kBiasBuckets ? round256(static_cast<size_t>(h) * (2 * f.mid + 1) * 4) : 0;
+    }
+};
+
+// Sizes only (no pointer of the form is needed): what a workspace depends on.
+bool form_sizes(const mha_score_form *form, Form &out) {
+    if (!form) return true;
+    if (form->num_buckets < 0 || form->num_buckets > kMaxBuckets) return false;
+    if (form->num_buckets > 0) {
+        if (!form->bucket_starts) return false;
+        out.bias = kBiasBuckets;
+        out.bk.num = form->num_buckets;
+        out.bk.both = form->bidirectional ? 1 : 0;
+        for (int i = 0; i < form->num_buckets; ++i) {
+            const int32_t s = form->bucket_starts[i];
+            if (i == 0 ? s != 0 : s <= form->bucket_starts[i - 1]) return false;
+            out.bk.starts[i] = s;
+        }
+        out.f.far = std::max(out.bk.starts[form->num_buckets - 1], 1);
+        if (out.f.far > kMaxFar) return false;
+        out.f.mid = out.f.far + 64;
+    }
+    return true;
+}
+
+mha_status check_form(const mha_score_form *form, float scale, int mask, bool decode, int T_q, int T_k, Form &out) {
+    if (!isfinite(scale)) return MHA_ERR_INVALID_ARG;
+    if (mask < MHA_MASK_NONE || mask > MHA_MASK_CAUSAL_KEY_PADDING) return MHA_ERR_INVALID_ARG;
+    const mha_score_form none{};
+    if (!form) form = &none;
+    if (!(form->cap >= 0.f) || !isfinite(form->cap)) return MHA_ERR_INVALID_ARG;
+    if (form->num_buckets < 0 || (form->table != nullptr) != (form->num_buckets > 0)) return MHA_ERR_INVALID_ARG;
+    if (form->slopes && form->table) return MHA_ERR_INVALID_ARG;
+    if (form->num_buckets > kMaxBuckets) return MHA_ERR_UNSUPPORTED;
+    if (form->num_buckets > 0) {
+        if (!form->bucket_starts || form->bucket_starts[0] != 0) return MHA_ERR_INVALID_ARG;
+        for (int i = 1; i < form->num_buckets; ++i)
+            if (form->bucket_starts[i] <= form->bucket_starts[i - 1]) return MHA_ERR_INVALID_ARG;
+        if (form->bucket_starts[form->num_buckets - 1] > kMaxFar) return MHA_ERR_UNSUPPORTED;
+    }
+    if (decode ? (form->prefix_lens || form->doc_ids)
+               : ((form->prefix_lens && !(mask & MHA_MASK_CAUSAL)) || (form->doc_ids && T_q != T_k)))
+        return MHA_ERR_INVALID_ARG;
+    if (!form_sizes(form, out)) return MHA_ERR_INVALID_ARG;
+    out.capped = form->cap > 0.f;
+    if (form->slopes) out.bias = kBiasSlopes;
+    constexpr float kLog2e = 1.4426950408889634f;
+    out.f.cap_in = out.capped ? scale / form->cap : 0.f;
+    out.f.mul = out.capped ? form->cap * kLog2e : scale * kLog2e;
+    if (!isfinite(out.f.cap_in) || !isfinite(out.f.mul)) return MHA_ERR_INVALID_ARG;
+    // A masked score is u = -inf before the multiplication by mul: with scale
+    // 0 a factor that makes every other product vanish beside 1 keeps it so.
+    if (out.f.mul == 0.f) out.f.mul = 1e-37f;
+    out.f.masked = out.f.mul < 0.f ? INFINITY : -INFINITY;
+    out.f.slopes = form->slopes;
+    out.bk.table = static_cast<const __nv_bfloat16 *>(form->table);
+    out.f.past_only = (mask & MHA_MASK_CAUSAL) && !form->prefix_lens && !decode;
+    out.prefix_lens = form->prefix_lens;
+    out.doc_ids = form->doc_ids;
+    return MHA_OK;
+}
+
+mha_status check_sizes(mha_dtype dt, int B, int h, int h_kv, int T_q, int T_k, int d_k, int d_v) {
+    if (B < 0 || h < 0 || h_kv < 0 || T_q < 0 || T_k < 0 || d_k <= 0 || d_v <= 0) return MHA_ERR_INVALID_ARG;
+    if (dt != MHA_BF16) return dt == MHA_F32 ? MHA_ERR_UNSUPPORTED : MHA_ERR_INVALID_ARG;
+    if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return MHA_ERR_INVALID_ARG;
+    if (d_k != 64 || d_v != 64) return MHA_ERR_UNSUPPORTED;
+    if (h > 65535 || static_cast<long long>(B) * h >= (1ll << 31)) return MHA_ERR_UNSUPPORTED;
+    if (T_q >= kMaxLength || T_k >= kMaxLength || (T_k + 127) / 128 > 65535) return MHA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(B) * h * ((T_q + 127) / 128) >= (1ll << 30)) return MHA_ERR_UNSUPPORTED;
+    return MHA_OK;
+}
+
+// Scratch of the preparing launch, at the start of every workspace.
+struct Prep {
+    size_t vec, docs, end;
+};
+Prep prep_layout(const Form &f, bool docs, int B, int h, int T) {
+    Prep p;
+    p.vec = 0;
+    p.docs = f.vec_bytes(h);
+    p.end = p.docs + (docs ? round256(static_cast<size_t>(B) * T * 8) : 0);
+    return p;
+}
+
+// Runs the preparing launch if the form needs one and fills in what it writes.
+mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h, int T, ScoreParams &sp, VisParams &vis,
+                   cudaStream_t stream, bool *any) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float *vec = f.bias == kBiasBuckets ? reinterpret_cast<float *>(ws + lay.vec) : nullptr;
+    int2 *docs = f.doc_ids ? reinterpret_cast<int2 *>(ws + lay.docs) : nullptr;
+    sp = f.f;
+    sp.vec = vec;
+    vis.doc_range = docs;
+    vis.prefix_lens = f.prefix_lens;
+    *any = vec || docs;
+    return launched(launch_scored_prep(vec, f.f.far, h, f.bk, docs, f.doc_ids, B, T, stream), "scored attention preparation");
+}
+
+struct BwdLayout {
+    Prep prep;
+    size_t dq, nlse2, dvec, diag, far, sums, end;
+    int near_blocks, near_slots;
+};
+BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int T_q, int T_k) {
+    BwdLayout l{};
+    l.prep = prep_layout(f, docs, B, h, T_k);
+    const size_t BH = static_cast<size_t>(B) * h;
+    const int n_qb = (T_q + 127) / 128, n_kb = (T_k + 127) / 128;
+    const size_t rows = BH * n_qb * 128;
+    l.dq = l.prep.end;
+    l.nlse2 = l.dq + round256(rows * 256);
+    l.dvec = l.nlse2 + round256(rows * 4);
+    l.diag = l.dvec + round256(rows * 4);
+    l.far = l.sums = l.end = l.diag;
+    if (f.bias == kBiasBuckets) {
+        // block pairs with |key - query| < far for some pair
+        l.near_blocks = std::min((f.f.far + 126) / 128, std::max(n_qb, n_kb));
+        l.near_slots = std::min(2 * l.near_blocks + 1, n_qb);
+        l.far = l.diag + round256(BH * n_kb * l.near_slots * 1024);
+        l.sums = l.far + round256(BH * n_kb * 8);
+        l.end = l.sums + round256(static_cast<size_t>(h) * (2 * l.near_blocks + 1) * 1024);
+    }
+    return l;
+}
+
+// Key ranges of the prefix: as many as give the SMs equal numbers of items,
+// an item costing its tiles and about three more (its query rows, the first
+// tile's exact maximum, the partial sums).
+struct Splits {
+    int row_tiles, splits, split_tiles;
+};
+Splits prefix_splits(int B, int h, int h_kv, int T_q, int T_p) {
+    Splits s{};
+    if (T_p <= 0 || h <= 0 || B <= 0 || T_q <= 0) return s;
+    const DecodeRows dr = decode_rows(h / h_kv * T_q);
+    s.row_tiles = dr.chunks > 1 ? B * dr.chunks : (B + dr.nb - 1) / dr.nb;
+    const long long items = static_cast<long long>(h_kv) * s.row_tiles;
+    const int tiles = (T_p + 127) / 128;
+    long long best = -1;
+    for (int n = 1; n <= tiles && n <= 64; ++n) {
+        const int per = (tiles + n - 1) / n;
+        const int real = (tiles + per - 1) / per;
+        const long long cost = (items * real + kSmsPerGpu - 1) / kSmsPerGpu * (per + 3);
+        if (best < 0 || cost < best) {
+            best = cost;
+            s.splits = real;
+            s.split_tiles = per;
+        }
+    }
+    return s;
+}
+
+}  // namespace
+
+MHA_EXPORT size_t sdpa_scored_workspace_bytes(int B, int h, int T_q, int T_k, const mha_score_form *form) {
+    Form f;
+    if (B < 0 || h < 0 || T_q < 0 || T_k < 0 || !form_sizes(form, f)) return 0;
+    return prep_layout(f, form && form->doc_ids, B, h, T_k).end;
+}
+
+MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const void *k, const void *v, void *o, float *lse,
+                                          void *o_lo, void *workspace, size_t workspace_bytes, int B, int h, int h_kv, int T_q,
+                                          int T_k, int d_k, int d_v, float scale, mha_mask mask,
+                                          const int32_t *key_lens, const mha_score_form *form, int *status_dev,
+                                          cudaStream_t stream) {
+    Form f;
+    mha_status s = check_sizes(dt, B, h, h_kv, T_q, T_k, d_k, d_v);
+    if (s != MHA_OK) return s;
+    if ((s = check_form(form, scale, mask, false, T_q, T_k, f)) != MHA_OK) return s;
+    if ((mask & MHA_MASK_KEY_PADDING) && !key_lens) return MHA_ERR_INVALID_ARG;
+    if (o_lo && !lse && B > 0 && h > 0 && T_q > 0) return MHA_ERR_INVALID_ARG;
+    if (B == 0 || h == 0 || T_q == 0) return MHA_OK;
+    if (!q || !o || (T_k > 0 && (!k || !v))) return MHA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(o_lo) || (T_k > 0 && (!aligned16(k) || !aligned16(v)))) return MHA_ERR_MISALIGNED;
+    const Prep lay = prep_layout(f, f.doc_ids != nullptr, B, h, T_k);
+    if (lay.end > 0 && (!workspace || workspace_bytes < lay.end)) return MHA_ERR_WORKSPACE;
+    if (lay.end > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
+
+    // T_k == 0: a one-row tensor that the kernel never loads
+    const int Tk_map = T_k > 0 ? T_k : 1;
+    CUtensorMap tq, tk, tv;
+    if ((s = encode_heads_map(&tq, q, static_cast<long long>(B) * h, T_q)) != MHA_OK) return s;
+    if ((s = encode_heads_map(&tk, T_k > 0 ? k : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
+    if ((s = encode_heads_map(&tv, T_k > 0 ? v : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
+    ScoredFwdParams p{};
+    bool prepared = false;
+    if ((s = prepare(f, lay, workspace, B, h, T_k, p.f, p.vis, stream, &prepared)) != MHA_OK) return s;
+    p.B = B;
+    p.H = h;
+    p.Hkv = h_kv;
+    p.Tq = T_q;
+    p.Tk = T_k;
+    p.vis.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+    p.vis.key_lens = (mask & MHA_MASK_KEY_PADDING) ? key_lens : nullptr;
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.o_lo = static_cast<__nv_bfloat16 *>(o_lo);
+    p.num_qblocks = (T_q + 127) / 128;
+    p.total_items = B * h * p.num_qblocks;
+    p.status = status_dev;
+    return launched(launch_attn_scored(tq, tk, tv, f.capped, f.bias, p, stream, prepared), "scored attention launch");
+}
+
+MHA_EXPORT size_t sdpa_scored_backward_workspace_bytes(int B, int h, int T_q, int T_k, const mha_score_form *form) {
+    Form f;
+    if (B < 0 || h < 0 || T_q < 0 || T_k < 0 || !form_sizes(form, f)) return 0;
+    return bwd_layout(f, form && form->doc_ids, B, h, T_q, T_k).end;
+}
+
+MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, const void *v, const void *o,
+                                           const void *o_lo, const void *dout, const float *lse, void *dq, void *dk, void *dv, void *dtable,
+                                           void *workspace, size_t workspace_bytes, int B, int h, int h_kv, int T_q,
+                                           int T_k, int d_k, int d_v, float scale, mha_mask mask,
+                                           const int32_t *key_lens, const mha_score_form *form, int *status_dev,
+                                           cudaStream_t stream) {
+    Form f;
+    mha_status s = check_sizes(dt, B, h, h_kv, T_q, T_k, d_k, d_v);
+    if (s != MHA_OK) return s;
+    if ((s = check_form(form, scale, mask, false, T_q, T_k, f)) != MHA_OK) return s;
+    if ((mask & MHA_MASK_KEY_PADDING) && !key_lens) return MHA_ERR_INVALID_ARG;
+    if (dtable && f.bias != kBiasBuckets) return MHA_ERR_INVALID_ARG;
+    const long long BH = static_cast<long long>(B) * h;
+    if (h == 0 || (BH == 0 && !dtable) || (T_q == 0 && T_k == 0 && !dtable)) return MHA_OK;
+    if (BH > 0 && ((T_q > 0 && (!q || !o || !dout || !lse || !dq)) || (T_k > 0 && (!k || !v || !dk || !dv))))
+        return MHA_ERR_INVALID_ARG;
+    const BwdLayout lay = bwd_layout(f, f.doc_ids != nullptr, B, h, T_q, T_k);
+    if (lay.end > 0 && (!workspace || workspace_bytes < lay.end)) return MHA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
+    if (BH > 0 && ((T_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(o_lo) || !aligned16(dout) || !aligned16(dq))) ||
+                   (T_k > 0 && (!aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv)))))
+        return MHA_ERR_MISALIGNED;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ScoredBwdParams p{};
+    if (BH > 0 && (T_q > 0 || T_k > 0)) {
+        // an empty side is described by a one-row tensor that is never loaded
+        const void *q_src = T_q > 0 ? q : k, *g_src = T_q > 0 ? dout : k;
+        const void *k_src = T_k > 0 ? k : q, *v_src = T_k > 0 ? v : q;
+        const long long BHk = static_cast<long long>(B) * h_kv;
+        CUtensorMap tq, tk, tv, tg;
+        if ((s = encode_heads_map(&tq, q_src, T_q > 0 ? BH : BHk, T_q > 0 ? T_q : 1)) != MHA_OK) return s;
+        if ((s = encode_heads_map(&tg, g_src, T_q > 0 ? BH : BHk, T_q > 0 ? T_q : 1)) != MHA_OK) return s;
+        if ((s = encode_heads_map(&tk, k_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
+        if ((s = encode_heads_map(&tv, v_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
+        bool prepared = false;
+        if ((s = prepare(f, lay.prep, workspace, B, h, T_k, p.f, p.vis, stream, &prepared)) != MHA_OK) return s;
+        p.B = B;
+        p.H = h;
+        p.Hkv = h_kv;
+        p.Tq = T_q;
+        p.Tk = T_k;
+        p.Tq_pad = (T_q + 127) / 128 * 128;
+        p.scale = scale;
+        p.vis.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+        p.vis.key_lens = (mask & MHA_MASK_KEY_PADDING) ? key_lens : nullptr;
+        float *nlse2 = reinterpret_cast<float *>(ws + lay.nlse2), *dvec = reinterpret_cast<float *>(ws + lay.dvec);
+        p.nlse2 = nlse2;
+        p.dvec = dvec;
+        p.dq_acc = reinterpret_cast<float *>(ws + lay.dq);
+        p.dk = static_cast<__nv_bfloat16 *>(dk);
+        p.dv = static_cast<__nv_bfloat16 *>(dv);
+        p.near_blocks = lay.near_blocks;
+        p.near_slots = lay.near_slots;
+        if (dtable) {
+            p.diag = reinterpret_cast<float *>(ws + lay.diag);
+            p.far_sum = reinterpret_cast<float *>(ws + lay.far);
+        }
+        p.status = status_dev;
+        if ((s = launched(launch_attn_bwd_pre(static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(o_lo),
+                                              static_cast<const __nv_bfloat16 *>(dout), lse, nlse2, dvec, p.dq_acc, BH, T_q, p.Tq_pad, stream),
+                          "scored attention backward, row terms")) != MHA_OK)
+            return s;
+        if (T_k > 0 && (s = launched(launch_attn_scored_bwd(tq, tk, tv, tg, f.capped, f.bias, p, stream),
+                                     "scored attention backward launch")) != MHA_OK)
+            return s;
+        if ((s = launched(launch_attn_bwd_post(p.dq_acc, static_cast<__nv_bfloat16 *>(dq), BH, T_q, p.Tq_pad, scale, stream),
+                          "scored attention backward, dq")) != MHA_OK)
+            return s;
+    }
+    if (!dtable) return MHA_OK;
+    return launched(launch_scored_dtable(reinterpret_cast<const float *>(ws + lay.diag),
+                                         reinterpret_cast<const float *>(ws + lay.far),
+                                         reinterpret_cast<float *>(ws + lay.sums), static_cast<__nv_bfloat16 *>(dtable), B, h,
+                                         (T_k + 127) / 128, (T_q + 127) / 128, lay.near_blocks, lay.near_slots, f.bk, stream),
+                    "bias table gradient launch");
+}
+
+MHA_EXPORT size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p, const mha_score_form *form) {
+    Form f;
+    if (B < 0 || h < 0 || h_kv < 0 || T_q < 0 || T_p < 0 || !form_sizes(form, f)) return 0;
+    if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return 0;
+    const size_t rows = static_cast<size_t>(B) * h * T_q;
+    const Splits sp = prefix_splits(B, h, h_kv, T_q, T_p);
+    return f.vec_bytes(h) + round256(sp.splits * rows * 256) + round256(sp.splits * rows * 8);
+}
+
+MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_prefix, const void *v_prefix,
+                                                 const void *k_cache, const void *v_cache, void *o, void *workspace,
+                                                 size_t workspace_bytes, int B, int h, int h_kv, int T_q, int T_p, int T_k,
+                                                 int d_k, int d_v, float scale, mha_mask mask, const int32_t *cache_lens,
+                                                 const mha_score_form *form, int *status_dev, cudaStream_t stream) {
+    Form f;
+    mha_status s = check_sizes(MHA_BF16, B, h, h_kv, T_q, T_k, d_k, d_v);
+    if (s != MHA_OK) return s;
+    if (T_p < 0) return MHA_ERR_INVALID_ARG;
+    if (T_q > kDecodeMaxRows) return MHA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(T_p) + T_k >= kMaxLength) return MHA_ERR_UNSUPPORTED;
+    if ((s = check_form(form, scale, mask, true, T_q, T_k, f)) != MHA_OK) return s;
+    if ((mask & MHA_MASK_KEY_PADDING) && !cache_lens) return MHA_ERR_INVALID_ARG;
+    if (h > 0 && static_cast<long long>(B) * h_kv * 8 >= (1ll << 31)) return MHA_ERR_UNSUPPORTED;
+    if (B == 0 || h == 0 || T_q == 0) return MHA_OK;
+    if (!q || !o || (T_k > 0 && (!k_cache || !v_cache)) || (T_p > 0 && (!k_prefix || !v_prefix))) return MHA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || (T_k > 0 && (!aligned16(k_cache) || !aligned16(v_cache))) ||
+        (T_p > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))))
+        return MHA_ERR_MISALIGNED;
+    const int rows = h / h_kv * T_q;
+    const size_t n_rows = static_cast<size_t>(B) * h * T_q;
+    const Splits sp = prefix_splits(B, h, h_kv, T_q, T_p);
+    if (static_cast<long long>(h_kv) * sp.row_tiles * sp.splits >= (1ll << 30)) return MHA_ERR_UNSUPPORTED;
+    const size_t at_o = f.vec_bytes(h), at_ml = at_o + round256(sp.splits * n_rows * 256);
+    const size_t need = at_ml + round256(sp.splits * n_rows * 8);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MHA_ERR_WORKSPACE;
+    if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    ScoredFwdParams p{};
+    bool prepared = false;
+    if ((s = prepare(f, prep_layout(f, false, B, h, 0), workspace, B, h, 0, p.f, p.vis, stream, &prepared)) != MHA_OK)
+        return s;
+    p.part_o = reinterpret_cast<float *>(ws + at_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + at_ml);
+    if (sp.splits > 0) {
+        CUtensorMap tq, tk, tv;
+        if ((s = encode_stacked_rows_map(&tq, q, B, h_kv, rows, decode_rows(rows))) != MHA_OK) return s;
+        if ((s = encode_heads_map(&tk, k_prefix, h_kv, T_p)) != MHA_OK) return s;
+        if ((s = encode_heads_map(&tv, v_prefix, h_kv, T_p)) != MHA_OK) return s;
+        p.B = B;
+        p.H = h;
+        p.Hkv = h_kv;
+        p.Tq = T_q;
+        p.Tk = T_p;
+        p.total_items = h_kv * sp.row_tiles * sp.splits;
+        p.status = status_dev;
+        p.cache_lens = cache_lens;
+        p.cache_cap = T_k;
+        p.splits = sp.splits;
+        p.split_tiles = sp.split_tiles;
+        p.row_tiles = sp.row_tiles;
+        if ((s = launched(launch_attn_scored(tq, tk, tv, f.capped, f.bias, p, stream, prepared), "shared prefix launch")) !=
+            MHA_OK)
+            return s;
+    }
+    DecodeSharedParams d{};
+    d.B = B;
+    d.H = h;
+    d.Hkv = h_kv;
+    d.Tq = T_q;
+    d.Tk = T_k;
+    d.capped = f.capped ? 1 : 0;
+    d.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+    d.f = p.f;
+    d.cache_lens = cache_lens;
+    d.q = static_cast<const __nv_bfloat16 *>(q);
+    d.k = static_cast<const __nv_bfloat16 *>(k_cache);
+    d.v = static_cast<const __nv_bfloat16 *>(v_cache);
+    d.o = static_cast<__nv_bfloat16 *>(o);
+    d.prefix_splits = sp.splits;
+    d.part_o = p.part_o;
+    d.part_ml = p.part_ml;
+    return launched(launch_decode_shared(d, f.bias, stream), "shared prefix decoding launch");
+}

@@ -30,8 +30,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------ pre and post
 // One thread per 8 features of a row; rows past Tq (padding up to a whole
-// query block) get lse = +inf, D = 0.
-__global__ void attn_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dout,
+// query block) get lse = +inf, D = 0.  o_lo: null, or what rounding took from o.
+__global__ void attn_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ o_lo, const __nv_bfloat16 *__restrict__ dout,
                              const float *__restrict__ lse, float *__restrict__ nlse2,
                              float *__restrict__ dvec, float *__restrict__ dq_acc, long long BH,
                              int Tq, int Tq_pad) {
@@ -52,6 +52,15 @@ __global__ void attn_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfl
         for (int e = 0; e < 4; ++e) {
             acc = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(gw[e] << 16), acc);
             acc = fmaf(__uint_as_float(aw[e] & 0xffff0000u), __uint_as_float(gw[e] & 0xffff0000u), acc);
+        }
+        if (o_lo) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(o_lo + src);
+            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc = fmaf(__uint_as_float(bw[e] << 16), __uint_as_float(gw[e] << 16), acc);
+                acc = fmaf(__uint_as_float(bw[e] & 0xffff0000u), __uint_as_float(gw[e] & 0xffff0000u), acc);
+            }
         }
     }
     // reduce over the 8 threads of the row (consecutive lanes)
@@ -540,6 +549,24 @@ size_t bwd_workspace_bytes(long long BH, int Tq) {
     return r256(rows * HD * 4) + 2 * r256(rows * 4);
 }
 
+cudaError_t launch_attn_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
+                                const float *lse, float *nlse2, float *dvec, float *dq_acc, long long BH, int Tq,
+                                int Tq_pad, cudaStream_t stream) {
+    const long long threads = BH * Tq_pad * 8;
+    if (threads == 0) return cudaSuccess;
+    attn_bwd_pre<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec,
+                                                                                   dq_acc, BH, Tq, Tq_pad);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_bwd_post(const float *dq_acc, __nv_bfloat16 *dq, long long BH, int Tq, int Tq_pad,
+                                 float scale, cudaStream_t stream) {
+    const long long threads = Tq > 0 ? BH * Tq_pad * 8 : 0;
+    if (threads == 0) return cudaSuccess;
+    return launch_kernel(attn_bwd_post, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream, true, 1,
+                         dq_acc, dq, BH, Tq, Tq_pad, scale);
+}
+
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const CUtensorMap &tg, const __nv_bfloat16 *o,
                                  const __nv_bfloat16 *dout, const float *lse, __nv_bfloat16 *dq,
@@ -554,12 +581,8 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
     p.nlse2 = nlse2;
     p.dvec = dvec;
     cudaError_t e = cudaSuccess;
-    const long long pre_threads = static_cast<long long>(rows) * 8;
-    if (pre_threads > 0) {
-        attn_bwd_pre<<<static_cast<unsigned>((pre_threads + 255) / 256), 256, 0, stream>>>(
-            o, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    if ((e = launch_attn_bwd_pre(o, nullptr, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, stream)) != cudaSuccess)
+        return e;
     if (p.Tk > 0) {
         const size_t smem = sizeof(SmemBwd) + 1024;
         e = cudaFuncSetAttribute(attn_bwd_main, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -570,10 +593,7 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
             cudaSuccess)
             return e;
     }
-    const long long post_threads = p.Tq > 0 ? BH * p.Tq_pad * 8 : 0;
-    if (post_threads == 0) return cudaSuccess;
-    return launch_kernel(attn_bwd_post, dim3(static_cast<unsigned>((post_threads + 255) / 256)), dim3(256), 0,
-                         stream, true, 1, static_cast<const float *>(p.dq_acc), dq, BH, p.Tq, p.Tq_pad, p.scale);
+    return launch_attn_bwd_post(p.dq_acc, dq, BH, p.Tq, p.Tq_pad, p.scale, stream);
 }
 
 }  // namespace mha

@@ -1,0 +1,18 @@
+// attn_scored_bf16.cu -- scored attention forward: uncapped instances and the
+// choice among all (the kernel is in attn_scored_bf16.cuh).
+#include "attn_scored_bf16.cuh"
+
+namespace mha {
+
+cudaError_t launch_attn_scored_capped(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int bias,
+                                      const ScoredFwdParams &p, cudaStream_t stream, bool pdl);
+
+cudaError_t launch_attn_scored(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, bool capped,
+                               int bias, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
+    if (capped) return launch_attn_scored_capped(tq, tk, tv, bias, p, stream, pdl);
+    if (bias == kBiasSlopes) return scored::launch_form<false, kBiasSlopes>(tq, tk, tv, p, stream, pdl);
+    if (bias == kBiasBuckets) return scored::launch_form<false, kBiasBuckets>(tq, tk, tv, p, stream, pdl);
+    return scored::launch_form<false, kBiasNone>(tq, tk, tv, p, stream, pdl);
+}
+
+}  // namespace mha

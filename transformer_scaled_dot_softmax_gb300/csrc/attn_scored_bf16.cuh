@@ -1,0 +1,719 @@
+// attn_scored_bf16.cuh -- attention forward whose scores are more than
+// scale q.k, for sm_103a: capped by a tanh, biased by distance, masked by
+// documents or prefixes (the definition is in scores.cuh), with K/V heads
+// shared by groups of query heads; and, as the same kernel over other rows,
+// the partial sums of decoding rows against a prefix that a batch shares.
+//
+// Mathematics: the online softmax of attn_bf16.cu.  A row keeps a reference
+// m (log2 units) and a sum l; P = 2^(y - m), O += P V; only a round whose sum
+// leaves [0, 2^16] takes the exact step (new maximum, O and l scaled).  What a
+// row sees is one interval of keys [lo, hi): the causal mask, key padding,
+// prefixes and documents all end in one, so a tile is masked by two
+// comparisons per key, and only tiles that some row sees in part are.
+//
+// With the log-sum-exp exported (the training forward) the row sum is also kept
+// of the unrounded weights, for lse alone, and the output's rounding remainder
+// can be stored beside it: the backward's P = 2^(y - lse) and D = rowsum(dO O)
+// then carry no bf16 rounding of this pass.
+//
+// The pipeline (persistent CTAs, TMA ring, S issuer, two PV issuers, two
+// softmax groups on alternate tiles, output warps, three rotating score
+// buffers in tensor memory) is that of attn_bf16.cu, described there.  What
+// differs:
+//   * an item's key tiles start at the tile that holds its diagonal and go
+//     down from there, then up: with a distance bias the largest scores come
+//     first, so the reference is set once instead of growing from tile to
+//     tile (a rescale of O each);
+//   * the score transform runs on the 64 scores a thread holds, in registers,
+//     packed two by two (scores.cuh);
+//   * V rows past the key length are cleared in shared memory before they are
+//     multiplied by their zero weights, so that what a padded buffer holds
+//     there (NaN included) never reaches the output.
+//
+// Bound: like attn_bf16.cu by the softmax warps, not by the tensor cores: the
+// weights take 128 x 128 / 16 = 1,024 special-function cycles per tile
+// against 512 of tensor-core time, and the cap adds 8 issue slots per pair.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "scores.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mha {
+namespace scored {
+
+constexpr int BM = kAttnRowsPerCta;
+constexpr int BN = 128;
+constexpr int HD = kAttnHeadDim;
+constexpr int STAGES = 5;
+constexpr int kSBufs = 3;
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8;
+constexpr int kMmaSWarp = 9;
+constexpr int kMmaPvWarp = 10;
+constexpr int kOutWarp = 12;
+constexpr uint32_t kTileBytes = BM * HD * 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 384;
+constexpr float kRoundSumLimit = 65536.0f;                // 2^16
+constexpr float kFirstSumMin = 5.421010862427522e-20f;    // 2^-64
+constexpr int kItemTable = 128;
+
+// What the kernel computes.
+enum Mode { kForward, kForwardLse, kDecode };
+
+// One work item: 128 query rows of one head against a range of key tiles.
+struct Item {
+    int b, hh, q0;         // decoding: first batch entry, K/V head, first row of the batch entry's
+    int kv_len;            // keys past it are padding
+    int j0, n_kv;          // key tiles j0 .. j0 + n_kv - 1
+    int jd;                // the first one visited
+    int full_lo, full_hi;  // keys [full_lo, full_hi) are seen by every row
+    int split;             // decoding: key range
+};
+
+struct __align__(1024) Smem {
+    uint8_t q[2][kTileBytes];
+    uint8_t k[STAGES][kTileBytes];
+    uint8_t v[STAGES][kTileBytes];
+    float red_m[2][BM];
+    float red_l[2][BM];
+    float red_e[2][BM];
+    uint64_t q_full[2];
+    uint64_t q_empty[2];
+    uint64_t kv_full[STAGES];
+    uint64_t kv_empty[STAGES];
+    uint64_t s_full[kSBufs];
+    uint64_t p_rd[2][2][2];  // [group][round][group tile mod 2]: P of the round written
+    uint64_t pv0[2][2];      // [group][group tile mod 2]: round-0 product complete
+    uint64_t ml_full, ml_free, o_final, o_free;
+    uint64_t drain[3];
+    Item item_tab[kItemTable];
+    int n_items;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+__device__ __forceinline__ int item_index(int t, int c, int G) {
+    return t * G + ((t & 1) ? (G - 1 - c) : c);
+}
+
+// Keys [lo, hi) that query row `i` of batch entry `b` sees.
+__device__ __forceinline__ int2 row_keys(const VisParams &v, int Tk, int Tq, int b, int i) {
+    int lo = 0, hi = Tk;
+    if (v.key_lens) hi = min(max(v.key_lens[b], 0), Tk);
+    if (v.causal) {
+        int seen = i + 1;
+        if (v.prefix_lens) seen = max(seen, v.prefix_lens[b]);
+        hi = min(hi, seen);
+    }
+    if (v.doc_range) {
+        const int2 d = v.doc_range[static_cast<long long>(b) * Tq + i];
+        lo = max(lo, d.x);
+        hi = min(hi, d.y);
+    }
+    return make_int2(lo, hi);
+}
+
+template <int kMode>
+__device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k) {
+    Item it;
+    if (kMode == kDecode) {
+        const DecodeRows dr = decode_rows(p.H / p.Hkv * p.Tq);
+        const int tile = k % p.row_tiles;
+        const int rest = k / p.row_tiles;
+        it.hh = rest % p.Hkv;
+        it.split = rest / p.Hkv;
+        it.b = dr.chunks > 1 ? tile / dr.chunks : tile * dr.nb;
+        it.q0 = dr.chunks > 1 ? (tile - it.b * dr.chunks) * 128 : 0;
+        it.kv_len = p.Tk;
+        it.j0 = it.split * p.split_tiles;
+        it.n_kv = max(0, min(p.split_tiles, (p.Tk + BN - 1) / BN - it.j0));
+        it.jd = it.j0 + it.n_kv - 1;
+        it.full_lo = 0;
+        it.full_hi = p.Tk;
+        return it;
+    }
+    const int BH = p.B * p.H;
+    const int qb = p.num_qblocks - 1 - k / BH;
+    const int bh = k - (k / BH) * BH;
+    it.b = bh / p.H;
+    it.hh = bh - it.b * p.H;
+    it.q0 = qb * BM;
+    it.split = 0;
+    it.kv_len = p.vis.key_lens ? min(max(p.vis.key_lens[it.b], 0), p.Tk) : p.Tk;
+    // lo and hi grow with the row: the first and the last row bound the block
+    const int2 first = row_keys(p.vis, p.Tk, p.Tq, it.b, it.q0);
+    const int2 last = row_keys(p.vis, p.Tk, p.Tq, it.b, min(it.q0 + BM, p.Tq) - 1);
+    it.j0 = max(first.x, 0) / BN;
+    it.n_kv = max(0, (last.y + BN - 1) / BN - it.j0);
+    it.jd = min(max(it.q0 / BN, it.j0), it.j0 + it.n_kv - 1);
+    it.full_lo = last.x;
+    it.full_hi = first.y;
+    return it;
+}
+
+// The t-th key tile of an item: down from jd, then up.
+__device__ __forceinline__ int tile_of(const Item &it, int t) {
+    const int down = it.jd - it.j0;
+    return t <= down ? it.jd - t : it.j0 + t;
+}
+
+template <int kMode>
+__device__ __forceinline__ Item item_of(const Smem &sm, const ScoredFwdParams &p, int t, int cta, int G) {
+    if (t >= kItemTable) return make_item<kMode>(p, item_index(t, cta, G));
+    return sm.item_tab[t];
+}
+
+// What a thread's row (r of the item's 128) is.
+struct Row {
+    bool live;       // an output row
+    int head;        // query head
+    int pos;         // position, for distances
+    long long out;   // row of the output (or of the partial sums of a split)
+    int2 keys;       // keys [x, y) seen
+};
+template <int kMode>
+__device__ __forceinline__ Row make_row(const ScoredFwdParams &p, const Item &it, int r) {
+    Row w;
+    if (kMode == kDecode) {
+        const int g = p.H / p.Hkv, rows = g * p.Tq;
+        const DecodeRows dr = decode_rows(rows);
+        const int bi = r / dr.per;
+        const int rem = it.q0 + r - bi * dr.per;
+        const int b = it.b + bi;
+        w.live = bi < dr.nb && b < p.B && rem < rows;
+        w.head = it.hh * g + (w.live ? rem / p.Tq : 0);
+        const int t = w.live ? rem % p.Tq : 0;
+        int len = p.cache_cap;
+        if (w.live && p.cache_lens) len = min(max(p.cache_lens[b], 0), p.cache_cap);
+        w.pos = p.Tk + len - p.Tq + t;
+        w.out = w.live ? (static_cast<long long>(b) * p.H + w.head) * p.Tq + t : 0;
+        w.keys = make_int2(0, p.Tk);
+    } else {
+        const int i = it.q0 + r, ic = min(i, p.Tq - 1);
+        w.live = i < p.Tq;
+        w.head = it.hh;
+        w.pos = i;
+        w.out = (static_cast<long long>(it.b) * p.H + it.hh) * p.Tq + ic;
+        w.keys = row_keys(p.vis, p.Tk, p.Tq, it.b, ic);
+    }
+    return w;
+}
+
+template <bool kCap, int kBias, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_scored_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ ScoredFwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int G = static_cast<int>(gridDim.x);
+    const int cta = static_cast<int>(blockIdx.x);
+    const int total = p.total_items;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+        }
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kSBufs; ++i) mbar_init(&sm.s_full[i], 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&sm.p_rd[i >> 2][(i >> 1) & 1][i & 1], kSoftmaxWarps / 2);
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.pv0[i >> 1][i & 1], 1);
+        mbar_init(&sm.ml_full, kSoftmaxWarps);
+        mbar_init(&sm.ml_free, 4);
+        mbar_init(&sm.o_final, 2);
+        mbar_init(&sm.o_free, 4);
+        for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
+        const int F = total / G, rem = total - F * G;
+        sm.n_items = F + ((((F & 1) ? (G - 1 - cta) : cta) < rem) ? 1 : 0);
+        sm.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaSWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    // Document ranges and the expanded bias are written by the launch before
+    // this one.  A launch after this one may begin once that one is complete,
+    // so it may read them too.
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int t = threadIdx.x; t < kItemTable; t += kThreads) {
+        const int k = item_index(t, cta, G);
+        if (k < total) sm.item_tab[t] = make_item<kMode>(p, k);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    const AbortState ab{&sm.abort_flag, p.status, 0};
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const int g = p.H / p.Hkv;
+            uint32_t q_bytes = kTileBytes;
+            if (kMode == kDecode) {
+                const DecodeRows dr = decode_rows(g * p.Tq);
+                q_bytes = static_cast<uint32_t>(dr.per * dr.nb) * (HD * 2);
+            }
+            int n = 0, v = 0;  // key tiles and items so far
+            bool ok = true;
+            for (int t = 0; ok && t < sm.n_items; ++t) {
+                const Item it = item_of<kMode>(sm, p, t, cta, G);
+                if (it.n_kv == 0) continue;
+                const int qbuf = v & 1;
+                if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
+                mbar_arrive_expect_tx(&sm.q_full[qbuf], q_bytes);
+                if (in_bounds(it.q0 >= 0 && it.b >= 0 && it.b < p.B && it.hh < (kMode == kDecode ? p.Hkv : p.H), p.status)) {
+                    if (kMode == kDecode)
+                        tma_load_4d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b, it.hh);
+                    else
+                        tma_load_3d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b * p.H + it.hh);
+                }
+                ++v;
+                const int z = kMode == kDecode ? it.hh : it.b * p.Hkv + it.hh / g;
+                for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
+                    const int j = tile_of(it, jt);
+                    const int st = n % STAGES;
+                    if (n >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
+                    mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
+                    if (in_bounds(j >= 0 && j * BN < p.Tk && z < (kMode == kDecode ? 1 : p.B) * p.Hkv, p.status)) {
+                        tma_load_3d(&tmap_k, &sm.kv_full[st], sm.k[st], 0, j * BN, z);
+                        tma_load_3d(&tmap_v, &sm.kv_full[st], sm.v[st], 0, j * BN, z);
+                    }
+                }
+            }
+            for (int x = max(0, n - STAGES); x < n; ++x)
+                mbar_wait_drain(&sm.kv_full[x % STAGES], (x / STAGES) & 1);
+            for (int x = max(0, v - 2); x < v; ++x) mbar_wait_drain(&sm.q_full[x & 1], (x >> 1) & 1);
+        }
+    } else if (warp == kMmaSWarp) {
+        // ----------------------------------------------------- S issuer
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, false);
+        constexpr uint64_t kTileDesc = kTileBytes >> 4;
+        const uint64_t q_desc0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+        const uint64_t k_desc0 = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < sm.n_items; ++t) {
+            const int n_kv = item_of<kMode>(sm, p, t, cta, G).n_kv;
+            if (n_kv == 0) continue;
+            const int qbuf = v & 1;
+            if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
+            for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                const int st = n % STAGES, sb = n % kSBufs;
+                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                if (n >= kSBufs) {
+                    const int np = n - kSBufs;
+                    if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
+                const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
+                warp_commit(&sm.s_full[sb]);
+            }
+            if (!ok) break;
+            warp_commit(&sm.q_empty[qbuf]);
+            ++v;
+        }
+        warp_commit(&sm.drain[0]);
+        mbar_wait_drain(&sm.drain[0], 0);
+    } else if (warp == kMmaPvWarp || warp == kMmaPvWarp + 1) {
+        // ---------------------------------------------------- PV issuers
+        const int hf = warp - kMmaPvWarp;
+        constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, false, true);
+        constexpr uint64_t kTileDesc = kTileBytes >> 4;
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), 1024, 1024);
+        const uint32_t d_o = tmem + kOCol + 64u * static_cast<uint32_t>(hf);
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < sm.n_items; ++t) {
+            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            if (it.n_kv == 0) continue;
+            if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
+            for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
+                if ((n & 1) != hf) continue;
+                const int st = n % STAGES, sb = n % kSBufs;
+                const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
+                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                // Padding past the key length: weights there are 0, and 0
+                // times whatever the buffer holds has to be 0.  (Rows past Tk
+                // are filled with zeros by the copy.)
+                const int rows = it.kv_len - tile_of(it, jt) * BN;
+                if (kMode != kDecode && rows < BN && it.kv_len < p.Tk) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
+                    for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (!(ok = warp_wait(&sm.p_rd[hf][0][slot], par, ab))) break;
+                tc_fence_after_sync();
+                const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
+                const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, (jt >= 2 || kk > 0) ? 1u : 0u);
+                warp_commit(&sm.pv0[hf][slot]);
+                if (!(ok = warp_wait(&sm.p_rd[hf][1][slot], par, ab))) break;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk)
+                    warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, 1u);
+                warp_commit(&sm.kv_empty[st]);
+            }
+            if (!ok) break;
+            warp_commit(&sm.o_final);
+            ++v;
+        }
+        warp_commit(&sm.drain[1 + hf]);
+        mbar_wait_drain(&sm.drain[1 + hf], 0);
+    } else if (warp < kSoftmaxWarps) {
+        // --------------------------------------------------------- softmax
+        const int half = warp >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
+        const int r = static_cast<int>(lane_base) + lane;
+        const uint32_t tl = tmem_addr(tmem, lane_base, 0);
+        const uint32_t to = tl + kOCol + 64u * half;
+        // With the log-sum-exp exported the first reference is the row's own
+        // maximum; otherwise a first round is tried against 0.
+        constexpr bool guess_first = kMode != kForwardLse;
+
+        // 2^y of a round in bf16 and the fp32 sum of the rounded weights (the
+        // values P V multiplies, so that normalised weights sum to 1).
+        // exact: with lse, the sum of the unrounded ones.
+        auto exp_round = [](const uint32_t(&a)[32], const uint32_t(&b)[32], float off, uint32_t(&pk)[32],
+                            float &exact) -> float {
+            const uint64_t off2 = f32x2_set(off);
+            uint64_t ex[2] = {0, 0};
+            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                float x0, x1, x2, x3;
+                f32x2_unpack(add_f32x2(f32x2_pack(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])), off2), x0, x1);
+                f32x2_unpack(add_f32x2(f32x2_pack(__uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1])), off2), x2, x3);
+                x0 = ex2_approx(x0);
+                x1 = ex2_approx(x1);
+                x2 = ex2_approx(x2);
+                x3 = ex2_approx(x3);
+                pk[c] = pack_bf16x2(x0, x1);
+                pk[16 + c] = pack_bf16x2(x2, x3);
+                if (kMode == kForwardLse) {
+                    ex[0] = add_f32x2(ex[0], f32x2_pack(x0, x1));
+                    ex[1] = add_f32x2(ex[1], f32x2_pack(x2, x3));
+                }
+                add_bf16x2_to_f32(acc[2 * (c & 1)], acc[2 * (c & 1) + 1], pk[c]);
+                add_bf16x2_to_f32(acc[4 + 2 * (c & 1)], acc[5 + 2 * (c & 1)], pk[16 + c]);
+            }
+            if (kMode == kForwardLse) {
+                float e0, e1;
+                f32x2_unpack(add_f32x2(ex[0], ex[1]), e0, e1);
+                exact = e0 + e1;
+            }
+            return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        };
+        auto row_max = [](const uint32_t(&a)[32], const uint32_t(&b)[32]) -> float {
+            float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                t0 = fmax3(t0, __uint_as_float(a[c]), __uint_as_float(a[c + 1]));
+                t1 = fmax3(t1, __uint_as_float(a[c + 2]), __uint_as_float(a[c + 3]));
+                t2 = fmax3(t2, __uint_as_float(b[c]), __uint_as_float(b[c + 1]));
+                t3 = fmax3(t3, __uint_as_float(b[c + 2]), __uint_as_float(b[c + 3]));
+            }
+            return fmaxf(fmax3(t0, t1, t2), t3);
+        };
+
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < sm.n_items; ++t) {
+            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            if (it.n_kv == 0) continue;
+            const Row w = make_row<kMode>(p, it, r);
+            const BiasRow br = bias_row<kBias>(p.f, w.head);
+            // decoding: rows past the stacked ones have nothing to compute
+            const bool warp_live = kMode != kDecode || __any_sync(0xffffffffu, w.live);
+            float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
+            float l_run = 0.f, e_run = 0.f;
+
+            for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
+                if ((n & 1) != half) continue;
+                const int j = tile_of(it, jt);
+                const int sb = n % kSBufs;
+                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                const bool edge = j * BN < it.full_lo || j * BN + BN > it.full_hi;
+#pragma unroll 1
+                for (int rd = 0; rd < 2; ++rd) {
+                    const int key0 = j * BN + 64 * rd;  // the round's first key
+                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
+                    // y - ref of the round's scores, masked ones -inf
+                    auto load_scores = [&](uint32_t(&s0)[32], uint32_t(&s1)[32], float ref) {
+                        tmem_ld32(tr, s0);
+                        tmem_ld32(tr + 32, s1);
+                        tmem_ld_wait(s0);
+                        reg_fence32(s1);
+                        const int lo = w.keys.x - key0, hi = w.keys.y - key0;
+                        auto mask_to = [&](float value) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                if (c < lo || c >= hi) s0[c] = __float_as_uint(value);
+                                if (c + 32 < lo || c + 32 >= hi) s1[c] = __float_as_uint(value);
+                            }
+                        };
+                        if (kCap) {
+                            // masked scores have no say in how tanh is taken
+                            if (edge) mask_to(0.f);
+                            const float big = fmaxf(max_abs(s0), max_abs(s1));
+                            const bool any = __any_sync(0xffffffffu, (kMode != kDecode || w.live) &&
+                                                                         big * fabsf(p.f.cap_in) > kTanhRange);
+                            cap_scores(s0, p.f.cap_in, any);
+                            cap_scores(s1, p.f.cap_in, any);
+                        }
+                        if (edge) mask_to(p.f.masked);
+                        add_bias<kBias, 1>(s0, p.f, br, key0 - w.pos, -ref);
+                        add_bias<kBias, 1>(s1, p.f, br, key0 + 32 - w.pos, -ref);
+                    };
+                    uint32_t pk[32];
+                    float lt = 0.f, et = 0.f;
+                    if (warp_live) {
+                        bool need = true;
+                        if (guess_first || jt >= 2 || rd == 1) {
+                            uint32_t s0[32], s1[32];
+                            load_scores(s0, s1, m_run == -INFINITY ? 0.f : m_run);
+                            lt = exp_round(s0, s1, 0.f, pk, et);
+                            need = m_run == -INFINITY
+                                       ? !(guess_first && lt >= kFirstSumMin && lt <= kRoundSumLimit)
+                                       : !(lt <= kRoundSumLimit);
+                            if (!need && m_run == -INFINITY) m_run = 0.f;
+                            // nothing visible in the round: weights 0, no reference
+                            if (w.keys.x >= key0 + 64 || w.keys.y <= key0) need = false;
+                        }
+                        // what shared memory held for a dead row decides nothing
+                        if (kMode == kDecode && !w.live) need = false;
+                        if (__any_sync(0xffffffffu, need)) {
+                            uint32_t s0[32], s1[32];
+                            const float ref = m_run == -INFINITY ? 0.f : m_run;
+                            load_scores(s0, s1, ref);
+                            float alpha = 1.f;
+                            if (need) {
+                                const float up = row_max(s0, s1);  // above ref
+                                float off = 0.f;
+                                if (m_run == -INFINITY) {
+                                    if (up != -INFINITY) {
+                                        m_run = up;
+                                        off = -up;
+                                    }
+                                } else if (up > 0.f) {
+                                    const float m_new = m_run + up;
+                                    off = m_run - m_new;
+                                    alpha = ex2_approx(off);
+                                    m_run = m_new;
+                                    l_run *= alpha;
+                                    e_run *= alpha;
+                                }
+                                lt = exp_round(s0, s1, off, pk, et);
+                            }
+                            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                                // O_h holds the group's earlier tiles of the
+                                // item (and, in round 1, this tile's round 0,
+                                // taken against the old reference): wait for
+                                // the last product it took.
+                                bool scale_o = true;
+                                if (rd == 1) {
+                                    ok = __all_sync(0xffffffffu,
+                                                    mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
+                                } else if (jt >= 2) {
+                                    const int np = n - 2;
+                                    ok = __all_sync(0xffffffffu,
+                                                    mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
+                                } else {
+                                    scale_o = false;
+                                }
+                                if (!ok) break;
+                                if (scale_o) {
+                                    tc_fence_after_sync();
+#pragma unroll 1
+                                    for (int part = 0; part < 4; ++part) {
+                                        uint32_t o0[16];
+                                        tmem_ld16(to + 16u * static_cast<uint32_t>(part), o0);
+                                        tmem_ld_wait(o0);
+#pragma unroll
+                                        for (int c = 0; c < 16; ++c)
+                                            o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
+                                        tmem_st16(to + 16u * static_cast<uint32_t>(part), o0);
+                                        tmem_st_wait();
+                                    }
+                                }
+                            }
+                        }
+                        tmem_st32(ts + 32u * static_cast<uint32_t>(rd), pk);
+                        l_run += lt;
+                        e_run += et;
+                        tmem_st_wait();
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+            if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
+            sm.red_m[half][r] = m_run;
+            sm.red_l[half][r] = l_run;
+            if (kMode == kForwardLse) sm.red_e[half][r] = e_run;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ml_full);
+            ++v;
+        }
+        if (!ok) tmem_st_wait();
+    } else if (warp >= kOutWarp) {
+        // ------------------------------------------------------------ output
+        const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
+        const int r = static_cast<int>(lane_base) + lane;
+        const uint32_t tl = tmem_addr(tmem, lane_base, 0);
+        int v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < sm.n_items; ++t) {
+            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            const Row w = make_row<kMode>(p, it, r);
+            const bool row_ok = in_bounds(w.out >= 0 && w.out < static_cast<long long>(p.B) * p.H * p.Tq, p.status) && w.live;
+            if (it.n_kv == 0) {
+                if (kMode != kDecode && row_ok) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(p.o + w.out * HD);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) d4[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (kMode == kForwardLse) {
+                        p.lse[w.out] = -INFINITY;
+                        if (p.o_lo) {
+                            uint4 *l4 = reinterpret_cast<uint4 *>(p.o_lo + w.out * HD);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) l4[c] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                continue;
+            }
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
+            const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
+            const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
+            const float ea = sm.red_e[0][r], eb = sm.red_e[1][r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ml_free);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
+            tc_fence_after_sync();
+            const float M = fmaxf(ma, mb);
+            const float wa = la > 0.f ? ex2_approx(ma - M) : 0.f;
+            const float wb = lb > 0.f ? ex2_approx(mb - M) : 0.f;
+            const float L = la * wa + lb * wb;
+            const float inv = kMode == kDecode ? 1.f : L > 0.f ? 1.0f / L : 0.f;
+            const float fa = wa * inv, fb = wb * inv;
+            const long long prow = kMode == kDecode ? it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out : 0;
+            if (row_ok) {
+                if (kMode == kDecode)
+                    p.part_ml[prow] = make_float2(L > 0.f ? M : -INFINITY, L);
+                else if (kMode == kForwardLse)
+                    p.lse[w.out] = L > 0.f ? fmaf(M, kLn2, logf(ea * wa + eb * wb)) : -INFINITY;
+            }
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint32_t oa[32], ob[32];
+                tmem_ld32(tl + kOCol + 32u * part, oa);
+                tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
+                tmem_ld_wait(oa);
+                reg_fence32(ob);
+                if (part == 1) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_free);
+                }
+                if (!row_ok) continue;
+                // a group without a visible key left its accumulator unwritten
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    oa[c] = __float_as_uint((la > 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
+                                            (lb > 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
+                if (kMode == kDecode) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(p.part_o + prow * HD) + 8 * part;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        d4[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
+                } else {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(p.o + w.out * HD) + 4 * part;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]), __uint_as_float(oa[2 * c + 1]));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        d4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    if (kMode == kForwardLse && p.o_lo) {
+                        uint4 *l4 = reinterpret_cast<uint4 *>(p.o_lo + w.out * HD) + 4 * part;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]) - __uint_as_float(pk[c] << 16),
+                                                __uint_as_float(oa[2 * c + 1]) - __uint_as_float(pk[c] & 0xffff0000u));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            l4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                    }
+                }
+            }
+            ++v;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaSWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <bool kCap, int kBias, int kMode>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ScoredFwdParams &p,
+                   cudaStream_t stream, bool pdl) {
+    auto kernel = attn_scored_kernel<kCap, kBias, kMode>;
+    const size_t smem = sizeof(Smem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    if ((e = sm_count(&sms)) != cudaSuccess) return e;
+    const int grid = p.total_items < sms ? p.total_items : sms;
+    if (grid <= 0) return cudaSuccess;
+    return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, pdl, 1, tq, tk, tv, p);
+}
+
+template <bool kCap, int kBias>
+cudaError_t launch_form(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ScoredFwdParams &p,
+                        cudaStream_t stream, bool pdl) {
+    if (p.part_o) return launch<kCap, kBias, kDecode>(tq, tk, tv, p, stream, pdl);
+    if (p.lse) return launch<kCap, kBias, kForwardLse>(tq, tk, tv, p, stream, pdl);
+    return launch<kCap, kBias, kForward>(tq, tk, tv, p, stream, pdl);
+}
+
+}  // namespace scored
+}  // namespace mha

@@ -1,0 +1,14 @@
+// attn_scored_capped_bf16.cu -- scored attention forward: capped instances
+// (apart from the others so that the two compile in parallel).
+#include "attn_scored_bf16.cuh"
+
+namespace mha {
+
+cudaError_t launch_attn_scored_capped(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int bias,
+                                      const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
+    if (bias == kBiasSlopes) return scored::launch_form<true, kBiasSlopes>(tq, tk, tv, p, stream, pdl);
+    if (bias == kBiasBuckets) return scored::launch_form<true, kBiasBuckets>(tq, tk, tv, p, stream, pdl);
+    return scored::launch_form<true, kBiasNone>(tq, tk, tv, p, stream, pdl);
+}
+
+}  // namespace mha

@@ -116,6 +116,120 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
                                  const __nv_bfloat16 *dout, const float *lse, __nv_bfloat16 *dq,
                                  BwdParams p, void *workspace, cudaStream_t stream);
 
+// The backward's row-term launch and dQ conversion, shared with the scored
+// backward; heads padded to Tq_pad rows.  o_lo (may be null) is added to o.
+cudaError_t launch_attn_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout, const float *lse, float *nlse2,
+                                float *dvec, float *dq_acc, long long BH, int Tq, int Tq_pad, cudaStream_t stream);
+cudaError_t launch_attn_bwd_post(const float *dq_acc, __nv_bfloat16 *dq, long long BH, int Tq, int Tq_pad,
+                                 float scale, cudaStream_t stream);
+
+// ------------------------------------------------ scored attention
+// Scores beyond scale q.k (see scores.cuh): what the kernels need of them.
+enum BiasKind { kBiasNone = 0, kBiasSlopes = 1, kBiasBuckets = 2 };
+struct ScoreParams {
+    float cap_in;         // scale / cap (capped scores), else unused
+    float mul;            // y = u mul + bias, u = q.k or tanh(q.k cap_in), y in log2 units; never 0
+    float masked;         // the u of a masked score: minus infinity times the sign of mul
+    const float *slopes;  // (H) fp32, kBiasSlopes
+    const float *vec;     // (H, 2 mid + 1) fp32 in log2 units, kBiasBuckets; written by scored_prep
+    int far, mid;         // distances from `far` on share the last bucket; mid = far + 64
+    int past_only;        // no visible key lies past its query (causal mask without prefixes)
+};
+// Which keys a query sees.
+struct VisParams {
+    int causal;
+    const int32_t *key_lens;     // (B) or null
+    const int32_t *prefix_lens;  // (B) or null: keys every query sees in spite of the causal mask
+    const int2 *doc_range;       // (B, T) or null: first position of a position's document, and past its last
+};
+
+constexpr int kMaxBuckets = 64;  // per direction
+struct BucketParams {
+    const __nv_bfloat16 *table;  // (num [* 2], H)
+    int num, both;
+    int32_t starts[kMaxBuckets];
+};
+// Writes vec and doc_range (each if not null) for one call.
+cudaError_t launch_scored_prep(float *vec, int far, int H, const BucketParams &bk, int2 *doc_range,
+                               const int32_t *doc_ids, int B, int T, cudaStream_t stream);
+
+struct ScoredFwdParams {
+    int B, H, Hkv, Tq, Tk;
+    ScoreParams f;
+    VisParams vis;
+    __nv_bfloat16 *o;  // (B, H, Tq, 64)
+    float *lse;        // optional (B, H, Tq)
+    __nv_bfloat16 *o_lo;  // optional with lse, (B, H, Tq, 64): what rounding took from o
+    int num_qblocks, total_items;
+    int *status;
+    // Decoding over a shared prefix (part_o not null): the keys are the
+    // prefix's (Tk of them), a K/V head's query rows of all batch entries are
+    // stacked, and each of `splits` key ranges leaves unnormalised partial
+    // sums instead of an output.
+    const int32_t *cache_lens;  // (B) or null: cache_cap rows everywhere
+    int cache_cap;
+    int splits, split_tiles;    // key ranges, 128-key tiles per range
+    int row_tiles;              // 128-row tiles per K/V head
+    float *part_o;              // (splits, B, H, Tq, 64)
+    float2 *part_ml;            // (splits, B, H, Tq): reference in log2 units, sum
+};
+// q: 3-D map (64, Tq, B H) -- decoding: 4-D (64, g Tq, B, Hkv), box of
+// decode_rows(); k, v: 3-D maps (64, Tk, B Hkv); 128-byte swizzling.
+cudaError_t launch_attn_scored(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, bool capped,
+                               int bias, const ScoredFwdParams &p, cudaStream_t stream, bool pdl);
+
+// How the g Tq query rows of a K/V head and batch entry are stacked into
+// 128-row tiles: `per` rows of each of `nb` batch entries, `chunks` tiles per
+// batch entry when they are more than 128.
+struct DecodeRows {
+    int per, nb, chunks;
+};
+inline __host__ __device__ DecodeRows decode_rows(int rows) {
+    DecodeRows d;
+    d.per = rows < 128 ? rows : 128;
+    d.nb = 128 / d.per;
+    d.chunks = (rows + 127) / 128;
+    return d;
+}
+
+struct ScoredBwdParams {
+    int B, H, Hkv, Tq, Tk, Tq_pad;
+    float scale;
+    ScoreParams f;
+    VisParams vis;
+    const float *nlse2, *dvec;  // as BwdParams
+    float *dq_acc;
+    __nv_bfloat16 *dk, *dv;     // (B, Hkv, Tk, 64)
+    // bucket bias gradient (null: none): sums of dS over equal distances
+    float *diag;                // (B, H, key blocks, near_slots, 256)
+    float *far_sum;             // (B, H, key blocks, 2): past, future distances beyond `near_slots`
+    int near_blocks, near_slots;
+    int *status;
+};
+cudaError_t launch_attn_scored_bwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                   const CUtensorMap &tg, bool capped, int bias, const ScoredBwdParams &p,
+                                   cudaStream_t stream);
+
+// dtable (num [* 2], H) from the backward's sums; sums: (H, 2 near + 1, 256) scratch.
+cudaError_t launch_scored_dtable(const float *diag, const float *far_sum, float *sums, __nv_bfloat16 *dtable, int B, int H,
+                                 int n_kb, int n_qb, int near, int near_slots, const BucketParams &bk,
+                                 cudaStream_t stream);
+
+// ------------------------------------------------ decoding over a shared prefix: the requests' own caches
+constexpr int kSmsPerGpu = 152;  // for the choice of splits, which fixes the workspace
+struct DecodeSharedParams {
+    int B, H, Hkv, Tq, Tk;
+    int capped, causal;
+    ScoreParams f;
+    const int32_t *cache_lens;
+    const __nv_bfloat16 *q, *k, *v;  // (B, H, Tq, 64), (B, Hkv, Tk, 64) twice
+    __nv_bfloat16 *o;
+    int prefix_splits;               // as ScoredFwdParams
+    const float *part_o;
+    const float2 *part_ml;
+};
+cudaError_t launch_decode_shared(const DecodeSharedParams &p, int bias, cudaStream_t stream);
+
 // ------------------------------------------------ positional encoding
 // out (rows, D) = x + PE(pos0 + row % T); D % 8 == 0; x and out may alias.
 cudaError_t launch_posenc_add_bf16(const __nv_bfloat16 *x, __nv_bfloat16 *out, long long rows, int T,
@@ -166,6 +280,11 @@ cudaError_t sm_count(int *sms);
 // Records "what: detail" as the calling thread's mha_last_error() text and
 // returns MHA_ERR_CUDA.
 mha_status record_cuda_failure(const char *what, const char *detail);
+
+// Tensor maps: (BH, T, 64) heads in 128-row boxes; the query rows of decoding,
+// (B, Hkv, rows, 64) in boxes of dr.per rows of dr.nb batch entries.
+mha_status encode_heads_map(CUtensorMap *m, const void *base, long long BH, int T);
+mha_status encode_stacked_rows_map(CUtensorMap *m, const void *base, int B, int Hkv, int rows, const DecodeRows &dr);
 
 // ------------------------------------ output projection + residual + LayerNorm
 constexpr int kLnMaxCluster = 8;  // CTAs per 128-row block (portable cluster size)
