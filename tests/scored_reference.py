@@ -24,8 +24,8 @@ U = 2.0 ** -8
 
 def score_error(cap, s_abs):
     """Bound of the error of one score: fp32 products and sums of 64 terms and the bias (2^-18 of the magnitudes),
-    the capping polynomial (2.8e-6 cap), 2^x (2^-21 relative)."""
-    return 2.0 ** -18 * s_abs + 3e-6 * (cap or 0.0) + 2.0 ** -20
+    the capping polynomials (2.2e-5 of a score below cap / 2, 2.2e-6 cap above), 2^x (2^-21 relative)."""
+    return 2.0 ** -18 * s_abs + ((2.2e-5 * s_abs).clamp(max=1.1e-5 * cap) + 3e-6 * cap if cap else 0.0) + 2.0 ** -20
 
 
 def bucket_of(d, starts, both):

@@ -83,9 +83,21 @@ mha_status check_form(const mha_score_form *form, float scale, int mask, bool de
     out.f.cap_in = out.capped ? scale / form->cap : 0.f;
     out.f.mul = out.capped ? form->cap * kLog2e : scale * kLog2e;
     if (!isfinite(out.f.cap_in) || !isfinite(out.f.mul)) return MHA_ERR_INVALID_ARG;
+    if (out.capped) {
+        // degree-2 fit of tanh(x) / x in x^2 over [0, 0.25] (scores.cuh)
+        constexpr double kNear[3] = {0.999978295, -0.331718863, 0.115318969};
+        const double a = out.f.cap_in;
+        double pow = out.f.mul * a;
+        for (int i = 0; i < 3; ++i, pow *= a * a) out.f.near[i] = static_cast<float>(kNear[i] * pow);
+        const double most = 0.25 / (a * a);
+        // the products of the polynomial stay within fp32's normal range
+        if (fabs(static_cast<double>(out.f.near[2])) > 1e-36 && fabs(out.f.near[2]) < 1e36f && most > 1e-18 && most < 1e18)
+            out.f.near_max = static_cast<float>(most);
+    }
     // A masked score is u = -inf before the multiplication by mul: with scale
     // 0 a factor that makes every other product vanish beside 1 keeps it so.
     if (out.f.mul == 0.f) out.f.mul = 1e-37f;
+    // The capped forward masks after its scores are multiplied: mul > 0 there.
     out.f.masked = out.f.mul < 0.f ? INFINITY : -INFINITY;
     out.f.slopes = form->slopes;
     out.bk.table = static_cast<const __nv_bfloat16 *>(form->table);

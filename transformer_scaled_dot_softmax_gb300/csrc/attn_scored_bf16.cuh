@@ -4,9 +4,12 @@
 // shared by groups of query heads; and, as the same kernel over other rows,
 // the partial sums of decoding rows against a prefix that a batch shares.
 //
-// Mathematics: the online softmax of attn_bf16.cu.  A row keeps a reference
-// m (log2 units) and a sum l; P = 2^(y - m), O += P V; only a round whose sum
-// leaves [0, 2^16] takes the exact step (new maximum, O and l scaled).  What a
+// Mathematics: the online softmax.  A row keeps a reference m (log2 units)
+// and a sum l; P = 2^(y - m), O += P V.  Softmax does not change with m, so the
+// first one is simply 0, and only a row whose weights leave the window
+// [2^-64, 2^64] moves it, by the exact step: m += the whole part of the
+// round's maximum, and what was summed so far (O, l, P not yet multiplied) is
+// scaled by that power of two, without rounding.  What a
 // row sees is one interval of keys [lo, hi): the causal mask, key padding,
 // prefixes and documents all end in one, so a tile is masked by two
 // comparisons per key, and only tiles that some row sees in part are.
@@ -24,8 +27,9 @@
 //     down from there, then up: with a distance bias the largest scores come
 //     first, so the reference is set once instead of growing from tile to
 //     tile (a rescale of O each);
-//   * the score transform runs on the 64 scores a thread holds, in registers,
-//     packed two by two (scores.cuh);
+//   * a softmax thread takes a round of 64 scores in one straight line where
+//     it is a common one (every key seen, the bias an arithmetic progression,
+//     capped scores in the polynomials' range), any other 32 by 32;
 //   * V rows past the key length are cleared in shared memory before they are
 //     multiplied by their zero weights, so that what a padded buffer holds
 //     there (NaN included) never reaches the output.
@@ -36,6 +40,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "scores.cuh"
@@ -58,8 +64,10 @@ constexpr int kOutWarp = 12;
 constexpr uint32_t kTileBytes = BM * HD * 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 384;
-constexpr float kRoundSumLimit = 65536.0f;                // 2^16
-constexpr float kFirstSumMin = 5.421010862427522e-20f;    // 2^-64
+// A row's reference serves while the sums of its rounds' weights lie in
+// [2^-64, 2^64]: weights, sums and O are floats, so that their common scale
+// costs no precision, and 2^64 times any length stays far from overflow.
+constexpr float kSumMin = 5.421010862427522e-20f, kSumMax = 1.8446744073709552e19f;
 constexpr int kItemTable = 128;
 
 // What the kernel computes.
@@ -92,6 +100,7 @@ struct __align__(1024) Smem {
     uint64_t ml_full, ml_free, o_final, o_free;
     uint64_t drain[3];
     Item item_tab[kItemTable];
+    Item item_own[kThreads / 32];
     int n_items;
     uint32_t tmem_base;
     int abort_flag;
@@ -162,10 +171,16 @@ __device__ __forceinline__ int tile_of(const Item &it, int t) {
     return t <= down ? it.jd - t : it.j0 + t;
 }
 
+// The CTA's t-th item, in shared memory (read there when needed rather than
+// held in registers); past the table each warp computes its own.
 template <int kMode>
-__device__ __forceinline__ Item item_of(const Smem &sm, const ScoredFwdParams &p, int t, int cta, int G) {
-    if (t >= kItemTable) return make_item<kMode>(p, item_index(t, cta, G));
-    return sm.item_tab[t];
+__device__ __forceinline__ const Item &item_of(Smem &sm, const ScoredFwdParams &p, int t, int cta, int G) {
+    if (t < kItemTable) return sm.item_tab[t];
+    Item &own = sm.item_own[threadIdx.x >> 5];
+    __syncwarp(__activemask());
+    own = make_item<kMode>(p, item_index(t, cta, G));  // every lane writes the same
+    __syncwarp(__activemask());
+    return own;
 }
 
 // What a thread's row (r of the item's 128) is.
@@ -275,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 0, v = 0;  // key tiles and items so far
             bool ok = true;
             for (int t = 0; ok && t < sm.n_items; ++t) {
-                const Item it = item_of<kMode>(sm, p, t, cta, G);
+                const Item &it = item_of<kMode>(sm, p, t, cta, G);
                 if (it.n_kv == 0) continue;
                 const int qbuf = v & 1;
                 if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0, v = 0;
         bool ok = true;
         for (int t = 0; ok && t < sm.n_items; ++t) {
-            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            const Item &it = item_of<kMode>(sm, p, t, cta, G);
             if (it.n_kv == 0) continue;
             if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
             for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
@@ -394,59 +409,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = static_cast<int>(lane_base) + lane;
         const uint32_t tl = tmem_addr(tmem, lane_base, 0);
         const uint32_t to = tl + kOCol + 64u * half;
-        // With the log-sum-exp exported the first reference is the row's own
-        // maximum; otherwise a first round is tried against 0.
-        constexpr bool guess_first = kMode != kForwardLse;
-
-        // 2^y of a round in bf16 and the fp32 sum of the rounded weights (the
-        // values P V multiplies, so that normalised weights sum to 1).
-        // exact: with lse, the sum of the unrounded ones.
-        auto exp_round = [](const uint32_t(&a)[32], const uint32_t(&b)[32], float off, uint32_t(&pk)[32],
-                            float &exact) -> float {
-            const uint64_t off2 = f32x2_set(off);
-            uint64_t ex[2] = {0, 0};
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        // 2^y of 32 scores in bf16 and the fp32 sum of the rounded weights (the
+        // values P V multiplies, so that normalised weights sum to 1); exact:
+        // with lse, the sum of the unrounded ones.
+        auto weigh = [](const uint32_t(&y)[32], uint32_t(&pk)[16], float &exact) -> float {
+            uint64_t ex = 0;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                float x0, x1, x2, x3;
-                f32x2_unpack(add_f32x2(f32x2_pack(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])), off2), x0, x1);
-                f32x2_unpack(add_f32x2(f32x2_pack(__uint_as_float(b[2 * c]), __uint_as_float(b[2 * c + 1])), off2), x2, x3);
-                x0 = ex2_approx(x0);
-                x1 = ex2_approx(x1);
-                x2 = ex2_approx(x2);
-                x3 = ex2_approx(x3);
+                const float x0 = ex2_approx(__uint_as_float(y[2 * c])), x1 = ex2_approx(__uint_as_float(y[2 * c + 1]));
                 pk[c] = pack_bf16x2(x0, x1);
-                pk[16 + c] = pack_bf16x2(x2, x3);
-                if (kMode == kForwardLse) {
-                    ex[0] = add_f32x2(ex[0], f32x2_pack(x0, x1));
-                    ex[1] = add_f32x2(ex[1], f32x2_pack(x2, x3));
-                }
+                if (kMode == kForwardLse) ex = add_f32x2(ex, f32x2_pack(x0, x1));
                 add_bf16x2_to_f32(acc[2 * (c & 1)], acc[2 * (c & 1) + 1], pk[c]);
-                add_bf16x2_to_f32(acc[4 + 2 * (c & 1)], acc[5 + 2 * (c & 1)], pk[16 + c]);
             }
             if (kMode == kForwardLse) {
                 float e0, e1;
-                f32x2_unpack(add_f32x2(ex[0], ex[1]), e0, e1);
+                f32x2_unpack(ex, e0, e1);
                 exact = e0 + e1;
             }
-            return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+            return (acc[0] + acc[1]) + (acc[2] + acc[3]);
         };
-        auto row_max = [](const uint32_t(&a)[32], const uint32_t(&b)[32]) -> float {
-            float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+        // The common round, load to packed weights in one straight line:
+        // y = u mul + b0 + c step.  a: its first 16 scores, on their way from
+        // tensor memory; the others follow 16 by 16 while the ones before them
+        // are worked on, and `next` starts the first of the round after it.  kind 0: no cap, 1: near, 2: wide range; big: the
+        // largest squared argument of the polynomial.
+        auto common_round = [&](auto kind, uint32_t tr, uint32_t(&a)[16], bool next, float b0, float step,
+                                uint32_t(&pk)[32], float &exact, float &big) -> float {
+            constexpr int kKind = decltype(kind)::value;
+            uint32_t b16[16];
+            const uint64_t mul2 = f32x2_set(kKind == 2 ? p.f.cap_in : p.f.mul);
+            const uint64_t n0 = f32x2_set(p.f.near[0]), n1 = f32x2_set(p.f.near[1]), n2 = f32x2_set(p.f.near[2]);
+            const TanhWide poly(p.f.mul);
+            constexpr int kChains = kBias == kBiasSlopes ? 4 : 1;
+            uint64_t b[kChains];
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-                t0 = fmax3(t0, __uint_as_float(a[c]), __uint_as_float(a[c + 1]));
-                t1 = fmax3(t1, __uint_as_float(a[c + 2]), __uint_as_float(a[c + 3]));
-                t2 = fmax3(t2, __uint_as_float(b[c]), __uint_as_float(b[c + 1]));
-                t3 = fmax3(t3, __uint_as_float(b[c + 2]), __uint_as_float(b[c + 3]));
+            for (int i = 0; i < kChains; ++i) b[i] = f32x2_pack(fmaf(2.f * i, step, b0), fmaf(2.f * i + 1.f, step, b0));
+            const uint64_t step2 = f32x2_set(8.f * step);
+            uint64_t ex = 0;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float big0 = 0.f, big1 = 0.f;
+            auto take = [&](const uint32_t(&sc)[16], int part) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint64_t s2 = f32x2_pack(__uint_as_float(sc[2 * c]), __uint_as_float(sc[2 * c + 1]));
+                    uint64_t y;
+                    if (kKind == 0) {
+                        y = fma_f32x2(s2, mul2, b[c % kChains]);
+                    } else {
+                        const uint64_t x = kKind == 1 ? s2 : mul_f32x2(s2, mul2), sq = mul_f32x2(x, x);
+                        float w0, w1;
+                        f32x2_unpack(sq, w0, w1);
+                        if (c & 1)
+                            big1 = fmax3(big1, w0, w1);
+                        else
+                            big0 = fmax3(big0, w0, w1);
+                        const uint64_t pol = kKind == 1 ? fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0) : poly(sq);
+                        y = fma_f32x2(x, pol, b[c % kChains]);
+                    }
+                    if (kBias == kBiasSlopes) b[c % kChains] = add_f32x2(b[c % kChains], step2);
+                    float x0, x1;
+                    f32x2_unpack(y, x0, x1);
+                    x0 = ex2_approx(x0);
+                    x1 = ex2_approx(x1);
+                    const uint32_t w = pack_bf16x2(x0, x1);
+                    pk[8 * part + c] = w;
+                    if (kMode == kForwardLse) ex = add_f32x2(ex, f32x2_pack(x0, x1));
+                    add_bf16x2_to_f32(acc[2 * (c & 1)], acc[2 * (c & 1) + 1], w);
+                }
+            };
+            tmem_ld_wait(a);
+            tmem_ld16(tr + 16, b16);
+            take(a, 0);
+            tmem_ld_wait(b16);
+            tmem_ld16(tr + 32, a);
+            take(b16, 1);
+            tmem_ld_wait(a);
+            tmem_ld16(tr + 48, b16);
+            take(a, 2);
+            tmem_ld_wait(b16);
+            if (next) tmem_ld16(tr + 64, a);
+            take(b16, 3);
+            if (kMode == kForwardLse) {
+                float e0, e1;
+                f32x2_unpack(ex, e0, e1);
+                exact = e0 + e1;
             }
-            return fmaxf(fmax3(t0, t1, t2), t3);
+            big = fmaxf(big0, big1);
+            return (acc[0] + acc[1]) + (acc[2] + acc[3]);
         };
 
         int n = 0, v = 0;
         bool ok = true;
         for (int t = 0; ok && t < sm.n_items; ++t) {
-            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            const Item &it = item_of<kMode>(sm, p, t, cta, G);
             if (it.n_kv == 0) continue;
             const Row w = make_row<kMode>(p, it, r);
             const BiasRow br = bias_row<kBias>(p.f, w.head);
@@ -454,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_live = kMode != kDecode || __any_sync(0xffffffffu, w.live);
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
             float l_run = 0.f, e_run = 0.f;
+            // the range the warp's capped scores need: near, wide, any
+            int tier = kCap && p.f.near_max == 0.f ? 1 : 0;
 
             for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
                 if ((n & 1) != half) continue;
@@ -464,115 +522,157 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
                 const bool edge = j * BN < it.full_lo || j * BN + BN > it.full_hi;
+                float b_tile, step;  // bias of the tile's key c: b_tile + c step, if `linear`
+                const bool linear = linear_bias<kBias>(p.f, br, j * BN - w.pos, BN, 0.f, b_tile, step);
+                uint32_t a[16];
+                tmem_ld16(ts, a);
 #pragma unroll 1
                 for (int rd = 0; rd < 2; ++rd) {
-                    const int key0 = j * BN + 64 * rd;  // the round's first key
-                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
-                    // y - ref of the round's scores, masked ones -inf
-                    auto load_scores = [&](uint32_t(&s0)[32], uint32_t(&s1)[32], float ref) {
-                        tmem_ld32(tr, s0);
-                        tmem_ld32(tr + 32, s1);
-                        tmem_ld_wait(s0);
-                        reg_fence32(s1);
-                        const int lo = w.keys.x - key0, hi = w.keys.y - key0;
-                        auto mask_to = [&](float value) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (c < lo || c >= hi) s0[c] = __float_as_uint(value);
-                                if (c + 32 < lo || c + 32 >= hi) s1[c] = __float_as_uint(value);
-                            }
-                        };
-                        if (kCap) {
-                            // masked scores have no say in how tanh is taken
-                            if (edge) mask_to(0.f);
-                            const float big = fmaxf(max_abs(s0), max_abs(s1));
-                            const bool any = __any_sync(0xffffffffu, (kMode != kDecode || w.live) &&
-                                                                         big * fabsf(p.f.cap_in) > kTanhRange);
-                            cap_scores(s0, p.f.cap_in, any);
-                            cap_scores(s1, p.f.cap_in, any);
-                        }
-                        if (edge) mask_to(p.f.masked);
-                        add_bias<kBias, 1>(s0, p.f, br, key0 - w.pos, -ref);
-                        add_bias<kBias, 1>(s1, p.f, br, key0 + 32 - w.pos, -ref);
+                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd), tp = ts + 32u * static_cast<uint32_t>(rd);
+                    // Does the row need the exact step after a sum against
+                    // the reference in hand (0 before there is one)?  first,
+                    // len: the keys summed.
+                    auto sees_none = [&](int first, int len) {
+                        return w.keys.x >= first + len || w.keys.y <= first || (kMode == kDecode && !w.live);
                     };
-                    uint32_t pk[32];
-                    float lt = 0.f, et = 0.f;
-                    if (warp_live) {
-                        bool need = true;
-                        if (guess_first || jt >= 2 || rd == 1) {
-                            uint32_t s0[32], s1[32];
-                            load_scores(s0, s1, m_run == -INFINITY ? 0.f : m_run);
-                            lt = exp_round(s0, s1, 0.f, pk, et);
-                            need = m_run == -INFINITY
-                                       ? !(guess_first && lt >= kFirstSumMin && lt <= kRoundSumLimit)
-                                       : !(lt <= kRoundSumLimit);
-                            if (!need && m_run == -INFINITY) m_run = 0.f;
-                            // nothing visible in the round: weights 0, no reference
-                            if (w.keys.x >= key0 + 64 || w.keys.y <= key0) need = false;
+                    auto judge = [&](float sum, bool none) -> bool {
+                        if (none) return false;
+                        if (m_run != -INFINITY) return !(sum <= kSumMax);
+                        if (!(sum >= kSumMin && sum <= kSumMax)) return true;
+                        m_run = 0.f;
+                        return false;
+                    };
+                    const int key0 = j * BN + 64 * rd;  // the round's first key
+                    bool done = false;
+                    if (linear && (!kCap || tier < 2) && warp_live &&
+                        (!edge || __all_sync(0xffffffffu, w.keys.x <= key0 && w.keys.y >= key0 + 64))) {
+                        uint32_t pk[32];
+                        const float ref = m_run == -INFINITY ? 0.f : m_run;
+                        // -ref and the bias's large part meet in one fused
+                        // multiply-add: far distances lose nothing
+                        const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(key0 - w.pos), -ref)
+                                                              : b_tile - ref;
+                        float lt, et = 0.f, big = 0.f;
+                        if (!kCap)
+                            lt = common_round(std::integral_constant<int, 0>{}, tr, a, rd == 0, b0, step, pk, et, big);
+                        else if (tier == 0)
+                            lt = common_round(std::integral_constant<int, 1>{}, tr, a, rd == 0, b0, step, pk, et, big);
+                        else
+                            lt = common_round(std::integral_constant<int, 2>{}, tr, a, rd == 0, b0, step, pk, et, big);
+                        if (kCap && kMode == kDecode && !w.live) big = 0.f;
+                        if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : kTanhWide * kTanhWide))) {
+                            ++tier;  // out of the polynomial's range: taken again below
+                        } else if (!__any_sync(0xffffffffu, judge(lt, kMode == kDecode && !w.live))) {
+                            tmem_st32(tp, pk);
+                            l_run += lt;
+                            e_run += et;
+                            done = true;
                         }
-                        // what shared memory held for a dead row decides nothing
-                        if (kMode == kDecode && !w.live) need = false;
-                        if (__any_sync(0xffffffffu, need)) {
-                            uint32_t s0[32], s1[32];
-                            const float ref = m_run == -INFINITY ? 0.f : m_run;
-                            load_scores(s0, s1, ref);
-                            float alpha = 1.f;
-                            if (need) {
-                                const float up = row_max(s0, s1);  // above ref
-                                float off = 0.f;
-                                if (m_run == -INFINITY) {
-                                    if (up != -INFINITY) {
-                                        m_run = up;
-                                        off = -up;
-                                    }
-                                } else if (up > 0.f) {
-                                    const float m_new = m_run + up;
-                                    off = m_run - m_new;
-                                    alpha = ex2_approx(off);
-                                    m_run = m_new;
-                                    l_run *= alpha;
-                                    e_run *= alpha;
-                                }
-                                lt = exp_round(s0, s1, off, pk, et);
-                            }
-                            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                                // O_h holds the group's earlier tiles of the
-                                // item (and, in round 1, this tile's round 0,
-                                // taken against the old reference): wait for
-                                // the last product it took.
-                                bool scale_o = true;
-                                if (rd == 1) {
-                                    ok = __all_sync(0xffffffffu,
-                                                    mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
-                                } else if (jt >= 2) {
-                                    const int np = n - 2;
-                                    ok = __all_sync(0xffffffffu,
-                                                    mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
-                                } else {
-                                    scale_o = false;
-                                }
-                                if (!ok) break;
-                                if (scale_o) {
-                                    tc_fence_after_sync();
+                    } else {
+                        tmem_ld_wait(a);
+                        if (rd == 0) tmem_ld16(tr + 64, a);
+                    }
+                    // Every other round, 32 keys at a time.
 #pragma unroll 1
-                                    for (int part = 0; part < 4; ++part) {
-                                        uint32_t o0[16];
-                                        tmem_ld16(to + 16u * static_cast<uint32_t>(part), o0);
-                                        tmem_ld_wait(o0);
+                    for (int h = done ? 2 : 0; h < 2; ++h) {
+                        const int kh = key0 + 32 * h;
+                        const bool none = sees_none(kh, 32);
+                        uint32_t pk[16];
+                        float lt = 0.f, et = 0.f, alpha = 1.f;
+                        if (__all_sync(0xffffffffu, none)) {
 #pragma unroll
-                                        for (int c = 0; c < 16; ++c)
-                                            o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
-                                        tmem_st16(to + 16u * static_cast<uint32_t>(part), o0);
-                                        tmem_st_wait();
-                                    }
+                            for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                        } else {
+                            const bool all = __all_sync(0xffffffffu, w.keys.x <= kh && w.keys.y >= kh + 32);
+                            bool need = false;
+                            // attempt 0 against the reference in hand; where a
+                            // row needs the exact step, 1 moves its reference
+                            // and 2 takes the keys again
+#pragma unroll 1
+                            for (int attempt = 0;; ++attempt) {
+                                uint32_t y[32];
+                                tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
+                                tmem_ld_wait(y);
+                                const int lo = w.keys.x - kh, hi = w.keys.y - kh;
+                                auto mask_to = [&](float value) {
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c)
+                                        if (c < lo || c >= hi) y[c] = __float_as_uint(value);
+                                };
+                                if (kCap) {
+                                    // masked scores have no say in how tanh is taken
+                                    if (!all) mask_to(0.f);
+                                    cap_scores(y, p.f.cap_in, p.f.mul,
+                                               __all_sync(0xffffffffu, (kMode == kDecode && !w.live) ||
+                                                                           max_abs(y) * fabsf(p.f.cap_in) <= kTanhWide));
                                 }
+                                if (!all) mask_to(p.f.masked);
+                                add_bias<kBias, 1, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
+                                if (attempt == 1) {
+                                    if (need) {
+                                        float up = -INFINITY;  // above the reference
+#pragma unroll
+                                        for (int c = 0; c < 32; c += 2)
+                                            up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                        up = ceilf(up);
+                                        if (m_run == -INFINITY) {
+                                            m_run = up;
+                                        } else if (up > 0.f) {
+                                            m_run += up;
+                                            alpha = ex2_approx(-up);
+                                            l_run *= alpha;
+                                            e_run *= alpha;
+                                        }
+                                    }
+                                    continue;
+                                }
+                                lt = weigh(y, pk, et);
+                                if (attempt == 2) break;
+                                need = judge(lt, none);
+                                if (!__any_sync(0xffffffffu, need)) break;
                             }
                         }
-                        tmem_st32(ts + 32u * static_cast<uint32_t>(rd), pk);
+                        tmem_st16(tp + 16u * static_cast<uint32_t>(h), pk);
                         l_run += lt;
                         e_run += et;
-                        tmem_st_wait();
+                        if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
+                        // What was summed before moves with the reference: the
+                        // round's first 32 weights, which wait to be multiplied
+                        // with these, and O_h, which holds the group's earlier
+                        // tiles of the item and, in round 1, this tile's round
+                        // 0: wait for the last product it took.
+                        if (h == 1) {
+                            tmem_st_wait();
+                            tmem_ld16(tp, pk);
+                            tmem_ld_wait(pk);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
+                                                    __uint_as_float(pk[c] & 0xffff0000u) * alpha);
+                            tmem_st16(tp, pk);
+                        }
+                        if (rd == 1) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
+                        } else if (jt >= 2) {
+                            const int np = n - 2;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
+                        } else {
+                            continue;  // O_h holds nothing of this item
+                        }
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t o0[32];
+                            tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                            tmem_ld_wait(o0);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
+                            tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                        }
                     }
+                    if (!ok) break;
+                    tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
@@ -597,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int v = 0;
         bool ok = true;
         for (int t = 0; ok && t < sm.n_items; ++t) {
-            const Item it = item_of<kMode>(sm, p, t, cta, G);
+            const Item &it = item_of<kMode>(sm, p, t, cta, G);
             const Row w = make_row<kMode>(p, it, r);
             const bool row_ok = in_bounds(w.out >= 0 && w.out < static_cast<long long>(p.B) * p.H * p.Tq, p.status) && w.live;
             if (it.n_kv == 0) {

@@ -86,11 +86,11 @@ __device__ __forceinline__ void score_terms(uint32_t (&sv)[16], uint32_t (&dp)[1
             for (int e = 0; e < 16; ++e)
                 if (e < lo || e >= hi) sv[e] = 0u;
         }
-        cap_scores(sv, f.cap_in, __any_sync(0xffffffffu, max_abs(sv) * fabsf(f.cap_in) > kTanhRange));
+        cap_scores(sv, f.cap_in, 1.f, __all_sync(0xffffffffu, max_abs(sv) * fabsf(f.cap_in) <= kTanhWide));
 #pragma unroll
         for (int e = 0; e < 16; ++e) u[kCap ? e : 0] = sv[e];
     }
-    if (kBias != kBiasNone) add_bias<kBias, -1>(sv, f, br, d0, 0.f);
+    if (kBias != kBiasNone) add_bias<kBias, -1, false>(sv, f, br, d0, 0.f);
     const uint64_t mul2 = f32x2_set(f.mul), one2 = f32x2_set(1.f);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {

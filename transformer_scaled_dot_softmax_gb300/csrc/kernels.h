@@ -129,6 +129,9 @@ enum BiasKind { kBiasNone = 0, kBiasSlopes = 1, kBiasBuckets = 2 };
 struct ScoreParams {
     float cap_in;         // scale / cap (capped scores), else unused
     float mul;            // y = u mul + bias, u = q.k or tanh(q.k cap_in), y in log2 units; never 0
+    // Capped scores with |q.k cap_in| <= 0.5: y = s (near[0] + near[1] s^2 +
+    // near[2] s^4), s = q.k; s^2 <= near_max (0: not representable, unused).
+    float near[3], near_max;
     float masked;         // the u of a masked score: minus infinity times the sign of mul
     const float *slopes;  // (H) fp32, kBiasSlopes
     const float *vec;     // (H, 2 mid + 1) fp32 in log2 units, kBiasBuckets; written by scored_prep

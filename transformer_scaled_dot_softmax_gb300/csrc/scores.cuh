@@ -21,25 +21,37 @@ namespace mha {
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// tanh(x) for |x| <= 1 as x p(x^2), p of degree 4: least maximum error
-// fitted over [-1, 1], 2.8e-6 absolute, i.e. 1.4e-4 in a score capped at 50
-// (a weight's bf16 rounding is 3.9e-3 of it).  Seven packed operations per
-// pair and none on the special-function unit, which the weights' 2^x already
-// fill; scores past the cap itself (|x| > 1) are rare and take tanh_any.
-constexpr float kTanhRange = 1.0f;
-constexpr float kTanhP0 = 0.999968469f, kTanhP1 = -0.332658231f, kTanhP2 = 0.129220663f,
-                kTanhP3 = -0.0432998549f, kTanhP4 = 0.00836588231f;
-
 __device__ __forceinline__ uint64_t f32x2_set(float v) { return f32x2_pack(v, v); }
 
-__device__ __forceinline__ uint64_t tanh_small_x2(uint64_t x) {
-    const uint64_t w = mul_f32x2(x, x);
-    uint64_t p = fma_f32x2(w, f32x2_set(kTanhP4), f32x2_set(kTanhP3));
-    p = fma_f32x2(w, p, f32x2_set(kTanhP2));
-    p = fma_f32x2(w, p, f32x2_set(kTanhP1));
-    p = fma_f32x2(w, p, f32x2_set(kTanhP0));
-    return mul_f32x2(x, p);
-}
+// tanh(x) as x p(x^2), on the FMA pipe, two scores per operation, and nothing
+// on the special-function unit, which the weights' 2^x already fill.  Three
+// ranges, each a warp's choice by the largest score it holds:
+//   near  |x| <= 0.5, p of degree 2 fitted to the least relative error, 2.2e-5:
+//         at most 5.5e-4 in a score of 25, where one step of a weight's bf16
+//         is 3.9e-3 to 7.8e-3 of it.  The coefficients (ScoreParams.near) hold
+//         mul and the powers of cap_in, so that y = s p(s^2) + bias is four
+//         packed operations per pair of scores, three more than uncapped;
+//   wide  |x| <= 1.75, degree 7, least absolute error, 2.2e-6 in fp32 (1.1e-4
+//         in a score capped at 50): ten operations;
+//   any   tanh_any, two special-function operations per score.
+constexpr float kTanhNear = 0.5f, kTanhWide = 1.75f;
+
+// mul p(w) for w = x^2, the wide range: x times it is mul tanh(x).
+struct TanhWide {
+    uint64_t c[8];
+    __device__ __forceinline__ explicit TanhWide(float mul) {
+        constexpr float k[8] = {0.99997997f,   -0.332981028f,   0.131501142f,    -0.0495564923f,
+                                0.0158997465f, -0.00376142941f, 0.000550391496f, -3.62618914e-05f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = f32x2_set(mul * k[i]);
+    }
+    __device__ __forceinline__ uint64_t operator()(uint64_t w) const {
+        uint64_t p = fma_f32x2(w, c[7], c[6]);
+#pragma unroll
+        for (int i = 5; i >= 0; --i) p = fma_f32x2(w, p, c[i]);
+        return p;
+    }
+};
 
 // tanh(x) = 1 - 2 / (1 + e^(2x)) for any x (absolute error ~2^-22; e^(2x)
 // overflowing to infinity gives 1, underflowing to 0 gives -1).
@@ -47,23 +59,24 @@ __device__ __forceinline__ float tanh_any(float x) {
     return 1.f - __fdividef(2.f, 1.f + ex2_approx(x * (2.f * kLog2E)));
 }
 
-// u = tanh(s cap_in) of N scores in place; `any_large` (warp-uniform): some
-// |s cap_in| of the warp is past kTanhRange.
+// s := mul tanh(s cap_in) of N scores in place.  wide (warp-uniform): no
+// |s cap_in| of the warp is past kTanhWide.
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float cap_in, bool any_large) {
-    if (any_large) {
-#pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(tanh_any(__uint_as_float(s[c]) * cap_in));
-    } else {
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float cap_in, float mul, bool wide) {
+    if (wide) {
         const uint64_t a2 = f32x2_set(cap_in);
+        const TanhWide poly(mul);
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
+            const uint64_t x = mul_f32x2(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), a2);
             float t0, t1;
-            f32x2_unpack(tanh_small_x2(mul_f32x2(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), a2)), t0,
-                         t1);
+            f32x2_unpack(mul_f32x2(x, poly(mul_f32x2(x, x))), t0, t1);
             s[c] = __float_as_uint(t0);
             s[c + 1] = __float_as_uint(t1);
         }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(mul * tanh_any(__uint_as_float(s[c]) * cap_in));
     }
 }
 
@@ -81,27 +94,57 @@ __device__ __forceinline__ float max_abs(const uint32_t (&s)[N]) {
 
 // One thread's bias: of head `h`.
 struct BiasRow {
-    float slope2;      // slope log2 e
-    const float *vec;  // vec[d]
+    float slope2;        // slope log2 e
+    const float *vec;    // vec[d]
+    float past, future;  // vec of the distances past `far`
 };
 
 template <int kBias>
 __device__ __forceinline__ BiasRow bias_row(const ScoreParams &f, int h) {
-    BiasRow r{0.f, nullptr};
+    BiasRow r{0.f, nullptr, 0.f, 0.f};
     if (kBias == kBiasSlopes) r.slope2 = f.slopes[h] * kLog2E;
-    if (kBias == kBiasBuckets) r.vec = f.vec + static_cast<long long>(h) * (2 * f.mid + 1) + f.mid;
+    if (kBias == kBiasBuckets) {
+        r.vec = f.vec + static_cast<long long>(h) * (2 * f.mid + 1) + f.mid;
+        r.past = r.vec[-f.mid];
+        r.future = r.vec[f.mid];
+    }
     return r;
 }
 
-// y = u mul + bias(d0 + kStep c) + add of N values in place, c = 0 .. N-1,
+// The bias of a run of keys as an arithmetic progression b0 + c step, c = 0 ..
+// n-1, where it is one for every lane of the warp; returns whether it is.
+template <int kBias>
+__device__ __forceinline__ bool linear_bias(const ScoreParams &f, const BiasRow &r, int d0, int n, float add, float &b0,
+                                            float &step) {
+    step = 0.f;
+    b0 = add;
+    if (kBias == kBiasNone) return true;
+    const int lim = kBias == kBiasSlopes ? 0 : f.far;
+    const bool past = __all_sync(0xffffffffu, d0 + n - 1 <= -lim || (kBias == kBiasSlopes && f.past_only));
+    if (!past && !__all_sync(0xffffffffu, d0 >= lim)) return false;
+    if (kBias == kBiasSlopes) {
+        step = past ? r.slope2 : -r.slope2;
+        b0 = fmaf(step, static_cast<float>(d0), add);
+    } else {
+        b0 = (past ? r.past : r.future) + add;
+    }
+    return true;
+}
+
+// y = u mul + bias(d0 + kStep c) + add of N values in place, c = 0 .. N-1
+// (kScaled: u holds u mul already),
 // kStep = +1 (keys run along the registers) or -1 (queries do).  The lanes of
 // a warp hold one query (key) each with its own d0.  add: minus the reference
 // the weights are taken against; the bias's large part and `add` meet in one
 // fused multiply-add, so that far distances lose nothing to cancellation.
-template <int kBias, int kStep, int N>
+template <int kBias, int kStep, bool kScaled, int N>
 __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f, const BiasRow &r, int d0,
                                          float add) {
     const uint64_t mul2 = f32x2_set(f.mul);
+    auto fma2 = [&](uint64_t u2, uint64_t b2) { return kScaled ? add_f32x2(u2, b2) : fma_f32x2(u2, mul2, b2); };
+    auto fma1 = [&](uint32_t x, float b) {
+        return __float_as_uint(kScaled ? __uint_as_float(x) + b : fmaf(__uint_as_float(x), f.mul, b));
+    };
     auto at = [&](int c) { return f32x2_pack(__uint_as_float(u[c]), __uint_as_float(u[c + 1])); };
     auto put = [&](int c, uint64_t v) {
         float a, b;
@@ -113,7 +156,7 @@ __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f,
     if (kBias == kBiasNone) {
         const uint64_t add2 = f32x2_set(add);
 #pragma unroll
-        for (int c = 0; c < N; c += 2) put(c, fma_f32x2(at(c), mul2, add2));
+        for (int c = 0; c < N; c += 2) put(c, fma2(at(c), add2));
     } else if (kBias == kBiasSlopes) {
         const int dmin = kStep > 0 ? d0 : d0 + kEnd, dmax = kStep > 0 ? d0 + kEnd : d0;
         const bool past = __all_sync(0xffffffffu, dmax <= 0 || f.past_only);
@@ -127,29 +170,28 @@ __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f,
             const uint64_t step = f32x2_set(8.f * st);
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
-                put(c, fma_f32x2(at(c), mul2, b[(c >> 1) & 3]));
+                put(c, fma2(at(c), b[(c >> 1) & 3]));
                 if (c + 8 < N) b[(c >> 1) & 3] = add_f32x2(b[(c >> 1) & 3], step);
             }
         } else {
             const float df = static_cast<float>(d0);
 #pragma unroll
             for (int c = 0; c < N; ++c)
-                u[c] = __float_as_uint(
-                    fmaf(__uint_as_float(u[c]), f.mul, fmaf(-r.slope2, fabsf(df + static_cast<float>(kStep * c)), add)));
+                u[c] = fma1(u[c], fmaf(-r.slope2, fabsf(df + static_cast<float>(kStep * c)), add));
         }
     } else {
         const int dmin = kStep > 0 ? d0 : d0 + kEnd, dmax = kStep > 0 ? d0 + kEnd : d0;
         const bool past = __all_sync(0xffffffffu, dmax <= -f.far);
         if (past || __all_sync(0xffffffffu, dmin >= f.far)) {
-            const uint64_t add2 = f32x2_set(r.vec[past ? -f.mid : f.mid] + add);
+            const uint64_t add2 = f32x2_set((past ? r.past : r.future) + add);
 #pragma unroll
-            for (int c = 0; c < N; c += 2) put(c, fma_f32x2(at(c), mul2, add2));
+            for (int c = 0; c < N; c += 2) put(c, fma2(at(c), add2));
         } else {
             const int dc = kStep > 0 ? min(max(d0, -f.mid), f.far) : min(max(d0, -f.far), f.mid);
             const float *src = r.vec + dc;
 #pragma unroll
             for (int c = 0; c < N; ++c)
-                u[c] = __float_as_uint(fmaf(__uint_as_float(u[c]), f.mul, src[kStep * c] + add));
+                u[c] = fma1(u[c], src[kStep * c] + add);
         }
     }
 }
