@@ -110,8 +110,9 @@ def test_workspace_sizes(lib):
     assert b(2, 3, 130, 7, ctypes.addressof(t)) == (plain + r(3 * (2 * 164 + 1) * 4) + 2 * 3 * 1 * 2 * 1024 + r(2 * 3 * 8) +
                                                     3 * 3 * 1024)
     d = lib.lib.sdpa_decode_shared_workspace_bytes
-    assert d(4, 8, 2, 1, 0, None) == 0 and d(4, 8, 3, 1, 10, None) == 0
-    assert d(4, 8, 2, 1, 100, None) == 4 * 8 * 256 + r(4 * 8 * 8)
+    assert d(4, 8, 2, 1, 0, 0, None) == 0 and d(4, 8, 3, 1, 10, 10, None) == 0
+    assert d(4, 8, 2, 1, 100, 0, None) == 4 * 8 * 256 + r(4 * 8 * 8)     # one key range of the prefix
+    assert d(4, 8, 2, 1, 100, 90, None) == 2 * 4 * 8 * 256 + r(2 * 4 * 8 * 8)
 
 
 def test_relative_bucket_starts():

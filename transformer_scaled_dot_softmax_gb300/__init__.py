@@ -526,7 +526,7 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
         _check_dev("status", status, torch.int32)
     form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
     pf = ctypes.addressof(form)
-    workspace = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, pf), dev)
+    workspace = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
     rc = lib.sdpa_decode_shared_forward(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache),
                                         _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                         B, h, h_kv, T_q, T_p, T_k, d, d,

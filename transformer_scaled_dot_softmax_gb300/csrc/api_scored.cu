@@ -171,28 +171,35 @@ BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int T_q, int T_k) {
     return l;
 }
 
-// Key ranges of the prefix: as many as give the SMs equal numbers of items,
-// an item costing its tiles and about three more (its query rows, the first
-// tile's exact maximum, the partial sums).
+// Division of a decoding step's keys into ranges of `tiles` 128-key tiles each:
+// an item (a range of the prefix for 128 stacked rows, or of one cache) costs
+// its tiles and about three more (query rows, pipeline start, partial sums).
+// Few items go in whole rounds over the SMs, many even out.
 struct Splits {
-    int row_tiles, splits, split_tiles;
+    int row_tiles, prefix, cache, tiles;
+    size_t parts() const { return static_cast<size_t>(prefix) + cache; }
 };
-Splits prefix_splits(int B, int h, int h_kv, int T_q, int T_p) {
+Splits decode_splits(int B, int h, int h_kv, int T_q, int T_p, int T_k) {
     Splits s{};
-    if (T_p <= 0 || h <= 0 || B <= 0 || T_q <= 0) return s;
+    if (h <= 0 || B <= 0 || T_q <= 0) return s;
     const DecodeRows dr = decode_rows(h / h_kv * T_q);
     s.row_tiles = dr.chunks > 1 ? B * dr.chunks : (B + dr.nb - 1) / dr.nb;
-    const long long items = static_cast<long long>(h_kv) * s.row_tiles;
-    const int tiles = (T_p + 127) / 128;
+    const long long np = static_cast<long long>(h_kv) * s.row_tiles, nc = static_cast<long long>(h_kv) * B * dr.chunks;
+    const int tp = (T_p + 127) / 128, tc = (T_k + 127) / 128;
     long long best = -1;
-    for (int n = 1; n <= tiles && n <= 64; ++n) {
-        const int per = (tiles + n - 1) / n;
-        const int real = (tiles + per - 1) / per;
-        const long long cost = (items * real + kSmsPerGpu - 1) / kSmsPerGpu * (per + 3);
+    for (int n = 2; n <= 32; ++n) {
+        const int prefix = (tp + n - 1) / n, cache = (tc + n - 1) / n;
+        const long long items = np * prefix + nc * cache;
+        long long cost = np * (tp + 3 * prefix) + nc * (tc + 3 * cache);  // all items', in tiles
+        if (items <= 4 * kSmsPerGpu)
+            cost = (items + kSmsPerGpu - 1) / kSmsPerGpu * (n + 3) * kSmsPerGpu;
+        else
+            cost += static_cast<long long>(n) * kSmsPerGpu / 2;
         if (best < 0 || cost < best) {
             best = cost;
-            s.splits = real;
-            s.split_tiles = per;
+            s.prefix = prefix;
+            s.cache = cache;
+            s.tiles = n;
         }
     }
     return s;
@@ -226,10 +233,11 @@ MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const voi
 
     // T_k == 0: a one-row tensor that the kernel never loads
     const int Tk_map = T_k > 0 ? T_k : 1;
-    CUtensorMap tq, tk, tv;
-    if ((s = encode_heads_map(&tq, q, static_cast<long long>(B) * h, T_q)) != MHA_OK) return s;
-    if ((s = encode_heads_map(&tk, T_k > 0 ? k : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
-    if ((s = encode_heads_map(&tv, T_k > 0 ? v : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
+    ScoredMaps maps;
+    if ((s = encode_heads_map(&maps.q, q, static_cast<long long>(B) * h, T_q)) != MHA_OK) return s;
+    if ((s = encode_heads_map(&maps.k, T_k > 0 ? k : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
+    if ((s = encode_heads_map(&maps.v, T_k > 0 ? v : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
+    maps.q_cache = maps.k_cache = maps.v_cache = maps.q;
     ScoredFwdParams p{};
     bool prepared = false;
     if ((s = prepare(f, lay, workspace, B, h, T_k, p.f, p.vis, stream, &prepared)) != MHA_OK) return s;
@@ -246,7 +254,7 @@ MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const voi
     p.num_qblocks = (T_q + 127) / 128;
     p.total_items = B * h * p.num_qblocks;
     p.status = status_dev;
-    return launched(launch_attn_scored(tq, tk, tv, f.capped, f.bias, p, stream, prepared), "scored attention launch");
+    return launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "scored attention launch");
 }
 
 MHA_EXPORT size_t sdpa_scored_backward_workspace_bytes(int B, int h, int T_q, int T_k, const mha_score_form *form) {
@@ -332,13 +340,14 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
                     "bias table gradient launch");
 }
 
-MHA_EXPORT size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p, const mha_score_form *form) {
+MHA_EXPORT size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p, int T_k,
+                                                     const mha_score_form *form) {
     Form f;
-    if (B < 0 || h < 0 || h_kv < 0 || T_q < 0 || T_p < 0 || !form_sizes(form, f)) return 0;
+    if (B < 0 || h < 0 || h_kv < 0 || T_q < 0 || T_p < 0 || T_k < 0 || !form_sizes(form, f)) return 0;
     if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return 0;
     const size_t rows = static_cast<size_t>(B) * h * T_q;
-    const Splits sp = prefix_splits(B, h, h_kv, T_q, T_p);
-    return f.vec_bytes(h) + round256(sp.splits * rows * 256) + round256(sp.splits * rows * 8);
+    const size_t parts = decode_splits(B, h, h_kv, T_q, T_p, T_k).parts();
+    return f.vec_bytes(h) + round256(parts * rows * 256) + round256(parts * rows * 8);
 }
 
 MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_prefix, const void *v_prefix,
@@ -354,7 +363,6 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
     if (static_cast<long long>(T_p) + T_k >= kMaxLength) return MHA_ERR_UNSUPPORTED;
     if ((s = check_form(form, scale, mask, true, T_q, T_k, f)) != MHA_OK) return s;
     if ((mask & MHA_MASK_KEY_PADDING) && !cache_lens) return MHA_ERR_INVALID_ARG;
-    if (h > 0 && static_cast<long long>(B) * h_kv * 8 >= (1ll << 31)) return MHA_ERR_UNSUPPORTED;
     if (B == 0 || h == 0 || T_q == 0) return MHA_OK;
     if (!q || !o || (T_k > 0 && (!k_cache || !v_cache)) || (T_p > 0 && (!k_prefix || !v_prefix))) return MHA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(o) || (T_k > 0 && (!aligned16(k_cache) || !aligned16(v_cache))) ||
@@ -362,57 +370,52 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
         return MHA_ERR_MISALIGNED;
     const int rows = h / h_kv * T_q;
     const size_t n_rows = static_cast<size_t>(B) * h * T_q;
-    const Splits sp = prefix_splits(B, h, h_kv, T_q, T_p);
-    if (static_cast<long long>(h_kv) * sp.row_tiles * sp.splits >= (1ll << 30)) return MHA_ERR_UNSUPPORTED;
-    const size_t at_o = f.vec_bytes(h), at_ml = at_o + round256(sp.splits * n_rows * 256);
-    const size_t need = at_ml + round256(sp.splits * n_rows * 8);
+    const DecodeRows dr = decode_rows(rows);
+    const Splits sp = decode_splits(B, h, h_kv, T_q, T_p, T_k);
+    const long long items = static_cast<long long>(h_kv) * sp.row_tiles * sp.prefix +
+                            static_cast<long long>(h_kv) * B * dr.chunks * sp.cache;
+    if (items >= (1ll << 30) || n_rows >= (1ull << 31)) return MHA_ERR_UNSUPPORTED;
+    const size_t at_o = f.vec_bytes(h), at_ml = at_o + round256(sp.parts() * n_rows * 256);
+    const size_t need = at_ml + round256(sp.parts() * n_rows * 8);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MHA_ERR_WORKSPACE;
     if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
 
+    // an empty side is described by a one-row tensor that is never loaded
+    ScoredMaps maps;
+    DecodeRows one = dr;
+    one.nb = 1;
+    if ((s = encode_stacked_rows_map(&maps.q, q, B, h_kv, rows, dr)) != MHA_OK) return s;
+    if ((s = encode_stacked_rows_map(&maps.q_cache, q, B, h_kv, rows, one)) != MHA_OK) return s;
+    if ((s = encode_heads_map(&maps.k, T_p > 0 ? k_prefix : q, T_p > 0 ? h_kv : 1, std::max(T_p, 1))) != MHA_OK) return s;
+    if ((s = encode_heads_map(&maps.v, T_p > 0 ? v_prefix : q, T_p > 0 ? h_kv : 1, std::max(T_p, 1))) != MHA_OK) return s;
+    const long long BHk = T_k > 0 ? static_cast<long long>(B) * h_kv : 1;
+    if ((s = encode_heads_map(&maps.k_cache, T_k > 0 ? k_cache : q, BHk, std::max(T_k, 1))) != MHA_OK) return s;
+    if ((s = encode_heads_map(&maps.v_cache, T_k > 0 ? v_cache : q, BHk, std::max(T_k, 1))) != MHA_OK) return s;
     ScoredFwdParams p{};
     bool prepared = false;
     if ((s = prepare(f, prep_layout(f, false, B, h, 0), workspace, B, h, 0, p.f, p.vis, stream, &prepared)) != MHA_OK)
         return s;
+    p.B = B;
+    p.H = h;
+    p.Hkv = h_kv;
+    p.Tq = T_q;
+    p.Tk = T_p;
+    p.vis.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+    p.total_items = static_cast<int>(items);
+    p.status = status_dev;
+    p.cache_lens = cache_lens;
+    p.cache_cap = T_k;
+    p.splits = sp.prefix;
+    p.cache_splits = sp.cache;
+    p.split_tiles = sp.tiles;
+    p.row_tiles = sp.row_tiles;
     p.part_o = reinterpret_cast<float *>(ws + at_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + at_ml);
-    if (sp.splits > 0) {
-        CUtensorMap tq, tk, tv;
-        if ((s = encode_stacked_rows_map(&tq, q, B, h_kv, rows, decode_rows(rows))) != MHA_OK) return s;
-        if ((s = encode_heads_map(&tk, k_prefix, h_kv, T_p)) != MHA_OK) return s;
-        if ((s = encode_heads_map(&tv, v_prefix, h_kv, T_p)) != MHA_OK) return s;
-        p.B = B;
-        p.H = h;
-        p.Hkv = h_kv;
-        p.Tq = T_q;
-        p.Tk = T_p;
-        p.total_items = h_kv * sp.row_tiles * sp.splits;
-        p.status = status_dev;
-        p.cache_lens = cache_lens;
-        p.cache_cap = T_k;
-        p.splits = sp.splits;
-        p.split_tiles = sp.split_tiles;
-        p.row_tiles = sp.row_tiles;
-        if ((s = launched(launch_attn_scored(tq, tk, tv, f.capped, f.bias, p, stream, prepared), "shared prefix launch")) !=
-            MHA_OK)
-            return s;
-    }
-    DecodeSharedParams d{};
-    d.B = B;
-    d.H = h;
-    d.Hkv = h_kv;
-    d.Tq = T_q;
-    d.Tk = T_k;
-    d.capped = f.capped ? 1 : 0;
-    d.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
-    d.f = p.f;
-    d.cache_lens = cache_lens;
-    d.q = static_cast<const __nv_bfloat16 *>(q);
-    d.k = static_cast<const __nv_bfloat16 *>(k_cache);
-    d.v = static_cast<const __nv_bfloat16 *>(v_cache);
-    d.o = static_cast<__nv_bfloat16 *>(o);
-    d.prefix_splits = sp.splits;
-    d.part_o = p.part_o;
-    d.part_ml = p.part_ml;
-    return launched(launch_decode_shared(d, f.bias, stream), "shared prefix decoding launch");
+    if ((s = launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "shared prefix decoding launch")) !=
+        MHA_OK)
+        return s;
+    return launched(launch_decode_merge(p.part_o, p.part_ml, static_cast<__nv_bfloat16 *>(o), static_cast<int>(sp.parts()),
+                                        static_cast<long long>(n_rows), stream),
+                    "shared prefix decoding, merge");
 }

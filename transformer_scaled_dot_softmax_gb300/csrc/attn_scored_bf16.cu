@@ -4,15 +4,15 @@
 
 namespace mha {
 
-cudaError_t launch_attn_scored_capped(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int bias,
-                                      const ScoredFwdParams &p, cudaStream_t stream, bool pdl);
+cudaError_t launch_attn_scored_capped(const ScoredMaps &maps, int bias, const ScoredFwdParams &p, cudaStream_t stream,
+                                      bool pdl);
 
-cudaError_t launch_attn_scored(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, bool capped,
-                               int bias, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
-    if (capped) return launch_attn_scored_capped(tq, tk, tv, bias, p, stream, pdl);
-    if (bias == kBiasSlopes) return scored::launch_form<false, kBiasSlopes>(tq, tk, tv, p, stream, pdl);
-    if (bias == kBiasBuckets) return scored::launch_form<false, kBiasBuckets>(tq, tk, tv, p, stream, pdl);
-    return scored::launch_form<false, kBiasNone>(tq, tk, tv, p, stream, pdl);
+cudaError_t launch_attn_scored(const ScoredMaps &maps, bool capped, int bias, const ScoredFwdParams &p,
+                               cudaStream_t stream, bool pdl) {
+    if (capped) return launch_attn_scored_capped(maps, bias, p, stream, pdl);
+    if (bias == kBiasSlopes) return scored::launch_form<false, kBiasSlopes>(maps, p, stream, pdl);
+    if (bias == kBiasBuckets) return scored::launch_form<false, kBiasBuckets>(maps, p, stream, pdl);
+    return scored::launch_form<false, kBiasNone>(maps, p, stream, pdl);
 }
 
 }  // namespace mha

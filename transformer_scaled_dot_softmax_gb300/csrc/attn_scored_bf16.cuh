@@ -2,7 +2,8 @@
 // scale q.k, for sm_103a: capped by a tanh, biased by distance, masked by
 // documents or prefixes (the definition is in scores.cuh), with K/V heads
 // shared by groups of query heads; and, as the same kernel over other rows,
-// the partial sums of decoding rows against a prefix that a batch shares.
+// the partial sums of decoding rows against a prefix that a batch shares and
+// against the requests' own caches.
 //
 // Mathematics: the online softmax.  A row keeps a reference m (log2 units)
 // and a sum l; P = 2^(y - m), O += P V.  Softmax does not change with m, so the
@@ -75,12 +76,12 @@ enum Mode { kForward, kForwardLse, kDecode };
 
 // One work item: 128 query rows of one head against a range of key tiles.
 struct Item {
-    int b, hh, q0;         // decoding: first batch entry, K/V head, first row of the batch entry's
+    int b, hh, q0;         // decoding: (first) batch entry, K/V head, first row of the batch entry's
     int kv_len;            // keys past it are padding
     int j0, n_kv;          // key tiles j0 .. j0 + n_kv - 1
     int jd;                // the first one visited
     int full_lo, full_hi;  // keys [full_lo, full_hi) are seen by every row
-    int split;             // decoding: key range
+    int split;             // decoding: key range, the prefix's before the caches'
 };
 
 struct __align__(1024) Smem {
@@ -132,18 +133,31 @@ __device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k) {
     Item it;
     if (kMode == kDecode) {
         const DecodeRows dr = decode_rows(p.H / p.Hkv * p.Tq);
-        const int tile = k % p.row_tiles;
-        const int rest = k / p.row_tiles;
-        it.hh = rest % p.Hkv;
-        it.split = rest / p.Hkv;
-        it.b = dr.chunks > 1 ? tile / dr.chunks : tile * dr.nb;
-        it.q0 = dr.chunks > 1 ? (tile - it.b * dr.chunks) * 128 : 0;
-        it.kv_len = p.Tk;
-        it.j0 = it.split * p.split_tiles;
-        it.n_kv = max(0, min(p.split_tiles, (p.Tk + BN - 1) / BN - it.j0));
-        it.jd = it.j0 + it.n_kv - 1;
+        const int prefix_items = p.Hkv * p.row_tiles * p.splits;
         it.full_lo = 0;
-        it.full_hi = p.Tk;
+        if (k < prefix_items) {
+            const int tile = k % p.row_tiles;
+            const int rest = k / p.row_tiles;
+            it.hh = rest % p.Hkv;
+            it.split = rest / p.Hkv;
+            it.b = dr.chunks > 1 ? tile / dr.chunks : tile * dr.nb;
+            it.q0 = dr.chunks > 1 ? (tile - it.b * dr.chunks) * 128 : 0;
+            it.kv_len = it.full_hi = p.Tk;
+            it.j0 = it.split * p.split_tiles;
+            it.n_kv = max(0, min(p.split_tiles, (p.Tk + BN - 1) / BN - it.j0));
+        } else {
+            const int x = (k - prefix_items) / dr.chunks;
+            const int bkv = x % (p.B * p.Hkv), cs = x / (p.B * p.Hkv);
+            it.b = bkv / p.Hkv;
+            it.hh = bkv - it.b * p.Hkv;
+            it.q0 = (k - prefix_items - x * dr.chunks) * 128;
+            it.split = p.splits + cs;
+            it.kv_len = p.cache_lens ? min(max(p.cache_lens[it.b], 0), p.cache_cap) : p.cache_cap;
+            it.full_hi = p.vis.causal ? max(it.kv_len - p.Tq + 1, 0) : it.kv_len;
+            it.j0 = cs * p.split_tiles;
+            it.n_kv = max(0, min(p.split_tiles, (it.kv_len + BN - 1) / BN - it.j0));
+        }
+        it.jd = it.j0 + it.n_kv - 1;
         return it;
     }
     const int BH = p.B * p.H;
@@ -197,17 +211,19 @@ __device__ __forceinline__ Row make_row(const ScoredFwdParams &p, const Item &it
     if (kMode == kDecode) {
         const int g = p.H / p.Hkv, rows = g * p.Tq;
         const DecodeRows dr = decode_rows(rows);
+        const bool cache = it.split >= p.splits;
         const int bi = r / dr.per;
         const int rem = it.q0 + r - bi * dr.per;
         const int b = it.b + bi;
-        w.live = bi < dr.nb && b < p.B && rem < rows;
+        w.live = bi < (cache ? 1 : dr.nb) && b < p.B && rem < rows;
         w.head = it.hh * g + (w.live ? rem / p.Tq : 0);
         const int t = w.live ? rem % p.Tq : 0;
         int len = p.cache_cap;
         if (w.live && p.cache_lens) len = min(max(p.cache_lens[b], 0), p.cache_cap);
-        w.pos = p.Tk + len - p.Tq + t;
+        w.pos = len - p.Tq + t;  // among the cache's rows
+        w.keys = cache ? make_int2(0, p.vis.causal ? min(w.pos + 1, len) : len) : make_int2(0, p.Tk);
+        if (!cache) w.pos += p.Tk;
         w.out = w.live ? (static_cast<long long>(b) * p.H + w.head) * p.Tq + t : 0;
-        w.keys = make_int2(0, p.Tk);
     } else {
         const int i = it.q0 + r, ic = min(i, p.Tq - 1);
         w.live = i < p.Tq;
@@ -221,8 +237,7 @@ __device__ __forceinline__ Row make_row(const ScoredFwdParams &p, const Item &it
 
 template <bool kCap, int kBias, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_scored_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ ScoredFwdParams p) {
+    attn_scored_kernel(const __grid_constant__ ScoredMaps maps, const __grid_constant__ ScoredFwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
@@ -259,9 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (warp == kLoadWarp && lane == 0) {
-        prefetch_tensormap(&tmap_q);
-        prefetch_tensormap(&tmap_k);
-        prefetch_tensormap(&tmap_v);
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
     }
     // Document ranges and the expanded bias are written by the launch before
     // this one.  A launch after this one may begin once that one is complete,
@@ -282,35 +297,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
             const int g = p.H / p.Hkv;
-            uint32_t q_bytes = kTileBytes;
-            if (kMode == kDecode) {
-                const DecodeRows dr = decode_rows(g * p.Tq);
-                q_bytes = static_cast<uint32_t>(dr.per * dr.nb) * (HD * 2);
-            }
+            const DecodeRows dr = decode_rows(g * p.Tq);
             int n = 0, v = 0;  // key tiles and items so far
             bool ok = true;
             for (int t = 0; ok && t < sm.n_items; ++t) {
                 const Item &it = item_of<kMode>(sm, p, t, cta, G);
                 if (it.n_kv == 0) continue;
                 const int qbuf = v & 1;
+                const bool cache = kMode == kDecode && it.split >= p.splits;
+                const CUtensorMap *mq = cache ? &maps.q_cache : &maps.q, *mk = cache ? &maps.k_cache : &maps.k,
+                                  *mv = cache ? &maps.v_cache : &maps.v;
                 if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
-                mbar_arrive_expect_tx(&sm.q_full[qbuf], q_bytes);
+                mbar_arrive_expect_tx(&sm.q_full[qbuf], kMode == kDecode
+                                                            ? static_cast<uint32_t>(dr.per * (cache ? 1 : dr.nb)) * (HD * 2)
+                                                            : kTileBytes);
                 if (in_bounds(it.q0 >= 0 && it.b >= 0 && it.b < p.B && it.hh < (kMode == kDecode ? p.Hkv : p.H), p.status)) {
                     if (kMode == kDecode)
-                        tma_load_4d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b, it.hh);
+                        tma_load_4d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b, it.hh);
                     else
-                        tma_load_3d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b * p.H + it.hh);
+                        tma_load_3d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b * p.H + it.hh);
                 }
                 ++v;
-                const int z = kMode == kDecode ? it.hh : it.b * p.Hkv + it.hh / g;
+                const int z = kMode == kDecode ? (cache ? it.b * p.Hkv + it.hh : it.hh) : it.b * p.Hkv + it.hh / g;
                 for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
                     const int j = tile_of(it, jt);
                     const int st = n % STAGES;
                     if (n >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
                     mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
-                    if (in_bounds(j >= 0 && j * BN < p.Tk && z < (kMode == kDecode ? 1 : p.B) * p.Hkv, p.status)) {
-                        tma_load_3d(&tmap_k, &sm.kv_full[st], sm.k[st], 0, j * BN, z);
-                        tma_load_3d(&tmap_v, &sm.kv_full[st], sm.v[st], 0, j * BN, z);
+                    if (in_bounds(j >= 0 && j * BN < (cache ? p.cache_cap : p.Tk) &&
+                                      z < (kMode == kDecode && !cache ? 1 : p.B) * p.Hkv,
+                                  p.status)) {
+                        tma_load_3d(mk, &sm.kv_full[st], sm.k[st], 0, j * BN, z);
+                        tma_load_3d(mv, &sm.kv_full[st], sm.v[st], 0, j * BN, z);
                     }
                 }
             }
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // times whatever the buffer holds has to be 0.  (Rows past Tk
                 // are filled with zeros by the copy.)
                 const int rows = it.kv_len - tile_of(it, jt) * BN;
-                if (kMode != kDecode && rows < BN && it.kv_len < p.Tk) {
+                if (rows < BN && it.kv_len < (kMode == kDecode && it.split >= p.splits ? p.cache_cap : p.Tk)) {
                     uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
                     for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
@@ -701,7 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Row w = make_row<kMode>(p, it, r);
             const bool row_ok = in_bounds(w.out >= 0 && w.out < static_cast<long long>(p.B) * p.H * p.Tq, p.status) && w.live;
             if (it.n_kv == 0) {
-                if (kMode != kDecode && row_ok) {
+                if (kMode == kDecode) {
+                    if (row_ok)
+                        p.part_ml[it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out] = make_float2(-INFINITY, 0.f);
+                } else if (row_ok) {
                     uint4 *d4 = reinterpret_cast<uint4 *>(p.o + w.out * HD);
 #pragma unroll
                     for (int c = 0; c < 8; ++c) d4[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -794,8 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kCap, int kBias, int kMode>
-cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ScoredFwdParams &p,
-                   cudaStream_t stream, bool pdl) {
+cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
     auto kernel = attn_scored_kernel<kCap, kBias, kMode>;
     const size_t smem = sizeof(Smem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -804,15 +824,14 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const int grid = p.total_items < sms ? p.total_items : sms;
     if (grid <= 0) return cudaSuccess;
-    return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, pdl, 1, tq, tk, tv, p);
+    return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, pdl, 1, maps, p);
 }
 
 template <bool kCap, int kBias>
-cudaError_t launch_form(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ScoredFwdParams &p,
-                        cudaStream_t stream, bool pdl) {
-    if (p.part_o) return launch<kCap, kBias, kDecode>(tq, tk, tv, p, stream, pdl);
-    if (p.lse) return launch<kCap, kBias, kForwardLse>(tq, tk, tv, p, stream, pdl);
-    return launch<kCap, kBias, kForward>(tq, tk, tv, p, stream, pdl);
+cudaError_t launch_form(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
+    if (p.part_o) return launch<kCap, kBias, kDecode>(maps, p, stream, pdl);
+    if (p.lse) return launch<kCap, kBias, kForwardLse>(maps, p, stream, pdl);
+    return launch<kCap, kBias, kForward>(maps, p, stream, pdl);
 }
 
 }  // namespace scored

@@ -165,21 +165,26 @@ struct ScoredFwdParams {
     __nv_bfloat16 *o_lo;  // optional with lse, (B, H, Tq, 64): what rounding took from o
     int num_qblocks, total_items;
     int *status;
-    // Decoding over a shared prefix (part_o not null): the keys are the
-    // prefix's (Tk of them), a K/V head's query rows of all batch entries are
-    // stacked, and each of `splits` key ranges leaves unnormalised partial
-    // sums instead of an output.
+    // Decoding over a shared prefix (part_o not null): Tk keys of the prefix,
+    // seen by a K/V head's query rows of all batch entries stacked, then each
+    // batch entry's cache, seen by its own; every key range of split_tiles
+    // 128-key tiles leaves unnormalised partial sums instead of an output.
     const int32_t *cache_lens;  // (B) or null: cache_cap rows everywhere
     int cache_cap;
-    int splits, split_tiles;    // key ranges, 128-key tiles per range
-    int row_tiles;              // 128-row tiles per K/V head
-    float *part_o;              // (splits, B, H, Tq, 64)
-    float2 *part_ml;            // (splits, B, H, Tq): reference in log2 units, sum
+    int splits, cache_splits;   // key ranges of the prefix and of a cache
+    int split_tiles;
+    int row_tiles;              // 128-row tiles per K/V head, all batch entries stacked
+    float *part_o;              // (splits + cache_splits, B, H, Tq, 64)
+    float2 *part_ml;            // (splits + cache_splits, B, H, Tq): reference in log2 units, sum
 };
-// q: 3-D map (64, Tq, B H) -- decoding: 4-D (64, g Tq, B, Hkv), box of
-// decode_rows(); k, v: 3-D maps (64, Tk, B Hkv); 128-byte swizzling.
-cudaError_t launch_attn_scored(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, bool capped,
-                               int bias, const ScoredFwdParams &p, cudaStream_t stream, bool pdl);
+// q: (64, Tq, B H); k, v: (64, Tk, B Hkv); 128-row boxes, 128-byte swizzling.
+// Decoding: q (64, g Tq, B, Hkv) in boxes of decode_rows(), k, v of the prefix
+// (64, Tk, Hkv), q_cache in boxes of one batch entry, the caches (64, cap, B Hkv).
+struct ScoredMaps {
+    CUtensorMap q, k, v, q_cache, k_cache, v_cache;
+};
+cudaError_t launch_attn_scored(const ScoredMaps &maps, bool capped, int bias, const ScoredFwdParams &p,
+                               cudaStream_t stream, bool pdl);
 
 // How the g Tq query rows of a K/V head and batch entry are stacked into
 // 128-row tiles: `per` rows of each of `nb` batch entries, `chunks` tiles per
@@ -218,20 +223,11 @@ cudaError_t launch_scored_dtable(const float *diag, const float *far_sum, float 
                                  int n_kb, int n_qb, int near, int near_slots, const BucketParams &bk,
                                  cudaStream_t stream);
 
-// ------------------------------------------------ decoding over a shared prefix: the requests' own caches
-constexpr int kSmsPerGpu = 152;  // for the choice of splits, which fixes the workspace
-struct DecodeSharedParams {
-    int B, H, Hkv, Tq, Tk;
-    int capped, causal;
-    ScoreParams f;
-    const int32_t *cache_lens;
-    const __nv_bfloat16 *q, *k, *v;  // (B, H, Tq, 64), (B, Hkv, Tk, 64) twice
-    __nv_bfloat16 *o;
-    int prefix_splits;               // as ScoredFwdParams
-    const float *part_o;
-    const float2 *part_ml;
-};
-cudaError_t launch_decode_shared(const DecodeSharedParams &p, int bias, cudaStream_t stream);
+// ------------------------------------------------ decoding: partial sums to outputs
+constexpr int kSmsPerGpu = 152;  // for the choice of key ranges, which fixes the workspace
+// o[row] = sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m), over `parts` key ranges.
+cudaError_t launch_decode_merge(const float *part_o, const float2 *part_ml, __nv_bfloat16 *o, int parts, long long rows,
+                                cudaStream_t stream);
 
 // ------------------------------------------------ positional encoding
 // out (rows, D) = x + PE(pos0 + row % T); D % 8 == 0; x and out may alias.
