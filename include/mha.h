@@ -349,7 +349,7 @@ mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const void *k, const
  * may differ in dq's last bit.  workspace:
  * >= sdpa_scored_backward_workspace_bytes() bytes, 256-byte aligned.
  */
-size_t sdpa_scored_backward_workspace_bytes(int B, int h, int T_q, int T_k,
+size_t sdpa_scored_backward_workspace_bytes(int B, int h, int h_kv, int T_q, int T_k,
                                             const mha_score_form *form);
 mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, const void *v,
                                 const void *o, const void *o_lo, const void *dout,

@@ -106,9 +106,11 @@ def test_workspace_sizes(lib):
     assert f(2, 3, 7, 7, form(lib, table=FAKE, starts=(0, 0))) == 0
     b = lib.lib.sdpa_scored_backward_workspace_bytes
     plain = 2 * 3 * 256 * 64 * 4 + 2 * 2 * 3 * 256 * 4
-    assert b(2, 3, 130, 7, None) == plain
-    assert b(2, 3, 130, 7, ctypes.addressof(t)) == (plain + r(3 * (2 * 164 + 1) * 4) + 2 * 3 * 1 * 2 * 1024 + r(2 * 3 * 8) +
-                                                    3 * 3 * 1024)
+    assert b(2, 3, 3, 130, 7, None) == plain and b(2, 3, 2, 130, 7, None) == 0
+    # three query heads on one K/V head, a CTA and fp32 sums of dk and dv each
+    assert b(2, 3, 1, 130, 7, None) == plain + 2 * r(3 * 2 * 1 * 7 * 64 * 4)
+    # the expanded bias and one sum per head, key block and bucket
+    assert b(2, 3, 3, 130, 7, ctypes.addressof(t)) == plain + r(3 * (2 * 164 + 1) * 4) + r(2 * 3 * 1 * 2 * 4)
     d = lib.lib.sdpa_decode_shared_workspace_bytes
     assert d(4, 8, 2, 1, 0, 0, None) == 0 and d(4, 8, 3, 1, 10, 10, None) == 0
     assert d(4, 8, 2, 1, 100, 0, None) == 4 * 8 * 256 + r(4 * 8 * 8)     # one key range of the prefix

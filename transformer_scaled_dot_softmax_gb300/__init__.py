@@ -58,6 +58,14 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _stream_on(stream, device):
+    """_stream_handle for a device index, without building a Stream object (it
+    costs a third of a small call's time on the host)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -331,17 +339,17 @@ def _starts_array(starts):
     return (ctypes.c_int32 * len(starts))(*starts)
 
 
-def _check_same(name, t, dtype, shape, device):
+def _require(name, t, dtype, shape, device):
+    """t is a contiguous CUDA tensor of that dtype, shape and device index."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     _check_dev(name, t, dtype)
-    if t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have the shape %s" % (name, shape))
-
-
-def _check_current(device):
-    if device.index != _torch().cuda.current_device():
-        raise ValueError("the tensors must be on the current CUDA device")
+    if t.get_device() != device:
+        raise ValueError("%s must be on cuda:%d, the current device" % (name, device))
+    raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
 
 
 def _score_form(h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens, doc_ids):
@@ -349,80 +357,85 @@ def _score_form(h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens,
     torch = _torch()
     f = _native.ScoreForm()
     keep = None
-    f.cap = 0.0 if cap is None else float(cap)
+    if cap is not None:
+        f.cap = cap
     if slopes is not None:
-        _check_same("slopes", slopes, torch.float32, (h,), device)
+        _require("slopes", slopes, torch.float32, (h,), device)
         f.slopes = slopes.data_ptr()
     if (table is None) != (bucket_starts is None):
         raise ValueError("table and bucket_starts go together")
     if table is not None:
-        starts = tuple(bucket_starts)
-        n = len(starts)
+        keep = _starts_array(tuple(bucket_starts))
+        n = len(keep)
         if n == 0 or not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[0] not in (n, 2 * n):
             raise ValueError("table must have one row per bucket, or two (bidirectional)")
-        _check_same("table", table, torch.bfloat16, (table.shape[0], h), device)
-        keep = _starts_array(starts)
+        _require("table", table, torch.bfloat16, (table.shape[0], h), device)
         f.table = table.data_ptr()
         f.bucket_starts = ctypes.addressof(keep)
         f.num_buckets = n
-        f.bidirectional = int(table.shape[0] == 2 * n)
+        f.bidirectional = table.shape[0] == 2 * n
     if prefix_lens is not None:
-        _check_same("prefix_lens", prefix_lens, torch.int32, (B,), device)
+        _require("prefix_lens", prefix_lens, torch.int32, (B,), device)
         f.prefix_lens = prefix_lens.data_ptr()
     if doc_ids is not None:
-        _check_same("doc_ids", doc_ids, torch.int32, (B, T), device)
+        _require("doc_ids", doc_ids, torch.int32, (B, T), device)
         f.doc_ids = doc_ids.data_ptr()
     return f, keep
 
 
-def _check_heads(q, k, v, names=("q", "k", "v")):
-    """Shapes (B, h, T_q, 64) and (B, h_kv, T_k, 64) of q, k, v."""
-    bf = _torch().bfloat16
-    _check_dev(names[0], q, bf)
-    if q.dim() != 4 or not hasattr(k, "dim") or k.dim() != 4:
-        raise ValueError("%s and %s must have four dimensions" % names[:2])
+def _heads(q, k, v, names=("q", "k", "v")):
+    """Checked (B, h, h_kv, T_q, T_k, d, device index) of q (B, h, T_q, d) and k,
+    v (B, h_kv, T_k, d), bf16 on the current device."""
+    torch = _torch()
+    bf = torch.bfloat16
+    device = torch.cuda.current_device()
+    for n, t in zip(names, (q, k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError("%s must be a tensor of four dimensions" % n)
     B, h, T_q, d = q.shape
-    h_kv, T_k = k.shape[1], k.shape[2]
-    for n, t in zip(names[1:], (k, v)):
-        _check_same(n, t, bf, (B, h_kv, T_k, d), q.device)
-    _check_current(q.device)
-    return B, h, h_kv, T_q, T_k, d
+    _, h_kv, T_k, _ = k.shape
+    _require(names[0], q, bf, (B, h, T_q, d), device)
+    _require(names[1], k, bf, (B, h_kv, T_k, d), device)
+    _require(names[2], v, bf, (B, h_kv, T_k, d), device)
+    return B, h, h_kv, T_q, T_k, d, device
 
 
 def _scratch(workspace, need, device):
-    if workspace is None:
-        return _torch().empty(max(need, 1), dtype=_torch().uint8, device=device)
-    _check_dev("workspace", workspace)
-    if workspace.device != device:
-        raise ValueError("workspace must be on %s" % device)
-    return workspace
-
-
-def _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask, key_lens,
-                 prefix_lens, doc_ids, status, stream):
+    """(workspace, bytes): the caller's, or a new one of `need` bytes."""
     torch = _torch()
-    B, h, h_kv, T_q, T_k, d = _check_heads(q, k, v)
-    dev = q.device
-    out = torch.empty_like(q) if out is None else out
-    _check_same("out", out, torch.bfloat16, (B, h, T_q, d), dev)
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
+    _check_dev("workspace", workspace)
+    if workspace.get_device() != device:
+        raise ValueError("workspace must be on cuda:%d, the current device" % device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
+                 key_lens, prefix_lens, doc_ids, status, stream):
+    torch = _torch()
+    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k, v)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _require("out", out, torch.bfloat16, q.shape, dev)
     if lse is not None:
-        _check_same("lse", lse, torch.float32, (B, h, T_q), dev)
+        _require("lse", lse, torch.float32, (B, h, T_q), dev)
     if out_lo is not None:
-        _check_same("out_lo", out_lo, torch.bfloat16, (B, h, T_q, d), dev)
+        _require("out_lo", out_lo, torch.bfloat16, q.shape, dev)
     if key_lens is not None:
-        _check_same("key_lens", key_lens, torch.int32, (B,), dev)
+        _require("key_lens", key_lens, torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
     form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
     pf = ctypes.addressof(form)
-    need = lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf)
-    if need or workspace is not None:
-        workspace = _scratch(workspace, need, dev)
-    rc = lib.sdpa_scored_forward(MHA_BF16, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(out_lo), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 B, h, h_kv, T_q, T_k, d, d,
-                                 1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
-                                 _ptr(key_lens), pf, _ptr(status), _stream_handle(stream))
+    size = 0
+    if table is not None or doc_ids is not None or workspace is not None:
+        workspace, size = _scratch(workspace, lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf), dev)
+    rc = lib.sdpa_scored_forward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
+                                 _ptr(out_lo), _ptr(workspace), size, B, h, h_kv, T_q, T_k, d, d,
+                                 1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask),
+                                 _ptr(key_lens), pf, _ptr(status), _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_scored_forward")
     return out
@@ -449,8 +462,8 @@ def sdpa_scored_forward_lse(q, k, v, out=None, lse=None, workspace=None, *, out_
     (B,h,T_q) fp32, which sdpa_scored_backward takes.  out_lo: a tensor like
     out to receive what rounding took from it, for the backward's o_lo.
     Returns (out, lse)."""
-    torch = _torch()
     if lse is None:
+        torch = _torch()
         _check_dev("q", q, torch.bfloat16)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     out = _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
@@ -468,35 +481,39 @@ def sdpa_scored_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, dtabl
     (dq, dk, dv, dtable), dtable None without a table."""
     torch = _torch()
     bf = torch.bfloat16
-    B, h, h_kv, T_q, T_k, d = _check_heads(q, k, v)
-    dev = q.device
-    _check_same("o", o, bf, (B, h, T_q, d), dev)
-    _check_same("dout", dout, bf, (B, h, T_q, d), dev)
-    _check_same("lse", lse, torch.float32, (B, h, T_q), dev)
+    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k, v)
+    _require("o", o, bf, q.shape, dev)
+    _require("dout", dout, bf, q.shape, dev)
+    _require("lse", lse, torch.float32, (B, h, T_q), dev)
     if o_lo is not None:
-        _check_same("o_lo", o_lo, bf, (B, h, T_q, d), dev)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+        _require("o_lo", o_lo, bf, q.shape, dev)
+    grads = []
     for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_same(n, t, bf, tuple(like.shape), dev)
+        if t is None:
+            t = torch.empty_like(like)
+        else:
+            _require(n, t, bf, like.shape, dev)
+        grads.append(t)
+    dq, dk, dv = grads
     if key_lens is not None:
-        _check_same("key_lens", key_lens, torch.int32, (B,), dev)
+        _require("key_lens", key_lens, torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
     form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
     if table is not None:
-        dtable = torch.empty_like(table) if dtable is None else dtable
-        _check_same("dtable", dtable, bf, tuple(table.shape), dev)
+        if dtable is None:
+            dtable = torch.empty_like(table)
+        else:
+            _require("dtable", dtable, bf, table.shape, dev)
     elif dtable is not None:
         raise ValueError("dtable needs a table")
     pf = ctypes.addressof(form)
-    workspace = _scratch(workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, T_q, T_k, pf), dev)
-    rc = lib.sdpa_scored_backward(MHA_BF16, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_lo), _ptr(dout),
-                                  _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dtable), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), B, h, h_kv, T_q, T_k, d, d,
-                                  1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
-                                  _ptr(key_lens), pf, _ptr(status), _stream_handle(stream))
+    workspace, size = _scratch(workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, h_kv, T_q, T_k, pf), dev)
+    rc = lib.sdpa_scored_backward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o_lo),
+                                  dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                  _ptr(dtable), workspace.data_ptr(), size, B, h, h_kv, T_q, T_k, d, d,
+                                  1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask),
+                                  _ptr(key_lens), pf, _ptr(status), _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_scored_backward")
     return dq, dk, dv, dtable
@@ -511,27 +528,28 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
     whose last T_q they are; with a causal mask row t sees the cache up to its
     own row.  Scores as sdpa_scored_forward.  Returns out (B,h,T_q,64)."""
     torch = _torch()
-    B, h, h_kv, T_q, T_k, d = _check_heads(q, k_cache, v_cache, ("q", "k_cache", "v_cache"))
-    dev = q.device
-    if not hasattr(k_prefix, "dim") or k_prefix.dim() != 3:
-        raise ValueError("k_prefix must have three dimensions")
+    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k_cache, v_cache, ("q", "k_cache", "v_cache"))
+    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
+        raise ValueError("k_prefix must be a tensor of three dimensions")
     T_p = k_prefix.shape[1]
-    for n, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-        _check_same(n, t, torch.bfloat16, (h_kv, T_p, d), dev)
-    out = torch.empty_like(q) if out is None else out
-    _check_same("out", out, torch.bfloat16, (B, h, T_q, d), dev)
+    _require("k_prefix", k_prefix, torch.bfloat16, (h_kv, T_p, d), dev)
+    _require("v_prefix", v_prefix, torch.bfloat16, (h_kv, T_p, d), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _require("out", out, torch.bfloat16, q.shape, dev)
     if cache_lens is not None:
-        _check_same("cache_lens", cache_lens, torch.int32, (B,), dev)
+        _require("cache_lens", cache_lens, torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
     form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
     pf = ctypes.addressof(form)
-    workspace = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
-    rc = lib.sdpa_decode_shared_forward(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache),
-                                        _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                        B, h, h_kv, T_q, T_p, T_k, d, d,
-                                        1.0 / math.sqrt(d) if scale is None else float(scale), _mask_code(mask),
-                                        _ptr(cache_lens), pf, _ptr(status), _stream_handle(stream))
+    workspace, size = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
+    rc = lib.sdpa_decode_shared_forward(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
+                                        v_cache.data_ptr(), out.data_ptr(), workspace.data_ptr(), size, B, h, h_kv,
+                                        T_q, T_p, T_k, d, d, 1.0 / math.sqrt(d) if scale is None else scale,
+                                        _mask_code(mask), _ptr(cache_lens), pf, _ptr(status),
+                                        _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_decode_shared_forward")
     return out

@@ -53,7 +53,7 @@ SIGNATURES = {
     "sdpa_scored_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _vp]),
     "sdpa_scored_forward": (_ci, [_ci] + [_vp] * 7 + [_sz] + [_ci] * 7 +
                             [_cf, _ci, _vp, _vp, _vp, _vp]),
-    "sdpa_scored_backward_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _vp]),
+    "sdpa_scored_backward_workspace_bytes": (_sz, [_ci] * 5 + [_vp]),
     "sdpa_scored_backward": (_ci, [_ci] + [_vp] * 12 + [_sz] + [_ci] * 7 +
                              [_cf, _ci, _vp, _vp, _vp, _vp]),
     "sdpa_decode_shared_workspace_bytes": (_sz, [_ci] * 6 + [_vp]),

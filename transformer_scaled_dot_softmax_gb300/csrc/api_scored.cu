@@ -146,10 +146,10 @@ mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h
 
 struct BwdLayout {
     Prep prep;
-    size_t dq, nlse2, dvec, diag, far, sums, end;
-    int near_blocks, near_slots;
+    size_t dq, nlse2, dvec, buckets, part_dk, part_dv, end;
+    int splits, near_blocks;
 };
-BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int T_q, int T_k) {
+BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int h_kv, int T_q, int T_k) {
     BwdLayout l{};
     l.prep = prep_layout(f, docs, B, h, T_k);
     const size_t BH = static_cast<size_t>(B) * h;
@@ -158,16 +158,26 @@ BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int T_q, int T_k) {
     l.dq = l.prep.end;
     l.nlse2 = l.dq + round256(rows * 256);
     l.dvec = l.nlse2 + round256(rows * 4);
-    l.diag = l.dvec + round256(rows * 4);
-    l.far = l.sums = l.end = l.diag;
+    l.buckets = l.dvec + round256(rows * 4);
+    l.part_dk = l.buckets;
+    l.splits = 1;
     if (f.bias == kBiasBuckets) {
         // block pairs with |key - query| < far for some pair
         l.near_blocks = std::min((f.f.far + 126) / 128, std::max(n_qb, n_kb));
-        l.near_slots = std::min(2 * l.near_blocks + 1, n_qb);
-        l.far = l.diag + round256(BH * n_kb * l.near_slots * 1024);
-        l.sums = l.far + round256(BH * n_kb * 8);
-        l.end = l.sums + round256(static_cast<size_t>(h) * (2 * l.near_blocks + 1) * 1024);
+        l.part_dk += round256(BH * n_kb * f.bk.num * (f.bk.both ? 2 : 1) * 4);
     }
+    if (h_kv > 0 && T_q > 0) {
+        // CTAs share a K/V head's query heads until there are about three for
+        // every SM (blocks of a causal mask differ in length), or one per head
+        const long long ctas = static_cast<long long>(B) * h_kv * n_kb;
+        const int group = h / h_kv;
+        while (l.splits < group && ctas * l.splits < 3 * kSmsPerGpu) ++l.splits;
+        const int per = (group + l.splits - 1) / l.splits;
+        l.splits = (group + per - 1) / per;
+    }
+    const size_t part = l.splits > 1 ? round256(static_cast<size_t>(l.splits) * B * h_kv * T_k * 256) : 0;
+    l.part_dv = l.part_dk + part;
+    l.end = l.part_dv + part;
     return l;
 }
 
@@ -257,10 +267,12 @@ MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const voi
     return launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "scored attention launch");
 }
 
-MHA_EXPORT size_t sdpa_scored_backward_workspace_bytes(int B, int h, int T_q, int T_k, const mha_score_form *form) {
+MHA_EXPORT size_t sdpa_scored_backward_workspace_bytes(int B, int h, int h_kv, int T_q, int T_k,
+                                                       const mha_score_form *form) {
     Form f;
-    if (B < 0 || h < 0 || T_q < 0 || T_k < 0 || !form_sizes(form, f)) return 0;
-    return bwd_layout(f, form && form->doc_ids, B, h, T_q, T_k).end;
+    if (B < 0 || h < 0 || h_kv < 0 || T_q < 0 || T_k < 0 || !form_sizes(form, f)) return 0;
+    if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return 0;
+    return bwd_layout(f, form && form->doc_ids, B, h, h_kv, T_q, T_k).end;
 }
 
 MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, const void *v, const void *o,
@@ -279,7 +291,7 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
     if (h == 0 || (BH == 0 && !dtable) || (T_q == 0 && T_k == 0 && !dtable)) return MHA_OK;
     if (BH > 0 && ((T_q > 0 && (!q || !o || !dout || !lse || !dq)) || (T_k > 0 && (!k || !v || !dk || !dv))))
         return MHA_ERR_INVALID_ARG;
-    const BwdLayout lay = bwd_layout(f, f.doc_ids != nullptr, B, h, T_q, T_k);
+    const BwdLayout lay = bwd_layout(f, f.doc_ids != nullptr, B, h, h_kv, T_q, T_k);
     if (lay.end > 0 && (!workspace || workspace_bytes < lay.end)) return MHA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
     if (BH > 0 && ((T_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(o_lo) || !aligned16(dout) || !aligned16(dq))) ||
@@ -287,6 +299,27 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
         return MHA_ERR_MISALIGNED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ScoredBwdParams p{};
+    p.B = B;
+    p.H = h;
+    p.Hkv = h_kv;
+    p.Tq = T_q;
+    p.Tk = T_k;
+    p.Tq_pad = (T_q + 127) / 128 * 128;
+    p.scale = scale;
+    p.f = f.f;
+    p.bk = f.bk;
+    p.vis.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+    p.vis.key_lens = (mask & MHA_MASK_KEY_PADDING) ? key_lens : nullptr;
+    p.vis.prefix_lens = f.prefix_lens;
+    p.dq_acc = reinterpret_cast<float *>(ws + lay.dq);
+    p.dk = static_cast<__nv_bfloat16 *>(dk);
+    p.dv = static_cast<__nv_bfloat16 *>(dv);
+    p.splits = lay.splits;
+    p.part_dk = reinterpret_cast<float *>(ws + lay.part_dk);
+    p.part_dv = reinterpret_cast<float *>(ws + lay.part_dv);
+    p.near_blocks = lay.near_blocks;
+    if (dtable) p.bucket_part = reinterpret_cast<float *>(ws + lay.buckets);
+    p.status = status_dev;
     if (BH > 0 && (T_q > 0 || T_k > 0)) {
         // an empty side is described by a one-row tensor that is never loaded
         const void *q_src = T_q > 0 ? q : k, *g_src = T_q > 0 ? dout : k;
@@ -297,47 +330,24 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
         if ((s = encode_heads_map(&tg, g_src, T_q > 0 ? BH : BHk, T_q > 0 ? T_q : 1)) != MHA_OK) return s;
         if ((s = encode_heads_map(&tk, k_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
         if ((s = encode_heads_map(&tv, v_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
-        bool prepared = false;
-        if ((s = prepare(f, lay.prep, workspace, B, h, T_k, p.f, p.vis, stream, &prepared)) != MHA_OK) return s;
-        p.B = B;
-        p.H = h;
-        p.Hkv = h_kv;
-        p.Tq = T_q;
-        p.Tk = T_k;
-        p.Tq_pad = (T_q + 127) / 128 * 128;
-        p.scale = scale;
-        p.vis.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
-        p.vis.key_lens = (mask & MHA_MASK_KEY_PADDING) ? key_lens : nullptr;
+        float *vec = f.bias == kBiasBuckets ? reinterpret_cast<float *>(ws + lay.prep.vec) : nullptr;
+        int2 *docs = f.doc_ids ? reinterpret_cast<int2 *>(ws + lay.prep.docs) : nullptr;
         float *nlse2 = reinterpret_cast<float *>(ws + lay.nlse2), *dvec = reinterpret_cast<float *>(ws + lay.dvec);
+        p.f.vec = vec;
+        p.vis.doc_range = docs;
         p.nlse2 = nlse2;
         p.dvec = dvec;
-        p.dq_acc = reinterpret_cast<float *>(ws + lay.dq);
-        p.dk = static_cast<__nv_bfloat16 *>(dk);
-        p.dv = static_cast<__nv_bfloat16 *>(dv);
-        p.near_blocks = lay.near_blocks;
-        p.near_slots = lay.near_slots;
-        if (dtable) {
-            p.diag = reinterpret_cast<float *>(ws + lay.diag);
-            p.far_sum = reinterpret_cast<float *>(ws + lay.far);
-        }
-        p.status = status_dev;
-        if ((s = launched(launch_attn_bwd_pre(static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(o_lo),
-                                              static_cast<const __nv_bfloat16 *>(dout), lse, nlse2, dvec, p.dq_acc, BH, T_q, p.Tq_pad, stream),
+        if ((s = launched(launch_scored_bwd_pre(static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(o_lo),
+                                                static_cast<const __nv_bfloat16 *>(dout), lse, nlse2, dvec, p, vec, docs,
+                                                f.doc_ids, stream),
                           "scored attention backward, row terms")) != MHA_OK)
             return s;
         if (T_k > 0 && (s = launched(launch_attn_scored_bwd(tq, tk, tv, tg, f.capped, f.bias, p, stream),
                                      "scored attention backward launch")) != MHA_OK)
             return s;
-        if ((s = launched(launch_attn_bwd_post(p.dq_acc, static_cast<__nv_bfloat16 *>(dq), BH, T_q, p.Tq_pad, scale, stream),
-                          "scored attention backward, dq")) != MHA_OK)
-            return s;
     }
-    if (!dtable) return MHA_OK;
-    return launched(launch_scored_dtable(reinterpret_cast<const float *>(ws + lay.diag),
-                                         reinterpret_cast<const float *>(ws + lay.far),
-                                         reinterpret_cast<float *>(ws + lay.sums), static_cast<__nv_bfloat16 *>(dtable), B, h,
-                                         (T_k + 127) / 128, (T_q + 127) / 128, lay.near_blocks, lay.near_slots, f.bk, stream),
-                    "bias table gradient launch");
+    return launched(launch_scored_bwd_post(p, static_cast<__nv_bfloat16 *>(dq), static_cast<__nv_bfloat16 *>(dtable), stream),
+                    "scored attention backward, conversion");
 }
 
 MHA_EXPORT size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p, int T_k,

@@ -17,6 +17,7 @@
 //   attn_bwd_post  dQ = bf16(scale * accumulator).
 #include <cuda_bf16.h>
 
+#include "attn_bwd_rows.cuh"
 #include "kernels.h"
 #include "sm103_ptx.cuh"
 
@@ -26,89 +27,19 @@ namespace {
 constexpr int HD = kAttnHeadDim;  // 64
 constexpr int BQ = 128;           // query rows per block
 constexpr int BKB = 128;          // keys per CTA
-constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------ pre and post
-// One thread per 8 features of a row; rows past Tq (padding up to a whole
-// query block) get lse = +inf, D = 0.  o_lo: null, or what rounding took from o.
-__global__ void attn_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ o_lo, const __nv_bfloat16 *__restrict__ dout,
-                             const float *__restrict__ lse, float *__restrict__ nlse2,
-                             float *__restrict__ dvec, float *__restrict__ dq_acc, long long BH,
-                             int Tq, int Tq_pad) {
-    const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const long long row = t >> 3;  // over BH * Tq_pad
-    const int part = static_cast<int>(t & 7);
-    // no early return: the row sum below is a full-warp shuffle
-    const bool valid = row < BH * Tq_pad;
-    const long long bh = valid ? row / Tq_pad : 0;
-    const int i = valid ? static_cast<int>(row - bh * Tq_pad) : Tq;
-    float acc = 0.f;
-    if (i < Tq) {
-        const long long src = (bh * Tq + i) * HD + part * 8;
-        const uint4 a = *reinterpret_cast<const uint4 *>(o + src);
-        const uint4 g = *reinterpret_cast<const uint4 *>(dout + src);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, gw[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc = fmaf(__uint_as_float(aw[e] << 16), __uint_as_float(gw[e] << 16), acc);
-            acc = fmaf(__uint_as_float(aw[e] & 0xffff0000u), __uint_as_float(gw[e] & 0xffff0000u), acc);
-        }
-        if (o_lo) {
-            const uint4 b = *reinterpret_cast<const uint4 *>(o_lo + src);
-            const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc = fmaf(__uint_as_float(bw[e] << 16), __uint_as_float(gw[e] << 16), acc);
-                acc = fmaf(__uint_as_float(bw[e] & 0xffff0000u), __uint_as_float(gw[e] & 0xffff0000u), acc);
-            }
-        }
-    }
-    // reduce over the 8 threads of the row (consecutive lanes)
-    acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-    acc += __shfl_xor_sync(0xffffffffu, acc, 2);
-    acc += __shfl_xor_sync(0xffffffffu, acc, 4);
-    if (!valid) return;
-    float4 *z = reinterpret_cast<float4 *>(dq_acc + row * HD + part * 8);
-    z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-    z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (part == 0) {
-        dvec[row] = acc;
-        float l = -INFINITY;
-        if (i < Tq) {
-            const float x = lse[bh * Tq + i];
-            l = x == -INFINITY ? -INFINITY : -x * kLog2e;
-        }
-        nlse2[row] = l;
-    }
+__global__ void attn_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dout,
+                             const float *__restrict__ lse, float *__restrict__ nlse2, float *__restrict__ dvec,
+                             float *__restrict__ dq_acc, long long BH, int Tq, int Tq_pad) {
+    bwd_row_terms(static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x, o, nullptr, dout, lse, nlse2, dvec, dq_acc,
+                  BH, Tq, Tq_pad);
 }
 
-// The dQ accumulator of a query block j of head bh is 128 rows x 64 fp32 at
-// (bh Tq_pad + 128 j) 64, stored as four 8 KiB quarters (rows 32w .. 32w+31),
-// each ordered [16-byte chunk x of the row][row within the quarter][4 floats]:
-// the order in which a dQ warp stages its rows without shared-memory bank
-// conflicts, so that one untiled bulk reduction adds the whole quarter.
-__device__ __forceinline__ long long dq_acc_index(long long bh, int Tq_pad, int i, int chunk) {
-    return (bh * Tq_pad + (i & ~31)) * HD + chunk * 128 + (i & 31) * 4;
-}
-
-// One thread per 8 features of a row; a warp takes 32 consecutive rows of one
-// feature group (coalesced accumulator reads).
-__global__ void attn_bwd_post(const float *__restrict__ dq_acc, __nv_bfloat16 *__restrict__ dq,
-                              long long BH, int Tq, int Tq_pad, float scale) {
+__global__ void attn_bwd_post(const float *__restrict__ dq_acc, __nv_bfloat16 *__restrict__ dq, long long BH, int Tq,
+                              int Tq_pad, float scale) {
     pdl_wait();  // the accumulator is complete once the main kernel is
-    const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const long long grp = t >> 8;  // 32-row group over BH * Tq_pad / 32
-    const int part = static_cast<int>((t >> 5) & 7);
-    const int groups = Tq_pad >> 5;
-    if (grp >= BH * groups) return;
-    const long long bh = grp / groups;
-    const int i = static_cast<int>(grp - bh * groups) * 32 + static_cast<int>(t & 31);
-    if (i >= Tq) return;
-    const float4 a = *reinterpret_cast<const float4 *>(dq_acc + dq_acc_index(bh, Tq_pad, i, 2 * part));
-    const float4 b = *reinterpret_cast<const float4 *>(dq_acc + dq_acc_index(bh, Tq_pad, i, 2 * part + 1));
-    const uint4 w = make_uint4(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(a.z * scale, a.w * scale),
-                               pack_bf16x2(b.x * scale, b.y * scale), pack_bf16x2(b.z * scale, b.w * scale));
-    *reinterpret_cast<uint4 *>(dq + (bh * Tq + i) * HD + part * 8) = w;
+    bwd_convert_dq(static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x, dq_acc, dq, BH, Tq, Tq_pad, scale);
 }
 
 // P^T and dS^T of N of one thread's query columns for its key:
@@ -549,24 +480,6 @@ size_t bwd_workspace_bytes(long long BH, int Tq) {
     return r256(rows * HD * 4) + 2 * r256(rows * 4);
 }
 
-cudaError_t launch_attn_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
-                                const float *lse, float *nlse2, float *dvec, float *dq_acc, long long BH, int Tq,
-                                int Tq_pad, cudaStream_t stream) {
-    const long long threads = BH * Tq_pad * 8;
-    if (threads == 0) return cudaSuccess;
-    attn_bwd_pre<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec,
-                                                                                   dq_acc, BH, Tq, Tq_pad);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_attn_bwd_post(const float *dq_acc, __nv_bfloat16 *dq, long long BH, int Tq, int Tq_pad,
-                                 float scale, cudaStream_t stream) {
-    const long long threads = Tq > 0 ? BH * Tq_pad * 8 : 0;
-    if (threads == 0) return cudaSuccess;
-    return launch_kernel(attn_bwd_post, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, stream, true, 1,
-                         dq_acc, dq, BH, Tq, Tq_pad, scale);
-}
-
 cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const CUtensorMap &tg, const __nv_bfloat16 *o,
                                  const __nv_bfloat16 *dout, const float *lse, __nv_bfloat16 *dq,
@@ -581,8 +494,12 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
     p.nlse2 = nlse2;
     p.dvec = dvec;
     cudaError_t e = cudaSuccess;
-    if ((e = launch_attn_bwd_pre(o, nullptr, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, stream)) != cudaSuccess)
-        return e;
+    const long long pre_threads = static_cast<long long>(rows) * 8;
+    if (pre_threads > 0) {
+        attn_bwd_pre<<<static_cast<unsigned>((pre_threads + 255) / 256), 256, 0, stream>>>(
+            o, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     if (p.Tk > 0) {
         const size_t smem = sizeof(SmemBwd) + 1024;
         e = cudaFuncSetAttribute(attn_bwd_main, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -593,7 +510,10 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
             cudaSuccess)
             return e;
     }
-    return launch_attn_bwd_post(p.dq_acc, dq, BH, p.Tq, p.Tq_pad, p.scale, stream);
+    const long long post_threads = p.Tq > 0 ? BH * p.Tq_pad * 8 : 0;
+    if (post_threads == 0) return cudaSuccess;
+    return launch_kernel(attn_bwd_post, dim3(static_cast<unsigned>((post_threads + 255) / 256)), dim3(256), 0,
+                         stream, true, 1, static_cast<const float *>(p.dq_acc), dq, BH, p.Tq, p.Tq_pad, p.scale);
 }
 
 }  // namespace mha

@@ -537,6 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int sb = n % kSBufs;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
                 if (!ok) break;
+                if (!warp_live) {
+                    // P of the warp's rows stays whatever it is: a row of
+                    // tensor memory only reaches its own row of O
+                    if (lane == 0) {
+                        mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
+                        mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                    }
+                    continue;
+                }
                 tc_fence_after_sync();
                 const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
                 const bool edge = j * BN < it.full_lo || j * BN + BN > it.full_hi;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     const int key0 = j * BN + 64 * rd;  // the round's first key
                     bool done = false;
-                    if (linear && (!kCap || tier < 2) && warp_live &&
+                    if (linear && (!kCap || tier < 2) &&
                         (!edge || __all_sync(0xffffffffu, w.keys.x <= key0 && w.keys.y >= key0 + 64))) {
                         uint32_t pk[32];
                         const float ref = m_run == -INFINITY ? 0.f : m_run;

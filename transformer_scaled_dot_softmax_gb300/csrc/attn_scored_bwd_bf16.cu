@@ -7,20 +7,24 @@
 //   dtable[u, h] = sum over pairs of bucket u of dS,
 // dK and dV summed over the query heads that share the K/V head.
 //
-// Launches: the row terms and the dQ conversion are attn_bwd_bf16.cu's;
-// between them the kernel below, whose warp roles, tensor-memory plan and
-// issue order are attn_bwd_main's.  What differs:
+// Launches: one before (row terms; the expanded bias and document ranges of
+// scored_prep.cu), the kernel below, one after (dQ to bf16, sums of partial dK,
+// dV and dtable).  The kernel's warp roles, tensor-memory plan and issue order
+// are attn_bwd_main's (attn_bwd_bf16.cu).  What differs:
 //   * one CTA per (K/V head, 128 keys) walks (query head of the group, query
 //     block) pairs, so dK and dV of the group are summed in tensor memory, in
-//     a fixed order;
+//     a fixed order.  Where that makes too few CTAs the group's heads are
+//     divided among several, which leave fp32 sums for the last launch;
 //   * a key is seen by one interval of queries [lo, hi) (causal, prefix,
 //     documents and padding all end in one), which bounds the query blocks
 //     walked and masks the ones seen in part;
-//   * a bucket bias sums dS over equal distances: blocks nearer than the last
-//     bucket's distance leave the 255 diagonal sums of their 128 x 128 pairs
-//     in a slot of their own, all others add to one sum per direction; a
-//     second launch adds slots and buckets in a fixed order, so dtable does
-//     not depend on the order in which CTAs finish.
+//   * a bucket bias sums dS over the buckets of its distances.  A block pair
+//     past the last bucket's first distance adds up in one register per
+//     thread; in a nearer one each warp adds its 32 x 32 pairs along their
+//     diagonals (a shuffle and an add per pair), then each warp adds the
+//     diagonals of the buckets it owns.  A CTA leaves one sum per head and
+//     bucket, and the last launch adds those, all in a fixed order: dtable
+//     does not depend on the order in which CTAs finish.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -48,7 +52,7 @@ struct __align__(1024) Smem {
     float nlse2[kStages][BQ];
     float dvec[kStages][BQ];
     float diag[2][kSoftmaxWarps][64];  // a warp's 32 x 32 pairs by distance
-    float far[2][kSoftmaxWarps][2];    // a warp's far sums of one query head
+    float far[2][kSoftmaxWarps][2];    // a warp's far sums of one query head (past, future)
     uint64_t kv_full;
     uint64_t stage_full[kStages];
     uint64_t q_empty[kStages];
@@ -141,11 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int bkv = static_cast<int>(blockIdx.x);  // b Hkv + K/V head
+    const int bkv = static_cast<int>(blockIdx.x) / p.splits;  // b Hkv + K/V head
     const int kb = static_cast<int>(blockIdx.y);
     const int b = bkv / p.Hkv, kvh = bkv - b * p.Hkv;
-    const int group = p.H / p.Hkv;
-    const int h0 = kvh * group;  // first query head of the group
+    // this CTA's query heads [h0, h0 + group) of the K/V head's
+    const int split = static_cast<int>(blockIdx.x) - bkv * p.splits;
+    const int all = p.H / p.Hkv, per = (all + p.splits - 1) / p.splits;
+    const int group = max(0, min(per, all - split * per));
+    const int h0 = kvh * all + split * per;
     const int k0 = kb * BKB;
 
     if (threadIdx.x == 0) {
@@ -348,13 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // Bucket bias gradient.  `gen` counts this CTA's exchanges through
         // shared memory (one per near block, one per head for the far sums).
-        const bool want_bias = kBias == kBiasBuckets && p.diag != nullptr;
-        const int j_near0 = max(0, kb - p.near_blocks);  // query block of slot 0
+        // Warp wi owns the buckets wi, wi + 16, ...; lane i holds the sum of
+        // the i-th of them.
+        const bool want_bias = kBias == kBiasBuckets && p.bucket_part != nullptr;
+        const int n_buckets = p.bk.num * (p.bk.both ? 2 : 1);
         int gen = 0;
-        float diag_hi = 0.f, diag_lo = 0.f, far_past = 0.f, far_future = 0.f;
-        auto slot_of = [&](int head, int j) {
-            return p.diag + (((static_cast<long long>(b) * p.H + head) * gridDim.y + kb) * p.near_slots + (j - j_near0)) * 256;
-        };
+        float diag_hi = 0.f, diag_lo = 0.f, far_past = 0.f, far_future = 0.f, mine = 0.f;
         auto exchange = [&]() -> bool {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.diag_full);
@@ -362,54 +368,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++gen;
             return got;
         };
-        // The warps' sums of one near block, added over the (quadrant, chunk)
-        // blocks that hold each distance, in that order.
-        auto put_diag = [&](int head, int j) -> bool {
+        auto warp_sum = [](float x) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            return x;
+        };
+        auto put_near = [&](int j) -> bool {
             const int buf = gen & 1;
             sm.diag[buf][wi][lane + 32] = diag_hi;  // distance `lane` within the warp's 32 x 32
             sm.diag[buf][wi][lane] = diag_lo;       // distance lane - 32
             diag_hi = diag_lo = 0.f;
             if (!exchange()) return false;
-            const int id = wi * 32 + lane;  // distance id - 127
-            if (id < 256) {
+            const int mid = BKB * (kb - j);  // distance of the block pair's main diagonal
+            for (int i = 0, u = wi; u < n_buckets; ++i, u += kSoftmaxWarps) {
+                // the bucket's distances [d0, d1], as bucket_of() has them
+                const int x = u < p.bk.num ? u : u - p.bk.num;
+                const int near = p.bk.starts[x], far = x + 1 < p.bk.num ? p.bk.starts[x + 1] - 1 : 1 << 30;
+                int d0 = u < p.bk.num ? -far : max(near, 1);
+                int d1 = u < p.bk.num ? (u == 0 && !p.bk.both ? 1 << 30 : -near) : far;
+                d0 = max(d0, mid - (BQ - 1));
+                d1 = min(d1, mid + BKB - 1);
+                if (d0 > d1) continue;
                 float sum = 0.f;
-                if (id < 255) {
+                for (int d = d0 + lane; d <= d1; d += 32) {
+                    // the warps' blocks that hold distance d: quadrant q, chunk
+                    // q - k or q - k - 1 for k = floor((d - mid) / 32)
+                    const int k = (d - mid) >> 5, loc = (d - mid) - 32 * k;
 #pragma unroll
-                    for (int w = 0; w < kSoftmaxWarps; ++w) {
-                        // warp index w: chunk w / 4, quadrant (w + 2) % 4
-                        const int local = id - 127 - 32 * (((w + 2) & 3) - (w >> 2));
-                        if (local > -32 && local < 32) sum += sm.diag[buf][w][local + 32];
+                    for (int q = 0; q < 4; ++q) {
+                        // warp index of (quadrant q, chunk c): 4 c + (q + 2) % 4
+                        const int c0 = q - k, c1 = c0 - 1;
+                        if (c0 >= 0 && c0 < 4) sum += sm.diag[buf][4 * c0 + ((q + 2) & 3)][loc + 32];
+                        if (c1 >= 0 && c1 < 4) sum += sm.diag[buf][4 * c1 + ((q + 2) & 3)][loc];
                     }
                 }
-                slot_of(head, j)[id] = sum;
+                sum = warp_sum(sum);
+                if (lane == i) mine += sum;
             }
             return true;
         };
-        auto put_far = [&](int head) -> bool {
+        auto finish_head = [&](int head) -> bool {
             const int buf = gen & 1;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) {
-                far_past += __shfl_xor_sync(0xffffffffu, far_past, x);
-                far_future += __shfl_xor_sync(0xffffffffu, far_future, x);
-            }
+            far_past = warp_sum(far_past);
+            far_future = warp_sum(far_future);
             if (lane == 0) {
                 sm.far[buf][wi][0] = far_past;
                 sm.far[buf][wi][1] = far_future;
             }
             far_past = far_future = 0.f;
             if (!exchange()) return false;
-            if (wi == 0 && lane < 2) {
-                float sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < kSoftmaxWarps; ++w) sum += sm.far[buf][w][lane];
-                p.far_sum[((static_cast<long long>(b) * p.H + head) * gridDim.y + kb) * 2 + lane] = sum;
+            const int u = wi + kSoftmaxWarps * lane;
+            if (u < n_buckets) {
+                // far past: the last bucket; far future: the last of the
+                // other direction, or, with one direction, bucket 0
+                const bool past = u == p.bk.num - 1, future = u == (p.bk.both ? 2 * p.bk.num - 1 : 0);
+                for (int w = 0; past && w < kSoftmaxWarps; ++w) mine += sm.far[buf][w][0];
+                for (int w = 0; future && w < kSoftmaxWarps; ++w) mine += sm.far[buf][w][1];
+                p.bucket_part[((static_cast<long long>(b) * p.H + head) * gridDim.y + kb) * n_buckets + u] = mine;
             }
-            // slots of near blocks that no key of this block is seen from
-            for (int s = 0; s < p.near_slots; ++s) {
-                const int j = j_near0 + s;
-                if (j < j_begin || j >= j_begin + n_j)
-                    for (int x = wi * 32 + lane; x < 256; x += 32 * kSoftmaxWarps) slot_of(head, j)[x] = 0.f;
-            }
+            mine = 0.f;
             return true;
         };
 
@@ -491,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.pds_full);
             if (t >= 1 && !(ok = add_dq(t - 1, bh_prev, j_prev))) break;
-            if (near && !(ok = put_diag(head, j))) break;
+            if (near && !(ok = put_near(j))) break;
             j_prev = j;
             bh_prev = b * p.H + head;
             if (++j == j_begin + n_j) {
-                if (want_bias && !(ok = put_far(head))) break;
+                if (want_bias && !(ok = finish_head(head))) break;
                 j = j_begin;
                 ++head;
                 if (t + 1 < n_t) br = bias_row<kBias>(p.f, head);
@@ -503,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && n_t > 0) ok = add_dq(n_t - 1, bh_prev, j_prev);
         if (n_t == 0 && want_bias)
-            for (int x = 0; x < group && ok; ++x) ok = put_far(h0 + x);
+            for (int x = 0; x < group && ok; ++x) ok = finish_head(h0 + x);
         if (ok && n_t > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sm.acc_done, 0, ab));
         if (ok) {
             const bool is_dv = c >= 2;
@@ -519,15 +536,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 32; ++e) a[e] = 0u;
             }
             if (key < p.Tk && in_bounds(key >= 0 && bkv < p.B * p.Hkv, p.status)) {
-                const float f = is_dv ? 1.f : p.scale;
-                __nv_bfloat16 *dst = (is_dv ? p.dv : p.dk) + (static_cast<long long>(bkv) * p.Tk + key) * HD + f0;
-                uint32_t w[16];
+                if (p.splits > 1) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        (is_dv ? p.part_dv : p.part_dk) +
+                        ((static_cast<long long>(split) * p.B * p.Hkv + bkv) * p.Tk + key) * HD + f0);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * f, __uint_as_float(a[2 * e + 1]) * f);
+                    for (int x = 0; x < 8; ++x) dst[x] = make_uint4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
+                } else {
+                    const float f = is_dv ? 1.f : p.scale;
+                    __nv_bfloat16 *dst = (is_dv ? p.dv : p.dk) + (static_cast<long long>(bkv) * p.Tk + key) * HD + f0;
+                    uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    reinterpret_cast<uint4 *>(dst)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(a[2 * e]) * f, __uint_as_float(a[2 * e + 1]) * f);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        reinterpret_cast<uint4 *>(dst)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                }
             }
         }
         if (!ok) tmem_st_wait();
@@ -548,7 +573,7 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
     const size_t smem = sizeof(Smem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    dim3 grid(static_cast<unsigned>(p.B * p.Hkv), static_cast<unsigned>((p.Tk + BKB - 1) / BKB));
+    dim3 grid(static_cast<unsigned>(p.B * p.Hkv * p.splits), static_cast<unsigned>((p.Tk + BKB - 1) / BKB));
     return launch_kernel(kernel, grid, dim3(kThreads), smem, stream, true, 1, tq, tk, tv, tg, p);
 }
 

@@ -116,13 +116,6 @@ cudaError_t launch_attn_bwd_bf16(const CUtensorMap &tq, const CUtensorMap &tk, c
                                  const __nv_bfloat16 *dout, const float *lse, __nv_bfloat16 *dq,
                                  BwdParams p, void *workspace, cudaStream_t stream);
 
-// The backward's row-term launch and dQ conversion, shared with the scored
-// backward; heads padded to Tq_pad rows.  o_lo (may be null) is added to o.
-cudaError_t launch_attn_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout, const float *lse, float *nlse2,
-                                float *dvec, float *dq_acc, long long BH, int Tq, int Tq_pad, cudaStream_t stream);
-cudaError_t launch_attn_bwd_post(const float *dq_acc, __nv_bfloat16 *dq, long long BH, int Tq, int Tq_pad,
-                                 float scale, cudaStream_t stream);
-
 // ------------------------------------------------ scored attention
 // Scores beyond scale q.k (see scores.cuh): what the kernels need of them.
 enum BiasKind { kBiasNone = 0, kBiasSlopes = 1, kBiasBuckets = 2 };
@@ -208,20 +201,28 @@ struct ScoredBwdParams {
     const float *nlse2, *dvec;  // as BwdParams
     float *dq_acc;
     __nv_bfloat16 *dk, *dv;     // (B, Hkv, Tk, 64)
-    // bucket bias gradient (null: none): sums of dS over equal distances
-    float *diag;                // (B, H, key blocks, near_slots, 256)
-    float *far_sum;             // (B, H, key blocks, 2): past, future distances beyond `near_slots`
-    int near_blocks, near_slots;
+    // CTAs that share a K/V head's query heads; more than one leave fp32 sums,
+    // part_dk, part_dv (splits, B, Hkv, Tk, 64), instead of dk and dv
+    int splits;
+    float *part_dk, *part_dv;
+    // bucket bias gradient (bucket_part null: none): (B, H, key blocks, buckets);
+    // block pairs up to near_blocks apart hold distances below the last bucket's
+    float *bucket_part;
+    int near_blocks;
+    BucketParams bk;
     int *status;
 };
+// Before it: row terms of o (+ o_lo, may be null) and dout, a zeroed dq_acc,
+// and what launch_scored_prep writes.  After it: dq, and dk, dv (splits > 1)
+// and dtable (not null) from the partial sums.
+cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
+                                  const float *lse, float *nlse2, float *dvec, const ScoredBwdParams &p, float *vec,
+                                  int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream);
+cudaError_t launch_scored_bwd_post(const ScoredBwdParams &p, __nv_bfloat16 *dq, __nv_bfloat16 *dtable,
+                                   cudaStream_t stream);
 cudaError_t launch_attn_scored_bwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                    const CUtensorMap &tg, bool capped, int bias, const ScoredBwdParams &p,
                                    cudaStream_t stream);
-
-// dtable (num [* 2], H) from the backward's sums; sums: (H, 2 near + 1, 256) scratch.
-cudaError_t launch_scored_dtable(const float *diag, const float *far_sum, float *sums, __nv_bfloat16 *dtable, int B, int H,
-                                 int n_kb, int n_qb, int near, int near_slots, const BucketParams &bk,
-                                 cudaStream_t stream);
 
 // ------------------------------------------------ decoding: partial sums to outputs
 constexpr int kSmsPerGpu = 152;  // for the choice of key ranges, which fixes the workspace

@@ -1,10 +1,12 @@
-// scored_prep.cu -- the small launches around scored attention: before it the
-// expanded bucket bias and the document ranges, after the backward the bias
-// table's gradient.
+// scored_prep.cu -- the small launches around scored attention: the expanded
+// bucket bias and the document ranges before it (with the row terms, before
+// the backward), and after the backward dQ, dK, dV and dtable from the sums
+// that it left.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
+#include "attn_bwd_rows.cuh"
 #include "kernels.h"
 #include "scores.cuh"
 #include "sm103_ptx.cuh"
@@ -22,136 +24,158 @@ __device__ __forceinline__ int bucket_of(const BucketParams &bk, int d) {
     return u + (bk.both && d > 0 ? bk.num : 0);
 }
 
-// Threads [0, n_vec) each write one entry of vec, the next B T one document
-// range: the first position of the thread's document and the one past its
-// last, by bisection (the ids do not decrease).  Latency-bound: log2 T
-// dependent loads.
-__global__ void scored_prep(float *__restrict__ vec, int mid, long long n_vec, int H,
-                            const __grid_constant__ BucketParams bk, int2 *__restrict__ doc_range,
-                            const int32_t *__restrict__ doc_ids, int B, int T) {
-    pdl_launch_dependents();
-    const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+struct PrepParams {
+    float *vec;  // (H, 2 mid + 1), or null
+    int mid, H;
+    BucketParams bk;
+    int2 *doc_range;  // (B, T), or null
+    const int32_t *doc_ids;
+    int B, T;
+    long long vec_entries() const { return vec ? static_cast<long long>(H) * (2 * mid + 1) : 0; }
+    long long entries() const { return vec_entries() + (doc_range ? static_cast<long long>(B) * T : 0); }
+};
+
+// Entry i: one of vec, then one document range -- the first position of the
+// entry's document and the one past its last, both by bisection at once (the
+// ids do not decrease).  Latency-bound: log2 T dependent loads.
+__device__ __forceinline__ void prep_entry(const PrepParams &p, long long n_vec, long long i) {
     if (i < n_vec) {
-        const int len = 2 * mid + 1;
+        const int len = 2 * p.mid + 1;
         const int h = static_cast<int>(i / len);
-        const int d = static_cast<int>(i - static_cast<long long>(h) * len) - mid;
-        vec[i] = __bfloat162float(bk.table[bucket_of(bk, d) * H + h]) * kLog2E;
+        const int d = static_cast<int>(i - static_cast<long long>(h) * len) - p.mid;
+        p.vec[i] = __bfloat162float(p.bk.table[bucket_of(p.bk, d) * p.H + h]) * kLog2E;
         return;
     }
     const long long x = i - n_vec;
-    if (!doc_range || x >= static_cast<long long>(B) * T) return;
-    const int t = static_cast<int>(x % T);
-    const int32_t *ids = doc_ids + (x - t);
+    if (!p.doc_range || x >= static_cast<long long>(p.B) * p.T) return;
+    const int t = static_cast<int>(x % p.T);
+    const int32_t *ids = p.doc_ids + (x - t);
     const int32_t id = ids[t];
-    int lo = 0, hi = t;  // first position with ids >= id
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (ids[m] < id)
-            lo = m + 1;
-        else
-            hi = m;
+    int lo = 0, hi = t;       // first position with ids >= id is in [lo, hi]
+    int a = t + 1, z = p.T;   // first position past t with ids > id is in [a, z]
+    while (lo < hi || a < z) {
+        const int m0 = (lo + hi) >> 1, m1 = (a + z) >> 1;
+        const int32_t v0 = ids[min(m0, p.T - 1)], v1 = ids[min(m1, p.T - 1)];
+        if (lo < hi) {
+            if (v0 < id)
+                lo = m0 + 1;
+            else
+                hi = m0;
+        }
+        if (a < z) {
+            if (v1 > id)
+                z = m1;
+            else
+                a = m1 + 1;
+        }
     }
-    int a = t + 1, z = T;  // first position past t with ids > id
-    while (a < z) {
-        const int m = (a + z) >> 1;
-        if (ids[m] > id)
-            z = m;
-        else
-            a = m + 1;
-    }
-    doc_range[x] = make_int2(lo, a);
+    p.doc_range[x] = make_int2(lo, a);
 }
 
-// Sums of dS over equal distances, all blocks together: block (h, x) adds the
-// slots of the block pairs with kb - j = x - near over batch and key blocks, in
-// that order (four interleaved chains).  sums: (H, 2 near + 1, 256).
-__global__ void __launch_bounds__(1024) sum_diagonals(const float *__restrict__ diag, float *__restrict__ sums, int B,
-                                                      int H, int n_kb, int n_qb, int near, int near_slots) {
-    __shared__ float part[4][256];
+__global__ void __launch_bounds__(kThreads) scored_prep(const __grid_constant__ PrepParams p, long long n_vec) {
     pdl_launch_dependents();
-    pdl_wait();
-    const int h = blockIdx.x, off = static_cast<int>(blockIdx.y) - near;  // kb - j
-    const int id = threadIdx.x & 255, chain = threadIdx.x >> 8;
-    const int kb0 = max(0, off), kb1 = min(n_kb, n_qb + off);  // j = kb - off in [0, n_qb)
-    float sum = 0.f;
-    for (int b = 0; b < B; ++b) {
-        const float *head = diag + (static_cast<long long>(b) * H + h) * n_kb * near_slots * 256 + id;
-#pragma unroll 4
-        for (int kb = kb0 + chain; kb < kb1; kb += 4) {
-            const int slot = kb - off - max(0, kb - near);
-            sum += head[(static_cast<long long>(kb) * near_slots + slot) * 256];
-        }
-    }
-    part[chain][id] = sum;
-    __syncthreads();
-    if (chain == 0)
-        sums[(static_cast<long long>(h) * gridDim.y + blockIdx.y) * 256 + id] =
-            (part[0][id] + part[1][id]) + (part[2][id] + part[3][id]);
+    prep_entry(p, n_vec, static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x);
 }
 
-// dtable[u, h] from the distance sums and the far sums: block (u, h) adds the
-// distances of bucket u (and the far sums of its direction, if it is the one
-// that holds them), threads in a fixed order.
-__global__ void __launch_bounds__(kThreads) sum_buckets(const float *__restrict__ sums, const float *__restrict__ far_sum,
-                                                        __nv_bfloat16 *__restrict__ dtable, int B, int H, int n_kb,
-                                                        int near, const __grid_constant__ BucketParams bk) {
-    __shared__ float part[kThreads / 32];
+// Blocks [0, row_blocks): row terms; the others: preparation.
+__global__ void __launch_bounds__(kThreads)
+    scored_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ o_lo,
+                   const __nv_bfloat16 *__restrict__ dout, const float *__restrict__ lse, float *__restrict__ nlse2,
+                   float *__restrict__ dvec, float *__restrict__ dq_acc, long long BH, int Tq, int Tq_pad,
+                   unsigned row_blocks, const __grid_constant__ PrepParams p, long long n_vec) {
+    pdl_launch_dependents();
+    if (blockIdx.x < row_blocks)
+        bwd_row_terms(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, o, o_lo, dout, lse, nlse2, dvec, dq_acc,
+                      BH, Tq, Tq_pad);
+    else
+        prep_entry(p, n_vec, static_cast<long long>(blockIdx.x - row_blocks) * kThreads + threadIdx.x);
+}
+
+// Blocks [0, dq_blocks): dQ to bf16.  The next kv_blocks: dK (times scale) and
+// dV from their partial sums, a thread 8 features of a row.  The others: 32
+// buckets of one head each, a lane one bucket, the 8 warps every eighth
+// (batch entry, key block) each, all added in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+    scored_bwd_post(const __grid_constant__ ScoredBwdParams p, __nv_bfloat16 *__restrict__ dq,
+                    __nv_bfloat16 *__restrict__ dtable, unsigned dq_blocks, unsigned kv_blocks, int n_kb) {
+    __shared__ float part[kThreads / 32][32];
     pdl_wait();
-    const int u = blockIdx.x, h = blockIdx.y;
-    const int rows = 2 * near + 1;
-    float sum = 0.f;
-    if (sums) {
-        for (int x = threadIdx.x; x < rows * 256; x += kThreads) {
-            const int id = x & 255, off = (x >> 8) - near;
-            if (id < 255 && bucket_of(bk, 128 * off + id - 127) == u)
-                sum += sums[(static_cast<long long>(h) * rows + (x >> 8)) * 256 + id];
-        }
-        // far past: the last bucket; far future: the last of the other
-        // direction, or, with one direction, bucket 0
-        const bool past = u == bk.num - 1, future = u == (bk.both ? 2 * bk.num - 1 : 0);
-        if (past || future)
-            for (int x = threadIdx.x; x < B * n_kb; x += kThreads) {
-                const int b = x / n_kb, kb = x - b * n_kb;
-                const float *f = far_sum + ((static_cast<long long>(b) * H + h) * n_kb + kb) * 2;
-                if (past) sum += f[0];
-                if (future) sum += f[1];
-            }
+    if (blockIdx.x < dq_blocks) {
+        bwd_convert_dq(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, p.dq_acc, dq,
+                       static_cast<long long>(p.B) * p.H, p.Tq, p.Tq_pad, p.scale);
+        return;
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    if (blockIdx.x < dq_blocks + kv_blocks) {
+        const long long n = static_cast<long long>(p.B) * p.Hkv * p.Tk * 8;  // of one tensor
+        long long t = static_cast<long long>(blockIdx.x - dq_blocks) * kThreads + threadIdx.x;
+        if (t >= 2 * n) return;
+        const bool is_dv = t >= n;
+        if (is_dv) t -= n;
+        const float f = is_dv ? 1.f : p.scale;
+        float s[8] = {};
+        for (int x = 0; x < p.splits; ++x) {
+            const float4 *src = reinterpret_cast<const float4 *>((is_dv ? p.part_dv : p.part_dk) + (x * n + t) * 8);
+            const float4 a = src[0], b = src[1];
+            s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+            s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+        }
+        reinterpret_cast<uint4 *>(is_dv ? p.dv : p.dk)[t] =
+            make_uint4(pack_bf16x2(s[0] * f, s[1] * f), pack_bf16x2(s[2] * f, s[3] * f), pack_bf16x2(s[4] * f, s[5] * f),
+                       pack_bf16x2(s[6] * f, s[7] * f));
+        return;
+    }
+    const int total = p.bk.num * (p.bk.both ? 2 : 1), per_head = (total + 31) / 32;
+    const int x = static_cast<int>(blockIdx.x - dq_blocks - kv_blocks);
+    const int h = x / per_head, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int u = (x - h * per_head) * 32 + lane;
+    float sum = 0.f;
+    if (u < total)
+#pragma unroll 4
+        for (int i = warp; i < p.B * n_kb; i += kThreads / 32) {
+            const int b = i / n_kb, kb = i - b * n_kb;
+            sum += p.bucket_part[((static_cast<long long>(b) * p.H + h) * n_kb + kb) * total + u];
+        }
+    part[warp][lane] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int x = 0; x < kThreads / 32; ++x) s += part[x];
-        dtable[u * H + h] = __float2bfloat16_rn(s);
+    if (warp == 0 && u < total) {
+        for (int w = 1; w < kThreads / 32; ++w) sum += part[w][lane];
+        dtable[u * p.H + h] = __float2bfloat16_rn(sum);
     }
 }
+
+unsigned blocks_of(long long threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
 
 }  // namespace
 
 cudaError_t launch_scored_prep(float *vec, int far, int H, const BucketParams &bk, int2 *doc_range,
                                const int32_t *doc_ids, int B, int T, cudaStream_t stream) {
-    const int mid = far + 64;
-    const long long n_vec = vec ? static_cast<long long>(H) * (2 * mid + 1) : 0;
-    const long long n = n_vec + (doc_range ? static_cast<long long>(B) * T : 0);
-    if (n == 0) return cudaSuccess;
-    scored_prep<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(vec, mid, n_vec, H, bk,
-                                                                                               doc_range, doc_ids, B, T);
+    const PrepParams p{vec, far + 64, H, bk, doc_range, doc_ids, B, T};
+    if (p.entries() == 0) return cudaSuccess;
+    scored_prep<<<blocks_of(p.entries()), kThreads, 0, stream>>>(p, p.vec_entries());
     return cudaGetLastError();
 }
 
-cudaError_t launch_scored_dtable(const float *diag, const float *far_sum, float *sums, __nv_bfloat16 *dtable, int B, int H,
-                                 int n_kb, int n_qb, int near, int near_slots, const BucketParams &bk,
-                                 cudaStream_t stream) {
-    const int total = bk.num * (bk.both ? 2 : 1);
-    const bool any = B > 0 && n_kb > 0 && n_qb > 0;
-    cudaError_t e;
-    if (any && (e = launch_kernel(sum_diagonals, dim3(H, 2 * near + 1), dim3(1024), 0, stream, true, 1, diag, sums, B, H,
-                                  n_kb, n_qb, near, near_slots)) != cudaSuccess)
-        return e;
-    return launch_kernel(sum_buckets, dim3(total, H), dim3(kThreads), 0, stream, any, 1,
-                         any ? static_cast<const float *>(sums) : nullptr, far_sum, dtable, B, H, n_kb, near, bk);
+cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
+                                  const float *lse, float *nlse2, float *dvec, const ScoredBwdParams &p, float *vec,
+                                  int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream) {
+    const long long BH = static_cast<long long>(p.B) * p.H;
+    const PrepParams pp{vec, p.f.mid, p.H, p.bk, doc_range, doc_ids, p.B, p.Tk};
+    const unsigned rows = blocks_of(BH * p.Tq_pad * 8), prep = blocks_of(pp.entries());
+    if (rows + prep == 0) return cudaSuccess;
+    scored_bwd_pre<<<rows + prep, kThreads, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows,
+                                                         pp, pp.vec_entries());
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scored_bwd_post(const ScoredBwdParams &p, __nv_bfloat16 *dq, __nv_bfloat16 *dtable,
+                                   cudaStream_t stream) {
+    const unsigned dq_blocks = p.Tq > 0 ? blocks_of(static_cast<long long>(p.B) * p.H * p.Tq_pad * 8) : 0;
+    const unsigned kv_blocks = p.splits > 1 ? blocks_of(static_cast<long long>(p.B) * p.Hkv * p.Tk * 16) : 0;
+    const unsigned table_blocks = dtable ? p.H * ((p.bk.num * (p.bk.both ? 2 : 1) + 31) / 32) : 0;
+    const unsigned n = dq_blocks + kv_blocks + table_blocks;
+    if (n == 0) return cudaSuccess;
+    return launch_kernel(scored_bwd_post, dim3(n), dim3(kThreads), 0, stream, true, 1, p, dq, dtable, dq_blocks, kv_blocks,
+                         p.Tq > 0 ? (p.Tk + 127) / 128 : 0);
 }
 
 }  // namespace mha
