@@ -2,18 +2,19 @@
 bounds on what the library's roundings may change.
 
 Bounds.  u = 2^-8 is the relative rounding of one bf16 rounding (half a step), w the exact weights.
-  weights  A weight enters P V rounded to bf16 (u) after a score error e_s, |e_s| <= SCORE (below); numerator and
-           normaliser use the same rounded weights, so o moves by at most (u + e) (sum w |v| + |o|), e = 2 e_s, and is
-           rounded once: u |o|.
-  lse      ln of the sum of the unrounded weights: e absolute, plus fp32.
+  weights  A weight enters P V after a score error e_s, |e_s| <= SCORE (below), and rounded to bf16 (r = u), or with lse
+           as two bf16 parts (r = u^2); numerator and normaliser use the same weights, so o moves by at most
+           (r + e) (sum w |v| + |o|), e = 2 e_s, and is rounded once: u |o|.
+  lse      ln of the sum of the weights: e absolute, plus fp32.
   P        recomputed as exp(s - lse): relative 2 e (score and lse), and rounded for dV: u.
-  D        sum dO o of the library's o + o_lo: the weights' roundings d_j move it by sum d_j w_j (dP_j - D), at most
-           (u + e) sum |dS|, the pair's own rounding by u^2 sum |dO| |o|; without o_lo by u sum |dO| |o|.
+  D        sum dO o of the library's o + o_lo: the weights' errors d_j move it by sum d_j w_j (dP_j - D), at most
+           (u^2 + e) sum |dS|, the pair's own rounding by u^2 sum |dO| |o|; without o_lo by u sum |dO| |o|.
   dS       relative 2 e, and P |dD|; rounded: u.  dP and D are fp32 sums of 64 products: 2^-16 of sum |dO| |v|.
   dq, dk, dv, dtable: the sums of those, rounded once more (u).
 A second check on the relative 2-norm takes each rounding at its mean square, u / sqrt(3), in quadrature (check's
-`roundings`).  Not for dtable: it holds sums of dS over buckets, and sum_j dS_ij = 0, so a bucket with most of a row's
-weight sums to little, while D's error enters it with sum_j P_ij = 1; there the elementwise bound alone stands.
+`roundings`).  That is an average: it holds where the tensor comes of many rows, and the check is left out below 64.  Nor
+for dtable: it holds sums of dS over buckets, and sum_j dS_ij = 0, so a bucket with most of a row's weight sums to little,
+while D's error enters it with sum_j P_ij = 1; there the elementwise bound alone stands.
 """
 import math
 
@@ -71,7 +72,7 @@ def weights(z, cap, bias, vis):
 
 
 def attention(q, k, v, *, scale, cap=None, slopes=None, table=None, bucket_starts=None, mask="none", key_lens=None,
-              prefix_lens=None, doc_ids=None, dout=None, o_lo=True):
+              prefix_lens=None, doc_ids=None, dout=None, o_lo=True, two_parts=False):
     """dict of exact values and, under the same names with "_tol", elementwise bounds."""
     B, h, T_q, d = q.shape
     h_kv, T_k = k.shape[1], k.shape[2]
@@ -89,7 +90,7 @@ def attention(q, k, v, *, scale, cap=None, slopes=None, table=None, bucket_start
     e = 2 * torch.where(vis, score_error(cap, mag), 0.0).amax(-1, keepdim=True)
     # weights that vanish beside their row's largest are flushed or underflow: 2^-120 of it at most
     r = {"o": p @ ve, "lse": lse}
-    r["o_tol"] = (U + e) * (p @ ve.abs() + r["o"].abs()) + U * r["o"].abs() + 1e-30
+    r["o_tol"] = ((U * U if two_parts else U) + e) * (p @ ve.abs() + r["o"].abs()) + U * r["o"].abs() + 1e-30
     r["lse_tol"] = e[..., 0] + 2.0 ** -22 * lse.abs().nan_to_num(0, 0, 0)
     if dout is None:
         return r
@@ -97,7 +98,7 @@ def attention(q, k, v, *, scale, cap=None, slopes=None, table=None, bucket_start
     dp = go @ ve.transpose(2, 3)
     D = (go * r["o"]).sum(-1, keepdim=True)
     ds = p * (dp - D)
-    D_tol = 1.02 * (U + e) * ds.abs().sum(-1, keepdim=True) + (2.0 ** -15 if o_lo else U) * (go.abs() * r["o"].abs()).sum(-1, keepdim=True)
+    D_tol = 1.02 * (U * U + e) * ds.abs().sum(-1, keepdim=True) + (2.0 ** -15 if o_lo else U) * (go.abs() * r["o"].abs()).sum(-1, keepdim=True)
     dp_tol = 2.0 ** -16 * (go.abs() @ ve.abs().transpose(2, 3))
     ds_tol = 2 * e * 1.05 * ds.abs() + 1.05 * p * (D_tol + dp_tol)
     f = 1.0 if t is None else 1 - t * t
@@ -152,7 +153,7 @@ def decode(q, k_prefix, v_prefix, k_cache, v_cache, cache_lens, *, scale, cap=No
     return o, tol
 
 
-def check(name, got, ref, tol, roundings):
+def check(name, got, ref, tol, roundings, rows=64):
     got = got.double()
     assert bool(torch.isfinite(got).all()) or not bool(torch.isfinite(ref).all()), name + ": not finite"
     fin = torch.isfinite(ref)
@@ -162,6 +163,6 @@ def check(name, got, ref, tol, roundings):
     assert worst <= 1, "%s: %.3g of the bound (largest error %.3g, |ref| up to %.3g)" % (
         name, worst, off.max().item(), ref[fin].abs().max().item())
     norm = ref[fin].norm().item()
-    if roundings and norm > 1e-3 * math.sqrt(max(off.numel(), 1)):
+    if roundings and rows >= 64 and norm > 1e-3 * math.sqrt(max(off.numel(), 1)):
         rel = off.norm().item() / norm
         assert rel <= U * math.sqrt(roundings / 3.0), "%s: relative error %.3g" % (name, rel)

@@ -26,7 +26,7 @@ def compare(lib, x, lens, form):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     want, tol = ref.decode(*x, lens, **{**form, "scale": form.get("scale") or 0.125})
-    ref.check("o", o, want, tol, 2)
+    ref.check("o", o, want, tol, 2, x[0].shape[0] * x[0].shape[1] * x[0].shape[2])
     return o
 
 
@@ -111,7 +111,7 @@ def test_training_step_then_serving(lib):
     dq, dk, dv, dtable = lib.sdpa_scored_backward(q, k, v, o, go, lse, mask="causal", o_lo=lo, **form)
     want = ref.attention(q, k, v, scale=0.125, mask="causal", dout=go, **form)
     for name, got in (("dq", dq), ("dk", dk), ("dv", dv), ("dtable", dtable)):
-        ref.check(name, got, want[name], want[name + "_tol"], 0 if name == "dtable" else 3)
+        ref.check(name, got, want[name], want[name + "_tol"], 0 if name == "dtable" else 2)
     form["table"] = (form["table"].float() - 0.1 * dtable.float()).to(BF)
     x = make(B, h, h_kv, 1, 150, 40, 12)
     compare(lib, x, ints(40, 13), form)

@@ -15,10 +15,15 @@
 // prefixes and documents all end in one, so a tile is masked by two
 // comparisons per key, and only tiles that some row sees in part are.
 //
-// With the log-sum-exp exported (the training forward) the row sum is also kept
-// of the unrounded weights, for lse alone, and the output's rounding remainder
-// can be stored beside it: the backward's P = 2^(y - lse) and D = rowsum(dO O)
-// then carry no bf16 rounding of this pass.
+// With the log-sum-exp exported (the training forward) P is multiplied as two
+// bf16 parts, P = hi + lo, hi the rounded weight and lo the rounded rest: O and
+// with it the backward's row terms D = rowsum(dO O) then carry no rounding of
+// the weights.  (With hi alone D is off by sum_j d_j w_j (dP_j - D), d_j the
+// weights' relative roundings, and every dS of the row with it: dQ and dtable
+// were 1.5 to 1.6 times as far from fp64 as fp32 arithmetic rounded once.)  It
+// costs the tensor cores half as much again, which they have to spare, and a
+// softmax thread one instruction per score.  The output's own rounding
+// remainder can be stored beside it.
 //
 // The pipeline (persistent CTAs, TMA ring, S issuer, two PV issuers, two
 // softmax groups on alternate tiles, output warps, three rotating score
@@ -90,7 +95,6 @@ struct __align__(1024) Smem {
     uint8_t v[STAGES][kTileBytes];
     float red_m[2][BM];
     float red_l[2][BM];
-    float red_e[2][BM];
     uint64_t q_full[2];
     uint64_t q_empty[2];
     uint64_t kv_full[STAGES];
@@ -126,6 +130,14 @@ __device__ __forceinline__ int2 row_keys(const VisParams &v, int Tk, int Tq, int
         hi = min(hi, d.y);
     }
     return make_int2(lo, hi);
+}
+
+// Column, in its score buffer, of the packed weights of keys 64 rd + 16 kk ..
+// + 15 (8 columns): over scores already read.  With lo parts, each 32 keys'
+// weights lie over their own scores, 16 columns of hi, then 16 of lo.
+template <int kMode>
+__device__ __forceinline__ constexpr uint32_t weight_col(int rd, int kk) {
+    return kMode == kForwardLse ? 64u * rd + 32u * (kk >> 1) + 8u * (kk & 1) : 32u * rd + 8u * kk;
 }
 
 template <int kMode>
@@ -399,19 +411,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (!(ok = warp_wait(&sm.p_rd[hf][0][slot], par, ab))) break;
-                tc_fence_after_sync();
                 const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
                 const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, (jt >= 2 || kk > 0) ? 1u : 0u);
-                warp_commit(&sm.pv0[hf][slot]);
-                if (!(ok = warp_wait(&sm.p_rd[hf][1][slot], par, ab))) break;
-                tc_fence_after_sync();
+                for (int rd = 0; rd < 2; ++rd) {
+                    if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
+                    tc_fence_after_sync();
 #pragma unroll
-                for (int kk = 4; kk < 8; ++kk)
-                    warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, 1u);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u;
+                        warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk), vd + 128 * (4 * rd + kk), idesc_o, acc);
+                        if (kMode == kForwardLse)
+                            warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk) + 16, vd + 128 * (4 * rd + kk), idesc_o, 1u);
+                    }
+                    if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                }
+                if (!ok) break;
                 warp_commit(&sm.kv_empty[st]);
             }
             if (!ok) break;
@@ -427,33 +442,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = static_cast<int>(lane_base) + lane;
         const uint32_t tl = tmem_addr(tmem, lane_base, 0);
         const uint32_t to = tl + kOCol + 64u * half;
-        // 2^y of 32 scores in bf16 and the fp32 sum of the rounded weights (the
-        // values P V multiplies, so that normalised weights sum to 1); exact:
-        // with lse, the sum of the unrounded ones.
-        auto weigh = [](const uint32_t(&y)[32], uint32_t(&pk)[16], float &exact) -> float {
-            uint64_t ex = 0;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float x0 = ex2_approx(__uint_as_float(y[2 * c])), x1 = ex2_approx(__uint_as_float(y[2 * c + 1]));
-                pk[c] = pack_bf16x2(x0, x1);
-                if (kMode == kForwardLse) ex = add_f32x2(ex, f32x2_pack(x0, x1));
-                add_bf16x2_to_f32(acc[2 * (c & 1)], acc[2 * (c & 1) + 1], pk[c]);
-            }
-            if (kMode == kForwardLse) {
+        // Weights of a pair of keys: packed, with lo parts where they are
+        // kept, and added to the row sum -- the rounded weights, which are
+        // what P V multiplies, so that normalised weights sum to 1; with lo
+        // parts the weights themselves.
+        struct Sum {
+            uint64_t both = 0;
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+            __device__ __forceinline__ float get() const {
                 float e0, e1;
-                f32x2_unpack(ex, e0, e1);
-                exact = e0 + e1;
+                f32x2_unpack(both, e0, e1);
+                return kMode == kForwardLse ? e0 + e1 : (a[0] + a[1]) + (a[2] + a[3]);
             }
-            return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        };
+        auto pack_pair = [](float x0, float x1, int c, uint32_t &hi, uint32_t &lo, Sum &sum) {
+            hi = pack_bf16x2(x0, x1);
+            if (kMode == kForwardLse) {
+                const uint64_t x = f32x2_pack(x0, x1);
+                float r0, r1;
+                f32x2_unpack(sub_f32x2(x, f32x2_pack(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u))), r0, r1);
+                lo = pack_bf16x2(r0, r1);
+                sum.both = add_f32x2(sum.both, x);
+            } else {
+                add_bf16x2_to_f32(sum.a[2 * (c & 1)], sum.a[2 * (c & 1) + 1], hi);
+            }
         };
         // The common round, load to packed weights in one straight line:
         // y = u mul + b0 + c step.  a: its first 16 scores, on their way from
         // tensor memory; the others follow 16 by 16 while the ones before them
-        // are worked on, and `next` starts the first of the round after it.  kind 0: no cap, 1: near, 2: wide range; big: the
-        // largest squared argument of the polynomial.
+        // are worked on, and `next` starts the first of the round after it.
+        // kind 0: no cap, 1: near, 2: wide range; big: the largest squared
+        // argument of the polynomial.  pk: the round's 64 weights; with lo parts
+        // 32 keys' hi and lo, of which `half_done` takes the first 32 keys' and
+        // says whether to go on.
         auto common_round = [&](auto kind, uint32_t tr, uint32_t(&a)[16], bool next, float b0, float step,
-                                uint32_t(&pk)[32], float &exact, float &big) -> float {
+                                uint32_t(&pk)[32], Sum &sum, float &big, auto half_done) -> bool {
             constexpr int kKind = decltype(kind)::value;
             uint32_t b16[16];
             const uint64_t mul2 = f32x2_set(kKind == 2 ? p.f.cap_in : p.f.mul);
@@ -464,8 +487,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kChains; ++i) b[i] = f32x2_pack(fmaf(2.f * i, step, b0), fmaf(2.f * i + 1.f, step, b0));
             const uint64_t step2 = f32x2_set(8.f * step);
-            uint64_t ex = 0;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
             float big0 = 0.f, big1 = 0.f;
             auto take = [&](const uint32_t(&sc)[16], int part) {
 #pragma unroll
@@ -490,10 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f32x2_unpack(y, x0, x1);
                     x0 = ex2_approx(x0);
                     x1 = ex2_approx(x1);
-                    const uint32_t w = pack_bf16x2(x0, x1);
-                    pk[8 * part + c] = w;
-                    if (kMode == kForwardLse) ex = add_f32x2(ex, f32x2_pack(x0, x1));
-                    add_bf16x2_to_f32(acc[2 * (c & 1)], acc[2 * (c & 1) + 1], w);
+                    const int at = kMode == kForwardLse ? 8 * (part & 1) + c : 8 * part + c;
+                    pack_pair(x0, x1, c, pk[at], pk[(16 + at) & 31], sum);
                 }
             };
             tmem_ld_wait(a);
@@ -502,19 +521,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait(b16);
             tmem_ld16(tr + 32, a);
             take(b16, 1);
+            big = fmaxf(big0, big1);
+            if (kMode == kForwardLse && !half_done()) return false;
             tmem_ld_wait(a);
             tmem_ld16(tr + 48, b16);
             take(a, 2);
             tmem_ld_wait(b16);
             if (next) tmem_ld16(tr + 64, a);
             take(b16, 3);
-            if (kMode == kForwardLse) {
-                float e0, e1;
-                f32x2_unpack(ex, e0, e1);
-                exact = e0 + e1;
-            }
             big = fmaxf(big0, big1);
-            return (acc[0] + acc[1]) + (acc[2] + acc[3]);
+            return true;
         };
 
         int n = 0, v = 0;
@@ -527,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // decoding: rows past the stacked ones have nothing to compute
             const bool warp_live = kMode != kDecode || __any_sync(0xffffffffu, w.live);
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
-            float l_run = 0.f, e_run = 0.f;
+            float l_run = 0.f;
             // the range the warp's capped scores need: near, wide, any
             int tier = kCap && p.f.near_max == 0.f ? 1 : 0;
 
@@ -555,13 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld16(ts, a);
 #pragma unroll 1
                 for (int rd = 0; rd < 2; ++rd) {
-                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd), tp = ts + 32u * static_cast<uint32_t>(rd);
-                    // Does the row need the exact step after a sum against
-                    // the reference in hand (0 before there is one)?  first,
-                    // len: the keys summed.
+                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
                     auto sees_none = [&](int first, int len) {
                         return w.keys.x >= first + len || w.keys.y <= first || (kMode == kDecode && !w.live);
                     };
+                    // Does the row need the exact step after a sum against
+                    // the reference in hand (0 before there is one)?
                     auto judge = [&](float sum, bool none) -> bool {
                         if (none) return false;
                         if (m_run != -INFINITY) return !(sum <= kSumMax);
@@ -570,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         return false;
                     };
                     const int key0 = j * BN + 64 * rd;  // the round's first key
-                    bool done = false;
+                    int done = 0;  // of the round's two halves
                     if (linear && (!kCap || tier < 2) &&
                         (!edge || __all_sync(0xffffffffu, w.keys.x <= key0 && w.keys.y >= key0 + 64))) {
                         uint32_t pk[32];
@@ -579,21 +594,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // multiply-add: far distances lose nothing
                         const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(key0 - w.pos), -ref)
                                                               : b_tile - ref;
-                        float lt, et = 0.f, big = 0.f;
-                        if (!kCap)
-                            lt = common_round(std::integral_constant<int, 0>{}, tr, a, rd == 0, b0, step, pk, et, big);
-                        else if (tier == 0)
-                            lt = common_round(std::integral_constant<int, 1>{}, tr, a, rd == 0, b0, step, pk, et, big);
-                        else
-                            lt = common_round(std::integral_constant<int, 2>{}, tr, a, rd == 0, b0, step, pk, et, big);
-                        if (kCap && kMode == kDecode && !w.live) big = 0.f;
-                        if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : kTanhWide * kTanhWide))) {
-                            ++tier;  // out of the polynomial's range: taken again below
-                        } else if (!__any_sync(0xffffffffu, judge(lt, kMode == kDecode && !w.live))) {
-                            tmem_st32(tp, pk);
+                        Sum sum;
+                        float big = 0.f;
+                        // The weights in pk, if the round may keep them: col,
+                        // their column.
+                        auto keep = [&](uint32_t col) -> bool {
+                            if (kCap && kMode == kDecode && !w.live) big = 0.f;
+                            if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : kTanhWide * kTanhWide))) {
+                                ++tier;  // out of the polynomial's range: taken again below
+                                return false;
+                            }
+                            const bool first = m_run == -INFINITY;
+                            const float lt = sum.get();
+                            if (__any_sync(0xffffffffu, judge(lt, kMode == kDecode && !w.live))) {
+                                if (first) m_run = -INFINITY;
+                                return false;
+                            }
+                            tmem_st32(ts + col, pk);
                             l_run += lt;
-                            e_run += et;
-                            done = true;
+                            return true;
+                        };
+                        auto half_done = [&]() {
+                            if (!keep(weight_col<kMode>(0, 0) + 64u * static_cast<uint32_t>(rd))) return false;
+                            done = 1;
+                            sum = Sum();
+                            return true;
+                        };
+                        bool whole;
+                        if (!kCap)
+                            whole = common_round(std::integral_constant<int, 0>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                        else if (tier == 0)
+                            whole = common_round(std::integral_constant<int, 1>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                        else
+                            whole = common_round(std::integral_constant<int, 2>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                        if (whole) {
+                            if (keep(kMode == kForwardLse ? 64u * static_cast<uint32_t>(rd) + 32u : 32u * static_cast<uint32_t>(rd)))
+                                done = 2;
+                        } else {
+                            tmem_ld_wait(a);
+                            if (rd == 0) tmem_ld16(tr + 64, a);
                         }
                     } else {
                         tmem_ld_wait(a);
@@ -601,14 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // Every other round, 32 keys at a time.
 #pragma unroll 1
-                    for (int h = done ? 2 : 0; h < 2; ++h) {
+                    for (int h = done; h < 2; ++h) {
                         const int kh = key0 + 32 * h;
                         const bool none = sees_none(kh, 32);
-                        uint32_t pk[16];
-                        float lt = 0.f, et = 0.f, alpha = 1.f;
+                        const uint32_t tp = ts + weight_col<kMode>(0, 0) + (kMode == kForwardLse ? 64u : 32u) * rd;
+                        uint32_t pk[16], pl[16];
+                        float lt = 0.f, alpha = 1.f;
                         if (__all_sync(0xffffffffu, none)) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                            for (int c = 0; c < 16; ++c) pk[c] = pl[c] = 0u;
                         } else {
                             const bool all = __all_sync(0xffffffffu, w.keys.x <= kh && w.keys.y >= kh + 32);
                             bool need = false;
@@ -648,20 +688,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             m_run += up;
                                             alpha = ex2_approx(-up);
                                             l_run *= alpha;
-                                            e_run *= alpha;
                                         }
                                     }
                                     continue;
                                 }
-                                lt = weigh(y, pk, et);
+                                Sum sum;
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    pack_pair(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])), c,
+                                              pk[c], pl[c], sum);
+                                lt = sum.get();
                                 if (attempt == 2) break;
                                 need = judge(lt, none);
                                 if (!__any_sync(0xffffffffu, need)) break;
                             }
                         }
-                        tmem_st16(tp + 16u * static_cast<uint32_t>(h), pk);
+                        const uint32_t th = tp + (kMode == kForwardLse ? 32u : 16u) * static_cast<uint32_t>(h);
+                        tmem_st16(th, pk);
+                        if (kMode == kForwardLse) tmem_st16(th + 16, pl);
                         l_run += lt;
-                        e_run += et;
                         if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
                         // What was summed before moves with the reference: the
                         // round's first 32 weights, which wait to be multiplied
@@ -670,13 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // 0: wait for the last product it took.
                         if (h == 1) {
                             tmem_st_wait();
-                            tmem_ld16(tp, pk);
-                            tmem_ld_wait(pk);
+#pragma unroll 1
+                            for (uint32_t part = 0; part < (kMode == kForwardLse ? 32u : 16u); part += 16u) {
+                                tmem_ld16(tp + part, pk);
+                                tmem_ld_wait(pk);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
-                                                    __uint_as_float(pk[c] & 0xffff0000u) * alpha);
-                            tmem_st16(tp, pk);
+                                for (int c = 0; c < 16; ++c)
+                                    pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
+                                                        __uint_as_float(pk[c] & 0xffff0000u) * alpha);
+                                tmem_st16(tp + part, pk);
+                            }
                         }
                         if (rd == 1) {
                             ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
@@ -710,7 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
             sm.red_m[half][r] = m_run;
             sm.red_l[half][r] = l_run;
-            if (kMode == kForwardLse) sm.red_e[half][r] = e_run;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.ml_full);
             ++v;
@@ -749,7 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
             const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
             const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
-            const float ea = sm.red_e[0][r], eb = sm.red_e[1][r];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.ml_free);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
@@ -765,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kMode == kDecode)
                     p.part_ml[prow] = make_float2(L > 0.f ? M : -INFINITY, L);
                 else if (kMode == kForwardLse)
-                    p.lse[w.out] = L > 0.f ? fmaf(M, kLn2, logf(ea * wa + eb * wb)) : -INFINITY;
+                    p.lse[w.out] = L > 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
             }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
