@@ -373,8 +373,10 @@ mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, cons
  * mask row t sees the first len_b - T_q + 1 + t of them (and all of the
  * prefix).  form: cap, slopes, table; prefix_lens and doc_ids must be NULL.
  * T_p == 0 and T_k == 0 are allowed; a row without any key outputs 0.
- * Two launches (prefix and caches on the tensor cores, divided by key ranges
- * into partial sums; their merge), and one before them that expands the table.  workspace: >= sdpa_decode_shared_workspace_bytes()
+ * Two launches (the prefix and, with more than one query row per K/V head, the
+ * caches on the tensor cores, divided by key ranges into partial sums; their
+ * merge, with the caches of single rows), and one before them that expands the
+ * table.  workspace: >= sdpa_decode_shared_workspace_bytes()
  * bytes, 256-byte aligned; one per call in flight.
  */
 size_t sdpa_decode_shared_workspace_bytes(int B, int h, int h_kv, int T_q, int T_p, int T_k,

@@ -195,7 +195,8 @@ Splits decode_splits(int B, int h, int h_kv, int T_q, int T_p, int T_k) {
     const DecodeRows dr = decode_rows(h / h_kv * T_q);
     s.row_tiles = dr.chunks > 1 ? B * dr.chunks : (B + dr.nb - 1) / dr.nb;
     const long long np = static_cast<long long>(h_kv) * s.row_tiles, nc = static_cast<long long>(h_kv) * B * dr.chunks;
-    const int tp = (T_p + 127) / 128, tc = (T_k + 127) / 128;
+    const bool single = h / h_kv * T_q == 1;  // the caches are launch_decode_row's
+    const int tp = (T_p + 127) / 128, tc = single ? 0 : (T_k + 127) / 128;
     long long best = -1;
     for (int n = 2; n <= 32; ++n) {
         const int prefix = (tp + n - 1) / n, cache = (tc + n - 1) / n;
@@ -384,7 +385,7 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
     const Splits sp = decode_splits(B, h, h_kv, T_q, T_p, T_k);
     const long long items = static_cast<long long>(h_kv) * sp.row_tiles * sp.prefix +
                             static_cast<long long>(h_kv) * B * dr.chunks * sp.cache;
-    if (items >= (1ll << 30) || n_rows >= (1ull << 31)) return MHA_ERR_UNSUPPORTED;
+    if (items >= (1ll << 30) || n_rows >= (1ull << 28)) return MHA_ERR_UNSUPPORTED;
     const size_t at_o = f.vec_bytes(h), at_ml = at_o + round256(sp.parts() * n_rows * 256);
     const size_t need = at_ml + round256(sp.parts() * n_rows * 8);
     if (need > 0 && (!workspace || workspace_bytes < need)) return MHA_ERR_WORKSPACE;
@@ -425,6 +426,23 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
     if ((s = launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "shared prefix decoding launch")) !=
         MHA_OK)
         return s;
+    if (rows == 1) {
+        DecodeRowParams d{};
+        d.B = B;
+        d.H = h;
+        d.Tk = T_k;
+        d.capped = f.capped ? 1 : 0;
+        d.f = p.f;
+        d.cache_lens = cache_lens;
+        d.q = static_cast<const __nv_bfloat16 *>(q);
+        d.k = static_cast<const __nv_bfloat16 *>(k_cache);
+        d.v = static_cast<const __nv_bfloat16 *>(v_cache);
+        d.o = static_cast<__nv_bfloat16 *>(o);
+        d.prefix_splits = sp.prefix;
+        d.part_o = p.part_o;
+        d.part_ml = p.part_ml;
+        return launched(launch_decode_row(d, f.bias, stream), "shared prefix decoding, caches and merge");
+    }
     return launched(launch_decode_merge(p.part_o, p.part_ml, static_cast<__nv_bfloat16 *>(o), static_cast<int>(sp.parts()),
                                         static_cast<long long>(n_rows), stream),
                     "shared prefix decoding, merge");

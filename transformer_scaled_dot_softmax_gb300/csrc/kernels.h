@@ -230,6 +230,22 @@ constexpr int kSmsPerGpu = 152;  // for the choice of key ranges, which fixes th
 cudaError_t launch_decode_merge(const float *part_o, const float2 *part_ml, __nv_bfloat16 *o, int parts, long long rows,
                                 cudaStream_t stream);
 
+// With one query row per K/V head and batch entry (H K/V heads, Tq = 1) the
+// caches are gone through by this launch, which also merges the prefix's
+// partial sums.
+struct DecodeRowParams {
+    int B, H, Tk;
+    int capped;
+    ScoreParams f;
+    const int32_t *cache_lens;
+    const __nv_bfloat16 *q, *k, *v;  // (B, H, 1, 64), (B, H, Tk, 64) twice
+    __nv_bfloat16 *o;
+    int prefix_splits;               // partial sums of the prefix
+    const float *part_o;
+    const float2 *part_ml;
+};
+cudaError_t launch_decode_row(const DecodeRowParams &p, int bias, cudaStream_t stream);
+
 // ------------------------------------------------ positional encoding
 // out (rows, D) = x + PE(pos0 + row % T); D % 8 == 0; x and out may alias.
 cudaError_t launch_posenc_add_bf16(const __nv_bfloat16 *x, __nv_bfloat16 *out, long long rows, int T,

@@ -99,12 +99,16 @@ struct BiasRow {
     float past, future;  // vec of the distances past `far`
 };
 
+__device__ __forceinline__ const float *bias_vec(const ScoreParams &f, int h) {
+    return f.vec + static_cast<long long>(h) * (2 * f.mid + 1) + f.mid;
+}
+
 template <int kBias>
 __device__ __forceinline__ BiasRow bias_row(const ScoreParams &f, int h) {
     BiasRow r{0.f, nullptr, 0.f, 0.f};
     if (kBias == kBiasSlopes) r.slope2 = f.slopes[h] * kLog2E;
     if (kBias == kBiasBuckets) {
-        r.vec = f.vec + static_cast<long long>(h) * (2 * f.mid + 1) + f.mid;
+        r.vec = bias_vec(f, h);
         r.past = r.vec[-f.mid];
         r.future = r.vec[f.mid];
     }
