@@ -101,7 +101,7 @@ def test_workspace_sizes(lib):
     f = lambda *a: lib.lib.sdpa_scored_workspace_bytes(*a[:4], ctypes.addressof(a[4]) if a[4] else None)  # noqa: E731
     assert f(2, 3, 130, 7, None) == 0 and f(-1, 3, 1, 1, None) == 0
     t = form(lib, table=FAKE, starts=(0, 100))
-    assert f(2, 3, 130, 7, t) == r(3 * (2 * 164 + 1) * 4)
+    assert f(2, 3, 130, 7, t) == r(3 * (2 * 368 + 16) * 4)        # distances past 100 + 256 and padding
     assert f(2, 3, 7, 7, form(lib, docs=FAKE)) == r(2 * 7 * 8)
     assert f(2, 3, 7, 7, form(lib, table=FAKE, starts=(0, 0))) == 0
     b = lib.lib.sdpa_scored_backward_workspace_bytes
@@ -110,7 +110,7 @@ def test_workspace_sizes(lib):
     # three query heads on one K/V head, a CTA and fp32 sums of dk and dv each
     assert b(2, 3, 1, 130, 7, None) == plain + 2 * r(3 * 2 * 1 * 7 * 64 * 4)
     # the expanded bias and one sum per head, key block and bucket
-    assert b(2, 3, 3, 130, 7, ctypes.addressof(t)) == plain + r(3 * (2 * 164 + 1) * 4) + r(2 * 3 * 1 * 2 * 4)
+    assert b(2, 3, 3, 130, 7, ctypes.addressof(t)) == plain + r(3 * (2 * 368 + 16) * 4) + r(2 * 368 + 16) + r(2 * 3 * 1 * 2 * 4)
     d = lib.lib.sdpa_decode_shared_workspace_bytes
     assert d(4, 8, 2, 1, 0, 0, None) == 0 and d(4, 8, 3, 1, 10, 10, None) == 0
     assert d(4, 8, 2, 1, 100, 0, None) == 4 * 8 * 256 + r(4 * 8 * 8)     # one key range of the prefix

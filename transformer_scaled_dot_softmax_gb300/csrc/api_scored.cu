@@ -33,7 +33,7 @@ struct Form {
     BucketParams bk{};
     const int32_t *prefix_lens = nullptr, *doc_ids = nullptr;
     size_t vec_bytes(int h) const {
-        return bias == kBiasBuckets ? round256(static_cast<size_t>(h) * (2 * f.mid + 1) * 4) : 0;
+        return bias == kBiasBuckets ? round256(static_cast<size_t>(h) * vec_stride(f.mid) * 4) : 0;
     }
 };
 
@@ -53,7 +53,7 @@ bool form_sizes(const mha_score_form *form, Form &out) {
         }
         out.f.far = std::max(out.bk.starts[form->num_buckets - 1], 1);
         if (out.f.far > kMaxFar) return false;
-        out.f.mid = out.f.far + 64;
+        out.f.mid = vec_mid(out.f.far);
     }
     return true;
 }
@@ -146,7 +146,7 @@ mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h
 
 struct BwdLayout {
     Prep prep;
-    size_t dq, nlse2, dvec, buckets, part_dk, part_dv, end;
+    size_t dq, nlse2, dvec, idx, buckets, part_dk, part_dv, end;
     int splits, near_blocks;
 };
 BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int h_kv, int T_q, int T_k) {
@@ -158,7 +158,8 @@ BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int h_kv, int T_q, 
     l.dq = l.prep.end;
     l.nlse2 = l.dq + round256(rows * 256);
     l.dvec = l.nlse2 + round256(rows * 4);
-    l.buckets = l.dvec + round256(rows * 4);
+    l.idx = l.dvec + round256(rows * 4);
+    l.buckets = l.idx + (f.bias == kBiasBuckets ? round256(vec_stride(f.f.mid)) : 0);
     l.part_dk = l.buckets;
     l.splits = 1;
     if (f.bias == kBiasBuckets) {
@@ -332,14 +333,16 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
         if ((s = encode_heads_map(&tk, k_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
         if ((s = encode_heads_map(&tv, v_src, BHk, T_k > 0 ? T_k : 1)) != MHA_OK) return s;
         float *vec = f.bias == kBiasBuckets ? reinterpret_cast<float *>(ws + lay.prep.vec) : nullptr;
+        uint8_t *idx = vec ? ws + lay.idx : nullptr;
         int2 *docs = f.doc_ids ? reinterpret_cast<int2 *>(ws + lay.prep.docs) : nullptr;
         float *nlse2 = reinterpret_cast<float *>(ws + lay.nlse2), *dvec = reinterpret_cast<float *>(ws + lay.dvec);
         p.f.vec = vec;
+        p.f.idx = idx;
         p.vis.doc_range = docs;
         p.nlse2 = nlse2;
         p.dvec = dvec;
         if ((s = launched(launch_scored_bwd_pre(static_cast<const __nv_bfloat16 *>(o), static_cast<const __nv_bfloat16 *>(o_lo),
-                                                static_cast<const __nv_bfloat16 *>(dout), lse, nlse2, dvec, p, vec, docs,
+                                                static_cast<const __nv_bfloat16 *>(dout), lse, nlse2, dvec, p, vec, idx, docs,
                                                 f.doc_ids, stream),
                           "scored attention backward, row terms")) != MHA_OK)
             return s;

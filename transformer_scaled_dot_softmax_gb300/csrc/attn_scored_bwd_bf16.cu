@@ -18,14 +18,22 @@
 //   * a key is seen by one interval of queries [lo, hi) (causal, prefix,
 //     documents and padding all end in one), which bounds the query blocks
 //     walked and masks the ones seen in part;
-//   * a bucket bias sums dS over the buckets of its distances.  A block pair
-//     past the last bucket's first distance adds up in one register per
+//   * a bucket bias is read from a window of 256 distances that comes with the
+//     query block, for block pairs nearer than the last bucket's first
+//     distance; past it, it is one value;
+//   * the bias's gradient sums dS over the buckets of its distances.  A block
+//     pair past the last bucket's first distance adds up in one register per
 //     thread; in a nearer one each warp adds its 32 x 32 pairs along their
-//     diagonals (a shuffle and an add per pair), then each warp adds the
-//     diagonals of the buckets it owns.  A CTA leaves one sum per head and
-//     bucket, and the last launch adds those, all in a fixed order: dtable
-//     does not depend on the order in which CTAs finish.
+//     diagonals (a shuffle and an add per pair), then the diagonals of each
+//     bucket (a segmented scan over the lanes), into sums of its own in shared
+//     memory.  A CTA adds the warps' sums once per head and leaves one per
+//     bucket, and the last launch adds those, all in a fixed order: dtable does
+//     not depend on the order in which CTAs finish.  (Adding over the warps in
+//     every near pair instead cost 4,300 cycles of its 3,900; a warp set apart
+//     for it fell behind.)
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "scores.cuh"
@@ -39,10 +47,19 @@ constexpr int BQ = 128;
 constexpr int BKB = 128;
 constexpr uint32_t kTile = BQ * HD * 2;
 constexpr uint32_t kColS = 0, kColDP = 128, kColP = 256, kColDV = 320, kColDK = 384, kColDQ = 448;
-constexpr int kThreads = 576;
 constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (2 + kSoftmaxWarps);
 constexpr int kStages = 3;
 
+// What only a bucket bias needs.
+struct SmemBuckets {
+    float bias[kStages][2 * BQ];                    // near block pairs: window of the expanded bias
+    uint8_t idx[kStages][2 * BQ];                   // and of its buckets
+    float sums[2][kSoftmaxWarps][2 * kMaxBuckets];  // a warp's sums of one head
+};
+struct SmemNone {};
+
+template <int kBias>
 struct __align__(1024) Smem {
     uint8_t k[kTile];
     uint8_t v[kTile];
@@ -51,14 +68,13 @@ struct __align__(1024) Smem {
     uint8_t ds[2][2 * kTile];
     float nlse2[kStages][BQ];
     float dvec[kStages][BQ];
-    float diag[2][kSoftmaxWarps][64];  // a warp's 32 x 32 pairs by distance
-    float far[2][kSoftmaxWarps][2];    // a warp's far sums of one query head (past, future)
+    std::conditional_t<kBias == kBiasBuckets, SmemBuckets, SmemNone> bk;
     uint64_t kv_full;
     uint64_t stage_full[kStages];
     uint64_t q_empty[kStages];
     uint64_t g_empty[kStages];
     uint64_t sdp_full, sdp_read, pds_full, tmem_free, p_free, dq_full, dq_free, acc_done, drain;
-    uint64_t diag_full;  // a near block's (or a head's far) sums are in shared memory (16 warps)
+    uint64_t buckets_full;  // a head's sums are complete (16 warps)
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -76,26 +92,69 @@ __device__ __forceinline__ int2 key_queries(const ScoredBwdParams &p, int b, int
     return make_int2(lo, hi);
 }
 
-// Weights P^T and dZ^T of 16 query columns for the thread's key, as bf16
-// pairs, from S^T and dP^T; returns dS^T (fp32) in dp.  kMasked: columns
-// outside [lo, hi) count nothing, whatever S and dP hold there.
+// Weights P^T and dZ^T of 16 query columns for the thread's key, as bf16 pairs,
+// from S^T and dP^T; leaves dS^T (fp32) in dp.  d0: the key's distance from the
+// first query; window: the bucket bias of column e at window[-e], null past the
+// last bucket's first distance.
+// kMasked: only the columns of `bits` count.
 template <bool kCap, int kBias, bool kMasked>
 __device__ __forceinline__ void score_terms(uint32_t (&sv)[16], uint32_t (&dp)[16], const float *nlse2,
                                             const float *dvec, const ScoreParams &f, const BiasRow &br, int d0,
-                                            int lo, int hi, uint32_t (&pk)[8], uint32_t (&dsk)[8]) {
-    uint32_t u[kCap ? 16 : 1];
+                                            const float *window, unsigned bits, uint32_t (&pk)[8],
+                                            uint32_t (&dsk)[8]) {
+    auto seen = [&](int e) { return !kMasked || (bits >> e & 1u); };
+    auto at = [](const uint32_t(&x)[16], int e) { return f32x2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])); };
     if (kCap) {
+        // sv := mul tanh(s cap_in); masked scores have no say in how
         if (kMasked) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (e < lo || e >= hi) sv[e] = 0u;
+                if (!seen(e)) sv[e] = 0u;
         }
-        cap_scores(sv, f.cap_in, 1.f, __all_sync(0xffffffffu, max_abs(sv) * fabsf(f.cap_in) <= kTanhWide));
+        const float big = max_abs(sv);
+        if (__all_sync(0xffffffffu, big * big <= f.near_max)) {
+            const uint64_t n0 = f32x2_set(f.near[0]), n1 = f32x2_set(f.near[1]), n2 = f32x2_set(f.near[2]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) u[kCap ? e : 0] = sv[e];
+            for (int e = 0; e < 16; e += 2) {
+                const uint64_t s2 = at(sv, e), sq = mul_f32x2(s2, s2);
+                float a, b;
+                f32x2_unpack(mul_f32x2(s2, fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0)), a, b);
+                sv[e] = __float_as_uint(a);
+                sv[e + 1] = __float_as_uint(b);
+            }
+        } else {
+            cap_scores(sv, f.cap_in, f.mul, __all_sync(0xffffffffu, big * fabsf(f.cap_in) <= kTanhWide));
+        }
     }
-    if (kBias != kBiasNone) add_bias<kBias, -1, false>(sv, f, br, d0, 0.f);
+    // mul tanh, before the bias comes to it
+    uint32_t yt[kCap && kBias != kBiasNone ? 16 : 1];
+    if (kCap && kBias != kBiasNone) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) yt[kBias != kBiasNone && kCap ? e : 0] = sv[e];
+    }
     const uint64_t mul2 = f32x2_set(f.mul), one2 = f32x2_set(1.f);
+    const uint64_t inv2 = f32x2_set(kCap ? -1.f / (f.mul * f.mul) : 0.f);
+    if (kBias == kBiasBuckets && window) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            const uint64_t w2 = f32x2_pack(window[-e], window[-e - 1]);
+            float a, b;
+            f32x2_unpack(kCap ? add_f32x2(at(sv, e), w2) : fma_f32x2(at(sv, e), mul2, w2), a, b);
+            sv[e] = __float_as_uint(a);
+            sv[e + 1] = __float_as_uint(b);
+        }
+    } else if (kBias == kBiasBuckets) {
+        const uint64_t w2 = f32x2_set(d0 < 0 ? br.past : br.future);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            float a, b;
+            f32x2_unpack(kCap ? add_f32x2(at(sv, e), w2) : fma_f32x2(at(sv, e), mul2, w2), a, b);
+            sv[e] = __float_as_uint(a);
+            sv[e + 1] = __float_as_uint(b);
+        }
+    } else if (kBias == kBiasSlopes) {
+        add_bias<kBiasSlopes, -1, kCap>(sv, f, br, d0, 0.f);
+    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         const float4 l4 = reinterpret_cast<const float4 *>(nlse2)[g];
@@ -103,34 +162,27 @@ __device__ __forceinline__ void score_terms(uint32_t (&sv)[16], uint32_t (&dp)[1
         const uint64_t nl[2] = {f32x2_pack(l4.x, l4.y), f32x2_pack(l4.z, l4.w)};
         const uint64_t d[2] = {f32x2_pack(d4.x, d4.y), f32x2_pack(d4.z, d4.w)};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int e = 4 * g + 2 * h;
-            const uint64_t s2 = f32x2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+        for (int i = 0; i < 2; ++i) {
+            const int e = 4 * g + 2 * i;
             float x0, x1;
-            f32x2_unpack(kBias == kBiasNone ? fma_f32x2(s2, mul2, nl[h]) : add_f32x2(s2, nl[h]), x0, x1);
+            f32x2_unpack(kCap || kBias != kBiasNone ? add_f32x2(at(sv, e), nl[i]) : fma_f32x2(at(sv, e), mul2, nl[i]), x0, x1);
             float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if (kMasked) {
-                if (e < lo || e >= hi) p0 = 0.f;
-                if (e + 1 < lo || e + 1 >= hi) p1 = 0.f;
-            }
-            const uint64_t dd = mul_f32x2(
-                f32x2_pack(p0, p1),
-                sub_f32x2(f32x2_pack(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d[h]));
+            if (!seen(e)) p0 = 0.f;
+            if (!seen(e + 1)) p1 = 0.f;
             float ds0, ds1;
-            f32x2_unpack(dd, ds0, ds1);
-            if (kMasked) {
-                if (e < lo || e >= hi) ds0 = 0.f;
-                if (e + 1 < lo || e + 1 >= hi) ds1 = 0.f;
-            }
+            f32x2_unpack(mul_f32x2(f32x2_pack(p0, p1), sub_f32x2(at(dp, e), d[i])), ds0, ds1);
             dp[e] = __float_as_uint(ds0);
             dp[e + 1] = __float_as_uint(ds1);
             if (kCap) {
-                const uint64_t t2 = f32x2_pack(__uint_as_float(u[kCap ? e : 0]), __uint_as_float(u[kCap ? e + 1 : 0]));
-                const uint64_t nt = f32x2_pack(-__uint_as_float(u[kCap ? e : 0]), -__uint_as_float(u[kCap ? e + 1 : 0]));
-                f32x2_unpack(mul_f32x2(f32x2_pack(ds0, ds1), fma_f32x2(t2, nt, one2)), ds0, ds1);
+                // 1 - t^2, t = sv / mul
+                const uint64_t t2 = kBias == kBiasNone
+                                        ? at(sv, e)
+                                        : f32x2_pack(__uint_as_float(yt[kBias != kBiasNone && kCap ? e : 0]),
+                                                     __uint_as_float(yt[kBias != kBiasNone && kCap ? e + 1 : 0]));
+                f32x2_unpack(mul_f32x2(f32x2_pack(ds0, ds1), fma_f32x2(mul_f32x2(t2, inv2), t2, one2)), ds0, ds1);
             }
-            pk[2 * g + h] = pack_bf16x2(p0, p1);
-            dsk[2 * g + h] = pack_bf16x2(ds0, ds1);
+            pk[2 * g + i] = pack_bf16x2(p0, p1);
+            dsk[2 * g + i] = pack_bf16x2(ds0, ds1);
         }
     }
 }
@@ -141,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_g,
                            const __grid_constant__ ScoredBwdParams p) {
     extern __shared__ uint8_t smem_raw[];
-    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+    Smem<kBias> &sm = *reinterpret_cast<Smem<kBias> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -171,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.dq_free, kSoftmaxWarps);
         mbar_init(&sm.acc_done, 1);
         mbar_init(&sm.drain, 1);
-        mbar_init(&sm.diag_full, kSoftmaxWarps);
+        mbar_init(&sm.buckets_full, kSoftmaxWarps);
         sm.abort_flag = 0;
         fence_barrier_init();
     }
@@ -184,6 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
         prefetch_tensormap(&tmap_g);
+    }
+    if constexpr (kBias == kBiasBuckets) {
+        for (int i = threadIdx.x; i < 2 * kSoftmaxWarps * 2 * kMaxBuckets; i += kThreads) (&sm.bk.sums[0][0][0])[i] = 0.f;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -215,17 +270,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(&tmap_v, &sm.kv_full, sm.v, 0, k0, bkv);
             }
             int issued = 0, j = j_begin, bh = b * p.H + h0;
+            const float *vec = kBias == kBiasBuckets ? bias_vec(p.f, h0) : nullptr;
             for (int t = 0; t < n_t; ++t) {
                 const int st = t % kStages, use = t / kStages;
                 if (t >= kStages && !mbar_wait(&sm.q_empty[st], (use - 1) & 1, ab)) break;
                 const long long vrow = static_cast<long long>(bh) * p.Tq_pad + j * BQ;
-                mbar_arrive_expect_tx(&sm.stage_full[st], 2 * kTile + 2 * BQ * 4);
+                const bool window = kBias == kBiasBuckets && abs(kb - j) <= p.near_blocks;
+                mbar_arrive_expect_tx(&sm.stage_full[st], 2 * kTile + 2 * BQ * 4 + (window ? 2 * BQ * 5 : 0));
                 const bool j_ok =
                     in_bounds(j * BQ < p.Tq && j * BQ + BQ <= p.Tq_pad && bh < p.B * p.H, p.status);
                 if (j_ok) {
                     tma_load_3d(&tmap_q, &sm.stage_full[st], sm.q[st], 0, j * BQ, bh);
                     bulk_load_1d(sm.nlse2[st], p.nlse2 + vrow, BQ * 4, &sm.stage_full[st]);
                     bulk_load_1d(sm.dvec[st], p.dvec + vrow, BQ * 4, &sm.stage_full[st]);
+                    if constexpr (kBias == kBiasBuckets) {
+                        if (window) {
+                            const int d = BKB * (kb - j - 1);  // first distance
+                            bulk_load_1d(sm.bk.bias[st], vec + d, 2 * BQ * 4, &sm.stage_full[st]);
+                            bulk_load_1d(sm.bk.idx[st], p.f.idx + p.f.mid + d, 2 * BQ, &sm.stage_full[st]);
+                        }
+                    }
                 }
                 issued = t + 1;
                 if (t >= kStages && !mbar_wait(&sm.g_empty[st], (use - 1) & 1, ab)) break;
@@ -233,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++j == j_begin + n_j) {
                     j = j_begin;
                     ++bh;
+                    if (kBias == kBiasBuckets) vec += vec_stride(p.f.mid);
                 }
             }
             mbar_wait_drain(&sm.kv_full, 0);
@@ -270,11 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     warp_mma_bf16_ss(tmem + kColDP, v_km + 2 * kk, g_km + so + 2 * kk, id_s, kk > 0 ? 1u : 0u);
             };
             bool ok = warp_wait(&sm.kv_full, 0, ab);
-            // Padded keys: their dS is 0, and dQ's 0 times whatever the
-            // buffer holds has to be 0 (rows past Tk the copy zeroed).
+            // Padded keys: their weight is 0, and 0 times whatever the buffer
+            // holds there has to be 0 (rows past Tk the copy zeroed).
             if (ok && k0 + BKB > kv_len && kv_len < p.Tk) {
-                uint4 *dst = reinterpret_cast<uint4 *>(sm.k);
-                for (int x = (kv_len - k0) * 8 + lane; x < BKB * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                uint4 *dk = reinterpret_cast<uint4 *>(sm.k), *dv = reinterpret_cast<uint4 *>(sm.v);
+                for (int x = (kv_len - k0) * 8 + lane; x < BKB * 8; x += 32) dk[x] = dv[x] = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
@@ -353,80 +418,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                            __uint_as_float(a[4 * x + 2]), __uint_as_float(a[4 * x + 3]));
             return true;
         };
-        // Bucket bias gradient.  `gen` counts this CTA's exchanges through
-        // shared memory (one per near block, one per head for the far sums).
-        // Warp wi owns the buckets wi, wi + 16, ...; lane i holds the sum of
-        // the i-th of them.
+        // Bucket bias gradient.  `gen`: heads finished; a head's sums go to one
+        // half of sm.buckets, the next one's to the other.
         const bool want_bias = kBias == kBiasBuckets && p.bucket_part != nullptr;
         const int n_buckets = p.bk.num * (p.bk.both ? 2 : 1);
         int gen = 0;
-        float diag_hi = 0.f, diag_lo = 0.f, far_past = 0.f, far_future = 0.f, mine = 0.f;
-        auto exchange = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.diag_full);
-            const bool got = __all_sync(0xffffffffu, mbar_wait(&sm.diag_full, gen & 1, ab));
-            ++gen;
-            return got;
-        };
-        auto warp_sum = [](float x) {
+        float diag_hi = 0.f, diag_lo = 0.f, far_past = 0.f, far_future = 0.f;
+        // x of the lane's distance, which is in bucket u, added over the lanes of
+        // the bucket (they are neighbours: distances rise with the lane) to the
+        // warp's sums.
+        auto put_diagonals = [&](float x, int u) {
+            if constexpr (kBias == kBiasBuckets) {
+                const int before = __shfl_up_sync(0xffffffffu, u, 1);
+                const unsigned heads = __ballot_sync(0xffffffffu, lane == 0 || before != u);
+                const int back = lane - (31 - __clz(heads & (0xffffffffu >> (31 - lane))));  // lanes since its first
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            return x;
-        };
-        auto put_near = [&](int j) -> bool {
-            const int buf = gen & 1;
-            sm.diag[buf][wi][lane + 32] = diag_hi;  // distance `lane` within the warp's 32 x 32
-            sm.diag[buf][wi][lane] = diag_lo;       // distance lane - 32
-            diag_hi = diag_lo = 0.f;
-            if (!exchange()) return false;
-            const int mid = BKB * (kb - j);  // distance of the block pair's main diagonal
-            for (int i = 0, u = wi; u < n_buckets; ++i, u += kSoftmaxWarps) {
-                // the bucket's distances [d0, d1], as bucket_of() has them
-                const int x = u < p.bk.num ? u : u - p.bk.num;
-                const int near = p.bk.starts[x], far = x + 1 < p.bk.num ? p.bk.starts[x + 1] - 1 : 1 << 30;
-                int d0 = u < p.bk.num ? -far : max(near, 1);
-                int d1 = u < p.bk.num ? (u == 0 && !p.bk.both ? 1 << 30 : -near) : far;
-                d0 = max(d0, mid - (BQ - 1));
-                d1 = min(d1, mid + BKB - 1);
-                if (d0 > d1) continue;
-                float sum = 0.f;
-                for (int d = d0 + lane; d <= d1; d += 32) {
-                    // the warps' blocks that hold distance d: quadrant q, chunk
-                    // q - k or q - k - 1 for k = floor((d - mid) / 32)
-                    const int k = (d - mid) >> 5, loc = (d - mid) - 32 * k;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        // warp index of (quadrant q, chunk c): 4 c + (q + 2) % 4
-                        const int c0 = q - k, c1 = c0 - 1;
-                        if (c0 >= 0 && c0 < 4) sum += sm.diag[buf][4 * c0 + ((q + 2) & 3)][loc + 32];
-                        if (c1 >= 0 && c1 < 4) sum += sm.diag[buf][4 * c1 + ((q + 2) & 3)][loc];
-                    }
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (back >= o) x += y;
                 }
-                sum = warp_sum(sum);
-                if (lane == i) mine += sum;
+                if (lane == 31 || (heads >> (lane + 1) & 1u)) sm.bk.sums[gen & 1][wi][u] += x;
+                __syncwarp();
             }
-            return true;
+        };
+        auto put_near = [&](int st) {
+            if constexpr (kBias == kBiasBuckets) {
+                // the warp's 32 x 32 pairs: distances -31 .. 31 around its own diagonal
+                const uint8_t *u = sm.bk.idx[st] + BKB + static_cast<int>(lane_base) - 32 * c + lane;
+                put_diagonals(diag_hi, u[0]);
+                put_diagonals(diag_lo, u[-32]);
+                diag_hi = diag_lo = 0.f;
+            }
         };
         auto finish_head = [&](int head) -> bool {
-            const int buf = gen & 1;
-            far_past = warp_sum(far_past);
-            far_future = warp_sum(far_future);
-            if (lane == 0) {
-                sm.far[buf][wi][0] = far_past;
-                sm.far[buf][wi][1] = far_future;
+            if constexpr (kBias == kBiasBuckets) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    far_past += __shfl_xor_sync(0xffffffffu, far_past, o);
+                    far_future += __shfl_xor_sync(0xffffffffu, far_future, o);
+                }
+                float(&mine)[kSoftmaxWarps][2 * kMaxBuckets] = sm.bk.sums[gen & 1];
+                if (lane == 0) {
+                    // far past: the last bucket; far future: the last of the other
+                    // direction, or, with one direction, bucket 0
+                    mine[wi][p.bk.num - 1] += far_past;
+                    mine[wi][p.bk.both ? 2 * p.bk.num - 1 : 0] += far_future;
+                }
+                far_past = far_future = 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.buckets_full);
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm.buckets_full, gen & 1, ab))) return false;
+                const int u = wi * 32 + lane;
+                if (u < n_buckets) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kSoftmaxWarps; ++w) {
+                        sum += mine[w][u];
+                        mine[w][u] = 0.f;
+                    }
+                    p.bucket_part[((static_cast<long long>(b) * p.H + head) * gridDim.y + kb) * n_buckets + u] = sum;
+                }
+                ++gen;
             }
-            far_past = far_future = 0.f;
-            if (!exchange()) return false;
-            const int u = wi + kSoftmaxWarps * lane;
-            if (u < n_buckets) {
-                // far past: the last bucket; far future: the last of the
-                // other direction, or, with one direction, bucket 0
-                const bool past = u == p.bk.num - 1, future = u == (p.bk.both ? 2 * p.bk.num - 1 : 0);
-                for (int w = 0; past && w < kSoftmaxWarps; ++w) mine += sm.far[buf][w][0];
-                for (int w = 0; future && w < kSoftmaxWarps; ++w) mine += sm.far[buf][w][1];
-                p.bucket_part[((static_cast<long long>(b) * p.H + head) * gridDim.y + kb) * n_buckets + u] = mine;
-            }
-            mine = 0.f;
             return true;
         };
 
@@ -440,7 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  __all_sync(0xffffffffu, mbar_wait(&sm.stage_full[st], (t / kStages) & 1, ab));
             if (!ok) break;
             tc_fence_after_sync();
-            const bool near = want_bias && abs(kb - j) <= p.near_blocks;
+            const bool near = kBias == kBiasBuckets && abs(kb - j) <= p.near_blocks;
+            const float *window = nullptr;
+            if constexpr (kBias == kBiasBuckets)
+                if (near) window = sm.bk.bias[st] + (r - 32 * c + BKB);
             uint8_t *blk = sm.ds[t & 1] + (c >> 1) * kTile + r * 128;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -448,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t sv[16], dp[16];
                 tmem_ld16(tl + kColS + col, sv);
                 tmem_ld16(tl + kColDP + col, dp);
-                const int lo = qs.x - (q0 + 16 * h), hi = qs.y - (q0 + 16 * h);  // columns that see the key
+                const int lo = qs.x - (q0 + 16 * h), hi = qs.y - (q0 + 16 * h);
                 tmem_ld_wait(sv);
                 tmem_ld_wait(dp);
                 if (h == 1) {
@@ -459,10 +515,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t pk[8], dsk[8];
                 const float *l2 = sm.nlse2[st] + 32 * c + 16 * h, *dv = sm.dvec[st] + 32 * c + 16 * h;
                 const int d0 = key - (q0 + 16 * h);
-                if (__all_sync(0xffffffffu, lo <= 0 && hi >= 16))
-                    score_terms<kCap, kBias, false>(sv, dp, l2, dv, p.f, br, d0, 0, 16, pk, dsk);
-                else
-                    score_terms<kCap, kBias, true>(sv, dp, l2, dv, p.f, br, d0, lo, hi, pk, dsk);
+                const float *win = window ? window - 16 * h : nullptr;
+                // columns that see the key
+                const unsigned bits = (hi <= 0 ? 0u : 0xffffu >> (16 - min(hi, 16))) & (0xffffu << min(max(lo, 0), 16));
+                if (__all_sync(0xffffffffu, bits == 0xffffu)) {
+                    score_terms<kCap, kBias, false>(sv, dp, l2, dv, p.f, br, d0, win, bits, pk, dsk);
+                } else if (kBias == kBiasBuckets || __any_sync(0xffffffffu, bits != 0)) {
+                    score_terms<kCap, kBias, true>(sv, dp, l2, dv, p.f, br, d0, win, bits, pk, dsk);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pk[e] = dsk[e] = 0u;
+                }
                 if (h == 0 && t >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (t - 1) & 1, ab))))
                     break;
                 tmem_st8(tl + kColP + 16u * c + 8u * h, pk);
@@ -508,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.pds_full);
             if (t >= 1 && !(ok = add_dq(t - 1, bh_prev, j_prev))) break;
-            if (near && !(ok = put_near(j))) break;
+            if (want_bias && near) put_near(st);
             j_prev = j;
             bh_prev = b * p.H + head;
             if (++j == j_begin + n_j) {
@@ -570,7 +633,7 @@ template <bool kCap, int kBias>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tg,
                    const ScoredBwdParams &p, cudaStream_t stream) {
     auto kernel = attn_scored_bwd_kernel<kCap, kBias>;
-    const size_t smem = sizeof(Smem) + 1024;
+    const size_t smem = sizeof(Smem<kBias>) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     dim3 grid(static_cast<unsigned>(p.B * p.Hkv * p.splits), static_cast<unsigned>((p.Tk + BKB - 1) / BKB));

@@ -127,8 +127,10 @@ struct ScoreParams {
     float near[3], near_max;
     float masked;         // the u of a masked score: minus infinity times the sign of mul
     const float *slopes;  // (H) fp32, kBiasSlopes
-    const float *vec;     // (H, 2 mid + 1) fp32 in log2 units, kBiasBuckets; written by scored_prep
-    int far, mid;         // distances from `far` on share the last bucket; mid = far + 64
+    // kBiasBuckets, written by the preparing launch for distances -mid .. mid:
+    const float *vec;     // (H, vec_stride(mid)) the bias, in log2 units
+    const uint8_t *idx;   // (vec_stride(mid)) the bucket (backward only)
+    int far, mid;         // distances from `far` on share the last bucket; mid = vec_mid(far)
     int past_only;        // no visible key lies past its query (causal mask without prefixes)
 };
 // Which keys a query sees.
@@ -138,6 +140,12 @@ struct VisParams {
     const int32_t *prefix_lens;  // (B) or null: keys every query sees in spite of the causal mask
     const int2 *doc_range;       // (B, T) or null: first position of a position's document, and past its last
 };
+
+// The expanded bias of a head: distances -mid .. mid and padding, so that the
+// 256 distances of a 128 x 128 block pair with one below `far`, from a multiple
+// of 128 on, are inside and 16-byte aligned.
+inline __host__ __device__ int vec_mid(int far) { return (far + 256 + 15) / 16 * 16; }
+inline __host__ __device__ int vec_stride(int mid) { return 2 * mid + 16; }
 
 constexpr int kMaxBuckets = 64;  // per direction
 struct BucketParams {
@@ -217,7 +225,7 @@ struct ScoredBwdParams {
 // and dtable (not null) from the partial sums.
 cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
                                   const float *lse, float *nlse2, float *dvec, const ScoredBwdParams &p, float *vec,
-                                  int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream);
+                                  uint8_t *idx, int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream);
 cudaError_t launch_scored_bwd_post(const ScoredBwdParams &p, __nv_bfloat16 *dq, __nv_bfloat16 *dtable,
                                    cudaStream_t stream);
 cudaError_t launch_attn_scored_bwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,

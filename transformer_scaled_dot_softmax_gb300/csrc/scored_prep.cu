@@ -25,13 +25,14 @@ __device__ __forceinline__ int bucket_of(const BucketParams &bk, int d) {
 }
 
 struct PrepParams {
-    float *vec;  // (H, 2 mid + 1), or null
+    float *vec;    // (H, vec_stride(mid)), or null
+    uint8_t *idx;  // (vec_stride(mid)), or null
     int mid, H;
     BucketParams bk;
     int2 *doc_range;  // (B, T), or null
     const int32_t *doc_ids;
     int B, T;
-    long long vec_entries() const { return vec ? static_cast<long long>(H) * (2 * mid + 1) : 0; }
+    long long vec_entries() const { return vec ? static_cast<long long>(H) * vec_stride(mid) : 0; }
     long long entries() const { return vec_entries() + (doc_range ? static_cast<long long>(B) * T : 0); }
 };
 
@@ -40,10 +41,12 @@ struct PrepParams {
 // ids do not decrease).  Latency-bound: log2 T dependent loads.
 __device__ __forceinline__ void prep_entry(const PrepParams &p, long long n_vec, long long i) {
     if (i < n_vec) {
-        const int len = 2 * p.mid + 1;
+        const int len = vec_stride(p.mid);
         const int h = static_cast<int>(i / len);
         const int d = static_cast<int>(i - static_cast<long long>(h) * len) - p.mid;
-        p.vec[i] = __bfloat162float(p.bk.table[bucket_of(p.bk, d) * p.H + h]) * kLog2E;
+        const int u = bucket_of(p.bk, d);
+        p.vec[i] = __bfloat162float(p.bk.table[u * p.H + h]) * kLog2E;
+        if (p.idx && h == 0) p.idx[i] = static_cast<uint8_t>(u);
         return;
     }
     const long long x = i - n_vec;
@@ -149,7 +152,7 @@ unsigned blocks_of(long long threads) { return static_cast<unsigned>((threads + 
 
 cudaError_t launch_scored_prep(float *vec, int far, int H, const BucketParams &bk, int2 *doc_range,
                                const int32_t *doc_ids, int B, int T, cudaStream_t stream) {
-    const PrepParams p{vec, far + 64, H, bk, doc_range, doc_ids, B, T};
+    const PrepParams p{vec, nullptr, vec_mid(far), H, bk, doc_range, doc_ids, B, T};
     if (p.entries() == 0) return cudaSuccess;
     scored_prep<<<blocks_of(p.entries()), kThreads, 0, stream>>>(p, p.vec_entries());
     return cudaGetLastError();
@@ -157,9 +160,9 @@ cudaError_t launch_scored_prep(float *vec, int far, int H, const BucketParams &b
 
 cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
                                   const float *lse, float *nlse2, float *dvec, const ScoredBwdParams &p, float *vec,
-                                  int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream) {
+                                  uint8_t *idx, int2 *doc_range, const int32_t *doc_ids, cudaStream_t stream) {
     const long long BH = static_cast<long long>(p.B) * p.H;
-    const PrepParams pp{vec, p.f.mid, p.H, p.bk, doc_range, doc_ids, p.B, p.Tk};
+    const PrepParams pp{vec, idx, p.f.mid, p.H, p.bk, doc_range, doc_ids, p.B, p.Tk};
     const unsigned rows = blocks_of(BH * p.Tq_pad * 8), prep = blocks_of(pp.entries());
     if (rows + prep == 0) return cudaSuccess;
     scored_bwd_pre<<<rows + prep, kThreads, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows,

@@ -7,9 +7,9 @@
 //
 // Scores are kept in log2 units (y = s log2 e) because the weights are taken
 // with 2^x.  The bucket bias is read from an expanded per-head row
-// vec[d], d in [-mid, mid], mid = far + 64, that a preparing launch writes
+// vec[d], d in [-mid, mid], mid >= far + 256, that a preparing launch writes
 // once per call (already times log2 e): from |d| >= far on all distances
-// share one bucket, so a run of 64 keys that lies wholly past `far` needs one
+// share one bucket, so a run of keys that lies wholly past `far` needs one
 // value, and any other run is read at d clamped per run, not per key.
 #pragma once
 
@@ -100,7 +100,7 @@ struct BiasRow {
 };
 
 __device__ __forceinline__ const float *bias_vec(const ScoreParams &f, int h) {
-    return f.vec + static_cast<long long>(h) * (2 * f.mid + 1) + f.mid;
+    return f.vec + static_cast<long long>(h) * vec_stride(f.mid) + f.mid;
 }
 
 template <int kBias>
