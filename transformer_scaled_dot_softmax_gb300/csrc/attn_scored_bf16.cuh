@@ -75,6 +75,7 @@ constexpr uint32_t kOCol = 384;
 // costs no precision, and 2^64 times any length stays far from overflow.
 constexpr float kSumMin = 5.421010862427522e-20f, kSumMax = 1.8446744073709552e19f;
 constexpr int kItemTable = 128;
+constexpr int kSorted = kThreads;
 
 // What the kernel computes.
 enum Mode { kForward, kForwardLse, kDecode };
@@ -104,6 +105,7 @@ struct __align__(1024) Smem {
     uint64_t pv0[2][2];      // [group][group tile mod 2]: round-0 product complete
     uint64_t ml_full, ml_free, o_final, o_free;
     uint64_t drain[3];
+    uint16_t len[kSorted], order[kSorted];
     Item item_tab[kItemTable];
     Item item_own[kThreads / 32];
     int n_items;
@@ -140,8 +142,12 @@ __device__ __forceinline__ constexpr uint32_t weight_col(int rd, int kk) {
     return kMode == kForwardLse ? 64u * rd + 32u * (kk >> 1) + 8u * (kk & 1) : 32u * rd + 8u * kk;
 }
 
+// Blocks of query rows are dealt to the CTAs longest first.  Under a causal
+// mask alone that is from the last block down; where lengths or documents make
+// it another order, up to kSorted blocks (of all batch entries, one head) are
+// ranked in the prologue, by every CTA alike.  `order`: null, or the ranking.
 template <int kMode>
-__device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k) {
+__device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k, const uint16_t *order) {
     Item it;
     if (kMode == kDecode) {
         const DecodeRows dr = decode_rows(p.H / p.Hkv * p.Tq);
@@ -172,12 +178,13 @@ __device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k) {
         it.jd = it.j0 + it.n_kv - 1;
         return it;
     }
-    const int BH = p.B * p.H;
-    const int qb = p.num_qblocks - 1 - k / BH;
-    const int bh = k - (k / BH) * BH;
-    it.b = bh / p.H;
-    it.hh = bh - it.b * p.H;
-    it.q0 = qb * BM;
+    // (block, head) pairs, blocks numbered from the last down, all batch
+    // entries' last blocks first
+    int blk = k / p.H;
+    it.hh = k - blk * p.H;
+    if (order) blk = order[blk];
+    it.b = blk % p.B;
+    it.q0 = (p.num_qblocks - 1 - blk / p.B) * BM;
     it.split = 0;
     it.kv_len = p.vis.key_lens ? min(max(p.vis.key_lens[it.b], 0), p.Tk) : p.Tk;
     // lo and hi grow with the row: the first and the last row bound the block
@@ -189,6 +196,11 @@ __device__ __forceinline__ Item make_item(const ScoredFwdParams &p, int k) {
     it.full_lo = last.x;
     it.full_hi = first.y;
     return it;
+}
+
+template <int kMode>
+__device__ __forceinline__ bool sorted(const ScoredFwdParams &p) {
+    return kMode != kDecode && (p.vis.key_lens || p.vis.prefix_lens || p.vis.doc_range) && p.B * p.num_qblocks <= kSorted;
 }
 
 // The t-th key tile of an item: down from jd, then up.
@@ -204,7 +216,7 @@ __device__ __forceinline__ const Item &item_of(Smem &sm, const ScoredFwdParams &
     if (t < kItemTable) return sm.item_tab[t];
     Item &own = sm.item_own[threadIdx.x >> 5];
     __syncwarp(__activemask());
-    own = make_item<kMode>(p, item_index(t, cta, G));  // every lane writes the same
+    own = make_item<kMode>(p, item_index(t, cta, G), sorted<kMode>(p) ? sm.order : nullptr);  // every lane writes the same
     __syncwarp(__activemask());
     return own;
 }
@@ -295,9 +307,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // so it may read them too.
     pdl_wait();
     pdl_launch_dependents();
+    if (sorted<kMode>(p)) {
+        const int n = p.B * p.num_qblocks, x = threadIdx.x;
+        int len = 0;
+        if (x < n) {
+            len = min(make_item<kMode>(p, x * p.H, nullptr).n_kv, 65535);
+            sm.len[x] = static_cast<uint16_t>(len);
+        }
+        __syncthreads();
+        if (x < n) {
+            int rank = 0;
+            for (int i = 0; i < n; ++i) {
+                const int other = sm.len[i];
+                rank += other > len || (other == len && i < x) ? 1 : 0;
+            }
+            sm.order[rank] = static_cast<uint16_t>(x);
+        }
+        __syncthreads();
+    }
     for (int t = threadIdx.x; t < kItemTable; t += kThreads) {
         const int k = item_index(t, cta, G);
-        if (k < total) sm.item_tab[t] = make_item<kMode>(p, k);
+        if (k < total) sm.item_tab[t] = make_item<kMode>(p, k, sorted<kMode>(p) ? sm.order : nullptr);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -650,7 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 16; ++c) pk[c] = pl[c] = 0u;
                         } else {
-                            const bool all = __all_sync(0xffffffffu, w.keys.x <= kh && w.keys.y >= kh + 32);
+                            const int lo = min(max(w.keys.x - kh, 0), 32), hi = min(w.keys.y - kh, 32);
+                            // the keys seen, a bit each
+                            const unsigned bits = none ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+                            const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
                             bool need = false;
                             // attempt 0 against the reference in hand; where a
                             // row needs the exact step, 1 moves its reference
@@ -660,11 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t y[32];
                                 tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
                                 tmem_ld_wait(y);
-                                const int lo = w.keys.x - kh, hi = w.keys.y - kh;
                                 auto mask_to = [&](float value) {
 #pragma unroll
                                     for (int c = 0; c < 32; ++c)
-                                        if (c < lo || c >= hi) y[c] = __float_as_uint(value);
+                                        if (!(bits >> c & 1u)) y[c] = __float_as_uint(value);
                                 };
                                 if (kCap) {
                                     // masked scores have no say in how tanh is taken
