@@ -53,8 +53,8 @@ constexpr int kStages = 3;
 
 // What only a bucket bias needs.
 struct SmemBuckets {
-    float bias[kStages][2 * BQ];                    // near block pairs: window of the expanded bias
-    uint8_t idx[kStages][2 * BQ];                   // and of its buckets
+    alignas(16) float bias[kStages][2 * BQ];                  // near block pairs: window of the expanded bias
+    alignas(16) uint8_t idx[kStages][2 * BQ];                  // and of its buckets
     float sums[2][kSoftmaxWarps][2 * kMaxBuckets];  // a warp's sums of one head
 };
 struct SmemNone {};

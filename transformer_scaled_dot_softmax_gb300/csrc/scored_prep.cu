@@ -94,23 +94,37 @@ __global__ void __launch_bounds__(kThreads)
         prep_entry(p, n_vec, static_cast<long long>(blockIdx.x - row_blocks) * kThreads + threadIdx.x);
 }
 
-// Blocks [0, dq_blocks): dQ to bf16.  The next kv_blocks: dK (times scale) and
-// dV from their partial sums, a thread 8 features of a row.  The others: 32
-// buckets of one head each, a lane one bucket, the 8 warps every eighth
-// (batch entry, key block) each, all added in a fixed order.
+// Blocks [0, table_blocks), first because they take longest: 32 buckets of one
+// head each, a lane one bucket, the 8 warps every eighth (batch entry, key
+// block) each, all added in a fixed order.  The next kv_blocks: dK (times scale)
+// and dV from their partial sums, a thread 8 features of a row.  The others: dQ
+// to bf16.
 __global__ void __launch_bounds__(kThreads)
     scored_bwd_post(const __grid_constant__ ScoredBwdParams p, __nv_bfloat16 *__restrict__ dq,
-                    __nv_bfloat16 *__restrict__ dtable, unsigned dq_blocks, unsigned kv_blocks, int n_kb) {
+                    __nv_bfloat16 *__restrict__ dtable, unsigned table_blocks, unsigned kv_blocks, int n_kb) {
     __shared__ float part[kThreads / 32][32];
     pdl_wait();
-    if (blockIdx.x < dq_blocks) {
-        bwd_convert_dq(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, p.dq_acc, dq,
-                       static_cast<long long>(p.B) * p.H, p.Tq, p.Tq_pad, p.scale);
-        return;
-    }
-    if (blockIdx.x < dq_blocks + kv_blocks) {
+    if (blockIdx.x < table_blocks) {
+        const int total = p.bk.num * (p.bk.both ? 2 : 1), per_head = (total + 31) / 32;
+        const int x = static_cast<int>(blockIdx.x);
+        const int h = x / per_head, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int u = (x - h * per_head) * 32 + lane;
+        float sum = 0.f;
+        if (u < total)
+#pragma unroll 8
+            for (int i = warp; i < p.B * n_kb; i += kThreads / 32) {
+                const int b = i / n_kb, kb = i - b * n_kb;
+                sum += p.bucket_part[((static_cast<long long>(b) * p.H + h) * n_kb + kb) * total + u];
+            }
+        part[warp][lane] = sum;
+        __syncthreads();
+        if (warp == 0 && u < total) {
+            for (int w = 1; w < kThreads / 32; ++w) sum += part[w][lane];
+            dtable[u * p.H + h] = __float2bfloat16_rn(sum);
+        }
+    } else if (blockIdx.x < table_blocks + kv_blocks) {
         const long long n = static_cast<long long>(p.B) * p.Hkv * p.Tk * 8;  // of one tensor
-        long long t = static_cast<long long>(blockIdx.x - dq_blocks) * kThreads + threadIdx.x;
+        long long t = static_cast<long long>(blockIdx.x - table_blocks) * kThreads + threadIdx.x;
         if (t >= 2 * n) return;
         const bool is_dv = t >= n;
         if (is_dv) t -= n;
@@ -125,24 +139,9 @@ __global__ void __launch_bounds__(kThreads)
         reinterpret_cast<uint4 *>(is_dv ? p.dv : p.dk)[t] =
             make_uint4(pack_bf16x2(s[0] * f, s[1] * f), pack_bf16x2(s[2] * f, s[3] * f), pack_bf16x2(s[4] * f, s[5] * f),
                        pack_bf16x2(s[6] * f, s[7] * f));
-        return;
-    }
-    const int total = p.bk.num * (p.bk.both ? 2 : 1), per_head = (total + 31) / 32;
-    const int x = static_cast<int>(blockIdx.x - dq_blocks - kv_blocks);
-    const int h = x / per_head, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int u = (x - h * per_head) * 32 + lane;
-    float sum = 0.f;
-    if (u < total)
-#pragma unroll 4
-        for (int i = warp; i < p.B * n_kb; i += kThreads / 32) {
-            const int b = i / n_kb, kb = i - b * n_kb;
-            sum += p.bucket_part[((static_cast<long long>(b) * p.H + h) * n_kb + kb) * total + u];
-        }
-    part[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && u < total) {
-        for (int w = 1; w < kThreads / 32; ++w) sum += part[w][lane];
-        dtable[u * p.H + h] = __float2bfloat16_rn(sum);
+    } else {
+        bwd_convert_dq(static_cast<long long>(blockIdx.x - table_blocks - kv_blocks) * kThreads + threadIdx.x, p.dq_acc, dq,
+                       static_cast<long long>(p.B) * p.H, p.Tq, p.Tq_pad, p.scale);
     }
 }
 
@@ -177,7 +176,7 @@ cudaError_t launch_scored_bwd_post(const ScoredBwdParams &p, __nv_bfloat16 *dq, 
     const unsigned table_blocks = dtable ? p.H * ((p.bk.num * (p.bk.both ? 2 : 1) + 31) / 32) : 0;
     const unsigned n = dq_blocks + kv_blocks + table_blocks;
     if (n == 0) return cudaSuccess;
-    return launch_kernel(scored_bwd_post, dim3(n), dim3(kThreads), 0, stream, true, 1, p, dq, dtable, dq_blocks, kv_blocks,
+    return launch_kernel(scored_bwd_post, dim3(n), dim3(kThreads), 0, stream, true, 1, p, dq, dtable, table_blocks, kv_blocks,
                          p.Tq > 0 ? (p.Tk + 127) / 128 : 0);
 }
 
