@@ -22,8 +22,8 @@ __all__ = ["sdpa_forward", "sdpa_forward_lse", "sdpa_forward_host", "sdpa_forwar
            "sdpa_bf16_key_split", "sdpa_backward", "positional_encoding_add",
            "encoder_layer_forward", "ENCODER_PARAMS", "sdpa_decode_forward",
            "sdpa_scored_forward", "sdpa_scored_forward_lse", "sdpa_scored_backward",
-           "sdpa_decode_shared_forward", "relative_bucket_starts", "mha_forward", "mha_forward_add_layernorm", "mha_workspace_bytes", "status_string", "MhaError",
-           "MASKS", "lib"]
+           "sdpa_decode_shared_forward", "relative_bucket_starts", "mha_forward",
+           "mha_forward_add_layernorm", "mha_workspace_bytes", "status_string", "MhaError", "MASKS", "lib"]
 
 MASKS = {"none": MHA_MASK_NONE, "causal": MHA_MASK_CAUSAL, "key_padding": MHA_MASK_KEY_PADDING,
          "causal_key_padding": MHA_MASK_CAUSAL_KEY_PADDING}
@@ -339,28 +339,32 @@ def _starts_array(starts):
     return (ctypes.c_int32 * len(starts))(*starts)
 
 
-def _require(name, t, dtype, shape, device):
-    """t is a contiguous CUDA tensor of that dtype, shape and device index."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
-            return
-    except AttributeError:
-        pass
-    _check_dev(name, t, dtype)
-    if t.get_device() != device:
-        raise ValueError("%s must be on cuda:%d, the current device" % (name, device))
-    raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
+def _require(names, tensors, dtype, shape, device):
+    """Each tensor that is not None is a contiguous CUDA tensor of that dtype,
+    shape and device index.  (One call for all of a kind: on the host a small
+    call's checks take as long as its launches.)"""
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _check_dev(names[i], t, dtype)
+        if t.get_device() != device:
+            raise ValueError("%s must be on cuda:%d, the current device" % (names[i], device))
+        raise ValueError("%s must have the shape %s" % (names[i], tuple(shape)))
 
 
-def _score_form(h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens, doc_ids):
+def _score_form(torch, h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens, doc_ids, dtable=None):
     """(ScoreForm, the bucket starts' array it points into)."""
-    torch = _torch()
     f = _native.ScoreForm()
     keep = None
     if cap is not None:
         f.cap = cap
     if slopes is not None:
-        _require("slopes", slopes, torch.float32, (h,), device)
+        _require(("slopes",), (slopes,), torch.float32, (h,), device)
         f.slopes = slopes.data_ptr()
     if (table is None) != (bucket_starts is None):
         raise ValueError("table and bucket_starts go together")
@@ -369,76 +373,75 @@ def _score_form(h, B, T, device, cap, slopes, table, bucket_starts, prefix_lens,
         n = len(keep)
         if n == 0 or not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[0] not in (n, 2 * n):
             raise ValueError("table must have one row per bucket, or two (bidirectional)")
-        _require("table", table, torch.bfloat16, (table.shape[0], h), device)
+        rows = table.shape[0]
+        _require(("table", "dtable"), (table, dtable), torch.bfloat16, (rows, h), device)
         f.table = table.data_ptr()
         f.bucket_starts = ctypes.addressof(keep)
         f.num_buckets = n
-        f.bidirectional = table.shape[0] == 2 * n
+        f.bidirectional = rows == 2 * n
     if prefix_lens is not None:
-        _require("prefix_lens", prefix_lens, torch.int32, (B,), device)
+        _require(("prefix_lens",), (prefix_lens,), torch.int32, (B,), device)
         f.prefix_lens = prefix_lens.data_ptr()
     if doc_ids is not None:
-        _require("doc_ids", doc_ids, torch.int32, (B, T), device)
+        _require(("doc_ids",), (doc_ids,), torch.int32, (B, T), device)
         f.doc_ids = doc_ids.data_ptr()
     return f, keep
 
 
-def _heads(q, k, v, names=("q", "k", "v")):
-    """Checked (B, h, h_kv, T_q, T_k, d, device index) of q (B, h, T_q, d) and k,
-    v (B, h_kv, T_k, d), bf16 on the current device."""
-    torch = _torch()
-    bf = torch.bfloat16
+def _heads(torch, q, k, v, names, like):
+    """Checked (B, h, h_kv, T_q, T_k, d, device index) of q (B, h, T_q, d), the
+    tensors like it, and k, v (B, h_kv, T_k, d), bf16 on the current device.
+    names: of k, v, q and the tensors like q."""
     device = torch.cuda.current_device()
-    for n, t in zip(names, (q, k)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError("%s must be a tensor of four dimensions" % n)
-    B, h, T_q, d = q.shape
-    _, h_kv, T_k, _ = k.shape
-    _require(names[0], q, bf, (B, h, T_q, d), device)
-    _require(names[1], k, bf, (B, h_kv, T_k, d), device)
-    _require(names[2], v, bf, (B, h_kv, T_k, d), device)
+    try:
+        shape = q.shape
+        B, h, T_q, d = shape
+        _, h_kv, T_k, _ = k.shape
+    except (AttributeError, ValueError):
+        raise ValueError("%s and %s must be tensors of four dimensions" % (names[2], names[0])) from None
+    if v is None:
+        raise ValueError("%s must be a tensor" % names[1])
+    _require(names[2:], (q, *like), torch.bfloat16, shape, device)
+    _require(names, (k, v), torch.bfloat16, (B, h_kv, T_k, d), device)
     return B, h, h_kv, T_q, T_k, d, device
 
 
-def _scratch(workspace, need, device):
+def _scratch(torch, workspace, need, device):
     """(workspace, bytes): the caller's, or a new one of `need` bytes."""
-    torch = _torch()
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device), need
+        return torch.empty(need or 1, dtype=torch.uint8, device=device), need
     _check_dev("workspace", workspace)
     if workspace.get_device() != device:
         raise ValueError("workspace must be on cuda:%d, the current device" % device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
-                 key_lens, prefix_lens, doc_ids, status, stream):
-    torch = _torch()
-    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k, v)
+def _scored_call(torch, q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
+                 key_lens, prefix_lens, doc_ids, status, stream, want_lse):
+    B, h, h_kv, T_q, T_k, d, dev = _heads(torch, q, k, v, ("k", "v", "q", "out", "out_lo"), (out, out_lo))
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _require("out", out, torch.bfloat16, q.shape, dev)
-    if lse is not None:
-        _require("lse", lse, torch.float32, (B, h, T_q), dev)
-    if out_lo is not None:
-        _require("out_lo", out_lo, torch.bfloat16, q.shape, dev)
+    if want_lse:
+        if lse is None:
+            lse = torch.empty((B, h, T_q), dtype=torch.float32, device=dev)
+        else:
+            _require(("lse",), (lse,), torch.float32, (B, h, T_q), dev)
     if key_lens is not None:
-        _require("key_lens", key_lens, torch.int32, (B,), dev)
+        _require(("key_lens",), (key_lens,), torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
-    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
+    form, keep = _score_form(torch, h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
     pf = ctypes.addressof(form)
     size = 0
     if table is not None or doc_ids is not None or workspace is not None:
-        workspace, size = _scratch(workspace, lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf), dev)
+        workspace, size = _scratch(torch, workspace, lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf), dev)
     rc = lib.sdpa_scored_forward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
                                  _ptr(out_lo), _ptr(workspace), size, B, h, h_kv, T_q, T_k, d, d,
                                  1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask),
                                  _ptr(key_lens), pf, _ptr(status), _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_scored_forward")
-    return out
+    return out, lse
 
 
 def sdpa_scored_forward(q, k, v, out=None, workspace=None, *, scale=None, cap=None, slopes=None,
@@ -451,8 +454,8 @@ def sdpa_scored_forward(q, k, v, out=None, workspace=None, *, scale=None, cap=No
     (int32 (B,), with a causal mask) and doc_ids (int32 (B, T), not
     decreasing) leave.  q (B,h,T_q,64), k and v (B,h_kv,T_k,64) with h a
     multiple of h_kv; bf16.  Returns out (B,h,T_q,64)."""
-    return _scored_call(q, k, v, out, None, None, workspace, scale, cap, slopes, table, bucket_starts, mask,
-                        key_lens, prefix_lens, doc_ids, status, stream)
+    return _scored_call(_torch(), q, k, v, out, None, None, workspace, scale, cap, slopes, table, bucket_starts,
+                        mask, key_lens, prefix_lens, doc_ids, status, stream, False)[0]
 
 
 def sdpa_scored_forward_lse(q, k, v, out=None, lse=None, workspace=None, *, out_lo=None,
@@ -462,13 +465,8 @@ def sdpa_scored_forward_lse(q, k, v, out=None, lse=None, workspace=None, *, out_
     (B,h,T_q) fp32, which sdpa_scored_backward takes.  out_lo: a tensor like
     out to receive what rounding took from it, for the backward's o_lo.
     Returns (out, lse)."""
-    if lse is None:
-        torch = _torch()
-        _check_dev("q", q, torch.bfloat16)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    out = _scored_call(q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
-                       key_lens, prefix_lens, doc_ids, status, stream)
-    return out, lse
+    return _scored_call(_torch(), q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts,
+                        mask, key_lens, prefix_lens, doc_ids, status, stream, True)
 
 
 def sdpa_scored_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, dtable=None,
@@ -480,35 +478,31 @@ def sdpa_scored_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, dtabl
     dout; every other argument as in the forward.  Returns
     (dq, dk, dv, dtable), dtable None without a table."""
     torch = _torch()
-    bf = torch.bfloat16
-    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k, v)
-    _require("o", o, bf, q.shape, dev)
-    _require("dout", dout, bf, q.shape, dev)
-    _require("lse", lse, torch.float32, (B, h, T_q), dev)
-    if o_lo is not None:
-        _require("o_lo", o_lo, bf, q.shape, dev)
-    grads = []
-    for n, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if t is None:
-            t = torch.empty_like(like)
-        else:
-            _require(n, t, bf, like.shape, dev)
-        grads.append(t)
-    dq, dk, dv = grads
+    B, h, h_kv, T_q, T_k, d, dev = _heads(torch, q, k, v, ("k", "v", "q", "o", "dout", "o_lo", "dq"),
+                                          (o, dout, o_lo, dq))
+    if o is None or dout is None or lse is None:
+        raise ValueError("o, dout and lse are needed")
+    _require(("lse",), (lse,), torch.float32, (B, h, T_q), dev)
+    if dk is not None or dv is not None:
+        _require(("dk", "dv"), (dk, dv), torch.bfloat16, k.shape, dev)
     if key_lens is not None:
-        _require("key_lens", key_lens, torch.int32, (B,), dev)
+        _require(("key_lens",), (key_lens,), torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
-    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids)
-    if table is not None:
-        if dtable is None:
-            dtable = torch.empty_like(table)
-        else:
-            _require("dtable", dtable, bf, table.shape, dev)
-    elif dtable is not None:
+    if table is None and dtable is not None:
         raise ValueError("dtable needs a table")
+    form, keep = _score_form(torch, h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids, dtable)
+    empty_like = torch.empty_like
+    if dq is None:
+        dq = empty_like(q)
+    if dk is None:
+        dk = empty_like(k)
+    if dv is None:
+        dv = empty_like(v)
+    if table is not None and dtable is None:
+        dtable = empty_like(table)
     pf = ctypes.addressof(form)
-    workspace, size = _scratch(workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, h_kv, T_q, T_k, pf), dev)
+    workspace, size = _scratch(torch, workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, h_kv, T_q, T_k, pf), dev)
     rc = lib.sdpa_scored_backward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o_lo),
                                   dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                   _ptr(dtable), workspace.data_ptr(), size, B, h, h_kv, T_q, T_k, d, d,
@@ -528,23 +522,23 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
     whose last T_q they are; with a causal mask row t sees the cache up to its
     own row.  Scores as sdpa_scored_forward.  Returns out (B,h,T_q,64)."""
     torch = _torch()
-    B, h, h_kv, T_q, T_k, d, dev = _heads(q, k_cache, v_cache, ("q", "k_cache", "v_cache"))
-    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
-        raise ValueError("k_prefix must be a tensor of three dimensions")
-    T_p = k_prefix.shape[1]
-    _require("k_prefix", k_prefix, torch.bfloat16, (h_kv, T_p, d), dev)
-    _require("v_prefix", v_prefix, torch.bfloat16, (h_kv, T_p, d), dev)
+    B, h, h_kv, T_q, T_k, d, dev = _heads(torch, q, k_cache, v_cache, ("k_cache", "v_cache", "q", "out"), (out,))
+    try:
+        _, T_p, _ = k_prefix.shape
+    except (AttributeError, ValueError):
+        raise ValueError("k_prefix must be a tensor of three dimensions") from None
+    if v_prefix is None:
+        raise ValueError("v_prefix must be a tensor")
+    _require(("k_prefix", "v_prefix"), (k_prefix, v_prefix), torch.bfloat16, (h_kv, T_p, d), dev)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _require("out", out, torch.bfloat16, q.shape, dev)
     if cache_lens is not None:
-        _require("cache_lens", cache_lens, torch.int32, (B,), dev)
+        _require(("cache_lens",), (cache_lens,), torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
-    form, keep = _score_form(h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
+    form, keep = _score_form(torch, h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
     pf = ctypes.addressof(form)
-    workspace, size = _scratch(workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
+    workspace, size = _scratch(torch, workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
     rc = lib.sdpa_decode_shared_forward(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
                                         v_cache.data_ptr(), out.data_ptr(), workspace.data_ptr(), size, B, h, h_kv,
                                         T_q, T_p, T_k, d, d, 1.0 / math.sqrt(d) if scale is None else scale,
