@@ -105,7 +105,7 @@ def test_workspace_sizes(lib):
     assert f(2, 3, 7, 7, form(lib, docs=FAKE)) == r(2 * 7 * 8)
     assert f(2, 3, 7, 7, form(lib, table=FAKE, starts=(0, 0))) == 0
     b = lib.lib.sdpa_scored_backward_workspace_bytes
-    plain = 2 * 3 * 256 * 64 * 4 + 2 * 2 * 3 * 256 * 4
+    plain = 256 + 2 * 3 * 256 * 64 * 4 + 2 * 2 * 3 * 256 * 4  # the item counter's 256 bytes, dQ's sums, two row terms
     assert b(2, 3, 3, 130, 7, None) == plain and b(2, 3, 2, 130, 7, None) == 0
     # three query heads on one K/V head, a CTA and fp32 sums of dk and dv each
     assert b(2, 3, 1, 130, 7, None) == plain + 2 * r(3 * 2 * 1 * 7 * 64 * 4)

@@ -146,7 +146,7 @@ mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h
 
 struct BwdLayout {
     Prep prep;
-    size_t dq, nlse2, dvec, idx, buckets, part_dk, part_dv, end;
+    size_t next, dq, nlse2, dvec, idx, buckets, part_dk, part_dv, end;
     int splits, near_blocks;
 };
 BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int h_kv, int T_q, int T_k) {
@@ -155,7 +155,8 @@ BwdLayout bwd_layout(const Form &f, bool docs, int B, int h, int h_kv, int T_q, 
     const size_t BH = static_cast<size_t>(B) * h;
     const int n_qb = (T_q + 127) / 128, n_kb = (T_k + 127) / 128;
     const size_t rows = BH * n_qb * 128;
-    l.dq = l.prep.end;
+    l.next = l.prep.end;
+    l.dq = l.next + 256;
     l.nlse2 = l.dq + round256(rows * 256);
     l.dvec = l.nlse2 + round256(rows * 4);
     l.idx = l.dvec + round256(rows * 4);
@@ -319,6 +320,10 @@ MHA_EXPORT mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const vo
     p.splits = lay.splits;
     p.part_dk = reinterpret_cast<float *>(ws + lay.part_dk);
     p.part_dv = reinterpret_cast<float *>(ws + lay.part_dv);
+    p.next_item = reinterpret_cast<unsigned *>(ws + lay.next);
+    const long long items = static_cast<long long>(B) * h_kv * lay.splits * ((T_k + 127) / 128);
+    if (items >= (1ll << 31)) return MHA_ERR_UNSUPPORTED;
+    p.total_items = static_cast<unsigned>(items);
     p.near_blocks = lay.near_blocks;
     if (dtable) p.bucket_part = reinterpret_cast<float *>(ws + lay.buckets);
     p.status = status_dev;

@@ -213,6 +213,8 @@ struct ScoredBwdParams {
     // part_dk, part_dv (splits, B, Hkv, Tk, 64), instead of dk and dv
     int splits;
     float *part_dk, *part_dv;
+    unsigned total_items;  // (key block, batch entry, K/V head, split)
+    unsigned *next_item;   // the counter that items past the grid's come from, zeroed before
     // bucket bias gradient (bucket_part null: none): (B, H, key blocks, buckets);
     // block pairs up to near_blocks apart hold distances below the last bucket's
     float *bucket_part;

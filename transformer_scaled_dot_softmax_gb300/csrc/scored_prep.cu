@@ -85,8 +85,10 @@ __global__ void __launch_bounds__(kThreads)
     scored_bwd_pre(const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ o_lo,
                    const __nv_bfloat16 *__restrict__ dout, const float *__restrict__ lse, float *__restrict__ nlse2,
                    float *__restrict__ dvec, float *__restrict__ dq_acc, long long BH, int Tq, int Tq_pad,
-                   unsigned row_blocks, const __grid_constant__ PrepParams p, long long n_vec) {
+                   unsigned row_blocks, const __grid_constant__ PrepParams p, long long n_vec,
+                   unsigned *__restrict__ next_item) {
     pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *next_item = 0u;
     if (blockIdx.x < row_blocks)
         bwd_row_terms(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, o, o_lo, dout, lse, nlse2, dvec, dq_acc,
                       BH, Tq, Tq_pad);
@@ -163,9 +165,8 @@ cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o
     const long long BH = static_cast<long long>(p.B) * p.H;
     const PrepParams pp{vec, idx, p.f.mid, p.H, p.bk, doc_range, doc_ids, p.B, p.Tk};
     const unsigned rows = blocks_of(BH * p.Tq_pad * 8), prep = blocks_of(pp.entries());
-    if (rows + prep == 0) return cudaSuccess;
-    scored_bwd_pre<<<rows + prep, kThreads, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows,
-                                                         pp, pp.vec_entries());
+    scored_bwd_pre<<<std::max(rows + prep, 1u), kThreads, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows,
+                                                                     pp, pp.vec_entries(), p.next_item);
     return cudaGetLastError();
 }
 
