@@ -699,11 +699,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         if (!(bits >> c & 1u)) y[c] = __float_as_uint(value);
                                 };
                                 if (kCap) {
-                                    // masked scores have no say in how tanh is taken
-                                    if (!all) mask_to(0.f);
-                                    cap_scores(y, p.f.cap_in, p.f.mul,
-                                               __all_sync(0xffffffffu, (kMode == kDecode && !w.live) ||
-                                                                           max_abs(y) * fabsf(p.f.cap_in) <= kTanhWide));
+                                    const bool dead = kMode == kDecode && !w.live;
+                                    float big = max_abs(y);
+                                    bool near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
+                                    if (!near && !all) {
+                                        // masked scores have no say in how tanh is taken
+                                        mask_to(0.f);
+                                        big = max_abs(y);
+                                        near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
+                                    }
+                                    if (near) {
+                                        const uint64_t n0 = f32x2_set(p.f.near[0]), n1 = f32x2_set(p.f.near[1]),
+                                                       n2 = f32x2_set(p.f.near[2]);
+#pragma unroll
+                                        for (int c = 0; c < 32; c += 2) {
+                                            const uint64_t s2 = f32x2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                            const uint64_t sq = mul_f32x2(s2, s2);
+                                            float t0, t1;
+                                            f32x2_unpack(mul_f32x2(s2, fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0)), t0, t1);
+                                            y[c] = __float_as_uint(t0);
+                                            y[c + 1] = __float_as_uint(t1);
+                                        }
+                                    } else {
+                                        cap_scores(y, p.f.cap_in, p.f.mul,
+                                                   __all_sync(0xffffffffu, dead || big * fabsf(p.f.cap_in) <= kTanhWide));
+                                    }
                                 }
                                 if (!all) mask_to(p.f.masked);
                                 add_bias<kBias, 1, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
