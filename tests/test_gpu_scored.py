@@ -348,6 +348,24 @@ def test_many_items_per_processor(lib):
     ref.check("o", o, want["o"], want["o_tol"], 2)
 
 
+@pytest.mark.parametrize("h_kv,bias,cap,mask", [(8, "buckets", None, "causal_key_padding"), (8, "buckets", 20.0, "key_padding"),
+                                                (8, "slopes", None, "documents"), (2, "buckets", None, "causal_key_padding"),
+                                                (4, "none", 20.0, "key_padding")])
+def test_gradients_of_many_items(lib, h_kv, bias, cap, mask):
+    # several key blocks for each processor one after the other, blocks that no query sees among them
+    B, T = (40, 260) if h_kv == 8 else (120, 390)
+    q, k, v, go = make(B, 8, h_kv, T, T, 91)
+    form = {"mask": "causal" if mask == "documents" else mask, "cap": cap, **bias_args(bias, 8, 92, both=mask == "key_padding")}
+    if mask == "documents":
+        form["doc_ids"] = docs(B, T, 6, 93)
+    else:
+        lens = torch.randint(0, T + 1, (B,), generator=gen(94), device="cuda", dtype=torch.int32)
+        lens[::5] = 0
+        lens[1::7] = 100
+        form["key_lens"] = lens
+    compare(lib, q, k, v, go, form)
+
+
 def test_refusals(lib):
     q, k, v, go = make(1, 4, 2, 8, 8, 56)
     bad = [({"slopes": torch.zeros(3, device="cuda")}, ValueError), ({"slopes": torch.zeros(4, device="cuda").half()}, ValueError),
