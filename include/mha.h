@@ -302,7 +302,10 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  * that sees no key outputs 0 (lse -inf, no gradient).
  *
  *   q, o (B, h, T_q, 64); k, v (B, h_kv, T_k, 64), h a multiple of h_kv: query
- *   head i reads K/V head i / (h / h_kv).  16-byte aligned.  T_q, T_k < 2^24.
+ *   head i reads K/V head i / (h / h_kv).  16-byte aligned.  T_q < 2^24, T_k
+ *   <= 8388480, h <= 65535, B h ceil(T_q / 128) < 2^30 (else
+ *   MHA_ERR_UNSUPPORTED).  Entries of v up to 2^46 in magnitude: the running
+ *   sums hold weights of up to 2^64 times them.
  *   lse: fp32 (B, h, T_q), the log-sum-exp of the row's scores (natural log,
  *   -inf for a query that sees no key), or NULL.  Unlike sdpa_forward_lse's it
  *   sums the unrounded weights: an fp32 result.
@@ -347,7 +350,10 @@ mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const void *k, const
  * are summed in a fixed order; dq adds key blocks by fp32 reductions in
  * global memory whose order is not fixed, as sdpa_backward does, so equal calls
  * may differ in dq's last bit.  workspace:
- * >= sdpa_scored_backward_workspace_bytes() bytes, 256-byte aligned.
+ * >= sdpa_scored_backward_workspace_bytes() bytes, 256-byte aligned; one per
+ * call in flight.  Three launches (row terms and what the form needs expanded;
+ * the products, one CTA per SM taking blocks of 128 keys off a counter in the
+ * workspace; dq to bf16 and the sums of partial dk, dv, dtable).
  */
 size_t sdpa_scored_backward_workspace_bytes(int B, int h, int h_kv, int T_q, int T_k,
                                             const mha_score_form *form);

@@ -1,7 +1,9 @@
 // scored_prep.cu -- the small launches around scored attention: the expanded
 // bucket bias and the document ranges before it (with the row terms, before
 // the backward), and after the backward dQ, dK, dV and dtable from the sums
-// that it left.
+// that it left.  Bound by latency where they are small (the preparation
+// 4 to 5 us), by their bytes where they are not (2 x 16 heads x 4,096: before
+// 15 us for 84 MB, after 12 us for 50).
 #include <cuda_bf16.h>
 
 #include <algorithm>
