@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     // Does the row need the exact step after a sum against
                     // the reference in hand (0 before there is one)?
-                    auto judge = [&](float sum, bool none) -> bool {
+                    auto must_move = [&](float sum, bool none) -> bool {
                         if (none) return false;
                         if (m_run != -INFINITY) return !(sum <= kSumMax);
                         if (!(sum >= kSumMin && sum <= kSumMax)) return true;
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             const bool first = m_run == -INFINITY;
                             const float lt = sum.get();
-                            if (__any_sync(0xffffffffu, judge(lt, kMode == kDecode && !w.live))) {
+                            if (__any_sync(0xffffffffu, must_move(lt, kMode == kDecode && !w.live))) {
                                 if (first) m_run = -INFINITY;
                                 return false;
                             }
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               pk[c], pl[c], sum);
                                 lt = sum.get();
                                 if (attempt == 2) break;
-                                need = judge(lt, none);
+                                need = must_move(lt, none);
                                 if (!__any_sync(0xffffffffu, need)) break;
                             }
                         }
