@@ -348,6 +348,58 @@ def test_many_items_per_processor(lib):
     ref.check("o", o, want["o"], want["o_tol"], 2)
 
 
+def test_inputs_written_just_before(lib):
+    """Each call's inputs come from work queued right before it (a kernel, a copy, a fill, another stream), eagerly and
+    captured, and each output is overwritten right after it: launches may overlap the ends of the ones before them."""
+    q, k, v, go = make(2, 4, 2, 700, 700, 95)
+    ids = docs(2, 700, 5, 96)
+    forms = [{"mask": "causal"}, {"mask": "causal", "doc_ids": ids.clone(), **bias_args("buckets", 4, 97)}]
+    x, y, z, g = (torch.empty_like(t) for t in (q, k, v, go))
+    o, lo = torch.empty_like(q), torch.empty_like(q)
+    side = torch.cuda.Stream()
+
+    def step(form):
+        out = []
+        for turn in range(3):
+            if turn:  # what the turn before used is destroyed
+                for t in (x, y, z, g, o, lo):
+                    t.fill_(float("nan")) if turn == 1 else t.zero_()
+            if "doc_ids" in form:
+                form["doc_ids"].zero_()
+                form["doc_ids"].copy_(ids)
+            torch.mul(q, 1.0, out=x)
+            y.copy_(k)
+            g.copy_(go)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                z.copy_(v)
+            torch.cuda.current_stream().wait_stream(side)
+            _, lse = lib.sdpa_scored_forward_lse(x, y, z, o, out_lo=lo, **form)
+            dq, dk, dv, dtable = lib.sdpa_scored_backward(x, y, z, o, g, lse, o_lo=lo, **form)
+            out.append([o.clone(), lse, dk, dv, dq] + ([] if dtable is None else [dtable]))
+        return out
+
+    for form in forms:
+        lo_want = torch.empty_like(q)
+        o_want, lse_want = lib.sdpa_scored_forward_lse(q, k, v, out_lo=lo_want, **form)
+        dq, dk, dv, dtable = lib.sdpa_scored_backward(q, k, v, o_want, go, lse_want, o_lo=lo_want, **form)
+        torch.cuda.synchronize()
+        want = [o_want, lse_want, dk, dv]
+        graph = torch.cuda.CUDAGraph()
+        eager = step(form)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            captured = step(form)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        for got in eager + captured:
+            for a, b in zip(want, got):
+                assert torch.equal(a, b)
+            assert (dq.double() - got[4].double()).norm() <= ref.U * dq.double().norm()  # added up in no fixed order
+            assert dtable is None or torch.equal(dtable, got[5])
+
+
 @pytest.mark.parametrize("h_kv,bias,cap,mask", [(8, "buckets", None, "causal_key_padding"), (8, "buckets", 20.0, "key_padding"),
                                                 (8, "slopes", None, "documents"), (2, "buckets", None, "causal_key_padding"),
                                                 (4, "none", 20.0, "key_padding")])

@@ -132,7 +132,7 @@ Prep prep_layout(const Form &f, bool docs, int B, int h, int T) {
 
 // Runs the preparing launch if the form needs one and fills in what it writes.
 mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h, int T, ScoreParams &sp, VisParams &vis,
-                   cudaStream_t stream, bool *any) {
+                   cudaStream_t stream) {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *vec = f.bias == kBiasBuckets ? reinterpret_cast<float *>(ws + lay.vec) : nullptr;
     int2 *docs = f.doc_ids ? reinterpret_cast<int2 *>(ws + lay.docs) : nullptr;
@@ -140,7 +140,6 @@ mha_status prepare(const Form &f, const Prep &lay, void *workspace, int B, int h
     sp.vec = vec;
     vis.doc_range = docs;
     vis.prefix_lens = f.prefix_lens;
-    *any = vec || docs;
     return launched(launch_scored_prep(vec, f.f.far, h, f.bk, docs, f.doc_ids, B, T, stream), "scored attention preparation");
 }
 
@@ -252,8 +251,7 @@ MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const voi
     if ((s = encode_heads_map(&maps.v, T_k > 0 ? v : q, static_cast<long long>(B) * h_kv, Tk_map)) != MHA_OK) return s;
     maps.q_cache = maps.k_cache = maps.v_cache = maps.q;
     ScoredFwdParams p{};
-    bool prepared = false;
-    if ((s = prepare(f, lay, workspace, B, h, T_k, p.f, p.vis, stream, &prepared)) != MHA_OK) return s;
+    if ((s = prepare(f, lay, workspace, B, h, T_k, p.f, p.vis, stream)) != MHA_OK) return s;
     p.B = B;
     p.H = h;
     p.Hkv = h_kv;
@@ -267,7 +265,7 @@ MHA_EXPORT mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const voi
     p.num_qblocks = (T_q + 127) / 128;
     p.total_items = B * h * p.num_qblocks;
     p.status = status_dev;
-    return launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "scored attention launch");
+    return launched(launch_attn_scored(maps, f.capped, f.bias, p, stream), "scored attention launch");
 }
 
 MHA_EXPORT size_t sdpa_scored_backward_workspace_bytes(int B, int h, int h_kv, int T_q, int T_k,
@@ -412,8 +410,7 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
     if ((s = encode_heads_map(&maps.k_cache, T_k > 0 ? k_cache : q, BHk, std::max(T_k, 1))) != MHA_OK) return s;
     if ((s = encode_heads_map(&maps.v_cache, T_k > 0 ? v_cache : q, BHk, std::max(T_k, 1))) != MHA_OK) return s;
     ScoredFwdParams p{};
-    bool prepared = false;
-    if ((s = prepare(f, prep_layout(f, false, B, h, 0), workspace, B, h, 0, p.f, p.vis, stream, &prepared)) != MHA_OK)
+    if ((s = prepare(f, prep_layout(f, false, B, h, 0), workspace, B, h, 0, p.f, p.vis, stream)) != MHA_OK)
         return s;
     p.B = B;
     p.H = h;
@@ -431,7 +428,7 @@ MHA_EXPORT mha_status sdpa_decode_shared_forward(const void *q, const void *k_pr
     p.row_tiles = sp.row_tiles;
     p.part_o = reinterpret_cast<float *>(ws + at_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + at_ml);
-    if ((s = launched(launch_attn_scored(maps, f.capped, f.bias, p, stream, prepared), "shared prefix decoding launch")) !=
+    if ((s = launched(launch_attn_scored(maps, f.capped, f.bias, p, stream), "shared prefix decoding launch")) !=
         MHA_OK)
         return s;
     if (rows == 1) {

@@ -316,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
     }
-    // Document ranges and the expanded bias are written by the launch before
-    // this one.  A launch after this one may begin once that one is complete,
-    // so it may read them too.
+    // The launch before this one may still run, of a call before it or the
+    // one that writes document ranges and the expanded bias (a call after
+    // another of these: 1 to 2 us less).  A launch after this one may begin
+    // once that one is complete, so it may read its results.
     pdl_wait();
     pdl_launch_dependents();
     if (sorted<kMode>(p)) {
@@ -936,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kCap, int kBias, int kMode>
-cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream) {
     auto kernel = attn_scored_kernel<kCap, kBias, kMode>;
     const size_t smem = sizeof(Smem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -945,14 +946,14 @@ cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const int grid = p.total_items < sms ? p.total_items : sms;
     if (grid <= 0) return cudaSuccess;
-    return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, pdl, 1, maps, p);
+    return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, true, 1, maps, p);
 }
 
 template <bool kCap, int kBias>
-cudaError_t launch_form(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream, bool pdl) {
-    if (p.part_o) return launch<kCap, kBias, kDecode>(maps, p, stream, pdl);
-    if (p.lse) return launch<kCap, kBias, kForwardLse>(maps, p, stream, pdl);
-    return launch<kCap, kBias, kForward>(maps, p, stream, pdl);
+cudaError_t launch_form(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream) {
+    if (p.part_o) return launch<kCap, kBias, kDecode>(maps, p, stream);
+    if (p.lse) return launch<kCap, kBias, kForwardLse>(maps, p, stream);
+    return launch<kCap, kBias, kForward>(maps, p, stream);
 }
 
 }  // namespace scored

@@ -4,11 +4,10 @@
 
 namespace mha {
 
-cudaError_t launch_attn_scored_capped(const ScoredMaps &maps, int bias, const ScoredFwdParams &p, cudaStream_t stream,
-                                      bool pdl) {
-    if (bias == kBiasSlopes) return scored::launch_form<true, kBiasSlopes>(maps, p, stream, pdl);
-    if (bias == kBiasBuckets) return scored::launch_form<true, kBiasBuckets>(maps, p, stream, pdl);
-    return scored::launch_form<true, kBiasNone>(maps, p, stream, pdl);
+cudaError_t launch_attn_scored_capped(const ScoredMaps &maps, int bias, const ScoredFwdParams &p, cudaStream_t stream) {
+    if (bias == kBiasSlopes) return scored::launch_form<true, kBiasSlopes>(maps, p, stream);
+    if (bias == kBiasBuckets) return scored::launch_form<true, kBiasBuckets>(maps, p, stream);
+    return scored::launch_form<true, kBiasNone>(maps, p, stream);
 }
 
 }  // namespace mha

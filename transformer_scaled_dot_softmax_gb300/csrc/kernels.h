@@ -185,7 +185,7 @@ struct ScoredMaps {
     CUtensorMap q, k, v, q_cache, k_cache, v_cache;
 };
 cudaError_t launch_attn_scored(const ScoredMaps &maps, bool capped, int bias, const ScoredFwdParams &p,
-                               cudaStream_t stream, bool pdl);
+                               cudaStream_t stream);
 
 // How the g Tq query rows of a K/V head and batch entry are stacked into
 // 128-row tiles: `per` rows of each of `nb` batch entries, `chunks` tiles per

@@ -77,7 +77,14 @@ __device__ __forceinline__ void prep_entry(const PrepParams &p, long long n_vec,
     p.doc_range[x] = make_int2(lo, a);
 }
 
+// It may begin while the launch before it ends, as the attention kernels do
+// after it.  (The attention may not begin before this has passed its wait: its
+// CTAs would sit on the SMs, 3 to 5 % slower.  The backward's first launch does
+// not begin early, nor does anything beside its last: row terms that start
+// while the forward or another conversion ends slow the products that follow,
+// 2 x 16 x 8,192 documents 388 to 397 us, causal 805 to 844.)
 __global__ void __launch_bounds__(kThreads) scored_prep(const __grid_constant__ PrepParams p, long long n_vec) {
+    pdl_wait();
     pdl_launch_dependents();
     prep_entry(p, n_vec, static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x);
 }
@@ -157,8 +164,7 @@ cudaError_t launch_scored_prep(float *vec, int far, int H, const BucketParams &b
                                const int32_t *doc_ids, int B, int T, cudaStream_t stream) {
     const PrepParams p{vec, nullptr, vec_mid(far), H, bk, doc_range, doc_ids, B, T};
     if (p.entries() == 0) return cudaSuccess;
-    scored_prep<<<blocks_of(p.entries()), kThreads, 0, stream>>>(p, p.vec_entries());
-    return cudaGetLastError();
+    return launch_kernel(scored_prep, dim3(blocks_of(p.entries())), dim3(kThreads), 0, stream, true, 1, p, p.vec_entries());
 }
 
 cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o_lo, const __nv_bfloat16 *dout,
@@ -167,9 +173,8 @@ cudaError_t launch_scored_bwd_pre(const __nv_bfloat16 *o, const __nv_bfloat16 *o
     const long long BH = static_cast<long long>(p.B) * p.H;
     const PrepParams pp{vec, idx, p.f.mid, p.H, p.bk, doc_range, doc_ids, p.B, p.Tk};
     const unsigned rows = blocks_of(BH * p.Tq_pad * 8), prep = blocks_of(pp.entries());
-    scored_bwd_pre<<<std::max(rows + prep, 1u), kThreads, 0, stream>>>(o, o_lo, dout, lse, nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows,
-                                                                     pp, pp.vec_entries(), p.next_item);
-    return cudaGetLastError();
+    return launch_kernel(scored_bwd_pre, dim3(std::max(rows + prep, 1u)), dim3(kThreads), 0, stream, false, 1, o, o_lo, dout, lse,
+                         nlse2, dvec, p.dq_acc, BH, p.Tq, p.Tq_pad, rows, pp, pp.vec_entries(), p.next_item);
 }
 
 cudaError_t launch_scored_bwd_post(const ScoredBwdParams &p, __nv_bfloat16 *dq, __nv_bfloat16 *dtable,
