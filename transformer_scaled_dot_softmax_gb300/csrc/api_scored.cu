@@ -84,15 +84,25 @@ mha_status check_form(const mha_score_form *form, float scale, int mask, bool de
     out.f.mul = out.capped ? form->cap * kLog2e : scale * kLog2e;
     if (!isfinite(out.f.cap_in) || !isfinite(out.f.mul)) return MHA_ERR_INVALID_ARG;
     if (out.capped) {
-        // degree-2 fit of tanh(x) / x in x^2 over [0, 0.25] (scores.cuh)
+        // fits of tanh(x) / x in x^2 over [0, 0.5^2] and [0, 1.7^2] (scores.cuh)
         constexpr double kNear[3] = {0.999978295, -0.331718863, 0.115318969};
+        constexpr double kWide[7] = {0.999964321,  -0.332565284,   0.129537331,   -0.0458991416,
+                                     0.0125609041, -0.00216785714, 0.000168549304};
+        // In s = x / cap_in, with the factor mul; usable where every coefficient
+        // and the squares stay within fp32's normal range.
         const double a = out.f.cap_in;
-        double pow = out.f.mul * a;
-        for (int i = 0; i < 3; ++i, pow *= a * a) out.f.near[i] = static_cast<float>(kNear[i] * pow);
-        const double most = 0.25 / (a * a);
-        // the products of the polynomial stay within fp32's normal range
-        if (fabs(static_cast<double>(out.f.near[2])) > 1e-36 && fabs(out.f.near[2]) < 1e36f && most > 1e-18 && most < 1e18)
-            out.f.near_max = static_cast<float>(most);
+        auto in_scores = [&](const double *k, int n, double most_x2, float *to) -> float {
+            bool fine = a != 0.0;
+            double pow = out.f.mul * a;
+            for (int i = 0; i < n; ++i, pow *= a * a) {
+                to[i] = static_cast<float>(k[i] * pow);
+                fine = fine && fabs(k[i] * pow) > 1e-36 && fabs(k[i] * pow) < 1e36;
+            }
+            const double most = most_x2 / (a * a);
+            return fine && most > 1e-18 && most < 1e18 ? static_cast<float>(most) : 0.f;
+        };
+        out.f.near_max = in_scores(kNear, 3, 0.25, out.f.near);
+        out.f.wide_max = in_scores(kWide, 7, 1.7 * 1.7, out.f.wide);
     }
     // A masked score is u = -inf before the multiplication by mul: with scale
     // 0 a factor that makes every other product vanish beside 1 keeps it so.

@@ -47,9 +47,9 @@
 // tensor memory in most others; the tensor cores are 28 to 38 % busy.
 //
 // Measured, 2 x 16 heads x 8,192, causal, without / with the log-sum-exp:
-// 287 / 348 us (958 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
-// 424 / 511, slopes 347 / 409, 32 buckets 337 / 387, cap 20 with half the tiles
-// past the polynomials' range 730 / 840, 12 documents 98 / 113.  Per item of
+// 285 / 347 us (965 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
+// 413 / 515, slopes 347 / 409, 32 buckets 336 / 382, cap 20 with scores in the
+// wide range 620 / 809, 12 documents 98 / 113 (capped 155 with).  Per item of
 // 128 rows about 2.5 us (3.5 with the log-sum-exp) and 0.6 (0.7) per key tile;
 // a tile seen in part costs two to three whole ones, which is what documents
 // and short sequences are bound by.
@@ -524,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t(&pk)[32], Sum &sum, float &big, auto half_done) -> bool {
             constexpr int kKind = decltype(kind)::value;
             uint32_t b16[16];
-            const uint64_t mul2 = f32x2_set(kKind == 2 ? p.f.cap_in : p.f.mul);
+            const uint64_t mul2 = f32x2_set(p.f.mul);
             const uint64_t n0 = f32x2_set(p.f.near[0]), n1 = f32x2_set(p.f.near[1]), n2 = f32x2_set(p.f.near[2]);
-            const TanhWide poly(p.f.mul);
+            const TanhWide poly(p.f);
             constexpr int kChains = kBias == kBiasSlopes ? 4 : 1;
             uint64_t b[kChains];
 #pragma unroll
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (kKind == 0) {
                         y = fma_f32x2(s2, mul2, b[c % kChains]);
                     } else {
-                        const uint64_t x = kKind == 1 ? s2 : mul_f32x2(s2, mul2), sq = mul_f32x2(x, x);
+                        const uint64_t sq = mul_f32x2(s2, s2);
                         float w0, w1;
                         f32x2_unpack(sq, w0, w1);
                         if (c & 1)
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             big0 = fmax3(big0, w0, w1);
                         const uint64_t pol = kKind == 1 ? fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0) : poly(sq);
-                        y = fma_f32x2(x, pol, b[c % kChains]);
+                        y = fma_f32x2(s2, pol, b[c % kChains]);
                     }
                     if (kBias == kBiasSlopes) b[c % kChains] = add_f32x2(b[c % kChains], step2);
                     float x0, x1;
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
             float l_run = 0.f;
             // the range the warp's capped scores need: near, wide, any
-            int tier = kCap && p.f.near_max == 0.f ? 1 : 0;
+            int tier = !kCap || p.f.near_max != 0.f ? 0 : p.f.wide_max != 0.f ? 1 : 2;
 
             for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
                 if ((n & 1) != half) continue;
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // their column.
                         auto keep = [&](uint32_t col) -> bool {
                             if (kCap && kMode == kDecode && !w.live) big = 0.f;
-                            if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : kTanhWide * kTanhWide))) {
+                            if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : p.f.wide_max))) {
                                 ++tier;  // out of the polynomial's range: taken again below
                                 return false;
                             }
@@ -736,8 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             y[c + 1] = __float_as_uint(t1);
                                         }
                                     } else {
-                                        cap_scores(y, p.f.cap_in, p.f.mul,
-                                                   __all_sync(0xffffffffu, dead || big * fabsf(p.f.cap_in) <= kTanhWide));
+                                        cap_scores(y, p.f, __all_sync(0xffffffffu, dead || big * big <= p.f.wide_max));
                                     }
                                 }
                                 if (!all) mask_to(p.f.masked);

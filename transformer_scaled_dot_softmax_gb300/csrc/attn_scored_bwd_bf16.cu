@@ -216,7 +216,7 @@ __device__ __forceinline__ void score_terms(uint32_t (&sv)[16], uint32_t (&dp)[1
                 sv[e + 1] = __float_as_uint(b);
             }
         } else {
-            cap_scores(sv, f.cap_in, f.mul, __all_sync(0xffffffffu, big * fabsf(f.cap_in) <= kTanhWide));
+            cap_scores(sv, f, __all_sync(0xffffffffu, big * big <= f.wide_max));
         }
     }
     // mul tanh, before the bias comes to it

@@ -124,7 +124,9 @@ struct ScoreParams {
     float mul;            // y = u mul + bias, u = q.k or tanh(q.k cap_in), y in log2 units; never 0
     // Capped scores with |q.k cap_in| <= 0.5: y = s (near[0] + near[1] s^2 +
     // near[2] s^4), s = q.k; s^2 <= near_max (0: not representable, unused).
+    // With |q.k cap_in| <= 1.7: the same of wide, s^2 <= wide_max.
     float near[3], near_max;
+    float wide[7], wide_max;
     float masked;         // the u of a masked score: minus infinity times the sign of mul
     const float *slopes;  // (H) fp32, kBiasSlopes
     // kBiasBuckets, written by the preparing launch for distances -mid .. mid:

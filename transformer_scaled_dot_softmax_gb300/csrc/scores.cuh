@@ -31,24 +31,23 @@ __device__ __forceinline__ uint64_t f32x2_set(float v) { return f32x2_pack(v, v)
 //         is 3.9e-3 to 7.8e-3 of it.  The coefficients (ScoreParams.near) hold
 //         mul and the powers of cap_in, so that y = s p(s^2) + bias is four
 //         packed operations per pair of scores, three more than uncapped;
-//   wide  |x| <= 1.75, degree 7, least absolute error, 2.2e-6 in fp32 (1.1e-4
-//         in a score capped at 50): ten operations;
+//   wide  |x| <= 1.7, degree 6, coefficients likewise (ScoreParams.wide), error
+//         at most 9.1e-6 of the cap (4.5e-4 in a score capped at 50, as near's)
+//         and 3.6e-5 of a small score: eight operations (degree 7 and x made
+//         first took ten, 2 x 16 x 8,192 causal, cap 20: 730 us);
 //   any   tanh_any, two special-function operations per score.
-constexpr float kTanhNear = 0.5f, kTanhWide = 1.75f;
 
-// mul p(w) for w = x^2, the wide range: x times it is mul tanh(x).
+// p(s^2) of the wide range: s times it is mul tanh(s cap_in).
 struct TanhWide {
-    uint64_t c[8];
-    __device__ __forceinline__ explicit TanhWide(float mul) {
-        constexpr float k[8] = {0.99997997f,   -0.332981028f,   0.131501142f,    -0.0495564923f,
-                                0.0158997465f, -0.00376142941f, 0.000550391496f, -3.62618914e-05f};
+    uint64_t c[7];
+    __device__ __forceinline__ explicit TanhWide(const ScoreParams &f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = f32x2_set(mul * k[i]);
+        for (int i = 0; i < 7; ++i) c[i] = f32x2_set(f.wide[i]);
     }
     __device__ __forceinline__ uint64_t operator()(uint64_t w) const {
-        uint64_t p = fma_f32x2(w, c[7], c[6]);
+        uint64_t p = fma_f32x2(w, c[6], c[5]);
 #pragma unroll
-        for (int i = 5; i >= 0; --i) p = fma_f32x2(w, p, c[i]);
+        for (int i = 4; i >= 0; --i) p = fma_f32x2(w, p, c[i]);
         return p;
     }
 };
@@ -59,16 +58,15 @@ __device__ __forceinline__ float tanh_any(float x) {
     return 1.f - __fdividef(2.f, 1.f + ex2_approx(x * (2.f * kLog2E)));
 }
 
-// s := mul tanh(s cap_in) of N scores in place.  wide (warp-uniform): no
-// |s cap_in| of the warp is past kTanhWide.
+// s := mul tanh(s cap_in) of N scores in place.  wide (warp-uniform): no s^2 of
+// the warp is past f.wide_max.
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float cap_in, float mul, bool wide) {
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams &f, bool wide) {
     if (wide) {
-        const uint64_t a2 = f32x2_set(cap_in);
-        const TanhWide poly(mul);
+        const TanhWide poly(f);
 #pragma unroll
         for (int c = 0; c < N; c += 2) {
-            const uint64_t x = mul_f32x2(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), a2);
+            const uint64_t x = f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
             float t0, t1;
             f32x2_unpack(mul_f32x2(x, poly(mul_f32x2(x, x))), t0, t1);
             s[c] = __float_as_uint(t0);
@@ -76,7 +74,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float cap_in, float
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(mul * tanh_any(__uint_as_float(s[c]) * cap_in));
+        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(f.mul * tanh_any(__uint_as_float(s[c]) * f.cap_in));
     }
 }
 
