@@ -35,7 +35,8 @@
 //     tile (a rescale of O each);
 //   * a softmax thread takes a round of 64 scores in one straight line where
 //     it is a common one (every key seen, the bias an arithmetic progression,
-//     capped scores in the polynomials' range), any other 32 by 32;
+//     capped scores in the polynomials' range), any other 32 by 32; in long
+//     items, without cap and log-sum-exp, a common tile's two rounds;
 //   * V rows past the key length are cleared in shared memory before they are
 //     multiplied by their zero weights, so that what a padded buffer holds
 //     there (NaN included) never reaches the output.
@@ -47,8 +48,8 @@
 // tensor memory in most others; the tensor cores are 28 to 38 % busy.
 //
 // Measured, 2 x 16 heads x 8,192, causal, without / with the log-sum-exp:
-// 285 / 347 us (965 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
-// 413 / 515, slopes 347 / 409, 32 buckets 336 / 382, cap 20 with scores in the
+// 254 / 347 us (1,082 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
+// 413 / 515, slopes 310 / 409, 32 buckets 291 / 382, cap 20 with scores in the
 // wide range 620 / 809, 12 documents 98 / 113 (capped 155 with).  Per item of
 // 128 rows about 2.5 us (3.5 with the log-sum-exp) and 0.6 (0.7) per key tile;
 // a tile seen in part costs two to three whole ones, which is what documents
@@ -56,7 +57,10 @@
 // Tried and slower: rounds of 32 scores throughout (382 us), key tiles in
 // ascending order under slopes (822, a rescale per tile), a straight-line
 // variant for masked rounds or for biases from a window in shared memory (the
-// common rounds lose 3 to 12 % to its registers and code).
+// common rounds lose 3 to 12 % to its registers and code), both rounds of a tile
+// in one line with lo parts (slopes 409 to 448, documents 113 to 119, plain 347
+// to 334) or with a cap (cap 50 413 to 392, cap 20 620 to 669, cap 50 with
+// slopes 16 x 8 x 512 29 to 37).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -89,6 +93,13 @@ constexpr uint32_t kOCol = 384;
 // costs no precision, and 2^64 times any length stays far from overflow.
 constexpr float kSumMin = 5.421010862427522e-20f, kSumMax = 1.8446744073709552e19f;
 constexpr int kItemTable = 128;
+// Items of so many key tiles take their common tiles in one straight line (see
+// kWhole), shorter ones and those with slopes round by round: there more tiles
+// move the reference, and the attempt is lost (causal, line / rounds: slopes
+// 16 x 8 x 1,024 52 / 44 us, 8 x 8 x 2,048 71 / 62, 2 x 16 x 8,192 310 / 346;
+// plain 32 x 8 x 512 28 / 24, 8,192 254 / 285; buckets 8 x 8 x 2,048 60 / 64).
+template <int kBias>
+constexpr int kFastTiles = kBias == kBiasSlopes ? 16 : 6;
 constexpr int kSorted = kThreads;
 
 // What the kernel computes.
@@ -520,6 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // argument of the polynomial.  pk: the round's 64 weights; with lo parts
         // 32 keys' hi and lo, of which `half_done` takes the first 32 keys' and
         // says whether to go on.
+        // Without cap and lo parts registers are to spare: a round's 64 scores
+        // are read at once, and a common tile's two rounds stand in one line.
+        constexpr bool kWhole = kMode == kForward && !kCap;
         auto common_round = [&](auto kind, uint32_t tr, uint32_t(&a)[16], bool next, float b0, float step,
                                 uint32_t(&pk)[32], Sum &sum, float &big, auto half_done) -> bool {
             constexpr int kKind = decltype(kind)::value;
@@ -533,9 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kChains; ++i) b[i] = f32x2_pack(fmaf(2.f * i, step, b0), fmaf(2.f * i + 1.f, step, b0));
             const uint64_t step2 = f32x2_set(8.f * step);
             float big0 = 0.f, big1 = 0.f;
-            auto take = [&](const uint32_t(&sc)[16], int part) {
+            auto take = [&](const auto &sc, int part) {
+                constexpr int kPairs = sizeof(sc) / 8;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < kPairs; ++c) {
                     const uint64_t s2 = f32x2_pack(__uint_as_float(sc[2 * c]), __uint_as_float(sc[2 * c + 1]));
                     uint64_t y;
                     if (kKind == 0) {
@@ -560,6 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pack_pair(x0, x1, c, pk[at], pk[(16 + at) & 31], sum);
                 }
             };
+            if constexpr (kWhole) {
+                uint32_t s0[32], s1[32];
+                tmem_ld32(tr, s0);
+                tmem_ld32(tr + 32, s1);
+                tmem_ld_wait(s0);
+                reg_fence32(s1);
+                take(s0, 0);
+                take(s1, 2);
+                return true;
+            }
             tmem_ld_wait(a);
             tmem_ld16(tr + 16, b16);
             take(a, 0);
@@ -587,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const BiasRow br = bias_row<kBias>(p.f, w.head);
             // decoding: rows past the stacked ones have nothing to compute
             const bool warp_live = kMode != kDecode || __any_sync(0xffffffffu, w.live);
+            const bool long_item = it.n_kv >= kFastTiles<kBias>;
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
             float l_run = 0.f;
             // the range the warp's capped scores need: near, wide, any
@@ -613,9 +639,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float b_tile, step;  // bias of the tile's key c: b_tile + c step, if `linear`
                 const bool linear = linear_bias<kBias>(p.f, br, j * BN - w.pos, BN, 0.f, b_tile, step);
                 uint32_t a[16];
-                tmem_ld16(ts, a);
+                int rd_first = 0;
+                if constexpr (kWhole) {
+                    if (!edge && linear && long_item) {
+#pragma unroll
+                        for (int rd = 0; rd < 2; ++rd) {
+                            uint32_t pk[32];
+                            const float ref = m_run == -INFINITY ? 0.f : m_run;
+                            const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(j * BN + 64 * rd - w.pos), -ref)
+                                                                  : b_tile - ref;
+                            Sum sum;
+                            float big = 0.f;
+                            common_round(std::integral_constant<int, 0>{}, ts + 64u * rd, a, false, b0, step, pk, sum, big, [] { return true; });
+                            const float lt = sum.get();
+                            // a reference has to move: to the rounds below
+                            if (__any_sync(0xffffffffu, !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
+                            if (m_run == -INFINITY) m_run = 0.f;
+                            tmem_st32(ts + 32u * rd, pk);
+                            l_run += lt;
+                            tmem_st_wait();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                            rd_first = rd + 1;
+                        }
+                    }
+                }
+                if (!kWhole) tmem_ld16(ts, a);
 #pragma unroll 1
-                for (int rd = 0; rd < 2; ++rd) {
+                for (int rd = rd_first; rd < 2; ++rd) {
                     const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
                     auto sees_none = [&](int first, int len) {
                         return w.keys.x >= first + len || w.keys.y <= first || (kMode == kDecode && !w.live);
@@ -679,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld_wait(a);
                             if (rd == 0) tmem_ld16(tr + 64, a);
                         }
-                    } else {
+                    } else if (!kWhole) {
                         tmem_ld_wait(a);
                         if (rd == 0) tmem_ld16(tr + 64, a);
                     }
