@@ -13,7 +13,10 @@
 // one lane in 128 of a tensor-core tile, whose softmax takes as long as a full
 // one's, while on the SIMT cores a key costs little more than its 256 bytes
 // (caches of up to 1,024 keys, 64 x 16 heads: 28 us against 54; with two rows
-// per K/V head 45 against 36, the other way round).  8 lanes read one 128-byte
+// per K/V head 45 against 36, the other way round).  Where the lengths of the
+// batch fit the CTA's threads, CTAs take them longest first (prefix 8,192 and
+// caches of random lengths up to 1,024, 64 x 16: 51.5 -> 45 us, without prefix
+// 29 -> 27; of equal lengths of 1,024, with prefix, 60 -> 70).  8 lanes read one 128-byte
 // key row, a warp 4 consecutive rows per load, 6 rows per lane group in flight
 // (as decode_bf16.cu); a CTA, or a cluster of them that splits the keys, serves
 // one head of one batch entry.
@@ -37,6 +40,7 @@ constexpr int kKeysPerStep = kRowWarps * 4 * kUnroll;
 struct SmemRow {
     float w_m[kRowWarps], w_l[kRowWarps], w_o[kRowWarps][HD];  // a warp's sums
     float c_m, c_l, c_o[HD];                                   // the CTA's, read by the cluster's rank 0
+    int len[kRowThreads], b;                                   // the batch's lengths, this CTA's entry
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -81,11 +85,28 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
     const int part = lane & 7;   // which 8 of the 64 features
     const int splits = static_cast<int>(cluster_size());
     const int split = static_cast<int>(cluster_rank());
-    const long long row = blockIdx.x / splits;  // b H + head: query row, output row and K/V head in one
-    const int b = static_cast<int>(row / p.H), head = static_cast<int>(row - static_cast<long long>(b) * p.H);
+    long long row = blockIdx.x / splits;  // b H + head: query row, output row and K/V head in one
+    int b = static_cast<int>(row / p.H);
+    const int head = static_cast<int>(row - static_cast<long long>(b) * p.H);
 
     int len = p.Tk;
-    if (p.cache_lens) len = min(max(p.cache_lens[b], 0), p.Tk);
+    if (p.cache_lens && p.B <= kRowThreads) {
+        // the longest caches first: they would end alone otherwise
+        if (threadIdx.x < p.B) sm.len[threadIdx.x] = min(max(p.cache_lens[threadIdx.x], 0), p.Tk);
+        __syncthreads();
+        if (threadIdx.x < p.B) {
+            const int mine = sm.len[threadIdx.x];
+            int rank = 0;
+            for (int i = 0; i < p.B; ++i) rank += sm.len[i] > mine || (sm.len[i] == mine && i < static_cast<int>(threadIdx.x));
+            if (rank == b) sm.b = threadIdx.x;
+        }
+        __syncthreads();
+        b = sm.b;
+        len = sm.len[b];
+        row = static_cast<long long>(b) * p.H + head;
+    } else if (p.cache_lens) {
+        len = min(max(p.cache_lens[b], 0), p.Tk);
+    }
     const int per = ((len + splits - 1) / splits + kKeysPerStep - 1) / kKeysPerStep * kKeysPerStep;
     const int k_begin = min(len, split * per);
     const int k_end = min(len, k_begin + per);
@@ -208,7 +229,12 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
 
 template <int kBias>
 cudaError_t launch_row(const DecodeRowParams &p, int cluster, cudaStream_t stream) {
-    return launch_kernel(decode_row_kernel<kBias>, dim3(static_cast<unsigned>(p.B * p.H * cluster)), dim3(kRowThreads), 0,
+    // Four CTAs on an SM at a time (by their shared memory) where each has a long
+    // cache to itself: those that start later even out what the first had (64 x
+    // 16 heads, prefix 8,192, caches to 1,024: 42 us, seven at a time 45; 128 x 8,
+    // caches to 512: 29 and 27).
+    const size_t smem = cluster == 1 && p.Tk > 512 ? 46 * 1024 : 0;
+    return launch_kernel(decode_row_kernel<kBias>, dim3(static_cast<unsigned>(p.B * p.H * cluster)), dim3(kRowThreads), smem,
                          stream, p.prefix_splits > 0, static_cast<unsigned>(cluster), p);
 }
 
