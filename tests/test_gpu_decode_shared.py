@@ -145,6 +145,55 @@ def test_streams_and_graphs(lib):
     assert all(torch.equal(a, out) for a, (_, out) in zip(want, graphs))
 
 
+@pytest.mark.parametrize("B,T_k", [(128, 40), (129, 40), (300, 700), (5, 3000)])
+def test_batches_of_single_rows(lib, B, T_k):
+    """Batches that are ordered by length and ones too large for that, equal lengths and empty caches among them."""
+    x = make(B, 2, 2, 1, 200, T_k, 41)
+    lens = torch.randint(0, T_k + 1, (B,), generator=gen(42), device="cuda", dtype=torch.int32)
+    lens[1::3] = lens[1]
+    lens[::4] = 0
+    compare(lib, x, lens, {"mask": "key_padding", **bias_args("slopes", 2, 43)})
+
+
+@pytest.mark.parametrize("h_kv,T_q", [(8, 1), (2, 1), (4, 3)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_inputs_written_just_before(lib, h_kv, T_q, biased):
+    """The caches, the query and the lengths are written right before each call and destroyed right after it, eagerly and
+    captured: launches may overlap the ends of the ones before them."""
+    B, h, P, T_k = 48, 8, 3000, 700
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    source = [n(B, h, T_q, 64), n(h_kv, P, 64), n(h_kv, P, 64), n(B, h_kv, T_k, 64), n(B, h_kv, T_k, 64)]
+    lens = torch.randint(T_q, T_k + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    form = {"table": n(16, h), "bucket_starts": lib.relative_bucket_starts(16, 128)} if biased else {}
+    want = lib.sdpa_decode_shared_forward(*source, lens, **form)
+    x, m = [torch.empty_like(t) for t in source], torch.empty_like(lens)
+
+    def step():
+        out = []
+        for _ in range(3):
+            for t, f in zip(x, source):
+                t.copy_(f)
+            torch.add(lens, 0, out=m)
+            out.append(lib.sdpa_decode_shared_forward(*x, m, **form))
+            for t in x:
+                t.fill_(float("nan"))
+            m.zero_()
+        return out
+
+    eager = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for o in eager + captured:
+        assert torch.equal(o, want)
+
+
 def test_refusals(lib):
     q, kp, vp, kc, vc = make(2, 4, 2, 9, 20, 10, 16)
     with pytest.raises(lib.MhaError):  # more rows than a decoding step has
