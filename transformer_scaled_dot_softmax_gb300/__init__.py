@@ -7,6 +7,12 @@ library's CUDA kernels.  PyTorch supplies device memory and the stream.
     out = sdpa_forward(q, k, v, mask="causal")            # (B, h, T, 64) bf16
     out = sdpa_decode_forward(q, k_cache, v_cache, lens)   # (B, h, T_q <= 8, 64) bf16
     out = mha_forward(x_q, x_kv, w_q, w_k, w_v, w_o, h=8)  # (B, T, d_model) bf16
+
+Every call runs on the current stream, or on the one passed as `stream`, which
+then has to wait for the work that writes the call's inputs, as for any other
+use of it (stream.wait_stream).  The tensors that a call makes itself are safe
+on both: scratch belongs to the stream it is used on, results may be used (once
+the current stream has waited) and dropped on the current one.
 """
 from __future__ import annotations
 
@@ -66,6 +72,37 @@ def _stream_on(stream, device):
     return _torch()._C._cuda_getCurrentRawStream(device)
 
 
+def _result(stream, make, *args, **kwargs):
+    """make(...), a tensor that the call's kernels write on `stream` and the
+    caller gets.  The allocator orders a block's reuse by the stream it was
+    allocated on, so a stream other than the current one allocates it (the
+    block may still be in use by work queued on the current one otherwise), and
+    its use on the current one is recorded, so that the caller may drop it there."""
+    if stream is None:
+        return make(*args, **kwargs)
+    torch = _torch()
+    current = torch.cuda.current_stream()
+    if stream == current:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(current)
+    return t
+
+
+def _scratch(torch, workspace, need, device, stream):
+    """(workspace, bytes): the caller's, or a new one of `need` bytes that
+    belongs to `stream`: it is dropped as the call returns, with the kernels
+    still to run, and only that stream's later work may have it then."""
+    if workspace is None:
+        if stream is None:
+            return torch.empty(need or 1, dtype=torch.uint8, device=device), need
+        with torch.cuda.stream(stream):
+            return torch.empty(need or 1, dtype=torch.uint8, device=device), need
+    _check_dev("workspace", workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -93,7 +130,7 @@ def sdpa_forward(q, k, v, out=None, *, scale=None, mask="none", key_lens=None, s
     B, h, T_q, d_k = q.shape
     T_k, d_v = k.shape[2], v.shape[3]
     if out is None:
-        out = torch.empty((B, h, T_q, d_v), dtype=dtype, device=q.device)
+        out = _result(stream, torch.empty, (B, h, T_q, d_v), dtype=dtype, device=q.device)
     _check_dev("out", out, dtype)
     if key_lens is not None:
         _check_dev("key_lens", key_lens, torch.int32)
@@ -120,9 +157,9 @@ def sdpa_forward_lse(q, k, v, out=None, lse=None, *, scale=None, mask="none", ke
     B, h, T_q, d_k = q.shape
     T_k, d_v = k.shape[2], v.shape[3]
     if out is None:
-        out = torch.empty((B, h, T_q, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, torch.empty, (B, h, T_q, d_v), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((B, h, T_q), dtype=torch.float32, device=q.device)
+        lse = _result(stream, torch.empty, (B, h, T_q), dtype=torch.float32, device=q.device)
     _check_dev("out", out, torch.bfloat16)
     _check_dev("lse", lse, torch.float32)
     if key_lens is not None:
@@ -187,13 +224,11 @@ def sdpa_forward_host(q, k, v, out=None, workspace=None, *, scale=None, mask="no
         _check_dev("status", status, torch.int32)
     dt = MHA_F32 if dtype == torch.float32 else MHA_BF16
     need = int(lib.sdpa_forward_host_workspace_bytes(dt, B, h, T_q, T_k, d_k, d_v))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
-    _check_dev("workspace", workspace)
+    workspace, size = _scratch(torch, workspace, need, "cuda", stream)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
     rc = lib.sdpa_forward_host(dt, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), B, h, T_q, T_k, d_k,
+                               size, B, h, T_q, T_k, d_k,
                                d_v, float(scale), _mask_code(mask), _ptr(key_lens), _ptr(status),
                                _stream_handle(stream))
     if rc != MHA_OK:
@@ -213,15 +248,13 @@ def sdpa_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, workspace=No
     _check_dev("lse", lse, torch.float32)
     B, h, T_q, d_k = q.shape
     T_k, d_v = k.shape[2], v.shape[3]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _result(stream, torch.empty_like, q) if dq is None else dq
+    dk = _result(stream, torch.empty_like, k) if dk is None else dk
+    dv = _result(stream, torch.empty_like, v) if dv is None else dv
     for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _check_dev(n, t, bf)
     need = int(lib.sdpa_backward_workspace_bytes(B, h, T_q, T_k, d_k, d_v))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    _check_dev("workspace", workspace)
+    workspace, size = _scratch(torch, workspace, need, q.device, stream)
     if key_lens is not None:
         _check_dev("key_lens", key_lens, torch.int32)
     if status is not None:
@@ -230,7 +263,7 @@ def sdpa_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, workspace=No
         scale = 1.0 / math.sqrt(d_k)
     rc = lib.sdpa_backward(MHA_BF16, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
                            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), B, h, T_q, T_k, d_k,
+                           size, B, h, T_q, T_k, d_k,
                            d_v, float(scale), _mask_code(mask), _ptr(key_lens), _ptr(status),
                            _stream_handle(stream))
     if rc != MHA_OK:
@@ -243,7 +276,7 @@ def positional_encoding_add(x, out=None, *, pos0=0, stream=None):
     torch = _torch()
     _check_dev("x", x, torch.bfloat16)
     B, T, D = x.shape
-    out = torch.empty_like(x) if out is None else out
+    out = _result(stream, torch.empty_like, x) if out is None else out
     _check_dev("out", out, torch.bfloat16)
     rc = lib.positional_encoding_add(_ptr(x), _ptr(out), B, T, D, int(pos0), _stream_handle(stream))
     if rc != MHA_OK:
@@ -267,12 +300,10 @@ def encoder_layer_forward(x, params, h, out=None, workspace=None, *, eps=1e-5, s
         _check_dev(n, params[n], bf)
     B, T, D = x.shape
     F = params["w1"].shape[1]
-    out = torch.empty_like(x) if out is None else out
+    out = _result(stream, torch.empty_like, x) if out is None else out
     _check_dev("out", out, bf)
     need = int(lib.encoder_layer_workspace_bytes(B, T, D, h, F))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
-    _check_dev("workspace", workspace)
+    workspace, size = _scratch(torch, workspace, need, x.device, stream)
     if key_lens is not None:
         _check_dev("key_lens", key_lens, torch.int32)
     if status is not None:
@@ -281,7 +312,7 @@ def encoder_layer_forward(x, params, h, out=None, workspace=None, *, eps=1e-5, s
         scale = 1.0 / math.sqrt(D // h)
     rc = lib.encoder_layer_forward(_ptr(x), *[_ptr(params[n]) for n in ENCODER_PARAMS], float(eps),
                                    _ptr(out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), B, T, D, h, F,
+                                   size, B, T, D, h, F,
                                    float(scale), _mask_code(mask), _ptr(key_lens), _ptr(status),
                                    _stream_handle(stream))
     if rc != MHA_OK:
@@ -301,7 +332,7 @@ def sdpa_decode_forward(q, k_cache, v_cache, cache_lens=None, out=None, *, scale
     B, h, T_q, d_k = q.shape
     T_k, d_v = k_cache.shape[2], v_cache.shape[3]
     if out is None:
-        out = torch.empty((B, h, T_q, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, torch.empty, (B, h, T_q, d_v), dtype=torch.bfloat16, device=q.device)
     _check_dev("out", out, torch.bfloat16)
     if cache_lens is not None:
         _check_dev("cache_lens", cache_lens, torch.int32)
@@ -406,24 +437,22 @@ def _heads(torch, q, k, v, names, like):
     return B, h, h_kv, T_q, T_k, d, device
 
 
-def _scratch(torch, workspace, need, device):
-    """(workspace, bytes): the caller's, or a new one of `need` bytes."""
-    if workspace is None:
-        return torch.empty(need or 1, dtype=torch.uint8, device=device), need
-    _check_dev("workspace", workspace)
+def _scratch_here(torch, workspace, need, device, stream):
+    """_scratch on the current device, whose index is `device`."""
+    workspace, size = _scratch(torch, workspace, need, device, stream)
     if workspace.get_device() != device:
         raise ValueError("workspace must be on cuda:%d, the current device" % device)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, size
 
 
 def _scored_call(torch, q, k, v, out, lse, out_lo, workspace, scale, cap, slopes, table, bucket_starts, mask,
                  key_lens, prefix_lens, doc_ids, status, stream, want_lse):
     B, h, h_kv, T_q, T_k, d, dev = _heads(torch, q, k, v, ("k", "v", "q", "out", "out_lo"), (out, out_lo))
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     if want_lse:
         if lse is None:
-            lse = torch.empty((B, h, T_q), dtype=torch.float32, device=dev)
+            lse = _result(stream, torch.empty, (B, h, T_q), dtype=torch.float32, device=dev)
         else:
             _require(("lse",), (lse,), torch.float32, (B, h, T_q), dev)
     if key_lens is not None:
@@ -434,7 +463,7 @@ def _scored_call(torch, q, k, v, out, lse, out_lo, workspace, scale, cap, slopes
     pf = ctypes.addressof(form)
     size = 0
     if table is not None or doc_ids is not None or workspace is not None:
-        workspace, size = _scratch(torch, workspace, lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf), dev)
+        workspace, size = _scratch_here(torch, workspace, lib.sdpa_scored_workspace_bytes(B, h, T_q, T_k, pf), dev, stream)
     rc = lib.sdpa_scored_forward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse),
                                  _ptr(out_lo), _ptr(workspace), size, B, h, h_kv, T_q, T_k, d, d,
                                  1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask),
@@ -492,17 +521,17 @@ def sdpa_scored_backward(q, k, v, o, dout, lse, dq=None, dk=None, dv=None, dtabl
     if table is None and dtable is not None:
         raise ValueError("dtable needs a table")
     form, keep = _score_form(torch, h, B, T_k, dev, cap, slopes, table, bucket_starts, prefix_lens, doc_ids, dtable)
-    empty_like = torch.empty_like
     if dq is None:
-        dq = empty_like(q)
+        dq = _result(stream, torch.empty_like, q)
     if dk is None:
-        dk = empty_like(k)
+        dk = _result(stream, torch.empty_like, k)
     if dv is None:
-        dv = empty_like(v)
+        dv = _result(stream, torch.empty_like, v)
     if table is not None and dtable is None:
-        dtable = empty_like(table)
+        dtable = _result(stream, torch.empty_like, table)
     pf = ctypes.addressof(form)
-    workspace, size = _scratch(torch, workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, h_kv, T_q, T_k, pf), dev)
+    workspace, size = _scratch_here(torch, workspace, lib.sdpa_scored_backward_workspace_bytes(B, h, h_kv, T_q, T_k, pf), dev,
+                                    stream)
     rc = lib.sdpa_scored_backward(MHA_BF16, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o_lo),
                                   dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                   _ptr(dtable), workspace.data_ptr(), size, B, h, h_kv, T_q, T_k, d, d,
@@ -531,14 +560,15 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
         raise ValueError("v_prefix must be a tensor")
     _require(("k_prefix", "v_prefix"), (k_prefix, v_prefix), torch.bfloat16, (h_kv, T_p, d), dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _result(stream, torch.empty_like, q)
     if cache_lens is not None:
         _require(("cache_lens",), (cache_lens,), torch.int32, (B,), dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
     form, keep = _score_form(torch, h, B, T_k, dev, cap, slopes, table, bucket_starts, None, None)
     pf = ctypes.addressof(form)
-    workspace, size = _scratch(torch, workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev)
+    workspace, size = _scratch_here(torch, workspace, lib.sdpa_decode_shared_workspace_bytes(B, h, h_kv, T_q, T_p, T_k, pf), dev,
+                                    stream)
     rc = lib.sdpa_decode_shared_forward(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(),
                                         v_cache.data_ptr(), out.data_ptr(), workspace.data_ptr(), size, B, h, h_kv,
                                         T_q, T_p, T_k, d, d, 1.0 / math.sqrt(d) if scale is None else scale,
@@ -565,19 +595,17 @@ def _mha_call(x_q, x_kv, w_q, w_k, w_v, w_o, h, out, workspace, scale, mask, key
     d_k = w_q.shape[1] // h
     d_v = w_v.shape[1] // h
     if out is None:
-        out = torch.empty((B, T_q, D), dtype=bf, device=x_q.device)
+        out = _result(stream, torch.empty, (B, T_q, D), dtype=bf, device=x_q.device)
     _check_dev("out", out, bf)
     need = mha_workspace_bytes(B, h, T_q, T_k, d_k, d_v)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x_q.device)
-    _check_dev("workspace", workspace)
+    workspace, size = _scratch(torch, workspace, need, x_q.device, stream)
     if key_lens is not None:
         _check_dev("key_lens", key_lens, torch.int32)
     if status is not None:
         _check_dev("status", status, torch.int32)
     if scale is None:
         scale = 1.0 / math.sqrt(d_k)
-    ws = (_ptr(workspace), workspace.numel() * workspace.element_size())
+    ws = (_ptr(workspace), size)
     tail = (B, h, T_q, T_k, D, d_k, d_v, float(scale), _mask_code(mask), _ptr(key_lens),
             _ptr(status), _stream_handle(stream))
     if ln is None:
