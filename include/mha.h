@@ -279,7 +279,10 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  *
  * The members of mha_score_form, each off when 0 / NULL (a NULL form: all
  * off; the call is then sdpa_forward with shared K/V heads):
- *   cap             caps |s| smoothly; >= 0, finite.
+ *   cap             caps |s| smoothly; 0, or 1e-18 to 1e18.  A capped score is
+ *                   taken to within 6e-4 and 2^-20 of itself, whichever is
+ *                   more (tanh by polynomials where they are that near): a
+ *                   seventh of a weight's rounding to bf16.
  *   slopes          DEVICE fp32 (h): bias_h(d) = -slopes[h] |d|.
  *   table           DEVICE bf16 (num_buckets, h), or (2 num_buckets, h) with
  *                   `bidirectional`: bias_h(d) = table[bucket(d), h], a learned
@@ -308,7 +311,8 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  *   sums hold weights of up to 2^64 times them.
  *   lse: fp32 (B, h, T_q), the log-sum-exp of the row's scores (natural log,
  *   -inf for a query that sees no key), or NULL.  Unlike sdpa_forward_lse's it
- *   sums the unrounded weights: an fp32 result.
+ *   sums the unrounded weights: an fp32 result without a cap, as near as the
+ *   scores with one.
  *   o_lo: bf16 like o, what rounding took from o, or NULL; needs lse.  The
  *   backward takes it so that its row terms carry no bf16 rounding, which
  *   matters where a few keys dominate their rows.

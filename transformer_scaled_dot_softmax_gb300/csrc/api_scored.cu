@@ -18,6 +18,12 @@ using namespace mha;
 
 constexpr int kMaxFar = 1 << 16;      // last bucket's first distance
 constexpr int kMaxLength = 1 << 24;   // distances are exact in fp32
+// Caps between which the score, its derivative and their factors stay well
+// inside fp32's range.
+constexpr float kLeastCap = 1e-18f, kMostCap = 1e18f;
+// What the capping polynomials may take from a score, in natural units: a
+// seventh of a weight's bf16 half step (2^-8 relative).
+constexpr double kCapError = 6e-4;
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -63,7 +69,7 @@ mha_status check_form(const mha_score_form *form, float scale, int mask, bool de
     if (mask < MHA_MASK_NONE || mask > MHA_MASK_CAUSAL_KEY_PADDING) return MHA_ERR_INVALID_ARG;
     const mha_score_form none{};
     if (!form) form = &none;
-    if (!(form->cap >= 0.f) || !isfinite(form->cap)) return MHA_ERR_INVALID_ARG;
+    if (!(form->cap >= 0.f && form->cap <= kMostCap) || (form->cap > 0.f && form->cap < kLeastCap)) return MHA_ERR_INVALID_ARG;
     if (form->num_buckets < 0 || (form->table != nullptr) != (form->num_buckets > 0)) return MHA_ERR_INVALID_ARG;
     if (form->slopes && form->table) return MHA_ERR_INVALID_ARG;
     if (form->num_buckets > kMaxBuckets) return MHA_ERR_UNSUPPORTED;
@@ -82,27 +88,35 @@ mha_status check_form(const mha_score_form *form, float scale, int mask, bool de
     constexpr float kLog2e = 1.4426950408889634f;
     out.f.cap_in = out.capped ? scale / form->cap : 0.f;
     out.f.mul = out.capped ? form->cap * kLog2e : scale * kLog2e;
-    if (!isfinite(out.f.cap_in) || !isfinite(out.f.mul)) return MHA_ERR_INVALID_ARG;
+    out.f.lin = scale * kLog2e;
+    if (!isfinite(out.f.cap_in) || !isfinite(out.f.mul) || !isfinite(out.f.lin)) return MHA_ERR_INVALID_ARG;
     if (out.capped) {
         // fits of tanh(x) / x in x^2 over [0, 0.5^2] and [0, 1.7^2] (scores.cuh)
         constexpr double kNear[3] = {0.999978295, -0.331718863, 0.115318969};
         constexpr double kWide[7] = {0.999964321,  -0.332565284,   0.129537331,   -0.0458991416,
                                      0.0125609041, -0.00216785714, 0.000168549304};
+        // ... and their errors, those of x p(x^2) against tanh(x): near's in
+        // parts of x, wide's absolute; times the cap they are a score's.
+        constexpr double kNearError = 2.2e-5, kWideError = 9.1e-6;
+        const double near_x = std::min(0.5, kCapError / (kNearError * form->cap));
+        const double wide_x = kWideError * form->cap <= kCapError ? 1.7 : 0.0;
         // In s = x / cap_in, with the factor mul; usable where every coefficient
         // and the squares stay within fp32's normal range.
         const double a = out.f.cap_in;
-        auto in_scores = [&](const double *k, int n, double most_x2, float *to) -> float {
+        auto in_scores = [&](const double *k, int n, double most_x, float *to) -> float {
             bool fine = a != 0.0;
             double pow = out.f.mul * a;
             for (int i = 0; i < n; ++i, pow *= a * a) {
                 to[i] = static_cast<float>(k[i] * pow);
                 fine = fine && fabs(k[i] * pow) > 1e-36 && fabs(k[i] * pow) < 1e36;
             }
-            const double most = most_x2 / (a * a);
-            return fine && most > 1e-18 && most < 1e18 ? static_cast<float>(most) : 0.f;
+            const double most = most_x * most_x / (a * a);
+            if (fine && most > 1e-18 && most < 1e18) return static_cast<float>(most);
+            std::fill(to, to + n, 0.f);  // scores of 0 alone
+            return 0.f;
         };
-        out.f.near_max = in_scores(kNear, 3, 0.25, out.f.near);
-        out.f.wide_max = in_scores(kWide, 7, 1.7 * 1.7, out.f.wide);
+        out.f.near_max = in_scores(kNear, 3, near_x, out.f.near);
+        out.f.wide_max = in_scores(kWide, 7, wide_x, out.f.wide);
     }
     // A masked score is u = -inf before the multiplication by mul: with scale
     // 0 a factor that makes every other product vanish beside 1 keeps it so.

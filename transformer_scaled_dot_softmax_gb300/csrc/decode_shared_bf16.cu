@@ -142,8 +142,7 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
             d += __shfl_xor_sync(0xffffffffu, d, 4);
             const int key = base + (u * kRowWarps + warp) * 4 + slot;
             const int dist = key - (len - 1);  // the query is the cache's last row
-            if (p.capped) d = tanh_any(d * p.f.cap_in);
-            float y = d * p.f.mul;
+            float y = p.capped ? cap_any(d, p.f) : d * p.f.mul;
             if (kBias == kBiasSlopes) y = fmaf(-slope2, fabsf(static_cast<float>(dist)), y);
             // vec may come from the launch two before this one: read past L1
             if (kBias == kBiasBuckets) y += __ldcg(vec + max(min(dist, 0), -p.f.mid));

@@ -24,18 +24,22 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ uint64_t f32x2_set(float v) { return f32x2_pack(v, v); }
 
 // tanh(x) as x p(x^2), on the FMA pipe, two scores per operation, and nothing
-// on the special-function unit, which the weights' 2^x already fill.  Three
-// ranges, each a warp's choice by the largest score it holds:
-//   near  |x| <= 0.5, p of degree 2 fitted to the least relative error, 2.2e-5:
-//         at most 5.5e-4 in a score of 25, where one step of a weight's bf16
-//         is 3.9e-3 to 7.8e-3 of it.  The coefficients (ScoreParams.near) hold
-//         mul and the powers of cap_in, so that y = s p(s^2) + bias is four
-//         packed operations per pair of scores, three more than uncapped;
-//   wide  |x| <= 1.7, degree 6, coefficients likewise (ScoreParams.wide), error
-//         at most 9.1e-6 of the cap (4.5e-4 in a score capped at 50, as near's)
-//         and 3.6e-5 of a small score: eight operations (degree 7 and x made
-//         first took ten, 2 x 16 x 8,192 causal, cap 20: 730 us);
-//   any   tanh_any, two special-function operations per score.
+// on the special-function unit, which the weights' 2^x need.  Three ranges, each
+// a warp's choice by the largest score it holds; near and wide only as far as
+// they take less than 6e-4 from a score (one step of a weight's bf16 is 3.9e-3
+// to 7.8e-3 of it), which is near whole up to a cap of 54 and to scores of 27
+// above, and wide up to a cap of 65:
+//   near  |x| <= 0.5, p of degree 2, off by 2.2e-5 x at most (2.4e-5 of tanh x,
+//         1.1e-5 of the cap).  The coefficients (ScoreParams.near) hold mul and
+//         the powers of cap_in, so that y = s p(s^2) + bias is four packed
+//         operations per pair of scores, three more than uncapped;
+//   wide  |x| <= 1.7, degree 6, coefficients likewise (ScoreParams.wide), off by
+//         8.8e-6 of the cap at most and by 3.6e-5 of a small score: eight
+//         operations (degree 7, 2.2e-6 of the cap, with x made first took ten,
+//         2 x 16 x 8,192 causal, cap 20: 730 us against 620);
+//   any   cap_any, to fp32's own precision, two special-function operations per
+//         score.
+// (1 - tanh^2 of the backward is off by 1.0e-5 in near's range, 1.7e-5 in wide's.)
 
 // p(s^2) of the wide range: s times it is mul tanh(s cap_in).
 struct TanhWide {
@@ -52,10 +56,15 @@ struct TanhWide {
     }
 };
 
-// tanh(x) = 1 - 2 / (1 + e^(2x)) for any x (absolute error ~2^-22; e^(2x)
-// overflowing to infinity gives 1, underflowing to 0 gives -1).
-__device__ __forceinline__ float tanh_any(float x) {
-    return 1.f - __fdividef(2.f, 1.f + ex2_approx(x * (2.f * kLog2E)));
+// mul tanh(x), x = s cap_in, for any s, to 2^-20 of itself: below |x| = 1/4 the
+// Taylor series (its next term is 9e-9 there), taken from s so that large caps
+// lose nothing; above, tanh(x) = 1 - 2 / (1 + e^(2x)), absolute error ~2^-22
+// (e^(2x) overflowing to infinity gives 1, underflowing to 0 gives -1).
+__device__ __forceinline__ float cap_any(float s, const ScoreParams &f) {
+    const float x = s * f.cap_in, w = x * x;
+    const float p = fmaf(w, fmaf(w, fmaf(w, fmaf(w, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    const float far = f.mul * (1.f - __fdividef(2.f, 1.f + ex2_approx(x * (2.f * kLog2E))));
+    return w <= 0.0625f ? s * f.lin * p : far;
 }
 
 // s := mul tanh(s cap_in) of N scores in place.  wide (warp-uniform): no s^2 of
@@ -74,7 +83,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], const ScoreParams &
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(f.mul * tanh_any(__uint_as_float(s[c]) * f.cap_in));
+        for (int c = 0; c < N; ++c) s[c] = __float_as_uint(cap_any(__uint_as_float(s[c]), f));
     }
 }
 
