@@ -302,7 +302,9 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  *                   are seen is unspecified; nothing is read or written out of
  *                   range).
  * All of them meet with `mask` and key_lens: a key must pass every one.  A query
- * that sees no key outputs 0 (lse -inf, no gradient).
+ * that sees no key outputs 0 (lse -inf, no gradient).  A NaN, or a positive
+ * infinity, among the scores that a query sees makes its o and lse NaN, and with
+ * them the gradients that it enters.
  *
  *   q, o (B, h, T_q, 64); k, v (B, h_kv, T_k, 64), h a multiple of h_kv: query
  *   head i reads K/V head i / (h / h_kv).  16-byte aligned.  T_q < 2^24, T_k
@@ -382,7 +384,8 @@ mha_status sdpa_scored_backward(mha_dtype dt, const void *q, const void *k, cons
  * T_p + len_b - T_q + t.  Every query row sees len_b cache rows; with a causal
  * mask row t sees the first len_b - T_q + 1 + t of them (and all of the
  * prefix).  form: cap, slopes, table; prefix_lens and doc_ids must be NULL.
- * T_p == 0 and T_k == 0 are allowed; a row without any key outputs 0.
+ * T_p == 0 and T_k == 0 are allowed; a row without any key outputs 0, one with a
+ * NaN among its scores NaN.
  * Two launches (the prefix and, with more than one query row per K/V head, the
  * caches on the tensor cores, divided by key ranges into partial sums; their
  * merge, with the caches of single rows), and one before them that expands the

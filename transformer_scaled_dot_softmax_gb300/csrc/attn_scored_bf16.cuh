@@ -920,17 +920,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
             tc_fence_after_sync();
             const float M = fmaxf(ma, mb);
-            const float wa = la > 0.f ? ex2_approx(ma - M) : 0.f;
-            const float wb = lb > 0.f ? ex2_approx(mb - M) : 0.f;
+            // A sum of 0: no visible key.  One of NaN (a NaN or +infinity among
+            // the visible scores) goes on to o and lse.
+            const float wa = la != 0.f ? ex2_approx(ma - M) : 0.f;
+            const float wb = lb != 0.f ? ex2_approx(mb - M) : 0.f;
             const float L = la * wa + lb * wb;
-            const float inv = kMode == kDecode ? 1.f : L > 0.f ? 1.0f / L : 0.f;
+            const float inv = kMode == kDecode ? 1.f : L != 0.f ? 1.0f / L : 0.f;
             const float fa = wa * inv, fb = wb * inv;
             const long long prow = kMode == kDecode ? it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out : 0;
             if (row_ok) {
                 if (kMode == kDecode)
-                    p.part_ml[prow] = make_float2(L > 0.f ? M : -INFINITY, L);
+                    // (the reference of a NaN is as good as any, if the merge takes it)
+                    p.part_ml[prow] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
                 else if (kMode == kForwardLse)
-                    p.lse[w.out] = L > 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
+                    p.lse[w.out] = L != 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
             }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -948,8 +951,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a group without a visible key left its accumulator unwritten
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
-                    oa[c] = __float_as_uint((la > 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
-                                            (lb > 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
+                    oa[c] = __float_as_uint((la != 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
+                                            (lb != 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
                 if (kMode == kDecode) {
                     uint4 *d4 = reinterpret_cast<uint4 *>(p.part_o + prow * HD) + 8 * part;
 #pragma unroll

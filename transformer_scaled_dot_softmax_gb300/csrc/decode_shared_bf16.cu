@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
         smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 8));
         smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, 16));
         const float m_new = fmaxf(m, smax);
-        if (m_new == -INFINITY) continue;
+        // without a key to count, or with NaN alone, which has to reach the sums
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
         m = m_new;
         l *= alpha;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
         for (int c = 0; c < 8; ++c) acc[c] *= alpha;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const float w = ex2_approx(s[u] - m_new);
+            const float w = ex2_approx(s[u] - ref);
             l += w;
             float vf[8];
             bf16x8_to_f32(vu[u], vf);
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
             L += f * ml.y;
             O += f * p.part_o[(r * rows + row) * HD + c];
         }
-        p.o[row * HD + c] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+        p.o[row * HD + c] = __float2bfloat16_rn(L != 0.f ? O / L : 0.f);
     }
     // keep every CTA's shared memory alive until rank 0 has read it
     cluster_sync();
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_merge(const float *__restr
         }
     }
     if (row >= rows) return;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
     reinterpret_cast<uint32_t *>(o + row * HD)[lane] = pack_bf16x2(acc.x * inv, acc.y * inv);
 }
 
