@@ -355,7 +355,9 @@ mha_status sdpa_scored_forward(mha_dtype dt, const void *q, const void *k, const
  * Shapes as the forward's; the same mask, lengths and form.  dk, dv and dtable
  * are summed in a fixed order; dq adds key blocks by fp32 reductions in
  * global memory whose order is not fixed, as sdpa_backward does, so equal calls
- * may differ in dq's last bit.  workspace:
+ * may differ in dq's last bit.  P carries the rounding of an fp32 lse, a factor
+ * of e^(2^-22 |lse|) at most that a row's P share: of note where all keys that a
+ * query sees are so far, under slopes, that |lse| is past 10,000.  workspace:
  * >= sdpa_scored_backward_workspace_bytes() bytes, 256-byte aligned; one per
  * call in flight.  Three launches (row terms and what the form needs expanded;
  * the products, one CTA per SM taking blocks of 128 keys off a counter in the

@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     }
                                 }
                                 if (!all) mask_to(p.f.masked);
-                                add_bias<kBias, 1, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
+                                add_bias<kBias, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
                                 if (attempt == 1) {
                                     if (need) {
                                         float up = -INFINITY;  // above the reference

@@ -219,49 +219,71 @@ __device__ __forceinline__ void score_terms(uint32_t (&sv)[16], uint32_t (&dp)[1
             cap_scores(sv, f, __all_sync(0xffffffffu, big * big <= f.wide_max));
         }
     }
-    // mul tanh, before the bias comes to it
-    constexpr bool kKeep = kCap && kBias == kBiasSlopes;
-    uint32_t yt[kKeep ? 16 : 1];
-    if (kKeep) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) yt[kKeep ? e : 0] = sv[e];
-    }
     const uint64_t mul2 = f32x2_set(f.mul), one2 = f32x2_set(1.f), far2 = f32x2_set(far);
     const uint64_t inv2 = f32x2_set(kCap ? -1.f / (f.mul * f.mul) : 0.f);
-    if (kBias == kBiasSlopes) add_bias<kBiasSlopes, -1, kCap>(sv, f, br, d0, 0.f);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const float4 l4 = reinterpret_cast<const float4 *>(nlse2)[g];
-        const float4 d4 = reinterpret_cast<const float4 *>(dvec)[g];
-        const uint64_t nl[2] = {f32x2_pack(l4.x, l4.y), f32x2_pack(l4.z, l4.w)};
-        const uint64_t d[2] = {f32x2_pack(d4.x, d4.y), f32x2_pack(d4.z, d4.w)};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int e = 4 * g + 2 * i;
-            uint64_t y = at(sv, e);
-            if (kBias == kBiasBuckets) {
-                const uint64_t w2 = kNearPair ? f32x2_pack(window[-e], window[-e - 1]) : far2;
-                y = kCap ? add_f32x2(y, w2) : fma_f32x2(y, mul2, w2);
-            }
-            float x0, x1;
-            f32x2_unpack(kCap || kBias != kBiasNone ? add_f32x2(y, nl[i]) : fma_f32x2(y, mul2, nl[i]), x0, x1);
-            float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            if (!seen(e)) p0 = 0.f;
-            if (!seen(e + 1)) p1 = 0.f;
-            float ds0, ds1;
-            f32x2_unpack(mul_f32x2(f32x2_pack(p0, p1), sub_f32x2(at(dp, e), d[i])), ds0, ds1);
-            dp[e] = __float_as_uint(ds0);
-            dp[e + 1] = __float_as_uint(ds1);
-            if (kCap) {
-                // 1 - t^2, t = sv / mul
-                const uint64_t t2 = kKeep ? f32x2_pack(__uint_as_float(yt[kKeep ? e : 0]), __uint_as_float(yt[kKeep ? e + 1 : 0]))
-                                          : at(sv, e);
-                f32x2_unpack(mul_f32x2(f32x2_pack(ds0, ds1), fma_f32x2(mul_f32x2(t2, inv2), t2, one2)), ds0, ds1);
-            }
-            pk[2 * g + i] = pack_bf16x2(p0, p1);
-            dsk[2 * g + i] = pack_bf16x2(ds0, ds1);
-        }
+    // Slopes: -slope |d| and -lse, both large where only far keys are seen, meet
+    // in one fused multiply-add from the whole distance d, so that their
+    // difference loses nothing.  One sign of d for all of the warp's columns
+    // but where they straddle the diagonal.
+    bool one_sign = false;
+    uint64_t dist = 0, slope = 0;
+    const uint64_t minus2 = f32x2_set(-2.f);
+    if (kBias == kBiasSlopes) {
+        const bool past = f.past_only || __all_sync(0xffffffffu, d0 <= 0);
+        one_sign = past || __all_sync(0xffffffffu, d0 >= 15);
+        const float df = static_cast<float>(d0);
+        dist = f32x2_pack(df, df - 1.f);
+        slope = f32x2_set(past ? br.slope2 : -br.slope2);
     }
+    auto columns = [&](auto one) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 l4 = reinterpret_cast<const float4 *>(nlse2)[g];
+            const float4 d4 = reinterpret_cast<const float4 *>(dvec)[g];
+            const uint64_t nl[2] = {f32x2_pack(l4.x, l4.y), f32x2_pack(l4.z, l4.w)};
+            const uint64_t d[2] = {f32x2_pack(d4.x, d4.y), f32x2_pack(d4.z, d4.w)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = 4 * g + 2 * i;
+                uint64_t y = at(sv, e);
+                if (kBias == kBiasBuckets) {
+                    const uint64_t w2 = kNearPair ? f32x2_pack(window[-e], window[-e - 1]) : far2;
+                    y = kCap ? add_f32x2(y, w2) : fma_f32x2(y, mul2, w2);
+                }
+                uint64_t add = nl[i];
+                if (kBias == kBiasSlopes) {
+                    uint64_t away = dist;
+                    if (!decltype(one)::value) {
+                        float a0, a1;
+                        f32x2_unpack(dist, a0, a1);
+                        away = f32x2_pack(fabsf(a0), fabsf(a1));
+                    }
+                    add = fma_f32x2(away, slope, add);
+                    dist = add_f32x2(dist, minus2);
+                }
+                float x0, x1;
+                f32x2_unpack(kCap || kBias == kBiasBuckets ? add_f32x2(y, add) : fma_f32x2(y, mul2, add), x0, x1);
+                float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                if (!seen(e)) p0 = 0.f;
+                if (!seen(e + 1)) p1 = 0.f;
+                float ds0, ds1;
+                f32x2_unpack(mul_f32x2(f32x2_pack(p0, p1), sub_f32x2(at(dp, e), d[i])), ds0, ds1);
+                dp[e] = __float_as_uint(ds0);
+                dp[e + 1] = __float_as_uint(ds1);
+                if (kCap) {
+                    // 1 - t^2, t = sv / mul
+                    const uint64_t t2 = at(sv, e);
+                    f32x2_unpack(mul_f32x2(f32x2_pack(ds0, ds1), fma_f32x2(mul_f32x2(t2, inv2), t2, one2)), ds0, ds1);
+                }
+                pk[2 * g + i] = pack_bf16x2(p0, p1);
+                dsk[2 * g + i] = pack_bf16x2(ds0, ds1);
+            }
+        }
+    };
+    if (kBias != kBiasSlopes || one_sign)
+        columns(std::true_type{});
+    else
+        columns(std::false_type{});
 }
 
 template <bool kCap, int kBias>

@@ -142,13 +142,12 @@ __device__ __forceinline__ bool linear_bias(const ScoreParams &f, const BiasRow 
     return true;
 }
 
-// y = u mul + bias(d0 + kStep c) + add of N values in place, c = 0 .. N-1
-// (kScaled: u holds u mul already),
-// kStep = +1 (keys run along the registers) or -1 (queries do).  The lanes of
-// a warp hold one query (key) each with its own d0.  add: minus the reference
-// the weights are taken against; the bias's large part and `add` meet in one
-// fused multiply-add, so that far distances lose nothing to cancellation.
-template <int kBias, int kStep, bool kScaled, int N>
+// y = u mul + bias(d0 + c) + add of N values in place, c = 0 .. N-1 (kScaled: u
+// holds u mul already): keys run along the registers, the lanes of a warp hold
+// one query each with its own d0.  add: minus the reference the weights are
+// taken against; the bias's large part and `add` meet in one fused
+// multiply-add, so that far distances lose nothing to cancellation.
+template <int kBias, bool kScaled, int N>
 __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f, const BiasRow &r, int d0,
                                          float add) {
     const uint64_t mul2 = f32x2_set(f.mul);
@@ -163,22 +162,20 @@ __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f,
         u[c] = __float_as_uint(a);
         u[c + 1] = __float_as_uint(b);
     };
-    constexpr int kEnd = kStep * (N - 1);
     if (kBias == kBiasNone) {
         const uint64_t add2 = f32x2_set(add);
 #pragma unroll
         for (int c = 0; c < N; c += 2) put(c, fma2(at(c), add2));
     } else if (kBias == kBiasSlopes) {
-        const int dmin = kStep > 0 ? d0 : d0 + kEnd, dmax = kStep > 0 ? d0 + kEnd : d0;
-        const bool past = __all_sync(0xffffffffu, dmax <= 0 || f.past_only);
-        if (past || __all_sync(0xffffffffu, dmin >= 0)) {
+        const bool past = __all_sync(0xffffffffu, d0 + N - 1 <= 0 || f.past_only);
+        if (past || __all_sync(0xffffffffu, d0 >= 0)) {
             // one sign for all: the bias is an arithmetic progression
             const float sl = past ? r.slope2 : -r.slope2;
-            const float b0 = fmaf(sl, static_cast<float>(d0), add), st = kStep * sl;
+            const float b0 = fmaf(sl, static_cast<float>(d0), add);
             uint64_t b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) b[i] = f32x2_pack(fmaf(2.f * i, st, b0), fmaf(2.f * i + 1.f, st, b0));
-            const uint64_t step = f32x2_set(8.f * st);
+            for (int i = 0; i < 4; ++i) b[i] = f32x2_pack(fmaf(2.f * i, sl, b0), fmaf(2.f * i + 1.f, sl, b0));
+            const uint64_t step = f32x2_set(8.f * sl);
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
                 put(c, fma2(at(c), b[(c >> 1) & 3]));
@@ -188,21 +185,20 @@ __device__ __forceinline__ void add_bias(uint32_t (&u)[N], const ScoreParams &f,
             const float df = static_cast<float>(d0);
 #pragma unroll
             for (int c = 0; c < N; ++c)
-                u[c] = fma1(u[c], fmaf(-r.slope2, fabsf(df + static_cast<float>(kStep * c)), add));
+                u[c] = fma1(u[c], fmaf(-r.slope2, fabsf(df + static_cast<float>(c)), add));
         }
     } else {
-        const int dmin = kStep > 0 ? d0 : d0 + kEnd, dmax = kStep > 0 ? d0 + kEnd : d0;
-        const bool past = __all_sync(0xffffffffu, dmax <= -f.far);
-        if (past || __all_sync(0xffffffffu, dmin >= f.far)) {
+        const bool past = __all_sync(0xffffffffu, d0 + N - 1 <= -f.far);
+        if (past || __all_sync(0xffffffffu, d0 >= f.far)) {
             const uint64_t add2 = f32x2_set((past ? r.past : r.future) + add);
 #pragma unroll
             for (int c = 0; c < N; c += 2) put(c, fma2(at(c), add2));
         } else {
-            const int dc = kStep > 0 ? min(max(d0, -f.mid), f.far) : min(max(d0, -f.far), f.mid);
+            const int dc = min(max(d0, -f.mid), f.far);
             const float *src = r.vec + dc;
 #pragma unroll
             for (int c = 0; c < N; ++c)
-                u[c] = fma1(u[c], src[kStep * c] + add);
+                u[c] = fma1(u[c], src[c] + add);
         }
     }
 }
