@@ -235,14 +235,17 @@ __device__ __forceinline__ int tile_of(const Item &it, int t) {
 }
 
 // The CTA's t-th item, in shared memory (read there when needed rather than
-// held in registers); past the table each warp computes its own.
+// held in registers); past the table each warp computes its own, once all of
+// its lanes that take part (`lanes`) are done with the one before: items without
+// a key tile pass no other barrier.
 template <int kMode>
-__device__ __forceinline__ const Item &item_of(Smem &sm, const ScoredFwdParams &p, int t, int cta, int G) {
+__device__ __forceinline__ const Item &item_of(Smem &sm, const ScoredFwdParams &p, int t, int cta, int G,
+                                               unsigned lanes = 0xffffffffu) {
     if (t < kItemTable) return sm.item_tab[t];
     Item &own = sm.item_own[threadIdx.x >> 5];
-    __syncwarp(__activemask());
+    __syncwarp(lanes);
     own = make_item<kMode>(p, item_index(t, cta, G), sorted<kMode>(p) ? sm.order : nullptr);  // every lane writes the same
-    __syncwarp(__activemask());
+    __syncwarp(lanes);
     return own;
 }
 
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 0, v = 0;  // key tiles and items so far
             bool ok = true;
             for (int t = 0; ok && t < sm.n_items; ++t) {
-                const Item &it = item_of<kMode>(sm, p, t, cta, G);
+                const Item &it = item_of<kMode>(sm, p, t, cta, G, 1u);
                 if (it.n_kv == 0) continue;
                 const int qbuf = v & 1;
                 const bool cache = kMode == kDecode && it.split >= p.splits;
