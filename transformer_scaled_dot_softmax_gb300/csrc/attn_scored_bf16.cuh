@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         auto keep = [&](uint32_t col) -> bool {
                             if (kCap && kMode == kDecode && !w.live) big = 0.f;
                             if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : p.f.wide_max))) {
-                                tier = tier == 0 && p.f.wide_max != 0.f ? 1 : 2;  // taken again below
+                                ++tier;  // out of the polynomial's range: taken again below
                                 return false;
                             }
                             const bool first = m_run == -INFINITY;

@@ -122,7 +122,6 @@ enum BiasKind { kBiasNone = 0, kBiasSlopes = 1, kBiasBuckets = 2 };
 struct ScoreParams {
     float cap_in;         // scale / cap (capped scores), else unused
     float mul;            // y = u mul + bias, u = q.k or tanh(q.k cap_in), y in log2 units; never 0
-    float lin;            // scale in log2 units: a capped score's y far below the cap is s lin, s = q.k
     // Capped scores with |q.k cap_in| <= 0.5: y = s (near[0] + near[1] s^2 +
     // near[2] s^4), s = q.k; s^2 <= near_max (less than that of 0.5 where the
     // fit's error would show; 0: unused, all coefficients 0).  With
@@ -130,6 +129,10 @@ struct ScoreParams {
     float near[3], near_max;
     float wide[7], wide_max;
     float masked;         // the u of a masked score: minus infinity times the sign of mul
+    // scale in log2 units: a capped score's y far below the cap is s lin, s = q.k.
+    // (Behind the others: ahead of them it moved the coefficients off their
+    // 8-byte pairs, and capped slopes took 484 us instead of 470.)
+    float lin;
     const float *slopes;  // (H) fp32, kBiasSlopes
     // kBiasBuckets, written by the preparing launch for distances -mid .. mid:
     const float *vec;     // (H, vec_stride(mid)) the bias, in log2 units
