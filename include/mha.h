@@ -287,6 +287,9 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  *   table           DEVICE bf16 (num_buckets, h), or (2 num_buckets, h) with
  *                   `bidirectional`: bias_h(d) = table[bucket(d), h], a learned
  *                   relative position bias.  At most one of slopes and table.
+ *                   -infinity, or less than -2.3e38 (the type's lowest), gives a
+ *                   bucket's keys no weight; a query with no other key outputs
+ *                   0, as one that sees none.
  *   bucket_starts   HOST int32 (num_buckets), read during the call: the first
  *                   distance of each bucket, [0] = 0, strictly ascending, the
  *                   last at most 65536.  bucket(d) = the largest u with
