@@ -1,4 +1,4 @@
-"""The scored attention's tests of caps, NaN, far keys, many items and edges under device-side bounds checks, as
+"""The scored attention's tests of NaN, far keys, many items and edges under device-side bounds checks, as
 test_gpu_scored_bounds_checked.py runs the others."""
 import os
 import re

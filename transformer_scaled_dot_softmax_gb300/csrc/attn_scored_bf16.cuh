@@ -41,16 +41,19 @@
 //     multiplied by their zero weights, so that what a padded buffer holds
 //     there (NaN included) never reaches the output.
 //
-// Bound: like attn_bf16.cu by the softmax warps, not by the tensor cores: the
-// weights take 128 x 128 / 16 = 1,024 special-function cycles per tile
-// against 512 of tensor-core time, and the cap adds 8 issue slots per pair.
+// Bound: like attn_bf16.cu by the softmax warps' instruction stream, not by a
+// pipe: a tile takes about 1,200 cycles, of which its weights need 512 of the
+// special-function unit (32 a cycle: 45 % busy) and its products 512 of the
+// tensor cores; the cap adds 8 issue slots per pair, on the FMA pipe (41 % busy).
 // Two warps share a scheduler and issue in 52 to 63 of 100 cycles, waiting for
-// tensor memory in most others; the tensor cores are 28 to 45 % busy.
+// tensor memory in most others.
 //
 // Measured, 2 x 16 heads x 8,192, causal, without / with the log-sum-exp:
-// 254 / 347 us (1,082 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
-// 413 / 515, slopes 310 / 409, 32 buckets 291 / 382, cap 20 with scores in the
-// wide range 620 / 809, 12 documents 98 / 113 (capped 155 with).  Per item of
+// 254 / 350 us (1,082 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
+// 410 / 506, slopes 310 / 411, both 468 / 608, 32 buckets 292 / 392, cap 20 under
+// scores of deviation 4 (some in the wide range) 555 / 670, cap 1,000 under scores
+// of deviation 6 (most warps past the polynomials) 722 / 905, 12 documents 97 / 115
+// (capped 130 / 151).  Per item of
 // 128 rows about 2.5 us (3.5 with the log-sum-exp) and 0.5 to 0.6 (0.7) per key tile;
 // a tile seen in part costs two to three whole ones, which is what documents
 // and short sequences are bound by.

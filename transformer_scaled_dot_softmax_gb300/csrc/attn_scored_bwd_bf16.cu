@@ -42,8 +42,8 @@
 // Bound: like attn_bwd_main by the score warps, 16 of them on 96 registers,
 // issuing in 47 to 56 of 100 cycles and waiting for tensor memory and for one
 // another in the others; the tensor cores are 28 to 35 % busy.  Measured, 2 x
-// 16 heads x 8,192, causal, all launches: plain 807 us (851 TFLOP/s), slopes
-// 844, 32 buckets 993, cap 50 946, 12 documents 209; 16 x 8 heads x 512,
+// 16 heads x 8,192, causal, all launches: plain 806 us (852 TFLOP/s), slopes
+// 843, 32 buckets 991, cap 50 947, both 1,030, 12 documents 208; 16 x 8 heads x 512,
 // all keys: plain 53, slopes 56, buckets 71.  Of that the launches before and
 // after take what their bytes do (at 8,192: 100 MB read and 67 written, 67
 // read and 34 written).

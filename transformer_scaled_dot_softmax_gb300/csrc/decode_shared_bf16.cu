@@ -14,12 +14,17 @@
 // one's, while on the SIMT cores a key costs little more than its 256 bytes
 // (caches of up to 1,024 keys, 64 x 16 heads: 28 us against 54; with two rows
 // per K/V head 45 against 36, the other way round).  Where the lengths of the
-// batch fit the CTA's threads, CTAs take them longest first (prefix 8,192 and
-// caches of random lengths up to 1,024, 64 x 16: 51.5 -> 45 us, without prefix
-// 29 -> 27; of equal lengths of 1,024, with prefix, 60 -> 70).  8 lanes read one 128-byte
-// key row, a warp 4 consecutive rows per load, 6 rows per lane group in flight
-// (as decode_bf16.cu); a CTA, or a cluster of them that splits the keys, serves
-// one head of one batch entry.
+// batch fit the CTA's threads, CTAs take them longest first, and where each has a
+// long cache to itself four of them share an SM.  Both, with the limit alone, with
+// the order alone, with neither (64 x 16 heads, caches to 1,024, us):
+//   random lengths, prefix 8,192  42.5  51.2  45.3  50.3    none  26.4  30.8  27.1  28.6
+//   all of 1,024, prefix 8,192    72.8  71.6  70.8  69.0    none  49.3  48.2  50.6  49.5
+// (lengths are on the device: no rule on the host can look at them).  The order's
+// own registers, 96 where the kernel without it took 80, leave five CTAs an SM
+// instead of six: behind a prefix full caches took 60 us then, without one 54.
+// 8 lanes read one 128-byte key row, a warp 4 consecutive rows per load, 6 rows per
+// lane group in flight (as decode_bf16.cu); a CTA, or a cluster of them that splits
+// the keys, serves one head of one batch entry.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -230,9 +235,9 @@ __global__ void __launch_bounds__(kRowThreads) decode_row_kernel(const __grid_co
 template <int kBias>
 cudaError_t launch_row(const DecodeRowParams &p, int cluster, cudaStream_t stream) {
     // Four CTAs on an SM at a time (by their shared memory) where each has a long
-    // cache to itself: those that start later even out what the first had (64 x
-    // 16 heads, prefix 8,192, caches to 1,024: 42 us, seven at a time 45; 128 x 8,
-    // caches to 512: 29 and 27).
+    // cache to itself: those that start later even out what the first had (figures
+    // at the top; 40 x 16, all of 1,000 behind 4,096: 41 us against 45 with five,
+    // 200 x 16: 158 against 154; 128 x 8, caches to 512: 29 and 27).
     const size_t smem = cluster == 1 && p.Tk > 512 ? 46 * 1024 : 0;
     return launch_kernel(decode_row_kernel<kBias>, dim3(static_cast<unsigned>(p.B * p.H * cluster)), dim3(kRowThreads), smem,
                          stream, p.prefix_splits > 0, static_cast<unsigned>(cluster), p);
