@@ -25,7 +25,8 @@
  *
  * Conventions shared by every entry point:
  *   - All tensor pointers are DEVICE pointers to caller-owned memory,
- *     row-major and contiguous (sdpa_forward_host alone takes host tensors).
+ *     row-major and contiguous (sdpa_forward_host alone takes host tensors, the
+ *     paged calls strides).
  *     The library never allocates device memory, frees or synchronises
  *     (sdpa_forward_host keeps two copy streams and a few events per device);
  *     every launch is enqueued on `stream` (0 = legacy default stream) and the
@@ -77,7 +78,7 @@ typedef enum {
     MHA_MASK_CAUSAL_KEY_PADDING = 3
 } mha_mask;
 
-typedef enum { MHA_F32 = 0, MHA_BF16 = 1 } mha_dtype;
+typedef enum { MHA_F32 = 0, MHA_BF16 = 1, MHA_INT8 = 2 /* paged caches only */ } mha_dtype;
 
 /*
  * Scaled dot-product attention, o = softmax(scale * q k^T + mask) v.
@@ -406,6 +407,100 @@ mha_status sdpa_decode_shared_forward(const void *q, const void *k_prefix, const
                                       float scale, mha_mask mask, const int32_t *cache_lens,
                                       const mha_score_form *form, int *status_dev,
                                       cudaStream_t stream);
+
+/*
+ * A paged K/V cache: the cached rows of B sequences in pages of a common pool.
+ *
+ *   k_pages, v_pages  DEVICE (num_pages, h_kv, page_rows, 64), `dtype` MHA_BF16 or
+ *                     MHA_INT8, page_stride elements from one page to the next (at
+ *                     least h_kv page_rows 64, a multiple of 16; inside a page
+ *                     contiguous), 16-byte aligned.  page_rows is a multiple of 16, up
+ *                     to 65536; h_kv page_rows is at most 2^24.
+ *   k_scales, v_scales  MHA_INT8: DEVICE uint8 (num_pages, h_kv, page_rows),
+ *                     contiguous, 16-byte aligned: a row's exponent + 127.
+ *   page_table        DEVICE int32 (B, max_pages): row j of sequence b is row
+ *                     j % page_rows of page page_table[b, j / page_rows].  An entry
+ *                     outside [0, num_pages) is a page that is not there: its keys
+ *                     are not seen, new rows for it are dropped, it reads as zeros.
+ *                     Entries past a sequence's length are not used.  Sequences may
+ *                     share pages that no call writes.
+ *   row_starts        DEVICE int32 (B + 1), for calls with new rows: sequence b's n_b
+ *                     new tokens are the packed rows row_starts[b] ..
+ *                     row_starts[b + 1] - 1 (ascending; clamped to [0, N]; a
+ *                     sequence may have none).  Rows that belong to no sequence are
+ *                     neither read nor written.
+ *   seq_lens          DEVICE int32 (B): cached rows L_b, the new ones, which are the
+ *                     last n_b, among them; clamped to [0, max_pages page_rows].  New
+ *                     token t is at position L_b - n_b + t (below 0: it is dropped
+ *                     by the append, and sees no key under a causal mask).
+ *
+ * The pages hold heads of 64 features (other d: MHA_ERR_UNSUPPORTED).
+ * max_pages page_rows < 2^30; B, h_kv <= 65535; page_stride < 2^38.
+ *
+ * MHA_INT8 keeps a row x of 64 as n_i = rint(x_i 2^-e) (ties to even) and the least
+ * e from -126 up with max |x_i| <= 127 2^e, stored as e + 127; a row with a NaN or
+ * an infinity as zeros and 255, which reads as NaN.  The values n_i 2^e are
+ * bf16 numbers, off by at most 2^(e-1) < max |x_i| / 127 (the largest finite
+ * numbers, 255 2^120, are kept as 63 2^122 instead of 2^128): attention over such
+ * a cache is attention over the rows that paged_cache_read returns.
+ */
+typedef struct {
+    mha_dtype dtype;
+    void *k_pages, *v_pages;
+    long long page_stride;
+    uint8_t *k_scales, *v_scales;
+    const int32_t *page_table;
+    const int32_t *row_starts;
+    const int32_t *seq_lens;
+    int B, h_kv, page_rows, num_pages, max_pages;
+} mha_paged_cache;
+
+/*
+ * Writes new rows into their pages.  k, v (h_kv, N, 64) bf16, packed, at strides (in
+ * elements, multiples of 8, at least 64) of the heads and of the tokens: a
+ * projection's output is taken as it is, head by head or token by token.
+ * 16-byte aligned.  Two rows for the same place (sequences that share the page)
+ * leave one of them or a mixture.  One launch, no workspace.
+ */
+mha_status paged_cache_append(const mha_paged_cache *cache, const void *k, long long k_stride_h,
+                              long long k_stride_t, const void *v, long long v_stride_h,
+                              long long v_stride_t, int N, int d, cudaStream_t stream);
+
+/*
+ * Reads rows 0 .. T - 1 of every sequence back, k, v (B, h_kv, T, 64) bf16,
+ * contiguous, 16-byte aligned: the layout of the calls above.  Rows at or past the
+ * length are zeros.  row_starts is not used.  One launch.
+ */
+mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int T, int d,
+                            cudaStream_t stream);
+
+/*
+ * Attention of every sequence's new tokens over its cached rows (their own, already
+ * appended, among them):
+ *   o = softmax(scale * q k^T + mask) v
+ * over the L_b rows of the sequence, or with a causal mask over those up to the
+ * token's own position.  Chunks of any length and single tokens may be mixed.
+ *   q, o (h, N, 64) bf16, packed, at strides as in paged_cache_append; h a
+ *   multiple of h_kv, h / h_kv <= 128; N h < 2^30.  16-byte aligned.
+ *   max_new: no sequence has more new tokens (a bound: what a batch of single tokens
+ *   does not launch depends on it).  Tokens past it are left out.
+ *   A token that sees no key outputs 0, one with a NaN or positive infinity among
+ *   its scores NaN.  Rows past L_b may hold anything; a NaN or infinity among a
+ *   sequence's own values may reach all its outputs.  Entries of k and v up to
+ *   2^46 in magnitude.
+ *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
+ *   in flight.
+ * Two launches (sequences with up to 64 query rows per K/V head; joining of the
+ * partial sums of divided key ranges), and a third between them when max_new
+ * allows more: tcgen05 products over tiles of 128 rows.  A call's results do not depend
+ * on timing (equal calls give equal bits).
+ */
+size_t sdpa_paged_workspace_bytes(int B, int h, int h_kv, int N, int max_new);
+mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
+                              long long q_stride_t, void *o, long long o_stride_h,
+                              long long o_stride_t, void *workspace, size_t workspace_bytes, int h,
+                              int N, int max_new, int d, float scale, mha_mask mask,
+                              int *status_dev, cudaStream_t stream);
 
 /*
  * Bytes of device workspace mha_forward needs: the projected Q, K, V in

@@ -21,14 +21,15 @@ import functools
 import math
 
 from . import _native
-from ._native import (MHA_BF16, MHA_F32, MHA_MASK_CAUSAL, MHA_MASK_CAUSAL_KEY_PADDING,
+from ._native import (MHA_BF16, MHA_F32, MHA_INT8, MHA_MASK_CAUSAL, MHA_MASK_CAUSAL_KEY_PADDING,
                       MHA_MASK_KEY_PADDING, MHA_MASK_NONE, MHA_OK, lib)
 
 __all__ = ["sdpa_forward", "sdpa_forward_lse", "sdpa_forward_host", "sdpa_forward_host_workspace_bytes",
            "sdpa_bf16_key_split", "sdpa_backward", "positional_encoding_add",
            "encoder_layer_forward", "ENCODER_PARAMS", "sdpa_decode_forward",
            "sdpa_scored_forward", "sdpa_scored_forward_lse", "sdpa_scored_backward",
-           "sdpa_decode_shared_forward", "relative_bucket_starts", "mha_forward",
+           "sdpa_decode_shared_forward", "relative_bucket_starts", "paged_cache_append",
+           "paged_cache_read", "sdpa_paged_forward", "mha_forward",
            "mha_forward_add_layernorm", "mha_workspace_bytes", "status_string", "MhaError", "MASKS", "lib"]
 
 MASKS = {"none": MHA_MASK_NONE, "causal": MHA_MASK_CAUSAL, "key_padding": MHA_MASK_KEY_PADDING,
@@ -576,6 +577,150 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
                                         _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "sdpa_decode_shared_forward")
+    return out
+
+
+# ------------------------------------------------------------------ paged K/V cache
+def _packed(torch, name, t, heads, n, d, device):
+    """(pointer, head stride, row stride) of bf16 rows t (heads, n, d), whose last
+    dimension alone has to be contiguous."""
+    try:
+        shape, strides, fine = t.shape, t.stride(), t.dtype is torch.bfloat16 and t.get_device() == device
+    except AttributeError:
+        raise ValueError("%s must be a CUDA tensor" % name) from None
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if not fine:
+        raise ValueError("%s must be bfloat16, on cuda:%d, the current device" % (name, device))
+    if shape != (heads, n, d):
+        raise ValueError("%s must have the shape %s" % (name, (heads, n, d)))
+    if strides[2] != 1 and d > 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    return t.data_ptr(), strides[0], strides[1]
+
+
+def _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales):
+    """Checked (PagedCache, head size, device index)."""
+    device = torch.cuda.current_device()
+    try:
+        pages, h_kv, rows, d = shape = k_pages.shape
+        strides, dtype = k_pages.stride(), k_pages.dtype
+        B, max_pages = page_table.shape
+    except (AttributeError, ValueError):
+        raise ValueError("k_pages must be a tensor of four dimensions, page_table one of two") from None
+    if dtype is not torch.bfloat16 and dtype is not torch.int8:
+        raise ValueError("k_pages must be bfloat16 or int8")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
+            raise ValueError("%s must be a tensor on cuda:%d, the current device" % (name, device))
+        if t.dtype is not dtype or t.shape != shape or t.stride() != strides:
+            raise ValueError("v_pages must have k_pages' dtype, shape and strides")
+    if pages and (strides[3] != 1 or strides[2] != d or (h_kv > 1 and strides[1] != rows * d)):
+        raise ValueError("a page must be contiguous")
+    c = _native.PagedCache()
+    c.dtype = MHA_BF16
+    if dtype is torch.int8:
+        if k_scales is None or v_scales is None:
+            raise ValueError("int8 pages need k_scales and v_scales")
+        _require(("k_scales", "v_scales"), (k_scales, v_scales), torch.uint8, (pages, h_kv, rows), device)
+        c.dtype, c.k_scales, c.v_scales = MHA_INT8, k_scales.data_ptr(), v_scales.data_ptr()
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("k_scales and v_scales go with int8 pages")
+    _require(("page_table",), (page_table,), torch.int32, (B, max_pages), device)
+    if seq_lens is None:
+        raise ValueError("seq_lens must be a tensor")
+    _require(("seq_lens",), (seq_lens,), torch.int32, (B,), device)
+    if row_starts is not None:
+        _require(("row_starts",), (row_starts,), torch.int32, (B + 1,), device)
+        c.row_starts = row_starts.data_ptr()
+    c.k_pages, c.v_pages, c.page_stride = k_pages.data_ptr(), v_pages.data_ptr(), strides[0]
+    c.page_table, c.seq_lens = page_table.data_ptr(), seq_lens.data_ptr()
+    c.B, c.h_kv, c.page_rows, c.num_pages, c.max_pages = B, h_kv, rows, pages, max_pages
+    return c, d, device
+
+
+def _needs_starts(row_starts):
+    if row_starts is None:
+        raise ValueError("row_starts must be a tensor")
+
+
+def paged_cache_append(k, v, k_pages, v_pages, page_table, row_starts, seq_lens, *, k_scales=None,
+                       v_scales=None, stream=None):
+    """Writes new rows into a paged K/V cache.  k, v (h_kv, N, 64) bf16, any strides
+    of heads and tokens: packed tokens, row_starts[b] .. row_starts[b + 1] - 1
+    (int32 (B + 1)) of sequence b, the last of its seq_lens[b] (int32 (B)) cached
+    rows.  Row j of a sequence lies in page page_table[b, j // P] (int32 (B,
+    max_pages); an entry outside the pool: the row is dropped), at row j % P of
+    it.  k_pages, v_pages (pages, h_kv, P, 64), P a multiple of 16, bf16; or int8
+    with k_scales, v_scales (pages, h_kv, P) uint8: a row's values are n 2^(scale
+    - 127).  Returns (k_pages, v_pages)."""
+    torch = _torch()
+    _needs_starts(row_starts)
+    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
+    try:
+        n = k.shape[1]
+    except (AttributeError, IndexError):
+        raise ValueError("k must be a tensor of three dimensions") from None
+    kp = _packed(torch, "k", k, cache.h_kv, n, d, dev)
+    vp = _packed(torch, "v", v, cache.h_kv, n, d, dev)
+    rc = lib.paged_cache_append(ctypes.addressof(cache), *kp, *vp, n, d, _stream_on(stream, dev))
+    if rc != MHA_OK:
+        raise MhaError(rc, "paged_cache_append")
+    return k_pages, v_pages
+
+
+def paged_cache_read(k_pages, v_pages, page_table, seq_lens, k=None, v=None, *, rows=None, k_scales=None,
+                     v_scales=None, stream=None):
+    """The cached rows of every sequence as contiguous bf16 tensors k, v (B, h_kv,
+    rows, 64), as the other calls take them; zeros from seq_lens[b] on.  rows:
+    those of k, else as many as the page table has.  Returns (k, v)."""
+    torch = _torch()
+    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, None, seq_lens, k_scales, v_scales)
+    if rows is None:
+        rows = cache.max_pages * cache.page_rows if k is None else k.shape[2]
+    shape = (cache.B, cache.h_kv, rows, d)
+    if k is None:
+        k = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
+    _require(("k", "v"), (k, v), torch.bfloat16, shape, dev)
+    rc = lib.paged_cache_read(ctypes.addressof(cache), k.data_ptr(), v.data_ptr(), rows, d, _stream_on(stream, dev))
+    if rc != MHA_OK:
+        raise MhaError(rc, "paged_cache_read")
+    return k, v
+
+
+def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, out=None, workspace=None, *,
+                       max_new=None, scale=None, mask="none", k_scales=None, v_scales=None, status=None,
+                       stream=None):
+    """Attention of every sequence's new tokens over its cached rows, which hold
+    the tokens' own already (paged_cache_append, which describes the cache).  q
+    (h, N, 64) bf16, packed like its k, any strides of heads and tokens; h a multiple of
+    h_kv.  With a causal mask a token sees the rows up to its own, else all of
+    its sequence's.  max_new: the most new tokens of a sequence (N if not given);
+    calls for single tokens are faster with it.  Returns out (h, N, 64), whose rows
+    past the last sequence's are not written."""
+    torch = _torch()
+    _needs_starts(row_starts)
+    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
+    try:
+        h, n, _ = q.shape
+    except (AttributeError, ValueError):
+        raise ValueError("q must be a tensor of three dimensions") from None
+    qp = _packed(torch, "q", q, h, n, d, dev)
+    if out is None:
+        out = _result(stream, torch.empty_like, q)
+    op = _packed(torch, "out", out, h, n, d, dev)
+    if status is not None:
+        _check_dev("status", status, torch.int32)
+    max_new = n if max_new is None else max_new
+    need = lib.sdpa_paged_workspace_bytes(cache.B, h, cache.h_kv, n, max_new)
+    workspace, size = _scratch_here(torch, workspace, need, dev, stream)
+    rc = lib.sdpa_paged_forward(ctypes.addressof(cache), *qp, *op, workspace.data_ptr(), size, h, n, max_new, d,
+                                1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask), _ptr(status),
+                                _stream_on(stream, dev))
+    if rc != MHA_OK:
+        raise MhaError(rc, "sdpa_paged_forward")
     return out
 
 

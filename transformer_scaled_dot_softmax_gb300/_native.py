@@ -14,7 +14,7 @@ LIB_PATH = os.environ.get("MHA_LIBRARY") or os.path.join(_HERE, "_build", "libmh
 
 MHA_OK, MHA_ERR_INVALID_ARG, MHA_ERR_UNSUPPORTED, MHA_ERR_WORKSPACE = 0, 1, 2, 3
 MHA_ERR_MISALIGNED, MHA_ERR_CUDA, MHA_ERR_TIMEOUT, MHA_ERR_BOUNDS = 4, 5, 6, 7
-MHA_F32, MHA_BF16 = 0, 1
+MHA_F32, MHA_BF16, MHA_INT8 = 0, 1, 2
 MHA_STATIC_WORKSPACE_BYTES = 32 << 20
 MHA_MASK_NONE, MHA_MASK_CAUSAL, MHA_MASK_KEY_PADDING, MHA_MASK_CAUSAL_KEY_PADDING = 0, 1, 2, 3
 
@@ -28,8 +28,19 @@ class ScoreForm(ctypes.Structure):
                 ("doc_ids", ctypes.c_void_p)]
 
 
+class PagedCache(ctypes.Structure):
+    """mha_paged_cache of include/mha.h."""
+    _fields_ = [("dtype", ctypes.c_int), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("row_starts", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("h_kv", ctypes.c_int), ("page_rows", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int)]
+
+
 # Every symbol include/mha.h declares, with its ctypes signature.
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "sdpa_forward": (_ci, [_ci, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _ci, _cf, _ci, _vp,
                            _vp, _vp]),
@@ -59,6 +70,11 @@ SIGNATURES = {
     "sdpa_decode_shared_workspace_bytes": (_sz, [_ci] * 6 + [_vp]),
     "sdpa_decode_shared_forward": (_ci, [_vp] * 7 + [_sz] + [_ci] * 8 +
                                    [_cf, _ci, _vp, _vp, _vp, _vp]),
+    "paged_cache_append": (_ci, [_vp, _vp, _ll, _ll, _vp, _ll, _ll, _ci, _ci, _vp]),
+    "paged_cache_read": (_ci, [_vp, _vp, _vp, _ci, _ci, _vp]),
+    "sdpa_paged_workspace_bytes": (_sz, [_ci] * 5),
+    "sdpa_paged_forward": (_ci, [_vp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _sz, _ci, _ci, _ci, _ci,
+                                 _cf, _ci, _vp, _vp]),
     "mha_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),
     "mha_forward": (_ci, [_ci, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _ci, _ci, _ci, _ci,
                           _ci, _ci, _ci, _cf, _ci, _vp, _vp, _vp]),

@@ -49,10 +49,10 @@ mha_status cuda_fail(const char *what, const char *detail) {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// bf16 tensor map with 128-byte swizzling.  dims/strides are innermost first;
-// strides are in bytes for dims 1..rank-1.
-mha_status encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
-                       const uint64_t *strides_bytes, const uint32_t *box) {
+// Tensor map: bf16 with 128-byte swizzling, or bytes without.  dims/strides are
+// innermost first; strides are in bytes for dims 1..rank-1.
+mha_status encode_tiled(CUtensorMap *m, const void *base, bool bytes, int rank, const uint64_t *dims,
+                        const uint64_t *strides_bytes, const uint32_t *box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cuda_fail("cuTensorMapEncodeTiled", "driver entry point not found");
     cuuint64_t d[5], s[4];
@@ -63,9 +63,11 @@ mha_status encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_
         es[i] = 1;
         if (i + 1 < rank) s[i] = strides_bytes[i];
     }
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
-                    const_cast<void *>(base), d, s, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, bx, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char buf[96];
@@ -75,6 +77,11 @@ mha_status encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_
         return cuda_fail("cuTensorMapEncodeTiled", buf);
     }
     return MHA_OK;
+}
+
+mha_status encode_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+                       const uint64_t *strides_bytes, const uint32_t *box) {
+    return encode_tiled(m, base, false, rank, dims, strides_bytes, box);
 }
 
 // (B*H, T, 64) head-split bf16 tensor, 128-row boxes.
@@ -211,6 +218,24 @@ mha_status encode_stacked_rows_map(CUtensorMap *m, const void *base, int B, int 
     const uint64_t strides[3] = {row, static_cast<uint64_t>(Hkv) * rows * row, static_cast<uint64_t>(rows) * row};
     const uint32_t box[4] = {kAttnHeadDim, static_cast<uint32_t>(dr.per), static_cast<uint32_t>(dr.nb), 1};
     return encode_bf16(m, base, 4, dims, strides, box);
+}
+mha_status encode_paged_maps(PagedMaps *m, const PagedAttnParams &p) {
+    const uint64_t hd = kAttnHeadDim;
+    const int g = p.H / p.c.Hkv;
+    const uint64_t qd[3] = {hd, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.c.N)};
+    const uint64_t qs[2] = {static_cast<uint64_t>(p.q.stride_h) * 2, static_cast<uint64_t>(p.q.stride_t) * 2};
+    const uint32_t qb[3] = {kAttnHeadDim, static_cast<uint32_t>(g), static_cast<uint32_t>(paged_tile_tokens(g))};
+    mha_status s = encode_bf16(&m->q, p.q.x, 3, qd, qs, qb);
+    if (s != MHA_OK) return s;
+    // an empty pool is described by a page that is never loaded
+    const bool none = p.c.num_pages == 0;
+    const uint64_t row = hd * (p.c.int8 ? 1 : 2);
+    const uint64_t d[4] = {hd, static_cast<uint64_t>(p.c.page), static_cast<uint64_t>(p.c.Hkv),
+                           static_cast<uint64_t>(none ? 1 : p.c.num_pages)};
+    const uint64_t st[3] = {row, row * p.c.page, static_cast<uint64_t>(p.c.stride) * (p.c.int8 ? 1 : 2)};
+    const uint32_t b[4] = {kAttnHeadDim, static_cast<uint32_t>(std::min(p.c.page & -p.c.page, 128)), 1, 1};
+    if ((s = encode_tiled(&m->k, none ? p.q.x : p.c.k, p.c.int8 != 0, 4, d, st, b)) != MHA_OK) return s;
+    return encode_tiled(&m->v, none ? p.q.x : p.c.v, p.c.int8 != 0, 4, d, st, b);
 }
 }  // namespace mha
 

@@ -1,0 +1,207 @@
+// api_paged.cu -- the paged K/V cache entry points of include/mha.h: argument
+// checks, workspace layout and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/mha.h"
+#include "kernels.h"
+
+#define MHA_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace mha;
+
+constexpr int kMostPageRows = 1 << 16;
+constexpr long long kMostRows = 1ll << 30;  // of a sequence
+constexpr long long kMostLine = 1ll << 31;  // units of the kernels' work lines
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+mha_status launched(cudaError_t e, const char *what) {
+    return e == cudaSuccess ? MHA_OK : record_cuda_failure(what, cudaGetErrorName(e));
+}
+
+// `rows`: the call takes packed rows (row_starts).
+mha_status check_cache(const mha_paged_cache *x, int d, bool rows, int N, PagedCache &c) {
+    if (!x) return MHA_ERR_INVALID_ARG;
+    if (x->dtype != MHA_BF16 && x->dtype != MHA_INT8)
+        return x->dtype == MHA_F32 ? MHA_ERR_UNSUPPORTED : MHA_ERR_INVALID_ARG;
+    if (x->B < 0 || x->h_kv < 0 || x->num_pages < 0 || x->max_pages < 0 || x->page_rows <= 0 || N < 0 || d <= 0)
+        return MHA_ERR_INVALID_ARG;
+    if (d != kAttnHeadDim || x->page_rows % 16 != 0 || x->page_rows > kMostPageRows || x->h_kv > 65535 || x->B > 65535)
+        return MHA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(x->max_pages) * x->page_rows >= kMostRows) return MHA_ERR_UNSUPPORTED;
+    const long long rows_of_page = static_cast<long long>(x->h_kv) * x->page_rows;
+    if (rows_of_page > (1 << 24)) return MHA_ERR_UNSUPPORTED;
+    c.int8 = x->dtype == MHA_INT8;
+    c.k = x->k_pages;
+    c.v = x->v_pages;
+    c.k_scales = x->k_scales;
+    c.v_scales = x->v_scales;
+    c.stride = x->page_stride;
+    c.table = x->page_table;
+    c.starts = x->row_starts;
+    c.lens = x->seq_lens;
+    c.B = x->B;
+    c.Hkv = x->h_kv;
+    c.page = x->page_rows;
+    c.num_pages = x->num_pages;
+    c.max_pages = x->max_pages;
+    c.N = N;
+    if (x->num_pages > 1 && (x->page_stride < rows_of_page * kAttnHeadDim || x->page_stride % 16 != 0)) return MHA_ERR_INVALID_ARG;
+    if (x->num_pages <= 1) c.stride = rows_of_page * kAttnHeadDim;
+    if (c.stride >= (1ll << 38)) return MHA_ERR_UNSUPPORTED;
+    if (x->B == 0 || x->h_kv == 0) return MHA_OK;
+    if (!x->seq_lens || (rows && !x->row_starts) || (x->max_pages > 0 && !x->page_table)) return MHA_ERR_INVALID_ARG;
+    if (x->num_pages > 0) {
+        if (!c.k || !c.v || (c.int8 && (!c.k_scales || !c.v_scales))) return MHA_ERR_INVALID_ARG;
+        if (!aligned16(c.k) || !aligned16(c.v) || (c.int8 && (!aligned16(c.k_scales) || !aligned16(c.v_scales))))
+            return MHA_ERR_MISALIGNED;
+    }
+    return MHA_OK;
+}
+
+// Rows (heads, N, 64) at strides of their own.
+mha_status check_rows(const void *x, long long stride_h, long long stride_t, int heads, int N, PagedRows &r) {
+    if (!x) return MHA_ERR_INVALID_ARG;
+    if (!aligned16(x)) return MHA_ERR_MISALIGNED;
+    if ((heads > 1 && stride_h < kAttnHeadDim) || (N > 1 && stride_t < kAttnHeadDim)) return MHA_ERR_INVALID_ARG;
+    if ((heads > 1 && stride_h % 8 != 0) || (N > 1 && stride_t % 8 != 0)) return MHA_ERR_MISALIGNED;
+    if (stride_h >= (1ll << 38) || stride_t >= (1ll << 38)) return MHA_ERR_UNSUPPORTED;
+    r.x = static_cast<const __nv_bfloat16 *>(x);
+    // the stride of a single head or row is never used but in a tensor map
+    r.stride_h = heads > 1 ? stride_h : kAttnHeadDim;
+    r.stride_t = N > 1 ? stride_t : kAttnHeadDim;
+    return MHA_OK;
+}
+
+// What a call's workspace holds.
+struct Layout {
+    bool tiles;      // sequences may have more than kPagedSmallRows stacked rows
+    int tile_rows;   // of paged_decode.cu
+    size_t part_o, part_ml, rec, plan, tile_o, tile_ml, tile_rec, bytes;
+};
+Layout layout(int B, int g, int N, int max_new) {
+    Layout l{};
+    const long long most = static_cast<long long>(std::min(max_new, N)) * g;
+    l.tiles = most > kPagedSmallRows;
+    // among longer chunks the short ones are taken for single tokens
+    l.tile_rows = paged_decode_rows(l.tiles ? g : static_cast<int>(most));
+    const size_t workers = static_cast<size_t>(
+        std::max(paged_decode_workers(l.tile_rows, false), paged_decode_workers(l.tile_rows, true)));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += round256(bytes);
+        return was;
+    };
+    l.part_o = take(2 * workers * l.tile_rows * kAttnHeadDim * sizeof(float));
+    l.part_ml = take(2 * workers * l.tile_rows * sizeof(float2));
+    l.rec = take(workers * sizeof(int4));
+    if (l.tiles) {
+        l.plan = take(sizeof(int) * static_cast<size_t>(paged_plan(B, paged_most_tiles(N, B, g)).ints));
+        l.tile_o = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * kAttnHeadDim * sizeof(float));
+        l.tile_ml = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * sizeof(float2));
+        l.tile_rec = take(kPagedTileCtas * sizeof(int4));
+    }
+    l.bytes = at;
+    return l;
+}
+
+mha_status check_heads(int B, int h, int h_kv, int N, int max_new) {
+    if (B < 0 || h < 0 || h_kv < 0 || N < 0 || max_new < 0) return MHA_ERR_INVALID_ARG;
+    if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return MHA_ERR_INVALID_ARG;
+    if (h > 0 && h / h_kv > 128) return MHA_ERR_UNSUPPORTED;
+    if (B > 65535 || h > 65535 || static_cast<long long>(N) * h >= (1ll << 30)) return MHA_ERR_UNSUPPORTED;
+    return MHA_OK;
+}
+
+}  // namespace
+
+MHA_EXPORT mha_status paged_cache_append(const mha_paged_cache *cache, const void *k, long long k_stride_h,
+                                         long long k_stride_t, const void *v, long long v_stride_h, long long v_stride_t,
+                                         int N, int d, cudaStream_t stream) {
+    PagedCache c{};
+    PagedRows kr, vr;
+    mha_status s = check_cache(cache, d, true, N, c);
+    if (s != MHA_OK) return s;
+    if (N == 0 || c.B == 0 || c.Hkv == 0 || c.max_pages == 0 || c.num_pages == 0) return MHA_OK;
+    if ((s = check_rows(k, k_stride_h, k_stride_t, c.Hkv, N, kr)) != MHA_OK) return s;
+    if ((s = check_rows(v, v_stride_h, v_stride_t, c.Hkv, N, vr)) != MHA_OK) return s;
+    return launched(launch_paged_append(c, kr, vr, stream), "paged cache append launch");
+}
+
+MHA_EXPORT mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int T, int d, cudaStream_t stream) {
+    PagedCache c{};
+    mha_status s = check_cache(cache, d, false, 0, c);
+    if (s != MHA_OK) return s;
+    if (T < 0) return MHA_ERR_INVALID_ARG;
+    if (T == 0 || c.B == 0 || c.Hkv == 0) return MHA_OK;
+    if (!k || !v) return MHA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return MHA_ERR_MISALIGNED;
+    if (T >= kMostRows || static_cast<long long>(c.B) * c.Hkv * ((T + 127) / 128) >= (1ll << 31)) return MHA_ERR_UNSUPPORTED;
+    return launched(launch_paged_read(c, static_cast<__nv_bfloat16 *>(k), static_cast<__nv_bfloat16 *>(v), T, stream),
+                    "paged cache read launch");
+}
+
+MHA_EXPORT size_t sdpa_paged_workspace_bytes(int B, int h, int h_kv, int N, int max_new) {
+    if (check_heads(B, h, h_kv, N, max_new) != MHA_OK || B == 0 || h == 0 || N == 0 || max_new == 0) return 0;
+    return layout(B, h / h_kv, N, max_new).bytes;
+}
+
+MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
+                                         long long q_stride_t, void *o, long long o_stride_h, long long o_stride_t,
+                                         void *workspace, size_t workspace_bytes, int h, int N, int max_new, int d,
+                                         float scale, mha_mask mask, int *status_dev, cudaStream_t stream) {
+    PagedAttnParams p{};
+    mha_status s = check_cache(cache, d, true, N, p.c);
+    if (s != MHA_OK) return s;
+    if ((s = check_heads(p.c.B, h, p.c.Hkv, N, max_new)) != MHA_OK) return s;
+    if (!isfinite(scale) || !isfinite(scale * 1.4426950408889634f)) return MHA_ERR_INVALID_ARG;
+    if (mask < MHA_MASK_NONE || mask > MHA_MASK_CAUSAL_KEY_PADDING) return MHA_ERR_INVALID_ARG;
+    if (p.c.B == 0 || h == 0 || N == 0 || max_new == 0) return MHA_OK;
+    PagedRows out;
+    if ((s = check_rows(q, q_stride_h, q_stride_t, h, N, p.q)) != MHA_OK) return s;
+    if ((s = check_rows(o, o_stride_h, o_stride_t, h, N, out)) != MHA_OK) return s;
+    const int g = h / p.c.Hkv;
+    const Layout l = layout(p.c.B, g, N, max_new);
+    // the work lines' lengths, for whatever lengths and starts the device holds
+    const long long cap = static_cast<long long>(p.c.max_pages) * p.c.page;
+    const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, kPagedSmallRows);
+    const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
+    if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1) >= kMostLine) return MHA_ERR_UNSUPPORTED;
+    if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 2) >= kMostLine)
+        return MHA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < l.bytes) return MHA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.o_stride_h = out.stride_h;
+    p.o_stride_t = out.stride_t;
+    p.H = h;
+    p.max_new = std::min(max_new, N);
+    p.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
+    p.mul = scale * 1.4426950408889634f;
+    p.small_rows = l.tiles ? std::max(kPagedSmallRows, 0) : 1 << 30;
+    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
+    p.rec = reinterpret_cast<int4 *>(ws + l.rec);
+    p.status = status_dev;
+    PagedMaps maps;
+    if (l.tiles) {
+        p.plan = reinterpret_cast<int *>(ws + l.plan);
+        p.tile_o = reinterpret_cast<float *>(ws + l.tile_o);
+        p.tile_ml = reinterpret_cast<float2 *>(ws + l.tile_ml);
+        p.tile_rec = reinterpret_cast<int4 *>(ws + l.tile_rec);
+        if ((s = encode_paged_maps(&maps, p)) != MHA_OK) return s;
+    }
+    if ((s = launched(launch_paged_decode(p, l.tiles, l.tile_rows, stream), "paged attention, few rows")) != MHA_OK) return s;
+    if (l.tiles && (s = launched(launch_attn_paged(maps, p, stream), "paged attention, row tiles")) != MHA_OK) return s;
+    return launched(launch_paged_merge(p, l.tiles, l.tile_rows, stream), "paged attention, joining");
+}

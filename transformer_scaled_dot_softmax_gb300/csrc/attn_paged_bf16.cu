@@ -1,0 +1,817 @@
+// attn_paged_bf16.cu -- attention of chunks of new tokens (prompts, parts of
+// them) over a paged K/V cache, for sm_103a.
+//
+// Row tiles.  A K/V head's query rows are stacked token by token, x = t g + i for
+// token t and the i-th of its g query heads, as many whole tokens to a tile of
+// 128 rows as fit: a chunk's heads share the K/V tiles they read, and a causal
+// tile spans few positions.  The launch before this one lists the row tiles of
+// all sequences with their numbers of key tiles (those that some row sees).
+// All (K/V head, row tile, key tile) stand in one line, of which every CTA takes
+// an equal share: no CTA waits for another's longer one, and a chunk with few rows
+// spreads over the GPU along its keys.  A row tile inside a share is written out;
+// pieces leave fp32 partial sums that the last launch joins (paged_decode.cu).
+//
+// Pages come by TMA, boxes of gcd(page, 128) rows out of a tensor of pages; a page
+// that is not there, and rows of pages past the length, are boxes past the
+// tensor's end, which arrive as zeros, and their keys are not seen.
+//
+// The pipeline (one CTA an SM, TMA ring, S issuer, two PV issuers, two softmax
+// groups on alternate tiles, output warps, three score buffers in tensor memory)
+// and the online softmax with its window of [2^-64, 2^64] around a row's reference
+// are attn_scored_bf16.cuh's, without cap and bias.
+//
+// int8 pages arrive in a ring of their own, 64 bytes a row, with the rows'
+// exponents; the output warps, which are idle while a row tile is worked on, write
+// them as bf16 into the K/V ring, in the 128-byte swizzle that TMA leaves
+// (n 2^e is exact).  Between two tiles they look for a finished row tile
+// first, since the products behind it wait for its accumulators.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mha {
+namespace {
+
+constexpr int BM = kAttnRowsPerCta;
+constexpr int BN = 128;
+constexpr int HD = kAttnHeadDim;
+constexpr int kSBufs = 3;
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8;
+constexpr int kMmaSWarp = 9;
+constexpr int kMmaPvWarp = 10;
+constexpr int kOutWarp = 12;
+constexpr uint32_t kTileBytes = BM * HD * 2;
+constexpr uint32_t kRawBytes = BN * HD;  // an int8 tile
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 384;
+constexpr float kSumMin = 5.421010862427522e-20f, kSumMax = 1.8446744073709552e19f;  // 2^-64, 2^64
+constexpr int kTable = 48;     // pieces whose geometry is kept on chip
+constexpr int kFastTiles = 6;  // pieces of so many key tiles take whole tiles in one line, as attn_scored_bf16.cuh's
+
+template <bool kInt8>
+constexpr int kStages = kInt8 ? 4 : 5;
+constexpr int kRaw = 3;  // int8 tiles in flight
+
+// One piece of work: a row tile against key tiles j0 .. j0 + n_kv - 1.
+struct Piece {
+    int b, head;      // sequence, K/V head
+    int t0, tokens;   // new tokens t0 .. t0 + tokens - 1 of the sequence's
+    int row0;         // packed row of token t0
+    int len, pos0;    // the sequence's length, the position of token t0
+    int j0, n_kv;
+    int full_hi;      // keys below it are seen by every row
+    int whole;        // all of the row tile's key tiles
+};
+
+template <bool kInt8>
+struct RawRing {
+    uint8_t k[kRaw][kRawBytes];
+    uint8_t v[kRaw][kRawBytes];
+    uint8_t ks[kRaw][BN], vs[kRaw][BN];
+    uint32_t bad[kRaw];
+    uint64_t full[kRaw], empty[kRaw];
+};
+template <>
+struct RawRing<false> {};
+
+template <bool kInt8>
+struct __align__(1024) Smem {
+    uint8_t q[2][kTileBytes];
+    uint8_t k[kStages<kInt8>][kTileBytes];
+    uint8_t v[kStages<kInt8>][kTileBytes];
+    RawRing<kInt8> raw;
+    float red_m[2][BM];
+    float red_l[2][BM];
+    uint64_t q_full[2];
+    uint64_t q_empty[2];
+    uint64_t kv_full[kStages<kInt8>];  // by TMA, or (int8) by the output warps
+    uint64_t kv_empty[kStages<kInt8>];
+    uint64_t s_full[kSBufs];
+    uint64_t p_rd[2][2][2];  // [group][round][group tile mod 2]: P of the round written
+    uint64_t pv0[2][2];      // [group][group tile mod 2]: round-0 product complete
+    uint64_t ml_full, ml_free, o_final, o_free;
+    uint64_t drain[3];
+    uint32_t bad[kStages<kInt8>];  // a bit for every 16 keys of the tile whose page is not there
+    Piece table[kTable];
+    Piece own[kThreads / 32];
+    int at_x, n_pieces;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// Where a CTA's share of the line lies.
+struct Share {
+    int tiles, keys;        // row tiles, key tiles of one K/V head
+    int start, end, share;  // of the line
+    int head0, x0;          // K/V head and row tile that it starts in
+};
+
+__device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Share &sh, int t) {
+    const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
+    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
+    const int i = sh.x0 + t, up = i / sh.tiles, x = i - up * sh.tiles;
+    Piece w;
+    w.head = sh.head0 + up;
+    w.b = p.plan[at.seq + x];
+    const PagedSeq s = paged_seq(p.c, w.b);
+    w.t0 = (x - p.plan[at.first + w.b]) * tt;
+    w.tokens = min(tt, min(s.n, p.max_new) - w.t0);
+    w.row0 = s.row0 + w.t0;
+    w.len = s.len;
+    w.pos0 = s.len - s.n + w.t0;
+    w.full_hi = p.causal ? min(max(w.pos0 + 1, 0), w.len) : w.len;
+    const int cum = p.plan[at.cum + x], n = p.plan[at.cum + x + 1] - cum;
+    const int first = w.head * sh.keys + cum;
+    w.j0 = max(sh.start - first, 0);
+    const int end = min(n, sh.end - first);
+    w.n_kv = end - w.j0;
+    w.whole = w.j0 == 0 && end == n;
+    return w;
+}
+
+template <bool kInt8>
+__device__ __forceinline__ const Piece &piece_of(Smem<kInt8> &sm, const PagedAttnParams &p, const Share &sh, int t) {
+    if (t < kTable) return sm.table[t];
+    Piece &own = sm.own[threadIdx.x >> 5];
+    __syncwarp();
+    own = make_piece(p, sh, t);  // every lane writes the same
+    __syncwarp();
+    return own;
+}
+
+// 16 int8 values of a row as bf16, times 2^e: the two 16-byte pieces.
+__device__ __forceinline__ void to_bf16(const uint4 &n, float power, uint4 &a, uint4 &b) {
+    const float off = -8388736.f * power;  // 2^23 + 128, the 0x4B000000 and the sign's offset below
+    const uint64_t p2 = f32x2_pack(power, power), off2 = f32x2_pack(off, off);
+    const uint32_t w[4] = {n.x ^ 0x80808080u, n.y ^ 0x80808080u, n.z ^ 0x80808080u, n.w ^ 0x80808080u};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = w[i >> 1];
+        float y0, y1;
+        f32x2_unpack(fma_f32x2(f32x2_pack(__uint_as_float(__byte_perm(u, 0x4B000000u, i & 1 ? 0x7442 : 0x7440)),
+                                          __uint_as_float(__byte_perm(u, 0x4B000000u, i & 1 ? 0x7443 : 0x7441))),
+                               p2, off2),
+                     y0, y1);
+        r[i] = pack_bf16x2(y0, y1);
+    }
+    a = make_uint4(r[0], r[1], r[2], r[3]);
+    b = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+template <bool kInt8>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_paged_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnParams p) {
+    constexpr int STAGES = kStages<kInt8>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem<kInt8> &sm = *reinterpret_cast<Smem<kInt8> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                       ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int cta = static_cast<int>(blockIdx.x), G = static_cast<int>(gridDim.x);
+    const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+        }
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&sm.kv_full[i], kInt8 ? 4 : 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        if constexpr (kInt8)
+            for (int i = 0; i < kRaw; ++i) {
+                mbar_init(&sm.raw.full[i], 1);
+                mbar_init(&sm.raw.empty[i], 4);
+            }
+        for (int i = 0; i < kSBufs; ++i) mbar_init(&sm.s_full[i], 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&sm.p_rd[i >> 2][(i >> 1) & 1][i & 1], kSoftmaxWarps / 2);
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.pv0[i >> 1][i & 1], 1);
+        mbar_init(&sm.ml_full, kSoftmaxWarps);
+        mbar_init(&sm.ml_free, 4);
+        mbar_init(&sm.o_final, 2);
+        mbar_init(&sm.o_free, 4);
+        for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
+        sm.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_tensormap(&maps.q);
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    Share sh;
+    sh.tiles = p.plan[0];
+    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
+    const int *cum = p.plan + at.cum;
+    sh.keys = cum[sh.tiles];
+    const int total = p.c.Hkv * sh.keys;
+    sh.share = (total + G - 1) / G;
+    if (total == 0 || static_cast<long long>(cta) * sh.share >= total) {
+        if (threadIdx.x == 0) p.tile_rec[cta] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    if (warp == kMmaSWarp) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    sh.start = cta * sh.share;
+    sh.end = min(sh.start + sh.share, total);
+    sh.head0 = sh.start / sh.keys;
+    const int head1 = (sh.end - 1) / sh.keys;
+    {
+        const int s0 = sh.start - sh.head0 * sh.keys, s1 = sh.end - 1 - head1 * sh.keys;
+        for (int x = threadIdx.x; x < sh.tiles; x += kThreads) {
+            const int lo = cum[x], hi = cum[x + 1];
+            if (lo <= s0 && s0 < hi) sm.at_x = x;
+            if (lo <= s1 && s1 < hi) sm.n_pieces = x;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    sh.x0 = sm.at_x;
+    const int pieces = (head1 - sh.head0) * sh.tiles + sm.n_pieces - sh.x0 + 1;
+    for (int t = threadIdx.x; t < min(pieces, kTable); t += kThreads) sm.table[t] = make_piece(p, sh, t);
+    __syncthreads();
+    const uint32_t tmem = sm.tmem_base;
+    const AbortState ab{&sm.abort_flag, p.status, 0};
+    const int my_tiles = sh.end - sh.start;
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------ TMA producer
+        // Lane i < boxes loads the i-th box of K and of V; its page is looked up
+        // a tile ahead.
+        const int box = min(p.c.page & -p.c.page, BN), boxes = BN / box;  // gcd(page, 128)
+        const int none = max(p.c.num_pages, 1);                            // past the tensor: zeros
+        int n = 0, v = 0;
+        bool ok = true;
+        int page = none, in_page = 0;
+        uint32_t gone = 0;  // 16-key bits of this lane's box, if it is seen but not there
+        auto look_up = [&](const Piece &w, int j) {
+            const int key = j * BN + lane * box;
+            page = none;
+            in_page = 0;
+            gone = 0;
+            if (lane < boxes && key < w.len) {
+                const int i = key / p.c.page, pg = paged_page(p.c, w.b, i);
+                if (pg >= 0) {
+                    page = pg;
+                    in_page = key - i * p.c.page;
+                } else {
+                    gone = ((1u << (box / 16)) - 1u) << (lane * (box / 16));
+                }
+            }
+        };
+        for (int t = 0; ok && t < pieces; ++t) {
+            const Piece &w = piece_of<kInt8>(sm, p, sh, t);
+            look_up(w, w.j0);
+            const int qbuf = v & 1;
+            if (v >= 2 && !(ok = warp_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.q_full[qbuf], static_cast<uint32_t>(tt * g) * (HD * 2));
+                if (in_bounds(w.head * g < p.H && w.row0 < p.c.N, p.status))
+                    tma_load_3d(&maps.q, &sm.q_full[qbuf], sm.q[qbuf], 0, w.head * g, w.row0);
+            }
+            ++v;
+            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
+                const int st = n % STAGES;
+                const int pg = page, in = in_page;
+                const uint32_t bad = __reduce_or_sync(0xffffffffu, gone);
+                if (jt + 1 < w.n_kv) look_up(w, w.j0 + jt + 1);
+                if constexpr (kInt8) {
+                    const int rs = n % kRaw;
+                    if (n >= kRaw && !(ok = warp_wait(&sm.raw.empty[rs], ((n / kRaw) - 1) & 1, ab))) break;
+                    const bool scales = lane < boxes && pg < none;
+                    const uint32_t bytes = 2 * kRawBytes + 2u * box * __popc(__ballot_sync(0xffffffffu, scales));
+                    if (lane == 0) {
+                        sm.raw.bad[rs] = bad;
+                        mbar_arrive_expect_tx(&sm.raw.full[rs], bytes);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        tma_load_4d(&maps.k, &sm.raw.full[rs], sm.raw.k[rs] + lane * box * HD, 0, in, w.head, pg);
+                        tma_load_4d(&maps.v, &sm.raw.full[rs], sm.raw.v[rs] + lane * box * HD, 0, in, w.head, pg);
+                        if (scales) {
+                            const long long from = (static_cast<long long>(pg) * p.c.Hkv + w.head) * p.c.page + in;
+                            bulk_load_1d(sm.raw.ks[rs] + lane * box, p.c.k_scales + from, box, &sm.raw.full[rs]);
+                            bulk_load_1d(sm.raw.vs[rs] + lane * box, p.c.v_scales + from, box, &sm.raw.full[rs]);
+                        }
+                    }
+                } else {
+                    if (n >= STAGES && !(ok = warp_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
+                    if (lane == 0) {
+                        sm.bad[st] = bad;
+                        mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        tma_load_4d(&maps.k, &sm.kv_full[st], sm.k[st] + lane * box * (HD * 2), 0, in, w.head, pg);
+                        tma_load_4d(&maps.v, &sm.kv_full[st], sm.v[st] + lane * box * (HD * 2), 0, in, w.head, pg);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            if constexpr (kInt8) {
+                for (int x = max(0, n - kRaw); x < n; ++x) mbar_wait_drain(&sm.raw.full[x % kRaw], (x / kRaw) & 1);
+            } else {
+                for (int x = max(0, n - STAGES); x < n; ++x) mbar_wait_drain(&sm.kv_full[x % STAGES], (x / STAGES) & 1);
+            }
+            for (int x = max(0, v - 2); x < v; ++x) mbar_wait_drain(&sm.q_full[x & 1], (x >> 1) & 1);
+        }
+    } else if (warp == kMmaSWarp) {
+        // ----------------------------------------------------- S issuer
+        constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, false);
+        constexpr uint64_t kTileDesc = kTileBytes >> 4;
+        const uint64_t q_desc0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+        const uint64_t k_desc0 = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < pieces; ++t) {
+            const int n_kv = piece_of<kInt8>(sm, p, sh, t).n_kv;
+            const int qbuf = v & 1;
+            if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
+            for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                const int st = n % STAGES, sb = n % kSBufs;
+                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                if (n >= kSBufs) {
+                    const int np = n - kSBufs;
+                    if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
+                const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
+                warp_commit(&sm.s_full[sb]);
+            }
+            if (!ok) break;
+            warp_commit(&sm.q_empty[qbuf]);
+            ++v;
+        }
+        warp_commit(&sm.drain[0]);
+        mbar_wait_drain(&sm.drain[0], 0);
+    } else if (warp == kMmaPvWarp || warp == kMmaPvWarp + 1) {
+        // ---------------------------------------------------- PV issuers
+        const int hf = warp - kMmaPvWarp;
+        constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, false, true);
+        constexpr uint64_t kTileDesc = kTileBytes >> 4;
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sm.v[0]), 1024, 1024);
+        const uint32_t d_o = tmem + kOCol + 64u * static_cast<uint32_t>(hf);
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < pieces; ++t) {
+            const Piece &w = piece_of<kInt8>(sm, p, sh, t);
+            if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
+            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
+                if ((n & 1) != hf) continue;
+                const int st = n % STAGES, sb = n % kSBufs;
+                const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
+                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                // Rows of the last page past the length: their weights are 0, and
+                // 0 times whatever the page holds has to be 0.
+                const int rows = w.len - (w.j0 + jt) * BN;
+                if (!kInt8 && rows < BN) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
+                    for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
+                const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
+#pragma unroll
+                for (int rd = 0; rd < 2; ++rd) {
+                    if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        warp_mma_bf16_ts(d_o, a + 32u * rd + 8u * kk, vd + 128 * (4 * rd + kk), idesc_o,
+                                         jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u);
+                    if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                }
+                if (!ok) break;
+                warp_commit(&sm.kv_empty[st]);
+            }
+            if (!ok) break;
+            warp_commit(&sm.o_final);
+            ++v;
+        }
+        warp_commit(&sm.drain[1 + hf]);
+        mbar_wait_drain(&sm.drain[1 + hf], 0);
+    } else if (warp < kSoftmaxWarps) {
+        // --------------------------------------------------------- softmax
+        const int half = warp >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
+        const int r = static_cast<int>(lane_base) + lane;
+        const uint32_t tl = tmem_addr(tmem, lane_base, 0);
+        const uint32_t to = tl + kOCol + 64u * half;
+        const uint64_t mul2 = f32x2_pack(p.mul, p.mul);
+        // Weights of N keys against the reference, packed; their sum, of the
+        // rounded weights (what the product multiplies).
+        auto weights = [&](const auto &s, float ref, uint32_t *pk, float (&sum)[4]) {
+            constexpr int kPairs = sizeof(s) / 8;
+            const uint64_t ref2 = f32x2_pack(-ref, -ref);
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c) {
+                float x0, x1;
+                f32x2_unpack(fma_f32x2(f32x2_pack(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), mul2, ref2), x0, x1);
+                pk[c] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
+                add_bf16x2_to_f32(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], pk[c]);
+            }
+        };
+        int n = 0, v = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < pieces; ++t) {
+            const Piece &w = piece_of<kInt8>(sm, p, sh, t);
+            const int token = r / g;
+            const bool live = token < w.tokens;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            // keys below it are seen; rows that are none hold nothing up
+            const int lim = !live ? 0x7fffffff : p.causal ? min(max(w.pos0 + token + 1, 0), w.len) : w.len;
+            const bool long_piece = w.n_kv >= kFastTiles;
+            float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
+            float l_run = 0.f;
+
+            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
+                if ((n & 1) != half) continue;
+                const int j = w.j0 + jt;
+                const int sb = n % kSBufs, st = n % STAGES;
+                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
+                if (!ok) break;
+                if (!warp_live) {
+                    // P of the warp's rows stays whatever it is: a row of
+                    // tensor memory only reaches its own row of O
+                    if (lane == 0) {
+                        mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
+                        mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                    }
+                    continue;
+                }
+                // (complete: the scores are of this tile; acquires its `bad`)
+                ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[st], (n / STAGES) & 1, ab));
+                if (!ok) break;
+                const uint32_t bad = sm.bad[st];
+                tc_fence_after_sync();
+                const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                const bool edge = j * BN + BN > w.full_hi || bad != 0;
+                int rd_first = 0;
+                if (!edge && long_piece) {
+#pragma unroll
+                    for (int rd = 0; rd < 2; ++rd) {
+                        uint32_t s0[32], s1[32], pk[32];
+                        tmem_ld32(ts + 64u * rd, s0);
+                        tmem_ld32(ts + 64u * rd + 32u, s1);
+                        tmem_ld_wait(s0);
+                        reg_fence32(s1);
+                        const float ref = m_run == -INFINITY ? 0.f : m_run;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        weights(s0, ref, pk, sum);
+                        weights(s1, ref, pk + 16, sum);
+                        const float lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        // a reference has to move: to the rounds below
+                        if (__any_sync(0xffffffffu, live && !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
+                        if (m_run == -INFINITY) m_run = 0.f;
+                        tmem_st32(ts + 32u * rd, pk);
+                        l_run += lt;
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                        rd_first = rd + 1;
+                    }
+                }
+#pragma unroll 1
+                for (int rd = rd_first; rd < 2; ++rd) {
+                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
+                    const int key0 = j * BN + 64 * rd;  // the round's first key
+                    const uint32_t gone = bad >> (4 * rd) & 15u;
+                    // Does the row need the exact step after a sum against
+                    // the reference in hand (0 before there is one)?
+                    auto must_move = [&](float sum, bool none) -> bool {
+                        if (none || !live) return false;
+                        if (m_run != -INFINITY) return !(sum <= kSumMax);
+                        if (!(sum >= kSumMin && sum <= kSumMax)) return true;
+                        m_run = 0.f;
+                        return false;
+                    };
+                    int done = 0;  // of the round's two halves
+                    if (gone == 0 && __all_sync(0xffffffffu, lim >= key0 + 64)) {
+                        uint32_t s0[32], s1[32], pk[32];
+                        tmem_ld32(tr, s0);
+                        tmem_ld32(tr + 32, s1);
+                        tmem_ld_wait(s0);
+                        reg_fence32(s1);
+                        const bool first = m_run == -INFINITY;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        weights(s0, first ? 0.f : m_run, pk, sum);
+                        weights(s1, first ? 0.f : m_run, pk + 16, sum);
+                        const float lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        if (__any_sync(0xffffffffu, must_move(lt, false))) {
+                            if (first) m_run = -INFINITY;
+                        } else {
+                            tmem_st32(ts + 32u * static_cast<uint32_t>(rd), pk);
+                            l_run += lt;
+                            done = 2;
+                        }
+                    }
+                    // Every other round, 32 keys at a time.
+#pragma unroll 1
+                    for (int h = done; h < 2; ++h) {
+                        const int kh = key0 + 32 * h;
+                        const uint32_t two = gone >> (2 * h) & 3u;
+                        const int hi = min(lim - kh, 32);
+                        // the keys seen, a bit each
+                        unsigned bits = hi <= 0 ? 0u : 0xffffffffu >> (32 - hi);
+                        if (two & 1u) bits &= 0xffff0000u;
+                        if (two & 2u) bits &= 0x0000ffffu;
+                        const bool none = bits == 0u;
+                        const uint32_t tp = ts + 32u * static_cast<uint32_t>(rd);
+                        uint32_t pk[16];
+                        float lt = 0.f, alpha = 1.f;
+                        if (__all_sync(0xffffffffu, none || !live)) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                        } else {
+                            const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
+                            bool need = false;
+                            // attempt 0 against the reference in hand; where a
+                            // row needs the exact step, 1 moves its reference
+                            // and 2 takes the keys again
+#pragma unroll 1
+                            for (int attempt = 0;; ++attempt) {
+                                uint32_t y[32];
+                                tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
+                                tmem_ld_wait(y);
+                                const float ref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) y[c] = __float_as_uint(fmaf(__uint_as_float(y[c]), p.mul, -ref));
+                                if (!all) {
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c)
+                                        if (!(bits >> c & 1u)) y[c] = __float_as_uint(-INFINITY);
+                                }
+                                if (attempt == 1) {
+                                    if (need) {
+                                        float up = -INFINITY;  // above the reference
+#pragma unroll
+                                        for (int c = 0; c < 32; c += 2)
+                                            up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                        up = ceilf(up);
+                                        if (m_run == -INFINITY) {
+                                            m_run = up;
+                                        } else if (up > 0.f) {
+                                            m_run += up;
+                                            alpha = ex2_approx(-up);
+                                            l_run *= alpha;
+                                        }
+                                    }
+                                    continue;
+                                }
+                                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    pk[c] = pack_bf16x2(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])));
+                                    add_bf16x2_to_f32(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], pk[c]);
+                                }
+                                lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                                if (attempt == 2) break;
+                                need = must_move(lt, none);
+                                if (!__any_sync(0xffffffffu, need)) break;
+                            }
+                        }
+                        tmem_st16(tp + 16u * static_cast<uint32_t>(h), pk);
+                        l_run += lt;
+                        if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
+                        // What was summed before moves with the reference: the
+                        // round's first 32 weights, which wait to be multiplied
+                        // with these, and O_h, which holds the group's earlier
+                        // tiles of the piece and, in round 1, this tile's round
+                        // 0: wait for the last product it took.
+                        if (h == 1) {
+                            tmem_st_wait();
+                            tmem_ld16(tp, pk);
+                            tmem_ld_wait(pk);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
+                                                    __uint_as_float(pk[c] & 0xffff0000u) * alpha);
+                            tmem_st16(tp, pk);
+                        }
+                        if (rd == 1) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
+                        } else if (jt >= 2) {
+                            const int np = n - 2;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
+                        } else {
+                            continue;  // O_h holds nothing of this piece
+                        }
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t o0[32];
+                            tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                            tmem_ld_wait(o0);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
+                            tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                        }
+                    }
+                    if (!ok) break;
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+            if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
+            sm.red_m[half][r] = m_run;
+            sm.red_l[half][r] = l_run;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ml_full);
+            ++v;
+        }
+        if (!ok) tmem_st_wait();
+    } else if (warp >= kOutWarp) {
+        // ------------------------------------------------- output, int8 tiles
+        const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
+        const int r = static_cast<int>(lane_base) + lane;
+        const uint32_t tl = tmem_addr(tmem, lane_base, 0);
+        if (warp == kOutWarp && lane == 0) {
+            // the block that joins a row tile is that of the first CTA that begins inside it
+            const Piece &w = sm.table[0];
+            const int first = sh.start - w.j0;
+            const int n = cum[sh.x0 + 1] - cum[sh.x0];
+            p.tile_rec[cta] = w.j0 > 0 && w.j0 <= sh.share ? make_int4(w.b, w.t0, w.head, (first + n - 1) / sh.share)
+                                                           : make_int4(-1, 0, 0, 0);
+        }
+        // The v-th piece's rows, once its products are complete.
+        auto output = [&](int v) -> bool {
+            const Piece &w = piece_of<kInt8>(sm, p, sh, v);
+            const int token = r / g, h = w.head * g + r - token * g;
+            const bool live = token < w.tokens && in_bounds(h < p.H && w.row0 + token < p.c.N, p.status);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab))) return false;
+            const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
+            const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ml_free);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab))) return false;
+            tc_fence_after_sync();
+            // A sum of 0: no visible key.  One of NaN goes on to the output.
+            const PagedLevel va = paged_level(ma, la), vb = paged_level(mb, lb);
+            const float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
+            const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
+            const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;
+            const float L = la * wa + lb * wb;
+            const float inv = !w.whole ? 1.f : L != 0.f ? 1.0f / L : 0.f;
+            const float fa = wa * inv, fb = wb * inv;
+            const long long slot = (2ll * cta + (w.j0 > 0 ? 0 : 1)) * BM + r;
+            // (the reference of a NaN is as good as any, if the merge takes it)
+            if (live && !w.whole) p.tile_ml[slot] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint32_t oa[32], ob[32];
+                tmem_ld32(tl + kOCol + 32u * part, oa);
+                tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
+                tmem_ld_wait(oa);
+                reg_fence32(ob);
+                if (part == 1) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_free);
+                }
+                if (!live) continue;
+                // a group without a visible key left its accumulator unwritten
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    oa[c] = __float_as_uint((la != 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
+                                            (lb != 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
+                if (!w.whole) {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(p.tile_o + slot * HD) + 8 * part;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) d4[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
+                } else {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(p.o + h * p.o_stride_h + (w.row0 + token) * p.o_stride_t) + 4 * part;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]), __uint_as_float(oa[2 * c + 1]));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) d4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                }
+            }
+            return true;
+        };
+        if constexpr (!kInt8) {
+            for (int v = 0; v < pieces; ++v)
+                if (!output(v)) break;
+        } else {
+            const int tid = threadIdx.x - 32 * kOutWarp;
+            // the piece that the next tile to be written belongs to
+            int piece = 0, jt = 0, n_kv = sm.table[0].n_kv, j0 = sm.table[0].j0, len = sm.table[0].len;
+            auto convert = [&](int n) {
+                const int rs = n % kRaw, st = n % STAGES;
+                const uint32_t bad = sm.raw.bad[rs];
+                const int keys = len - (j0 + jt) * BN;  // rows past it are cleared
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int x = (i & 3) * 128 + tid, row = x >> 2, quarter = x & 3;
+                    const uint8_t *from = i < 4 ? sm.raw.k[rs] : sm.raw.v[rs];
+                    const uint32_t e = (i < 4 ? sm.raw.ks[rs] : sm.raw.vs[rs])[row];
+                    const uint4 u = reinterpret_cast<const uint4 *>(from)[x];
+                    const bool there = row < keys && !(bad >> (row >> 4) & 1u);
+                    uint4 a, b;
+                    to_bf16(u, there ? paged_power(e) : 0.f, a, b);
+                    uint4 *to = reinterpret_cast<uint4 *>(i < 4 ? sm.k[st] : sm.v[st]) + row * 8;
+                    to[(2 * quarter) ^ (row & 7)] = a;
+                    to[(2 * quarter + 1) ^ (row & 7)] = b;
+                }
+                if (tid == 0) sm.bad[st] = bad;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.kv_full[st]);
+                    mbar_arrive(&sm.raw.empty[rs]);
+                }
+                if (++jt == n_kv && ++piece < pieces) {
+                    const Piece &w = piece_of<true>(sm, p, sh, piece);
+                    jt = 0;
+                    n_kv = w.n_kv;
+                    j0 = w.j0;
+                    len = w.len;
+                }
+            };
+            auto ready = [&](uint64_t *bar, int parity) {
+                return __all_sync(0xffffffffu, mbar_try_wait(bar, static_cast<uint32_t>(parity)));
+            };
+            int n = 0, v = 0;
+            unsigned long long since = 0;
+            while (v < pieces) {
+                if (n == my_tiles) {
+                    if (!output(v)) break;
+                    ++v;
+                    continue;
+                }
+                const int rs = n % kRaw, st = n % STAGES;
+                if (ready(&sm.o_final, v & 1)) {
+                    if (!output(v)) break;
+                    ++v;
+                } else if (n < STAGES || ready(&sm.kv_empty[st], ((n / STAGES) - 1) & 1)) {
+                    // (raw tiles wait for nothing but these warps)
+                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.raw.full[rs], (n / kRaw) & 1, ab))) break;
+                    convert(n);
+                    ++n;
+                } else {
+                    // neither: look again, within the waits' limit
+                    const unsigned long long now = global_timer_ns();
+                    if (since == 0) since = now;
+                    bool stop = should_abort(ab);
+                    if (now - since > kWaitLimitNs) {
+                        raise_abort(ab);
+                        stop = true;
+                    }
+                    if (__any_sync(0xffffffffu, stop)) break;
+                    continue;
+                }
+                since = 0;
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaSWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <bool kInt8>
+cudaError_t launch(const PagedMaps &maps, const PagedAttnParams &p, cudaStream_t stream) {
+    auto kernel = attn_paged_kernel<kInt8>;
+    const size_t smem = sizeof(Smem<kInt8>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, dim3(kPagedTileCtas), dim3(kThreads), smem, stream, true, 1, maps, p);
+}
+static_assert(sizeof(Smem<true>) + 1024 <= 227 * 1024 && sizeof(Smem<false>) + 1024 <= 227 * 1024, "shared memory");
+
+}  // namespace
+
+cudaError_t launch_attn_paged(const PagedMaps &maps, const PagedAttnParams &p, cudaStream_t stream) {
+    return p.c.int8 ? launch<true>(maps, p, stream) : launch<false>(maps, p, stream);
+}
+
+}  // namespace mha

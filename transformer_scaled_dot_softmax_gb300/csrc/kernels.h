@@ -263,6 +263,90 @@ struct DecodeRowParams {
 };
 cudaError_t launch_decode_row(const DecodeRowParams &p, int bias, cudaStream_t stream);
 
+// ------------------------------------------------ paged K/V cache
+// Checked arguments of the paged entry points (mha_paged_cache, include/mha.h).
+struct PagedCache {
+    void *k, *v;                    // (num_pages, Hkv, page, 64) bf16 or int8, pages `stride` elements apart
+    uint8_t *k_scales, *v_scales;   // int8: (num_pages, Hkv, page), exponent + 127
+    long long stride;
+    const int32_t *table;           // (B, max_pages)
+    const int32_t *starts, *lens;   // (B + 1) packed rows (null where there are none), (B)
+    int int8;
+    int B, Hkv, page, num_pages, max_pages;
+    int N;                          // packed rows
+};
+// New rows (heads, tokens, 64), strides in elements.
+struct PagedRows {
+    const __nv_bfloat16 *x;
+    long long stride_h, stride_t;
+};
+cudaError_t launch_paged_append(const PagedCache &c, const PagedRows &k, const PagedRows &v, cudaStream_t stream);
+// k, v: (B, Hkv, T, 64) bf16.
+cudaError_t launch_paged_read(const PagedCache &c, __nv_bfloat16 *k, __nv_bfloat16 *v, int T, cudaStream_t stream);
+
+struct PagedAttnParams {
+    PagedCache c;
+    PagedRows q;
+    __nv_bfloat16 *o;
+    long long o_stride_h, o_stride_t;
+    int H, max_new;
+    int causal;
+    float mul;             // scale log2(e)
+    // Sequences of at most small_rows stacked rows (g query heads of a K/V head
+    // x new tokens) are gone through by paged_decode.cu, the others by
+    // attn_paged_bf16.cu (small_rows is 2^30 where there can be none).
+    int small_rows;
+    // paged_decode.cu: partial sums of key ranges that end inside an item
+    float *part_o;         // (2 workers, rows of a tile, 64)
+    float2 *part_ml;       // (2 workers, rows of a tile): reference in log2 units, sum
+    int4 *rec;             // (workers): the item that a worker's merge block finishes
+    // attn_paged_bf16.cu: its row tiles, listed by the launch before it, and the same
+    int *plan;             // [0] the number of row tiles; then kPlanHead on: see PagedPlan
+    float *tile_o;
+    float2 *tile_ml;
+    int4 *tile_rec;
+    int *status;
+};
+constexpr int kPagedSmallRows = 64;
+constexpr int kPagedTileCtas = kSmsPerGpu;  // persistent CTAs of attn_paged_bf16.cu
+// Rows that a warp of paged_decode.cu takes at once, its workers (warps), for
+// calls whose sequences have up to `rows` stacked rows there.
+int paged_decode_rows(int rows);
+int paged_decode_workers(int tile_rows, bool int8);
+// The launch that goes through the small sequences and lists the others' row
+// tiles, and the one that joins both kernels' partial sums.
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream);
+// q: (64, H, N) in boxes of the query heads of a K/V head x as many tokens as
+// fit 128 rows; k, v: (64, page, Hkv, num_pages) in boxes of gcd(page, 128) rows.
+struct PagedMaps {
+    CUtensorMap q, k, v;
+};
+cudaError_t launch_attn_paged(const PagedMaps &maps, const PagedAttnParams &p, cudaStream_t stream);
+mha_status encode_paged_maps(PagedMaps *m, const PagedAttnParams &p);
+
+// Lists in PagedAttnParams::plan, of at most `tiles` row tiles and B sequences.
+struct PagedPlan {
+    int first;   // (B + 1) first row tile of each sequence
+    int cum;     // (tiles + 1) key tiles of one K/V head before a row tile
+    int seq;     // (tiles) its sequence
+    int ints;
+};
+inline __host__ __device__ PagedPlan paged_plan(int B, int tiles) {
+    PagedPlan l;
+    l.first = 4;
+    l.cum = l.first + B + 1;
+    l.seq = l.cum + tiles + 1;
+    l.ints = l.seq + tiles;
+    return l;
+}
+// Tokens of a row tile, and row tiles of a call at most.
+inline __host__ __device__ int paged_tile_tokens(int g) { return 128 / g; }
+inline __host__ __device__ int paged_most_tiles(int N, int B, int g) {
+    const int tt = paged_tile_tokens(g);
+    return (N + tt - 1) / tt + B;
+}
+
 // ------------------------------------------------ positional encoding
 // out (rows, D) = x + PE(pos0 + row % T); D % 8 == 0; x and out may alias.
 cudaError_t launch_posenc_add_bf16(const __nv_bfloat16 *x, __nv_bfloat16 *out, long long rows, int T,

@@ -1,0 +1,710 @@
+// paged_decode.cu -- attention of few query rows (single tokens, drafted
+// tokens, short chunks) over a paged K/V cache, and the joining of partial sums.
+//
+// A K/V head's query rows are stacked: x = t g + i for token t and the i-th of
+// its g query heads.  An item is up to kRows of them against all cached rows of
+// the sequence, in units of 16 keys (bf16) or 32 (int8): 4 KB of K and V.  All
+// units of the batch stand in one line; every warp takes an equal share of it,
+// whatever the lengths, keeps the online softmax of the item it is in (reference
+// m in log2 units, sum l, unnormalised O) and leaves it behind where the item ends
+// inside the share: whole items are written out, pieces as partial sums that
+// paged_merge_kernel joins, in a fixed order.
+//
+// The products run on mma.sync with the keys as rows: S^T = K Q^T and
+// O^T = V^T P^T, m16n8k16, because the work is bound by memory and a tile of 8
+// query rows wastes the least (a tcgen05 tile has 128).  K and V go from global
+// memory straight into the fragments: the order of the 64 features in a dot product
+// is free, so that a lane's fragments of a K row are 16 consecutive bytes, four lanes a
+// row; for V^T a lane holds 8 consecutive features of the four keys its fragments
+// need, and pairs of keys are merged by byte permutes.  A unit is loaded while the
+// one before it is worked on.
+//
+// int8: K n and q are multiplied as fp16, K's whole numbers exactly, a query row
+// scaled by a power of two so that its largest element lies in [2^14, 2^15)
+// (elements below 2^-31 of it lose bits, 2^-39 of it at most); the keys' powers of
+// two and the row's meet the fp32 score.  V becomes bf16 with its power
+// of two, which is exact.  The whole numbers come out of their bytes by permutes:
+// 0x6400 | u is 1024 + u in fp16, 0x4B000000 | u is 2^23 + u in fp32, u = n + 128.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+#include "paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mha {
+namespace {
+
+constexpr int HD = kAttnHeadDim;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMergeThreads = 256;
+// A row's reference serves until a unit's weights sum to more than this.
+constexpr float kSumMax = 65536.0f;
+// A worker's least share of the line, in units: what a piece costs to write
+// and join is worth a few units of reading.
+constexpr int kLeastShare = 4;
+
+template <bool kInt8>
+constexpr int kUnitKeys = kInt8 ? 32 : 16;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8 x 8 matrix of 16-bit elements held as an accumulator's halves are.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint4 load16(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint2 load8(const void *p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+
+// The two fp16 pairs n0 n1, n2 n3 of four whole numbers.
+__device__ __forceinline__ void to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = n ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), off), y = __hsub2(*reinterpret_cast<__half2 *>(&b), off);
+    lo = *reinterpret_cast<uint32_t *>(&x);
+    hi = *reinterpret_cast<uint32_t *>(&y);
+}
+
+// One lane's part of a unit.
+template <bool kInt8>
+struct Unit {
+    uint4 k[4];      // bf16: keys l/4 and l/4 + 8, two pieces of 8 features; int8: keys l/4 + 8 i, 16 features
+    uint4 v[4];      // bf16: keys 2c, 2c+1, 2c+8, 2c+9 (c = l % 4), features 8 (l/4) on; int8: two such keys in each
+    uint32_t ks[kInt8 ? 4 : 1], vs[kInt8 ? 4 : 1];  // stored exponents: of those keys of K; pairs of V's
+    uint32_t there;  // a bit for every 16 keys: their page is there
+};
+
+struct Shape {
+    int units, tiles, total;  // of a row tile; row tiles; of the sequence
+};
+template <bool kInt8, int kRows>
+__device__ __forceinline__ Shape shape_of(const PagedAttnParams &p, const PagedSeq &s, int g) {
+    Shape r;
+    const int rows = min(s.n, p.max_new) * g;
+    r.units = max((s.len + kUnitKeys<kInt8> - 1) / kUnitKeys<kInt8>, 1);
+    r.tiles = rows > p.small_rows ? 0 : (rows + kRows - 1) / kRows;
+    r.total = p.c.Hkv * r.tiles * r.units;
+    return r;
+}
+
+// Sum over the block of one value a thread; `excl`: of the threads before it.
+__device__ __forceinline__ int block_sum(int x, int *warp_sums, int &excl) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    excl = before + incl - x;
+    return total;
+}
+
+// The row tiles of the sequences that attn_paged_bf16.cu goes through, with
+// their key tiles, in plan.
+__device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
+    const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
+    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
+    int *first = p.plan + at.first, *cum = p.plan + at.cum, *seq = p.plan + at.seq;
+    const int most = paged_most_tiles(p.c.N, p.c.B, g);
+    int tiles = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int n = 0, excl;
+        if (b < p.c.B) {
+            const PagedSeq s = paged_seq(p.c, b);
+            const int tokens = min(s.n, p.max_new);
+            if (tokens * g > p.small_rows) n = (tokens + tt - 1) / tt;
+        }
+        const int total = block_sum(n, warp_sums, excl);
+        if (b < p.c.B) first[b] = min(tiles + excl, most);
+        tiles = min(tiles + total, most);  // (more than that only where sequences overlap)
+    }
+    if (threadIdx.x == 0) first[p.c.B] = tiles;
+    __syncthreads();
+    int keys = 0;
+    for (int x0 = 0; x0 < tiles; x0 += kThreads) {
+        const int x = x0 + threadIdx.x;
+        int n = 0, excl, b = 0;
+        if (x < tiles) {
+            int lo = 0, hi = p.c.B;  // the last sequence whose first tile is at most x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (first[mid] <= x)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            b = lo;
+            const PagedSeq s = paged_seq(p.c, b);
+            const int last = min((x - first[b] + 1) * tt, min(s.n, p.max_new)) - 1;
+            const int end = p.causal ? min(max(s.len - s.n + last + 1, 0), s.len) : s.len;
+            n = max((end + 127) / 128, 1);
+        }
+        const int total = block_sum(n, warp_sums, excl);
+        if (x < tiles) {
+            cum[x] = keys + excl;
+            seq[x] = b;
+        }
+        keys += total;
+    }
+    if (threadIdx.x == 0) {
+        cum[tiles] = keys;
+        p.plan[0] = tiles;
+    }
+}
+
+template <bool kInt8, int kN>
+__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnParams p, int list) {
+    constexpr int kRows = 8 * kN, kKeys = kUnitKeys<kInt8>, kBlocks = kKeys / 16;
+    __shared__ int warp_sums[kWarps], at_b[kWarps], at_start[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l4 = lane >> 2, c = lane & 3;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (list && blockIdx.x == gridDim.x - 1) {
+        list_tiles(p, warp_sums);
+        return;
+    }
+    const int workers = (gridDim.x - (list ? 1 : 0)) * kWarps, me = blockIdx.x * kWarps + warp;
+    const int g = p.H / p.c.Hkv;
+    const int per_page = p.c.page / 16;
+
+    // The line's length, the shares, and where this warp's begins.
+    int total = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int excl;
+        total += block_sum(b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0, warp_sums, excl);
+    }
+    const int share = max((total + workers - 1) / workers, kLeastShare);
+    if (lane == 0) at_b[warp] = -1;
+    int base = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int excl;
+        const int mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
+        const int sum = block_sum(mine, warp_sums, excl);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            // (a share past the line's end may start past 2^31)
+            const long long s = static_cast<long long>(blockIdx.x * kWarps + w) * share;
+            if (s >= base + excl && s < base + excl + mine) {
+                at_b[w] = b;
+                at_start[w] = base + excl;
+            }
+        }
+        base += sum;
+    }
+    __syncthreads();
+    int b = at_b[warp];
+    if (b < 0) {
+        if (lane == 0) p.rec[me] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    const int start = me * share;
+    int left = min(share, total - start), rel = start - at_start[warp];
+    bool first_piece = true;
+
+    while (left > 0) {
+        const PagedSeq s = paged_seq(p.c, b);
+        const Shape sh = shape_of<kInt8, kRows>(p, s, g);
+        const int item = rel / sh.units, u0 = rel - item * sh.units, u1 = min(sh.units, u0 + left);
+        const int head = item / sh.tiles, tile = item - head * sh.tiles;
+        const int rows = min(s.n, p.max_new) * g - tile * kRows;  // of this item, if less than kRows
+        if (first_piece && lane == 0) {
+            // The block of the first worker that begins inside an item joins it.
+            p.rec[me] = u0 > 0 && u0 <= share ? make_int4(b, item, (start - u0 + sh.units - 1) / share, 0)
+                                              : make_int4(-1, 0, 0, 0);
+        }
+
+        // Queries: a lane's features of row l/4, in every 8 rows.
+        uint32_t q[kN][8];
+        float mul[kN][2];  // of the scores of rows 2c, 2c + 1
+        int lim[kN][2];    // keys below it are seen
+        int least = s.len;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int x = tile * kRows + 8 * n + l4;
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a;
+            if (8 * n + l4 < rows) {
+                const int t = x / g;
+                const __nv_bfloat16 *src = p.q.x + (head * g + x - t * g) * p.q.stride_h + (s.row0 + t) * p.q.stride_t;
+                a = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c : 8 * c));
+                d = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c + 8 : 8 * c + 32));
+            }
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+            float f = p.mul;
+            if (kInt8) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^k, the largest element's (at least the least normal number's)
+                const int k = max(static_cast<int>(top >> 7), 1) - 127;
+                const float up0 = __uint_as_float((127 - k / 2) << 23), up1 = __uint_as_float((127 + 14 - (k - k / 2)) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * up0 * up1,
+                                                        __uint_as_float(w[i] & 0xffff0000u) * up0 * up1);
+                    q[n][i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                f *= __uint_as_float((127 + k / 2) << 23) * __uint_as_float((127 - 14 + (k - k / 2)) << 23);
+                if (top >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: NaN
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[n][i] = w[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * c + i;
+                mul[n][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
+                lim[n][i] = 0x7fffffff;
+                if (r < rows) {
+                    lim[n][i] = p.causal ? min(s.len, max(s.len - s.n + (tile * kRows + r) / g + 1, 0)) : s.len;
+                    least = min(least, lim[n][i]);
+                }
+            }
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+
+        // Sub-units of 16 keys, 32 from `sub0` on: a lane holds the page of its one.
+        int sub0 = u0 * kBlocks, page = -1, in_page = 0;
+        auto look_up = [&](int sub) {
+            sub0 = sub;
+            const int i = (sub0 + lane) / per_page;
+            in_page = (sub0 + lane - i * per_page) * 16;
+            page = (sub0 + lane) * 16 < s.len ? paged_page(p.c, b, i) : -1;
+        };
+        look_up(sub0);
+        auto load = [&](int u, Unit<kInt8> &x) {
+            if (u * kBlocks - sub0 >= 32) look_up(u * kBlocks);
+            x.there = 0;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                const int pg = __shfl_sync(0xffffffffu, page, u * kBlocks + i - sub0);
+                const int in = __shfl_sync(0xffffffffu, in_page, u * kBlocks + i - sub0);
+                if (pg >= 0) x.there |= 1u << i;
+                const int key0 = (u * kBlocks + i) * 16;
+                const int valid = pg >= 0 ? s.len - key0 : 0;  // keys of the 16 that are there
+                const int row = head * p.c.page + in;
+                const long long at = pg * p.c.stride + static_cast<long long>(row) * HD;
+                if constexpr (kInt8) {
+                    const int8_t *kp = static_cast<const int8_t *>(p.c.k) + at, *vp = static_cast<const int8_t *>(p.c.v) + at;
+                    const long long sat = static_cast<long long>(pg) * p.c.Hkv * p.c.page + row;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x.k[2 * i + j] = make_uint4(0u, 0u, 0u, 0u);
+                        x.ks[2 * i + j] = 0u;
+                        if (l4 + 8 * j < valid) {
+                            x.k[2 * i + j] = load16(kp + (l4 + 8 * j) * HD + 16 * c);
+                            x.ks[2 * i + j] = __ldg(p.c.k_scales + sat + l4 + 8 * j);
+                        }
+                        uint2 v0 = make_uint2(0u, 0u), v1 = v0;
+                        const int kv = 2 * c + 8 * j;
+                        x.vs[2 * i + j] = 0u;
+                        if (kv < valid) {
+                            v0 = load8(vp + kv * HD + 8 * l4);
+                            // (both exponents: a page's rows come in 16s; the second is cut off below)
+                            x.vs[2 * i + j] = __ldg(reinterpret_cast<const unsigned short *>(p.c.v_scales + sat + kv));
+                        }
+                        if (kv + 1 < valid)
+                            v1 = load8(vp + (kv + 1) * HD + 8 * l4);
+                        else
+                            x.vs[2 * i + j] &= 0xffu;
+                        x.v[2 * i + j] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                    }
+                } else {
+                    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(p.c.k) + at,
+                                        *vp = static_cast<const __nv_bfloat16 *>(p.c.v) + at;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        x.k[2 * j] = x.k[2 * j + 1] = make_uint4(0u, 0u, 0u, 0u);
+                        if (l4 + 8 * j < valid) {
+                            x.k[2 * j] = load16(kp + (l4 + 8 * j) * HD + 8 * c);
+                            x.k[2 * j + 1] = load16(kp + (l4 + 8 * j) * HD + 8 * c + 32);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int kv = 2 * c + (j & 1) + 8 * (j >> 1);
+                        x.v[j] = make_uint4(0u, 0u, 0u, 0u);
+                        if (kv < valid) x.v[j] = load16(vp + kv * HD + 8 * l4);
+                    }
+                }
+            }
+        };
+
+        float o[kN][4][4], m[kN][2], l[kN][2];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[n][i / 4][i % 4] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+
+        auto work = [&](int u, const Unit<kInt8> &x) {
+            // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
+            float st[kN][kBlocks][4];
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                uint32_t ka[2][8];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (kInt8) {
+                        const uint4 &w = x.k[2 * i + j];
+                        to_f16(w.x, ka[j][0], ka[j][1]);
+                        to_f16(w.y, ka[j][2], ka[j][3]);
+                        to_f16(w.z, ka[j][4], ka[j][5]);
+                        to_f16(w.w, ka[j][6], ka[j][7]);
+                    } else {
+                        const uint4 &w = x.k[2 * j], &z = x.k[2 * j + 1];
+                        ka[j][0] = w.x, ka[j][1] = w.y, ka[j][2] = w.z, ka[j][3] = w.w;
+                        ka[j][4] = z.x, ka[j][5] = z.y, ka[j][6] = z.z, ka[j][7] = z.w;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[n][i][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a[4] = {ka[0][2 * k], ka[1][2 * k], ka[0][2 * k + 1], ka[1][2 * k + 1]};
+                        if constexpr (kInt8)
+                            mma_f16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
+                        else
+                            mma_bf16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
+                    }
+                }
+            }
+            // in log2 units; a key that is not seen to minus infinity
+            const int key0 = u * kKeys;
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y = st[n][i][e];
+                        if constexpr (kInt8) y *= paged_power(x.ks[2 * i + (e >> 1)]);
+                        st[n][i][e] = y * mul[n][e & 1];
+                    }
+            if (key0 + kKeys > least || x.there != (1u << kBlocks) - 1u) {
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + 16 * i + l4 + 8 * (e >> 1) >= min(lim[n][e & 1], s.len) || !(x.there >> i & 1u))
+                                st[n][i][e] = -INFINITY;
+            }
+            // weights against the reference in hand; where a row has none yet, or
+            // its sum leaves the range, against the unit's maximum
+            uint32_t pk[kN][kBlocks][2];
+            float sum[kN][2];
+#pragma unroll 1
+            for (int attempt = 0;; ++attempt) {
+                bool need = false;
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                    sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            pk[n][i][j] = pack_bf16x2(ex2_approx(st[n][i][2 * j] - r0), ex2_approx(st[n][i][2 * j + 1] - r1));
+                            add_bf16x2_to_f32(sum[n][0], sum[n][1], pk[n][i][j]);
+                        }
+                    need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax) || m[n][0] == -INFINITY || m[n][1] == -INFINITY;
+                }
+                if (attempt == 1 || !__any_sync(0xffffffffu, need)) break;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float top = m[n][r];
+#pragma unroll
+                        for (int i = 0; i < kBlocks; ++i) top = fmax3(top, st[n][i][r], st[n][i][2 + r]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        if (m[n][r] != -INFINITY) {
+                            const float alpha = ex2_approx(m[n][r] - top);
+                            l[n][r] *= alpha;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[n][i][r] *= alpha;
+                                o[n][i][2 + r] *= alpha;
+                            }
+                        }
+                        m[n][r] = top;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                l[n][0] += sum[n][0];
+                l[n][1] += sum[n][1];
+            }
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                // V^T: features 8 (l/4) + 2 f, + 1 in rows l/4, l/4 + 8 of tile f
+                uint32_t va[4][4];
+                if constexpr (kInt8) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 &w = x.v[2 * i + j];
+                        const float s0 = paged_power(x.vs[2 * i + j] & 0xffu), s1 = paged_power(x.vs[2 * i + j] >> 8);
+                        const uint64_t s2 = f32x2_pack(s0, s1), off = f32x2_pack(-8388736.f * s0, -8388736.f * s1);
+                        const uint32_t a[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u}, d[2] = {w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t sel = 0x7440u + (e & 3);
+                            float y0, y1;
+                            f32x2_unpack(fma_f32x2(f32x2_pack(__uint_as_float(__byte_perm(a[e >> 2], 0x4B000000u, sel)),
+                                                              __uint_as_float(__byte_perm(d[e >> 2], 0x4B000000u, sel))),
+                                                   s2, off),
+                                         y0, y1);
+                            va[e >> 1][2 * j + (e & 1)] = pack_bf16x2(y0, y1);
+                        }
+                    }
+                } else {
+                    const uint32_t w[4][4] = {{x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w}, {x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w},
+                                              {x.v[2].x, x.v[2].y, x.v[2].z, x.v[2].w}, {x.v[3].x, x.v[3].y, x.v[3].z, x.v[3].w}};
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        va[f][0] = __byte_perm(w[0][f], w[1][f], 0x5410);
+                        va[f][1] = __byte_perm(w[0][f], w[1][f], 0x7632);
+                        va[f][2] = __byte_perm(w[2][f], w[3][f], 0x5410);
+                        va[f][3] = __byte_perm(w[2][f], w[3][f], 0x7632);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const uint32_t b0 = transpose8(pk[n][i][0]), b1 = transpose8(pk[n][i][1]);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
+                }
+            }
+        };
+
+        Unit<kInt8> x0, x1;
+        load(u0, x0);
+#pragma unroll 1
+        for (int u = u0; u < u1; u += 2) {
+            if (u + 1 < u1) load(u + 1, x1);
+            work(u, x0);
+            if (u + 1 < u1) {
+                if (u + 2 < u1) load(u + 2, x0);
+                work(u + 1, x1);
+            }
+        }
+
+        // The item, or the piece: slot 2 me of one that began before this
+        // worker, 2 me + 1 of one that goes on behind it.
+        const bool whole = u0 == 0 && u1 == sh.units;
+        const long long slot = (2ll * me + (u0 > 0 ? 0 : 1)) * kRows;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float sum = l[n][r];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = 8 * n + 2 * c + r;
+                if (row >= rows) continue;
+                float y[8];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    y[2 * f] = o[n][f][r];
+                    y[2 * f + 1] = o[n][f][2 + r];
+                }
+                if (whole) {
+                    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+                    const int at = tile * kRows + row, t = at / g;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) w[f] = sum != 0.f ? pack_bf16x2(y[2 * f] * inv, y[2 * f + 1] * inv) : 0u;
+                    if (in_bounds(head * g + at - t * g < p.H && s.row0 + t < p.c.N, p.status))
+                        *reinterpret_cast<uint4 *>(p.o + (head * g + at - t * g) * p.o_stride_h + (s.row0 + t) * p.o_stride_t +
+                                                   8 * l4) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else if (in_bounds(me < workers, p.status)) {
+                    float4 *to = reinterpret_cast<float4 *>(p.part_o + (slot + row) * HD + 8 * l4);
+                    to[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    to[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    if (l4 == 0) p.part_ml[slot + row] = make_float2(m[n][r], sum);
+                }
+            }
+
+        left -= u1 - u0;
+        rel += u1 - u0;
+        first_piece = false;
+        if (rel == sh.total) {
+            rel = 0;
+            do ++b;
+            while (left > 0 && b < p.c.B && shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total == 0);
+        }
+    }
+}
+
+// ------------------------------------------------------------ joining partial sums
+//   o = (sum_s w_s O_s) / (sum_s w_s l_s),  w_s = 2^(m_s - M),  M = max_s m_s
+// over the pieces of an item: the tail slot of worker `first`, then the head
+// slots up to worker `last`.  16 lanes take one row (4 features each); groups
+// that would be idle share a row's pieces.  A piece without a visible key has
+// m = -inf, l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is
+// taken as paged_level gives it.
+__device__ __forceinline__ float piece_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
+
+template <typename Out>
+__device__ void join(const float *part_o, const float2 *part_ml, int slot_rows, int first, int last, int row0, int rows,
+                     float (&sh_o)[kMergeThreads / 16][HD], float2 (&sh_ml)[kMergeThreads / 16], Out out) {
+    constexpr int kGroups = kMergeThreads / 16;
+    const int grp = threadIdx.x / 16, lane = threadIdx.x & 15;
+    int per = 1;  // groups of a row
+    while (per * 2 * rows <= kGroups) per *= 2;
+    const int pieces = last - first + 1;
+    for (int r0 = 0; r0 < rows; r0 += kGroups / per) {
+        const int row = r0 + grp / per, part = grp % per;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows) {
+#pragma unroll 4
+            for (int i = part; i < pieces; i += per) {
+                const long long slot = (i == 0 ? 2ll * first + 1 : 2ll * (first + i)) * slot_rows + row0 + row;
+                const float2 ml = part_ml[slot];
+                const float4 x = reinterpret_cast<const float4 *>(part_o + slot * HD)[lane];
+                if (ml.y == 0.f) continue;  // no visible key
+                const PagedLevel v = paged_level(ml.x, ml.y);
+                const float top = fmaxf(m, v.m);
+                const float a = piece_weight(m, top), w = piece_weight(v.m, top) * v.down;
+                m = top;
+                l = l * a + ml.y * w;
+                o = make_float4(o.x * a + x.x * w, o.y * a + x.y * w, o.z * a + x.z * w, o.w * a + x.w * w);
+            }
+        }
+        if (per > 1) {
+            __syncthreads();
+            reinterpret_cast<float4 *>(sh_o[grp])[lane] = o;
+            if (lane == 0) sh_ml[grp] = make_float2(m, l);
+            __syncthreads();
+            if (part == 0) {
+                for (int i = 1; i < per; ++i) {
+                    const float2 ml = sh_ml[grp + i];
+                    const float4 x = reinterpret_cast<const float4 *>(sh_o[grp + i])[lane];
+                    const float top = fmaxf(m, ml.x);
+                    const float a = piece_weight(m, top), w = piece_weight(ml.x, top);
+                    m = top;
+                    l = l * a + ml.y * w;
+                    o = make_float4(o.x * a + x.x * w, o.y * a + x.y * w, o.z * a + x.z * w, o.w * a + x.w * w);
+                }
+            }
+        }
+        if (part == 0 && row < rows) {
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            out(row0 + row, lane, make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)));
+        }
+    }
+}
+
+// Blocks 0 .. workers - 1 join the items of the kernel above, a block for every
+// worker that began inside one; the others those of attn_paged_bf16.cu, 8
+// blocks of 16 rows for each of its CTAs.
+constexpr int kTileJoinRows = 16;
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int workers, int tile_rows) {
+    __shared__ float sh_o[kMergeThreads / 16][HD];
+    __shared__ float2 sh_ml[kMergeThreads / 16];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int g = p.H / p.c.Hkv;
+    const int x = blockIdx.x;
+    if (x < workers) {
+        const int4 rec = p.rec[x];
+        if (rec.x < 0) return;
+        const PagedSeq s = paged_seq(p.c, rec.x);
+        const int all = min(s.n, p.max_new) * g, tiles = (all + tile_rows - 1) / tile_rows;
+        const int head = rec.y / tiles, tile = rec.y - head * tiles;
+        join(p.part_o, p.part_ml, tile_rows, x - 1, rec.z, 0, min(all - tile * tile_rows, tile_rows), sh_o, sh_ml,
+             [&](int row, int lane, uint2 y) {
+                 const int at = tile * tile_rows + row, t = at / g, h = head * g + at - t * g;
+                 if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
+                     reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[lane] = y;
+             });
+        return;
+    }
+    const int per = 128 / kTileJoinRows, cta = (x - workers) / per, row0 = (x - workers - cta * per) * kTileJoinRows;
+    const int4 rec = p.tile_rec[cta];
+    if (rec.x < 0) return;
+    const PagedSeq s = paged_seq(p.c, rec.x);
+    const int t0 = rec.y, head = rec.z;
+    const int rows = min(min(s.n, p.max_new) - t0, paged_tile_tokens(g)) * g;
+    if (row0 >= rows) return;
+    join(p.tile_o, p.tile_ml, 128, cta - 1, rec.w, row0, min(rows - row0, kTileJoinRows), sh_o, sh_ml,
+         [&](int row, int lane, uint2 y) {
+             const int t = t0 + row / g, h = head * g + row % g;
+             if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
+                 reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[lane] = y;
+         });
+}
+
+template <bool kInt8>
+cudaError_t launch_rows(const PagedAttnParams &p, int list, int tile_rows, cudaStream_t stream) {
+    const dim3 grid(paged_decode_workers(tile_rows, kInt8) / kWarps + list), block(kThreads);
+    if (tile_rows == 8) return launch_kernel(paged_decode_kernel<kInt8, 1>, grid, block, 0, stream, true, 1, p, list);
+    if (tile_rows == 16) return launch_kernel(paged_decode_kernel<kInt8, 2>, grid, block, 0, stream, true, 1, p, list);
+    return launch_kernel(paged_decode_kernel<kInt8, 4>, grid, block, 0, stream, true, 1, p, list);
+}
+
+}  // namespace
+
+int paged_decode_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+int paged_decode_workers(int tile_rows, bool int8) {
+    const int ctas = tile_rows == 32 ? 2 : 3;  // of an SM
+    return kSmsPerGpu * ctas * kWarps;
+}
+
+cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
+    return p.c.int8 ? launch_rows<true>(p, tiles ? 1 : 0, tile_rows, stream) : launch_rows<false>(p, tiles ? 1 : 0, tile_rows, stream);
+}
+
+cudaError_t launch_paged_merge(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
+    const int workers = paged_decode_workers(tile_rows, p.c.int8 != 0);
+    const unsigned grid = workers + (tiles ? kPagedTileCtas * (128 / kTileJoinRows) : 0);
+    return launch_kernel(paged_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
+}
+
+}  // namespace mha
