@@ -84,7 +84,7 @@ mha_status check_rows(const void *x, long long stride_h, long long stride_t, int
 struct Layout {
     bool tiles;      // sequences may have more than kPagedSmallRows stacked rows
     int tile_rows;   // of paged_decode.cu
-    size_t part_o, part_ml, rec, plan, tile_o, tile_ml, tile_rec, bytes;
+    size_t part_o, part_ml, join, plan, tile_o, tile_ml, tile_join, bytes;
 };
 Layout layout(int B, int g, int N, int max_new) {
     Layout l{};
@@ -102,12 +102,12 @@ Layout layout(int B, int g, int N, int max_new) {
     };
     l.part_o = take(2 * workers * l.tile_rows * kAttnHeadDim * sizeof(float));
     l.part_ml = take(2 * workers * l.tile_rows * sizeof(float2));
-    l.rec = take(workers * sizeof(int4));
+    l.join = take(workers * sizeof(PagedJoin));
     if (l.tiles) {
         l.plan = take(sizeof(int) * static_cast<size_t>(paged_plan(B, paged_most_tiles(N, B, g)).ints));
         l.tile_o = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * kAttnHeadDim * sizeof(float));
         l.tile_ml = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * sizeof(float2));
-        l.tile_rec = take(kPagedTileCtas * sizeof(int4));
+        l.tile_join = take(kPagedTileCtas * sizeof(PagedJoin));
     }
     l.bytes = at;
     return l;
@@ -175,7 +175,7 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, kPagedSmallRows);
     const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
     if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1) >= kMostLine) return MHA_ERR_UNSUPPORTED;
-    if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 2) >= kMostLine)
+    if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 8) >= kMostLine)
         return MHA_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < l.bytes) return MHA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
@@ -191,14 +191,14 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     p.small_rows = l.tiles ? std::max(kPagedSmallRows, 0) : 1 << 30;
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
-    p.rec = reinterpret_cast<int4 *>(ws + l.rec);
+    p.join = reinterpret_cast<PagedJoin *>(ws + l.join);
     p.status = status_dev;
     PagedMaps maps;
     if (l.tiles) {
         p.plan = reinterpret_cast<int *>(ws + l.plan);
         p.tile_o = reinterpret_cast<float *>(ws + l.tile_o);
         p.tile_ml = reinterpret_cast<float2 *>(ws + l.tile_ml);
-        p.tile_rec = reinterpret_cast<int4 *>(ws + l.tile_rec);
+        p.tile_join = reinterpret_cast<PagedJoin *>(ws + l.tile_join);
         if ((s = encode_paged_maps(&maps, p)) != MHA_OK) return s;
     }
     if ((s = launched(launch_paged_decode(p, l.tiles, l.tile_rows, stream), "paged attention, few rows")) != MHA_OK) return s;

@@ -103,12 +103,17 @@ struct __align__(1024) Smem {
     int abort_flag;
 };
 
-// Where a CTA's share of the line lies.
+// Where a CTA's share of the line lies.  A row tile takes kTileCost places on it
+// before those of its key tiles: what a piece costs besides them, in key tiles.
+// (Causal, 2 x 16 x 8,192: CTAs with the short row tiles of a head have 29 of them,
+// others 7; counted by key tiles alone the former took 305 us, the latter 280.)
+constexpr int kTileCost = 2;
 struct Share {
-    int tiles, keys;        // row tiles, key tiles of one K/V head
+    int tiles, keys;        // row tiles, places of one K/V head
     int start, end, share;  // of the line
     int head0, x0;          // K/V head and row tile that it starts in
 };
+__device__ __forceinline__ int place_of(const int *cum, int x) { return cum[x] + kTileCost * x; }
 
 __device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Share &sh, int t) {
     const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
@@ -124,14 +129,19 @@ __device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Shar
     w.len = s.len;
     w.pos0 = s.len - s.n + w.t0;
     w.full_hi = p.causal ? min(max(w.pos0 + 1, 0), w.len) : w.len;
-    const int cum = p.plan[at.cum + x], n = p.plan[at.cum + x + 1] - cum;
-    const int first = w.head * sh.keys + cum;
+    const int n = p.plan[at.cum + x + 1] - p.plan[at.cum + x];
+    const int first = w.head * sh.keys + place_of(p.plan + at.cum, x) + kTileCost;  // its first key tile's place
     w.j0 = max(sh.start - first, 0);
     const int end = min(n, sh.end - first);
-    w.n_kv = end - w.j0;
+    w.n_kv = end - w.j0;  // (none or less: the share ends before it)
     w.whole = w.j0 == 0 && end == n;
     return w;
 }
+
+// The t-th key tile of a piece: from the last one down.  The tiles that some rows
+// see in part are the last ones, and slow; at a piece's end they would hold up the
+// accumulators' handing on.
+__device__ __forceinline__ int tile_of(const Piece &w, int t) { return w.j0 + w.n_kv - 1 - t; }
 
 template <bool kInt8>
 __device__ __forceinline__ const Piece &piece_of(Smem<kInt8> &sm, const PagedAttnParams &p, const Share &sh, int t) {
@@ -211,11 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.tiles = p.plan[0];
     const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
     const int *cum = p.plan + at.cum;
-    sh.keys = cum[sh.tiles];
+    sh.keys = place_of(cum, sh.tiles);
     const int total = p.c.Hkv * sh.keys;
     sh.share = (total + G - 1) / G;
     if (total == 0 || static_cast<long long>(cta) * sh.share >= total) {
-        if (threadIdx.x == 0) p.tile_rec[cta] = make_int4(-1, 0, 0, 0);
+        if (threadIdx.x == 0) p.tile_join[cta] = PagedJoin{};
         return;
     }
     if (warp == kMmaSWarp) {
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         const int s0 = sh.start - sh.head0 * sh.keys, s1 = sh.end - 1 - head1 * sh.keys;
         for (int x = threadIdx.x; x < sh.tiles; x += kThreads) {
-            const int lo = cum[x], hi = cum[x + 1];
+            const int lo = place_of(cum, x), hi = place_of(cum, x + 1);
             if (lo <= s0 && s0 < hi) sm.at_x = x;
             if (lo <= s1 && s1 < hi) sm.n_pieces = x;
         }
@@ -238,41 +248,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     sh.x0 = sm.at_x;
-    const int pieces = (head1 - sh.head0) * sh.tiles + sm.n_pieces - sh.x0 + 1;
+    int pieces = (head1 - sh.head0) * sh.tiles + sm.n_pieces - sh.x0 + 1;
     for (int t = threadIdx.x; t < min(pieces, kTable); t += kThreads) sm.table[t] = make_piece(p, sh, t);
+    // the last one, if the share ends before its first key tile, is the next CTA's
+    if (make_piece(p, sh, pieces - 1).n_kv <= 0) --pieces;
     __syncthreads();
     const uint32_t tmem = sm.tmem_base;
     const AbortState ab{&sm.abort_flag, p.status, 0};
-    const int my_tiles = sh.end - sh.start;
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------ TMA producer
-        // Lane i < boxes loads the i-th box of K and of V; its page is looked up
-        // a tile ahead.
+        // Lane i < boxes loads the i-th box of K and of V.  The pages of the next
+        // 32 boxes, 32 / boxes tiles, are looked up at once, a lane each: a look-up
+        // a tile would be a trip to L2 for every one (341 us, causal 2 x 16 x 8,192).
         const int box = min(p.c.page & -p.c.page, BN), boxes = BN / box;  // gcd(page, 128)
         const int none = max(p.c.num_pages, 1);                            // past the tensor: zeros
+        const int window = 32 / boxes;                                     // tiles
+        const int my_box = lane % boxes, my_tile = lane / boxes;
         int n = 0, v = 0;
         bool ok = true;
         int page = none, in_page = 0;
         uint32_t gone = 0;  // 16-key bits of this lane's box, if it is seen but not there
-        auto look_up = [&](const Piece &w, int j) {
-            const int key = j * BN + lane * box;
+        bool any_gone = false;
+        auto look_up = [&](const Piece &w, int jt) {
+            const int j = tile_of(w, jt + my_tile), key = j * BN + my_box * box;
             page = none;
             in_page = 0;
             gone = 0;
-            if (lane < boxes && key < w.len) {
+            if (j >= w.j0 && key < w.len) {
                 const int i = key / p.c.page, pg = paged_page(p.c, w.b, i);
                 if (pg >= 0) {
                     page = pg;
                     in_page = key - i * p.c.page;
                 } else {
-                    gone = ((1u << (box / 16)) - 1u) << (lane * (box / 16));
+                    gone = ((1u << (box / 16)) - 1u) << (my_box * (box / 16));
                 }
             }
+            any_gone = __any_sync(0xffffffffu, gone != 0u);
         };
         for (int t = 0; ok && t < pieces; ++t) {
             const Piece &w = piece_of<kInt8>(sm, p, sh, t);
-            look_up(w, w.j0);
             const int qbuf = v & 1;
             if (v >= 2 && !(ok = warp_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
             if (lane == 0) {
@@ -281,28 +296,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(&maps.q, &sm.q_full[qbuf], sm.q[qbuf], 0, w.head * g, w.row0);
             }
             ++v;
-            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
+            int at = window;  // the tile's place in the window
+            for (int jt = 0; jt < w.n_kv; ++jt, ++n, ++at) {
                 const int st = n % STAGES;
-                const int pg = page, in = in_page;
-                const uint32_t bad = __reduce_or_sync(0xffffffffu, gone);
-                if (jt + 1 < w.n_kv) look_up(w, w.j0 + jt + 1);
+                if (at == window) {
+                    look_up(w, jt);
+                    at = 0;
+                }
+                const uint32_t bad = any_gone ? __reduce_or_sync(0xffffffffu, my_tile == at ? gone : 0u) : 0u;
                 if constexpr (kInt8) {
                     const int rs = n % kRaw;
                     if (n >= kRaw && !(ok = warp_wait(&sm.raw.empty[rs], ((n / kRaw) - 1) & 1, ab))) break;
-                    const bool scales = lane < boxes && pg < none;
+                    const bool scales = my_tile == at && page < none;
                     const uint32_t bytes = 2 * kRawBytes + 2u * box * __popc(__ballot_sync(0xffffffffu, scales));
                     if (lane == 0) {
                         sm.raw.bad[rs] = bad;
                         mbar_arrive_expect_tx(&sm.raw.full[rs], bytes);
                     }
                     __syncwarp();
-                    if (lane < boxes) {
-                        tma_load_4d(&maps.k, &sm.raw.full[rs], sm.raw.k[rs] + lane * box * HD, 0, in, w.head, pg);
-                        tma_load_4d(&maps.v, &sm.raw.full[rs], sm.raw.v[rs] + lane * box * HD, 0, in, w.head, pg);
+                    if (my_tile == at) {
+                        tma_load_4d(&maps.k, &sm.raw.full[rs], sm.raw.k[rs] + my_box * box * HD, 0, in_page, w.head, page);
+                        tma_load_4d(&maps.v, &sm.raw.full[rs], sm.raw.v[rs] + my_box * box * HD, 0, in_page, w.head, page);
                         if (scales) {
-                            const long long from = (static_cast<long long>(pg) * p.c.Hkv + w.head) * p.c.page + in;
-                            bulk_load_1d(sm.raw.ks[rs] + lane * box, p.c.k_scales + from, box, &sm.raw.full[rs]);
-                            bulk_load_1d(sm.raw.vs[rs] + lane * box, p.c.v_scales + from, box, &sm.raw.full[rs]);
+                            const long long from = (static_cast<long long>(page) * p.c.Hkv + w.head) * p.c.page + in_page;
+                            bulk_load_1d(sm.raw.ks[rs] + my_box * box, p.c.k_scales + from, box, &sm.raw.full[rs]);
+                            bulk_load_1d(sm.raw.vs[rs] + my_box * box, p.c.v_scales + from, box, &sm.raw.full[rs]);
                         }
                     }
                 } else {
@@ -312,9 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
                     }
                     __syncwarp();
-                    if (lane < boxes) {
-                        tma_load_4d(&maps.k, &sm.kv_full[st], sm.k[st] + lane * box * (HD * 2), 0, in, w.head, pg);
-                        tma_load_4d(&maps.v, &sm.kv_full[st], sm.v[st] + lane * box * (HD * 2), 0, in, w.head, pg);
+                    if (my_tile == at) {
+                        tma_load_4d(&maps.k, &sm.kv_full[st], sm.k[st] + my_box * box * (HD * 2), 0, in_page, w.head, page);
+                        tma_load_4d(&maps.v, &sm.kv_full[st], sm.v[st] + my_box * box * (HD * 2), 0, in_page, w.head, page);
                     }
                 }
             }
@@ -380,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
                 // Rows of the last page past the length: their weights are 0, and
                 // 0 times whatever the page holds has to be 0.
-                const int rows = w.len - (w.j0 + jt) * BN;
+                const int rows = w.len - tile_of(w, jt) * BN;
                 if (!kInt8 && rows < BN) {
                     uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
                     for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
                 if ((n & 1) != half) continue;
-                const int j = w.j0 + jt;
+                const int j = tile_of(w, jt);
                 const int sb = n % kSBufs, st = n % STAGES;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
                 if (!ok) break;
@@ -457,12 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
-                // (complete: the scores are of this tile; acquires its `bad`)
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_full[st], (n / STAGES) & 1, ab));
-                if (!ok) break;
-                const uint32_t bad = sm.bad[st];
                 tc_fence_after_sync();
                 const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                // (written before the tile was handed to the S issuer, which waited
+                // for that before it issued the products whose end s_full tells)
+                const uint32_t bad = *static_cast<volatile uint32_t *>(&sm.bad[st]);
                 const bool edge = j * BN + BN > w.full_hi || bad != 0;
                 int rd_first = 0;
                 if (!edge && long_piece) {
@@ -652,10 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kOutWarp && lane == 0) {
             // the block that joins a row tile is that of the first CTA that begins inside it
             const Piece &w = sm.table[0];
-            const int first = sh.start - w.j0;
             const int n = cum[sh.x0 + 1] - cum[sh.x0];
-            p.tile_rec[cta] = w.j0 > 0 && w.j0 <= sh.share ? make_int4(w.b, w.t0, w.head, (first + n - 1) / sh.share)
-                                                           : make_int4(-1, 0, 0, 0);
+            PagedJoin j{};
+            if (pieces > 0 && w.j0 > 0 && w.j0 <= sh.share)
+                j = PagedJoin{w.tokens * g, 0, w.head, w.row0, (sh.start - w.j0 + n - 1) / sh.share};
+            p.tile_join[cta] = j;
         }
         // The v-th piece's rows, once its products are complete.
         auto output = [&](int v) -> bool {
@@ -719,24 +737,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!output(v)) break;
         } else {
             const int tid = threadIdx.x - 32 * kOutWarp;
-            // the piece that the next tile to be written belongs to
-            int piece = 0, jt = 0, n_kv = sm.table[0].n_kv, j0 = sm.table[0].j0, len = sm.table[0].len;
-            auto convert = [&](int n) {
+            // 4 rows of a tile, a quarter of each: rows tid / 4 + 32 i
+            const int row0 = tid >> 2, quarter = tid & 3;
+            auto convert = [&](int n, int keys) {  // rows from `keys` on are cleared
                 const int rs = n % kRaw, st = n % STAGES;
                 const uint32_t bad = sm.raw.bad[rs];
-                const int keys = len - (j0 + jt) * BN;  // rows past it are cleared
+                uint4 u[8];
+                uint32_t e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // (all loads before the first store: they may not pass it)
+                    u[i] = reinterpret_cast<const uint4 *>(i < 4 ? sm.raw.k[rs] : sm.raw.v[rs])[(i & 3) * 128 + tid];
+                    e[i] = (i < 4 ? sm.raw.ks[rs] : sm.raw.vs[rs])[row0 + 32 * (i & 3)];
+                }
+                if (keys < BN || bad != 0u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = row0 + 32 * (i & 3);
+                        if (row >= keys || (bad >> (row >> 4) & 1u)) e[i] = 0u;
+                    }
+                }
+                uint4 *k = reinterpret_cast<uint4 *>(sm.k[st]) + row0 * 8, *v = reinterpret_cast<uint4 *>(sm.v[st]) + row0 * 8;
+                const int at = (2 * quarter) ^ (row0 & 7);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int x = (i & 3) * 128 + tid, row = x >> 2, quarter = x & 3;
-                    const uint8_t *from = i < 4 ? sm.raw.k[rs] : sm.raw.v[rs];
-                    const uint32_t e = (i < 4 ? sm.raw.ks[rs] : sm.raw.vs[rs])[row];
-                    const uint4 u = reinterpret_cast<const uint4 *>(from)[x];
-                    const bool there = row < keys && !(bad >> (row >> 4) & 1u);
                     uint4 a, b;
-                    to_bf16(u, there ? paged_power(e) : 0.f, a, b);
-                    uint4 *to = reinterpret_cast<uint4 *>(i < 4 ? sm.k[st] : sm.v[st]) + row * 8;
-                    to[(2 * quarter) ^ (row & 7)] = a;
-                    to[(2 * quarter + 1) ^ (row & 7)] = b;
+                    to_bf16(u[i], paged_power(e[i]), a, b);
+                    uint4 *to = (i < 4 ? k : v) + 256 * (i & 3);
+                    to[at] = a;
+                    to[at ^ 1] = b;
                 }
                 if (tid == 0) sm.bad[st] = bad;
                 fence_proxy_async_smem();
@@ -745,48 +773,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&sm.kv_full[st]);
                     mbar_arrive(&sm.raw.empty[rs]);
                 }
-                if (++jt == n_kv && ++piece < pieces) {
-                    const Piece &w = piece_of<true>(sm, p, sh, piece);
-                    jt = 0;
-                    n_kv = w.n_kv;
-                    j0 = w.j0;
-                    len = w.len;
-                }
             };
-            auto ready = [&](uint64_t *bar, int parity) {
-                return __all_sync(0xffffffffu, mbar_try_wait(bar, static_cast<uint32_t>(parity)));
+            auto wait = [&](uint64_t *bar, int parity) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(parity), ab));
             };
-            int n = 0, v = 0;
-            unsigned long long since = 0;
-            while (v < pieces) {
-                if (n == my_tiles) {
-                    if (!output(v)) break;
-                    ++v;
-                    continue;
-                }
-                const int rs = n % kRaw, st = n % STAGES;
-                if (ready(&sm.o_final, v & 1)) {
-                    if (!output(v)) break;
-                    ++v;
-                } else if (n < STAGES || ready(&sm.kv_empty[st], ((n / STAGES) - 1) & 1)) {
-                    // (raw tiles wait for nothing but these warps)
-                    if (!__all_sync(0xffffffffu, mbar_wait(&sm.raw.full[rs], (n / kRaw) & 1, ab))) break;
-                    convert(n);
-                    ++n;
-                } else {
-                    // neither: look again, within the waits' limit
-                    const unsigned long long now = global_timer_ns();
-                    if (since == 0) since = now;
-                    bool stop = should_abort(ab);
-                    if (now - since > kWaitLimitNs) {
-                        raise_abort(ab);
-                        stop = true;
+            // Tiles are written as stages come free.  Behind a piece's last one the
+            // next piece's wait for its output at the latest, when they wait
+            // for a stage that only products behind the output give back.
+            int n = 0, v = 0;  // tiles written, pieces put out
+            bool ok = true;
+            for (int piece = 0; ok && piece < pieces; ++piece) {
+                const Piece &w = piece_of<true>(sm, p, sh, piece);
+                const int n_kv = w.n_kv, len = w.len, first = w.j0;
+                for (int jt = 0; ok && jt < n_kv; ++jt, ++n) {
+                    unsigned long long since = 0;
+                    while (ok && n >= STAGES && v < piece) {
+                        if (__all_sync(0xffffffffu, mbar_test(&sm.o_final, static_cast<uint32_t>(v & 1)))) {
+                            ok = output(v++);
+                        } else if (__all_sync(0xffffffffu, mbar_test(&sm.kv_empty[n % STAGES], static_cast<uint32_t>((n / STAGES - 1) & 1)))) {
+                            break;
+                        } else {
+                            // neither: look again, within the waits' limit
+                            const unsigned long long now = global_timer_ns();
+                            if (since == 0) since = now;
+                            bool stop = should_abort(ab);
+                            if (now - since > kWaitLimitNs) {
+                                raise_abort(ab);
+                                stop = true;
+                            }
+                            if (__any_sync(0xffffffffu, stop)) ok = false;
+                        }
                     }
-                    if (__any_sync(0xffffffffu, stop)) break;
-                    continue;
+                    if (ok && n >= STAGES) ok = wait(&sm.kv_empty[n % STAGES], (n / STAGES - 1) & 1);
+                    // (raw tiles wait for nothing but these warps)
+                    if (ok) ok = wait(&sm.raw.full[n % kRaw], (n / kRaw) & 1);
+                    if (ok) convert(n, len - (first + n_kv - 1 - jt) * BN);
                 }
-                since = 0;
             }
+            while (ok && v < pieces) ok = output(v++);
         }
     }
 

@@ -284,6 +284,12 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedRows &k, const P
 // k, v: (B, Hkv, T, 64) bf16.
 cudaError_t launch_paged_read(const PagedCache &c, __nv_bfloat16 *k, __nv_bfloat16 *v, int T, cudaStream_t stream);
 
+// An item whose key range is divided over CTAs or warps, left by the first worker
+// that begins inside it: its rows (0: none to join), the first one's place among
+// the K/V head's stacked rows from packed row row0 on, and the item's last worker.
+struct __align__(16) PagedJoin {
+    int rows, x0, head, row0, last;
+};
 struct PagedAttnParams {
     PagedCache c;
     PagedRows q;
@@ -299,12 +305,13 @@ struct PagedAttnParams {
     // paged_decode.cu: partial sums of key ranges that end inside an item
     float *part_o;         // (2 workers, rows of a tile, 64)
     float2 *part_ml;       // (2 workers, rows of a tile): reference in log2 units, sum
-    int4 *rec;             // (workers): the item that a worker's merge block finishes
-    // attn_paged_bf16.cu: its row tiles, listed by the launch before it, and the same
-    int *plan;             // [0] the number of row tiles; then kPlanHead on: see PagedPlan
+    PagedJoin *join;       // (workers)
+    // attn_paged_bf16.cu: its row tiles, listed by the launch before it ([0] their
+    // number, then PagedPlan's lists), and the same
+    int *plan;
     float *tile_o;
     float2 *tile_ml;
-    int4 *tile_rec;
+    PagedJoin *tile_join;
     int *status;
 };
 constexpr int kPagedSmallRows = 64;

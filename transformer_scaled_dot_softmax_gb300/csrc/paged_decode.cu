@@ -28,6 +28,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
@@ -38,12 +40,15 @@ namespace {
 constexpr int HD = kAttnHeadDim;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 // A row's reference serves until a unit's weights sum to more than this.
 constexpr float kSumMax = 65536.0f;
 // A worker's least share of the line, in units: what a piece costs to write
 // and join is worth a few units of reading.
 constexpr int kLeastShare = 4;
+
+// CTAs of an SM, by the rows of an item in eights.
+constexpr int paged_decode_ctas(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
 
 template <bool kInt8>
 constexpr int kUnitKeys = kInt8 ? 32 : 16;
@@ -85,13 +90,13 @@ __device__ __forceinline__ void to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<uint32_t *>(&y);
 }
 
-// One lane's part of a unit.
-template <bool kInt8>
-struct Unit {
-    uint4 k[4];      // bf16: keys l/4 and l/4 + 8, two pieces of 8 features; int8: keys l/4 + 8 i, 16 features
-    uint4 v[4];      // bf16: keys 2c, 2c+1, 2c+8, 2c+9 (c = l % 4), features 8 (l/4) on; int8: two such keys in each
-    uint32_t ks[kInt8 ? 4 : 1], vs[kInt8 ? 4 : 1];  // stored exponents: of those keys of K; pairs of V's
-    uint32_t there;  // a bit for every 16 keys: their page is there
+// One lane's part of a unit's K, or of its V.
+struct Part {
+    // K, bf16: keys l/4 and l/4 + 8, two pieces of 8 features; int8: keys l/4 + 8 i,
+    // 16 features.  V, bf16: keys 2c, 2c+1, 2c+8, 2c+9 (c = l % 4), features 8 (l/4)
+    // on; int8: two such keys in each.
+    uint4 x[4];
+    uint32_t s;  // int8: the stored exponent of the unit's key `lane`
 };
 
 struct Shape {
@@ -184,7 +189,7 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
 }
 
 template <bool kInt8, int kN>
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnParams p, int list) {
+__global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_kernel(const PagedAttnParams p, int list) {
     constexpr int kRows = 8 * kN, kKeys = kUnitKeys<kInt8>, kBlocks = kKeys / 16;
     __shared__ int warp_sums[kWarps], at_b[kWarps], at_start[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -200,20 +205,19 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
     const int per_page = p.c.page / 16;
 
     // The line's length, the shares, and where this warp's begins.
-    int total = 0;
+    if (lane == 0) at_b[warp] = -1;
+    int total = 0, mine = 0, excl = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        int excl;
-        total += block_sum(b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0, warp_sums, excl);
+        mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
+        total += block_sum(mine, warp_sums, excl);
     }
     const int share = max((total + workers - 1) / workers, kLeastShare);
-    if (lane == 0) at_b[warp] = -1;
     int base = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        int excl;
-        const int mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
-        const int sum = block_sum(mine, warp_sums, excl);
+        if (p.c.B > kThreads) mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
+        const int sum = p.c.B > kThreads ? block_sum(mine, warp_sums, excl) : 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             // (a share past the line's end may start past 2^31)
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
     __syncthreads();
     int b = at_b[warp];
     if (b < 0) {
-        if (lane == 0) p.rec[me] = make_int4(-1, 0, 0, 0);
+        if (lane == 0) p.join[me] = PagedJoin{};
         return;
     }
     const int start = me * share;
@@ -242,9 +246,10 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
         const int head = item / sh.tiles, tile = item - head * sh.tiles;
         const int rows = min(s.n, p.max_new) * g - tile * kRows;  // of this item, if less than kRows
         if (first_piece && lane == 0) {
-            // The block of the first worker that begins inside an item joins it.
-            p.rec[me] = u0 > 0 && u0 <= share ? make_int4(b, item, (start - u0 + sh.units - 1) / share, 0)
-                                              : make_int4(-1, 0, 0, 0);
+            PagedJoin j{};
+            if (u0 > 0 && u0 <= share)
+                j = PagedJoin{min(rows, kRows), tile * kRows, head, s.row0, (start - u0 + sh.units - 1) / share};
+            p.join[me] = j;
         }
 
         // Queries: a lane's features of row l/4, in every 8 rows.
@@ -307,62 +312,69 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
             page = (sub0 + lane) * 16 < s.len ? paged_page(p.c, b, i) : -1;
         };
         look_up(sub0);
-        auto load = [&](int u, Unit<kInt8> &x) {
+        // Where the unit's blocks of 16 keys lie, how many of their keys are there;
+        // the exponent of the lane's key.
+        long long at[kBlocks], s_at = 0;
+        int valid[kBlocks], s_valid = 0;
+        bool full = false;  // all of them
+        auto place = [&](int u) {
             if (u * kBlocks - sub0 >= 32) look_up(u * kBlocks);
-            x.there = 0;
+            full = (u + 1) * kKeys <= s.len;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
                 const int pg = __shfl_sync(0xffffffffu, page, u * kBlocks + i - sub0);
                 const int in = __shfl_sync(0xffffffffu, in_page, u * kBlocks + i - sub0);
-                if (pg >= 0) x.there |= 1u << i;
-                const int key0 = (u * kBlocks + i) * 16;
-                const int valid = pg >= 0 ? s.len - key0 : 0;  // keys of the 16 that are there
                 const int row = head * p.c.page + in;
-                const long long at = pg * p.c.stride + static_cast<long long>(row) * HD;
-                if constexpr (kInt8) {
-                    const int8_t *kp = static_cast<const int8_t *>(p.c.k) + at, *vp = static_cast<const int8_t *>(p.c.v) + at;
-                    const long long sat = static_cast<long long>(pg) * p.c.Hkv * p.c.page + row;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x.k[2 * i + j] = make_uint4(0u, 0u, 0u, 0u);
-                        x.ks[2 * i + j] = 0u;
-                        if (l4 + 8 * j < valid) {
-                            x.k[2 * i + j] = load16(kp + (l4 + 8 * j) * HD + 16 * c);
-                            x.ks[2 * i + j] = __ldg(p.c.k_scales + sat + l4 + 8 * j);
-                        }
-                        uint2 v0 = make_uint2(0u, 0u), v1 = v0;
-                        const int kv = 2 * c + 8 * j;
-                        x.vs[2 * i + j] = 0u;
-                        if (kv < valid) {
-                            v0 = load8(vp + kv * HD + 8 * l4);
-                            // (both exponents: a page's rows come in 16s; the second is cut off below)
-                            x.vs[2 * i + j] = __ldg(reinterpret_cast<const unsigned short *>(p.c.v_scales + sat + kv));
-                        }
-                        if (kv + 1 < valid)
-                            v1 = load8(vp + (kv + 1) * HD + 8 * l4);
-                        else
-                            x.vs[2 * i + j] &= 0xffu;
-                        x.v[2 * i + j] = make_uint4(v0.x, v0.y, v1.x, v1.y);
-                    }
-                } else {
-                    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(p.c.k) + at,
-                                        *vp = static_cast<const __nv_bfloat16 *>(p.c.v) + at;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        x.k[2 * j] = x.k[2 * j + 1] = make_uint4(0u, 0u, 0u, 0u);
-                        if (l4 + 8 * j < valid) {
-                            x.k[2 * j] = load16(kp + (l4 + 8 * j) * HD + 8 * c);
-                            x.k[2 * j + 1] = load16(kp + (l4 + 8 * j) * HD + 8 * c + 32);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int kv = 2 * c + (j & 1) + 8 * (j >> 1);
-                        x.v[j] = make_uint4(0u, 0u, 0u, 0u);
-                        if (kv < valid) x.v[j] = load16(vp + kv * HD + 8 * l4);
-                    }
+                at[i] = pg * p.c.stride + row * HD;
+                valid[i] = pg >= 0 ? s.len - (u * kBlocks + i) * 16 : 0;
+                full = full && pg >= 0;
+                if (kInt8 && lane >> 4 == i) {
+                    s_at = static_cast<long long>(pg) * (p.c.Hkv * p.c.page) + row + (lane & 15);
+                    s_valid = valid[i];
                 }
             }
+        };
+        // K or V of the unit that place() has found
+        auto load = [&](auto is_v, Part &to) {
+            constexpr bool kV = decltype(is_v)::value;
+            auto rows = [&](auto all) {
+                constexpr bool kAll = decltype(all)::value;
+                to.s = 0u;
+                if (kInt8 && (kAll || (lane & 15) < s_valid)) to.s = __ldg((kV ? p.c.v_scales : p.c.k_scales) + s_at);
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    const void *base = kV ? p.c.v : p.c.k;
+                    if constexpr (kInt8) {
+                        const int8_t *from = static_cast<const int8_t *>(base) + at[i];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint4 &x = to.x[2 * i + j];
+                            if constexpr (kV) {
+                                const int key = 2 * c + 8 * j;
+                                uint2 v0 = make_uint2(0u, 0u), v1 = v0;
+                                if (kAll || key < valid[i]) v0 = load8(from + key * HD + 8 * l4);
+                                if (kAll || key + 1 < valid[i]) v1 = load8(from + (key + 1) * HD + 8 * l4);
+                                x = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                            } else {
+                                x = make_uint4(0u, 0u, 0u, 0u);
+                                if (kAll || l4 + 8 * j < valid[i]) x = load16(from + (l4 + 8 * j) * HD + 16 * c);
+                            }
+                        }
+                    } else {
+                        const __nv_bfloat16 *from = static_cast<const __nv_bfloat16 *>(base) + at[i];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int key = kV ? 2 * c + (j & 1) + 8 * (j >> 1) : l4 + 8 * (j >> 1);
+                            to.x[j] = make_uint4(0u, 0u, 0u, 0u);
+                            if (kAll || key < valid[i]) to.x[j] = load16(from + key * HD + (kV ? 8 * l4 : 8 * c + 32 * (j & 1)));
+                        }
+                    }
+                }
+            };
+            if (full)
+                rows(std::true_type{});
+            else
+                rows(std::false_type{});
         };
 
         float o[kN][4][4], m[kN][2], l[kN][2];
@@ -374,7 +386,15 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
             l[n][0] = l[n][1] = 0.f;
         }
 
-        auto work = [&](int u, const Unit<kInt8> &x) {
+        // K of the next unit is on its way while this one's weights are taken, its V
+        // while the next one's scores are: 32 registers instead of 64, and four
+        // CTAs an SM.
+        Part kp, vp;
+        place(u0);
+        load(std::false_type{}, kp);
+        load(std::true_type{}, vp);
+#pragma unroll 1
+        for (int u = u0; u < u1; ++u) {
             // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
             float st[kN][kBlocks][4];
 #pragma unroll
@@ -383,13 +403,13 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if constexpr (kInt8) {
-                        const uint4 &w = x.k[2 * i + j];
+                        const uint4 &w = kp.x[2 * i + j];
                         to_f16(w.x, ka[j][0], ka[j][1]);
                         to_f16(w.y, ka[j][2], ka[j][3]);
                         to_f16(w.z, ka[j][4], ka[j][5]);
                         to_f16(w.w, ka[j][6], ka[j][7]);
                     } else {
-                        const uint4 &w = x.k[2 * j], &z = x.k[2 * j + 1];
+                        const uint4 &w = kp.x[2 * j], &z = kp.x[2 * j + 1];
                         ka[j][0] = w.x, ka[j][1] = w.y, ka[j][2] = w.z, ka[j][3] = w.w;
                         ka[j][4] = z.x, ka[j][5] = z.y, ka[j][6] = z.z, ka[j][7] = z.w;
                     }
@@ -408,34 +428,32 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
                     }
                 }
             }
-            // in log2 units; a key that is not seen to minus infinity
-            const int key0 = u * kKeys;
+            int here[kBlocks];  // keys of a block that are there
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
+            for (int i = 0; i < kBlocks; ++i) here[i] = valid[i];
+            const bool whole = full && (u + 1) * kKeys <= least;  // every row sees every key
+            if constexpr (kInt8) {
 #pragma unroll
                 for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y = st[n][i][e];
-                        if constexpr (kInt8) y *= paged_power(x.ks[2 * i + (e >> 1)]);
-                        st[n][i][e] = y * mul[n][e & 1];
+                    for (int j = 0; j < 2; ++j) {
+                        const float power = paged_power(__shfl_sync(0xffffffffu, kp.s, 16 * i + 8 * j + l4));
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) {
+                            st[n][i][2 * j] *= power;
+                            st[n][i][2 * j + 1] *= power;
+                        }
                     }
-            if (key0 + kKeys > least || x.there != (1u << kBlocks) - 1u) {
-#pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (key0 + 16 * i + l4 + 8 * (e >> 1) >= min(lim[n][e & 1], s.len) || !(x.there >> i & 1u))
-                                st[n][i][e] = -INFINITY;
             }
-            // weights against the reference in hand; where a row has none yet, or
-            // its sum leaves the range, against the unit's maximum
+            if (u + 1 < u1) {
+                place(u + 1);
+                load(std::false_type{}, kp);
+            }
+            // Weights against the reference in hand.  `shift`: -reference, 0 before
+            // there is one.
             uint32_t pk[kN][kBlocks][2];
             float sum[kN][2];
-#pragma unroll 1
-            for (int attempt = 0;; ++attempt) {
+            auto weights = [&](bool masked) -> bool {
                 bool need = false;
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
@@ -445,33 +463,52 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
                     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            pk[n][i][j] = pack_bf16x2(ex2_approx(st[n][i][2 * j] - r0), ex2_approx(st[n][i][2 * j + 1] - r1));
+                            float y0 = masked ? st[n][i][2 * j] - r0 : fmaf(st[n][i][2 * j], mul[n][0], -r0);
+                            float y1 = masked ? st[n][i][2 * j + 1] - r1 : fmaf(st[n][i][2 * j + 1], mul[n][1], -r1);
+                            pk[n][i][j] = pack_bf16x2(ex2_approx(y0), ex2_approx(y1));
                             add_bf16x2_to_f32(sum[n][0], sum[n][1], pk[n][i][j]);
                         }
                     need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax) || m[n][0] == -INFINITY || m[n][1] == -INFINITY;
                 }
-                if (attempt == 1 || !__any_sync(0xffffffffu, need)) break;
+                return __any_sync(0xffffffffu, need);
+            };
+            if (!whole || weights(false)) {
+                // Scores in log2 units, a key that is not seen at minus infinity;
+                // where a row has no reference yet, or its sum leaves the
+                // range, against the unit's maximum.
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float top = m[n][r];
+                    for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                        for (int i = 0; i < kBlocks; ++i) top = fmax3(top, st[n][i][r], st[n][i][2 + r]);
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        if (m[n][r] != -INFINITY) {
-                            const float alpha = ex2_approx(m[n][r] - top);
-                            l[n][r] *= alpha;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[n][i][r] *= alpha;
-                                o[n][i][2 + r] *= alpha;
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const int in = l4 + 8 * (e >> 1), key = u * kKeys + 16 * i + in;
+                            st[n][i][e] = in < here[i] && key < lim[n][e & 1] ? st[n][i][e] * mul[n][e & 1] : -INFINITY;
                         }
-                        m[n][r] = top;
-                    }
+                if (weights(true)) {
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            float top = m[n][r];
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i) top = fmax3(top, st[n][i][r], st[n][i][2 + r]);
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            if (m[n][r] != -INFINITY) {
+                                const float alpha = ex2_approx(m[n][r] - top);
+                                l[n][r] *= alpha;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[n][i][r] *= alpha;
+                                    o[n][i][2 + r] *= alpha;
+                                }
+                            }
+                            m[n][r] = top;
+                        }
+                    weights(true);
+                }
             }
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
@@ -485,8 +522,9 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
                 if constexpr (kInt8) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const uint4 &w = x.v[2 * i + j];
-                        const float s0 = paged_power(x.vs[2 * i + j] & 0xffu), s1 = paged_power(x.vs[2 * i + j] >> 8);
+                        const uint4 &w = vp.x[2 * i + j];
+                        const float s0 = paged_power(__shfl_sync(0xffffffffu, vp.s, 16 * i + 8 * j + 2 * c));
+                        const float s1 = paged_power(__shfl_sync(0xffffffffu, vp.s, 16 * i + 8 * j + 2 * c + 1));
                         const uint64_t s2 = f32x2_pack(s0, s1), off = f32x2_pack(-8388736.f * s0, -8388736.f * s1);
                         const uint32_t a[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u}, d[2] = {w.z ^ 0x80808080u, w.w ^ 0x80808080u};
 #pragma unroll
@@ -501,8 +539,8 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
                         }
                     }
                 } else {
-                    const uint32_t w[4][4] = {{x.v[0].x, x.v[0].y, x.v[0].z, x.v[0].w}, {x.v[1].x, x.v[1].y, x.v[1].z, x.v[1].w},
-                                              {x.v[2].x, x.v[2].y, x.v[2].z, x.v[2].w}, {x.v[3].x, x.v[3].y, x.v[3].z, x.v[3].w}};
+                    const uint32_t w[4][4] = {{vp.x[0].x, vp.x[0].y, vp.x[0].z, vp.x[0].w}, {vp.x[1].x, vp.x[1].y, vp.x[1].z, vp.x[1].w},
+                                              {vp.x[2].x, vp.x[2].y, vp.x[2].z, vp.x[2].w}, {vp.x[3].x, vp.x[3].y, vp.x[3].z, vp.x[3].w}};
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
                         va[f][0] = __byte_perm(w[0][f], w[1][f], 0x5410);
@@ -518,18 +556,7 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
                     for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
                 }
             }
-        };
-
-        Unit<kInt8> x0, x1;
-        load(u0, x0);
-#pragma unroll 1
-        for (int u = u0; u < u1; u += 2) {
-            if (u + 1 < u1) load(u + 1, x1);
-            work(u, x0);
-            if (u + 1 < u1) {
-                if (u + 2 < u1) load(u + 2, x0);
-                work(u + 1, x1);
-            }
+            if (u + 1 < u1) load(std::true_type{}, vp);
         }
 
         // The item, or the piece: slot 2 me of one that began before this
@@ -582,102 +609,111 @@ __global__ void __launch_bounds__(kThreads) paged_decode_kernel(const PagedAttnP
 
 // ------------------------------------------------------------ joining partial sums
 //   o = (sum_s w_s O_s) / (sum_s w_s l_s),  w_s = 2^(m_s - M),  M = max_s m_s
-// over the pieces of an item: the tail slot of worker `first`, then the head
-// slots up to worker `last`.  16 lanes take one row (4 features each); groups
-// that would be idle share a row's pieces.  A piece without a visible key has
-// m = -inf, l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is
-// taken as paged_level gives it.
+// over the pieces of an item: the tail slot of the worker before the record's, then
+// the head slots up to the item's last worker, in that order whatever the timing.
+// 16 lanes take one row (4 features each), up to 8 pieces at a time; groups that
+// would be idle share a row's pieces.  A piece without a visible key has m = -inf,
+// l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is taken as
+// paged_level gives it.
+//
+// Bound by latency: a block for every worker, most of which find nothing to join,
+// and for every 16 rows of a CTA's row tile; small, so that all of them are
+// resident together.
+constexpr int kMergeRows = 16;  // of a row tile of 128
+constexpr int kGroups = kMergeThreads / 16;
+constexpr int kBatch = 8;
+
 __device__ __forceinline__ float piece_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
 
-template <typename Out>
-__device__ void join(const float *part_o, const float2 *part_ml, int slot_rows, int first, int last, int row0, int rows,
-                     float (&sh_o)[kMergeThreads / 16][HD], float2 (&sh_ml)[kMergeThreads / 16], Out out) {
-    constexpr int kGroups = kMergeThreads / 16;
+// A partial sum, and others joined to it.
+struct Sum {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // pieces with l = 0 are left out
+    __device__ __forceinline__ void add(const float2 (&ml)[kBatch], const float4 (&x)[kBatch]) {
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (ml[i].y != 0.f) top = fmaxf(top, paged_level(ml[i].x, ml[i].y).m);
+        const float a = piece_weight(m, top);
+        m = top;
+        l *= a;
+        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (ml[i].y != 0.f) {
+                const PagedLevel v = paged_level(ml[i].x, ml[i].y);
+                const float w = piece_weight(v.m, top) * v.down;
+                l += ml[i].y * w;
+                o = make_float4(o.x + x[i].x * w, o.y + x[i].y * w, o.z + x[i].z * w, o.w + x[i].w * w);
+            }
+    }
+};
+
+__global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const PagedAttnParams p, int workers, int tile_rows) {
+    __shared__ float4 sh_o[kGroups][16];
+    __shared__ float2 sh_ml[kGroups];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int x = blockIdx.x;
+    const bool small = x < workers;
+    const int w = small ? x : (x - workers) / (128 / kMergeRows);
+    const int from = small ? 0 : (x - workers - w * (128 / kMergeRows)) * kMergeRows;
+    const PagedJoin j = small ? p.join[w] : p.tile_join[w];
+    if (j.rows <= from) return;
+    const int g = p.H / p.c.Hkv;
     const int grp = threadIdx.x / 16, lane = threadIdx.x & 15;
+    const int rows = small ? j.rows : min(j.rows - from, kMergeRows), slot_rows = small ? tile_rows : 128;
+    const float *part_o = small ? p.part_o : p.tile_o;
+    const float2 *part_ml = small ? p.part_ml : p.tile_ml;
+    const int pieces = j.last - w + 2;
     int per = 1;  // groups of a row
     while (per * 2 * rows <= kGroups) per *= 2;
-    const int pieces = last - first + 1;
     for (int r0 = 0; r0 < rows; r0 += kGroups / per) {
         const int row = r0 + grp / per, part = grp % per;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 ml[kBatch];
+        float4 o[kBatch];
+        Sum sum;
         if (row < rows) {
-#pragma unroll 4
-            for (int i = part; i < pieces; i += per) {
-                const long long slot = (i == 0 ? 2ll * first + 1 : 2ll * (first + i)) * slot_rows + row0 + row;
-                const float2 ml = part_ml[slot];
-                const float4 x = reinterpret_cast<const float4 *>(part_o + slot * HD)[lane];
-                if (ml.y == 0.f) continue;  // no visible key
-                const PagedLevel v = paged_level(ml.x, ml.y);
-                const float top = fmaxf(m, v.m);
-                const float a = piece_weight(m, top), w = piece_weight(v.m, top) * v.down;
-                m = top;
-                l = l * a + ml.y * w;
-                o = make_float4(o.x * a + x.x * w, o.y * a + x.y * w, o.z * a + x.z * w, o.w * a + x.w * w);
+            for (int i0 = part; i0 < pieces; i0 += kBatch * per) {
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    const int i = i0 + e * per;
+                    ml[e] = make_float2(-INFINITY, 0.f);
+                    o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < pieces) {
+                        const long long slot = (2ll * (w - 1 + i) + (i == 0 ? 1 : 0)) * slot_rows + from + row;
+                        ml[e] = part_ml[slot];
+                        o[e] = reinterpret_cast<const float4 *>(part_o + slot * HD)[lane];
+                    }
+                }
+                sum.add(ml, o);
             }
         }
         if (per > 1) {
             __syncthreads();
-            reinterpret_cast<float4 *>(sh_o[grp])[lane] = o;
-            if (lane == 0) sh_ml[grp] = make_float2(m, l);
+            sh_o[grp][lane] = sum.o;
+            if (lane == 0) sh_ml[grp] = make_float2(sum.m, sum.l);
             __syncthreads();
             if (part == 0) {
-                for (int i = 1; i < per; ++i) {
-                    const float2 ml = sh_ml[grp + i];
-                    const float4 x = reinterpret_cast<const float4 *>(sh_o[grp + i])[lane];
-                    const float top = fmaxf(m, ml.x);
-                    const float a = piece_weight(m, top), w = piece_weight(ml.x, top);
-                    m = top;
-                    l = l * a + ml.y * w;
-                    o = make_float4(o.x * a + x.x * w, o.y * a + x.y * w, o.z * a + x.z * w, o.w * a + x.w * w);
+                static_assert(kGroups <= kBatch, "a row's groups are joined at once");
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    ml[e] = e < per ? sh_ml[grp + e] : make_float2(-INFINITY, 0.f);
+                    o[e] = e < per ? sh_o[grp + e][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
+                sum = Sum();
+                sum.add(ml, o);
             }
         }
         if (part == 0 && row < rows) {
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            out(row0 + row, lane, make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)));
+            const float inv = sum.l != 0.f ? 1.f / sum.l : 0.f;
+            const int at = j.x0 + from + row, t = at / g, h = j.head * g + at - t * g;
+            if (in_bounds(h < p.H && j.row0 + t < p.c.N, p.status))
+                reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (j.row0 + t) * p.o_stride_t)[lane] =
+                    make_uint2(pack_bf16x2(sum.o.x * inv, sum.o.y * inv), pack_bf16x2(sum.o.z * inv, sum.o.w * inv));
         }
     }
-}
-
-// Blocks 0 .. workers - 1 join the items of the kernel above, a block for every
-// worker that began inside one; the others those of attn_paged_bf16.cu, 8
-// blocks of 16 rows for each of its CTAs.
-constexpr int kTileJoinRows = 16;
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int workers, int tile_rows) {
-    __shared__ float sh_o[kMergeThreads / 16][HD];
-    __shared__ float2 sh_ml[kMergeThreads / 16];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int g = p.H / p.c.Hkv;
-    const int x = blockIdx.x;
-    if (x < workers) {
-        const int4 rec = p.rec[x];
-        if (rec.x < 0) return;
-        const PagedSeq s = paged_seq(p.c, rec.x);
-        const int all = min(s.n, p.max_new) * g, tiles = (all + tile_rows - 1) / tile_rows;
-        const int head = rec.y / tiles, tile = rec.y - head * tiles;
-        join(p.part_o, p.part_ml, tile_rows, x - 1, rec.z, 0, min(all - tile * tile_rows, tile_rows), sh_o, sh_ml,
-             [&](int row, int lane, uint2 y) {
-                 const int at = tile * tile_rows + row, t = at / g, h = head * g + at - t * g;
-                 if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
-                     reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[lane] = y;
-             });
-        return;
-    }
-    const int per = 128 / kTileJoinRows, cta = (x - workers) / per, row0 = (x - workers - cta * per) * kTileJoinRows;
-    const int4 rec = p.tile_rec[cta];
-    if (rec.x < 0) return;
-    const PagedSeq s = paged_seq(p.c, rec.x);
-    const int t0 = rec.y, head = rec.z;
-    const int rows = min(min(s.n, p.max_new) - t0, paged_tile_tokens(g)) * g;
-    if (row0 >= rows) return;
-    join(p.tile_o, p.tile_ml, 128, cta - 1, rec.w, row0, min(rows - row0, kTileJoinRows), sh_o, sh_ml,
-         [&](int row, int lane, uint2 y) {
-             const int t = t0 + row / g, h = head * g + row % g;
-             if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
-                 reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[lane] = y;
-         });
 }
 
 template <bool kInt8>
@@ -693,8 +729,8 @@ cudaError_t launch_rows(const PagedAttnParams &p, int list, int tile_rows, cudaS
 int paged_decode_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 int paged_decode_workers(int tile_rows, bool int8) {
-    const int ctas = tile_rows == 32 ? 2 : 3;  // of an SM
-    return kSmsPerGpu * ctas * kWarps;
+    (void)int8;
+    return kSmsPerGpu * paged_decode_ctas(tile_rows / 8) * kWarps;
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
@@ -703,7 +739,7 @@ cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_r
 
 cudaError_t launch_paged_merge(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
     const int workers = paged_decode_workers(tile_rows, p.c.int8 != 0);
-    const unsigned grid = workers + (tiles ? kPagedTileCtas * (128 / kTileJoinRows) : 0);
+    const unsigned grid = workers + (tiles ? kPagedTileCtas * (128 / kMergeRows) : 0);
     return launch_kernel(paged_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
 }
 

@@ -78,6 +78,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Is the phase complete?  Never suspends the thread (mbar_try_wait may, for
+// microseconds), for a warp that has something else to do.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // As mbar_try_wait, but lets the hardware suspend the thread for up to
 // `suspend_ns` while the phase is incomplete (it resumes when the phase
 // completes), so a waiting warp does not keep polling shared memory.
