@@ -15,7 +15,7 @@
 // that is not there, and rows of pages past the length, are boxes past the
 // tensor's end, which arrive as zeros, and their keys are not seen.
 //
-// The pipeline (one CTA an SM, TMA ring, S issuer, two PV issuers, two softmax
+// The pipeline (one CTA an SM, TMA rings, S issuer, two PV issuers, two softmax
 // groups on alternate tiles, output warps, three score buffers in tensor memory)
 // and the online softmax with its window of [2^-64, 2^64] around a row's reference
 // are attn_scored_bf16.cuh's, without cap and bias.
@@ -26,6 +26,8 @@
 // (n 2^e is exact).  Between two tiles they look for a finished row tile
 // first, since the products behind it wait for its accumulators.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged.cuh"
@@ -49,8 +51,10 @@ constexpr uint32_t kRawBytes = BN * HD;  // an int8 tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 384;
 constexpr float kSumMin = 5.421010862427522e-20f, kSumMax = 1.8446744073709552e19f;  // 2^-64, 2^64
+// About a second, for a loop of its own between two barriers (the wall clock takes
+// microseconds to read).
+constexpr long long kSpinClocks = 2000ll * 1000 * 1000;
 constexpr int kTable = 48;     // pieces whose geometry is kept on chip
-constexpr int kFastTiles = 6;  // pieces of so many key tiles take whole tiles in one line, as attn_scored_bf16.cuh's
 
 template <bool kInt8>
 constexpr int kStages = kInt8 ? 4 : 5;
@@ -103,6 +107,33 @@ struct __align__(1024) Smem {
     int abort_flag;
 };
 
+// (the ring of one type is not there in the other)
+template <bool kInt8>
+__device__ __forceinline__ uint64_t *raw_full(Smem<kInt8> &sm, int i) {
+    if constexpr (kInt8) return &sm.raw.full[i];
+    return nullptr;
+}
+template <bool kInt8>
+__device__ __forceinline__ uint64_t *raw_empty(Smem<kInt8> &sm, int i) {
+    if constexpr (kInt8) return &sm.raw.empty[i];
+    return nullptr;
+}
+template <bool kInt8>
+__device__ __forceinline__ uint8_t *raw_k(Smem<kInt8> &sm, int i) {
+    if constexpr (kInt8) return sm.raw.k[i];
+    return nullptr;
+}
+template <bool kInt8>
+__device__ __forceinline__ uint8_t *raw_v(Smem<kInt8> &sm, int i) {
+    if constexpr (kInt8) return sm.raw.v[i];
+    return nullptr;
+}
+template <bool kInt8>
+__device__ __forceinline__ uint32_t *raw_bad(Smem<kInt8> &sm, int i) {
+    if constexpr (kInt8) return &sm.raw.bad[i];
+    return nullptr;
+}
+
 // Where a CTA's share of the line lies.  A row tile takes kTileCost places on it
 // before those of its key tiles: what a piece costs besides them, in key tiles.
 // (Causal, 2 x 16 x 8,192: CTAs with the short row tiles of a head have 29 of them,
@@ -152,6 +183,46 @@ __device__ __forceinline__ const Piece &piece_of(Smem<kInt8> &sm, const PagedAtt
     __syncwarp();
     return own;
 }
+
+// The boxes that a warp loads tiles in.  A lane holds where one of the next 32, those
+// of 32 / boxes tiles, lies (a look-up a tile would be a trip to L2 for each).
+struct Boxes {
+    int box, boxes, window;  // rows of a box: gcd(page, 128); boxes of a tile; tiles looked up at once
+    int none;                // a page past the tensor: zeros
+    int at = 0;              // the tile's first box among the 32
+    int page = 0, in_page = 0;
+    uint32_t gone = 0;       // 16-key bits of this lane's box in its tile, if it is seen but not there
+    bool any_gone = false;
+    __device__ __forceinline__ explicit Boxes(const PagedAttnParams &p) {
+        box = min(p.c.page & -p.c.page, BN);
+        boxes = BN / box;
+        window = 32 / boxes;
+        none = max(p.c.num_pages, 1);
+    }
+    // for tile jt of a piece, called for jt = 0, 1, ... by the converged warp
+    __device__ __forceinline__ void next(const PagedAttnParams &p, const Piece &w, int jt, int lane) {
+        at += boxes;
+        if (jt != 0 && at < 32) return;
+        at = 0;
+        const int j = tile_of(w, jt + lane / boxes), key = j * BN + lane % boxes * box;
+        page = none;
+        in_page = 0;
+        gone = 0;
+        if (j >= w.j0 && key < w.len) {
+            const int i = key / p.c.page, pg = paged_page(p.c, w.b, i);
+            if (pg >= 0) {
+                page = pg;
+                in_page = key - i * p.c.page;
+            } else {
+                gone = ((1u << (box / 16)) - 1u) << (lane % boxes * (box / 16));
+            }
+        }
+        any_gone = __any_sync(0xffffffffu, gone != 0u);
+    }
+    __device__ __forceinline__ uint32_t bad(int lane) const {
+        return any_gone ? __reduce_or_sync(0xffffffffu, lane >= at && lane < at + boxes ? gone : 0u) : 0u;
+    }
+};
 
 // 16 int8 values of a row as bf16, times 2^e: the two 16-byte pieces.
 __device__ __forceinline__ void to_bf16(const uint4 &n, float power, uint4 &a, uint4 &b) {
@@ -258,91 +329,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------ TMA producer
-        // Lane i < boxes loads the i-th box of K and of V.  The pages of the next
-        // 32 boxes, 32 / boxes tiles, are looked up at once, a lane each: a look-up
-        // a tile would be a trip to L2 for every one (341 us, causal 2 x 16 x 8,192).
-        const int box = min(p.c.page & -p.c.page, BN), boxes = BN / box;  // gcd(page, 128)
-        const int none = max(p.c.num_pages, 1);                            // past the tensor: zeros
-        const int window = 32 / boxes;                                     // tiles
-        const int my_box = lane % boxes, my_tile = lane / boxes;
-        int n = 0, v = 0;
-        bool ok = true;
-        int page = none, in_page = 0;
-        uint32_t gone = 0;  // 16-key bits of this lane's box, if it is seen but not there
-        bool any_gone = false;
-        auto look_up = [&](const Piece &w, int jt) {
-            const int j = tile_of(w, jt + my_tile), key = j * BN + my_box * box;
-            page = none;
-            in_page = 0;
-            gone = 0;
-            if (j >= w.j0 && key < w.len) {
-                const int i = key / p.c.page, pg = paged_page(p.c, w.b, i);
-                if (pg >= 0) {
-                    page = pg;
-                    in_page = key - i * p.c.page;
-                } else {
-                    gone = ((1u << (box / 16)) - 1u) << (my_box * (box / 16));
-                }
-            }
-            any_gone = __any_sync(0xffffffffu, gone != 0u);
-        };
+        // By the converged warp: an instruction of this warp takes about 10 cycles
+        // beside two softmax warps, and 100 of them a tile are more than the tile's
+        // weights take.
+        Boxes bx(p);
+        int n = 0, v = 0, st = 0;
+        uint32_t par = 1;
+        constexpr int kRing = kInt8 ? kRaw : STAGES;
+        const int box_bytes = bx.box * HD * (kInt8 ? 1 : 2);
+        bool ok = true, marked = false;  // marked: stages may hold a `bad` other than 0
+        if (!kInt8 && lane < STAGES) sm.bad[lane] = 0;
         for (int t = 0; ok && t < pieces; ++t) {
             const Piece &w = piece_of<kInt8>(sm, p, sh, t);
-            const int qbuf = v & 1;
+            const int n_kv = w.n_kv, head = w.head, qbuf = v & 1;
             if (v >= 2 && !(ok = warp_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&sm.q_full[qbuf], static_cast<uint32_t>(tt * g) * (HD * 2));
                 if (in_bounds(w.head * g < p.H && w.row0 < p.c.N, p.status))
                     tma_load_3d(&maps.q, &sm.q_full[qbuf], sm.q[qbuf], 0, w.head * g, w.row0);
             }
+            __syncwarp();
             ++v;
-            int at = window;  // the tile's place in the window
-            for (int jt = 0; jt < w.n_kv; ++jt, ++n, ++at) {
-                const int st = n % STAGES;
-                if (at == window) {
-                    look_up(w, jt);
-                    at = 0;
-                }
-                const uint32_t bad = any_gone ? __reduce_or_sync(0xffffffffu, my_tile == at ? gone : 0u) : 0u;
+            for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                bx.next(p, w, jt, lane);
+                uint64_t *full = kInt8 ? raw_full(sm, st) : &sm.kv_full[st], *empty = kInt8 ? raw_empty(sm, st) : &sm.kv_empty[st];
+                uint8_t *k = kInt8 ? raw_k(sm, st) : sm.k[st], *vv = kInt8 ? raw_v(sm, st) : sm.v[st];
+                uint32_t bytes = 2 * (kInt8 ? kRawBytes : kTileBytes);
                 if constexpr (kInt8) {
-                    const int rs = n % kRaw;
-                    if (n >= kRaw && !(ok = warp_wait(&sm.raw.empty[rs], ((n / kRaw) - 1) & 1, ab))) break;
-                    const bool scales = my_tile == at && page < none;
-                    const uint32_t bytes = 2 * kRawBytes + 2u * box * __popc(__ballot_sync(0xffffffffu, scales));
-                    if (lane == 0) {
-                        sm.raw.bad[rs] = bad;
-                        mbar_arrive_expect_tx(&sm.raw.full[rs], bytes);
-                    }
+                    const bool there = lane >= bx.at && lane < bx.at + bx.boxes && bx.page < bx.none;
+                    bytes += 2u * bx.box * __popc(__ballot_sync(0xffffffffu, there));
+                }
+                if (n >= kRing && !(ok = warp_wait(empty, par, ab))) break;
+                if (bx.any_gone || marked || kInt8) {
+                    marked = true;
+                    const uint32_t bad = bx.bad(lane);
+                    if (lane == 0) *(kInt8 ? raw_bad(sm, st) : &sm.bad[st]) = bad;
                     __syncwarp();
-                    if (my_tile == at) {
-                        tma_load_4d(&maps.k, &sm.raw.full[rs], sm.raw.k[rs] + my_box * box * HD, 0, in_page, w.head, page);
-                        tma_load_4d(&maps.v, &sm.raw.full[rs], sm.raw.v[rs] + my_box * box * HD, 0, in_page, w.head, page);
-                        if (scales) {
-                            const long long from = (static_cast<long long>(page) * p.c.Hkv + w.head) * p.c.page + in_page;
-                            bulk_load_1d(sm.raw.ks[rs] + my_box * box, p.c.k_scales + from, box, &sm.raw.full[rs]);
-                            bulk_load_1d(sm.raw.vs[rs] + my_box * box, p.c.v_scales + from, box, &sm.raw.full[rs]);
+                }
+                warp_arrive_expect_tx(full, bytes);
+#pragma unroll 1
+                for (int i = 0; i < bx.boxes; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, bx.page, bx.at + i), in = __shfl_sync(0xffffffffu, bx.in_page, bx.at + i);
+                    warp_tma_load_4d(&maps.k, full, k + i * box_bytes, 0, in, head, pg);
+                    warp_tma_load_4d(&maps.v, full, vv + i * box_bytes, 0, in, head, pg);
+                    if constexpr (kInt8)
+                        if (pg < bx.none) {
+                            const long long from = (static_cast<long long>(pg) * p.c.Hkv + head) * p.c.page + in;
+                            warp_bulk_load_1d(sm.raw.ks[st] + i * bx.box, p.c.k_scales + from, bx.box, full);
+                            warp_bulk_load_1d(sm.raw.vs[st] + i * bx.box, p.c.v_scales + from, bx.box, full);
                         }
-                    }
-                } else {
-                    if (n >= STAGES && !(ok = warp_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
-                    if (lane == 0) {
-                        sm.bad[st] = bad;
-                        mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
-                    }
-                    __syncwarp();
-                    if (my_tile == at) {
-                        tma_load_4d(&maps.k, &sm.kv_full[st], sm.k[st] + my_box * box * (HD * 2), 0, in_page, w.head, page);
-                        tma_load_4d(&maps.v, &sm.kv_full[st], sm.v[st] + my_box * box * (HD * 2), 0, in_page, w.head, page);
-                    }
+                }
+                if (++st == kRing) {
+                    st = 0;
+                    par ^= 1u;
                 }
             }
         }
+        // Let every copy still in flight land before the CTA exits.
         if (lane == 0) {
-            if constexpr (kInt8) {
-                for (int x = max(0, n - kRaw); x < n; ++x) mbar_wait_drain(&sm.raw.full[x % kRaw], (x / kRaw) & 1);
-            } else {
-                for (int x = max(0, n - STAGES); x < n; ++x) mbar_wait_drain(&sm.kv_full[x % STAGES], (x / STAGES) & 1);
-            }
+            for (int x = max(0, n - kRing); x < n; ++x)
+                mbar_wait_drain(kInt8 ? raw_full(sm, x % kRing) : &sm.kv_full[x % kRing], (x / kRing) & 1);
             for (int x = max(0, v - 2); x < v; ++x) mbar_wait_drain(&sm.q_full[x & 1], (x >> 1) & 1);
         }
     } else if (warp == kMmaSWarp) {
@@ -456,7 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_live = __any_sync(0xffffffffu, live);
             // keys below it are seen; rows that are none hold nothing up
             const int lim = !live ? 0x7fffffff : p.causal ? min(max(w.pos0 + token + 1, 0), w.len) : w.len;
-            const bool long_piece = w.n_kv >= kFastTiles;
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
             float l_run = 0.f;
 
@@ -482,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bad = *static_cast<volatile uint32_t *>(&sm.bad[st]);
                 const bool edge = j * BN + BN > w.full_hi || bad != 0;
                 int rd_first = 0;
-                if (!edge && long_piece) {
+                if (!edge) {
 #pragma unroll
                     for (int rd = 0; rd < 2; ++rd) {
                         uint32_t s0[32], s1[32], pk[32];
@@ -521,29 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m_run = 0.f;
                         return false;
                     };
-                    int done = 0;  // of the round's two halves
-                    if (gone == 0 && __all_sync(0xffffffffu, lim >= key0 + 64)) {
-                        uint32_t s0[32], s1[32], pk[32];
-                        tmem_ld32(tr, s0);
-                        tmem_ld32(tr + 32, s1);
-                        tmem_ld_wait(s0);
-                        reg_fence32(s1);
-                        const bool first = m_run == -INFINITY;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                        weights(s0, first ? 0.f : m_run, pk, sum);
-                        weights(s1, first ? 0.f : m_run, pk + 16, sum);
-                        const float lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        if (__any_sync(0xffffffffu, must_move(lt, false))) {
-                            if (first) m_run = -INFINITY;
-                        } else {
-                            tmem_st32(ts + 32u * static_cast<uint32_t>(rd), pk);
-                            l_run += lt;
-                            done = 2;
-                        }
-                    }
-                    // Every other round, 32 keys at a time.
+                    // 32 keys at a time.
 #pragma unroll 1
-                    for (int h = done; h < 2; ++h) {
+                    for (int h = 0; h < 2; ++h) {
                         const int kh = key0 + 32 * h;
                         const uint32_t two = gone >> (2 * h) & 3u;
                         const int hi = min(lim - kh, 32);
@@ -661,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++v;
         }
         if (!ok) tmem_st_wait();
-    } else if (warp >= kOutWarp) {
+    } else {
         // ------------------------------------------------- output, int8 tiles
         const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
         const int r = static_cast<int>(lane_base) + lane;
@@ -732,39 +757,82 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
+        // int8: pieces are put out as their products are complete, K and V of tile
+        // after tile written as stages come free.  Behind a piece's last tile it may be a stage that only products after
+        // that piece's output give back: whichever comes first.  (One place in the
+        // code for each: all roles' loops together have to stay in the instruction
+        // cache, 32 KB or so; with three copies of output() here a causal prompt took
+        // 392 us instead of 290.)
+        auto put_first = [&](int v, uint64_t *bar, uint32_t parity, bool &ok) -> bool {
+            const long long since = clock64();
+            while (true) {
+                if (__all_sync(0xffffffffu, mbar_test(&sm.o_final, static_cast<uint32_t>(v & 1)))) return true;
+                if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return false;
+                bool stop = should_abort(ab);
+                if (clock64() - since > kSpinClocks) {
+                    raise_abort(ab);
+                    stop = true;
+                }
+                if (__any_sync(0xffffffffu, stop)) {
+                    ok = false;
+                    return false;
+                }
+            }
+        };
         if constexpr (!kInt8) {
             for (int v = 0; v < pieces; ++v)
                 if (!output(v)) break;
         } else {
             const int tid = threadIdx.x - 32 * kOutWarp;
-            // 4 rows of a tile, a quarter of each: rows tid / 4 + 32 i
-            const int row0 = tid >> 2, quarter = tid & 3;
-            auto convert = [&](int n, int keys) {  // rows from `keys` on are cleared
-                const int rs = n % kRaw, st = n % STAGES;
+            const int row0 = tid >> 2, quarter = tid & 3;  // rows tid / 4 + 32 i of a tile, a quarter of each
+            int v = 0, piece = 0, jt = 0, st = 0, rs = 0;
+            uint32_t st_par = 1, rs_par = 0;
+            int n_kv = 0, keys = 0;
+            bool fill = true, ok = true;  // fill: the ring's first round, nothing to wait for
+            while (ok && (piece < pieces || v < pieces)) {
+                bool put = piece == pieces;
+                if (!put && jt == 0) {
+                    const Piece &w = piece_of<true>(sm, p, sh, piece);
+                    n_kv = w.n_kv;
+                    keys = w.len - (w.j0 + n_kv - 1) * BN;  // of the tile; rows past them are cleared
+                }
+                if (!put && !fill) {
+                    if (v < piece) put = put_first(v, &sm.kv_empty[st], st_par, ok);
+                    if (ok && !put) ok = warp_wait(&sm.kv_empty[st], st_par, ab);
+                    if (!ok) break;
+                }
+                if (put) {
+                    ok = output(v++);
+                    continue;
+                }
+                // (raw tiles wait for nothing but these warps)
+                if (!(ok = warp_wait(&sm.raw.full[rs], rs_par, ab))) break;
                 const uint32_t bad = sm.raw.bad[rs];
-                uint4 u[8];
-                uint32_t e[8];
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint4 *from = reinterpret_cast<const uint4 *>(kv ? sm.raw.v[rs] : sm.raw.k[rs]) + tid;
+                    const uint8_t *es = (kv ? sm.raw.vs[rs] : sm.raw.ks[rs]) + row0;
+                    uint4 *to = reinterpret_cast<uint4 *>(kv ? sm.v[st] : sm.k[st]) + row0 * 8 + ((2 * quarter) ^ (row0 & 7));
+                    const int other = (row0 & 1) ? -1 : 1;
+                    uint4 u[4];
+                    uint32_t e[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // (all loads before the first store: they may not pass it)
-                    u[i] = reinterpret_cast<const uint4 *>(i < 4 ? sm.raw.k[rs] : sm.raw.v[rs])[(i & 3) * 128 + tid];
-                    e[i] = (i < 4 ? sm.raw.ks[rs] : sm.raw.vs[rs])[row0 + 32 * (i & 3)];
-                }
-                if (keys < BN || bad != 0u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = row0 + 32 * (i & 3);
-                        if (row >= keys || (bad >> (row >> 4) & 1u)) e[i] = 0u;
+                    for (int i = 0; i < 4; ++i) {  // (all loads before the first store: they may not pass it)
+                        u[i] = from[i * 128];
+                        e[i] = es[32 * i];
                     }
-                }
-                uint4 *k = reinterpret_cast<uint4 *>(sm.k[st]) + row0 * 8, *v = reinterpret_cast<uint4 *>(sm.v[st]) + row0 * 8;
-                const int at = (2 * quarter) ^ (row0 & 7);
+                    if (keys < BN || bad != 0u) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint4 a, b;
-                    to_bf16(u[i], paged_power(e[i]), a, b);
-                    uint4 *to = (i < 4 ? k : v) + 256 * (i & 3);
-                    to[at] = a;
-                    to[at ^ 1] = b;
+                        for (int i = 0; i < 4; ++i)
+                            if (row0 + 32 * i >= keys || (bad >> ((row0 + 32 * i) >> 4) & 1u)) e[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 a, b;
+                        to_bf16(u[i], paged_power(e[i]), a, b);
+                        to[256 * i] = a;
+                        to[256 * i + other] = b;
+                    }
                 }
                 if (tid == 0) sm.bad[st] = bad;
                 fence_proxy_async_smem();
@@ -773,44 +841,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&sm.kv_full[st]);
                     mbar_arrive(&sm.raw.empty[rs]);
                 }
-            };
-            auto wait = [&](uint64_t *bar, int parity) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, static_cast<uint32_t>(parity), ab));
-            };
-            // Tiles are written as stages come free.  Behind a piece's last one the
-            // next piece's wait for its output at the latest, when they wait
-            // for a stage that only products behind the output give back.
-            int n = 0, v = 0;  // tiles written, pieces put out
-            bool ok = true;
-            for (int piece = 0; ok && piece < pieces; ++piece) {
-                const Piece &w = piece_of<true>(sm, p, sh, piece);
-                const int n_kv = w.n_kv, len = w.len, first = w.j0;
-                for (int jt = 0; ok && jt < n_kv; ++jt, ++n) {
-                    unsigned long long since = 0;
-                    while (ok && n >= STAGES && v < piece) {
-                        if (__all_sync(0xffffffffu, mbar_test(&sm.o_final, static_cast<uint32_t>(v & 1)))) {
-                            ok = output(v++);
-                        } else if (__all_sync(0xffffffffu, mbar_test(&sm.kv_empty[n % STAGES], static_cast<uint32_t>((n / STAGES - 1) & 1)))) {
-                            break;
-                        } else {
-                            // neither: look again, within the waits' limit
-                            const unsigned long long now = global_timer_ns();
-                            if (since == 0) since = now;
-                            bool stop = should_abort(ab);
-                            if (now - since > kWaitLimitNs) {
-                                raise_abort(ab);
-                                stop = true;
-                            }
-                            if (__any_sync(0xffffffffu, stop)) ok = false;
-                        }
-                    }
-                    if (ok && n >= STAGES) ok = wait(&sm.kv_empty[n % STAGES], (n / STAGES - 1) & 1);
-                    // (raw tiles wait for nothing but these warps)
-                    if (ok) ok = wait(&sm.raw.full[n % kRaw], (n / kRaw) & 1);
-                    if (ok) convert(n, len - (first + n_kv - 1 - jt) * BN);
+                if (++st == STAGES) {
+                    st = 0;
+                    st_par ^= 1u;
+                    fill = false;
+                }
+                if (++rs == kRaw) {
+                    rs = 0;
+                    rs_par ^= 1u;
+                }
+                keys += BN;
+                if (++jt == n_kv) {
+                    jt = 0;
+                    ++piece;
                 }
             }
-            while (ok && v < pieces) ok = output(v++);
         }
     }
 
