@@ -490,12 +490,16 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  *   2^46 in magnitude.
  *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
  *   in flight.
- * Two launches (sequences with up to 64 query rows per K/V head; joining of the
- * partial sums of divided key ranges), and a third between them when max_new
- * allows more: tcgen05 products over tiles of 128 rows.  A call's results do not depend
- * on timing (equal calls give equal bits).
+ * Two launches (sequences with up to 32 query rows per K/V head; joining of the
+ * partial sums of divided key ranges), a third between them when max_new allows
+ * more: tcgen05 products over tiles of 128 rows; and when it allows 512 and the cache
+ * is int8, or has pages that are not a multiple of 64 rows, one that lays these
+ * sequences' rows out as bf16 first, in up to 4 GiB of the workspace (where that would
+ * take more it is left out).  A call's results do not depend on timing (equal calls
+ * give equal bits).
  */
-size_t sdpa_paged_workspace_bytes(int B, int h, int h_kv, int N, int max_new);
+/* From the sizes in `cache` (its pointers may be NULL); 0 for sizes that are not valid. */
+size_t sdpa_paged_workspace_bytes(const mha_paged_cache *cache, int h, int N, int max_new);
 mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
                               long long q_stride_t, void *o, long long o_stride_h,
                               long long o_stride_t, void *workspace, size_t workspace_bytes, int h,

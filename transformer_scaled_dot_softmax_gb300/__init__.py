@@ -714,7 +714,7 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, ou
     if status is not None:
         _check_dev("status", status, torch.int32)
     max_new = n if max_new is None else max_new
-    need = lib.sdpa_paged_workspace_bytes(cache.B, h, cache.h_kv, n, max_new)
+    need = lib.sdpa_paged_workspace_bytes(ctypes.addressof(cache), h, n, max_new)
     workspace, size = _scratch_here(torch, workspace, need, dev, stream)
     rc = lib.sdpa_paged_forward(ctypes.addressof(cache), *qp, *op, workspace.data_ptr(), size, h, n, max_new, d,
                                 1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask), _ptr(status),

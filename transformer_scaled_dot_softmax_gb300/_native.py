@@ -72,7 +72,7 @@ SIGNATURES = {
                                    [_cf, _ci, _vp, _vp, _vp, _vp]),
     "paged_cache_append": (_ci, [_vp, _vp, _ll, _ll, _vp, _ll, _ll, _ci, _ci, _vp]),
     "paged_cache_read": (_ci, [_vp, _vp, _vp, _ci, _ci, _vp]),
-    "sdpa_paged_workspace_bytes": (_sz, [_ci] * 5),
+    "sdpa_paged_workspace_bytes": (_sz, [_vp, _ci, _ci, _ci]),
     "sdpa_paged_forward": (_ci, [_vp, _vp, _ll, _ll, _vp, _ll, _ll, _vp, _sz, _ci, _ci, _ci, _ci,
                                  _cf, _ci, _vp, _vp]),
     "mha_workspace_bytes": (_sz, [_ci, _ci, _ci, _ci, _ci, _ci]),

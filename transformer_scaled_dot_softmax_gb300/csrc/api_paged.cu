@@ -26,9 +26,8 @@ mha_status launched(cudaError_t e, const char *what) {
     return e == cudaSuccess ? MHA_OK : record_cuda_failure(what, cudaGetErrorName(e));
 }
 
-// `rows`: the call takes packed rows (row_starts).
-mha_status check_cache(const mha_paged_cache *x, int d, bool rows, int N, PagedCache &c) {
-    if (!x) return MHA_ERR_INVALID_ARG;
+// Everything but the pointers.
+mha_status check_sizes(const mha_paged_cache *x, int d, int N, PagedCache &c) {
     if (x->dtype != MHA_BF16 && x->dtype != MHA_INT8)
         return x->dtype == MHA_F32 ? MHA_ERR_UNSUPPORTED : MHA_ERR_INVALID_ARG;
     if (x->B < 0 || x->h_kv < 0 || x->num_pages < 0 || x->max_pages < 0 || x->page_rows <= 0 || N < 0 || d <= 0)
@@ -52,10 +51,18 @@ mha_status check_cache(const mha_paged_cache *x, int d, bool rows, int N, PagedC
     c.page = x->page_rows;
     c.num_pages = x->num_pages;
     c.max_pages = x->max_pages;
+    c.cap = x->max_pages * x->page_rows;
     c.N = N;
     if (x->num_pages > 1 && (x->page_stride < rows_of_page * kAttnHeadDim || x->page_stride % 16 != 0)) return MHA_ERR_INVALID_ARG;
     if (x->num_pages <= 1) c.stride = rows_of_page * kAttnHeadDim;
-    if (c.stride >= (1ll << 38)) return MHA_ERR_UNSUPPORTED;
+    return c.stride < (1ll << 38) ? MHA_OK : MHA_ERR_UNSUPPORTED;
+}
+
+// `rows`: the call takes packed rows (row_starts).
+mha_status check_cache(const mha_paged_cache *x, int d, bool rows, int N, PagedCache &c) {
+    if (!x) return MHA_ERR_INVALID_ARG;
+    const mha_status s = check_sizes(x, d, N, c);
+    if (s != MHA_OK) return s;
     if (x->B == 0 || x->h_kv == 0) return MHA_OK;
     if (!x->seq_lens || (rows && !x->row_starts) || (x->max_pages > 0 && !x->page_table)) return MHA_ERR_INVALID_ARG;
     if (x->num_pages > 0) {
@@ -84,16 +91,16 @@ mha_status check_rows(const void *x, long long stride_h, long long stride_t, int
 struct Layout {
     bool tiles;      // sequences may have more than kPagedSmallRows stacked rows
     int tile_rows;   // of paged_decode.cu
-    size_t part_o, part_ml, join, plan, tile_o, tile_ml, tile_join, bytes;
+    int slots, wide_cap;  // places for rows laid out as bf16 (0: none), their rows
+    size_t part_o, part_ml, join, plan, tile_o, tile_ml, tile_join, wide_k, wide_v, gone, bytes;
 };
-Layout layout(int B, int g, int N, int max_new) {
+Layout layout(const PagedCache &c, int g, int max_new) {
     Layout l{};
-    const long long most = static_cast<long long>(std::min(max_new, N)) * g;
+    const long long most = static_cast<long long>(std::min(max_new, c.N)) * g;
     l.tiles = most > kPagedSmallRows;
     // among longer chunks the short ones are taken for single tokens
     l.tile_rows = paged_decode_rows(l.tiles ? g : static_cast<int>(most));
-    const size_t workers = static_cast<size_t>(
-        std::max(paged_decode_workers(l.tile_rows, false), paged_decode_workers(l.tile_rows, true)));
+    const size_t workers = static_cast<size_t>(paged_decode_workers(l.tile_rows));
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t was = at;
@@ -104,10 +111,23 @@ Layout layout(int B, int g, int N, int max_new) {
     l.part_ml = take(2 * workers * l.tile_rows * sizeof(float2));
     l.join = take(workers * sizeof(PagedJoin));
     if (l.tiles) {
-        l.plan = take(sizeof(int) * static_cast<size_t>(paged_plan(B, paged_most_tiles(N, B, g)).ints));
+        l.plan = take(sizeof(int) * static_cast<size_t>(paged_plan(c.B, paged_most_tiles(c.N, c.B, g)).ints));
         l.tile_o = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * kAttnHeadDim * sizeof(float));
         l.tile_ml = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * sizeof(float2));
         l.tile_join = take(kPagedTileCtas * sizeof(PagedJoin));
+        // sequences with more than kPagedSmallRows rows are no more than these
+        const int slots = static_cast<int>(std::min<long long>(c.B, static_cast<long long>(c.N) * g / (kPagedSmallRows + 1)));
+        const int cap = (c.cap + 127) / 128 * 128;
+        const size_t rows = static_cast<size_t>(slots) * c.Hkv * cap;
+        const bool wide = c.int8 || c.page % 32 != 0 ? most >= kPagedWideRows : c.page % 64 != 0 && most >= kPagedWideRows32;
+        if (wide && rows > 0 &&
+            rows <= kPagedWideBytes / (2 * kAttnHeadDim * sizeof(__nv_bfloat16))) {
+            l.slots = slots;
+            l.wide_cap = cap;
+            l.wide_k = take(rows * kAttnHeadDim * sizeof(__nv_bfloat16));
+            l.wide_v = take(rows * kAttnHeadDim * sizeof(__nv_bfloat16));
+            l.gone = take(static_cast<size_t>(slots) * (cap / 128) * sizeof(uint32_t));
+        }
     }
     l.bytes = at;
     return l;
@@ -149,9 +169,12 @@ MHA_EXPORT mha_status paged_cache_read(const mha_paged_cache *cache, void *k, vo
                     "paged cache read launch");
 }
 
-MHA_EXPORT size_t sdpa_paged_workspace_bytes(int B, int h, int h_kv, int N, int max_new) {
-    if (check_heads(B, h, h_kv, N, max_new) != MHA_OK || B == 0 || h == 0 || N == 0 || max_new == 0) return 0;
-    return layout(B, h / h_kv, N, max_new).bytes;
+MHA_EXPORT size_t sdpa_paged_workspace_bytes(const mha_paged_cache *cache, int h, int N, int max_new) {
+    PagedCache c{};
+    // (sizes alone: the pointers may be missing)
+    if (!cache || check_sizes(cache, kAttnHeadDim, N, c) != MHA_OK || check_heads(c.B, h, c.Hkv, N, max_new) != MHA_OK) return 0;
+    if (c.B == 0 || h == 0 || N == 0 || max_new == 0) return 0;
+    return layout(c, h / c.Hkv, max_new).bytes;
 }
 
 MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
@@ -169,9 +192,9 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     if ((s = check_rows(q, q_stride_h, q_stride_t, h, N, p.q)) != MHA_OK) return s;
     if ((s = check_rows(o, o_stride_h, o_stride_t, h, N, out)) != MHA_OK) return s;
     const int g = h / p.c.Hkv;
-    const Layout l = layout(p.c.B, g, N, max_new);
+    const Layout l = layout(p.c, g, max_new);
     // the work lines' lengths, for whatever lengths and starts the device holds
-    const long long cap = static_cast<long long>(p.c.max_pages) * p.c.page;
+    const long long cap = p.c.cap;
     const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, kPagedSmallRows);
     const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
     if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1) >= kMostLine) return MHA_ERR_UNSUPPORTED;
@@ -199,9 +222,29 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
         p.tile_o = reinterpret_cast<float *>(ws + l.tile_o);
         p.tile_ml = reinterpret_cast<float2 *>(ws + l.tile_ml);
         p.tile_join = reinterpret_cast<PagedJoin *>(ws + l.tile_join);
-        if ((s = encode_paged_maps(&maps, p)) != MHA_OK) return s;
     }
+    PagedAttnParams t = p;  // of the row tiles
+    PagedWide w{};
+    if (l.slots > 0) {
+        w.k = reinterpret_cast<__nv_bfloat16 *>(ws + l.wide_k);
+        w.v = reinterpret_cast<__nv_bfloat16 *>(ws + l.wide_v);
+        w.gone = reinterpret_cast<uint32_t *>(ws + l.gone);
+        w.cap = l.wide_cap;
+        w.slots = l.slots;
+        // a bf16 cache with a page for every such sequence
+        t.gone = w.gone;
+        t.c.int8 = 0;
+        t.c.k = w.k;
+        t.c.v = w.v;
+        t.c.stride = static_cast<long long>(p.c.Hkv) * w.cap * kAttnHeadDim;
+        t.c.table = p.plan + paged_plan(p.c.B, paged_most_tiles(N, p.c.B, g)).slot;
+        t.c.max_pages = 1;
+        t.c.num_pages = w.slots;
+        t.c.page = w.cap;
+    }
+    if (l.tiles && (s = encode_paged_maps(&maps, t)) != MHA_OK) return s;
     if ((s = launched(launch_paged_decode(p, l.tiles, l.tile_rows, stream), "paged attention, few rows")) != MHA_OK) return s;
-    if (l.tiles && (s = launched(launch_attn_paged(maps, p, stream), "paged attention, row tiles")) != MHA_OK) return s;
+    if (l.slots > 0 && (s = launched(launch_paged_widen(p, w, stream), "paged attention, rows to bf16")) != MHA_OK) return s;
+    if (l.tiles && (s = launched(launch_attn_paged(maps, t, stream), "paged attention, row tiles")) != MHA_OK) return s;
     return launched(launch_paged_merge(p, l.tiles, l.tile_rows, stream), "paged attention, joining");
 }

@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t *raw_bad(Smem<kInt8> &sm, int i) {
 // before those of its key tiles: what a piece costs besides them, in key tiles.
 // (Causal, 2 x 16 x 8,192: CTAs with the short row tiles of a head have 29 of them,
 // others 7; counted by key tiles alone the former took 305 us, the latter 280.)
-constexpr int kTileCost = 2;
+constexpr int kTileCost = 3;
 struct Share {
     int tiles, keys;        // row tiles, places of one K/V head
     int start, end, share;  // of the line
@@ -213,6 +213,7 @@ struct Boxes {
             if (pg >= 0) {
                 page = pg;
                 in_page = key - i * p.c.page;
+                if (p.gone) gone = p.gone[static_cast<long long>(pg) * (p.c.page / BN) + j];
             } else {
                 gone = ((1u << (box / 16)) - 1u) << (lane % boxes * (box / 16));
             }
@@ -692,12 +693,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = static_cast<int>(lane_base) + lane;
         const uint32_t tl = tmem_addr(tmem, lane_base, 0);
         if (warp == kOutWarp && lane == 0) {
-            // the block that joins a row tile is that of the first CTA that begins inside it
             const Piece &w = sm.table[0];
             const int n = cum[sh.x0 + 1] - cum[sh.x0];
             PagedJoin j{};
-            if (pieces > 0 && w.j0 > 0 && w.j0 <= sh.share)
-                j = PagedJoin{w.tokens * g, 0, w.head, w.row0, (sh.start - w.j0 + n - 1) / sh.share};
+            const int first = sh.start - w.j0;  // the place of its first key tile
+            if (pieces > 0 && w.j0 > 0)
+                j = PagedJoin{w.tokens * g, 0, w.head, w.row0, first / sh.share, (first + n - 1) / sh.share};
             p.tile_join[cta] = j;
         }
         // The v-th piece's rows, once its products are complete.

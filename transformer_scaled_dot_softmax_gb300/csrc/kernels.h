@@ -273,6 +273,7 @@ struct PagedCache {
     const int32_t *starts, *lens;   // (B + 1) packed rows (null where there are none), (B)
     int int8;
     int B, Hkv, page, num_pages, max_pages;
+    int cap;                        // rows of a sequence: max_pages page
     int N;                          // packed rows
 };
 // New rows (heads, tokens, 64), strides in elements.
@@ -284,11 +285,11 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedRows &k, const P
 // k, v: (B, Hkv, T, 64) bf16.
 cudaError_t launch_paged_read(const PagedCache &c, __nv_bfloat16 *k, __nv_bfloat16 *v, int T, cudaStream_t stream);
 
-// An item whose key range is divided over CTAs or warps, left by the first worker
-// that begins inside it: its rows (0: none to join), the first one's place among
-// the K/V head's stacked rows from packed row row0 on, and the item's last worker.
-struct __align__(16) PagedJoin {
-    int rows, x0, head, row0, last;
+// An item whose key range is divided over several workers (warps or CTAs), left by
+// every one that begins inside it: its rows (0: none to join), the first one's place
+// among the K/V head's stacked rows from packed row row0 on, and the workers.
+struct __align__(8) PagedJoin {
+    int rows, x0, head, row0, first, last;
 };
 struct PagedAttnParams {
     PagedCache c;
@@ -312,14 +313,18 @@ struct PagedAttnParams {
     float *tile_o;
     float2 *tile_ml;
     PagedJoin *tile_join;
+    // Where attn_paged_bf16.cu goes through rows that paged_cache.cu has laid out as
+    // bf16 pages of a whole sequence each: a word for every 128 of them, a bit for
+    // every 16 whose page was not there (else null).
+    const uint32_t *gone;
     int *status;
 };
-constexpr int kPagedSmallRows = 64;
+constexpr int kPagedSmallRows = 32;
 constexpr int kPagedTileCtas = kSmsPerGpu;  // persistent CTAs of attn_paged_bf16.cu
 // Rows that a warp of paged_decode.cu takes at once, its workers (warps), for
 // calls whose sequences have up to `rows` stacked rows there.
 int paged_decode_rows(int rows);
-int paged_decode_workers(int tile_rows, bool int8);
+int paged_decode_workers(int tile_rows);
 // The launch that goes through the small sequences and lists the others' row
 // tiles, and the one that joins both kernels' partial sums.
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream);
@@ -333,10 +338,14 @@ cudaError_t launch_attn_paged(const PagedMaps &maps, const PagedAttnParams &p, c
 mha_status encode_paged_maps(PagedMaps *m, const PagedAttnParams &p);
 
 // Lists in PagedAttnParams::plan, of at most `tiles` row tiles and B sequences.
+// plan[0]: the number of row tiles; [1]: of sequences that have some.
 struct PagedPlan {
     int first;   // (B + 1) first row tile of each sequence
     int cum;     // (tiles + 1) key tiles of one K/V head before a row tile
     int seq;     // (tiles) its sequence
+    int slot;    // (B) a sequence's place among those that have row tiles, or -1
+    int slot_b;  // (B) the sequence at a place
+    int blocks;  // (B + 1) blocks of 128 cached rows before it
     int ints;
 };
 inline __host__ __device__ PagedPlan paged_plan(int B, int tiles) {
@@ -344,9 +353,28 @@ inline __host__ __device__ PagedPlan paged_plan(int B, int tiles) {
     l.first = 4;
     l.cum = l.first + B + 1;
     l.seq = l.cum + tiles + 1;
-    l.ints = l.seq + tiles;
+    l.slot = l.seq + tiles;
+    l.slot_b = l.slot + B;
+    l.blocks = l.slot_b + B;
+    l.ints = l.blocks + B + 1;
     return l;
 }
+// The cached rows of the sequences that have row tiles, at most `slots` of them, as
+// bf16 (slots, Hkv, cap rounded up to 128, 64).
+struct PagedWide {
+    __nv_bfloat16 *k, *v;
+    uint32_t *gone;  // PagedAttnParams::gone
+    int cap, slots;
+};
+cudaError_t launch_paged_widen(const PagedAttnParams &p, const PagedWide &w, cudaStream_t stream);
+// Query rows of a K/V head (new tokens x query heads) from which on rows are laid out
+// that way first: int8 ones and those of pages of 16 rows or an odd number of
+// them, and of pages of 32 rows or an odd number.  Measured, 32,768 keys x 4 K/V
+// heads, first / straight from the pages, us: int8, 64-row pages, 256 query rows 43 /
+// 40, 512 48 / 53, 4,096 151 / 271; bf16, 16-row pages 256 42 / 38, 512 47 / 50, 4,096
+// 151 / 247; 32-row pages 512 47 / 40, 2,048 90 / 95, 4,096 151 / 171.
+constexpr int kPagedWideRows = 512, kPagedWideRows32 = 4096;
+constexpr size_t kPagedWideBytes = static_cast<size_t>(4) << 30;  // as long as it does not take more than this
 // Tokens of a row tile, and row tiles of a call at most.
 inline __host__ __device__ int paged_tile_tokens(int g) { return 128 / g; }
 inline __host__ __device__ int paged_most_tiles(int N, int B, int g) {

@@ -4,7 +4,7 @@
 // Sequence b holds len rows; row j is row j % page of the page
 // table[b][j / page].  Its n new tokens are packed rows row0 .. row0 + n - 1 and
 // the last n of its len rows.  Nothing on the device is trusted: packed rows
-// are cut to [0, N), lengths to [0, max_pages page], and a table entry
+// are cut to [0, N), lengths to [0, cap] (max_pages page), and a table entry
 // outside [0, num_pages) is a page that is not there.
 #pragma once
 
@@ -20,7 +20,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedCache &c, int b) {
     PagedSeq s;
     s.row0 = min(max(c.starts[b], 0), c.N);
     s.n = max(min(c.starts[b + 1], c.N) - s.row0, 0);
-    s.len = min(max(c.lens[b], 0), c.max_pages * c.page);
+    s.len = min(max(c.lens[b], 0), c.cap);
     return s;
 }
 

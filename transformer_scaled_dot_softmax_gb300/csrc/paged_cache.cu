@@ -118,26 +118,25 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedCache
     }
 }
 
-template <bool kInt8>
-__global__ void __launch_bounds__(kThreads) paged_read_kernel(const PagedCache c, __nv_bfloat16 *__restrict__ k,
-                                                              __nv_bfloat16 *__restrict__ v, int T, int blocks) {
-    const int bh = blockIdx.x / blocks, head = bh % c.Hkv, b = bh / c.Hkv, lane = threadIdx.x & 7;
-    const int first = (blockIdx.x - bh * blocks) * (kRows * kReadRows) + threadIdx.x / 8;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int len = min(min(max(c.lens[b], 0), c.max_pages * c.page), T);
+// 128 rows from `first` on (those before `len`) of a head of sequence b into k, v, at
+// row first + i; zeros for pages that are not there and, with kTail, for rows from
+// `len` to T.  Called by a whole block.
+template <bool kInt8, bool kTail>
+__device__ __forceinline__ void copy_rows(const PagedCache &c, int b, int head, int first, int len, int T, __nv_bfloat16 *k,
+                                          __nv_bfloat16 *v) {
+    const int lane = threadIdx.x & 7, row0 = first + threadIdx.x / 8;
     uint4 x[kReadRows], y[kReadRows];
     uint2 nx[kReadRows], ny[kReadRows];
     uint32_t ex[kReadRows], ey[kReadRows];
     int page[kReadRows];
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
-        const int row = first + i * kRows;
+        const int row = row0 + i * kRows;
         page[i] = row < len ? paged_page(c, b, row / c.page) : -1;
     }
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
-        const int in = head * c.page + (first + i * kRows) % c.page;
+        const int in = head * c.page + (row0 + i * kRows) % c.page;
         const long long at = page[i] * c.stride + in * static_cast<long long>(HD) + 8 * lane;
         x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
         if (kInt8) {
@@ -157,11 +156,58 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const PagedCache c
     }
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
-        const int row = first + i * kRows;
-        if (row >= T) continue;
-        const long long to = (static_cast<long long>(bh) * T + row) * HD + 8 * lane;
+        const int row = row0 + i * kRows;
+        if (row >= (kTail ? T : len)) continue;
+        const long long to = static_cast<long long>(row) * HD + 8 * lane;
         *reinterpret_cast<uint4 *>(k + to) = kInt8 ? values(nx[i], paged_power(ex[i])) : x[i];
         *reinterpret_cast<uint4 *>(v + to) = kInt8 ? values(ny[i], paged_power(ey[i])) : y[i];
+    }
+}
+constexpr int kBlockRows = kRows * kReadRows;
+static_assert(kBlockRows == 128, "PagedPlan::blocks");
+
+template <bool kInt8>
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(const PagedCache c, __nv_bfloat16 *__restrict__ k,
+                                                              __nv_bfloat16 *__restrict__ v, int T, int blocks) {
+    const int bh = blockIdx.x / blocks, head = bh % c.Hkv, b = bh / c.Hkv;
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long to = static_cast<long long>(bh) * T * HD;
+    copy_rows<kInt8, true>(c, b, head, (blockIdx.x - bh * blocks) * kBlockRows, min(min(max(c.lens[b], 0), c.cap), T), T, k + to,
+                           v + to);
+}
+
+// The rows of the sequences that have row tiles (see PagedWide), in blocks of 128 rows
+// of a head: what attn_paged_bf16.cu would do to an int8 tile for each of the row
+// tiles that read it is done once (a chunk of 1,024 x 4 query heads behind 31,744 int8
+// rows 274 -> 165 us).
+template <bool kInt8>
+__global__ void __launch_bounds__(kThreads) paged_widen_kernel(const PagedAttnParams p, const PagedWide w) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, p.H / p.c.Hkv));
+    const int *blocks = p.plan + at.blocks, *slot_b = p.plan + at.slot_b;
+    const int slots = min(p.plan[1], w.slots), all = blocks[slots];
+    for (long long x = blockIdx.x; x < static_cast<long long>(all) * p.c.Hkv; x += gridDim.x) {
+        const int head = static_cast<int>(x / all), i = static_cast<int>(x - static_cast<long long>(head) * all);
+        int lo = 0, hi = slots;  // the last place whose first block is at most i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (blocks[mid] <= i)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int b = slot_b[lo], blk = i - blocks[lo], first = blk * kBlockRows;
+        const PagedSeq s = paged_seq(p.c, b);
+        const long long to = (static_cast<long long>(lo) * p.c.Hkv + head) * w.cap * HD;
+        copy_rows<kInt8, false>(p.c, b, head, first, s.len, s.len, w.k + to, w.v + to);
+        if (head == 0 && threadIdx.x < 32) {
+            const int key = first + static_cast<int>(threadIdx.x) * 16;
+            const bool gone = threadIdx.x < 8 && key < s.len && paged_page(p.c, b, key / p.c.page) < 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, gone);
+            if (threadIdx.x == 0) w.gone[static_cast<long long>(lo) * (w.cap / kBlockRows) + blk] = bits;
+        }
     }
 }
 
@@ -173,10 +219,16 @@ cudaError_t launch_paged_append(const PagedCache &c, const PagedRows &k, const P
 }
 
 cudaError_t launch_paged_read(const PagedCache &c, __nv_bfloat16 *k, __nv_bfloat16 *v, int T, cudaStream_t stream) {
-    const int blocks = (T + kRows * kReadRows - 1) / (kRows * kReadRows);
+    const int blocks = (T + kBlockRows - 1) / kBlockRows;
     const dim3 grid(static_cast<unsigned>(static_cast<long long>(blocks) * c.B * c.Hkv));
     return c.int8 ? launch_kernel(paged_read_kernel<true>, grid, dim3(kThreads), 0, stream, true, 1, c, k, v, T, blocks)
                   : launch_kernel(paged_read_kernel<false>, grid, dim3(kThreads), 0, stream, true, 1, c, k, v, T, blocks);
+}
+
+cudaError_t launch_paged_widen(const PagedAttnParams &p, const PagedWide &w, cudaStream_t stream) {
+    const dim3 grid(8 * kSmsPerGpu);
+    return p.c.int8 ? launch_kernel(paged_widen_kernel<true>, grid, dim3(kThreads), 0, stream, true, 1, p, w)
+                    : launch_kernel(paged_widen_kernel<false>, grid, dim3(kThreads), 0, stream, true, 1, p, w);
 }
 
 }  // namespace mha

@@ -43,9 +43,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMergeThreads = 128;
 // A row's reference serves until a unit's weights sum to more than this.
 constexpr float kSumMax = 65536.0f;
-// A worker's least share of the line, in units: what a piece costs to write
-// and join is worth a few units of reading.
-constexpr int kLeastShare = 4;
+// A worker's least share of the line, in units: what a piece costs to write and
+// join is worth a few units of reading.  (Alone, and of the four warps of a CTA.)
+constexpr int kLeastShare = 4, kLeastTeamShare = 8;
 
 // CTAs of an SM, by the rows of an item in eights.
 constexpr int paged_decode_ctas(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
@@ -141,20 +141,36 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
     const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
     int *first = p.plan + at.first, *cum = p.plan + at.cum, *seq = p.plan + at.seq;
     const int most = paged_most_tiles(p.c.N, p.c.B, g);
-    int tiles = 0;
+    int *slot = p.plan + at.slot, *slot_b = p.plan + at.slot_b, *blocks = p.plan + at.blocks;
+    int tiles = 0, slots = 0, rows = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        int n = 0, excl;
+        int n = 0, len = 0, excl;
         if (b < p.c.B) {
             const PagedSeq s = paged_seq(p.c, b);
             const int tokens = min(s.n, p.max_new);
             if (tokens * g > p.small_rows) n = (tokens + tt - 1) / tt;
+            len = s.len;
         }
         const int total = block_sum(n, warp_sums, excl);
         if (b < p.c.B) first[b] = min(tiles + excl, most);
         tiles = min(tiles + total, most);  // (more than that only where sequences overlap)
+        const int taken = block_sum(n > 0 ? 1 : 0, warp_sums, excl);
+        const int mine = slots + excl;
+        if (b < p.c.B) {
+            slot[b] = n > 0 ? mine : -1;
+            if (n > 0) slot_b[mine] = b;
+        }
+        const int all = block_sum(n > 0 ? (len + 127) / 128 : 0, warp_sums, excl);
+        if (b < p.c.B && n > 0) blocks[mine] = rows + excl;
+        slots += taken;
+        rows += all;
     }
-    if (threadIdx.x == 0) first[p.c.B] = tiles;
+    if (threadIdx.x == 0) {
+        first[p.c.B] = tiles;
+        blocks[slots] = rows;
+        p.plan[1] = slots;
+    }
     __syncthreads();
     int keys = 0;
     for (int x0 = 0; x0 < tiles; x0 += kThreads) {
@@ -192,6 +208,8 @@ template <bool kInt8, int kN>
 __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_kernel(const PagedAttnParams p, int list) {
     constexpr int kRows = 8 * kN, kKeys = kUnitKeys<kInt8>, kBlocks = kKeys / 16;
     __shared__ int warp_sums[kWarps], at_b[kWarps], at_start[kWarps];
+    __shared__ float4 sh_o[kWarps][kRows][HD / 4];
+    __shared__ float2 sh_ml[kWarps][kRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l4 = lane >> 2, c = lane & 3;
     pdl_wait();
@@ -200,19 +218,27 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         list_tiles(p, warp_sums);
         return;
     }
-    const int workers = (gridDim.x - (list ? 1 : 0)) * kWarps, me = blockIdx.x * kWarps + warp;
+    const int ctas = gridDim.x - (list ? 1 : 0);
     const int g = p.H / p.c.Hkv;
     const int per_page = p.c.page / 16;
 
-    // The line's length, the shares, and where this warp's begins.
+    // The line's length, the shares, and where this worker's begins.
     if (lane == 0) at_b[warp] = -1;
-    int total = 0, mine = 0, excl = 0;
+    int total = 0, items = 0, mine = 0, excl = 0, unused;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
+        Shape sh{};
+        if (b < p.c.B) sh = shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g);
+        mine = sh.total;
+        items += block_sum(p.c.Hkv * sh.tiles, warp_sums, unused);
         total += block_sum(mine, warp_sums, excl);
     }
-    const int share = max((total + workers - 1) / workers, kLeastShare);
+    // A CTA's warps are workers of their own, or, where items would be divided among
+    // more than two of those, one together.
+    const int alone = (total + ctas * kWarps - 1) / (ctas * kWarps);
+    const bool team = total >= 2ll * alone * items;
+    const int share = team ? max((total + ctas - 1) / ctas, kLeastTeamShare) : max(alone, kLeastShare);
+    const int me = team ? blockIdx.x : blockIdx.x * kWarps + warp;
     int base = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
@@ -221,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             // (a share past the line's end may start past 2^31)
-            const long long s = static_cast<long long>(blockIdx.x * kWarps + w) * share;
+            const long long s = static_cast<long long>(team ? blockIdx.x : blockIdx.x * kWarps + w) * share;
             if (s >= base + excl && s < base + excl + mine) {
                 at_b[w] = b;
                 at_start[w] = base + excl;
@@ -229,10 +255,13 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         }
         base += sum;
     }
+    // (a record for every warp, whether it is a worker or not)
+    if (team && warp > 0 && lane == 0) p.join[ctas + blockIdx.x * (kWarps - 1) + warp - 1] = PagedJoin{};
+    const int sub = team ? warp : 0, step = team ? kWarps : 1;
     __syncthreads();
     int b = at_b[warp];
     if (b < 0) {
-        if (lane == 0) p.join[me] = PagedJoin{};
+        if (lane == 0 && sub == 0) p.join[me] = PagedJoin{};
         return;
     }
     const int start = me * share;
@@ -245,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         const int item = rel / sh.units, u0 = rel - item * sh.units, u1 = min(sh.units, u0 + left);
         const int head = item / sh.tiles, tile = item - head * sh.tiles;
         const int rows = min(s.n, p.max_new) * g - tile * kRows;  // of this item, if less than kRows
-        if (first_piece && lane == 0) {
+        if (first_piece && lane == 0 && sub == 0) {
             PagedJoin j{};
-            if (u0 > 0 && u0 <= share)
-                j = PagedJoin{min(rows, kRows), tile * kRows, head, s.row0, (start - u0 + sh.units - 1) / share};
+            if (u0 > 0)
+                j = PagedJoin{min(rows, kRows), tile * kRows, head, s.row0, (start - u0) / share, (start - u0 + sh.units - 1) / share};
             p.join[me] = j;
         }
 
@@ -303,27 +332,29 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         }
         least = __reduce_min_sync(0xffffffffu, least);
 
-        // Sub-units of 16 keys, 32 from `sub0` on: a lane holds the page of its one.
-        int sub0 = u0 * kBlocks, page = -1, in_page = 0;
-        auto look_up = [&](int sub) {
-            sub0 = sub;
-            const int i = (sub0 + lane) / per_page;
-            in_page = (sub0 + lane - i * per_page) * 16;
-            page = (sub0 + lane) * 16 < s.len ? paged_page(p.c, b, i) : -1;
+        // The pages of the warp's next 32 blocks of 16 keys, those of units window0,
+        // window0 + step, ..., a lane each.
+        int window0 = 0, page = -1, in_page = 0;
+        auto look_up = [&](int u) {
+            window0 = u;
+            const int block = (u + lane / kBlocks * step) * kBlocks + lane % kBlocks, i = block / per_page;
+            in_page = (block - i * per_page) * 16;
+            page = block * 16 < s.len ? paged_page(p.c, b, i) : -1;
         };
-        look_up(sub0);
+        look_up(u0 + sub);
         // Where the unit's blocks of 16 keys lie, how many of their keys are there;
         // the exponent of the lane's key.
         long long at[kBlocks], s_at = 0;
         int valid[kBlocks], s_valid = 0;
         bool full = false;  // all of them
         auto place = [&](int u) {
-            if (u * kBlocks - sub0 >= 32) look_up(u * kBlocks);
+            if (u - window0 >= 32 / kBlocks * step) look_up(u);
+            const int from = (team ? (u - window0) / kWarps : u - window0) * kBlocks;
             full = (u + 1) * kKeys <= s.len;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
-                const int pg = __shfl_sync(0xffffffffu, page, u * kBlocks + i - sub0);
-                const int in = __shfl_sync(0xffffffffu, in_page, u * kBlocks + i - sub0);
+                const int pg = __shfl_sync(0xffffffffu, page, from + i);
+                const int in = __shfl_sync(0xffffffffu, in_page, from + i);
                 const int row = head * p.c.page + in;
                 at[i] = pg * p.c.stride + row * HD;
                 valid[i] = pg >= 0 ? s.len - (u * kBlocks + i) * 16 : 0;
@@ -390,11 +421,13 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         // while the next one's scores are: 32 registers instead of 64, and four
         // CTAs an SM.
         Part kp, vp;
-        place(u0);
-        load(std::false_type{}, kp);
-        load(std::true_type{}, vp);
+        if (u0 + sub < u1) {
+            place(u0 + sub);
+            load(std::false_type{}, kp);
+            load(std::true_type{}, vp);
+        }
 #pragma unroll 1
-        for (int u = u0; u < u1; ++u) {
+        for (int u = u0 + sub; u < u1; u += step) {
             // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
             float st[kN][kBlocks][4];
 #pragma unroll
@@ -445,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                         }
                     }
             }
-            if (u + 1 < u1) {
-                place(u + 1);
+            if (u + step < u1) {
+                place(u + step);
                 load(std::false_type{}, kp);
             }
             // Weights against the reference in hand.  `shift`: -reference, 0 before
@@ -556,13 +589,16 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                     for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
                 }
             }
-            if (u + 1 < u1) load(std::true_type{}, vp);
+            if (u + step < u1) load(std::true_type{}, vp);
         }
 
-        // The item, or the piece: slot 2 me of one that began before this
-        // worker, 2 me + 1 of one that goes on behind it.
-        const bool whole = u0 == 0 && u1 == sh.units;
-        const long long slot = (2ll * me + (u0 > 0 ? 0 : 1)) * kRows;
+        // The sums of the worker's warps meet in shared memory.
+        auto meet = [team]() {
+            if (team)
+                __syncthreads();
+            else
+                __syncwarp();
+        };
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -572,29 +608,40 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = 8 * n + 2 * c + r;
-                if (row >= rows) continue;
-                float y[8];
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    y[2 * f] = o[n][f][r];
-                    y[2 * f + 1] = o[n][f][2 + r];
-                }
-                if (whole) {
-                    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-                    const int at = tile * kRows + row, t = at / g;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) w[f] = sum != 0.f ? pack_bf16x2(y[2 * f] * inv, y[2 * f + 1] * inv) : 0u;
-                    if (in_bounds(head * g + at - t * g < p.H && s.row0 + t < p.c.N, p.status))
-                        *reinterpret_cast<uint4 *>(p.o + (head * g + at - t * g) * p.o_stride_h + (s.row0 + t) * p.o_stride_t +
-                                                   8 * l4) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else if (in_bounds(me < workers, p.status)) {
-                    float4 *to = reinterpret_cast<float4 *>(p.part_o + (slot + row) * HD + 8 * l4);
-                    to[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    to[1] = make_float4(y[4], y[5], y[6], y[7]);
-                    if (l4 == 0) p.part_ml[slot + row] = make_float2(m[n][r], sum);
-                }
+                sh_o[warp][row][2 * l4] = make_float4(o[n][0][r], o[n][0][2 + r], o[n][1][r], o[n][1][2 + r]);
+                sh_o[warp][row][2 * l4 + 1] = make_float4(o[n][2][r], o[n][2][2 + r], o[n][3][r], o[n][3][2 + r]);
+                if (l4 == 0) sh_ml[warp][row] = make_float2(m[n][r], sum);
             }
+        meet();
+        // The item, or the piece: slot 2 me of one that began before this worker,
+        // 2 me + 1 of one that goes on behind it.  16 lanes take a row.
+        const bool whole = u0 == 0 && u1 == sh.units;
+        const long long slot = (2ll * me + (u0 > 0 ? 0 : 1)) * kRows;
+        const int w0 = team ? 0 : warp, wn = team ? kWarps : 1, part = lane & 15;
+        for (int row = (team ? threadIdx.x : lane) / 16; row < min(rows, kRows); row += 2 * wn) {
+            float top = -INFINITY, sum = 0.f;
+            for (int w = w0; w < w0 + wn; ++w) top = fmaxf(top, sh_ml[w][row].x);
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = w0; w < w0 + wn; ++w) {
+                const float2 ml = sh_ml[w][row];
+                if (ml.y == 0.f) continue;  // no visible key
+                const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+                const float4 x = sh_o[w][row][part];
+                sum += ml.y * f;
+                y = make_float4(y.x + x.x * f, y.y + x.y * f, y.z + x.z * f, y.w + x.w * f);
+            }
+            if (whole) {
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;
+                const int at = tile * kRows + row, t = at / g, h = head * g + at - t * g;
+                if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
+                    reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[part] =
+                        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+            } else if (in_bounds(me < ctas * kWarps, p.status)) {
+                reinterpret_cast<float4 *>(p.part_o + (slot + row) * HD)[part] = y;
+                if (part == 0) p.part_ml[slot + row] = make_float2(top, sum);
+            }
+        }
+        meet();
 
         left -= u1 - u0;
         rel += u1 - u0;
@@ -609,17 +656,16 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
 
 // ------------------------------------------------------------ joining partial sums
 //   o = (sum_s w_s O_s) / (sum_s w_s l_s),  w_s = 2^(m_s - M),  M = max_s m_s
-// over the pieces of an item: the tail slot of the worker before the record's, then
-// the head slots up to the item's last worker, in that order whatever the timing.
+// over the pieces of an item: the tail slot of its first worker, then the head slots
+// up to its last one, in that order whatever the timing.
 // 16 lanes take one row (4 features each), up to 8 pieces at a time; groups that
 // would be idle share a row's pieces.  A piece without a visible key has m = -inf,
 // l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is taken as
 // paged_level gives it.
 //
-// Bound by latency: a block for every worker, most of which find nothing to join,
-// and for every 16 rows of a CTA's row tile; small, so that all of them are
-// resident together.
-constexpr int kMergeRows = 16;  // of a row tile of 128
+// Bound by latency: small blocks, so that all of them are resident together, one for
+// every worker and several for every CTA with row tiles; most find nothing to join.
+constexpr int kTileBlocks = 8;  // for a worker of attn_paged_bf16.cu
 constexpr int kGroups = kMergeThreads / 16;
 constexpr int kBatch = 8;
 
@@ -657,16 +703,20 @@ __global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const Pag
     pdl_launch_dependents();
     const int x = blockIdx.x;
     const bool small = x < workers;
-    const int w = small ? x : (x - workers) / (128 / kMergeRows);
-    const int from = small ? 0 : (x - workers - w * (128 / kMergeRows)) * kMergeRows;
+    const int w = small ? x : (x - workers) / kTileBlocks;
     const PagedJoin j = small ? p.join[w] : p.tile_join[w];
-    if (j.rows <= from) return;
+    if (j.rows == 0) return;
+    // the rows are divided among the blocks of all workers that began inside the item
+    const int blocks = (j.last - j.first) * (small ? 1 : kTileBlocks);
+    const int block = (w - 1 - j.first) * (small ? 1 : kTileBlocks) + (small ? 0 : (x - workers) % kTileBlocks);
+    const int from = j.rows * block / blocks, rows = j.rows * (block + 1) / blocks - from;
+    if (rows == 0) return;
     const int g = p.H / p.c.Hkv;
     const int grp = threadIdx.x / 16, lane = threadIdx.x & 15;
-    const int rows = small ? j.rows : min(j.rows - from, kMergeRows), slot_rows = small ? tile_rows : 128;
+    const int slot_rows = small ? tile_rows : 128;
     const float *part_o = small ? p.part_o : p.tile_o;
     const float2 *part_ml = small ? p.part_ml : p.tile_ml;
-    const int pieces = j.last - w + 2;
+    const int pieces = j.last - j.first + 1;
     int per = 1;  // groups of a row
     while (per * 2 * rows <= kGroups) per *= 2;
     for (int r0 = 0; r0 < rows; r0 += kGroups / per) {
@@ -682,7 +732,7 @@ __global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const Pag
                     ml[e] = make_float2(-INFINITY, 0.f);
                     o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i < pieces) {
-                        const long long slot = (2ll * (w - 1 + i) + (i == 0 ? 1 : 0)) * slot_rows + from + row;
+                        const long long slot = (2ll * (j.first + i) + (i == 0 ? 1 : 0)) * slot_rows + from + row;
                         ml[e] = part_ml[slot];
                         o[e] = reinterpret_cast<const float4 *>(part_o + slot * HD)[lane];
                     }
@@ -718,7 +768,7 @@ __global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const Pag
 
 template <bool kInt8>
 cudaError_t launch_rows(const PagedAttnParams &p, int list, int tile_rows, cudaStream_t stream) {
-    const dim3 grid(paged_decode_workers(tile_rows, kInt8) / kWarps + list), block(kThreads);
+    const dim3 grid(paged_decode_workers(tile_rows) / kWarps + list), block(kThreads);
     if (tile_rows == 8) return launch_kernel(paged_decode_kernel<kInt8, 1>, grid, block, 0, stream, true, 1, p, list);
     if (tile_rows == 16) return launch_kernel(paged_decode_kernel<kInt8, 2>, grid, block, 0, stream, true, 1, p, list);
     return launch_kernel(paged_decode_kernel<kInt8, 4>, grid, block, 0, stream, true, 1, p, list);
@@ -728,18 +778,15 @@ cudaError_t launch_rows(const PagedAttnParams &p, int list, int tile_rows, cudaS
 
 int paged_decode_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-int paged_decode_workers(int tile_rows, bool int8) {
-    (void)int8;
-    return kSmsPerGpu * paged_decode_ctas(tile_rows / 8) * kWarps;
-}
+int paged_decode_workers(int tile_rows) { return kSmsPerGpu * paged_decode_ctas(tile_rows / 8) * kWarps; }
 
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
     return p.c.int8 ? launch_rows<true>(p, tiles ? 1 : 0, tile_rows, stream) : launch_rows<false>(p, tiles ? 1 : 0, tile_rows, stream);
 }
 
 cudaError_t launch_paged_merge(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
-    const int workers = paged_decode_workers(tile_rows, p.c.int8 != 0);
-    const unsigned grid = workers + (tiles ? kPagedTileCtas * (128 / kMergeRows) : 0);
+    const int workers = paged_decode_workers(tile_rows);
+    const unsigned grid = workers + (tiles ? kPagedTileCtas * kTileBlocks : 0);
     return launch_kernel(paged_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
 }
 
