@@ -581,62 +581,77 @@ def sdpa_decode_shared_forward(q, k_prefix, v_prefix, k_cache, v_cache, cache_le
 
 
 # ------------------------------------------------------------------ paged K/V cache
-def _packed(torch, name, t, heads, n, d, device):
+def _packed(torch, name, t, shape, device):
     """(pointer, head stride, row stride) of bf16 rows t (heads, n, d), whose last
     dimension alone has to be contiguous."""
     try:
-        shape, strides, fine = t.shape, t.stride(), t.dtype is torch.bfloat16 and t.get_device() == device
-    except AttributeError:
-        raise ValueError("%s must be a CUDA tensor" % name) from None
-    if not t.is_cuda:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == device:
+            head, row, one = t.stride()
+            if one == 1:
+                return t.data_ptr(), head, row
+    except (AttributeError, ValueError):
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if not fine:
+    if t.dtype is not torch.bfloat16 or t.get_device() != device:
         raise ValueError("%s must be bfloat16, on cuda:%d, the current device" % (name, device))
-    if shape != (heads, n, d):
-        raise ValueError("%s must have the shape %s" % (name, (heads, n, d)))
-    if strides[2] != 1 and d > 1:
-        raise ValueError("%s must be contiguous in its last dimension" % name)
-    return t.data_ptr(), strides[0], strides[1]
+    if t.shape != shape:
+        raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
+    raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
 def _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales):
-    """Checked (PagedCache, head size, device index)."""
+    """Checked (mha_paged_cache as bytes, B, h_kv, page rows, max_pages, head size,
+    device index)."""
     device = torch.cuda.current_device()
+    int32 = torch.int32
     try:
         pages, h_kv, rows, d = shape = k_pages.shape
         strides, dtype = k_pages.stride(), k_pages.dtype
         B, max_pages = page_table.shape
+        fine = (k_pages.get_device() == device and v_pages.get_device() == device and v_pages.dtype is dtype
+                and v_pages.shape == shape and v_pages.stride() == strides
+                and page_table.dtype is int32 and page_table.get_device() == device and page_table.is_contiguous()
+                and seq_lens.dtype is int32 and seq_lens.shape == (B,) and seq_lens.get_device() == device
+                and seq_lens.is_contiguous())
     except (AttributeError, ValueError):
-        raise ValueError("k_pages must be a tensor of four dimensions, page_table one of two") from None
-    if dtype is not torch.bfloat16 and dtype is not torch.int8:
-        raise ValueError("k_pages must be bfloat16 or int8")
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
-            raise ValueError("%s must be a tensor on cuda:%d, the current device" % (name, device))
-        if t.dtype is not dtype or t.shape != shape or t.stride() != strides:
-            raise ValueError("v_pages must have k_pages' dtype, shape and strides")
+        fine = False
+    if not fine:
+        _refuse_paged(torch, k_pages, v_pages, page_table, seq_lens, device)
     if pages and (strides[3] != 1 or strides[2] != d or (h_kv > 1 and strides[1] != rows * d)):
         raise ValueError("a page must be contiguous")
-    c = _native.PagedCache()
-    c.dtype = MHA_BF16
-    if dtype is torch.int8:
+    if dtype is torch.bfloat16:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("k_scales and v_scales go with int8 pages")
+        kind, ks, vs = MHA_BF16, 0, 0
+    elif dtype is torch.int8:
         if k_scales is None or v_scales is None:
             raise ValueError("int8 pages need k_scales and v_scales")
         _require(("k_scales", "v_scales"), (k_scales, v_scales), torch.uint8, (pages, h_kv, rows), device)
-        c.dtype, c.k_scales, c.v_scales = MHA_INT8, k_scales.data_ptr(), v_scales.data_ptr()
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("k_scales and v_scales go with int8 pages")
-    _require(("page_table",), (page_table,), torch.int32, (B, max_pages), device)
-    if seq_lens is None:
-        raise ValueError("seq_lens must be a tensor")
-    _require(("seq_lens",), (seq_lens,), torch.int32, (B,), device)
+        kind, ks, vs = MHA_INT8, k_scales.data_ptr(), v_scales.data_ptr()
+    else:
+        raise ValueError("k_pages must be bfloat16 or int8")
+    starts = 0
     if row_starts is not None:
-        _require(("row_starts",), (row_starts,), torch.int32, (B + 1,), device)
-        c.row_starts = row_starts.data_ptr()
-    c.k_pages, c.v_pages, c.page_stride = k_pages.data_ptr(), v_pages.data_ptr(), strides[0]
-    c.page_table, c.seq_lens = page_table.data_ptr(), seq_lens.data_ptr()
-    c.B, c.h_kv, c.page_rows, c.num_pages, c.max_pages = B, h_kv, rows, pages, max_pages
-    return c, d, device
+        _require(("row_starts",), (row_starts,), int32, (B + 1,), device)
+        starts = row_starts.data_ptr()
+    return (_native.pack_paged_cache(kind, k_pages.data_ptr(), v_pages.data_ptr(), strides[0], ks, vs, page_table.data_ptr(),
+                                     starts, seq_lens.data_ptr(), B, h_kv, rows, pages, max_pages),
+            B, h_kv, rows, max_pages, d, device)
+
+
+def _refuse_paged(torch, k_pages, v_pages, page_table, seq_lens, device):
+    """What _paged_cache found wrong."""
+    for name, t, dims in (("k_pages", k_pages, 4), ("v_pages", v_pages, 4), ("page_table", page_table, 2), ("seq_lens", seq_lens, 1)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device:
+            raise ValueError("%s must be a tensor on cuda:%d, the current device" % (name, device))
+        if t.dim() != dims:
+            raise ValueError("%s must have %d dimensions" % (name, dims))
+    if v_pages.dtype is not k_pages.dtype or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("v_pages must have k_pages' dtype, shape and strides")
+    for name, t in (("page_table", page_table), ("seq_lens", seq_lens)):
+        _check_dev(name, t, torch.int32)
+    raise ValueError("seq_lens must have the shape (%d,)" % page_table.shape[0])
 
 
 def _needs_starts(row_starts):
@@ -656,14 +671,15 @@ def paged_cache_append(k, v, k_pages, v_pages, page_table, row_starts, seq_lens,
     - 127).  Returns (k_pages, v_pages)."""
     torch = _torch()
     _needs_starts(row_starts)
-    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
+    cache, _, h_kv, _, _, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
     try:
         n = k.shape[1]
     except (AttributeError, IndexError):
         raise ValueError("k must be a tensor of three dimensions") from None
-    kp = _packed(torch, "k", k, cache.h_kv, n, d, dev)
-    vp = _packed(torch, "v", v, cache.h_kv, n, d, dev)
-    rc = lib.paged_cache_append(ctypes.addressof(cache), *kp, *vp, n, d, _stream_on(stream, dev))
+    shape = (h_kv, n, d)
+    kp, kh, kt = _packed(torch, "k", k, shape, dev)
+    vp, vh, vt = _packed(torch, "v", v, shape, dev)
+    rc = lib.paged_cache_append(cache, kp, kh, kt, vp, vh, vt, n, d, _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "paged_cache_append")
     return k_pages, v_pages
@@ -675,16 +691,20 @@ def paged_cache_read(k_pages, v_pages, page_table, seq_lens, k=None, v=None, *, 
     rows, 64), as the other calls take them; zeros from seq_lens[b] on.  rows:
     those of k, else as many as the page table has.  Returns (k, v)."""
     torch = _torch()
-    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, None, seq_lens, k_scales, v_scales)
+    cache, B, h_kv, page_rows, max_pages, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, None, seq_lens, k_scales,
+                                                                v_scales)
     if rows is None:
-        rows = cache.max_pages * cache.page_rows if k is None else k.shape[2]
-    shape = (cache.B, cache.h_kv, rows, d)
+        rows = max_pages * page_rows if k is None else k.shape[2]
+    shape = (B, h_kv, rows, d)
     if k is None:
         k = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _require(("k",), (k,), torch.bfloat16, shape, dev)
     if v is None:
         v = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
-    _require(("k", "v"), (k, v), torch.bfloat16, shape, dev)
-    rc = lib.paged_cache_read(ctypes.addressof(cache), k.data_ptr(), v.data_ptr(), rows, d, _stream_on(stream, dev))
+    else:
+        _require(("v",), (v,), torch.bfloat16, shape, dev)
+    rc = lib.paged_cache_read(cache, k.data_ptr(), v.data_ptr(), rows, d, _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "paged_cache_read")
     return k, v
@@ -702,21 +722,21 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, ou
     past the last sequence's are not written."""
     torch = _torch()
     _needs_starts(row_starts)
-    cache, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
+    cache, _, _, _, _, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales)
     try:
-        h, n, _ = q.shape
+        h, n, _ = shape = q.shape
     except (AttributeError, ValueError):
         raise ValueError("q must be a tensor of three dimensions") from None
-    qp = _packed(torch, "q", q, h, n, d, dev)
+    qp, qh, qt = _packed(torch, "q", q, (h, n, d), dev)
     if out is None:
         out = _result(stream, torch.empty_like, q)
-    op = _packed(torch, "out", out, h, n, d, dev)
+    op, oh, ot = _packed(torch, "out", out, shape, dev)
     if status is not None:
         _check_dev("status", status, torch.int32)
-    max_new = n if max_new is None else max_new
-    need = lib.sdpa_paged_workspace_bytes(ctypes.addressof(cache), h, n, max_new)
-    workspace, size = _scratch_here(torch, workspace, need, dev, stream)
-    rc = lib.sdpa_paged_forward(ctypes.addressof(cache), *qp, *op, workspace.data_ptr(), size, h, n, max_new, d,
+    if max_new is None:
+        max_new = n
+    workspace, size = _scratch_here(torch, workspace, lib.sdpa_paged_workspace_bytes(cache, h, n, max_new), dev, stream)
+    rc = lib.sdpa_paged_forward(cache, qp, qh, qt, op, oh, ot, workspace.data_ptr(), size, h, n, max_new, d,
                                 1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask), _ptr(status),
                                 _stream_on(stream, dev))
     if rc != MHA_OK:

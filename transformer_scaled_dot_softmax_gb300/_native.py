@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # MHA_LIBRARY may name another build of this same library (the tests load the
@@ -37,6 +38,10 @@ class PagedCache(ctypes.Structure):
                 ("h_kv", ctypes.c_int), ("page_rows", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("max_pages", ctypes.c_int)]
 
+
+# The same as bytes, a call's fields in one packing (attribute by attribute they
+# take longer than the launch); bytes pass as the pointer they are.
+pack_paged_cache = struct.Struct("@iPPqPPPPPiiiii").pack
 
 # Every symbol include/mha.h declares, with its ctypes signature.
 _vp, _ci, _cf, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
