@@ -489,8 +489,9 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  *   sequence's own values may reach all its outputs.  Entries of k and v up to
  *   2^46 in magnitude.
  *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
- *   in flight.
- * Two launches (sequences with up to 32 query rows per K/V head; joining of the
+ *   in flight.  Few query rows of short sequences (max_pages page_rows <= 1024) take
+ *   one launch and 0 bytes; NULL is allowed then.
+ * Two launches (sequences with up to 16 query rows per K/V head, 32 with int8; joining of the
  * partial sums of divided key ranges), a third between them when max_new allows
  * more: tcgen05 products over tiles of 128 rows; and when it allows 512 and the cache
  * is int8, or has pages that are not a multiple of 64 rows, one that lays these

@@ -201,9 +201,10 @@ SHAPES = [(1, 1, 16, [1], [1]), (4, 2, 16, [5, 16, 17, 100], [1, 1, 1, 1]), (8, 
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("causal", [True, False])
-def test_attention(lib, shape, int8, causal):
+@pytest.mark.parametrize("capacity", [0, 2000])  # room for 2,000 rows: key ranges may be divided
+def test_attention(lib, shape, int8, causal, capacity):
     h, *rest = shape
-    c = pr.Cache(*rest, int8=int8, seed=sum(rest[2])).fill()
+    c = pr.Cache(*rest, int8=int8, seed=sum(rest[2]), capacity=capacity).fill()
     for gain in (1.0, 6.0):
         compare(lib, c, queries(c, h, gain), causal)
 
@@ -230,9 +231,10 @@ def test_strides_of_queries_outputs_and_pages(lib, int8, new):
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("new", [1, 3, 100])
-def test_pages_that_are_not_there_are_not_seen(lib, int8, new):
+@pytest.mark.parametrize("capacity", [0, 2000])
+def test_pages_that_are_not_there_are_not_seen(lib, int8, new, capacity):
     """Table entries of -1 and past the pool, at the beginning, inside and for a whole sequence."""
-    c = pr.Cache(2, 32, [300, 130, 40, 700], [new, new, min(new, 40), new], int8=int8, seed=9).fill()
+    c = pr.Cache(2, 32, [300, 130, 40, 700], [new, new, min(new, 40), new], int8=int8, seed=9, capacity=capacity).fill()
     gone = [torch.zeros(n, dtype=torch.bool, device="cuda") for n in c.lens]
     for b, i, entry in ((0, 0, -1), (0, 1, -1), (0, 5, c.pages), (1, 4, 1 << 30), (2, 0, -1), (2, 1, -5), (3, 7, -2), (3, 8, -1)):
         c.page_table[b, i] = entry
@@ -288,9 +290,10 @@ def test_scales_of_the_scores(lib, int8, scale):
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("new", [1, 2, 90])
-def test_scores_that_grow_and_shrink_along_the_keys(lib, int8, new):
+@pytest.mark.parametrize("capacity", [0, 2000])
+def test_scores_that_grow_and_shrink_along_the_keys(lib, int8, new, capacity):
     """Scores that rise by thousands towards either end, so that references move at almost every step, and rows far below 0."""
-    c = pr.Cache(1, 16, [900, 900, 260], [new, new, new], int8=int8, seed=13)
+    c = pr.Cache(1, 16, [900, 900, 260], [new, new, new], int8=int8, seed=13, capacity=capacity)
     ramp = torch.linspace(0, 60, 900, device="cuda")
     up = torch.ones(64, device="cuda")
     for b, r in enumerate((ramp, ramp.flip(0), -ramp[:260] - 40)):

@@ -28,11 +28,12 @@ MIXES = [(1, [900, 70, 333], [1, 1, 1]), (20, [900, 70, 333], [20, 3, 1]), (300,
 
 @pytest.mark.parametrize("most,lens,new", MIXES)
 @pytest.mark.parametrize("int8", [False, True])
-def test_streams_and_graphs(lib, most, lens, new, int8):
+@pytest.mark.parametrize("capacity", [0, 2000])  # items whole, and divided
+def test_streams_and_graphs(lib, most, lens, new, int8, capacity):
     """Two calls at once on two streams, each with scratch of its own; captured calls replayed one after another."""
     cases = []
     for seed in (1, 2):
-        c = pr.Cache(2, 16, lens, new, int8=int8, seed=seed).fill()
+        c = pr.Cache(2, 16, lens, new, int8=int8, seed=seed, capacity=capacity).fill()
         cases.append((c, queries(c, 8, seed=seed)))
     want = [compare(lib, c, q, True) for c, q in cases]
     streams = [torch.cuda.Stream() for _ in cases]
@@ -113,10 +114,11 @@ def test_a_captured_step_follows_lengths_tables_and_starts(lib, int8):
 
 @pytest.mark.parametrize("most,lens,new", MIXES)
 @pytest.mark.parametrize("int8", [False, True])
-def test_inputs_written_just_before(lib, most, lens, new, int8):
+@pytest.mark.parametrize("capacity", [0, 2000])
+def test_inputs_written_just_before(lib, most, lens, new, int8, capacity):
     """Everything a call reads is written right before it and destroyed right after it, eagerly and captured: launches may
     overlap the ends of the ones before them."""
-    c = pr.Cache(2, 32, lens, new, int8=int8, seed=6).fill()
+    c = pr.Cache(2, 32, lens, new, int8=int8, seed=6, capacity=capacity).fill()
     q = queries(c, 8)
     want, (wk, wv) = call(lib, c, q, most), lib.paged_cache_read(*c.args, c.seq_lens, **c.scales)
     names = ["k_pages", "v_pages", "page_table", "row_starts", "seq_lens"] + (["k_scales", "v_scales"] if int8 else [])
@@ -244,7 +246,7 @@ def test_long_sequences(lib):
 
 
 def test_refusals_on_the_device(lib):
-    c = pr.Cache(2, 16, [40, 30], [3, 1]).fill()
+    c = pr.Cache(2, 16, [40, 30], [3, 1], capacity=2000).fill()
     q = queries(c, 4)
     with pytest.raises(ValueError):  # not contiguous in the last dimension
         call(lib, c, torch.cat((q, q), 2)[:, :, ::2], 3)

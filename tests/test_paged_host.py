@@ -20,7 +20,7 @@ def nat():
 
 def cache(nat, **kw):
     f = dict(dtype=nat.MHA_BF16, k_pages=FAKE, v_pages=FAKE, page_stride=4 * 16 * 64, k_scales=None, v_scales=None,
-             page_table=FAKE, row_starts=FAKE, seq_lens=FAKE, B=2, h_kv=4, page_rows=16, num_pages=10, max_pages=8)
+             page_table=FAKE, row_starts=FAKE, seq_lens=FAKE, B=2, h_kv=4, page_rows=16, num_pages=10, max_pages=80)
     f.update(kw)
     return nat.PagedCache(**f)
 
@@ -134,11 +134,14 @@ def test_workspace_sizes(nat):
     assert need(cache(nat, page_rows=8)) == 0
     # sizes alone count
     assert need(cache(nat, k_pages=None, v_pages=None, page_table=None, seq_lens=None, row_starts=None)) == need(cache(nat))
+    # none where every item is one CTA's: few query rows of short sequences
+    assert need(cache(nat, max_pages=64)) == 0 < need(cache(nat, max_pages=65))
+    assert need(cache(nat, max_pages=64), N=17, most=17) > 0
     # it grows with the rows that may have to be stacked, and an int8 chunk's cache has room as bf16
     small, chunk = need(cache(nat), N=600, most=1), need(cache(nat, page_rows=64, page_stride=4 * 64 * 64), N=600, most=600)
     assert 0 < small < chunk
     wide = need(cache(nat, dtype=nat.MHA_INT8, page_rows=64, page_stride=4 * 64 * 64), N=600, most=600)
-    assert wide >= chunk + 2 * 2 * 4 * (8 * 64) * 64 * 2
+    assert wide >= chunk + 2 * 2 * 4 * (80 * 64) * 64 * 2
     # ... up to 4 GiB of it
     huge = cache(nat, dtype=nat.MHA_INT8, B=64, page_rows=64, page_stride=4 * 64 * 64, max_pages=1 << 14)
     assert need(huge, N=60000, most=600) < 1 << 30

@@ -735,8 +735,10 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, ou
         _check_dev("status", status, torch.int32)
     if max_new is None:
         max_new = n
-    workspace, size = _scratch_here(torch, workspace, lib.sdpa_paged_workspace_bytes(cache, h, n, max_new), dev, stream)
-    rc = lib.sdpa_paged_forward(cache, qp, qh, qt, op, oh, ot, workspace.data_ptr(), size, h, n, max_new, d,
+    size = lib.sdpa_paged_workspace_bytes(cache, h, n, max_new)
+    if size or workspace is not None:
+        workspace, size = _scratch_here(torch, workspace, size, dev, stream)
+    rc = lib.sdpa_paged_forward(cache, qp, qh, qt, op, oh, ot, _ptr(workspace), size, h, n, max_new, d,
                                 1.0 / math.sqrt(d) if scale is None else scale, _mask_code(mask), _ptr(status),
                                 _stream_on(stream, dev))
     if rc != MHA_OK:

@@ -89,7 +89,8 @@ mha_status check_rows(const void *x, long long stride_h, long long stride_t, int
 
 // What a call's workspace holds.
 struct Layout {
-    bool tiles;      // sequences may have more than kPagedSmallRows stacked rows
+    bool tiles;      // sequences may have more than paged_small_rows() stacked rows
+    bool undivided;  // no key range is divided
     int tile_rows;   // of paged_decode.cu
     int slots, wide_cap;  // places for rows laid out as bf16 (0: none), their rows
     size_t part_o, part_ml, join, plan, tile_o, tile_ml, tile_join, wide_k, wide_v, gone, bytes;
@@ -97,9 +98,13 @@ struct Layout {
 Layout layout(const PagedCache &c, int g, int max_new) {
     Layout l{};
     const long long most = static_cast<long long>(std::min(max_new, c.N)) * g;
-    l.tiles = most > kPagedSmallRows;
+    const int small = paged_small_rows(c.int8 != 0);
+    l.tiles = most > small;
     // among longer chunks the short ones are taken for single tokens
-    l.tile_rows = paged_decode_rows(l.tiles ? g : static_cast<int>(most));
+    l.tile_rows = paged_decode_rows(l.tiles ? std::min(g, small) : static_cast<int>(most));
+    const long long items = static_cast<long long>(c.B) * c.Hkv * ((most + l.tile_rows - 1) / l.tile_rows);
+    l.undivided = !l.tiles && c.cap <= kPagedWholeRows && items <= paged_decode_ctas(l.tile_rows);
+    if (l.undivided) return l;
     const size_t workers = static_cast<size_t>(paged_decode_workers(l.tile_rows));
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -115,8 +120,8 @@ Layout layout(const PagedCache &c, int g, int max_new) {
         l.tile_o = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * kAttnHeadDim * sizeof(float));
         l.tile_ml = take(static_cast<size_t>(2) * kPagedTileCtas * 128 * sizeof(float2));
         l.tile_join = take(kPagedTileCtas * sizeof(PagedJoin));
-        // sequences with more than kPagedSmallRows rows are no more than these
-        const int slots = static_cast<int>(std::min<long long>(c.B, static_cast<long long>(c.N) * g / (kPagedSmallRows + 1)));
+        // sequences with more than `small` rows are no more than these
+        const int slots = static_cast<int>(std::min<long long>(c.B, static_cast<long long>(c.N) * g / (small + 1)));
         const int cap = (c.cap + 127) / 128 * 128;
         const size_t rows = static_cast<size_t>(slots) * c.Hkv * cap;
         const bool wide = c.int8 || c.page % 32 != 0 ? most >= kPagedWideRows : c.page % 64 != 0 && most >= kPagedWideRows32;
@@ -195,15 +200,15 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     const Layout l = layout(p.c, g, max_new);
     // the work lines' lengths, for whatever lengths and starts the device holds
     const long long cap = p.c.cap;
-    const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, kPagedSmallRows);
+    const int small = paged_small_rows(p.c.int8 != 0);
+    const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, small);
     const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
     if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1) >= kMostLine) return MHA_ERR_UNSUPPORTED;
     if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 8) >= kMostLine)
         return MHA_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < l.bytes) return MHA_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
+    if (l.bytes > 0 && (!workspace || workspace_bytes < l.bytes)) return MHA_ERR_WORKSPACE;
+    if (l.bytes > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.o_stride_h = out.stride_h;
     p.o_stride_t = out.stride_t;
@@ -211,10 +216,13 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     p.max_new = std::min(max_new, N);
     p.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
     p.mul = scale * 1.4426950408889634f;
-    p.small_rows = l.tiles ? std::max(kPagedSmallRows, 0) : 1 << 30;
-    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
-    p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
-    p.join = reinterpret_cast<PagedJoin *>(ws + l.join);
+    p.small_rows = l.tiles ? small : 1 << 30;
+    p.undivided = l.undivided ? 1 : 0;
+    if (!l.undivided) {
+        p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+        p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
+        p.join = reinterpret_cast<PagedJoin *>(ws + l.join);
+    }
     p.status = status_dev;
     PagedMaps maps;
     if (l.tiles) {
@@ -246,5 +254,6 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     if ((s = launched(launch_paged_decode(p, l.tiles, l.tile_rows, stream), "paged attention, few rows")) != MHA_OK) return s;
     if (l.slots > 0 && (s = launched(launch_paged_widen(p, w, stream), "paged attention, rows to bf16")) != MHA_OK) return s;
     if (l.tiles && (s = launched(launch_attn_paged(maps, t, stream), "paged attention, row tiles")) != MHA_OK) return s;
+    if (l.undivided) return MHA_OK;
     return launched(launch_paged_merge(p, l.tiles, l.tile_rows, stream), "paged attention, joining");
 }

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.tiles = p.plan[0];
     const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
     const int *cum = p.plan + at.cum;
-    sh.keys = place_of(cum, sh.tiles);
+    sh.keys = p.plan[2] + kTileCost * sh.tiles;
     const int total = p.c.Hkv * sh.keys;
     sh.share = (total + G - 1) / G;
     if (total == 0 || static_cast<long long>(cta) * sh.share >= total) {

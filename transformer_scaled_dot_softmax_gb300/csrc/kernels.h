@@ -300,9 +300,10 @@ struct PagedAttnParams {
     int causal;
     float mul;             // scale log2(e)
     // Sequences of at most small_rows stacked rows (g query heads of a K/V head
-    // x new tokens) are gone through by paged_decode.cu, the others by
-    // attn_paged_bf16.cu (small_rows is 2^30 where there can be none).
+    // x new tokens: paged_small_rows()) are gone through by paged_decode.cu, the others
+    // by attn_paged_bf16.cu (small_rows is 2^30 where there can be none).
     int small_rows;
+    int undivided;         // no item of paged_decode.cu is divided: nothing to join
     // paged_decode.cu: partial sums of key ranges that end inside an item
     float *part_o;         // (2 workers, rows of a tile, 64)
     float2 *part_ml;       // (2 workers, rows of a tile): reference in log2 units, sum
@@ -319,11 +320,20 @@ struct PagedAttnParams {
     const uint32_t *gone;
     int *status;
 };
-constexpr int kPagedSmallRows = 32;
+// Measured there / as row tiles, us (4 K/V heads of 32,768 keys; 16 sequences x 8 heads of
+// 2,048 to 4,096): bf16 16 rows 17, 29 / 19, 32, 24 rows 21, 40 / the same; int8 16 rows
+// 19, 28 / 23, 44, 32 rows 26, 40 / the same.
+inline constexpr int paged_small_rows(bool int8) { return int8 ? 32 : 16; }
+// Up to so many rows of a sequence, and as long as each CTA has one at most, items
+// are taken whole: one launch, no workspace.  Measured, whole / divided and joined,
+// us: 8 K/V heads of one sequence of 100 bf16 rows 5.2 / 12.3, 1,000 10.6 / 10.3; of 64
+// sequences of 500 11.8 / 17.5, 1,000 20.3 / 23.6.
+constexpr int kPagedWholeRows = 1024;
 constexpr int kPagedTileCtas = kSmsPerGpu;  // persistent CTAs of attn_paged_bf16.cu
-// Rows that a warp of paged_decode.cu takes at once, its workers (warps), for
-// calls whose sequences have up to `rows` stacked rows there.
+// Rows that a warp of paged_decode.cu takes at once, for calls whose sequences have up
+// to `rows` stacked rows there; its CTAs, and its warps, each of which may be a worker.
 int paged_decode_rows(int rows);
+int paged_decode_ctas(int tile_rows);
 int paged_decode_workers(int tile_rows);
 // The launch that goes through the small sequences and lists the others' row
 // tiles, and the one that joins both kernels' partial sums.
@@ -338,7 +348,8 @@ cudaError_t launch_attn_paged(const PagedMaps &maps, const PagedAttnParams &p, c
 mha_status encode_paged_maps(PagedMaps *m, const PagedAttnParams &p);
 
 // Lists in PagedAttnParams::plan, of at most `tiles` row tiles and B sequences.
-// plan[0]: the number of row tiles; [1]: of sequences that have some.
+// plan[0]: the number of row tiles; [1]: of sequences that have some; [2]: key tiles of
+// a K/V head.
 struct PagedPlan {
     int first;   // (B + 1) first row tile of each sequence
     int cum;     // (tiles + 1) key tiles of one K/V head before a row tile

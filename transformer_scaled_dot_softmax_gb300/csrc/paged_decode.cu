@@ -22,9 +22,10 @@
 // int8: K n and q are multiplied as fp16, K's whole numbers exactly, a query row
 // scaled by a power of two so that its largest element lies in [2^14, 2^15)
 // (elements below 2^-31 of it lose bits, 2^-39 of it at most); the keys' powers of
-// two and the row's meet the fp32 score.  V becomes bf16 with its power
-// of two, which is exact.  The whole numbers come out of their bytes by permutes:
-// 0x6400 | u is 1024 + u in fp16, 0x4B000000 | u is 2^23 + u in fp32, u = n + 128.
+// two and the row's meet the fp32 score.  V's whole numbers are bf16 numbers, and its
+// rows' powers of two meet the weights, without rounding.  The numbers come out of
+// their bytes by permutes: 0x6400 | u is 1024 + u in fp16, u = n + 128, and 0x4300 | u
+// is 128 + u in bf16 for the 7 low bits u.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -48,7 +49,7 @@ constexpr float kSumMax = 65536.0f;
 constexpr int kLeastShare = 4, kLeastTeamShare = 8;
 
 // CTAs of an SM, by the rows of an item in eights.
-constexpr int paged_decode_ctas(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
+constexpr int ctas_of_sm(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
 
 template <bool kInt8>
 constexpr int kUnitKeys = kInt8 ? 32 : 16;
@@ -90,6 +91,15 @@ __device__ __forceinline__ void to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<uint32_t *>(&y);
 }
 
+// Whole number e of a and of b, as the bf16 pair: byte n, twice in a half word, gives
+// 128 + its low 7 bits, and 128 or, if it is negative, 256 to take from that.
+__device__ __forceinline__ uint32_t to_bf16(uint32_t a, uint32_t b, int e) {
+    const uint32_t w = __byte_perm(a, b, 0x4400 + 0x1111 * e);
+    const uint32_t x = (w & 0x007f007fu) | 0x43004300u, y = (w & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
 // One lane's part of a unit's K, or of its V.
 struct Part {
     // K, bf16: keys l/4 and l/4 + 8, two pieces of 8 features; int8: keys l/4 + 8 i,
@@ -100,15 +110,17 @@ struct Part {
 };
 
 struct Shape {
-    int units, tiles, total;  // of a row tile; row tiles; of the sequence
+    int units, places;  // of an item: units, and places on the line (1 where items are not divided)
+    int tiles, total;   // row tiles, places of the sequence
 };
 template <bool kInt8, int kRows>
 __device__ __forceinline__ Shape shape_of(const PagedAttnParams &p, const PagedSeq &s, int g) {
     Shape r;
     const int rows = min(s.n, p.max_new) * g;
     r.units = max((s.len + kUnitKeys<kInt8> - 1) / kUnitKeys<kInt8>, 1);
+    r.places = p.undivided ? 1 : r.units;
     r.tiles = rows > p.small_rows ? 0 : (rows + kRows - 1) / kRows;
-    r.total = p.c.Hkv * r.tiles * r.units;
+    r.total = p.c.Hkv * r.tiles * r.places;
     return r;
 }
 
@@ -201,11 +213,12 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
     if (threadIdx.x == 0) {
         cum[tiles] = keys;
         p.plan[0] = tiles;
+        p.plan[2] = keys;
     }
 }
 
 template <bool kInt8, int kN>
-__global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_kernel(const PagedAttnParams p, int list) {
+__global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(const PagedAttnParams p, int list) {
     constexpr int kRows = 8 * kN, kKeys = kUnitKeys<kInt8>, kBlocks = kKeys / 16;
     __shared__ int warp_sums[kWarps], at_b[kWarps], at_start[kWarps];
     __shared__ float4 sh_o[kWarps][kRows][HD / 4];
@@ -236,8 +249,10 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
     // A CTA's warps are workers of their own, or, where items would be divided among
     // more than two of those, one together.
     const int alone = (total + ctas * kWarps - 1) / (ctas * kWarps);
-    const bool team = total >= 2ll * alone * items;
-    const int share = team ? max((total + ctas - 1) / ctas, kLeastTeamShare) : max(alone, kLeastShare);
+    const bool team = p.undivided || total >= 2ll * alone * items;
+    const int share = p.undivided ? (total + ctas - 1) / ctas
+                      : team      ? max((total + ctas - 1) / ctas, kLeastTeamShare)
+                                  : max(alone, kLeastShare);
     const int me = team ? blockIdx.x : blockIdx.x * kWarps + warp;
     int base = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
@@ -256,25 +271,26 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         base += sum;
     }
     // (a record for every warp, whether it is a worker or not)
-    if (team && warp > 0 && lane == 0) p.join[ctas + blockIdx.x * (kWarps - 1) + warp - 1] = PagedJoin{};
+    if (!p.undivided && team && warp > 0 && lane == 0) p.join[ctas + blockIdx.x * (kWarps - 1) + warp - 1] = PagedJoin{};
     const int sub = team ? warp : 0, step = team ? kWarps : 1;
     __syncthreads();
     int b = at_b[warp];
     if (b < 0) {
-        if (lane == 0 && sub == 0) p.join[me] = PagedJoin{};
+        if (!p.undivided && lane == 0 && sub == 0) p.join[me] = PagedJoin{};
         return;
     }
     const int start = me * share;
     int left = min(share, total - start), rel = start - at_start[warp];
     bool first_piece = true;
 
-    while (left > 0) {
+    while (left > 0 && b < p.c.B) {
         const PagedSeq s = paged_seq(p.c, b);
         const Shape sh = shape_of<kInt8, kRows>(p, s, g);
-        const int item = rel / sh.units, u0 = rel - item * sh.units, u1 = min(sh.units, u0 + left);
+        const int item = rel / sh.places, at0 = rel - item * sh.places, at1 = min(sh.places, at0 + left);
+        const int u0 = at0, u1 = p.undivided ? sh.units : at1;
         const int head = item / sh.tiles, tile = item - head * sh.tiles;
         const int rows = min(s.n, p.max_new) * g - tile * kRows;  // of this item, if less than kRows
-        if (first_piece && lane == 0 && sub == 0) {
+        if (!p.undivided && first_piece && lane == 0 && sub == 0) {
             PagedJoin j{};
             if (u0 > 0)
                 j = PagedJoin{min(rows, kRows), tile * kRows, head, s.row0, (start - u0) / share, (start - u0 + sh.units - 1) / share};
@@ -409,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         };
 
         float o[kN][4][4], m[kN][2], l[kN][2];
+        bool set = false;  // every row has a reference
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
 #pragma unroll
@@ -482,15 +499,16 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                 place(u + step);
                 load(std::false_type{}, kp);
             }
-            // Weights against the reference in hand.  `shift`: -reference, 0 before
-            // there is one.
+            // Weights against the reference in hand, 0 before there is one.  Masked:
+            // of scores in log2 units.
             uint32_t pk[kN][kBlocks][2];
             float sum[kN][2];
-            auto weights = [&](bool masked) -> bool {
-                bool need = false;
+            auto weights = [&](auto is_masked, bool has_ref) -> bool {
+                constexpr bool masked = decltype(is_masked)::value;
+                bool need = !has_ref;
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
-                    const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+                    const float r0 = masked && m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = masked && m[n][1] == -INFINITY ? 0.f : m[n][1];
                     sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i)
@@ -501,11 +519,11 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                             pk[n][i][j] = pack_bf16x2(ex2_approx(y0), ex2_approx(y1));
                             add_bf16x2_to_f32(sum[n][0], sum[n][1], pk[n][i][j]);
                         }
-                    need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax) || m[n][0] == -INFINITY || m[n][1] == -INFINITY;
+                    need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax);
                 }
                 return __any_sync(0xffffffffu, need);
             };
-            if (!whole || weights(false)) {
+            if (!whole || !set || weights(std::false_type{}, true)) {
                 // Scores in log2 units, a key that is not seen at minus infinity;
                 // where a row has no reference yet, or its sum leaves the
                 // range, against the unit's maximum.
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                             const int in = l4 + 8 * (e >> 1), key = u * kKeys + 16 * i + in;
                             st[n][i][e] = in < here[i] && key < lim[n][e & 1] ? st[n][i][e] * mul[n][e & 1] : -INFINITY;
                         }
-                if (weights(true)) {
+                if (weights(std::true_type{}, set)) {
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -540,7 +558,11 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                             }
                             m[n][r] = top;
                         }
-                    weights(true);
+                    weights(std::true_type{}, true);
+                    bool all = true;
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) all = all && m[n][0] != -INFINITY && m[n][1] != -INFINITY;
+                    set = __all_sync(0xffffffffu, all);
                 }
             }
 #pragma unroll
@@ -556,20 +578,9 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint4 &w = vp.x[2 * i + j];
-                        const float s0 = paged_power(__shfl_sync(0xffffffffu, vp.s, 16 * i + 8 * j + 2 * c));
-                        const float s1 = paged_power(__shfl_sync(0xffffffffu, vp.s, 16 * i + 8 * j + 2 * c + 1));
-                        const uint64_t s2 = f32x2_pack(s0, s1), off = f32x2_pack(-8388736.f * s0, -8388736.f * s1);
-                        const uint32_t a[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u}, d[2] = {w.z ^ 0x80808080u, w.w ^ 0x80808080u};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t sel = 0x7440u + (e & 3);
-                            float y0, y1;
-                            f32x2_unpack(fma_f32x2(f32x2_pack(__uint_as_float(__byte_perm(a[e >> 2], 0x4B000000u, sel)),
-                                                              __uint_as_float(__byte_perm(d[e >> 2], 0x4B000000u, sel))),
-                                                   s2, off),
-                                         y0, y1);
-                            va[e >> 1][2 * j + (e & 1)] = pack_bf16x2(y0, y1);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            va[e >> 1][2 * j + (e & 1)] = to_bf16(e < 4 ? w.x : w.y, e < 4 ? w.z : w.w, e & 3);
                     }
                 } else {
                     const uint32_t w[4][4] = {{vp.x[0].x, vp.x[0].y, vp.x[0].z, vp.x[0].w}, {vp.x[1].x, vp.x[1].y, vp.x[1].z, vp.x[1].w},
@@ -582,8 +593,22 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
                         va[f][3] = __byte_perm(w[2][f], w[3][f], 0x7632);
                     }
                 }
+                // (exact; as bf16 a power's bits are its stored exponent, 7 bits up)
+                uint32_t power[2] = {0u, 0u};
+                if constexpr (kInt8) {
+                    power[0] = __shfl_sync(0xffffffffu, vp.s, 16 * i + l4) * 0x00800080u;
+                    power[1] = __shfl_sync(0xffffffffu, vp.s, 16 * i + 8 + l4) * 0x00800080u;
+                }
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
+                    if constexpr (kInt8) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const __nv_bfloat162 w = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[n][i][j]),
+                                                             *reinterpret_cast<const __nv_bfloat162 *>(&power[j]));
+                            pk[n][i][j] = *reinterpret_cast<const uint32_t *>(&w);
+                        }
+                    }
                     const uint32_t b0 = transpose8(pk[n][i][0]), b1 = transpose8(pk[n][i][1]);
 #pragma unroll
                     for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
@@ -643,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
         }
         meet();
 
-        left -= u1 - u0;
-        rel += u1 - u0;
+        left -= at1 - at0;
+        rel += at1 - at0;
         first_piece = false;
         if (rel == sh.total) {
             rel = 0;
@@ -658,20 +683,21 @@ __global__ void __launch_bounds__(kThreads, paged_decode_ctas(kN)) paged_decode_
 //   o = (sum_s w_s O_s) / (sum_s w_s l_s),  w_s = 2^(m_s - M),  M = max_s m_s
 // over the pieces of an item: the tail slot of its first worker, then the head slots
 // up to its last one, in that order whatever the timing.
-// 16 lanes take one row (4 features each), up to 8 pieces at a time; groups that
+// 16 lanes take one row (4 features each), up to kBatch pieces at a time; groups that
 // would be idle share a row's pieces.  A piece without a visible key has m = -inf,
 // l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is taken as
 // paged_level gives it.
 //
-// Bound by latency: small blocks, so that all of them are resident together, one for
-// every worker and several for every CTA with row tiles; most find nothing to join.
+// Bound by latency: small blocks, most of which find nothing to join.  Behind row
+// tiles, whose blocks come on top, one looks at four workers' records, and takes fewer
+// pieces at a time to be resident with the others (10 us -> 7).
 constexpr int kTileBlocks = 8;  // for a worker of attn_paged_bf16.cu
 constexpr int kGroups = kMergeThreads / 16;
-constexpr int kBatch = 8;
 
 __device__ __forceinline__ float piece_weight(float m, float top) { return m == -INFINITY ? 0.f : ex2_approx(m - top); }
 
 // A partial sum, and others joined to it.
+template <int kBatch>
 struct Sum {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -696,34 +722,21 @@ struct Sum {
     }
 };
 
-__global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const PagedAttnParams p, int workers, int tile_rows) {
-    __shared__ float4 sh_o[kGroups][16];
-    __shared__ float2 sh_ml[kGroups];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int x = blockIdx.x;
-    const bool small = x < workers;
-    const int w = small ? x : (x - workers) / kTileBlocks;
-    const PagedJoin j = small ? p.join[w] : p.tile_join[w];
-    if (j.rows == 0) return;
-    // the rows are divided among the blocks of all workers that began inside the item
-    const int blocks = (j.last - j.first) * (small ? 1 : kTileBlocks);
-    const int block = (w - 1 - j.first) * (small ? 1 : kTileBlocks) + (small ? 0 : (x - workers) % kTileBlocks);
-    const int from = j.rows * block / blocks, rows = j.rows * (block + 1) / blocks - from;
-    if (rows == 0) return;
+template <int kBatch>
+__device__ __forceinline__ void join_rows(const PagedAttnParams &p, const PagedJoin &j, bool small, int slot_rows, int from, int rows,
+                                          float4 (&sh_o)[kGroups][16], float2 (&sh_ml)[kGroups]) {
     const int g = p.H / p.c.Hkv;
     const int grp = threadIdx.x / 16, lane = threadIdx.x & 15;
-    const int slot_rows = small ? tile_rows : 128;
     const float *part_o = small ? p.part_o : p.tile_o;
     const float2 *part_ml = small ? p.part_ml : p.tile_ml;
     const int pieces = j.last - j.first + 1;
     int per = 1;  // groups of a row
-    while (per * 2 * rows <= kGroups) per *= 2;
+    while (per < kGroups && per * 2 * rows <= kGroups) per *= 2;
     for (int r0 = 0; r0 < rows; r0 += kGroups / per) {
         const int row = r0 + grp / per, part = grp % per;
         float2 ml[kBatch];
         float4 o[kBatch];
-        Sum sum;
+        Sum<kBatch> sum;
         if (row < rows) {
             for (int i0 = part; i0 < pieces; i0 += kBatch * per) {
 #pragma unroll
@@ -746,14 +759,15 @@ __global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const Pag
             if (lane == 0) sh_ml[grp] = make_float2(sum.m, sum.l);
             __syncthreads();
             if (part == 0) {
-                static_assert(kGroups <= kBatch, "a row's groups are joined at once");
+                sum = Sum<kBatch>();
+                for (int i0 = 0; i0 < per; i0 += kBatch) {
 #pragma unroll
-                for (int e = 0; e < kBatch; ++e) {
-                    ml[e] = e < per ? sh_ml[grp + e] : make_float2(-INFINITY, 0.f);
-                    o[e] = e < per ? sh_o[grp + e][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int e = 0; e < kBatch; ++e) {
+                        ml[e] = i0 + e < per ? sh_ml[grp + i0 + e] : make_float2(-INFINITY, 0.f);
+                        o[e] = i0 + e < per ? sh_o[grp + i0 + e][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    sum.add(ml, o);
                 }
-                sum = Sum();
-                sum.add(ml, o);
             }
         }
         if (part == 0 && row < rows) {
@@ -766,19 +780,51 @@ __global__ void __launch_bounds__(kMergeThreads, 5) paged_merge_kernel(const Pag
     }
 }
 
+// Blocks 0 .. workers / kRecords - 1 look at kRecords of the warps' records each, far
+// apart; the others, kTileBlocks for each of attn_paged_bf16.cu's CTAs, at that CTA's.
+// The rows of an item are divided among the blocks of all workers that began inside.
+template <int kBatch, int kRecords>
+__global__ void __launch_bounds__(kMergeThreads, kBatch == 8 ? 5 : 8) paged_merge_kernel(const PagedAttnParams p, int workers,
+                                                                                         int tile_rows) {
+    __shared__ float4 sh_o[kGroups][16];
+    __shared__ float2 sh_ml[kGroups];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int own = workers / kRecords, x = blockIdx.x;
+    auto join = [&](const PagedJoin &j, bool small, int w, int per, int block) {
+        if (j.rows == 0) return;
+        const int blocks = (j.last - j.first) * per, at = (w - 1 - j.first) * per + block;
+        const int from = j.rows * at / blocks, rows = j.rows * (at + 1) / blocks - from;
+        if (rows > 0) join_rows<kBatch>(p, j, small, small ? tile_rows : 128, from, rows, sh_o, sh_ml);
+    };
+    if (x >= own) {
+        const int w = (x - own) / kTileBlocks;
+        join(p.tile_join[w], false, w, kTileBlocks, (x - own) % kTileBlocks);
+    } else if (kRecords == 1) {
+        join(p.join[x], true, x, 1, 0);
+    } else {
+        __shared__ PagedJoin sh_j[kRecords];
+        if (threadIdx.x < kRecords) sh_j[threadIdx.x] = p.join[x + threadIdx.x * own];
+        __syncthreads();
+        for (int i = 0; i < kRecords; ++i) join(sh_j[i], true, x + i * own, 1, 0);
+    }
+}
+
 template <bool kInt8>
 cudaError_t launch_rows(const PagedAttnParams &p, int list, int tile_rows, cudaStream_t stream) {
-    const dim3 grid(paged_decode_workers(tile_rows) / kWarps + list), block(kThreads);
+    const dim3 grid(paged_decode_ctas(tile_rows) + list), block(kThreads);
     if (tile_rows == 8) return launch_kernel(paged_decode_kernel<kInt8, 1>, grid, block, 0, stream, true, 1, p, list);
-    if (tile_rows == 16) return launch_kernel(paged_decode_kernel<kInt8, 2>, grid, block, 0, stream, true, 1, p, list);
-    return launch_kernel(paged_decode_kernel<kInt8, 4>, grid, block, 0, stream, true, 1, p, list);
+    if constexpr (kInt8)  // (paged_small_rows())
+        if (tile_rows == 32) return launch_kernel(paged_decode_kernel<true, 4>, grid, block, 0, stream, true, 1, p, list);
+    return launch_kernel(paged_decode_kernel<kInt8, 2>, grid, block, 0, stream, true, 1, p, list);
 }
 
 }  // namespace
 
 int paged_decode_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
-int paged_decode_workers(int tile_rows) { return kSmsPerGpu * paged_decode_ctas(tile_rows / 8) * kWarps; }
+int paged_decode_ctas(int tile_rows) { return kSmsPerGpu * ctas_of_sm(tile_rows / 8); }
+int paged_decode_workers(int tile_rows) { return paged_decode_ctas(tile_rows) * kWarps; }
 
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
     return p.c.int8 ? launch_rows<true>(p, tiles ? 1 : 0, tile_rows, stream) : launch_rows<false>(p, tiles ? 1 : 0, tile_rows, stream);
@@ -786,8 +832,10 @@ cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_r
 
 cudaError_t launch_paged_merge(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream) {
     const int workers = paged_decode_workers(tile_rows);
-    const unsigned grid = workers + (tiles ? kPagedTileCtas * kTileBlocks : 0);
-    return launch_kernel(paged_merge_kernel, dim3(grid), dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
+    if (!tiles)
+        return launch_kernel(paged_merge_kernel<8, 1>, dim3(workers), dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
+    const dim3 grid(workers / 4 + kPagedTileCtas * kTileBlocks);
+    return launch_kernel(paged_merge_kernel<4, 4>, grid, dim3(kMergeThreads), 0, stream, true, 1, p, workers, tile_rows);
 }
 
 }  // namespace mha
