@@ -63,12 +63,20 @@ mha_status encode_tiled(CUtensorMap *m, const void *base, bool bytes, int rank, 
         es[i] = 1;
         if (i + 1 < rank) s[i] = strides_bytes[i];
     }
-    CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, bx, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto encode = [&]() {
+        return fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    int device;
+    // A host thread whose first call of CUDA this is has no context yet; the
+    // runtime makes its device's current.
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess &&
+        cudaSetDevice(device) == cudaSuccess)
+        r = encode();
     if (r != CUDA_SUCCESS) {
         char buf[96];
         snprintf(buf, sizeof(buf), "CUresult %d (rank %d, dims %llu x %llu x %llu)", (int)r, rank,
