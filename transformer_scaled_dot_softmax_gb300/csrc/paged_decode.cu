@@ -348,37 +348,42 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
         }
         least = __reduce_min_sync(0xffffffffu, least);
 
-        // The pages of the warp's next 32 blocks of 16 keys, those of units window0,
-        // window0 + step, ..., a lane each.
-        int window0 = 0, page = -1, in_page = 0;
+        // Where the warp's next 32 blocks of 16 keys lie, those of units window0,
+        // window0 + step, ..., a lane each: offsets of the rows and of their exponents,
+        // how many of the 16 are there; and a bit for each block with all of them.
+        int window0 = 0, my_valid = 0;
+        unsigned all_there = 0;
+        long long my_at = 0, my_scales = 0;
         auto look_up = [&](int u) {
             window0 = u;
             const int block = (u + lane / kBlocks * step) * kBlocks + lane % kBlocks, i = block / per_page;
-            in_page = (block - i * per_page) * 16;
-            page = block * 16 < s.len ? paged_page(p.c, b, i) : -1;
+            const int row = head * p.c.page + (block - i * per_page) * 16;
+            const int pg = block * 16 < s.len ? paged_page(p.c, b, i) : -1;
+            my_valid = pg >= 0 ? min(s.len - block * 16, 16) : 0;
+            my_at = pg * p.c.stride + row * HD;
+            if (kInt8) my_scales = static_cast<long long>(pg) * (p.c.Hkv * p.c.page) + row;
+            all_there = __ballot_sync(0xffffffffu, my_valid == 16);
         };
         look_up(u0 + sub);
-        // Where the unit's blocks of 16 keys lie, how many of their keys are there;
-        // the exponent of the lane's key.
+        // The same for a unit's blocks; the exponent of its key `lane`.
         long long at[kBlocks], s_at = 0;
-        int valid[kBlocks], s_valid = 0;
-        bool full = false;  // all of them
+        int valid[kBlocks], s_valid = 16;
+        bool full = false;  // all its keys are there
         auto place = [&](int u) {
             if (u - window0 >= 32 / kBlocks * step) look_up(u);
             const int from = (team ? (u - window0) / kWarps : u - window0) * kBlocks;
-            full = (u + 1) * kKeys <= s.len;
+            constexpr unsigned kAll = (1u << kBlocks) - 1u;
+            full = (all_there >> from & kAll) == kAll;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
-                const int pg = __shfl_sync(0xffffffffu, page, from + i);
-                const int in = __shfl_sync(0xffffffffu, in_page, from + i);
-                const int row = head * p.c.page + in;
-                at[i] = pg * p.c.stride + row * HD;
-                valid[i] = pg >= 0 ? s.len - (u * kBlocks + i) * 16 : 0;
-                full = full && pg >= 0;
-                if (kInt8 && lane >> 4 == i) {
-                    s_at = static_cast<long long>(pg) * (p.c.Hkv * p.c.page) + row + (lane & 15);
-                    s_valid = valid[i];
-                }
+                at[i] = __shfl_sync(0xffffffffu, my_at, from + i);
+                valid[i] = 16;
+            }
+            if (kInt8) s_at = __shfl_sync(0xffffffffu, my_scales, from + (lane >> 4)) + (lane & 15);
+            if (!full) {
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) valid[i] = __shfl_sync(0xffffffffu, my_valid, from + i);
+                if (kInt8) s_valid = __shfl_sync(0xffffffffu, my_valid, from + (lane >> 4));
             }
         };
         // K or V of the unit that place() has found
