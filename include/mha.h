@@ -491,13 +491,13 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
  *   in flight.  Few query rows of short sequences (max_pages page_rows <= 1024) take
  *   one launch and 0 bytes; NULL is allowed then.
- * Two launches (sequences with up to 16 query rows per K/V head, 32 with int8; joining of the
- * partial sums of divided key ranges), a third between them when max_new allows
- * more: tcgen05 products over tiles of 128 rows; and when it allows 512 and the cache
- * is int8, or has pages that are not a multiple of 64 rows, one that lays these
- * sequences' rows out as bf16 first, in up to 4 GiB of the workspace (where that would
- * take more it is left out).  A call's results do not depend on timing (equal calls
- * give equal bits).
+ * Two launches (sequences with up to 16 query rows per K/V head, 32 with int8;
+ * joining of the partial sums of divided key ranges), a third between them when
+ * max_new allows more: tcgen05 products over tiles of 128 rows.  When it allows 512
+ * rows and the cache is int8 or its pages are no multiple of 32 rows, or 4,096 and
+ * they are no multiple of 64, one more lays these sequences' cached rows out as bf16
+ * first, in up to 4 GiB of the workspace (where that would take more it is left out).
+ * A call's results do not depend on timing (equal calls give equal bits).
  */
 /* From the sizes in `cache` (its pointers may be NULL); 0 for sizes that are not valid. */
 size_t sdpa_paged_workspace_bytes(const mha_paged_cache *cache, int h, int N, int max_new);

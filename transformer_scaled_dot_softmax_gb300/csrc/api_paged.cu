@@ -18,7 +18,8 @@ using namespace mha;
 
 constexpr int kMostPageRows = 1 << 16;
 constexpr long long kMostRows = 1ll << 30;  // of a sequence
-constexpr long long kMostLine = 1ll << 31;  // units of the kernels' work lines
+// Units of the kernels' work lines: 32 bits, with room to round up to equal shares.
+constexpr long long kMostLine = (1ll << 31) - (1 << 14);
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -15,16 +15,28 @@
 // that is not there, and rows of pages past the length, are boxes past the
 // tensor's end, which arrive as zeros, and their keys are not seen.
 //
-// The pipeline (one CTA an SM, TMA rings, S issuer, two PV issuers, two softmax
+// The pipeline (one CTA an SM, a TMA ring, S issuer, two PV issuers, two softmax
 // groups on alternate tiles, output warps, three score buffers in tensor memory)
 // and the online softmax with its window of [2^-64, 2^64] around a row's reference
 // are attn_scored_bf16.cuh's, without cap and bias.
+//
+// Bound, like that kernel, by the softmax warps' instruction stream (issue 60 %, tensor
+// 42 %, special functions 41 % of their cycles).  Measured, causal, 2 x 16 heads x 8,192
+// in 64-row pages: 277 us (990 TFLOP/s) from cold memory, the whole call 282; 1,024
+// tokens x 16 heads, 4 to a K/V head, behind 31,744 rows 130 (1,040 TFLOP/s).
 //
 // int8 pages arrive in a ring of their own, 64 bytes a row, with the rows'
 // exponents; the output warps, which are idle while a row tile is worked on, write
 // them as bf16 into the K/V ring, in the 128-byte swizzle that TMA leaves
 // (n 2^e is exact).  Between two tiles they look for a finished row tile
-// first, since the products behind it wait for its accumulators.
+// first, since the products behind it wait for its accumulators.  A key tile takes 1.27
+// us so, 0.57 without, in every row tile that reads it: from
+// kPagedWideRows query rows on the rows are laid out as bf16 before instead.
+//
+// Tried and dropped: stages of their own for K, free earlier, V loaded by an output
+// warp, boxes issued by single threads (prompts 318 to 650 us against 285 to 291): each
+// adds instructions a tile to a warp that gets few to issue beside the softmax, and to
+// code that already fills the instruction cache.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -137,7 +149,7 @@ __device__ __forceinline__ uint32_t *raw_bad(Smem<kInt8> &sm, int i) {
 // Where a CTA's share of the line lies.  A row tile takes kTileCost places on it
 // before those of its key tiles: what a piece costs besides them, in key tiles.
 // (Causal, 2 x 16 x 8,192: CTAs with the short row tiles of a head have 29 of them,
-// others 7; counted by key tiles alone the former took 305 us, the latter 280.)
+// others 7.  0 places 301 us, 1 294, 2 287, 3 286, 4 288.)
 constexpr int kTileCost = 3;
 struct Share {
     int tiles, keys;        // row tiles, places of one K/V head
@@ -759,11 +771,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         // int8: pieces are put out as their products are complete, K and V of tile
-        // after tile written as stages come free.  Behind a piece's last tile it may be a stage that only products after
-        // that piece's output give back: whichever comes first.  (One place in the
-        // code for each: all roles' loops together have to stay in the instruction
-        // cache, 32 KB or so; with three copies of output() here a causal prompt took
-        // 392 us instead of 290.)
+        // after tile written as stages come free.  Behind a piece's last tile it may
+        // be a stage that only products after that piece's output give back:
+        // whichever comes first.  (One place in the code for each: all roles' loops
+        // together have to stay in the instruction cache, 32 KB or so; with three
+        // copies of output() here a causal prompt took 392 us instead of 290.)
         auto put_first = [&](int v, uint64_t *bar, uint32_t parity, bool &ok) -> bool {
             const long long since = clock64();
             while (true) {

@@ -4,11 +4,15 @@
 // A K/V head's query rows are stacked: x = t g + i for token t and the i-th of
 // its g query heads.  An item is up to kRows of them against all cached rows of
 // the sequence, in units of 16 keys (bf16) or 32 (int8): 4 KB of K and V.  All
-// units of the batch stand in one line; every warp takes an equal share of it,
+// units of the batch stand in one line; every worker takes an equal share of it,
 // whatever the lengths, keeps the online softmax of the item it is in (reference
 // m in log2 units, sum l, unnormalised O) and leaves it behind where the item ends
 // inside the share: whole items are written out, pieces as partial sums that
-// paged_merge_kernel joins, in a fixed order.
+// paged_merge_kernel joins, in a fixed order.  A worker is a warp, or, where items
+// would be divided among more than two of those, the four warps of a CTA, which take
+// every fourth unit and meet in shared memory (8 to 16 rows of 4 K/V heads behind
+// 32,768 keys: about 600 pieces an item to join, 59 to 104 us, against 15 to 18).  Short
+// sequences' items are taken whole, without anything to join (kPagedWholeRows).
 //
 // The products run on mma.sync with the keys as rows: S^T = K Q^T and
 // O^T = V^T P^T, m16n8k16, because the work is bound by memory and a tile of 8
@@ -16,8 +20,8 @@
 // memory straight into the fragments: the order of the 64 features in a dot product
 // is free, so that a lane's fragments of a K row are 16 consecutive bytes, four lanes a
 // row; for V^T a lane holds 8 consecutive features of the four keys its fragments
-// need, and pairs of keys are merged by byte permutes.  A unit is loaded while the
-// one before it is worked on.
+// need, and pairs of keys are merged by byte permutes.  A unit's K is on its way while
+// the weights of the one before it are taken, its V while its scores are.
 //
 // int8: K n and q are multiplied as fp16, K's whole numbers exactly, a query row
 // scaled by a power of two so that its largest element lies in [2^14, 2^15)
@@ -26,6 +30,14 @@
 // rows' powers of two meet the weights, without rounding.  The numbers come out of
 // their bytes by permutes: 0x6400 | u is 1024 + u in fp16, u = n + 128, and 0x4300 | u
 // is 128 + u in bf16 for the 7 low bits u.
+//
+// Measured, single tokens, whole calls: 16 sequences of up to 8,192 bf16 rows x 16
+// heads 68 us (403 MB, 5.9 TB/s; of up to 32,768 rows 241, the time of a copy of as many
+// bytes); 64 sequences of up to 8,192 int8 rows x 2 heads, 8 query heads each, 33 us
+// (102 MB, 3.1 TB/s; of up to 32,768 rows 91, 4.5 TB/s).  bf16 is bound by DRAM, but for
+// 7 us of launches and joining; int8 by the latency of a unit's chain and by the ALU
+// pipe, which takes about 290 of a unit's 570 instructions, most of them the conversion.
+// A second unit in flight would not leave the registers for four CTAs an SM.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
