@@ -309,57 +309,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
             p.join[me] = j;
         }
 
-        // Queries: a lane's features of row l/4, in every 8 rows.
-        uint32_t q[kN][8];
-        float mul[kN][2];  // of the scores of rows 2c, 2c + 1
-        int lim[kN][2];    // keys below it are seen
-        int least = s.len;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const int x = tile * kRows + 8 * n + l4;
-            uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a;
-            if (8 * n + l4 < rows) {
-                const int t = x / g;
-                const __nv_bfloat16 *src = p.q.x + (head * g + x - t * g) * p.q.stride_h + (s.row0 + t) * p.q.stride_t;
-                a = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c : 8 * c));
-                d = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c + 8 : 8 * c + 32));
-            }
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
-            float f = p.mul;
-            if (kInt8) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^k, the largest element's (at least the least normal number's)
-                const int k = max(static_cast<int>(top >> 7), 1) - 127;
-                const float up0 = __uint_as_float((127 - k / 2) << 23), up1 = __uint_as_float((127 + 14 - (k - k / 2)) << 23);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * up0 * up1,
-                                                        __uint_as_float(w[i] & 0xffff0000u) * up0 * up1);
-                    q[n][i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                f *= __uint_as_float((127 + k / 2) << 23) * __uint_as_float((127 - 14 + (k - k / 2)) << 23);
-                if (top >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: NaN
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q[n][i] = w[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 8 * n + 2 * c + i;
-                mul[n][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
-                lim[n][i] = 0x7fffffff;
-                if (r < rows) {
-                    lim[n][i] = p.causal ? min(s.len, max(s.len - s.n + (tile * kRows + r) / g + 1, 0)) : s.len;
-                    least = min(least, lim[n][i]);
-                }
-            }
-        }
-        least = __reduce_min_sync(0xffffffffu, least);
-
         // Where the warp's next 32 blocks of 16 keys lie, those of units window0,
         // window0 + step, ..., a lane each: offsets of the rows and of their exponents,
         // how many of the 16 are there; and a bit for each block with all of them.
@@ -460,6 +409,57 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
             load(std::false_type{}, kp);
             load(std::true_type{}, vp);
         }
+        // Queries: a lane's features of row l/4, in every 8 rows.
+        uint32_t q[kN][8];
+        float mul[kN][2];  // of the scores of rows 2c, 2c + 1
+        int lim[kN][2];    // keys below it are seen
+        int least = s.len;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int x = tile * kRows + 8 * n + l4;
+            uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a;
+            if (8 * n + l4 < rows) {
+                const int t = x / g;
+                const __nv_bfloat16 *src = p.q.x + (head * g + x - t * g) * p.q.stride_h + (s.row0 + t) * p.q.stride_t;
+                a = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c : 8 * c));
+                d = *reinterpret_cast<const uint4 *>(src + (kInt8 ? 16 * c + 8 : 8 * c + 32));
+            }
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+            float f = p.mul;
+            if (kInt8) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^k, the largest element's (at least the least normal number's)
+                const int k = max(static_cast<int>(top >> 7), 1) - 127;
+                const float up0 = __uint_as_float((127 - k / 2) << 23), up1 = __uint_as_float((127 + 14 - (k - k / 2)) << 23);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * up0 * up1,
+                                                        __uint_as_float(w[i] & 0xffff0000u) * up0 * up1);
+                    q[n][i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                f *= __uint_as_float((127 + k / 2) << 23) * __uint_as_float((127 - 14 + (k - k / 2)) << 23);
+                if (top >= 0x7f80u) f = __uint_as_float(0x7fc00000u);  // an infinity or NaN in the row: NaN
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[n][i] = w[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * n + 2 * c + i;
+                mul[n][i] = __shfl_sync(0xffffffffu, f, (2 * c + i) * 4);
+                lim[n][i] = 0x7fffffff;
+                if (r < rows) {
+                    lim[n][i] = p.causal ? min(s.len, max(s.len - s.n + (tile * kRows + r) / g + 1, 0)) : s.len;
+                    least = min(least, lim[n][i]);
+                }
+            }
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+
 #pragma unroll 1
         for (int u = u0 + sub; u < u1; u += step) {
             // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
