@@ -204,7 +204,7 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     const int small = paged_small_rows(p.c.int8 != 0);
     const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, small);
     const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
-    if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1) >= kMostLine) return MHA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1 + kPagedItemPlaces) >= kMostLine) return MHA_ERR_UNSUPPORTED;
     if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 8) >= kMostLine)
         return MHA_ERR_UNSUPPORTED;
     if (l.bytes > 0 && (!workspace || workspace_bytes < l.bytes)) return MHA_ERR_WORKSPACE;

@@ -335,6 +335,8 @@ constexpr int kPagedTileCtas = kSmsPerGpu;  // persistent CTAs of attn_paged_bf1
 int paged_decode_rows(int rows);
 int paged_decode_ctas(int tile_rows);
 int paged_decode_workers(int tile_rows);
+// Places on its work line that an item takes besides its units, at most.
+constexpr int kPagedItemPlaces = 16;
 // The launch that goes through the small sequences and lists the others' row
 // tiles, and the one that joins both kernels' partial sums.
 cudaError_t launch_paged_decode(const PagedAttnParams &p, bool tiles, int tile_rows, cudaStream_t stream);

@@ -28,16 +28,18 @@
 // (elements below 2^-31 of it lose bits, 2^-39 of it at most); the keys' powers of
 // two and the row's meet the fp32 score.  V's whole numbers are bf16 numbers, and its
 // rows' powers of two meet the weights, without rounding.  The numbers come out of
-// their bytes by permutes: 0x6400 | u is 1024 + u in fp16, u = n + 128, and 0x4300 | u
-// is 128 + u in bf16 for the 7 low bits u.
+// their bytes by permutes: 0x6400 | u is 1024 + u in fp16, u = n + 128, and u alone
+// u 2^-133 in bf16.
 //
 // Measured, single tokens, whole calls: 16 sequences of up to 8,192 bf16 rows x 16
-// heads 68 us (403 MB, 5.9 TB/s; of up to 32,768 rows 241, the time of a copy of as many
-// bytes); 64 sequences of up to 8,192 int8 rows x 2 heads, 8 query heads each, 33 us
-// (102 MB, 3.1 TB/s; of up to 32,768 rows 91, 4.5 TB/s).  bf16 is bound by DRAM, but for
-// 7 us of launches and joining; int8 by the latency of a unit's chain and by the ALU
-// pipe, which takes about 290 of a unit's 570 instructions, most of them the conversion.
-// A second unit in flight would not leave the registers for four CTAs an SM.
+// heads 65.5 us (403 MB, 6.2 TB/s; of up to 32,768 rows 232, 6.9 TB/s); 64 sequences of
+// up to 8,192 int8 rows x 2 heads, 8 query heads each, 29 us (102 MB, 3.5 TB/s; of up to
+// 32,768 rows 84, 4.9 TB/s).  bf16 is bound by DRAM, but for 7 us of launches and
+// joining.  int8 is bound by the ALU pipe: 32 of a lane's 290 instructions a unit there
+// less (V's numbers by 2 and a multiply-add instead of 3 and a subtraction) took 33.2 to
+// 30.9 us, where 40 less on other pipes (first products without cleared accumulators,
+// powers before their shuffles, pairs of scores at a time) and K or V asked for earlier
+// gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,6 +67,19 @@ constexpr int ctas_of_sm(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
 
 template <bool kInt8>
 constexpr int kUnitKeys = kInt8 ? 32 : 16;
+// bf16: units behind a piece's first one that are asked for with it (16 sequences of up
+// to 32,768 rows 240 us without, 236 with 2 of them; 128 of up to 2,048 133, 129).
+// int8 units take longer to work on than to come, and these instructions as well: 31.3
+// us without, 32.9 with them for 64 sequences of up to 8,192.
+constexpr int kAhead = 2;
+// Places on the line that an item takes before those of its units, for what beginning
+// one costs a worker: a CTA's four warps together, or a warp.  Without / with them, us:
+// 64 sequences of up to 8,192 int8 rows x 2 heads 30.8 / 29.4, 32 of up to 4,096 bf16
+// rows x 8 heads 31.2 / 27.5; of warps, 128 of up to 2,048 x 16 heads 134.8 / 131.5.
+template <bool kInt8>
+constexpr int kTeamCost = kInt8 ? 12 : 8;
+constexpr int kAloneCost = 1;
+static_assert(kTeamCost<true> <= kPagedItemPlaces && kTeamCost<false> <= kPagedItemPlaces);
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -93,6 +108,10 @@ __device__ __forceinline__ uint2 load8(const void *p) {
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // The two fp16 pairs n0 n1, n2 n3 of four whole numbers.
 __device__ __forceinline__ void to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
     const uint32_t u = n ^ 0x80808080u;
@@ -103,13 +122,15 @@ __device__ __forceinline__ void to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
     hi = *reinterpret_cast<uint32_t *>(&y);
 }
 
-// Whole number e of a and of b, as the bf16 pair: byte n, twice in a half word, gives
-// 128 + its low 7 bits, and 128 or, if it is negative, 256 to take from that.
+// Whole number e of a and of b times 2^-6, as a bf16 pair: the half word n + 128 is the
+// bf16 number (n + 128) 2^-133 (of its numbers below 2^-125 the bits count multiples of
+// 2^-133), and times 2^127, less 128 2^-6, that is exact.
+constexpr float kIntUnit = 0.015625f;
 __device__ __forceinline__ uint32_t to_bf16(uint32_t a, uint32_t b, int e) {
-    const uint32_t w = __byte_perm(a, b, 0x4400 + 0x1111 * e);
-    const uint32_t x = (w & 0x007f007fu) | 0x43004300u, y = (w & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&y));
-    return *reinterpret_cast<const uint32_t *>(&d);
+    const uint32_t u = (__byte_perm(a, b, 0x4400 + 0x1111 * e) & 0x00ff00ffu) ^ 0x00800080u;
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
+    return d;
 }
 
 // One lane's part of a unit's K, or of its V.
@@ -126,11 +147,11 @@ struct Shape {
     int tiles, total;   // row tiles, places of the sequence
 };
 template <bool kInt8, int kRows>
-__device__ __forceinline__ Shape shape_of(const PagedAttnParams &p, const PagedSeq &s, int g) {
+__device__ __forceinline__ Shape shape_of(const PagedAttnParams &p, const PagedSeq &s, int g, int cost) {
     Shape r;
     const int rows = min(s.n, p.max_new) * g;
     r.units = max((s.len + kUnitKeys<kInt8> - 1) / kUnitKeys<kInt8>, 1);
-    r.places = p.undivided ? 1 : r.units;
+    r.places = p.undivided ? 1 : r.units + cost;
     r.tiles = rows > p.small_rows ? 0 : (rows + kRows - 1) / kRows;
     r.total = p.c.Hkv * r.tiles * r.places;
     return r;
@@ -232,7 +253,10 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
 template <bool kInt8, int kN>
 __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(const PagedAttnParams p, int list) {
     constexpr int kRows = 8 * kN, kKeys = kUnitKeys<kInt8>, kBlocks = kKeys / 16;
-    __shared__ int warp_sums[kWarps], at_b[kWarps], at_start[kWarps];
+    __shared__ int warp_sums[kWarps];
+    // Where every warp is on the line: sequence, place in it, places left to it.  Read
+    // anew around an item's keys, and not kept over them: registers.
+    __shared__ volatile int at_b[kWarps], at_rel[kWarps], at_left[kWarps];
     __shared__ float4 sh_o[kWarps][kRows][HD / 4];
     __shared__ float2 sh_ml[kWarps][kRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -249,27 +273,32 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
 
     // The line's length, the shares, and where this worker's begins.
     if (lane == 0) at_b[warp] = -1;
-    int total = 0, items = 0, mine = 0, excl = 0, unused;
+    int total = 0, items = 0, mine = 0, excl = 0, my_items = 0, items_excl = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         Shape sh{};
-        if (b < p.c.B) sh = shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g);
+        if (b < p.c.B) sh = shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g, 0);
         mine = sh.total;
-        items += block_sum(p.c.Hkv * sh.tiles, warp_sums, unused);
+        my_items = p.c.Hkv * sh.tiles;
+        items += block_sum(my_items, warp_sums, items_excl);
         total += block_sum(mine, warp_sums, excl);
     }
     // A CTA's warps are workers of their own, or, where items would be divided among
     // more than two of those, one together.
     const int alone = (total + ctas * kWarps - 1) / (ctas * kWarps);
     const bool team = p.undivided || total >= 2ll * alone * items;
+    const int cost = p.undivided ? 0 : team ? kTeamCost<kInt8> : kAloneCost;
+    total += cost * items;
+    mine += cost * my_items;
+    excl += cost * items_excl;
     const int share = p.undivided ? (total + ctas - 1) / ctas
                       : team      ? max((total + ctas - 1) / ctas, kLeastTeamShare)
-                                  : max(alone, kLeastShare);
+                                  : max((total + ctas * kWarps - 1) / (ctas * kWarps), kLeastShare);
     const int me = team ? blockIdx.x : blockIdx.x * kWarps + warp;
     int base = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        if (p.c.B > kThreads) mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total : 0;
+        if (p.c.B > kThreads) mine = b < p.c.B ? shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g, cost).total : 0;
         const int sum = p.c.B > kThreads ? block_sum(mine, warp_sums, excl) : 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -277,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
             const long long s = static_cast<long long>(team ? blockIdx.x : blockIdx.x * kWarps + w) * share;
             if (s >= base + excl && s < base + excl + mine) {
                 at_b[w] = b;
-                at_start[w] = base + excl;
+                at_rel[w] = static_cast<int>(s - (base + excl));
+                at_left[w] = min(share, static_cast<int>(total - s));
             }
         }
         base += sum;
@@ -286,28 +316,49 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
     if (!p.undivided && team && warp > 0 && lane == 0) p.join[ctas + blockIdx.x * (kWarps - 1) + warp - 1] = PagedJoin{};
     const int sub = team ? warp : 0, step = team ? kWarps : 1;
     __syncthreads();
-    int b = at_b[warp];
-    if (b < 0) {
+    if (at_b[warp] < 0) {
         if (!p.undivided && lane == 0 && sub == 0) p.join[me] = PagedJoin{};
         return;
     }
-    const int start = me * share;
-    int left = min(share, total - start), rel = start - at_start[warp];
-    bool first_piece = true;
-
-    while (left > 0 && b < p.c.B) {
-        const PagedSeq s = paged_seq(p.c, b);
-        const Shape sh = shape_of<kInt8, kRows>(p, s, g);
-        const int item = rel / sh.places, at0 = rel - item * sh.places, at1 = min(sh.places, at0 + left);
-        const int u0 = at0, u1 = p.undivided ? sh.units : at1;
-        const int head = item / sh.tiles, tile = item - head * sh.tiles;
-        const int rows = min(s.n, p.max_new) * g - tile * kRows;  // of this item, if less than kRows
-        if (!p.undivided && first_piece && lane == 0 && sub == 0) {
-            PagedJoin j{};
-            if (u0 > 0)
-                j = PagedJoin{min(rows, kRows), tile * kRows, head, s.row0, (start - u0) / share, (start - u0 + sh.units - 1) / share};
-            p.join[me] = j;
+    struct Item {
+        PagedSeq s;
+        int b, places, total, at0, at1;  // places of the item, of the sequence; of these, this worker's
+        int u0, u1;                      // its units
+        int units, head, tile, rows;     // of the item
+    };
+    auto item_now = [&]() {
+        Item w;
+        w.b = at_b[warp];
+        w.s = paged_seq(p.c, w.b);
+        const Shape sh = shape_of<kInt8, kRows>(p, w.s, g, cost);
+        const int rel = at_rel[warp], item = rel / sh.places;
+        w.places = sh.places;
+        w.total = sh.total;
+        w.units = sh.units;
+        w.at0 = rel - item * sh.places;
+        w.at1 = min(sh.places, w.at0 + at_left[warp]);
+        w.u0 = max(w.at0 - cost, 0);
+        w.u1 = p.undivided ? sh.units : w.at1 - cost;
+        w.head = item / sh.tiles;
+        w.tile = item - w.head * sh.tiles;
+        w.rows = min(min(w.s.n, p.max_new) * g - w.tile * kRows, kRows);
+        return w;
+    };
+    if (!p.undivided && lane == 0 && sub == 0) {
+        const Item w = item_now();
+        PagedJoin j{};
+        if (w.u0 > 0) {
+            const int first = me * share - w.at0;  // the item's place on the line
+            j = PagedJoin{w.rows, w.tile * kRows, w.head, w.s.row0, (first + cost) / share, (first + w.places - 1) / share};
         }
+        p.join[me] = j;
+    }
+
+    while (true) {
+        const Item it = item_now();
+        const PagedSeq s = it.s;
+        const int b = it.b, u0 = it.u0, u1 = it.u1, head = it.head, tile = it.tile, rows = it.rows;
+        if (u1 <= u0) break;  // the share ends before its first key
 
         // Where the warp's next 32 blocks of 16 keys lie, those of units window0,
         // window0 + step, ..., a lane each: offsets of the rows and of their exponents,
@@ -324,6 +375,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
             my_at = pg * p.c.stride + row * HD;
             if (kInt8) my_scales = static_cast<long long>(pg) * (p.c.Hkv * p.c.page) + row;
             all_there = __ballot_sync(0xffffffffu, my_valid == 16);
+            if (!kInt8 && lane >= kBlocks && lane < (1 + kAhead) * kBlocks && my_valid > 0 && u + lane / kBlocks * step < u1) {
+                prefetch_l2(static_cast<const __nv_bfloat16 *>(p.c.k) + my_at, 16 * HD * sizeof(__nv_bfloat16));
+                prefetch_l2(static_cast<const __nv_bfloat16 *>(p.c.v) + my_at, 16 * HD * sizeof(__nv_bfloat16));
+            }
         };
         look_up(u0 + sub);
         // The same for a unit's blocks; the exponent of its key `lane`.
@@ -650,48 +705,57 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = 8 * n + 2 * c + r;
-                sh_o[warp][row][2 * l4] = make_float4(o[n][0][r], o[n][0][2 + r], o[n][1][r], o[n][1][2 + r]);
-                sh_o[warp][row][2 * l4 + 1] = make_float4(o[n][2][r], o[n][2][2 + r], o[n][3][r], o[n][3][2 + r]);
+                constexpr float f = kInt8 ? 1.f / kIntUnit : 1.f;
+                sh_o[warp][row][2 * l4] = make_float4(o[n][0][r] * f, o[n][0][2 + r] * f, o[n][1][r] * f, o[n][1][2 + r] * f);
+                sh_o[warp][row][2 * l4 + 1] = make_float4(o[n][2][r] * f, o[n][2][2 + r] * f, o[n][3][r] * f, o[n][3][2 + r] * f);
                 if (l4 == 0) sh_ml[warp][row] = make_float2(m[n][r], sum);
             }
         meet();
         // The item, or the piece: slot 2 me of one that began before this worker,
         // 2 me + 1 of one that goes on behind it.  16 lanes take a row.
-        const bool whole = u0 == 0 && u1 == sh.units;
-        const long long slot = (2ll * me + (u0 > 0 ? 0 : 1)) * kRows;
-        const int w0 = team ? 0 : warp, wn = team ? kWarps : 1, part = lane & 15;
-        for (int row = (team ? threadIdx.x : lane) / 16; row < min(rows, kRows); row += 2 * wn) {
-            float top = -INFINITY, sum = 0.f;
-            for (int w = w0; w < w0 + wn; ++w) top = fmaxf(top, sh_ml[w][row].x);
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = w0; w < w0 + wn; ++w) {
-                const float2 ml = sh_ml[w][row];
-                if (ml.y == 0.f) continue;  // no visible key
-                const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-                const float4 x = sh_o[w][row][part];
-                sum += ml.y * f;
-                y = make_float4(y.x + x.x * f, y.y + x.y * f, y.z + x.z * f, y.w + x.w * f);
+        {
+            const Item w = item_now();
+            const bool whole = w.u0 == 0 && w.u1 == w.units;
+            const long long slot = (2ll * me + (w.u0 > 0 ? 0 : 1)) * kRows;
+            const int w0 = team ? 0 : warp, wn = team ? kWarps : 1, part = lane & 15;
+            for (int row = (team ? threadIdx.x : lane) / 16; row < w.rows; row += 2 * wn) {
+                float top = -INFINITY, sum = 0.f;
+                for (int i = w0; i < w0 + wn; ++i) top = fmaxf(top, sh_ml[i][row].x);
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = w0; i < w0 + wn; ++i) {
+                    const float2 ml = sh_ml[i][row];
+                    if (ml.y == 0.f) continue;  // no visible key
+                    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+                    const float4 x = sh_o[i][row][part];
+                    sum += ml.y * f;
+                    y = make_float4(y.x + x.x * f, y.y + x.y * f, y.z + x.z * f, y.w + x.w * f);
+                }
+                if (whole) {
+                    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+                    const int at = w.tile * kRows + row, t = at / g, h = w.head * g + at - t * g;
+                    if (in_bounds(h < p.H && w.s.row0 + t < p.c.N, p.status))
+                        reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (w.s.row0 + t) * p.o_stride_t)[part] =
+                            make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+                } else if (in_bounds(me < ctas * kWarps, p.status)) {
+                    reinterpret_cast<float4 *>(p.part_o + (slot + row) * HD)[part] = y;
+                    if (part == 0) p.part_ml[slot + row] = make_float2(top, sum);
+                }
             }
-            if (whole) {
-                const float inv = sum != 0.f ? 1.f / sum : 0.f;
-                const int at = tile * kRows + row, t = at / g, h = head * g + at - t * g;
-                if (in_bounds(h < p.H && s.row0 + t < p.c.N, p.status))
-                    reinterpret_cast<uint2 *>(p.o + h * p.o_stride_h + (s.row0 + t) * p.o_stride_t)[part] =
-                        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-            } else if (in_bounds(me < ctas * kWarps, p.status)) {
-                reinterpret_cast<float4 *>(p.part_o + (slot + row) * HD)[part] = y;
-                if (part == 0) p.part_ml[slot + row] = make_float2(top, sum);
+            const int left = at_left[warp] - (w.at1 - w.at0);
+            int next = w.b, rel = at_rel[warp] + w.at1 - w.at0;
+            if (rel == w.total) {
+                rel = 0;
+                do ++next;
+                while (left > 0 && next < p.c.B && shape_of<kInt8, kRows>(p, paged_seq(p.c, next), g, cost).total == 0);
             }
-        }
-        meet();
-
-        left -= at1 - at0;
-        rel += at1 - at0;
-        first_piece = false;
-        if (rel == sh.total) {
-            rel = 0;
-            do ++b;
-            while (left > 0 && b < p.c.B && shape_of<kInt8, kRows>(p, paged_seq(p.c, b), g).total == 0);
+            meet();
+            if (left <= 0 || next >= p.c.B) break;
+            if (lane == 0) {
+                at_b[warp] = next;
+                at_rel[warp] = rel;
+                at_left[warp] = left;
+            }
+            __syncwarp();
         }
     }
 }
