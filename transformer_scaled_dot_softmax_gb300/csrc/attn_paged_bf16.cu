@@ -75,9 +75,8 @@ constexpr int kRaw = 3;  // int8 tiles in flight
 // One piece of work: a row tile against key tiles j0 .. j0 + n_kv - 1.
 struct Piece {
     int b, head;      // sequence, K/V head
-    int t0, tokens;   // new tokens t0 .. t0 + tokens - 1 of the sequence's
-    int row0;         // packed row of token t0
-    int len, pos0;    // the sequence's length, the position of token t0
+    int tokens, row0; // new tokens, the first one's packed row
+    int len, pos0;    // the sequence's length, the position of that token
     int j0, n_kv;
     int full_hi;      // keys below it are seen by every row
     int whole;        // all of the row tile's key tiles
@@ -159,18 +158,16 @@ struct Share {
 __device__ __forceinline__ int place_of(const int *cum, int x) { return cum[x] + kTileCost * x; }
 
 __device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Share &sh, int t) {
-    const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
-    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
+    const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, p.H / p.c.Hkv));
     const int i = sh.x0 + t, up = i / sh.tiles, x = i - up * sh.tiles;
+    const PagedTile tile = reinterpret_cast<const PagedTile *>(p.plan + at.tile)[x];
     Piece w;
     w.head = sh.head0 + up;
-    w.b = p.plan[at.seq + x];
-    const PagedSeq s = paged_seq(p.c, w.b);
-    w.t0 = (x - p.plan[at.first + w.b]) * tt;
-    w.tokens = min(tt, min(s.n, p.max_new) - w.t0);
-    w.row0 = s.row0 + w.t0;
-    w.len = s.len;
-    w.pos0 = s.len - s.n + w.t0;
+    w.b = tile.b;
+    w.tokens = tile.tokens;
+    w.row0 = tile.row0;
+    w.len = tile.len;
+    w.pos0 = tile.pos0;
     w.full_hi = p.causal ? min(max(w.pos0 + 1, 0), w.len) : w.len;
     const int n = p.plan[at.cum + x + 1] - p.plan[at.cum + x];
     const int first = w.head * sh.keys + place_of(p.plan + at.cum, x) + kTileCost;  // its first key tile's place

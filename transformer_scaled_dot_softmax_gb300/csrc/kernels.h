@@ -349,13 +349,18 @@ struct PagedMaps {
 cudaError_t launch_attn_paged(const PagedMaps &maps, const PagedAttnParams &p, cudaStream_t stream);
 mha_status encode_paged_maps(PagedMaps *m, const PagedAttnParams &p);
 
+// A row tile: its sequence and that one's cached rows, its first packed row and that
+// one's position, its tokens.
+struct __align__(16) PagedTile {
+    int b, len, row0, pos0, tokens, unused[3];
+};
 // Lists in PagedAttnParams::plan, of at most `tiles` row tiles and B sequences.
 // plan[0]: the number of row tiles; [1]: of sequences that have some; [2]: key tiles of
 // a K/V head.
 struct PagedPlan {
+    int tile;    // (tiles) PagedTile, 8 ints each
     int first;   // (B + 1) first row tile of each sequence
     int cum;     // (tiles + 1) key tiles of one K/V head before a row tile
-    int seq;     // (tiles) its sequence
     int slot;    // (B) a sequence's place among those that have row tiles, or -1
     int slot_b;  // (B) the sequence at a place
     int blocks;  // (B + 1) blocks of 128 cached rows before it
@@ -363,10 +368,10 @@ struct PagedPlan {
 };
 inline __host__ __device__ PagedPlan paged_plan(int B, int tiles) {
     PagedPlan l;
-    l.first = 4;
+    l.tile = 8;
+    l.first = l.tile + 8 * tiles;
     l.cum = l.first + B + 1;
-    l.seq = l.cum + tiles + 1;
-    l.slot = l.seq + tiles;
+    l.slot = l.cum + tiles + 1;
     l.slot_b = l.slot + B;
     l.blocks = l.slot_b + B;
     l.ints = l.blocks + B + 1;

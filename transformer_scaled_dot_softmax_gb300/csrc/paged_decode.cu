@@ -184,7 +184,8 @@ __device__ __forceinline__ int block_sum(int x, int *warp_sums, int &excl) {
 __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
     const int g = p.H / p.c.Hkv, tt = paged_tile_tokens(g);
     const PagedPlan at = paged_plan(p.c.B, paged_most_tiles(p.c.N, p.c.B, g));
-    int *first = p.plan + at.first, *cum = p.plan + at.cum, *seq = p.plan + at.seq;
+    int *first = p.plan + at.first, *cum = p.plan + at.cum;
+    PagedTile *tile = reinterpret_cast<PagedTile *>(p.plan + at.tile);
     const int most = paged_most_tiles(p.c.N, p.c.B, g);
     int *slot = p.plan + at.slot, *slot_b = p.plan + at.slot_b, *blocks = p.plan + at.blocks;
     int tiles = 0, slots = 0, rows = 0;
@@ -220,7 +221,7 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
     int keys = 0;
     for (int x0 = 0; x0 < tiles; x0 += kThreads) {
         const int x = x0 + threadIdx.x;
-        int n = 0, excl, b = 0;
+        int n = 0, excl;
         if (x < tiles) {
             int lo = 0, hi = p.c.B;  // the last sequence whose first tile is at most x
             while (hi - lo > 1) {
@@ -230,17 +231,14 @@ __device__ void list_tiles(const PagedAttnParams &p, int *warp_sums) {
                 else
                     hi = mid;
             }
-            b = lo;
-            const PagedSeq s = paged_seq(p.c, b);
-            const int last = min((x - first[b] + 1) * tt, min(s.n, p.max_new)) - 1;
-            const int end = p.causal ? min(max(s.len - s.n + last + 1, 0), s.len) : s.len;
+            const PagedSeq s = paged_seq(p.c, lo);
+            const int t0 = (x - first[lo]) * tt, tokens = min(tt, min(s.n, p.max_new) - t0), pos0 = s.len - s.n + t0;
+            const int end = p.causal ? min(max(pos0 + tokens, 0), s.len) : s.len;
             n = max((end + 127) / 128, 1);
+            tile[x] = PagedTile{lo, s.len, s.row0 + t0, pos0, tokens, {}};
         }
         const int total = block_sum(n, warp_sums, excl);
-        if (x < tiles) {
-            cum[x] = keys + excl;
-            seq[x] = b;
-        }
+        if (x < tiles) cum[x] = keys + excl;
         keys += total;
     }
     if (threadIdx.x == 0) {
