@@ -515,9 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
             float l_run = 0.f;
 
-            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
+            const int n_kv = w.n_kv, j0 = w.j0, full_hi = w.full_hi;
+            for (int jt = 0; jt < n_kv; ++jt, ++n) {
                 if ((n & 1) != half) continue;
-                const int j = tile_of(w, jt);
+                const int j = j0 + n_kv - 1 - jt;
                 const int sb = n % kSBufs, st = n % STAGES;
                 ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
                 if (!ok) break;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (written before the tile was handed to the S issuer, which waited
                 // for that before it issued the products whose end s_full tells)
                 const uint32_t bad = *static_cast<volatile uint32_t *>(&sm.bad[st]);
-                const bool edge = j * BN + BN > w.full_hi || bad != 0;
+                const bool edge = j * BN + BN > full_hi || bad != 0;
                 int rd_first = 0;
                 if (!edge) {
 #pragma unroll
