@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         int n = 0, v = 0;
+        int sb = half, s_par = 0, st = half;  // n mod kSBufs and how often that was, n mod STAGES, of this group's next tile
         bool ok = true;
         for (int t = 0; ok && t < pieces; ++t) {
             const Piece &w = piece_of<kInt8>(sm, p, sh, t);
@@ -516,11 +517,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l_run = 0.f;
 
             const int n_kv = w.n_kv, j0 = w.j0, full_hi = w.full_hi;
-            for (int jt = 0; jt < n_kv; ++jt, ++n) {
-                if ((n & 1) != half) continue;
+            const int n0 = n;
+            auto step = [&]() {
+                sb += 2;
+                if (sb >= kSBufs) {
+                    sb -= kSBufs;
+                    s_par ^= 1;
+                }
+                st += 2;
+                if (st >= STAGES) st -= STAGES;
+            };
+            for (int jt = (n0 ^ half) & 1; jt < n_kv; jt += 2, step()) {
+                n = n0 + jt;
                 const int j = j0 + n_kv - 1 - jt;
-                const int sb = n % kSBufs, st = n % STAGES;
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
+                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], s_par, ab));
                 if (!ok) break;
                 if (!warp_live) {
                     // P of the warp's rows stays whatever it is: a row of
@@ -689,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
             }
             if (!ok) break;
+            n = n0 + n_kv;
             if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
             sm.red_m[half][r] = m_run;
             sm.red_l[half][r] = l_run;
