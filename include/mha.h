@@ -494,7 +494,7 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  * Two launches (sequences with up to 16 query rows per K/V head, 32 with int8;
  * joining of the partial sums of divided key ranges), a third between them when
  * max_new allows more: tcgen05 products over tiles of 128 rows.  When it allows 512
- * rows and the cache is int8 or its pages are no multiple of 32 rows, or 4,096 and
+ * rows and the cache is int8 or its pages are no multiple of 32 rows, or 2,048 and
  * they are no multiple of 64, one more lays these sequences' cached rows out as bf16
  * first, in up to 4 GiB of the workspace (where that would take more it is left out).
  * A call's results do not depend on timing (equal calls give equal bits).

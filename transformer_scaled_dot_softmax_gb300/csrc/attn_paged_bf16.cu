@@ -21,20 +21,20 @@
 // are attn_scored_bf16.cuh's, without cap and bias.
 //
 // Bound, like that kernel, by the softmax warps' instruction stream (issue 60 %, tensor
-// 42 %, special functions 41 % of their cycles).  Measured, causal, 2 x 16 heads x 8,192
-// in 64-row pages: 277 us (990 TFLOP/s) from cold memory, the whole call 282; 1,024
-// tokens x 16 heads, 4 to a K/V head, behind 31,744 rows 130 (1,040 TFLOP/s).
+// 43 %, special functions 43 % of their cycles).  Measured, causal, 2 x 16 heads x 8,192
+// in 64-row pages: the whole call 271 us (1,015 TFLOP/s), listing and joining included;
+// 1,024 tokens x 16 heads, 4 to a K/V head, behind 31,744 rows 125 (1,080 TFLOP/s).
 //
 // int8 pages arrive in a ring of their own, 64 bytes a row, with the rows'
 // exponents; the output warps, which are idle while a row tile is worked on, write
 // them as bf16 into the K/V ring, in the 128-byte swizzle that TMA leaves
 // (n 2^e is exact).  Between two tiles they look for a finished row tile
-// first, since the products behind it wait for its accumulators.  A key tile takes 1.27
-// us so, 0.57 without, in every row tile that reads it: from
-// kPagedWideRows query rows on the rows are laid out as bf16 before instead.
+// first, since the products behind it wait for its accumulators.  A key tile takes 1.25
+// us so, 0.53 without, in every row tile that reads it: from kPagedWideRows query rows
+// on the rows are laid out as bf16 before instead.
 //
 // Tried and dropped: stages of their own for K, free earlier, V loaded by an output
-// warp, boxes issued by single threads (prompts 318 to 650 us against 285 to 291): each
+// warp, boxes issued by single threads (prompts 318 to 650 us against 291): each
 // adds instructions a tile to a warp that gets few to issue beside the softmax, and to
 // code that already fills the instruction cache.
 #include <cuda_bf16.h>
@@ -148,7 +148,7 @@ __device__ __forceinline__ uint32_t *raw_bad(Smem<kInt8> &sm, int i) {
 // Where a CTA's share of the line lies.  A row tile takes kTileCost places on it
 // before those of its key tiles: what a piece costs besides them, in key tiles.
 // (Causal, 2 x 16 x 8,192: CTAs with the short row tiles of a head have 29 of them,
-// others 7.  0 places 301 us, 1 294, 2 287, 3 286, 4 288.)
+// others 7.  1 place 285 us, 2 279, 3 271, 4 275, 5 276.)
 constexpr int kTileCost = 3;
 struct Share {
     int tiles, keys;        // row tiles, places of one K/V head

@@ -321,13 +321,14 @@ struct PagedAttnParams {
     int *status;
 };
 // Measured there / as row tiles, us (4 K/V heads of 32,768 keys; 16 sequences x 8 heads of
-// 2,048 to 4,096): bf16 16 rows 17, 29 / 19, 32, 24 rows 21, 40 / the same; int8 16 rows
-// 19, 28 / 23, 44, 32 rows 26, 40 / the same.
+// 2,048 to 4,096): bf16 16 rows 16, 26 / 19, 30; int8 16 rows 16, 24 / 24, 48, 32 rows 20,
+// 37 / 24, 48; bf16 past 16 is the same either way.
 inline constexpr int paged_small_rows(bool int8) { return int8 ? 32 : 16; }
 // Up to so many rows of a sequence, and as long as each CTA has one at most, items
 // are taken whole: one launch, no workspace.  Measured, whole / divided and joined,
-// us: 8 K/V heads of one sequence of 100 bf16 rows 5.2 / 12.3, 1,000 10.6 / 10.3; of 64
-// sequences of 500 11.8 / 17.5, 1,000 20.3 / 23.6.
+// us: 8 K/V heads of one sequence of up to 100 bf16 rows 5.5 / 8.8, 500 7.7 / 8.3, 1,000
+// 10.6 / 8.8; of 64 sequences of up to 500 11.8 / 15.9, 1,000 20.5 / 22.1.  (The rows are
+// those that the page table has room for; the sequences are mostly shorter.)
 constexpr int kPagedWholeRows = 1024;
 constexpr int kPagedTileCtas = kSmsPerGpu;  // persistent CTAs of attn_paged_bf16.cu
 // Rows that a warp of paged_decode.cu takes at once, for calls whose sequences have up
@@ -388,10 +389,10 @@ cudaError_t launch_paged_widen(const PagedAttnParams &p, const PagedWide &w, cud
 // Query rows of a K/V head (new tokens x query heads) from which on rows are laid out
 // that way first: int8 ones and those of pages of 16 rows or an odd number of
 // them, and of pages of 32 rows or an odd number.  Measured, 32,768 keys x 4 K/V
-// heads, first / straight from the pages, us: int8, 64-row pages, 256 query rows 43 /
-// 40, 512 48 / 53, 4,096 151 / 271; bf16, 16-row pages 256 42 / 38, 512 47 / 50, 4,096
-// 151 / 247; 32-row pages 512 47 / 40, 2,048 90 / 95, 4,096 151 / 171.
-constexpr int kPagedWideRows = 512, kPagedWideRows32 = 4096;
+// heads, first / straight from the pages, us: int8, 64-row pages, 256 query rows 38 /
+// 35, 512 44 / 51, 4,096 140 / 268; bf16, 16-row pages 256 37 / 33, 512 43 / 46, 4,096
+// 141 / 242; 32-row pages 512 43 / 37, 2,048 84 / 91, 4,096 140 / 165.
+constexpr int kPagedWideRows = 512, kPagedWideRows32 = 2048;
 constexpr size_t kPagedWideBytes = static_cast<size_t>(4) << 30;  // as long as it does not take more than this
 // Tokens of a row tile, and row tiles of a call at most.
 inline __host__ __device__ int paged_tile_tokens(int g) { return 128 / g; }

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const PagedCache c
 // The rows of the sequences that have row tiles (see PagedWide), in blocks of 128 rows
 // of a head: what attn_paged_bf16.cu would do to an int8 tile for each of the row
 // tiles that read it is done once (a chunk of 1,024 x 4 query heads behind 31,744 int8
-// rows 274 -> 149 us, this launch 16 of them from cold memory).
+// rows 268 -> 138 us, this launch 16 of them from cold memory).
 template <bool kInt8>
 __global__ void __launch_bounds__(kThreads) paged_widen_kernel(const PagedAttnParams p, const PagedWide w) {
     pdl_wait();
