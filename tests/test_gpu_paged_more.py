@@ -182,6 +182,24 @@ def test_many_sequences(lib, shape, int8):
     compare(lib, c, queries(c, h, 2.0), True)
 
 
+# (h, h_kv, page, lengths, new) in tables of 2,000 rows, whose items are divided: so short that workers' shares end before the
+# first key of an item, or hold one piece's last keys and another's beginning
+SHORT = [(1, 1, 16, [1], [1]), (4, 2, 16, [17, 1, 0, 33, 64], [1, 1, 0, 1, 1]), (8, 8, 32, [1 + i % 40 for i in range(40)], [1] * 40),
+         (16, 16, 16, [5 + i for i in range(130)], [1 + i % 3 for i in range(130)]), (8, 1, 64, [500, 3, 900, 64], [1, 1, 2, 0]),
+         (12, 4, 48, [1999, 1, 1, 1500], [1, 1, 1, 4])]
+
+
+@pytest.mark.parametrize("shape", SHORT)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("most", [None, 40])
+def test_short_items_that_are_divided(lib, shape, int8, most):
+    h, *rest = shape
+    c = pr.Cache(*rest, int8=int8, seed=12, capacity=2000).fill()
+    out = compare(lib, c, queries(c, h, 2.0), True, max_new=max(c.new) if most is None else most)
+    again = compare(lib, c, queries(c, h, 2.0), True, max_new=max(c.new) if most is None else most)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
 # (h, h_kv, page, lengths, new): int8 rows, and pages of 16, 48 and 32 rows, that are laid out as bf16 first, some sequences
 # of a batch among others that are not
 WIDE = [(8, 2, 16, [700], [200]), (4, 1, 48, [300, 1000, 50, 129], [130, 200, 1, 129]), (16, 2, 32, [520, 2, 900], [513, 1, 7]),
