@@ -15,7 +15,8 @@
 // Bound by memory.  8 lanes take one row, 16 bytes each, K and V together; a
 // block takes 32 consecutive tokens (or cached rows) of one head, which lie
 // together in pages as in head-major rows.  Measured on a GB300: append, 2 x 8,192 tokens
-// x 16 heads, bf16 20.6 us (6.5 TB/s of its copy), 16 tokens 2.6 us (a launch); read, 16
+// x 16 heads, bf16 20.0 us (6.7 TB/s of its copy; 20.6 with a row loaded only once its
+// page is known), 16 tokens 2.6 us (a launch); read, 16
 // sequences of up to 7,936 int8 rows x 16 heads 113 us (204 MB read, 469 MB written, the
 // zeros behind shorter sequences among them: 5.9 TB/s).  16-byte loads of int8 rows, 4
 // lanes each, take 129: a lane's two stores then lie 32 bytes apart.  8 rows a thread
@@ -95,13 +96,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedCache
     const int pos = s.len - s.n + token - s.row0;
     bool ok = token < c.N && token >= s.row0 && token < s.row0 + s.n && pos >= 0;
     int page = -1;
-    if (ok) page = paged_page(c, lo, pos / c.page);
-    ok = page >= 0;
     uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
     if (ok) {
         x = *reinterpret_cast<const uint4 *>(k.x + head * k.stride_h + token * k.stride_t + 8 * lane);
         y = *reinterpret_cast<const uint4 *>(v.x + head * v.stride_h + token * v.stride_t + 8 * lane);
+        page = paged_page(c, lo, pos / c.page);
     }
+    ok = page >= 0;
     const int row = head * c.page + pos % c.page;
     const long long at = page * c.stride + row * static_cast<long long>(HD) + 8 * lane;
     if (!c.int8) {
