@@ -67,10 +67,12 @@ constexpr int ctas_of_sm(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
 
 template <bool kInt8>
 constexpr int kUnitKeys = kInt8 ? 32 : 16;
-// bf16: units behind a piece's first one that are asked for with it (16 sequences of up
-// to 32,768 rows 240 us without, 236 with 2 of them; 128 of up to 2,048 133, 129).
-// int8 units take longer to work on than to come, and these instructions as well: 31.3
-// us without, 32.9 with them for 64 sequences of up to 8,192.
+// bf16: units behind a piece's first one that are asked for with it.  Calls back to back,
+// without / with 2 of them, us: 16 sequences of up to 8,192 rows x 16 heads 70 / 69, of up
+// to 32,768 240 / 236, 128 of up to 2,048 136 / 134; one call alone on an idle GPU takes 1
+// to 2 more with them.  Every unit's asked for ahead: 84 against 79 alone, 128 of up to
+// 2,048 163 against 149.  int8 units take longer to work on than to come, and these
+// instructions as well: 31.3 us without, 32.9 with them for 64 sequences of up to 8,192.
 constexpr int kAhead = 2;
 // Places on the line that an item takes before those of its units, for what beginning
 // one costs a worker: a CTA's four warps together, or a warp.  Without / with them, us:
