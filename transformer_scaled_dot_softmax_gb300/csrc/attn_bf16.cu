@@ -676,7 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         //   w_h = 2^((m_h - M) c), M = max(m_A, m_B);
         // a group that saw no visible key (or no tile) has weight 0 and its
         // accumulator, possibly never written for this item, is left out of
-        // the result; a row with no visible key at all outputs 0.
+        // the result; a row with no visible key at all outputs 0.  (Where w is
+        // flushed, m_h < M - 126 log2 units: the group's rounds, 2^16 at most
+        // each, then have 2^-29 of the other's weight at most, which is 2^-64 or
+        // more against M, over 2^17 rounds.)
         const uint32_t lane_base = static_cast<uint32_t>(warp & 3) * 32;
         const int r = static_cast<int>(lane_base) + lane;
         const uint32_t tl = tmem_addr(tmem, lane_base, 0);

@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab))) return false;
             tc_fence_after_sync();
             // A sum of 0: no visible key.  One of NaN goes on to the output.
-            const PagedLevel va = paged_level(ma, la), vb = paged_level(mb, lb);
+            const SumLevel va = sum_level(ma, la), vb = sum_level(mb, lb);
             const float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
             const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
             const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;

@@ -72,6 +72,7 @@
 
 #include "kernels.h"
 #include "scores.cuh"
+#include "softmax_sums.cuh"
 #include "sm103_ptx.cuh"
 
 namespace mha {
@@ -925,18 +926,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&sm.ml_free);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
             tc_fence_after_sync();
-            const float M = fmaxf(ma, mb);
             // A sum of 0: no visible key.  One of NaN (a NaN or +infinity among
             // the visible scores) goes on to o and lse.
-            const float wa = la != 0.f ? ex2_approx(ma - M) : 0.f;
-            const float wb = lb != 0.f ? ex2_approx(mb - M) : 0.f;
+            const SumLevel va = sum_level(ma, la), vb = sum_level(mb, lb);
+            const float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
+            const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
+            const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;
             const float L = la * wa + lb * wb;
             const float inv = kMode == kDecode ? 1.f : L != 0.f ? 1.0f / L : 0.f;
             const float fa = wa * inv, fb = wb * inv;
             const long long prow = kMode == kDecode ? it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out : 0;
             if (row_ok) {
                 if (kMode == kDecode)
-                    // (the reference of a NaN is as good as any, if the merge takes it)
+                    // (L in [1, 4): the merge joins by M alone; the reference of a
+                    // NaN is as good as any, if the merge takes it)
                     p.part_ml[prow] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
                 else if (kMode == kForwardLse)
                     p.lse[w.out] = L != 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;

@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
 // 16 lanes take one row (4 features each), up to kBatch pieces at a time; groups that
 // would be idle share a row's pieces.  A piece without a visible key has m = -inf,
 // l = 0; one with a NaN or infinity among its scores l = NaN.  m_s is taken as
-// paged_level gives it.
+// sum_level gives it.
 //
 // Bound by latency: small blocks, most of which find nothing to join.  Behind row
 // tiles, whose blocks come on top, one looks at four workers' records, and takes fewer
@@ -787,7 +787,7 @@ struct Sum {
         float top = m;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (ml[i].y != 0.f) top = fmaxf(top, paged_level(ml[i].x, ml[i].y).m);
+            if (ml[i].y != 0.f) top = fmaxf(top, sum_level(ml[i].x, ml[i].y).m);
         const float a = piece_weight(m, top);
         m = top;
         l *= a;
@@ -795,7 +795,7 @@ struct Sum {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (ml[i].y != 0.f) {
-                const PagedLevel v = paged_level(ml[i].x, ml[i].y);
+                const SumLevel v = sum_level(ml[i].x, ml[i].y);
                 const float w = piece_weight(v.m, top) * v.down;
                 l += ml[i].y * w;
                 o = make_float4(o.x + x[i].x * w, o.y + x[i].y * w, o.z + x[i].z * w, o.w + x[i].w * w);

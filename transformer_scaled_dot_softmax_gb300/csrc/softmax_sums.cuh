@@ -1,0 +1,24 @@
+// softmax_sums.cuh -- joining a row's partial sums (reference m, sum l of the weights
+// against it, unnormalised O) of different keys.
+#pragma once
+
+namespace mha {
+
+// A partial sum (m in log2 units, l > 0) is 2^m l, and where a reference serves
+// as long as sums fit (m = 0 for scores of -70 as well) l may be as far from 1 as
+// 2^+-64 and more: two of them are compared and joined by m + e, e the whole part of
+// log2 l, with O and l taken times 2^-e.  By m alone 64 keys at -130 and 64 at -72.5
+// against -130, a sum of 2^63.5, would vanish beside 64 at -68 against 0, one of 2^-62:
+// 2^-130 is flushed to 0, although they weigh a 23rd of those.
+struct SumLevel {
+    float m, down;  // m + e, 2^-e
+};
+__device__ __forceinline__ SumLevel sum_level(float m, float l) {
+    const int e = min(max(static_cast<int>(__float_as_uint(l) >> 23 & 255u) - 127, -100), 100);  // (any, for a NaN)
+    SumLevel r;
+    r.m = m + static_cast<float>(e);
+    r.down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return r;
+}
+
+}  // namespace mha
