@@ -314,7 +314,8 @@ mha_status sdpa_decode_forward(const void *q, const void *k_cache, const void *v
  *   head i reads K/V head i / (h / h_kv).  16-byte aligned.  T_q < 2^24, T_k
  *   <= 8388480, h <= 65535, B h ceil(T_q / 128) < 2^30 (else
  *   MHA_ERR_UNSUPPORTED).  Entries of v up to 2^46 in magnitude: the running
- *   sums hold weights of up to 2^64 times them.
+ *   sums hold weights of up to 2^64 times them, and of down to 2^-64 where all of
+ *   a row's scores are that far below 0 (v's parts below 2^-62 may be lost there).
  *   lse: fp32 (B, h, T_q), the log-sum-exp of the row's scores (natural log,
  *   -inf for a query that sees no key), or NULL.  Unlike sdpa_forward_lse's it
  *   sums the unrounded weights: an fp32 result without a cap, as near as the
@@ -487,7 +488,9 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  *   A token that sees no key outputs 0, one with a NaN or positive infinity among
  *   its scores NaN.  Rows past L_b may hold anything; a NaN or infinity among a
  *   sequence's own values may reach all its outputs.  Entries of k and v up to
- *   2^46 in magnitude.
+ *   2^46 in magnitude; as small ones as a cache holds count, but that where all of
+ *   a row's scores lie up to 44 below 0 (64 as powers of 2), v's parts below 2^-62
+ *   may be lost.
  *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
  *   in flight.  Few query rows of short sequences (max_pages page_rows <= 1024) take
  *   one launch and 0 bytes; NULL is allowed then.

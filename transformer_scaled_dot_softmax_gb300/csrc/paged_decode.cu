@@ -27,7 +27,8 @@
 // scaled by a power of two so that its largest element lies in [2^14, 2^15)
 // (elements below 2^-31 of it lose bits, 2^-39 of it at most); the keys' powers of
 // two and the row's meet the fp32 score.  V's whole numbers are bf16 numbers, and its
-// rows' powers of two meet the weights, without rounding.  The numbers come out of
+// rows' powers of two, times 2^kPowerUp, meet the weights, without rounding but for weights
+// below 2^-kPowerUp beside rows as small as there are.  The numbers come out of
 // their bytes by permutes: 0x6400 | u is 1024 + u in fp16, u = n + 128, and u alone
 // u 2^-133 in bf16.
 //
@@ -134,6 +135,16 @@ __device__ __forceinline__ uint32_t to_bf16(uint32_t a, uint32_t b, int e) {
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
     return d;
 }
+
+// Weights times V's powers of two are bf16 numbers of their own, whole down to 2^-126 only:
+// a weight of 2^-10 beside a row of 2^-120 would keep no bit.  They are taken 2^40 times
+// as large, which keeps weights down to 2^-40 of a row whole beside any power.  Up to
+// the 2^46 that V may hold there is room: powers of 2^40, weights of 2^16 and sums of 2^26
+// units of them come to 2^122.
+constexpr int kPowerUp = 40;
+constexpr float kPowerDown = 1.f / static_cast<float>(1ull << kPowerUp);
+// The exponent that it makes of a stored one; 255 (NaN) stays.
+__device__ __forceinline__ uint32_t raised(uint32_t stored) { return min(stored + kPowerUp, 255u); }
 
 // One lane's part of a unit's K, or of its V.
 struct Part {
@@ -642,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
                 l[n][0] += sum[n][0];
                 l[n][1] += sum[n][1];
             }
+            const uint32_t v_power = kInt8 ? raised(vp.s) * 0x00800080u : 0u;  // of the unit's key `lane`
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
                 // V^T: features 8 (l/4) + 2 f, + 1 in rows l/4, l/4 + 8 of tile f
@@ -665,11 +677,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
                         va[f][3] = __byte_perm(w[2][f], w[3][f], 0x7632);
                     }
                 }
-                // (exact; as bf16 a power's bits are its stored exponent, 7 bits up)
+                // (as bf16 a power's bits are its stored exponent, 7 bits up)
                 uint32_t power[2] = {0u, 0u};
                 if constexpr (kInt8) {
-                    power[0] = __shfl_sync(0xffffffffu, vp.s, 16 * i + l4) * 0x00800080u;
-                    power[1] = __shfl_sync(0xffffffffu, vp.s, 16 * i + 8 + l4) * 0x00800080u;
+                    power[0] = __shfl_sync(0xffffffffu, v_power, 16 * i + l4);
+                    power[1] = __shfl_sync(0xffffffffu, v_power, 16 * i + 8 + l4);
                 }
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
@@ -705,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 const int row = 8 * n + 2 * c + r;
-                constexpr float f = kInt8 ? 1.f / kIntUnit : 1.f;
+                constexpr float f = kInt8 ? 1.f / kIntUnit * kPowerDown : 1.f;
                 sh_o[warp][row][2 * l4] = make_float4(o[n][0][r] * f, o[n][0][2 + r] * f, o[n][1][r] * f, o[n][1][2 + r] * f);
                 sh_o[warp][row][2 * l4 + 1] = make_float4(o[n][2][r] * f, o[n][2][2 + r] * f, o[n][3][r] * f, o[n][3][2 + r] * f);
                 if (l4 == 0) sh_ml[warp][row] = make_float2(m[n][r], sum);
