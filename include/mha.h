@@ -492,8 +492,13 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  *   a row's scores lie up to 44 below 0 (64 as powers of 2), v's parts below 2^-62
  *   may be lost.
  *   workspace: >= sdpa_paged_workspace_bytes() bytes, 256-byte aligned; one per call
- *   in flight.  Few query rows of short sequences (max_pages page_rows <= 1024) take
- *   one launch and 0 bytes; NULL is allowed then.
+ *   in flight.  Few query rows of few short sequences take one launch and 0 bytes, and
+ *   NULL is allowed then: where max_pages page_rows <= 1024, max_new h / h_kv <= 16
+ *   (int8 32) and B h_kv <= 608 (456 past 8 rows, 304 past 16).
+ *   32 bits number the work: with c = max_pages page_rows, B h_kv (c / 16 + 17) <
+ *   2^31 - 2^14 (int8: c / 32), and where max_new h / h_kv > 16 (int8 32) up to twice
+ *   (int8 four times) as many are, and (ceil(N / floor(128 h_kv / h)) + B) h_kv
+ *   (c / 128 + 8).  What has more is MHA_ERR_UNSUPPORTED.
  * Two launches (sequences with up to 16 query rows per K/V head, 32 with int8;
  * joining of the partial sums of divided key ranges), a third between them when
  * max_new allows more: tcgen05 products over tiles of 128 rows.  When it allows 512
@@ -502,7 +507,8 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  * first, in up to 4 GiB of the workspace (where that would take more it is left out).
  * A call's results do not depend on timing (equal calls give equal bits).
  */
-/* From the sizes in `cache` (its pointers may be NULL); 0 for sizes that are not valid. */
+/* From the sizes in `cache` (its pointers may be NULL); 0 for sizes that are not valid or
+ * too large, and for calls that need none. */
 size_t sdpa_paged_workspace_bytes(const mha_paged_cache *cache, int h, int N, int max_new);
 mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
                               long long q_stride_t, void *o, long long o_stride_h,

@@ -139,6 +139,16 @@ Layout layout(const PagedCache &c, int g, int max_new) {
     return l;
 }
 
+// Do 32 bits number the kernels' work lines, for whatever lengths and starts the device
+// holds?  (Units of 16 bf16 or 32 int8 keys of what is taken as few rows; key tiles.)
+bool lines_fit(const PagedCache &c, const Layout &l, int g, int max_new) {
+    const long long cap = c.cap, unit = c.int8 ? 32 : 16;
+    const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, c.N)) * g, paged_small_rows(c.int8 != 0));
+    const long long row_tiles = (rows + l.tile_rows - 1) / l.tile_rows;
+    if (static_cast<long long>(c.B) * c.Hkv * row_tiles * (cap / unit + 1 + kPagedItemPlaces) >= kMostLine) return false;
+    return !l.tiles || static_cast<long long>(paged_most_tiles(c.N, c.B, g)) * c.Hkv * (cap / 128 + 8) < kMostLine;
+}
+
 mha_status check_heads(int B, int h, int h_kv, int N, int max_new) {
     if (B < 0 || h < 0 || h_kv < 0 || N < 0 || max_new < 0) return MHA_ERR_INVALID_ARG;
     if (h > 0 && (h_kv == 0 || h % h_kv != 0)) return MHA_ERR_INVALID_ARG;
@@ -180,7 +190,8 @@ MHA_EXPORT size_t sdpa_paged_workspace_bytes(const mha_paged_cache *cache, int h
     // (sizes alone: the pointers may be missing)
     if (!cache || check_sizes(cache, kAttnHeadDim, N, c) != MHA_OK || check_heads(c.B, h, c.Hkv, N, max_new) != MHA_OK) return 0;
     if (c.B == 0 || h == 0 || N == 0 || max_new == 0) return 0;
-    return layout(c, h / c.Hkv, max_new).bytes;
+    const Layout l = layout(c, h / c.Hkv, max_new);
+    return lines_fit(c, l, h / c.Hkv, max_new) ? l.bytes : 0;
 }
 
 MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const void *q, long long q_stride_h,
@@ -199,14 +210,7 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     if ((s = check_rows(o, o_stride_h, o_stride_t, h, N, out)) != MHA_OK) return s;
     const int g = h / p.c.Hkv;
     const Layout l = layout(p.c, g, max_new);
-    // the work lines' lengths, for whatever lengths and starts the device holds
-    const long long cap = p.c.cap;
-    const int small = paged_small_rows(p.c.int8 != 0);
-    const long long rows = std::min<long long>(static_cast<long long>(std::min(max_new, N)) * g, small);
-    const long long row_tiles = (std::max<long long>(rows, g) + l.tile_rows - 1) / l.tile_rows;
-    if (static_cast<long long>(p.c.B) * p.c.Hkv * row_tiles * (cap / 16 + 1 + kPagedItemPlaces) >= kMostLine) return MHA_ERR_UNSUPPORTED;
-    if (l.tiles && static_cast<long long>(paged_most_tiles(N, p.c.B, g)) * p.c.Hkv * (cap / 128 + 8) >= kMostLine)
-        return MHA_ERR_UNSUPPORTED;
+    if (!lines_fit(p.c, l, g, max_new)) return MHA_ERR_UNSUPPORTED;
     if (l.bytes > 0 && (!workspace || workspace_bytes < l.bytes)) return MHA_ERR_WORKSPACE;
     if (l.bytes > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return MHA_ERR_MISALIGNED;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -217,7 +221,7 @@ MHA_EXPORT mha_status sdpa_paged_forward(const mha_paged_cache *cache, const voi
     p.max_new = std::min(max_new, N);
     p.causal = (mask & MHA_MASK_CAUSAL) ? 1 : 0;
     p.mul = scale * 1.4426950408889634f;
-    p.small_rows = l.tiles ? small : 1 << 30;
+    p.small_rows = l.tiles ? paged_small_rows(p.c.int8 != 0) : 1 << 30;
     p.undivided = l.undivided ? 1 : 0;
     if (!l.undivided) {
         p.part_o = reinterpret_cast<float *>(ws + l.part_o);
