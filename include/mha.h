@@ -460,7 +460,7 @@ typedef struct {
  * Writes new rows into their pages.  k, v (h_kv, N, 64) bf16, packed, at strides (in
  * elements, multiples of 8, at least 64) of the heads and of the tokens: a
  * projection's output is taken as it is, head by head or token by token.
- * 16-byte aligned.  Two rows for the same place (sequences that share the page)
+ * 16-byte aligned.  N < 2^30.  Two rows for the same place (sequences that share the page)
  * leave one of them or a mixture.  One launch, no workspace.
  */
 mha_status paged_cache_append(const mha_paged_cache *cache, const void *k, long long k_stride_h,

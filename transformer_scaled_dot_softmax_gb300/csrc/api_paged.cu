@@ -17,7 +17,7 @@ namespace {
 using namespace mha;
 
 constexpr int kMostPageRows = 1 << 16;
-constexpr long long kMostRows = 1ll << 30;  // of a sequence
+constexpr long long kMostRows = 1ll << 30;  // of a sequence, or packed
 // Units of the kernels' work lines: 32 bits, with room to round up to equal shares.
 constexpr long long kMostLine = (1ll << 31) - (1 << 14);
 
@@ -166,6 +166,7 @@ MHA_EXPORT mha_status paged_cache_append(const mha_paged_cache *cache, const voi
     PagedRows kr, vr;
     mha_status s = check_cache(cache, d, true, N, c);
     if (s != MHA_OK) return s;
+    if (N >= kMostRows) return MHA_ERR_UNSUPPORTED;
     if (N == 0 || c.B == 0 || c.Hkv == 0 || c.max_pages == 0 || c.num_pages == 0) return MHA_OK;
     if ((s = check_rows(k, k_stride_h, k_stride_t, c.Hkv, N, kr)) != MHA_OK) return s;
     if ((s = check_rows(v, v_stride_h, v_stride_t, c.Hkv, N, vr)) != MHA_OK) return s;
