@@ -735,6 +735,10 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, ou
         _check_dev("status", status, torch.int32)
     if max_new is None:
         max_new = n
+    elif max_new < 0:
+        raise ValueError("max_new must not be negative")
+    else:
+        max_new = min(max_new, n)
     size = lib.sdpa_paged_workspace_bytes(cache, h, n, max_new)
     if size or workspace is not None:
         workspace, size = _scratch_here(torch, workspace, size, dev, stream)
