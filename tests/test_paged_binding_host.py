@@ -43,3 +43,16 @@ def test_a_bound_below_zero_is_refused(fakes, most):
     with pytest.raises(ValueError):
         attend(m, max_new=most)
     assert lib.streams == []
+
+
+PAGES = (Strided((9, 2, 16, 64), "bfloat16"), Strided((9, 2, 16, 64), "bfloat16"), Strided((3, 5), "int32"), Strided((3,), "int32"))
+
+
+@pytest.mark.parametrize("kw", [{"k": 5}, {"k": Strided((3, 2), "bfloat16")}, {"k": Strided((3, 2, 80, 64), "float32")},
+                                {"v": 5}, {"v": Strided((3, 2, 81, 64), "bfloat16")}, {"rows": -1},
+                                {"rows": 7, "k": Strided((3, 2, 80, 64), "bfloat16")}])
+def test_results_of_a_read_that_do_not_fit_are_refused(fakes, kw):
+    m, torch, lib = fakes
+    with pytest.raises(ValueError):
+        m.paged_cache_read(*PAGES, **kw)
+    assert lib.streams == [] and not torch.made

@@ -694,16 +694,22 @@ def paged_cache_read(k_pages, v_pages, page_table, seq_lens, k=None, v=None, *, 
     cache, B, h_kv, page_rows, max_pages, d, dev = _paged_cache(torch, k_pages, v_pages, page_table, None, seq_lens, k_scales,
                                                                 v_scales)
     if rows is None:
-        rows = max_pages * page_rows if k is None else k.shape[2]
+        if k is None:
+            rows = max_pages * page_rows
+        else:
+            try:
+                rows = k.shape[2]
+            except (AttributeError, IndexError):
+                raise ValueError("k must be a tensor of four dimensions") from None
+    elif rows < 0:
+        raise ValueError("rows must not be negative")
     shape = (B, h_kv, rows, d)
+    if k is not None or v is not None:
+        _require(("k", "v"), (k, v), torch.bfloat16, shape, dev)
     if k is None:
         k = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
-    else:
-        _require(("k",), (k,), torch.bfloat16, shape, dev)
     if v is None:
         v = _result(stream, torch.empty, shape, dtype=torch.bfloat16, device=dev)
-    else:
-        _require(("v",), (v,), torch.bfloat16, shape, dev)
     rc = lib.paged_cache_read(cache, k.data_ptr(), v.data_ptr(), rows, d, _stream_on(stream, dev))
     if rc != MHA_OK:
         raise MhaError(rc, "paged_cache_read")
