@@ -56,3 +56,36 @@ def test_results_of_a_read_that_do_not_fit_are_refused(fakes, kw):
     with pytest.raises(ValueError):
         m.paged_cache_read(*PAGES, **kw)
     assert lib.streams == [] and not torch.made
+
+
+class Laid(Strided):
+    """With strides of its own."""
+
+    def __init__(self, shape, dtype, strides):
+        super().__init__(shape, dtype)
+        self.strides = strides
+
+    def stride(self):
+        return self.strides
+
+
+# (shape, K's strides, V's): the stride of a dimension of size 1 means nothing, that of pages with one of them neither
+ALIKE = [((1, 2, 16, 64), (2048, 1024, 64, 1), (4096, 1024, 64, 1)), ((9, 1, 16, 64), (1024, 1024, 64, 1), (1024, 77, 64, 1)),
+         ((1, 1, 16, 64), (1024, 1024, 64, 1), (1, 1, 64, 1))]
+UNLIKE = [((9, 2, 16, 64), (2048, 1024, 64, 1), (4096, 1024, 64, 1)), ((1, 2, 16, 64), (2048, 1024, 64, 1), (2048, 2048, 64, 1)),
+          ((9, 1, 16, 64), (1024, 1024, 64, 1), (1024, 1024, 128, 1))]
+
+
+@pytest.mark.parametrize("shape,ks,vs,taken", [(*x, True) for x in ALIKE] + [(*x, False) for x in UNLIKE])
+def test_strides_that_count(fakes, shape, ks, vs, taken):
+    m, torch, lib = fakes
+    h_kv = shape[1]
+    change = dict(k_pages=Laid(shape, "bfloat16", ks), v_pages=Laid(shape, "bfloat16", vs),
+                  k=Strided((h_kv, 7, 64), "bfloat16"), v=Strided((h_kv, 7, 64), "bfloat16"))
+    for name in ("append", "read", "attend"):
+        if taken:
+            paged_calls(m, **change)[name](None)
+        else:
+            with pytest.raises(ValueError):
+                paged_calls(m, **change)[name](None)
+    assert len(lib.streams) == (3 if taken else 0)

@@ -600,6 +600,11 @@ def _packed(torch, name, t, shape, device):
     raise ValueError("%s must be contiguous in its last dimension" % name)
 
 
+def _same_places(shape, strides, others):
+    """Equal strides, but for dimensions of one element, whose strides mean nothing."""
+    return all(n <= 1 or x == y for n, x, y in zip(shape, strides, others))
+
+
 def _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_scales, v_scales):
     """Checked (mha_paged_cache as bytes, B, h_kv, page rows, max_pages, head size,
     device index)."""
@@ -610,7 +615,7 @@ def _paged_cache(torch, k_pages, v_pages, page_table, row_starts, seq_lens, k_sc
         strides, dtype = k_pages.stride(), k_pages.dtype
         B, max_pages = page_table.shape
         fine = (k_pages.get_device() == device and v_pages.get_device() == device and v_pages.dtype is dtype
-                and v_pages.shape == shape and v_pages.stride() == strides
+                and v_pages.shape == shape and (v_pages.stride() == strides or _same_places(shape, strides, v_pages.stride()))
                 and page_table.dtype is int32 and page_table.get_device() == device and page_table.is_contiguous()
                 and seq_lens.dtype is int32 and seq_lens.shape == (B,) and seq_lens.get_device() == device
                 and seq_lens.is_contiguous())
@@ -647,7 +652,8 @@ def _refuse_paged(torch, k_pages, v_pages, page_table, seq_lens, device):
             raise ValueError("%s must be a tensor on cuda:%d, the current device" % (name, device))
         if t.dim() != dims:
             raise ValueError("%s must have %d dimensions" % (name, dims))
-    if v_pages.dtype is not k_pages.dtype or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+    if (v_pages.dtype is not k_pages.dtype or v_pages.shape != k_pages.shape
+            or not _same_places(k_pages.shape, k_pages.stride(), v_pages.stride())):
         raise ValueError("v_pages must have k_pages' dtype, shape and strides")
     for name, t in (("page_table", page_table), ("seq_lens", seq_lens)):
         _check_dev(name, t, torch.int32)
