@@ -20,7 +20,7 @@ struct PagedSeq {
 __device__ __forceinline__ PagedSeq paged_seq(const PagedCache &c, int b) {
     PagedSeq s;
     s.row0 = min(max(c.starts[b], 0), c.N);
-    s.n = max(min(c.starts[b + 1], c.N) - s.row0, 0);
+    s.n = max(min(max(c.starts[b + 1], 0), c.N) - s.row0, 0);  // (the least int less row0 would wrap)
     s.len = min(max(c.lens[b], 0), c.cap);
     return s;
 }
