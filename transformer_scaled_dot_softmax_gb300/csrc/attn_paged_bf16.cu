@@ -183,6 +183,14 @@ __device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Shar
 // accumulators' handing on.
 __device__ __forceinline__ int tile_of(const Piece &w, int t) { return w.j0 + w.n_kv - 1 - t; }
 
+// Key tiles that are summed in tensor memory without a break: a longer piece goes through
+// the pipeline in runs of so many, whose sums are joined outside it.  The tensor cores'
+// accumulators drop, towards zero, what lies below a sum's last places when it is added:
+// values of one sign averaged over 2^20 rows came out 0.4 % too small in one run, over 2^26
+// 18 %; in runs of 2,048 / 1,024 / 512 tiles 2.5e-4 / 8e-5 / 2e-5, whatever the length
+// (a head's prompt of 131,072 takes 1 % longer than without).
+constexpr int kRunTiles = 1024;
+
 template <bool kInt8>
 __device__ __forceinline__ const Piece &piece_of(Smem<kInt8> &sm, const PagedAttnParams &p, const Share &sh, int t) {
     if (t < kTable) return sm.table[t];
@@ -351,47 +359,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kInt8 && lane < STAGES) sm.bad[lane] = 0;
         for (int t = 0; ok && t < pieces; ++t) {
             const Piece &w = piece_of<kInt8>(sm, p, sh, t);
-            const int n_kv = w.n_kv, head = w.head, qbuf = v & 1;
-            if (v >= 2 && !(ok = warp_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&sm.q_full[qbuf], static_cast<uint32_t>(tt * g) * (HD * 2));
-                if (in_bounds(w.head * g < p.H && w.row0 < p.c.N, p.status))
-                    tma_load_3d(&maps.q, &sm.q_full[qbuf], sm.q[qbuf], 0, w.head * g, w.row0);
-            }
-            __syncwarp();
-            ++v;
-            for (int jt = 0; jt < n_kv; ++jt, ++n) {
-                bx.next(p, w, jt, lane);
-                uint64_t *full = kInt8 ? raw_full(sm, st) : &sm.kv_full[st], *empty = kInt8 ? raw_empty(sm, st) : &sm.kv_empty[st];
-                uint8_t *k = kInt8 ? raw_k(sm, st) : sm.k[st], *vv = kInt8 ? raw_v(sm, st) : sm.v[st];
-                uint32_t bytes = 2 * (kInt8 ? kRawBytes : kTileBytes);
-                if constexpr (kInt8) {
-                    const bool there = lane >= bx.at && lane < bx.at + bx.boxes && bx.page < bx.none;
-                    bytes += 2u * bx.box * __popc(__ballot_sync(0xffffffffu, there));
+            const int n_kv = w.n_kv, head = w.head;
+            for (int jt = 0; ok && jt < n_kv;) {
+                const int qbuf = v & 1, run_end = min(jt + kRunTiles, n_kv);
+                if (v >= 2 && !(ok = warp_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.q_full[qbuf], static_cast<uint32_t>(tt * g) * (HD * 2));
+                    if (in_bounds(w.head * g < p.H && w.row0 < p.c.N, p.status))
+                        tma_load_3d(&maps.q, &sm.q_full[qbuf], sm.q[qbuf], 0, w.head * g, w.row0);
                 }
-                if (n >= kRing && !(ok = warp_wait(empty, par, ab))) break;
-                if (bx.any_gone || marked || kInt8) {
-                    marked = true;
-                    const uint32_t bad = bx.bad(lane);
-                    if (lane == 0) *(kInt8 ? raw_bad(sm, st) : &sm.bad[st]) = bad;
-                    __syncwarp();
-                }
-                warp_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                ++v;
+                for (; jt < run_end; ++jt, ++n) {
+                    bx.next(p, w, jt, lane);
+                    uint64_t *full = kInt8 ? raw_full(sm, st) : &sm.kv_full[st], *empty = kInt8 ? raw_empty(sm, st) : &sm.kv_empty[st];
+                    uint8_t *k = kInt8 ? raw_k(sm, st) : sm.k[st], *vv = kInt8 ? raw_v(sm, st) : sm.v[st];
+                    uint32_t bytes = 2 * (kInt8 ? kRawBytes : kTileBytes);
+                    if constexpr (kInt8) {
+                        const bool there = lane >= bx.at && lane < bx.at + bx.boxes && bx.page < bx.none;
+                        bytes += 2u * bx.box * __popc(__ballot_sync(0xffffffffu, there));
+                    }
+                    if (n >= kRing && !(ok = warp_wait(empty, par, ab))) break;
+                    if (bx.any_gone || marked || kInt8) {
+                        marked = true;
+                        const uint32_t bad = bx.bad(lane);
+                        if (lane == 0) *(kInt8 ? raw_bad(sm, st) : &sm.bad[st]) = bad;
+                        __syncwarp();
+                    }
+                    warp_arrive_expect_tx(full, bytes);
 #pragma unroll 1
-                for (int i = 0; i < bx.boxes; ++i) {
-                    const int pg = __shfl_sync(0xffffffffu, bx.page, bx.at + i), in = __shfl_sync(0xffffffffu, bx.in_page, bx.at + i);
-                    warp_tma_load_4d(&maps.k, full, k + i * box_bytes, 0, in, head, pg);
-                    warp_tma_load_4d(&maps.v, full, vv + i * box_bytes, 0, in, head, pg);
-                    if constexpr (kInt8)
-                        if (pg < bx.none) {
-                            const long long from = (static_cast<long long>(pg) * p.c.Hkv + head) * p.c.page + in;
-                            warp_bulk_load_1d(sm.raw.ks[st] + i * bx.box, p.c.k_scales + from, bx.box, full);
-                            warp_bulk_load_1d(sm.raw.vs[st] + i * bx.box, p.c.v_scales + from, bx.box, full);
-                        }
-                }
-                if (++st == kRing) {
-                    st = 0;
-                    par ^= 1u;
+                    for (int i = 0; i < bx.boxes; ++i) {
+                        const int pg = __shfl_sync(0xffffffffu, bx.page, bx.at + i), in = __shfl_sync(0xffffffffu, bx.in_page, bx.at + i);
+                        warp_tma_load_4d(&maps.k, full, k + i * box_bytes, 0, in, head, pg);
+                        warp_tma_load_4d(&maps.v, full, vv + i * box_bytes, 0, in, head, pg);
+                        if constexpr (kInt8)
+                            if (pg < bx.none) {
+                                const long long from = (static_cast<long long>(pg) * p.c.Hkv + head) * p.c.page + in;
+                                warp_bulk_load_1d(sm.raw.ks[st] + i * bx.box, p.c.k_scales + from, bx.box, full);
+                                warp_bulk_load_1d(sm.raw.vs[st] + i * bx.box, p.c.v_scales + from, bx.box, full);
+                            }
+                    }
+                    if (++st == kRing) {
+                        st = 0;
+                        par ^= 1u;
+                    }
                 }
             }
         }
@@ -411,27 +422,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = 0; ok && t < pieces; ++t) {
             const int n_kv = piece_of<kInt8>(sm, p, sh, t).n_kv;
-            const int qbuf = v & 1;
-            if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
-            const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
-            for (int jt = 0; jt < n_kv; ++jt, ++n) {
-                const int st = n % STAGES, sb = n % kSBufs;
-                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
-                if (n >= kSBufs) {
-                    const int np = n - kSBufs;
-                    if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
-                const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
+            for (int jt = 0; ok && jt < n_kv;) {
+                const int qbuf = v & 1, run_end = min(jt + kRunTiles, n_kv);
+                if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
+                const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
+                for (; jt < run_end; ++jt, ++n) {
+                    const int st = n % STAGES, sb = n % kSBufs;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                    if (n >= kSBufs) {
+                        const int np = n - kSBufs;
+                        if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
-                warp_commit(&sm.s_full[sb]);
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
+                    warp_commit(&sm.s_full[sb]);
+                }
+                if (!ok) break;
+                warp_commit(&sm.q_empty[qbuf]);
+                ++v;
             }
-            if (!ok) break;
-            warp_commit(&sm.q_empty[qbuf]);
-            ++v;
         }
         warp_commit(&sm.drain[0]);
         mbar_wait_drain(&sm.drain[0], 0);
@@ -446,39 +459,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int t = 0; ok && t < pieces; ++t) {
             const Piece &w = piece_of<kInt8>(sm, p, sh, t);
-            if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
-            for (int jt = 0; jt < w.n_kv; ++jt, ++n) {
-                if ((n & 1) != hf) continue;
-                const int st = n % STAGES, sb = n % kSBufs;
-                const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
-                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
-                // Rows of the last page past the length: their weights are 0, and
-                // 0 times whatever the page holds has to be 0.
-                const int rows = w.len - tile_of(w, jt) * BN;
-                if (!kInt8 && rows < BN) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
-                    for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
-                const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
+            for (int run = 0; ok && run < w.n_kv; run += kRunTiles) {
+                if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
+                const int n_kv = min(w.n_kv - run, kRunTiles);
+                for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                    if ((n & 1) != hf) continue;
+                    const int st = n % STAGES, sb = n % kSBufs;
+                    const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                    // Rows of the last page past the length: their weights are 0, and
+                    // 0 times whatever the page holds has to be 0.
+                    const int rows = w.len - tile_of(w, run + jt) * BN;
+                    if (!kInt8 && rows < BN) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
+                        for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                for (int rd = 0; rd < 2; ++rd) {
-                    if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
-                    tc_fence_after_sync();
+                    for (int rd = 0; rd < 2; ++rd) {
+                        if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
+                        tc_fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        warp_mma_bf16_ts(d_o, a + 32u * rd + 8u * kk, vd + 128 * (4 * rd + kk), idesc_o,
-                                         jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u);
-                    if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                        for (int kk = 0; kk < 4; ++kk)
+                            warp_mma_bf16_ts(d_o, a + 32u * rd + 8u * kk, vd + 128 * (4 * rd + kk), idesc_o,
+                                             jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u);
+                        if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                    }
+                    if (!ok) break;
+                    warp_commit(&sm.kv_empty[st]);
                 }
                 if (!ok) break;
-                warp_commit(&sm.kv_empty[st]);
+                warp_commit(&sm.o_final);
+                ++v;
             }
-            if (!ok) break;
-            warp_commit(&sm.o_final);
-            ++v;
         }
         warp_commit(&sm.drain[1 + hf]);
         mbar_wait_drain(&sm.drain[1 + hf], 0);
@@ -513,199 +529,202 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_live = __any_sync(0xffffffffu, live);
             // keys below it are seen; rows that are none hold nothing up
             const int lim = !live ? 0x7fffffff : p.causal ? min(max(w.pos0 + token + 1, 0), w.len) : w.len;
-            float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
-            float l_run = 0.f;
+            const int full_hi = w.full_hi;
+            for (int run = 0; ok && run < w.n_kv; run += kRunTiles) {
+                float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
+                float l_run = 0.f;
 
-            const int n_kv = w.n_kv, j0 = w.j0, full_hi = w.full_hi;
-            const int n0 = n;
-            auto step = [&]() {
-                sb += 2;
-                if (sb >= kSBufs) {
-                    sb -= kSBufs;
-                    s_par ^= 1;
-                }
-                st += 2;
-                if (st >= STAGES) st -= STAGES;
-            };
-            for (int jt = (n0 ^ half) & 1; jt < n_kv; jt += 2, step()) {
-                n = n0 + jt;
-                const int j = j0 + n_kv - 1 - jt;
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], s_par, ab));
-                if (!ok) break;
-                if (!warp_live) {
-                    // P of the warp's rows stays whatever it is: a row of
-                    // tensor memory only reaches its own row of O
-                    if (lane == 0) {
-                        mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
-                        mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                const int n_kv = min(w.n_kv - run, kRunTiles), j_last = w.j0 + w.n_kv - 1 - run;
+                const int n0 = n;
+                auto step = [&]() {
+                    sb += 2;
+                    if (sb >= kSBufs) {
+                        sb -= kSBufs;
+                        s_par ^= 1;
                     }
-                    continue;
-                }
-                tc_fence_after_sync();
-                const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
-                // (written before the tile was handed to the S issuer, which waited
-                // for that before it issued the products whose end s_full tells)
-                const uint32_t bad = *static_cast<volatile uint32_t *>(&sm.bad[st]);
-                const bool edge = j * BN + BN > full_hi || bad != 0;
-                int rd_first = 0;
-                if (!edge) {
+                    st += 2;
+                    if (st >= STAGES) st -= STAGES;
+                };
+                for (int jt = (n0 ^ half) & 1; jt < n_kv; jt += 2, step()) {
+                    n = n0 + jt;
+                    const int j = j_last - jt;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], s_par, ab));
+                    if (!ok) break;
+                    if (!warp_live) {
+                        // P of the warp's rows stays whatever it is: a row of
+                        // tensor memory only reaches its own row of O
+                        if (lane == 0) {
+                            mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
+                            mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                        }
+                        continue;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                    // (written before the tile was handed to the S issuer, which waited
+                    // for that before it issued the products whose end s_full tells)
+                    const uint32_t bad = *static_cast<volatile uint32_t *>(&sm.bad[st]);
+                    const bool edge = j * BN + BN > full_hi || bad != 0;
+                    int rd_first = 0;
+                    if (!edge) {
 #pragma unroll
-                    for (int rd = 0; rd < 2; ++rd) {
-                        uint32_t s0[32], s1[32], pk[32];
-                        tmem_ld32(ts + 64u * rd, s0);
-                        tmem_ld32(ts + 64u * rd + 32u, s1);
-                        tmem_ld_wait(s0);
-                        reg_fence32(s1);
-                        const float ref = m_run == -INFINITY ? 0.f : m_run;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                        weights(s0, ref, pk, sum);
-                        weights(s1, ref, pk + 16, sum);
-                        const float lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        // a reference has to move: to the rounds below
-                        if (__any_sync(0xffffffffu, live && !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
-                        if (m_run == -INFINITY) m_run = 0.f;
-                        tmem_st32(ts + 32u * rd, pk);
-                        l_run += lt;
+                        for (int rd = 0; rd < 2; ++rd) {
+                            uint32_t s0[32], s1[32], pk[32];
+                            tmem_ld32(ts + 64u * rd, s0);
+                            tmem_ld32(ts + 64u * rd + 32u, s1);
+                            tmem_ld_wait(s0);
+                            reg_fence32(s1);
+                            const float ref = m_run == -INFINITY ? 0.f : m_run;
+                            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                            weights(s0, ref, pk, sum);
+                            weights(s1, ref, pk + 16, sum);
+                            const float lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                            // a reference has to move: to the rounds below
+                            if (__any_sync(0xffffffffu, live && !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
+                            if (m_run == -INFINITY) m_run = 0.f;
+                            tmem_st32(ts + 32u * rd, pk);
+                            l_run += lt;
+                            tmem_st_wait();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                            rd_first = rd + 1;
+                        }
+                    }
+#pragma unroll 1
+                    for (int rd = rd_first; rd < 2; ++rd) {
+                        const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
+                        const int key0 = j * BN + 64 * rd;  // the round's first key
+                        const uint32_t gone = bad >> (4 * rd) & 15u;
+                        // Does the row need the exact step after a sum against
+                        // the reference in hand (0 before there is one)?
+                        auto must_move = [&](float sum, bool none) -> bool {
+                            if (none || !live) return false;
+                            if (m_run != -INFINITY) return !(sum <= kSumMax);
+                            if (!(sum >= kSumMin && sum <= kSumMax)) return true;
+                            m_run = 0.f;
+                            return false;
+                        };
+                        // 32 keys at a time.
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const int kh = key0 + 32 * h;
+                            const uint32_t two = gone >> (2 * h) & 3u;
+                            const int hi = min(lim - kh, 32);
+                            // the keys seen, a bit each
+                            unsigned bits = hi <= 0 ? 0u : 0xffffffffu >> (32 - hi);
+                            if (two & 1u) bits &= 0xffff0000u;
+                            if (two & 2u) bits &= 0x0000ffffu;
+                            const bool none = bits == 0u;
+                            const uint32_t tp = ts + 32u * static_cast<uint32_t>(rd);
+                            uint32_t pk[16];
+                            float lt = 0.f, alpha = 1.f;
+                            if (__all_sync(0xffffffffu, none || !live)) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) pk[c] = 0u;
+                            } else {
+                                const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
+                                bool need = false;
+                                // attempt 0 against the reference in hand; where a
+                                // row needs the exact step, 1 moves its reference
+                                // and 2 takes the keys again
+#pragma unroll 1
+                                for (int attempt = 0;; ++attempt) {
+                                    uint32_t y[32];
+                                    tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
+                                    tmem_ld_wait(y);
+                                    const float ref = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) y[c] = __float_as_uint(fmaf(__uint_as_float(y[c]), p.mul, -ref));
+                                    if (!all) {
+#pragma unroll
+                                        for (int c = 0; c < 32; ++c)
+                                            if (!(bits >> c & 1u)) y[c] = __float_as_uint(-INFINITY);
+                                    }
+                                    if (attempt == 1) {
+                                        if (need) {
+                                            float up = -INFINITY;  // above the reference
+#pragma unroll
+                                            for (int c = 0; c < 32; c += 2)
+                                                up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                            up = ceilf(up);
+                                            if (m_run == -INFINITY) {
+                                                m_run = up;
+                                            } else if (up > 0.f) {
+                                                m_run += up;
+                                                alpha = ex2_approx(-up);
+                                                l_run *= alpha;
+                                            }
+                                        }
+                                        continue;
+                                    }
+                                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) {
+                                        pk[c] = pack_bf16x2(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])));
+                                        add_bf16x2_to_f32(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], pk[c]);
+                                    }
+                                    lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                                    if (attempt == 2) break;
+                                    need = must_move(lt, none);
+                                    if (!__any_sync(0xffffffffu, need)) break;
+                                }
+                            }
+                            tmem_st16(tp + 16u * static_cast<uint32_t>(h), pk);
+                            l_run += lt;
+                            if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
+                            // What was summed before moves with the reference: the
+                            // round's first 32 weights, which wait to be multiplied
+                            // with these, and O_h, which holds the group's earlier
+                            // tiles of the piece and, in round 1, this tile's round
+                            // 0: wait for the last product it took.
+                            if (h == 1) {
+                                tmem_st_wait();
+                                tmem_ld16(tp, pk);
+                                tmem_ld_wait(pk);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
+                                                        __uint_as_float(pk[c] & 0xffff0000u) * alpha);
+                                tmem_st16(tp, pk);
+                            }
+                            if (rd == 1) {
+                                ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
+                            } else if (jt >= 2) {
+                                const int np = n - 2;
+                                ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
+                            } else {
+                                continue;  // O_h holds nothing of this piece
+                            }
+                            if (!ok) break;
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t o0[32];
+                                tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                                tmem_ld_wait(o0);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
+                                tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                            }
+                        }
+                        if (!ok) break;
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
-                        rd_first = rd + 1;
-                    }
-                }
-#pragma unroll 1
-                for (int rd = rd_first; rd < 2; ++rd) {
-                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
-                    const int key0 = j * BN + 64 * rd;  // the round's first key
-                    const uint32_t gone = bad >> (4 * rd) & 15u;
-                    // Does the row need the exact step after a sum against
-                    // the reference in hand (0 before there is one)?
-                    auto must_move = [&](float sum, bool none) -> bool {
-                        if (none || !live) return false;
-                        if (m_run != -INFINITY) return !(sum <= kSumMax);
-                        if (!(sum >= kSumMin && sum <= kSumMax)) return true;
-                        m_run = 0.f;
-                        return false;
-                    };
-                    // 32 keys at a time.
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const int kh = key0 + 32 * h;
-                        const uint32_t two = gone >> (2 * h) & 3u;
-                        const int hi = min(lim - kh, 32);
-                        // the keys seen, a bit each
-                        unsigned bits = hi <= 0 ? 0u : 0xffffffffu >> (32 - hi);
-                        if (two & 1u) bits &= 0xffff0000u;
-                        if (two & 2u) bits &= 0x0000ffffu;
-                        const bool none = bits == 0u;
-                        const uint32_t tp = ts + 32u * static_cast<uint32_t>(rd);
-                        uint32_t pk[16];
-                        float lt = 0.f, alpha = 1.f;
-                        if (__all_sync(0xffffffffu, none || !live)) {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) pk[c] = 0u;
-                        } else {
-                            const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
-                            bool need = false;
-                            // attempt 0 against the reference in hand; where a
-                            // row needs the exact step, 1 moves its reference
-                            // and 2 takes the keys again
-#pragma unroll 1
-                            for (int attempt = 0;; ++attempt) {
-                                uint32_t y[32];
-                                tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
-                                tmem_ld_wait(y);
-                                const float ref = m_run == -INFINITY ? 0.f : m_run;
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) y[c] = __float_as_uint(fmaf(__uint_as_float(y[c]), p.mul, -ref));
-                                if (!all) {
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c)
-                                        if (!(bits >> c & 1u)) y[c] = __float_as_uint(-INFINITY);
-                                }
-                                if (attempt == 1) {
-                                    if (need) {
-                                        float up = -INFINITY;  // above the reference
-#pragma unroll
-                                        for (int c = 0; c < 32; c += 2)
-                                            up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-                                        up = ceilf(up);
-                                        if (m_run == -INFINITY) {
-                                            m_run = up;
-                                        } else if (up > 0.f) {
-                                            m_run += up;
-                                            alpha = ex2_approx(-up);
-                                            l_run *= alpha;
-                                        }
-                                    }
-                                    continue;
-                                }
-                                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    pk[c] = pack_bf16x2(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])));
-                                    add_bf16x2_to_f32(sum[2 * (c & 1)], sum[2 * (c & 1) + 1], pk[c]);
-                                }
-                                lt = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                                if (attempt == 2) break;
-                                need = must_move(lt, none);
-                                if (!__any_sync(0xffffffffu, need)) break;
-                            }
-                        }
-                        tmem_st16(tp + 16u * static_cast<uint32_t>(h), pk);
-                        l_run += lt;
-                        if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
-                        // What was summed before moves with the reference: the
-                        // round's first 32 weights, which wait to be multiplied
-                        // with these, and O_h, which holds the group's earlier
-                        // tiles of the piece and, in round 1, this tile's round
-                        // 0: wait for the last product it took.
-                        if (h == 1) {
-                            tmem_st_wait();
-                            tmem_ld16(tp, pk);
-                            tmem_ld_wait(pk);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
-                                                    __uint_as_float(pk[c] & 0xffff0000u) * alpha);
-                            tmem_st16(tp, pk);
-                        }
-                        if (rd == 1) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
-                        } else if (jt >= 2) {
-                            const int np = n - 2;
-                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
-                        } else {
-                            continue;  // O_h holds nothing of this piece
-                        }
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int part = 0; part < 2; ++part) {
-                            uint32_t o0[32];
-                            tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
-                            tmem_ld_wait(o0);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
-                            tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
-                        }
                     }
                     if (!ok) break;
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
                 }
                 if (!ok) break;
+                n = n0 + n_kv;
+                if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
+                sm.red_m[half][r] = m_run;
+                sm.red_l[half][r] = l_run;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ml_full);
+                ++v;
             }
-            if (!ok) break;
-            n = n0 + n_kv;
-            if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
-            sm.red_m[half][r] = m_run;
-            sm.red_l[half][r] = l_run;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ml_full);
-            ++v;
         }
         if (!ok) tmem_st_wait();
     } else {
@@ -722,9 +741,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 j = PagedJoin{w.tokens * g, 0, w.head, w.row0, first / sh.share, (first + n - 1) / sh.share};
             p.tile_join[cta] = j;
         }
-        // The v-th piece's rows, once its products are complete.
-        auto output = [&](int v) -> bool {
-            const Piece &w = piece_of<kInt8>(sm, p, sh, v);
+        // The next run's rows (the v-th of all), once its products are complete: tiles
+        // `run` to run + kRunTiles - 1 of piece `t`.  What a piece's runs before have summed
+        // waits in its slot.
+        int v = 0, t = 0, run = 0;
+        auto output = [&]() -> bool {
+            const Piece &w = piece_of<kInt8>(sm, p, sh, t);
+            const bool first = run == 0, last = run + kRunTiles >= w.n_kv, whole = w.whole && last;
             const int token = r / g, h = w.head * g + r - token * g;
             const bool live = token < w.tokens && in_bounds(h < p.H && w.row0 + token < p.c.N, p.status);
             if (!__all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab))) return false;
@@ -739,12 +762,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
             const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
             const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;
-            const float L = la * wa + lb * wb;
-            const float inv = !w.whole ? 1.f : L != 0.f ? 1.0f / L : 0.f;
-            const float fa = wa * inv, fb = wb * inv;
+            float L = la * wa + lb * wb, f = 1.f, keep = 0.f;
             const long long slot = (2ll * cta + (w.j0 > 0 ? 0 : 1)) * BM + r;
             // (the reference of a NaN is as good as any, if the merge takes it)
-            if (live && !w.whole) p.tile_ml[slot] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
+            float top = L > 0.f ? M : L == 0.f ? -INFINITY : 0.f;
+            if (live && !first) {
+                const float2 before = p.tile_ml[slot];
+                const float m = top;
+                top = fmaxf(before.x, m);
+                f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                keep = before.x == -INFINITY ? 0.f : ex2_approx(before.x - top);
+                L = L * f + before.y * keep;
+            }
+            if (whole) {
+                const float inv = L != 0.f ? 1.0f / L : 0.f;
+                f *= inv;
+                keep *= inv;
+            }
+            const float fa = wa * f, fb = wb * f;
+            if (live && !whole) p.tile_ml[slot] = make_float2(top, L);
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
                 uint32_t oa[32], ob[32];
@@ -763,10 +799,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 32; ++c)
                     oa[c] = __float_as_uint((la != 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
                                             (lb != 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
-                if (!w.whole) {
-                    uint4 *d4 = reinterpret_cast<uint4 *>(p.tile_o + slot * HD) + 8 * part;
+                uint4 *sum = reinterpret_cast<uint4 *>(p.tile_o + slot * HD) + 8 * part;
+                if (!first) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) d4[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 x = sum[c];
+                        oa[4 * c] = __float_as_uint(fmaf(__uint_as_float(x.x), keep, __uint_as_float(oa[4 * c])));
+                        oa[4 * c + 1] = __float_as_uint(fmaf(__uint_as_float(x.y), keep, __uint_as_float(oa[4 * c + 1])));
+                        oa[4 * c + 2] = __float_as_uint(fmaf(__uint_as_float(x.z), keep, __uint_as_float(oa[4 * c + 2])));
+                        oa[4 * c + 3] = __float_as_uint(fmaf(__uint_as_float(x.w), keep, __uint_as_float(oa[4 * c + 3])));
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) sum[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
                 } else {
                     uint4 *d4 = reinterpret_cast<uint4 *>(p.o + h * p.o_stride_h + (w.row0 + token) * p.o_stride_t) + 4 * part;
                     uint32_t pk[16];
@@ -777,15 +823,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) d4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
                 }
             }
+            ++v;
+            run += kRunTiles;
+            if (last) {
+                run = 0;
+                ++t;
+            }
             return true;
         };
-        // int8: pieces are put out as their products are complete, K and V of tile
-        // after tile written as stages come free.  Behind a piece's last tile it may
-        // be a stage that only products after that piece's output give back:
+        // int8: runs are put out as their products are complete, K and V of tile
+        // after tile written as stages come free.  Behind a run's last tile it may
+        // be a stage that only products after that run's output give back:
         // whichever comes first.  (One place in the code for each: all roles' loops
         // together have to stay in the instruction cache, 32 KB or so; with three
         // copies of output() here a causal prompt took 392 us instead of 290.)
-        auto put_first = [&](int v, uint64_t *bar, uint32_t parity, bool &ok) -> bool {
+        auto put_first = [&](uint64_t *bar, uint32_t parity, bool &ok) -> bool {
             const long long since = clock64();
             while (true) {
                 if (__all_sync(0xffffffffu, mbar_test(&sm.o_final, static_cast<uint32_t>(v & 1)))) return true;
@@ -802,16 +854,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         if constexpr (!kInt8) {
-            for (int v = 0; v < pieces; ++v)
-                if (!output(v)) break;
+            while (t < pieces && output()) {
+            }
         } else {
             const int tid = threadIdx.x - 32 * kOutWarp;
             const int row0 = tid >> 2, quarter = tid & 3;  // rows tid / 4 + 32 i of a tile, a quarter of each
-            int v = 0, piece = 0, jt = 0, st = 0, rs = 0;
+            int runs = 0, piece = 0, jt = 0, st = 0, rs = 0;  // runs: whose tiles are all written
             uint32_t st_par = 1, rs_par = 0;
             int n_kv = 0, keys = 0;
             bool fill = true, ok = true;  // fill: the ring's first round, nothing to wait for
-            while (ok && (piece < pieces || v < pieces)) {
+            while (ok && (piece < pieces || v < runs)) {
                 bool put = piece == pieces;
                 if (!put && jt == 0) {
                     const Piece &w = piece_of<true>(sm, p, sh, piece);
@@ -819,12 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     keys = w.len - (w.j0 + n_kv - 1) * BN;  // of the tile; rows past them are cleared
                 }
                 if (!put && !fill) {
-                    if (v < piece) put = put_first(v, &sm.kv_empty[st], st_par, ok);
+                    if (v < runs) put = put_first(&sm.kv_empty[st], st_par, ok);
                     if (ok && !put) ok = warp_wait(&sm.kv_empty[st], st_par, ab);
                     if (!ok) break;
                 }
                 if (put) {
-                    ok = output(v++);
+                    ok = output();
                     continue;
                 }
                 // (raw tiles wait for nothing but these warps)
@@ -873,7 +925,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rs_par ^= 1u;
                 }
                 keys += BN;
-                if (++jt == n_kv) {
+                ++jt;
+                if (jt == n_kv || jt % kRunTiles == 0) ++runs;
+                if (jt == n_kv) {
                     jt = 0;
                     ++piece;
                 }
