@@ -93,3 +93,66 @@ def test_a_key_far_ahead_in_another_run(lib, int8):
         want = c.cached(0)[1][0, at]
         # the others have 2^-40 each, 2^-21.9 together
         assert (out.double() - want).abs().max() <= ref.U * want.abs().max() + 2.0 ** -20
+
+
+# Few query rows: a warp's own sum is as long only where the batch's rows are many times those that fit a GPU: pages of 4,096
+# rows that sequences share.
+def shared(c, q, table, lens, scale):
+    """(o, bound) of single tokens q (h, B, 64), from what the pages hold and how often each row counts."""
+    g = q.shape[0] // c.h_kv
+    k, v = (torch.stack([c.cached(b)[i] for b in range(c.B)]).transpose(0, 1).reshape(c.h_kv, -1, 64).repeat_interleave(g, 0)
+            for i in range(2))
+    which = torch.empty(c.pages, dtype=torch.long, device="cuda")
+    which[c.page_table[:, 0].long()] = torch.arange(c.B, device="cuda")
+    times = torch.zeros(q.shape[1], c.B, c.page, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        whole, rest = divmod(n, c.page)
+        times[b] = torch.bincount(which[table[b, :whole].long()], minlength=c.B).double()[:, None]
+        if rest:
+            times[b, which[table[b, whole].long()], :rest] += 1
+    s = q.double() @ k.transpose(1, 2) * scale
+    times = times.reshape(len(lens), -1)
+    w = torch.where(times > 0, torch.exp(s - torch.where(times > 0, s, -math.inf).amax(-1, keepdim=True)), 0.0) * times
+    w = w / w.sum(-1, keepdim=True)
+    e = 2 * ref.score_error(None, abs(scale) * (q.double().abs() @ k.abs().transpose(1, 2))).amax(-1, keepdim=True)
+    o = w @ v
+    return o, (ref.U + e) * (w @ v.abs() + o.abs()) + ref.U * o.abs() + 2.0 ** -51 * v.abs().max()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("g", [1, 9, 20])
+def test_single_tokens_over_many_rows_of_one_sign(lib, int8, g):
+    if g == 20 and not int8:
+        g = 16
+    B, h_kv, length, page = 64, 16, (1 << 22) + 1000, 4096
+    c = pr.Cache(h_kv, page, [page], [0], int8=int8, seed=64, spare=0)
+    c.rows = [(c.rows[0][0], (torch.rand(h_kv, page, 64, generator=c.g, device="cuda") / 2 + 0.5).to(BF))]
+    c.fill()
+    q = torch.randn(g * h_kv, B, 64, generator=c.g, device="cuda").to(BF)
+    table = torch.zeros(B, length // page + 1, dtype=torch.int32, device="cuda")
+    out = lib.sdpa_paged_forward(q, c.k_pages, c.v_pages, table, torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+                                 ints(*[length] * B), max_new=1, **c.scales)
+    ref.check("o", out, *shared(c, q, table, [length] * B, 0.125), 0)
+    mean = ((out.double() - shared(c, q, table, [length] * B, 0.125)[0]).mean() / 0.75).item()
+    # outputs near 0.75 are rounded to multiples of 2^-8: half a step at most were they all alike
+    assert abs(mean) <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("orders", [["ABC", "BAC", "CAB", "CBA"], ["AAB", "BBA", "BCB", "ACA"]])
+def test_single_tokens_whose_references_differ_between_runs(lib, int8, orders):
+    h_kv, page, h = 16, 4096, 32
+    c = pr.Cache(h_kv, page, [page] * 3, [0] * 3, int8=int8, seed=65, spare=0)
+    g = torch.Generator(device="cuda").manual_seed(65)
+    c.rows = [keys(t * (page // 128), g, (h_kv,)) for t in "ABC"]
+    c.fill()
+    lens = [3 * 400 * page - 7 * b for b in range(4)]
+    table = torch.stack([torch.cat([c.page_table["ABC".index(t), 0].repeat(400) for t in o]) for o in orders]).contiguous()
+    q, starts = rows(g, h, 4), ints(0, 1, 2, 3, 4)
+
+    def call():
+        return lib.sdpa_paged_forward(q, c.k_pages, c.v_pages, table, starts, ints(*lens), max_new=1, scale=SCALE, **c.scales)
+
+    out = call()
+    assert torch.equal(out, call())
+    ref.check("o", out, *shared(c, q, table, lens, SCALE), 0)

@@ -146,6 +146,13 @@ constexpr float kPowerDown = 1.f / static_cast<float>(1ull << kPowerUp);
 // The exponent that it makes of a stored one; 255 (NaN) stays.
 __device__ __forceinline__ uint32_t raised(uint32_t stored) { return min(stored + kPowerUp, 255u); }
 
+// Units of an item that a warp sums in its accumulators without a break, 65,536 keys: then
+// they are added to what lies in shared memory.  (The matrix instructions drop, towards
+// zero, what lies below a sum's last places: 64 x 16 heads over 2^22 rows each, 1.7 million
+// of them a warp, averaged values of one sign to 0.5 % too little.)
+template <bool kInt8>
+constexpr int kRunUnits = (1 << 16) / kUnitKeys<kInt8>;
+
 // One lane's part of a unit's K, or of its V.
 struct Part {
     // K, bf16: keys l/4 and l/4 + 8, two pieces of 8 features; int8: keys l/4 + 8 i,
@@ -526,179 +533,221 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
         }
         least = __reduce_min_sync(0xffffffffu, least);
 
+        int u = u0 + sub;
 #pragma unroll 1
-        for (int u = u0 + sub; u < u1; u += step) {
-            // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
-            float st[kN][kBlocks][4];
+        for (bool carried = false;; carried = true) {
+            const int run_end = min(u1, u + kRunUnits<kInt8> * step);
+#pragma unroll 1
+            for (; u < run_end; u += step) {
+                // scores: key l/4 + 8 j (+ 16 i) of row 2c + r in st[n][i][2 j + r]
+                float st[kN][kBlocks][4];
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                uint32_t ka[2][8];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if constexpr (kInt8) {
-                        const uint4 &w = kp.x[2 * i + j];
-                        to_f16(w.x, ka[j][0], ka[j][1]);
-                        to_f16(w.y, ka[j][2], ka[j][3]);
-                        to_f16(w.z, ka[j][4], ka[j][5]);
-                        to_f16(w.w, ka[j][6], ka[j][7]);
-                    } else {
-                        const uint4 &w = kp.x[2 * j], &z = kp.x[2 * j + 1];
-                        ka[j][0] = w.x, ka[j][1] = w.y, ka[j][2] = w.z, ka[j][3] = w.w;
-                        ka[j][4] = z.x, ka[j][5] = z.y, ka[j][6] = z.z, ka[j][7] = z.w;
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < kN; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) st[n][i][e] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a[4] = {ka[0][2 * k], ka[1][2 * k], ka[0][2 * k + 1], ka[1][2 * k + 1]};
-                        if constexpr (kInt8)
-                            mma_f16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
-                        else
-                            mma_bf16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
-                    }
-                }
-            }
-            int here[kBlocks];  // keys of a block that are there
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i) here[i] = valid[i];
-            const bool whole = full && (u + 1) * kKeys <= least;  // every row sees every key
-            if constexpr (kInt8) {
-#pragma unroll
-                for (int i = 0; i < kBlocks; ++i)
+                for (int i = 0; i < kBlocks; ++i) {
+                    uint32_t ka[2][8];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float power = paged_power(__shfl_sync(0xffffffffu, kp.s, 16 * i + 8 * j + l4));
-#pragma unroll
-                        for (int n = 0; n < kN; ++n) {
-                            st[n][i][2 * j] *= power;
-                            st[n][i][2 * j + 1] *= power;
+                        if constexpr (kInt8) {
+                            const uint4 &w = kp.x[2 * i + j];
+                            to_f16(w.x, ka[j][0], ka[j][1]);
+                            to_f16(w.y, ka[j][2], ka[j][3]);
+                            to_f16(w.z, ka[j][4], ka[j][5]);
+                            to_f16(w.w, ka[j][6], ka[j][7]);
+                        } else {
+                            const uint4 &w = kp.x[2 * j], &z = kp.x[2 * j + 1];
+                            ka[j][0] = w.x, ka[j][1] = w.y, ka[j][2] = w.z, ka[j][3] = w.w;
+                            ka[j][4] = z.x, ka[j][5] = z.y, ka[j][6] = z.z, ka[j][7] = z.w;
                         }
                     }
-            }
-            if (u + step < u1) {
-                place(u + step);
-                load(std::false_type{}, kp);
-            }
-            // Weights against the reference in hand, 0 before there is one.  Masked:
-            // of scores in log2 units.
-            uint32_t pk[kN][kBlocks][2];
-            float sum[kN][2];
-            auto weights = [&](auto is_masked, bool has_ref) -> bool {
-                constexpr bool masked = decltype(is_masked)::value;
-                bool need = !has_ref;
 #pragma unroll
-                for (int n = 0; n < kN; ++n) {
-                    const float r0 = masked && m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = masked && m[n][1] == -INFINITY ? 0.f : m[n][1];
-                    sum[n][0] = sum[n][1] = 0.f;
+                    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) st[n][i][e] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a[4] = {ka[0][2 * k], ka[1][2 * k], ka[0][2 * k + 1], ka[1][2 * k + 1]};
+                            if constexpr (kInt8)
+                                mma_f16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
+                            else
+                                mma_bf16(st[n][i], a, q[n][2 * k], q[n][2 * k + 1]);
+                        }
+                    }
+                }
+                int here[kBlocks];  // keys of a block that are there
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) here[i] = valid[i];
+                const bool whole = full && (u + 1) * kKeys <= least;  // every row sees every key
+                if constexpr (kInt8) {
 #pragma unroll
                     for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float y0 = masked ? st[n][i][2 * j] - r0 : fmaf(st[n][i][2 * j], mul[n][0], -r0);
-                            float y1 = masked ? st[n][i][2 * j + 1] - r1 : fmaf(st[n][i][2 * j + 1], mul[n][1], -r1);
-                            pk[n][i][j] = pack_bf16x2(ex2_approx(y0), ex2_approx(y1));
-                            add_bf16x2_to_f32(sum[n][0], sum[n][1], pk[n][i][j]);
+                            const float power = paged_power(__shfl_sync(0xffffffffu, kp.s, 16 * i + 8 * j + l4));
+#pragma unroll
+                            for (int n = 0; n < kN; ++n) {
+                                st[n][i][2 * j] *= power;
+                                st[n][i][2 * j + 1] *= power;
+                            }
                         }
-                    need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax);
                 }
-                return __any_sync(0xffffffffu, need);
-            };
-            if (!whole || !set || weights(std::false_type{}, true)) {
-                // Scores in log2 units, a key that is not seen at minus infinity;
-                // where a row has no reference yet, or its sum leaves the
-                // range, against the unit's maximum.
+                if (u + step < u1) {
+                    place(u + step);
+                    load(std::false_type{}, kp);
+                }
+                // Weights against the reference in hand, 0 before there is one.  Masked:
+                // of scores in log2 units.
+                uint32_t pk[kN][kBlocks][2];
+                float sum[kN][2];
+                auto weights = [&](auto is_masked, bool has_ref) -> bool {
+                    constexpr bool masked = decltype(is_masked)::value;
+                    bool need = !has_ref;
 #pragma unroll
-                for (int n = 0; n < kN; ++n)
+                    for (int n = 0; n < kN; ++n) {
+                        const float r0 = masked && m[n][0] == -INFINITY ? 0.f : m[n][0];
+                        const float r1 = masked && m[n][1] == -INFINITY ? 0.f : m[n][1];
+                        sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kBlocks; ++i)
+                        for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int in = l4 + 8 * (e >> 1), key = u * kKeys + 16 * i + in;
-                            st[n][i][e] = in < here[i] && key < lim[n][e & 1] ? st[n][i][e] * mul[n][e & 1] : -INFINITY;
-                        }
-                if (weights(std::true_type{}, set)) {
+                            for (int j = 0; j < 2; ++j) {
+                                float y0 = masked ? st[n][i][2 * j] - r0 : fmaf(st[n][i][2 * j], mul[n][0], -r0);
+                                float y1 = masked ? st[n][i][2 * j + 1] - r1 : fmaf(st[n][i][2 * j + 1], mul[n][1], -r1);
+                                pk[n][i][j] = pack_bf16x2(ex2_approx(y0), ex2_approx(y1));
+                                add_bf16x2_to_f32(sum[n][0], sum[n][1], pk[n][i][j]);
+                            }
+                        need |= !(sum[n][0] <= kSumMax) || !(sum[n][1] <= kSumMax);
+                    }
+                    return __any_sync(0xffffffffu, need);
+                };
+                if (!whole || !set || weights(std::false_type{}, true)) {
+                    // Scores in log2 units, a key that is not seen at minus infinity;
+                    // where a row has no reference yet, or its sum leaves the
+                    // range, against the unit's maximum.
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float top = m[n][r];
+                        for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                            for (int i = 0; i < kBlocks; ++i) top = fmax3(top, st[n][i][r], st[n][i][2 + r]);
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                            if (m[n][r] != -INFINITY) {
-                                const float alpha = ex2_approx(m[n][r] - top);
-                                l[n][r] *= alpha;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    o[n][i][r] *= alpha;
-                                    o[n][i][2 + r] *= alpha;
-                                }
+                            for (int e = 0; e < 4; ++e) {
+                                const int in = l4 + 8 * (e >> 1), key = u * kKeys + 16 * i + in;
+                                st[n][i][e] = in < here[i] && key < lim[n][e & 1] ? st[n][i][e] * mul[n][e & 1] : -INFINITY;
                             }
-                            m[n][r] = top;
-                        }
-                    weights(std::true_type{}, true);
-                    bool all = true;
+                    if (weights(std::true_type{}, set)) {
 #pragma unroll
-                    for (int n = 0; n < kN; ++n) all = all && m[n][0] != -INFINITY && m[n][1] != -INFINITY;
-                    set = __all_sync(0xffffffffu, all);
-                }
-            }
+                        for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                l[n][0] += sum[n][0];
-                l[n][1] += sum[n][1];
-            }
-            const uint32_t v_power = kInt8 ? raised(vp.s) * 0x00800080u : 0u;  // of the unit's key `lane`
+                            for (int r = 0; r < 2; ++r) {
+                                float top = m[n][r];
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                // V^T: features 8 (l/4) + 2 f, + 1 in rows l/4, l/4 + 8 of tile f
-                uint32_t va[4][4];
-                if constexpr (kInt8) {
+                                for (int i = 0; i < kBlocks; ++i) top = fmax3(top, st[n][i][r], st[n][i][2 + r]);
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                                if (m[n][r] != -INFINITY) {
+                                    const float alpha = ex2_approx(m[n][r] - top);
+                                    l[n][r] *= alpha;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 &w = vp.x[2 * i + j];
+                                    for (int i = 0; i < 4; ++i) {
+                                        o[n][i][r] *= alpha;
+                                        o[n][i][2 + r] *= alpha;
+                                    }
+                                }
+                                m[n][r] = top;
+                            }
+                        weights(std::true_type{}, true);
+                        bool all = true;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            va[e >> 1][2 * j + (e & 1)] = to_bf16(e < 4 ? w.x : w.y, e < 4 ? w.z : w.w, e & 3);
+                        for (int n = 0; n < kN; ++n) all = all && m[n][0] != -INFINITY && m[n][1] != -INFINITY;
+                        set = __all_sync(0xffffffffu, all);
                     }
-                } else {
-                    const uint32_t w[4][4] = {{vp.x[0].x, vp.x[0].y, vp.x[0].z, vp.x[0].w}, {vp.x[1].x, vp.x[1].y, vp.x[1].z, vp.x[1].w},
-                                              {vp.x[2].x, vp.x[2].y, vp.x[2].z, vp.x[2].w}, {vp.x[3].x, vp.x[3].y, vp.x[3].z, vp.x[3].w}};
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        va[f][0] = __byte_perm(w[0][f], w[1][f], 0x5410);
-                        va[f][1] = __byte_perm(w[0][f], w[1][f], 0x7632);
-                        va[f][2] = __byte_perm(w[2][f], w[3][f], 0x5410);
-                        va[f][3] = __byte_perm(w[2][f], w[3][f], 0x7632);
-                    }
-                }
-                // (as bf16 a power's bits are its stored exponent, 7 bits up)
-                uint32_t power[2] = {0u, 0u};
-                if constexpr (kInt8) {
-                    power[0] = __shfl_sync(0xffffffffu, v_power, 16 * i + l4);
-                    power[1] = __shfl_sync(0xffffffffu, v_power, 16 * i + 8 + l4);
                 }
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
+                    l[n][0] += sum[n][0];
+                    l[n][1] += sum[n][1];
+                }
+                const uint32_t v_power = kInt8 ? raised(vp.s) * 0x00800080u : 0u;  // of the unit's key `lane`
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    // V^T: features 8 (l/4) + 2 f, + 1 in rows l/4, l/4 + 8 of tile f
+                    uint32_t va[4][4];
                     if constexpr (kInt8) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const __nv_bfloat162 w = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[n][i][j]),
-                                                             *reinterpret_cast<const __nv_bfloat162 *>(&power[j]));
-                            pk[n][i][j] = *reinterpret_cast<const uint32_t *>(&w);
+                            const uint4 &w = vp.x[2 * i + j];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                va[e >> 1][2 * j + (e & 1)] = to_bf16(e < 4 ? w.x : w.y, e < 4 ? w.z : w.w, e & 3);
+                        }
+                    } else {
+                        const uint32_t w[4][4] = {{vp.x[0].x, vp.x[0].y, vp.x[0].z, vp.x[0].w},
+                                                  {vp.x[1].x, vp.x[1].y, vp.x[1].z, vp.x[1].w},
+                                                  {vp.x[2].x, vp.x[2].y, vp.x[2].z, vp.x[2].w},
+                                                  {vp.x[3].x, vp.x[3].y, vp.x[3].z, vp.x[3].w}};
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            va[f][0] = __byte_perm(w[0][f], w[1][f], 0x5410);
+                            va[f][1] = __byte_perm(w[0][f], w[1][f], 0x7632);
+                            va[f][2] = __byte_perm(w[2][f], w[3][f], 0x5410);
+                            va[f][3] = __byte_perm(w[2][f], w[3][f], 0x7632);
                         }
                     }
-                    const uint32_t b0 = transpose8(pk[n][i][0]), b1 = transpose8(pk[n][i][1]);
+                    // (as bf16 a power's bits are its stored exponent, 7 bits up)
+                    uint32_t power[2] = {0u, 0u};
+                    if constexpr (kInt8) {
+                        power[0] = __shfl_sync(0xffffffffu, v_power, 16 * i + l4);
+                        power[1] = __shfl_sync(0xffffffffu, v_power, 16 * i + 8 + l4);
+                    }
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
+                    for (int n = 0; n < kN; ++n) {
+                        if constexpr (kInt8) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const __nv_bfloat162 w = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[n][i][j]),
+                                                                 *reinterpret_cast<const __nv_bfloat162 *>(&power[j]));
+                                pk[n][i][j] = *reinterpret_cast<const uint32_t *>(&w);
+                            }
+                        }
+                        const uint32_t b0 = transpose8(pk[n][i][0]), b1 = transpose8(pk[n][i][1]);
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) mma_bf16(o[n][f], va[f], b0, b1);
+                    }
                 }
+                if (u + step < u1) load(std::true_type{}, vp);
             }
-            if (u + step < u1) load(std::true_type{}, vp);
+            // what the runs before have left in shared memory, against the references of then
+            if (carried) {
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 8 * n + 2 * c + r;
+                        const float was = sh_ml[warp][row].x, f = was == -INFINITY ? 0.f : ex2_approx(was - m[n][r]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 x = sh_o[warp][row][2 * l4 + i];
+                            o[n][2 * i][r] = fmaf(x.x, f, o[n][2 * i][r]);
+                            o[n][2 * i][2 + r] = fmaf(x.y, f, o[n][2 * i][2 + r]);
+                            o[n][2 * i + 1][r] = fmaf(x.z, f, o[n][2 * i + 1][r]);
+                            o[n][2 * i + 1][2 + r] = fmaf(x.w, f, o[n][2 * i + 1][2 + r]);
+                        }
+                    }
+                __syncwarp();
+            }
+            if (u >= u1) break;
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 8 * n + 2 * c + r;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        sh_o[warp][row][2 * l4 + i] =
+                            make_float4(o[n][2 * i][r], o[n][2 * i][2 + r], o[n][2 * i + 1][r], o[n][2 * i + 1][2 + r]);
+                        o[n][2 * i][r] = o[n][2 * i][2 + r] = o[n][2 * i + 1][r] = o[n][2 * i + 1][2 + r] = 0.f;
+                    }
+                    if (l4 == 0) sh_ml[warp][row].x = m[n][r];
+                }
+            __syncwarp();
         }
 
         // The sums of the worker's warps meet in shared memory.
