@@ -68,13 +68,6 @@ constexpr int ctas_of_sm(int n) { return n == 4 ? 2 : n == 2 ? 3 : 4; }
 
 template <bool kInt8>
 constexpr int kUnitKeys = kInt8 ? 32 : 16;
-// bf16: units behind a piece's first one that are asked for with it.  Calls back to back,
-// without / with 2 of them, us: 16 sequences of up to 8,192 rows x 16 heads 70 / 69, of up
-// to 32,768 240 / 236, 128 of up to 2,048 136 / 134; one call alone on an idle GPU takes 1
-// to 2 more with them.  Every unit's asked for ahead: 84 against 79 alone, 128 of up to
-// 2,048 163 against 149.  int8 units take longer to work on than to come, and these
-// instructions as well: 31.3 us without, 32.9 with them for 64 sequences of up to 8,192.
-constexpr int kAhead = 2;
 // Places on the line that an item takes before those of its units, for what beginning
 // one costs a worker: a CTA's four warps together, or a warp.  Without / with them, us:
 // 64 sequences of up to 8,192 int8 rows x 2 heads 30.8 / 29.4, 32 of up to 4,096 bf16
@@ -109,10 +102,6 @@ __device__ __forceinline__ uint2 load8(const void *p) {
     uint2 r;
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
     return r;
-}
-
-__device__ __forceinline__ void prefetch_l2(const void *p, int bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // The two fp16 pairs n0 n1, n2 n3 of four whole numbers.
@@ -393,10 +382,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
             my_at = pg * p.c.stride + row * HD;
             if (kInt8) my_scales = static_cast<long long>(pg) * (p.c.Hkv * p.c.page) + row;
             all_there = __ballot_sync(0xffffffffu, my_valid == 16);
-            if (!kInt8 && lane >= kBlocks && lane < (1 + kAhead) * kBlocks && my_valid > 0 && u + lane / kBlocks * step < u1) {
-                prefetch_l2(static_cast<const __nv_bfloat16 *>(p.c.k) + my_at, 16 * HD * sizeof(__nv_bfloat16));
-                prefetch_l2(static_cast<const __nv_bfloat16 *>(p.c.v) + my_at, 16 * HD * sizeof(__nv_bfloat16));
-            }
         };
         look_up(u0 + sub);
         // The same for a unit's blocks; the exponent of its key `lane`.
