@@ -106,6 +106,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "softmax_sums.cuh"
 #include "sm103_ptx.cuh"
 
 namespace mha {
@@ -128,6 +129,7 @@ constexpr uint32_t kOCol = 384;  // O_A [384,448), O_B [448,512)
 constexpr float kTileSumLimit = 65536.0f;  // 2^16: a tile sum above it takes the exact step
 // A row's first round is tried against the reference 0; a sum below 2^-64
 // (the scores far below 0, or none visible) takes the exact step instead.
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFirstSumMin = 5.421010862427522e-20f;  // 2^-64
 // Per-batch key lengths are read from the CTA's shared-memory copy when it
 // holds them all (B <= kLensCache), else from global memory.
@@ -207,7 +209,7 @@ __device__ __forceinline__ Item item_of(const SmemAttn &sm, const AttnParams &p,
     return it;
 }
 
-template <bool kTiles, bool kLse>
+template <bool kTiles, bool kLse, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmap_q,
                          const __grid_constant__ CUtensorMap tmap_k,
@@ -308,25 +310,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t >= sm.n_items) break;
                 const Item it = item_of(sm, p, t, cta, G);
                 if (it.n_kv == 0) continue;
-                const int qbuf = v & 1;
-                // Q buffer qbuf last served item v-2: wait until all of its
-                // score products have completed.
-                if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
-                mbar_arrive_expect_tx(&sm.q_full[qbuf], kTileBytes);
-                if (in_bounds(it.q0 >= 0 && it.q0 < p.Tq && it.bh >= 0 && it.bh < p.B * p.H, p.status))
-                    tma_load_3d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.bh);
-                ++v;
-                for (int j = 0; j < it.n_kv; ++j, ++g) {
-                    const int st = g % STAGES;
-                    if (g >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((g / STAGES) - 1) & 1, ab)))
-                        break;
-                    if (g + 1 == p.drill_skip_tile) continue;  // drill: this stage never fills
-                    mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
-                    if (in_bounds(j * BN < p.Tk && it.bh < p.B * p.H, p.status)) {
-                        tma_load_3d(&tmap_k, &sm.kv_full[st], sm.k[st], 0, j * BN, it.bh);
-                        tma_load_3d(&tmap_v, &sm.kv_full[st], sm.v[st], 0, j * BN, it.bh);
+                int run = 0;
+                do {
+                    const int qbuf = v & 1, run_end = kRuns ? min(run + kRunTiles, it.n_kv) : it.n_kv;
+                    // Q buffer qbuf last served run v-2: wait until all of its
+                    // score products have completed.
+                    if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
+                    mbar_arrive_expect_tx(&sm.q_full[qbuf], kTileBytes);
+                    if (in_bounds(it.q0 >= 0 && it.q0 < p.Tq && it.bh >= 0 && it.bh < p.B * p.H, p.status))
+                        tma_load_3d(&tmap_q, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.bh);
+                    ++v;
+                    for (int j = run; j < run_end; ++j, ++g) {
+                        const int st = g % STAGES;
+                        if (g >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((g / STAGES) - 1) & 1, ab)))
+                            break;
+                        if (g + 1 == p.drill_skip_tile) continue;  // drill: this stage never fills
+                        mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
+                        if (in_bounds(j * BN < p.Tk && it.bh < p.B * p.H, p.status)) {
+                            tma_load_3d(&tmap_k, &sm.kv_full[st], sm.k[st], 0, j * BN, it.bh);
+                            tma_load_3d(&tmap_v, &sm.kv_full[st], sm.v[st], 0, j * BN, it.bh);
+                        }
                     }
-                }
+                } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
             }
             // Let every copy still in flight land before the CTA exits (on the
             // normal path these phases completed long ago).
@@ -354,29 +359,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t >= sm.n_items) break;
             const Item it = item_of(sm, p, t, cta, G);
             if (it.n_kv == 0) continue;
-            const int qbuf = v & 1;
-            if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
-            const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
-            for (int j = 0; j < it.n_kv; ++j, ++g) {
-                const int st = g % STAGES, sb = g % kSBufs;
-                if (!(ok = warp_wait(&sm.kv_full[st], (g / STAGES) & 1, ab))) break;
-                if (g >= kSBufs) {
-                    const int gp = g - kSBufs;
-                    if (!(ok = warp_wait(&sm.kv_empty[gp % STAGES], (gp / STAGES) & 1, ab))) break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
-                const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
+            int run = 0;
+            do {
+                const int qbuf = v & 1, run_end = kRuns ? min(run + kRunTiles, it.n_kv) : it.n_kv;
+                if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
+                const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
+                for (int j = run; j < run_end; ++j, ++g) {
+                    const int st = g % STAGES, sb = g % kSBufs;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (g / STAGES) & 1, ab))) break;
+                    if (g >= kSBufs) {
+                        const int gp = g - kSBufs;
+                        if (!(ok = warp_wait(&sm.kv_empty[gp % STAGES], (gp / STAGES) & 1, ab))) break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
-                warp_commit(&sm.s_full[sb]);
-            }
-            if (!ok) break;
-            // Every score product of this item is issued: the Q buffer is
-            // free once they complete.
-            warp_commit(&sm.q_empty[qbuf]);
-            ++v;
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
+                    warp_commit(&sm.s_full[sb]);
+                }
+                if (!ok) break;
+                // Every score product of this run is issued: the Q buffer is
+                // free once they complete.
+                warp_commit(&sm.q_empty[qbuf]);
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
         // Always wait (time-bounded, whatever the abort state) until every
         // MMA this warp issued has completed: tensor memory is released and
@@ -405,37 +413,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t >= sm.n_items) break;
             const Item it = item_of(sm, p, t, cta, G);
             if (it.n_kv == 0) continue;
-            if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
-            for (int j = 0; j < it.n_kv; ++j, ++g) {
-                if (kTiles && (g & 1) != hf) continue;
-                const int st = g % STAGES, sb = g % kSBufs;
-                const int slot = (g >> 1) & 1, par = (g >> 2) & 1;
-                if (!(ok = warp_wait(kTiles ? &sm.p_rd[hf][0][slot] : &sm.p_full[sb][hf],
-                                     kTiles ? par : (g / kSBufs) & 1, ab)))
-                    break;
-                if (!(ok = warp_wait(&sm.kv_full[st], (g / STAGES) & 1, ab))) break;
-                tc_fence_after_sync();
-                const uint32_t a = p_col + 128u * static_cast<uint32_t>(sb);
-                const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o,
-                                     (j >= (kTiles ? 2 : 1) || kk > 0) ? 1u : 0u);
-                if (kTiles) {
-                    // The round-0 half is issued while the softmax works on
-                    // round 1; the second half follows round 1's P.
-                    warp_commit(&sm.pv0[hf][slot]);
-                    if (!(ok = warp_wait(&sm.p_rd[hf][1][slot], par, ab))) break;
+            int run = 0;
+            do {
+                const int n_kv = kRuns ? min(it.n_kv - run, kRunTiles) : it.n_kv;
+                if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
+                for (int j = 0; j < n_kv; ++j, ++g) {
+                    if (kTiles && (g & 1) != hf) continue;
+                    const int st = g % STAGES, sb = g % kSBufs;
+                    const int slot = (g >> 1) & 1, par = (g >> 2) & 1;
+                    if (!(ok = warp_wait(kTiles ? &sm.p_rd[hf][0][slot] : &sm.p_full[sb][hf],
+                                         kTiles ? par : (g / kSBufs) & 1, ab)))
+                        break;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (g / STAGES) & 1, ab))) break;
                     tc_fence_after_sync();
+                    const uint32_t a = p_col + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                    for (int kk = 4; kk < 8; ++kk)
-                        warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, 1u);
+                    for (int kk = 0; kk < 4; ++kk)
+                        warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o,
+                                         (j >= (kTiles ? 2 : 1) || kk > 0) ? 1u : 0u);
+                    if (kTiles) {
+                        // The round-0 half is issued while the softmax works on
+                        // round 1; the second half follows round 1's P.
+                        warp_commit(&sm.pv0[hf][slot]);
+                        if (!(ok = warp_wait(&sm.p_rd[hf][1][slot], par, ab))) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            warp_mma_bf16_ts(d_o, a + 8 * kk, vd + 128 * kk, idesc_o, 1u);
+                    }
+                    warp_commit(&sm.kv_empty[st]);
                 }
-                warp_commit(&sm.kv_empty[st]);
-            }
-            if (!ok) break;
-            warp_commit(&sm.o_final);
-            ++v;
+                if (!ok) break;
+                warp_commit(&sm.o_final);
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
         warp_commit(&sm.drain[1 + hf]);
         mbar_wait_drain(&sm.drain[1 + hf], 0);
@@ -535,137 +547,141 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.n_kv == 0) continue;
             const int row = it.q0 + r;  // query index
             const int row_lim = causal ? min(it.kv_len, row + 1) : it.kv_len;  // keys < row_lim visible
-            float m_run = -INFINITY;  // -inf until this group has seen a visible key
-            float l_run = 0.f;
+            int run = 0;
+            do {
+                const int n_kv = kRuns ? min(it.n_kv - run, kRunTiles) : it.n_kv;
+                float m_run = -INFINITY;  // -inf until this group has seen a visible key
+                float l_run = 0.f;
 
-            for (int j = 0; j < it.n_kv; ++j, ++g) {
-                if (kTiles && (g & 1) != half) continue;
-                const int sb = g % kSBufs;
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (g / kSBufs) & 1, ab));
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
-                const bool edge =
-                    (j * BN + BN > it.kv_len) || (causal && j * BN + BN - 1 > it.q0);
+                for (int j = 0; j < n_kv; ++j, ++g) {
+                    if (kTiles && (g & 1) != half) continue;
+                    const int sb = g % kSBufs;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (g / kSBufs) & 1, ab));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                    const int key0 = (run + j) * BN;
+                    const bool edge = (key0 + BN > it.kv_len) || (causal && key0 + BN - 1 > it.q0);
 #pragma unroll
-                for (int rd = 0; rd < kRounds; ++rd) {
-                    const int c0 = kTiles ? 64 * rd : 64 * half;  // the round's first key in the tile
-                    const uint32_t tr = ts + static_cast<uint32_t>(c0);
-                    const int lim = row_lim - (j * BN + c0);
-                    uint32_t pk[32];
-                    float lt = 0.f;
-                    bool need = true;  // no reference yet: exact unless the guess holds
-                    if (guess_first || (kTiles ? (j >= 2 || rd == 1) : j > 0)) {
-                        uint32_t s0[32], s1[32];
-                        tmem_ld32(tr, s0);
-                        tmem_ld32(tr + 32, s1);
-                        tmem_ld_wait(s0);
-                        reg_fence32(s1);
-                        if (edge) mask_scores(s0, s1, lim);
-                        lt = exp_tile(s0, s1, m_run == -INFINITY ? 0.f : m_run * C, pk);
-                        // without a reference yet, the round was taken against 0:
-                        // kept if its sum lies in [2^-64, 2^16], which then
-                        // becomes the row's reference
-                        need = m_run == -INFINITY
-                                   ? !(guess_first && lt >= kFirstSumMin && lt <= kTileSumLimit)
-                                   : !(lt <= kTileSumLimit);
-                        if (!need && m_run == -INFINITY) m_run = 0.f;
-                        // by halves (short items) a round with no visible key
-                        // for this row -- the second key half of a diagonal
-                        // tile -- has P = 0 exactly and needs no exact step (a
-                        // missing reference stays missing)
-                        if (!kTiles && lim <= 0) need = false;
-                    }
-                    if (__any_sync(0xffffffffu, need)) {
-                        uint32_t s0[32], s1[32];
-                        tmem_ld32(tr, s0);
-                        tmem_ld32(tr + 32, s1);
-                        tmem_ld_wait(s0);
-                        reg_fence32(s1);
-                        if (edge) mask_scores(s0, s1, lim);
-                        float alpha = 1.f;
-                        if (need) {
-                            const float m_new = fmaxf(m_run, row_max(s0, s1));
-                            if (m_run != -INFINITY) alpha = ex2_approx((m_run - m_new) * C);
-                            m_run = m_new;
-                            l_run *= alpha;
+                    for (int rd = 0; rd < kRounds; ++rd) {
+                        const int c0 = kTiles ? 64 * rd : 64 * half;  // the round's first key in the tile
+                        const uint32_t tr = ts + static_cast<uint32_t>(c0);
+                        const int lim = row_lim - (key0 + c0);
+                        uint32_t pk[32];
+                        float lt = 0.f;
+                        bool need = true;  // no reference yet: exact unless the guess holds
+                        if (guess_first || (kTiles ? (j >= 2 || rd == 1) : j > 0)) {
+                            uint32_t s0[32], s1[32];
+                            tmem_ld32(tr, s0);
+                            tmem_ld32(tr + 32, s1);
+                            tmem_ld_wait(s0);
+                            reg_fence32(s1);
+                            if (edge) mask_scores(s0, s1, lim);
                             lt = exp_tile(s0, s1, m_run == -INFINITY ? 0.f : m_run * C, pk);
+                            // without a reference yet, the round was taken against 0:
+                            // kept if its sum lies in [2^-64, 2^16], which then
+                            // becomes the row's reference
+                            need = m_run == -INFINITY
+                                       ? !(guess_first && lt >= kFirstSumMin && lt <= kTileSumLimit)
+                                       : !(lt <= kTileSumLimit);
+                            if (!need && m_run == -INFINITY) m_run = 0.f;
+                            // by halves (short items) a round with no visible key
+                            // for this row -- the second key half of a diagonal
+                            // tile -- has P = 0 exactly and needs no exact step (a
+                            // missing reference stays missing)
+                            if (!kTiles && lim <= 0) need = false;
                         }
-                        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                            if (kTiles && rd == 1) {
-                                // O_h holds the item's earlier tiles and this
-                                // tile's round 0 (taken against the old
-                                // reference): wait for that product.
-                                ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(g >> 1) & 1],
-                                                                       (g >> 2) & 1, ab));
-                                if (!ok) break;
-                                tc_fence_after_sync();
-#pragma unroll 1
-                                for (int part = 0; part < 2; ++part) {
-                                    uint32_t o0[32];
-                                    tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
-                                    tmem_ld_wait(o0);
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c) o0[c] = f2u(u2f(o0[c]) * alpha);
-                                    tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
-                                    tmem_st_wait();
-                                }
-                            } else if (!kTiles || j >= 2) {
-                                // O_h holds the earlier tiles of the item:
-                                // wait for the product of the previous tile
-                                // it took (g-2 by tiles; g-1, both halves, by
-                                // halves, where a finite old reference means
-                                // j >= 1).  That release's next phase needs
-                                // P_g, not yet published, so it cannot alias.
-                                const int gp = g - (kTiles ? 2 : 1);
-                                ok = __all_sync(0xffffffffu,
-                                                mbar_wait(&sm.kv_empty[gp % STAGES],
-                                                          (gp / STAGES) & 1, ab));
-                                if (!ok) break;
-                                tc_fence_after_sync();
-#pragma unroll 1
-                                for (int part = 0; part < 2; ++part) {
-                                    uint32_t o0[32];
-                                    tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
-                                    tmem_ld_wait(o0);
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c) o0[c] = f2u(u2f(o0[c]) * alpha);
-                                    tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
-                                    tmem_st_wait();
-                                }
+                        if (__any_sync(0xffffffffu, need)) {
+                            uint32_t s0[32], s1[32];
+                            tmem_ld32(tr, s0);
+                            tmem_ld32(tr + 32, s1);
+                            tmem_ld_wait(s0);
+                            reg_fence32(s1);
+                            if (edge) mask_scores(s0, s1, lim);
+                            float alpha = 1.f;
+                            if (need) {
+                                const float m_new = fmaxf(m_run, row_max(s0, s1));
+                                if (m_run != -INFINITY) alpha = ex2_approx((m_run - m_new) * C);
+                                m_run = m_new;
+                                l_run *= alpha;
+                                lt = exp_tile(s0, s1, m_run == -INFINITY ? 0.f : m_run * C, pk);
                             }
+                            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                                if (kTiles && rd == 1) {
+                                    // O_h holds the run's earlier tiles and this
+                                    // tile's round 0 (taken against the old
+                                    // reference): wait for that product.
+                                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(g >> 1) & 1],
+                                                                           (g >> 2) & 1, ab));
+                                    if (!ok) break;
+                                    tc_fence_after_sync();
+#pragma unroll 1
+                                    for (int part = 0; part < 2; ++part) {
+                                        uint32_t o0[32];
+                                        tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                                        tmem_ld_wait(o0);
+#pragma unroll
+                                        for (int c = 0; c < 32; ++c) o0[c] = f2u(u2f(o0[c]) * alpha);
+                                        tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                                        tmem_st_wait();
+                                    }
+                                } else if (!kTiles || j >= 2) {
+                                    // O_h holds the earlier tiles of the run:
+                                    // wait for the product of the previous tile
+                                    // it took (g-2 by tiles; g-1, both halves, by
+                                    // halves, where a finite old reference means
+                                    // j >= 1).  That release's next phase needs
+                                    // P_g, not yet published, so it cannot alias.
+                                    const int gp = g - (kTiles ? 2 : 1);
+                                    ok = __all_sync(0xffffffffu,
+                                                    mbar_wait(&sm.kv_empty[gp % STAGES],
+                                                              (gp / STAGES) & 1, ab));
+                                    if (!ok) break;
+                                    tc_fence_after_sync();
+#pragma unroll 1
+                                    for (int part = 0; part < 2; ++part) {
+                                        uint32_t o0[32];
+                                        tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                                        tmem_ld_wait(o0);
+#pragma unroll
+                                        for (int c = 0; c < 32; ++c) o0[c] = f2u(u2f(o0[c]) * alpha);
+                                        tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                                        tmem_st_wait();
+                                    }
+                                }
 
+                            }
+                        }
+                        // P columns: [32 rd, 32 rd + 32) by tiles, [64 h, 64 h + 32)
+                        // by halves; both lie over scores already read.
+                        tmem_st32(ts + static_cast<uint32_t>(kTiles ? 32 * rd : 64 * half), pk);
+                        l_run += lt;
+                        if (kTiles) {
+                            tmem_st_wait();
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(g >> 1) & 1]);
                         }
                     }
-                    // P columns: [32 rd, 32 rd + 32) by tiles, [64 h, 64 h + 32)
-                    // by halves; both lie over scores already read.
-                    tmem_st32(ts + static_cast<uint32_t>(kTiles ? 32 * rd : 64 * half), pk);
-                    l_run += lt;
-                    if (kTiles) {
+                    if (!ok) break;
+                    if (!kTiles) {
                         tmem_st_wait();
                         tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(g >> 1) & 1]);
+                        if (lane == 0) mbar_arrive(&sm.p_full[sb][half]);
                     }
                 }
                 if (!ok) break;
-                if (!kTiles) {
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[sb][half]);
-                }
-            }
-            if (!ok) break;
-            // Row statistics of this item for the output warps, once they have
-            // read the previous item's.
-            if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab))))
-                break;
-            sm.red_m[half][r] = m_run;
-            sm.red_l[half][r] = l_run;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ml_full);
-            ++v;
+                // Row statistics of this item for the output warps, once they have
+                // read the previous item's.
+                if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab))))
+                    break;
+                sm.red_m[half][r] = m_run;
+                sm.red_l[half][r] = l_run;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ml_full);
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
         if (!ok) tmem_st_wait();  // no tensor-memory store may outlive the CTA
     } else if (warp >= kOutWarp) {
@@ -707,53 +723,84 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
-            const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
-            const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ml_free);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
-            tc_fence_after_sync();
-            const float M = fmaxf(ma, mb);
-            const float wa = la > 0.f ? ex2_approx((ma - M) * C) : 0.f;
-            const float wb = lb > 0.f ? ex2_approx((mb - M) * C) : 0.f;
-            const float L = la * wa + lb * wb;
-            const float inv = L > 0.f ? 1.0f / L : 0.f;
-            const float fa = wa * inv, fb = wb * inv;
-            // Log-sum-exp of the row's visible scores: sum_j 2^(s_j c) =
-            // 2^(M c) L with c = scale log2(e), so lse = M scale + ln L.
-            // L sums the bf16-rounded weights (the normaliser of the output),
-            // within a relative 2^-8 of the exact sum.
-            if (lse_row) *lse_row = L > 0.f ? M * p.scale + logf(L) : -INFINITY;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                uint32_t oa[32], ob[32];
-                tmem_ld32(tl + kOCol + 32u * part, oa);
-                tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
-                tmem_ld_wait(oa);
-                reg_fence32(ob);
-                if (part == 1) {
-                    // O_A and O_B are read: the next item's products may
-                    // overwrite them.
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.o_free);
+            // what an item's runs before have summed, and the reference (log2 units) and
+            // sum that go with it (in local memory: few items have more than one)
+            volatile float sum_o[kRuns ? HD : 1];
+            float sum_m = -INFINITY, sum_l = 0.f;
+            const bool single = !kRuns || it.n_kv <= kRunTiles;
+            int run = 0;
+            do {
+                const bool last = !kRuns || run + kRunTiles >= it.n_kv;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
+                const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
+                const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ml_free);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
+                tc_fence_after_sync();
+                const float M = fmaxf(ma, mb);
+                const float wa = la > 0.f ? ex2_approx((ma - M) * C) : 0.f;
+                const float wb = lb > 0.f ? ex2_approx((mb - M) * C) : 0.f;
+                float L = la * wa + lb * wb, f = 1.f, keep = 0.f;
+                if (!single) {
+                    const SumLevel run_sum = sum_level(M * C, L);
+                    const float m = L > 0.f ? run_sum.m : -INFINITY, top = fmaxf(sum_m, m);
+                    f = m == -INFINITY ? 0.f : ex2_approx(m - top) * run_sum.down;
+                    keep = sum_m == -INFINITY ? 0.f : ex2_approx(sum_m - top);
+                    L = L * f + sum_l * keep;
+                    sum_m = top;
+                    sum_l = L;
                 }
-                if (row < p.Tq && row_ok) {
-                    uint32_t packed[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        packed[c] = pack_bf16x2((la > 0.f ? u2f(oa[2 * c]) * fa : 0.f) +
-                                                    (lb > 0.f ? u2f(ob[2 * c]) * fb : 0.f),
-                                                (la > 0.f ? u2f(oa[2 * c + 1]) * fa : 0.f) +
-                                                    (lb > 0.f ? u2f(ob[2 * c + 1]) * fb : 0.f));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        d4[4 * part + c] = make_uint4(packed[4 * c], packed[4 * c + 1],
-                                                      packed[4 * c + 2], packed[4 * c + 3]);
+                if (last) {
+                    const float inv = L > 0.f ? 1.0f / L : 0.f;
+                    f *= inv;
+                    keep *= inv;
                 }
-            }
-            ++v;
+                const float fa = wa * f, fb = wb * f;
+                // Log-sum-exp of the row's visible scores: sum_j 2^(s_j c) =
+                // 2^(M c) L with c = scale log2(e), so lse = M scale + ln L.
+                // L sums the bf16-rounded weights (the normaliser of the output),
+                // within a relative 2^-8 of the exact sum.
+                if (lse_row && last)
+                    *lse_row = L > 0.f ? (single ? M * p.scale : sum_m * kLn2) + logf(L) : -INFINITY;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t oa[32], ob[32];
+                    tmem_ld32(tl + kOCol + 32u * part, oa);
+                    tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
+                    tmem_ld_wait(oa);
+                    reg_fence32(ob);
+                    if (part == 1) {
+                        // O_A and O_B are read: the next run's products may
+                        // overwrite them.
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.o_free);
+                    }
+                    if (row < p.Tq && row_ok) {
+                        float x[32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            x[c] = (la > 0.f ? u2f(oa[c]) * fa : 0.f) + (lb > 0.f ? u2f(ob[c]) * fb : 0.f);
+                            if constexpr (kRuns) {
+                                if (!single) {
+                                    if (run > 0) x[c] = fmaf(sum_o[32 * part + c], keep, x[c]);
+                                    if (!last) sum_o[32 * part + c] = x[c];
+                                }
+                            }
+                        }
+                        if (!last) continue;
+                        uint32_t packed[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) packed[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            d4[4 * part + c] = make_uint4(packed[4 * c], packed[4 * c + 1],
+                                                          packed[4 * c + 2], packed[4 * c + 3]);
+                    }
+                }
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
     }
 
@@ -784,8 +831,15 @@ cudaError_t launch_attn_bf16(const CUtensorMap &tq, const CUtensorMap &tk,
                              bool pdl) {
     const bool by_tiles = attn_bf16_splits_by_tiles(p.Tq, p.Tk, p.mask);
     // kLse: the log-sum-exp is exported (the first round always exact)
-    auto kernel = p.lse ? (by_tiles ? attn_fwd_bf16_kernel<true, true> : attn_fwd_bf16_kernel<false, true>)
-                        : (by_tiles ? attn_fwd_bf16_kernel<true, false> : attn_fwd_bf16_kernel<false, false>);
+    // kRuns: so many keys that they are summed in runs (by tiles: a split by
+    // halves has a few tiles at most)
+    const bool runs = by_tiles && needs_runs(p.Tk);
+    auto kernel = p.lse ? (runs       ? attn_fwd_bf16_kernel<true, true, true>
+                           : by_tiles ? attn_fwd_bf16_kernel<true, true, false>
+                                      : attn_fwd_bf16_kernel<false, true, false>)
+                        : (runs       ? attn_fwd_bf16_kernel<true, false, true>
+                           : by_tiles ? attn_fwd_bf16_kernel<true, false, false>
+                                      : attn_fwd_bf16_kernel<false, false, false>);
     const size_t smem = sizeof(SmemAttn) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));

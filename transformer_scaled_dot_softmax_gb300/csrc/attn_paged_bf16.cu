@@ -183,14 +183,6 @@ __device__ __forceinline__ Piece make_piece(const PagedAttnParams &p, const Shar
 // accumulators' handing on.
 __device__ __forceinline__ int tile_of(const Piece &w, int t) { return w.j0 + w.n_kv - 1 - t; }
 
-// Key tiles that are summed in tensor memory without a break: a longer piece goes through
-// the pipeline in runs of so many, whose sums are joined outside it.  The tensor cores'
-// accumulators drop, towards zero, what lies below a sum's last places when it is added:
-// values of one sign averaged over 2^20 rows came out 0.4 % too small in one run, over 2^26
-// 18 %; in runs of 2,048 / 1,024 / 512 tiles 2.5e-4 / 8e-5 / 2e-5, whatever the length
-// (a head's prompt of 131,072 takes 1 % longer than without).
-constexpr int kRunTiles = 1024;
-
 template <bool kInt8>
 __device__ __forceinline__ const Piece &piece_of(Smem<kInt8> &sm, const PagedAttnParams &p, const Share &sh, int t) {
     if (t < kTable) return sm.table[t];

@@ -291,7 +291,7 @@ __device__ __forceinline__ Row make_row(const ScoredFwdParams &p, const Item &it
     return w;
 }
 
-template <bool kCap, int kBias, int kMode>
+template <bool kCap, int kBias, int kMode, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_scored_kernel(const __grid_constant__ ScoredMaps maps, const __grid_constant__ ScoredFwdParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -378,34 +378,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; ok && t < sm.n_items; ++t) {
                 const Item &it = item_of<kMode>(sm, p, t, cta, G, 1u);
                 if (it.n_kv == 0) continue;
-                const int qbuf = v & 1;
                 const bool cache = kMode == kDecode && it.split >= p.splits;
                 const CUtensorMap *mq = cache ? &maps.q_cache : &maps.q, *mk = cache ? &maps.k_cache : &maps.k,
                                   *mv = cache ? &maps.v_cache : &maps.v;
-                if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
-                mbar_arrive_expect_tx(&sm.q_full[qbuf], kMode == kDecode
-                                                            ? static_cast<uint32_t>(dr.per * (cache ? 1 : dr.nb)) * (HD * 2)
-                                                            : kTileBytes);
-                if (in_bounds(it.q0 >= 0 && it.b >= 0 && it.b < p.B && it.hh < (kMode == kDecode ? p.Hkv : p.H), p.status)) {
-                    if (kMode == kDecode)
-                        tma_load_4d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b, it.hh);
-                    else
-                        tma_load_3d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b * p.H + it.hh);
-                }
-                ++v;
                 const int z = kMode == kDecode ? (cache ? it.b * p.Hkv + it.hh : it.hh) : it.b * p.Hkv + it.hh / g;
-                for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
-                    const int j = tile_of(it, jt);
-                    const int st = n % STAGES;
-                    if (n >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
-                    mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
-                    if (in_bounds(j >= 0 && j * BN < (cache ? p.cache_cap : p.Tk) &&
-                                      z < (kMode == kDecode && !cache ? 1 : p.B) * p.Hkv,
-                                  p.status)) {
-                        tma_load_3d(mk, &sm.kv_full[st], sm.k[st], 0, j * BN, z);
-                        tma_load_3d(mv, &sm.kv_full[st], sm.v[st], 0, j * BN, z);
+                int jt = 0;
+                do {
+                    const int qbuf = v & 1, run_end = kRuns ? min(jt + kRunTiles, it.n_kv) : it.n_kv;
+                    if (v >= 2 && !(ok = mbar_wait(&sm.q_empty[qbuf], ((v - 2) >> 1) & 1, ab))) break;
+                    mbar_arrive_expect_tx(&sm.q_full[qbuf], kMode == kDecode
+                                                                ? static_cast<uint32_t>(dr.per * (cache ? 1 : dr.nb)) * (HD * 2)
+                                                                : kTileBytes);
+                    if (in_bounds(it.q0 >= 0 && it.b >= 0 && it.b < p.B && it.hh < (kMode == kDecode ? p.Hkv : p.H), p.status)) {
+                        if (kMode == kDecode)
+                            tma_load_4d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b, it.hh);
+                        else
+                            tma_load_3d(mq, &sm.q_full[qbuf], sm.q[qbuf], 0, it.q0, it.b * p.H + it.hh);
                     }
-                }
+                    ++v;
+                    for (; jt < run_end; ++jt, ++n) {
+                        const int j = tile_of(it, jt);
+                        const int st = n % STAGES;
+                        if (n >= STAGES && !(ok = mbar_wait(&sm.kv_empty[st], ((n / STAGES) - 1) & 1, ab))) break;
+                        mbar_arrive_expect_tx(&sm.kv_full[st], 2 * kTileBytes);
+                        if (in_bounds(j >= 0 && j * BN < (cache ? p.cache_cap : p.Tk) &&
+                                          z < (kMode == kDecode && !cache ? 1 : p.B) * p.Hkv,
+                                      p.status)) {
+                            tma_load_3d(mk, &sm.kv_full[st], sm.k[st], 0, j * BN, z);
+                            tma_load_3d(mv, &sm.kv_full[st], sm.v[st], 0, j * BN, z);
+                        }
+                    }
+                } while (kRuns && ok && jt < it.n_kv);
             }
             for (int x = max(0, n - STAGES); x < n; ++x)
                 mbar_wait_drain(&sm.kv_full[x % STAGES], (x / STAGES) & 1);
@@ -422,27 +425,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; ok && t < sm.n_items; ++t) {
             const int n_kv = item_of<kMode>(sm, p, t, cta, G).n_kv;
             if (n_kv == 0) continue;
-            const int qbuf = v & 1;
-            if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
-            const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
-            for (int jt = 0; jt < n_kv; ++jt, ++n) {
-                const int st = n % STAGES, sb = n % kSBufs;
-                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
-                if (n >= kSBufs) {
-                    const int np = n - kSBufs;
-                    if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
-                }
-                tc_fence_after_sync();
-                const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
-                const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
+            int jt = 0;
+            do {
+                const int qbuf = v & 1, run_end = kRuns ? min(jt + kRunTiles, n_kv) : n_kv;
+                if (!(ok = warp_wait(&sm.q_full[qbuf], (v >> 1) & 1, ab))) break;
+                const uint64_t qd = q_desc0 + static_cast<uint64_t>(qbuf) * kTileDesc;
+                for (; jt < run_end; ++jt, ++n) {
+                    const int st = n % STAGES, sb = n % kSBufs;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                    if (n >= kSBufs) {
+                        const int np = n - kSBufs;
+                        if (!(ok = warp_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab))) break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t kd = k_desc0 + static_cast<uint64_t>(st) * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
-                warp_commit(&sm.s_full[sb]);
-            }
-            if (!ok) break;
-            warp_commit(&sm.q_empty[qbuf]);
-            ++v;
+                    for (int kk = 0; kk < HD / 16; ++kk)
+                        warp_mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, idesc_s, kk > 0 ? 1u : 0u);
+                    warp_commit(&sm.s_full[sb]);
+                }
+                if (!ok) break;
+                warp_commit(&sm.q_empty[qbuf]);
+                ++v;
+            } while (kRuns && ok && jt < n_kv);
         }
         warp_commit(&sm.drain[0]);
         mbar_wait_drain(&sm.drain[0], 0);
@@ -458,43 +464,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; ok && t < sm.n_items; ++t) {
             const Item &it = item_of<kMode>(sm, p, t, cta, G);
             if (it.n_kv == 0) continue;
-            if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
-            for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
-                if ((n & 1) != hf) continue;
-                const int st = n % STAGES, sb = n % kSBufs;
-                const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
-                if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
-                // Padding past the key length: weights there are 0, and 0
-                // times whatever the buffer holds has to be 0.  (Rows past Tk
-                // are filled with zeros by the copy.)
-                const int rows = it.kv_len - tile_of(it, jt) * BN;
-                if (rows < BN && it.kv_len < (kMode == kDecode && it.split >= p.splits ? p.cache_cap : p.Tk)) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
-                    for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
-                const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
-#pragma unroll
-                for (int rd = 0; rd < 2; ++rd) {
-                    if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t acc = jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u;
-                        warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk), vd + 128 * (4 * rd + kk), idesc_o, acc);
-                        if (kMode == kForwardLse)
-                            warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk) + 16, vd + 128 * (4 * rd + kk), idesc_o, 1u);
+            int run = 0;
+            do {
+                const int n_kv = kRuns ? min(it.n_kv - run, kRunTiles) : it.n_kv;
+                if (v >= 1 && !(ok = warp_wait(&sm.o_free, (v - 1) & 1, ab))) break;
+                for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                    if ((n & 1) != hf) continue;
+                    const int st = n % STAGES, sb = n % kSBufs;
+                    const int slot = (n >> 1) & 1, par = (n >> 2) & 1;
+                    if (!(ok = warp_wait(&sm.kv_full[st], (n / STAGES) & 1, ab))) break;
+                    // Padding past the key length: weights there are 0, and 0
+                    // times whatever the buffer holds has to be 0.  (Rows past Tk
+                    // are filled with zeros by the copy.)
+                    const int rows = it.kv_len - tile_of(it, run + jt) * BN;
+                    if (rows < BN && it.kv_len < (kMode == kDecode && it.split >= p.splits ? p.cache_cap : p.Tk)) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(sm.v[st]);
+                        for (int x = max(rows, 0) * 8 + lane; x < BN * 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                    const uint32_t a = tmem + 128u * static_cast<uint32_t>(sb);
+                    const uint64_t vd = v_desc + static_cast<uint64_t>(st) * kTileDesc;
+#pragma unroll
+                    for (int rd = 0; rd < 2; ++rd) {
+                        if (!(ok = warp_wait(&sm.p_rd[hf][rd][slot], par, ab))) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t acc = jt >= 2 || rd > 0 || kk > 0 ? 1u : 0u;
+                            warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk), vd + 128 * (4 * rd + kk), idesc_o, acc);
+                            if (kMode == kForwardLse)
+                                warp_mma_bf16_ts(d_o, a + weight_col<kMode>(rd, kk) + 16, vd + 128 * (4 * rd + kk), idesc_o, 1u);
+                        }
+                        if (rd == 0) warp_commit(&sm.pv0[hf][slot]);
+                    }
+                    if (!ok) break;
+                    warp_commit(&sm.kv_empty[st]);
                 }
                 if (!ok) break;
-                warp_commit(&sm.kv_empty[st]);
-            }
-            if (!ok) break;
-            warp_commit(&sm.o_final);
-            ++v;
+                warp_commit(&sm.o_final);
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
         warp_commit(&sm.drain[1 + hf]);
         mbar_wait_drain(&sm.drain[1 + hf], 0);
@@ -621,272 +631,276 @@ __global__ void __launch_bounds__(kThreads, 1)
             // decoding: rows past the stacked ones have nothing to compute
             const bool warp_live = kMode != kDecode || __any_sync(0xffffffffu, w.live);
             const bool long_item = it.n_kv >= kFastTiles<kBias>;
-            float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
-            float l_run = 0.f;
             // the range the warp's capped scores need: near, wide, any
             int tier = !kCap || p.f.near_max != 0.f ? 0 : p.f.wide_max != 0.f ? 1 : 2;
+            int run = 0;
+            do {
+                const int n_kv = kRuns ? min(it.n_kv - run, kRunTiles) : it.n_kv;
+                float m_run = -INFINITY;  // log2 units; -inf until this group has seen a visible key
+                float l_run = 0.f;
 
-            for (int jt = 0; jt < it.n_kv; ++jt, ++n) {
-                if ((n & 1) != half) continue;
-                const int j = tile_of(it, jt);
-                const int sb = n % kSBufs;
-                ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
-                if (!ok) break;
-                if (!warp_live) {
-                    // P of the warp's rows stays whatever it is: a row of
-                    // tensor memory only reaches its own row of O
-                    if (lane == 0) {
-                        mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
-                        mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                for (int jt = 0; jt < n_kv; ++jt, ++n) {
+                    if ((n & 1) != half) continue;
+                    const int j = tile_of(it, run + jt);
+                    const int sb = n % kSBufs;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[sb], (n / kSBufs) & 1, ab));
+                    if (!ok) break;
+                    if (!warp_live) {
+                        // P of the warp's rows stays whatever it is: a row of
+                        // tensor memory only reaches its own row of O
+                        if (lane == 0) {
+                            mbar_arrive(&sm.p_rd[half][0][(n >> 1) & 1]);
+                            mbar_arrive(&sm.p_rd[half][1][(n >> 1) & 1]);
+                        }
+                        continue;
                     }
-                    continue;
-                }
-                tc_fence_after_sync();
-                const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
-                const bool edge = j * BN < it.full_lo || j * BN + BN > it.full_hi;
-                float b_tile, step;  // bias of the tile's key c: b_tile + c step, if `linear`
-                const bool linear = linear_bias<kBias>(p.f, br, j * BN - w.pos, BN, 0.f, b_tile, step);
-                uint32_t a[16];
-                int rd_first = 0;
-                if constexpr (kWhole && kMode == kForward) {
-                    if (!edge && linear && long_item) {
+                    tc_fence_after_sync();
+                    const uint32_t ts = tl + 128u * static_cast<uint32_t>(sb);
+                    const bool edge = j * BN < it.full_lo || j * BN + BN > it.full_hi;
+                    float b_tile, step;  // bias of the tile's key c: b_tile + c step, if `linear`
+                    const bool linear = linear_bias<kBias>(p.f, br, j * BN - w.pos, BN, 0.f, b_tile, step);
+                    uint32_t a[16];
+                    int rd_first = 0;
+                    if constexpr (kWhole && kMode == kForward) {
+                        if (!edge && linear && long_item) {
 #pragma unroll
-                        for (int rd = 0; rd < 2; ++rd) {
+                            for (int rd = 0; rd < 2; ++rd) {
+                                uint32_t pk[32];
+                                const float ref = m_run == -INFINITY ? 0.f : m_run;
+                                const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(j * BN + 64 * rd - w.pos), -ref)
+                                                                      : b_tile - ref;
+                                Sum sum;
+                                float big = 0.f;
+                                common_round(std::integral_constant<int, 0>{}, ts + 64u * rd, a, false, b0, step, pk, sum, big, [] { return true; });
+                                const float lt = sum.get();
+                                // a reference has to move: to the rounds below
+                                if (__any_sync(0xffffffffu, !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
+                                if (m_run == -INFINITY) m_run = 0.f;
+                                tmem_st32(ts + 32u * rd, pk);
+                                l_run += lt;
+                                tmem_st_wait();
+                                tc_fence_before_sync();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
+                                rd_first = rd + 1;
+                            }
+                        }
+                    }
+                    if (!kWhole) tmem_ld16(ts, a);
+#pragma unroll 1
+                    for (int rd = rd_first; rd < 2; ++rd) {
+                        const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
+                        auto sees_none = [&](int first, int len) {
+                            return w.keys.x >= first + len || w.keys.y <= first || (kMode == kDecode && !w.live);
+                        };
+                        // Does the row need the exact step after a sum against
+                        // the reference in hand (0 before there is one)?
+                        auto must_move = [&](float sum, bool none) -> bool {
+                            if (none) return false;
+                            if (m_run != -INFINITY) return !(sum <= kSumMax);
+                            if (!(sum >= kSumMin && sum <= kSumMax)) return true;
+                            m_run = 0.f;
+                            return false;
+                        };
+                        const int key0 = j * BN + 64 * rd;  // the round's first key
+                        int done = 0;  // of the round's two halves
+                        if (linear && (!kCap || tier < 2) &&
+                            (!edge || __all_sync(0xffffffffu, w.keys.x <= key0 && w.keys.y >= key0 + 64))) {
                             uint32_t pk[32];
                             const float ref = m_run == -INFINITY ? 0.f : m_run;
-                            const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(j * BN + 64 * rd - w.pos), -ref)
+                            // -ref and the bias's large part meet in one fused
+                            // multiply-add: far distances lose nothing
+                            const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(key0 - w.pos), -ref)
                                                                   : b_tile - ref;
                             Sum sum;
                             float big = 0.f;
-                            common_round(std::integral_constant<int, 0>{}, ts + 64u * rd, a, false, b0, step, pk, sum, big, [] { return true; });
-                            const float lt = sum.get();
-                            // a reference has to move: to the rounds below
-                            if (__any_sync(0xffffffffu, !(lt <= kSumMax && (m_run != -INFINITY || lt >= kSumMin)))) break;
-                            if (m_run == -INFINITY) m_run = 0.f;
-                            tmem_st32(ts + 32u * rd, pk);
-                            l_run += lt;
-                            tmem_st_wait();
-                            tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
-                            rd_first = rd + 1;
-                        }
-                    }
-                }
-                if (!kWhole) tmem_ld16(ts, a);
-#pragma unroll 1
-                for (int rd = rd_first; rd < 2; ++rd) {
-                    const uint32_t tr = ts + 64u * static_cast<uint32_t>(rd);
-                    auto sees_none = [&](int first, int len) {
-                        return w.keys.x >= first + len || w.keys.y <= first || (kMode == kDecode && !w.live);
-                    };
-                    // Does the row need the exact step after a sum against
-                    // the reference in hand (0 before there is one)?
-                    auto must_move = [&](float sum, bool none) -> bool {
-                        if (none) return false;
-                        if (m_run != -INFINITY) return !(sum <= kSumMax);
-                        if (!(sum >= kSumMin && sum <= kSumMax)) return true;
-                        m_run = 0.f;
-                        return false;
-                    };
-                    const int key0 = j * BN + 64 * rd;  // the round's first key
-                    int done = 0;  // of the round's two halves
-                    if (linear && (!kCap || tier < 2) &&
-                        (!edge || __all_sync(0xffffffffu, w.keys.x <= key0 && w.keys.y >= key0 + 64))) {
-                        uint32_t pk[32];
-                        const float ref = m_run == -INFINITY ? 0.f : m_run;
-                        // -ref and the bias's large part meet in one fused
-                        // multiply-add: far distances lose nothing
-                        const float b0 = kBias == kBiasSlopes ? fmaf(step, static_cast<float>(key0 - w.pos), -ref)
-                                                              : b_tile - ref;
-                        Sum sum;
-                        float big = 0.f;
-                        // The weights in pk, if the round may keep them: col,
-                        // their column.
-                        auto keep = [&](uint32_t col) -> bool {
-                            if (kCap && kMode == kDecode && !w.live) big = 0.f;
-                            if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : p.f.wide_max))) {
-                                ++tier;  // out of the polynomial's range: taken again below
-                                return false;
+                            // The weights in pk, if the round may keep them: col,
+                            // their column.
+                            auto keep = [&](uint32_t col) -> bool {
+                                if (kCap && kMode == kDecode && !w.live) big = 0.f;
+                                if (kCap && __any_sync(0xffffffffu, big > (tier == 0 ? p.f.near_max : p.f.wide_max))) {
+                                    ++tier;  // out of the polynomial's range: taken again below
+                                    return false;
+                                }
+                                const bool first = m_run == -INFINITY;
+                                const float lt = sum.get();
+                                if (__any_sync(0xffffffffu, must_move(lt, kMode == kDecode && !w.live))) {
+                                    if (first) m_run = -INFINITY;
+                                    return false;
+                                }
+                                tmem_st32(ts + col, pk);
+                                l_run += lt;
+                                return true;
+                            };
+                            auto half_done = [&]() {
+                                if (!keep(weight_col<kMode>(0, 0) + 64u * static_cast<uint32_t>(rd))) return false;
+                                done = 1;
+                                sum = Sum();
+                                return true;
+                            };
+                            bool whole;
+                            if (!kCap)
+                                whole = common_round(std::integral_constant<int, 0>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                            else if (tier == 0)
+                                whole = common_round(std::integral_constant<int, 1>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                            else
+                                whole = common_round(std::integral_constant<int, 2>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
+                            if (whole) {
+                                if (keep(kMode == kForwardLse ? 64u * static_cast<uint32_t>(rd) + 32u : 32u * static_cast<uint32_t>(rd)))
+                                    done = 2;
+                            } else {
+                                tmem_ld_wait(a);
+                                if (rd == 0) tmem_ld16(tr + 64, a);
                             }
-                            const bool first = m_run == -INFINITY;
-                            const float lt = sum.get();
-                            if (__any_sync(0xffffffffu, must_move(lt, kMode == kDecode && !w.live))) {
-                                if (first) m_run = -INFINITY;
-                                return false;
-                            }
-                            tmem_st32(ts + col, pk);
-                            l_run += lt;
-                            return true;
-                        };
-                        auto half_done = [&]() {
-                            if (!keep(weight_col<kMode>(0, 0) + 64u * static_cast<uint32_t>(rd))) return false;
-                            done = 1;
-                            sum = Sum();
-                            return true;
-                        };
-                        bool whole;
-                        if (!kCap)
-                            whole = common_round(std::integral_constant<int, 0>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
-                        else if (tier == 0)
-                            whole = common_round(std::integral_constant<int, 1>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
-                        else
-                            whole = common_round(std::integral_constant<int, 2>{}, tr, a, rd == 0, b0, step, pk, sum, big, half_done);
-                        if (whole) {
-                            if (keep(kMode == kForwardLse ? 64u * static_cast<uint32_t>(rd) + 32u : 32u * static_cast<uint32_t>(rd)))
-                                done = 2;
-                        } else {
+                        } else if (!kWhole) {
                             tmem_ld_wait(a);
                             if (rd == 0) tmem_ld16(tr + 64, a);
                         }
-                    } else if (!kWhole) {
-                        tmem_ld_wait(a);
-                        if (rd == 0) tmem_ld16(tr + 64, a);
-                    }
-                    // Every other round, 32 keys at a time.
+                        // Every other round, 32 keys at a time.
 #pragma unroll 1
-                    for (int h = done; h < 2; ++h) {
-                        const int kh = key0 + 32 * h;
-                        const bool none = sees_none(kh, 32);
-                        const uint32_t tp = ts + weight_col<kMode>(0, 0) + (kMode == kForwardLse ? 64u : 32u) * rd;
-                        uint32_t pk[16], pl[16];
-                        float lt = 0.f, alpha = 1.f;
-                        if (__all_sync(0xffffffffu, none)) {
+                        for (int h = done; h < 2; ++h) {
+                            const int kh = key0 + 32 * h;
+                            const bool none = sees_none(kh, 32);
+                            const uint32_t tp = ts + weight_col<kMode>(0, 0) + (kMode == kForwardLse ? 64u : 32u) * rd;
+                            uint32_t pk[16], pl[16];
+                            float lt = 0.f, alpha = 1.f;
+                            if (__all_sync(0xffffffffu, none)) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) pk[c] = pl[c] = 0u;
-                        } else {
-                            const int lo = min(max(w.keys.x - kh, 0), 32), hi = min(w.keys.y - kh, 32);
-                            // the keys seen, a bit each
-                            const unsigned bits = none ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
-                            const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
-                            bool need = false;
-                            // attempt 0 against the reference in hand; where a
-                            // row needs the exact step, 1 moves its reference
-                            // and 2 takes the keys again
+                                for (int c = 0; c < 16; ++c) pk[c] = pl[c] = 0u;
+                            } else {
+                                const int lo = min(max(w.keys.x - kh, 0), 32), hi = min(w.keys.y - kh, 32);
+                                // the keys seen, a bit each
+                                const unsigned bits = none ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+                                const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
+                                bool need = false;
+                                // attempt 0 against the reference in hand; where a
+                                // row needs the exact step, 1 moves its reference
+                                // and 2 takes the keys again
 #pragma unroll 1
-                            for (int attempt = 0;; ++attempt) {
-                                uint32_t y[32];
-                                tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
-                                tmem_ld_wait(y);
-                                auto mask_to = [&](float value) {
+                                for (int attempt = 0;; ++attempt) {
+                                    uint32_t y[32];
+                                    tmem_ld32(tr + 32u * static_cast<uint32_t>(h), y);
+                                    tmem_ld_wait(y);
+                                    auto mask_to = [&](float value) {
 #pragma unroll
-                                    for (int c = 0; c < 32; ++c)
-                                        if (!(bits >> c & 1u)) y[c] = __float_as_uint(value);
-                                };
-                                if (kCap) {
-                                    const bool dead = kMode == kDecode && !w.live;
-                                    float big = max_abs(y);
-                                    bool near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
-                                    if (!near && !all) {
-                                        // masked scores have no say in how tanh is taken
-                                        mask_to(0.f);
-                                        big = max_abs(y);
-                                        near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
-                                    }
-                                    if (near) {
-                                        const uint64_t n0 = f32x2_set(p.f.near[0]), n1 = f32x2_set(p.f.near[1]),
-                                                       n2 = f32x2_set(p.f.near[2]);
-#pragma unroll
-                                        for (int c = 0; c < 32; c += 2) {
-                                            const uint64_t s2 = f32x2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-                                            const uint64_t sq = mul_f32x2(s2, s2);
-                                            float t0, t1;
-                                            f32x2_unpack(mul_f32x2(s2, fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0)), t0, t1);
-                                            y[c] = __float_as_uint(t0);
-                                            y[c + 1] = __float_as_uint(t1);
+                                        for (int c = 0; c < 32; ++c)
+                                            if (!(bits >> c & 1u)) y[c] = __float_as_uint(value);
+                                    };
+                                    if (kCap) {
+                                        const bool dead = kMode == kDecode && !w.live;
+                                        float big = max_abs(y);
+                                        bool near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
+                                        if (!near && !all) {
+                                            // masked scores have no say in how tanh is taken
+                                            mask_to(0.f);
+                                            big = max_abs(y);
+                                            near = __all_sync(0xffffffffu, dead || big * big <= p.f.near_max);
                                         }
-                                    } else {
-                                        cap_scores(y, p.f, __all_sync(0xffffffffu, dead || big * big <= p.f.wide_max));
-                                    }
-                                }
-                                if (!all) mask_to(p.f.masked);
-                                add_bias<kBias, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
-                                if (attempt == 1) {
-                                    if (need) {
-                                        float up = -INFINITY;  // above the reference
+                                        if (near) {
+                                            const uint64_t n0 = f32x2_set(p.f.near[0]), n1 = f32x2_set(p.f.near[1]),
+                                                           n2 = f32x2_set(p.f.near[2]);
 #pragma unroll
-                                        for (int c = 0; c < 32; c += 2)
-                                            up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-                                        up = ceilf(up);
-                                        if (m_run == -INFINITY) {
-                                            m_run = up;
-                                        } else if (up > 0.f) {
-                                            m_run += up;
-                                            alpha = ex2_approx(-up);
-                                            l_run *= alpha;
+                                            for (int c = 0; c < 32; c += 2) {
+                                                const uint64_t s2 = f32x2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                                const uint64_t sq = mul_f32x2(s2, s2);
+                                                float t0, t1;
+                                                f32x2_unpack(mul_f32x2(s2, fma_f32x2(sq, fma_f32x2(sq, n2, n1), n0)), t0, t1);
+                                                y[c] = __float_as_uint(t0);
+                                                y[c + 1] = __float_as_uint(t1);
+                                            }
+                                        } else {
+                                            cap_scores(y, p.f, __all_sync(0xffffffffu, dead || big * big <= p.f.wide_max));
                                         }
                                     }
-                                    continue;
+                                    if (!all) mask_to(p.f.masked);
+                                    add_bias<kBias, kCap>(y, p.f, br, kh - w.pos, m_run == -INFINITY ? 0.f : -m_run);
+                                    if (attempt == 1) {
+                                        if (need) {
+                                            float up = -INFINITY;  // above the reference
+#pragma unroll
+                                            for (int c = 0; c < 32; c += 2)
+                                                up = fmax3(up, __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                                            up = ceilf(up);
+                                            if (m_run == -INFINITY) {
+                                                m_run = up;
+                                            } else if (up > 0.f) {
+                                                m_run += up;
+                                                alpha = ex2_approx(-up);
+                                                l_run *= alpha;
+                                            }
+                                        }
+                                        continue;
+                                    }
+                                    Sum sum;
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c)
+                                        pack_pair(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])), c,
+                                                  pk[c], pl[c], sum);
+                                    lt = sum.get();
+                                    if (attempt == 2) break;
+                                    need = must_move(lt, none);
+                                    if (!__any_sync(0xffffffffu, need)) break;
                                 }
-                                Sum sum;
-#pragma unroll
-                                for (int c = 0; c < 16; ++c)
-                                    pack_pair(ex2_approx(__uint_as_float(y[2 * c])), ex2_approx(__uint_as_float(y[2 * c + 1])), c,
-                                              pk[c], pl[c], sum);
-                                lt = sum.get();
-                                if (attempt == 2) break;
-                                need = must_move(lt, none);
-                                if (!__any_sync(0xffffffffu, need)) break;
                             }
-                        }
-                        const uint32_t th = tp + (kMode == kForwardLse ? 32u : 16u) * static_cast<uint32_t>(h);
-                        tmem_st16(th, pk);
-                        if (kMode == kForwardLse) tmem_st16(th + 16, pl);
-                        l_run += lt;
-                        if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
-                        // What was summed before moves with the reference: the
-                        // round's first 32 weights, which wait to be multiplied
-                        // with these, and O_h, which holds the group's earlier
-                        // tiles of the item and, in round 1, this tile's round
-                        // 0: wait for the last product it took.
-                        if (h == 1) {
-                            tmem_st_wait();
+                            const uint32_t th = tp + (kMode == kForwardLse ? 32u : 16u) * static_cast<uint32_t>(h);
+                            tmem_st16(th, pk);
+                            if (kMode == kForwardLse) tmem_st16(th + 16, pl);
+                            l_run += lt;
+                            if (!__any_sync(0xffffffffu, alpha != 1.f)) continue;
+                            // What was summed before moves with the reference: the
+                            // round's first 32 weights, which wait to be multiplied
+                            // with these, and O_h, which holds the group's earlier
+                            // tiles of the item and, in round 1, this tile's round
+                            // 0: wait for the last product it took.
+                            if (h == 1) {
+                                tmem_st_wait();
 #pragma unroll 1
-                            for (uint32_t part = 0; part < (kMode == kForwardLse ? 32u : 16u); part += 16u) {
-                                tmem_ld16(tp + part, pk);
-                                tmem_ld_wait(pk);
+                                for (uint32_t part = 0; part < (kMode == kForwardLse ? 32u : 16u); part += 16u) {
+                                    tmem_ld16(tp + part, pk);
+                                    tmem_ld_wait(pk);
 #pragma unroll
-                                for (int c = 0; c < 16; ++c)
-                                    pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
-                                                        __uint_as_float(pk[c] & 0xffff0000u) * alpha);
-                                tmem_st16(tp + part, pk);
+                                    for (int c = 0; c < 16; ++c)
+                                        pk[c] = pack_bf16x2(__uint_as_float(pk[c] << 16) * alpha,
+                                                            __uint_as_float(pk[c] & 0xffff0000u) * alpha);
+                                    tmem_st16(tp + part, pk);
+                                }
                             }
-                        }
-                        if (rd == 1) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
-                        } else if (jt >= 2) {
-                            const int np = n - 2;
-                            ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
-                        } else {
-                            continue;  // O_h holds nothing of this item
+                            if (rd == 1) {
+                                ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv0[half][(n >> 1) & 1], (n >> 2) & 1, ab));
+                            } else if (jt >= 2) {
+                                const int np = n - 2;
+                                ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_empty[np % STAGES], (np / STAGES) & 1, ab));
+                            } else {
+                                continue;  // O_h holds nothing of this item
+                            }
+                            if (!ok) break;
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int part = 0; part < 2; ++part) {
+                                uint32_t o0[32];
+                                tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
+                                tmem_ld_wait(o0);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
+                                tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
+                            }
                         }
                         if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int part = 0; part < 2; ++part) {
-                            uint32_t o0[32];
-                            tmem_ld32(to + 32u * static_cast<uint32_t>(part), o0);
-                            tmem_ld_wait(o0);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) o0[c] = __float_as_uint(__uint_as_float(o0[c]) * alpha);
-                            tmem_st32(to + 32u * static_cast<uint32_t>(part), o0);
-                        }
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
                     }
                     if (!ok) break;
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_rd[half][rd][(n >> 1) & 1]);
                 }
                 if (!ok) break;
-            }
-            if (!ok) break;
-            if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
-            sm.red_m[half][r] = m_run;
-            sm.red_l[half][r] = l_run;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ml_full);
-            ++v;
+                if (v >= 1 && !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_free, (v - 1) & 1, ab)))) break;
+                sm.red_m[half][r] = m_run;
+                sm.red_l[half][r] = l_run;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ml_full);
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
         if (!ok) tmem_st_wait();
     } else if (warp >= kOutWarp) {
@@ -919,76 +933,109 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
-            const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
-            const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.ml_free);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
-            tc_fence_after_sync();
-            // A sum of 0: no visible key.  One of NaN (a NaN or +infinity among
-            // the visible scores) goes on to o and lse.
-            const SumLevel va = sum_level(ma, la), vb = sum_level(mb, lb);
-            const float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
-            const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
-            const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;
-            const float L = la * wa + lb * wb;
-            const float inv = kMode == kDecode ? 1.f : L != 0.f ? 1.0f / L : 0.f;
-            const float fa = wa * inv, fb = wb * inv;
-            const long long prow = kMode == kDecode ? it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out : 0;
-            if (row_ok) {
-                if (kMode == kDecode)
-                    // (L in [1, 4): the merge joins by M alone; the reference of a
-                    // NaN is as good as any, if the merge takes it)
-                    p.part_ml[prow] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
-                else if (kMode == kForwardLse)
-                    p.lse[w.out] = L != 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
-            }
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                uint32_t oa[32], ob[32];
-                tmem_ld32(tl + kOCol + 32u * part, oa);
-                tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
-                tmem_ld_wait(oa);
-                reg_fence32(ob);
-                if (part == 1) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.o_free);
+            // what an item's runs before have summed (in local memory: few items have any)
+            volatile float sum_o[kRuns ? HD : 1];
+            float sum_m = -INFINITY, sum_l = 0.f;
+            const bool single = !kRuns || it.n_kv <= kRunTiles;
+            int run = 0;
+            do {
+                const bool last = !kRuns || run + kRunTiles >= it.n_kv;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, v & 1, ab)))) break;
+                const float ma = sm.red_m[0][r], mb = sm.red_m[1][r];
+                const float la = sm.red_l[0][r], lb = sm.red_l[1][r];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.ml_free);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_final, v & 1, ab)))) break;
+                tc_fence_after_sync();
+                // A sum of 0: no visible key.  One of NaN (a NaN or +infinity among
+                // the visible scores) goes on to o and lse.
+                const SumLevel va = sum_level(ma, la), vb = sum_level(mb, lb);
+                float M = fmaxf(la != 0.f ? va.m : -INFINITY, lb != 0.f ? vb.m : -INFINITY);
+                const float wa = la != 0.f ? ex2_approx(va.m - M) * va.down : 0.f;
+                const float wb = lb != 0.f ? ex2_approx(vb.m - M) * vb.down : 0.f;
+                float L = la * wa + lb * wb, f = 1.f, keep = 0.f;
+                if (!single) {
+                    const float m = L > 0.f ? M : L == 0.f ? -INFINITY : 0.f;
+                    M = fmaxf(sum_m, m);
+                    f = m == -INFINITY ? 0.f : ex2_approx(m - M);
+                    keep = sum_m == -INFINITY ? 0.f : ex2_approx(sum_m - M);
+                    L = L * f + sum_l * keep;
+                    sum_m = M;
+                    sum_l = L;
                 }
-                if (!row_ok) continue;
-                // a group without a visible key left its accumulator unwritten
+                if (kMode != kDecode && last) {
+                    const float inv = L != 0.f ? 1.0f / L : 0.f;
+                    f *= inv;
+                    keep *= inv;
+                }
+                const float fa = wa * f, fb = wb * f;
+                const long long prow = kMode == kDecode ? it.split * (static_cast<long long>(p.B) * p.H * p.Tq) + w.out : 0;
+                if (row_ok && last) {
+                    if (kMode == kDecode)
+                        // (L in [1, 4): the merge joins by M alone; the reference of a
+                        // NaN is as good as any, if the merge takes it)
+                        p.part_ml[prow] = make_float2(L > 0.f ? M : L == 0.f ? -INFINITY : 0.f, L);
+                    else if (kMode == kForwardLse)
+                        p.lse[w.out] = L != 0.f ? fmaf(M, kLn2, logf(L)) : -INFINITY;
+                }
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    oa[c] = __float_as_uint((la != 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
-                                            (lb != 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
-                if (kMode == kDecode) {
-                    uint4 *d4 = reinterpret_cast<uint4 *>(p.part_o + prow * HD) + 8 * part;
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t oa[32], ob[32];
+                    tmem_ld32(tl + kOCol + 32u * part, oa);
+                    tmem_ld32(tl + kOCol + 64u + 32u * part, ob);
+                    tmem_ld_wait(oa);
+                    reg_fence32(ob);
+                    if (part == 1) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.o_free);
+                    }
+                    if (!row_ok) continue;
+                    // a group without a visible key left its accumulator unwritten
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        d4[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
-                } else {
-                    uint4 *d4 = reinterpret_cast<uint4 *>(p.o + w.out * HD) + 4 * part;
-                    uint32_t pk[16];
+                    for (int c = 0; c < 32; ++c)
+                        oa[c] = __float_as_uint((la != 0.f ? __uint_as_float(oa[c]) * fa : 0.f) +
+                                                (lb != 0.f ? __uint_as_float(ob[c]) * fb : 0.f));
+                    if constexpr (kRuns) {
+                        if (!single) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]), __uint_as_float(oa[2 * c + 1]));
+                            for (int c = 0; c < 32; ++c) {
+                                float x = __uint_as_float(oa[c]);
+                                if (run > 0) x = fmaf(sum_o[32 * part + c], keep, x);
+                                oa[c] = __float_as_uint(x);
+                                if (!last) sum_o[32 * part + c] = x;
+                            }
+                            if (!last) continue;
+                        }
+                    }
+                    if (kMode == kDecode) {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(p.part_o + prow * HD) + 8 * part;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        d4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                    if (kMode == kForwardLse && p.o_lo) {
-                        uint4 *l4 = reinterpret_cast<uint4 *>(p.o_lo + w.out * HD) + 4 * part;
+                        for (int c = 0; c < 8; ++c)
+                            d4[c] = make_uint4(oa[4 * c], oa[4 * c + 1], oa[4 * c + 2], oa[4 * c + 3]);
+                    } else {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(p.o + w.out * HD) + 4 * part;
+                        uint32_t pk[16];
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
-                            pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]) - __uint_as_float(pk[c] << 16),
-                                                __uint_as_float(oa[2 * c + 1]) - __uint_as_float(pk[c] & 0xffff0000u));
+                            pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]), __uint_as_float(oa[2 * c + 1]));
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            l4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                            d4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                        if (kMode == kForwardLse && p.o_lo) {
+                            uint4 *l4 = reinterpret_cast<uint4 *>(p.o_lo + w.out * HD) + 4 * part;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                pk[c] = pack_bf16x2(__uint_as_float(oa[2 * c]) - __uint_as_float(pk[c] << 16),
+                                                    __uint_as_float(oa[2 * c + 1]) - __uint_as_float(pk[c] & 0xffff0000u));
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                l4[c] = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                        }
                     }
                 }
-            }
-            ++v;
+                ++v;
+            } while (kRuns && ok && (run += kRunTiles) < it.n_kv);
         }
     }
 
@@ -1000,9 +1047,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool kCap, int kBias, int kMode>
+template <bool kCap, int kBias, int kMode, bool kRuns>
 cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream) {
-    auto kernel = attn_scored_kernel<kCap, kBias, kMode>;
+    auto kernel = attn_scored_kernel<kCap, kBias, kMode, kRuns>;
     const size_t smem = sizeof(Smem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -1013,11 +1060,18 @@ cudaError_t launch(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_
     return launch_kernel(kernel, dim3(grid), dim3(kThreads), smem, stream, true, 1, maps, p);
 }
 
-template <bool kCap, int kBias>
+template <bool kCap, int kBias, bool kRuns>
 cudaError_t launch_form(const ScoredMaps &maps, const ScoredFwdParams &p, cudaStream_t stream) {
-    if (p.part_o) return launch<kCap, kBias, kDecode>(maps, p, stream);
-    if (p.lse) return launch<kCap, kBias, kForwardLse>(maps, p, stream);
-    return launch<kCap, kBias, kForward>(maps, p, stream);
+    if (p.part_o) return launch<kCap, kBias, kDecode, kRuns>(maps, p, stream);
+    if (p.lse) return launch<kCap, kBias, kForwardLse, kRuns>(maps, p, stream);
+    return launch<kCap, kBias, kForward, kRuns>(maps, p, stream);
+}
+
+template <bool kCap, bool kRuns>
+cudaError_t launch_any(const ScoredMaps &maps, int bias, const ScoredFwdParams &p, cudaStream_t stream) {
+    if (bias == kBiasSlopes) return launch_form<kCap, kBiasSlopes, kRuns>(maps, p, stream);
+    if (bias == kBiasBuckets) return launch_form<kCap, kBiasBuckets, kRuns>(maps, p, stream);
+    return launch_form<kCap, kBiasNone, kRuns>(maps, p, stream);
 }
 
 }  // namespace scored

@@ -21,4 +21,17 @@ __device__ __forceinline__ SumLevel sum_level(float m, float l) {
     return r;
 }
 
+// Key tiles (of 128) of a query block that are summed in tensor memory without a break: a
+// longer range goes through the pipeline in runs of so many, whose sums are joined
+// outside it.  The tensor cores' accumulators drop, towards zero, what lies below a sum's
+// last places when it is added: values of one sign averaged over 2^20 rows came out 0.4 %
+// too small in one run, over 2^26 18 %; in runs of 2,048 / 1,024 / 512 tiles 2.5e-4 / 8e-5 /
+// 2e-5, whatever the length (a head's prompt of 131,072 takes 1 % longer than without).
+constexpr int kRunTiles = 1024;
+// Whether the contiguous forwards go about it so, in instances of their own: the loop and
+// the joining cost their softmax warps 9 % (1 head of 270,000 x 270,000: 17.5 ms against
+// 16.1; as part of the common instances 2 x 16 x 8,192 causal took 277 us against 251), and
+// up to this many keys the bias is below 2.5e-4, a 16th of a rounding to bf16.
+inline bool needs_runs(int keys) { return keys > 2 * kRunTiles * 128; }
+
 }  // namespace mha
