@@ -503,8 +503,14 @@ mha_status paged_cache_read(const mha_paged_cache *cache, void *k, void *v, int 
  * joining of the partial sums of divided key ranges), a third between them when
  * max_new allows more: tcgen05 products over tiles of 128 rows.  When it allows 512
  * rows and the cache is int8 or its pages are no multiple of 32 rows, or 2,048 and
- * they are no multiple of 64, one more lays these sequences' cached rows out as bf16
- * first, in up to 4 GiB of the workspace (where that would take more it is left out).
+ * they are no multiple of 64 in a table of 8,192 rows or more, one more lays these sequences' cached rows out as bf16
+ * first, in up to 4 GiB of the workspace (where that would take more it is left out,
+ * and such chunks take up to twice as long).  The room is that of whole tables,
+ * whatever the lengths: 256 bytes for each of max_pages page_rows rows x h_kv x
+ * min(B, N h / h_kv / 17 (int8 33)) sequences.  A table no wider than the batch
+ * needs, and max_new, keep it small.
+ * Weights are rounded to bf16 for the product with v, and their sum is that of the
+ * rounded ones (sdpa_decode_forward keeps its weights in fp32).
  * A call's results do not depend on timing (equal calls give equal bits).
  */
 /* From the sizes in `cache` (its pointers may be NULL); 0 for sizes that are not valid or

@@ -125,7 +125,9 @@ Layout layout(const PagedCache &c, int g, int max_new) {
         const int slots = static_cast<int>(std::min<long long>(c.B, static_cast<long long>(c.N) * g / (small + 1)));
         const int cap = (c.cap + 127) / 128 * 128;
         const size_t rows = static_cast<size_t>(slots) * c.Hkv * cap;
-        const bool wide = c.int8 || c.page % 32 != 0 ? most >= kPagedWideRows : c.page % 64 != 0 && most >= kPagedWideRows32;
+        const bool wide = c.int8 || c.page % 32 != 0
+                              ? most >= kPagedWideRows
+                              : c.page % 64 != 0 && most >= kPagedWideRows32 && c.cap >= kPagedWideKeys32;
         if (wide && rows > 0 &&
             rows <= kPagedWideBytes / (2 * kAttnHeadDim * sizeof(__nv_bfloat16))) {
             l.slots = slots;

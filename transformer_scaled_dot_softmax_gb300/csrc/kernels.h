@@ -391,8 +391,16 @@ cudaError_t launch_paged_widen(const PagedAttnParams &p, const PagedWide &w, cud
 // them, and of pages of 32 rows or an odd number.  Measured, 32,768 keys x 4 K/V
 // heads, first / straight from the pages, us: int8, 64-row pages, 256 query rows 38 /
 // 35, 512 44 / 51, 4,096 140 / 268; bf16, 16-row pages 256 37 / 33, 512 43 / 46, 4,096
-// 141 / 242; 32-row pages 512 43 / 37, 2,048 84 / 91, 4,096 140 / 165.
-constexpr int kPagedWideRows = 512, kPagedWideRows32 = 2048;
+// 141 / 242; 32-row pages 512 43 / 37, 2,048 84 / 91, 4,096 140 / 165.  Behind shorter
+// contexts a pass over the rows saves less: int8, one sequence, 512 rows behind 2,048 keys
+// 23 / 20, 8,192 27 / 27, 2,048 rows behind 512 24 / 23, 4,096 behind 2,048 34 / 43; 16
+// sequences, 512 rows each behind 512 keys 33 / 36, 2,048 49 / 62.  (The lengths are on
+// the device: no rule on the host can look at them.)  Pages of 32 rows cost less to go
+// through, and are left as they are where the table has fewer than kPagedWideKeys32 rows:
+// one sequence, 2,048 rows behind 2,048 keys 26 / 24, 8,192 38 / 37, 4,096 rows behind none
+// 29 / 22, 2,048 33 / 31, 8,192 55 / 59; 777 tokens x 4 of a prompt among 32 single ones
+// 45 / 40.
+constexpr int kPagedWideRows = 512, kPagedWideRows32 = 2048, kPagedWideKeys32 = 8192;
 constexpr size_t kPagedWideBytes = static_cast<size_t>(4) << 30;  // as long as it does not take more than this
 // Tokens of a row tile, and row tiles of a call at most.
 inline __host__ __device__ int paged_tile_tokens(int g) { return 128 / g; }
