@@ -96,7 +96,8 @@ def test_long_chunks_straight_from_their_pages(lib, shape, int8, causal):
 
 
 def test_cases_pass_with_bounds_checks():
-    here = ["test_gpu_paged_clamped.py", "test_gpu_paged_small_values.py", "test_gpu_scored_windows.py"]
+    here = ["test_gpu_paged_clamped.py", "test_gpu_paged_small_values.py", "test_gpu_scored_windows.py", "test_gpu_paged_runs.py",
+            "test_gpu_forward_runs.py"]
     r = subprocess.run(
         [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", *(os.path.join("tests", n) for n in here),
          "-k", "not bounds_checks and not shape4"],

@@ -730,7 +730,8 @@ def sdpa_paged_forward(q, k_pages, v_pages, page_table, row_starts, seq_lens, ou
     (h, N, 64) bf16, packed like its k, any strides of heads and tokens; h a multiple of
     h_kv.  With a causal mask a token sees the rows up to its own, else all of
     its sequence's.  max_new: the most new tokens of a sequence (N if not given);
-    calls for single tokens are faster with it.  Returns out (h, N, 64), whose rows
+    calls for single tokens are faster with it, and without it may ask for scratch of
+    the size of the page table, as calls with long chunks do (see include/mha.h).  Returns out (h, N, 64), whose rows
     past the last sequence's are not written."""
     torch = _torch()
     _needs_starts(row_starts)

@@ -20,8 +20,10 @@
 // and the online softmax with its window of [2^-64, 2^64] around a row's reference
 // are attn_scored_bf16.cuh's, without cap and bias.
 //
-// Bound, like that kernel, by the softmax warps' instruction stream (issue 60 %, tensor
-// 43 %, special functions 43 % of their cycles).  Measured, causal, 2 x 16 heads x 8,192
+// Bound, like that kernel, by the latency of the chain from a tile's weights over their
+// product to the next scores in the same of the three buffers: no pipe is full (issue
+// 60 %, tensor 43 %, special functions 43 % of their cycles), and every instruction less
+// in the softmax warps' part of it shows.  Measured, causal, 2 x 16 heads x 8,192
 // in 64-row pages: the whole call 271 us (1,015 TFLOP/s), listing and joining included;
 // 1,024 tokens x 16 heads, 4 to a K/V head, behind 31,744 rows 125 (1,080 TFLOP/s).
 //
@@ -499,7 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t to = tl + kOCol + 64u * half;
         const uint64_t mul2 = f32x2_pack(p.mul, p.mul);
         // Weights of N keys against the reference, packed; their sum, of the
-        // rounded weights (what the product multiplies).
+        // rounded weights (what the product multiplies, so that they still add up
+        // to 1).  bf16, 2^-8 off at most each, is what the matrix instructions take
+        // beside bf16 V; a second part for the rest would double their number.
         auto weights = [&](const auto &s, float ref, uint32_t *pk, float (&sum)[4]) {
             constexpr int kPairs = sizeof(s) / 8;
             const uint64_t ref2 = f32x2_pack(-ref, -ref);

@@ -579,7 +579,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of_sm(kN)) paged_decode_kernel(
                     load(std::false_type{}, kp);
                 }
                 // Weights against the reference in hand, 0 before there is one.  Masked:
-                // of scores in log2 units.
+                // of scores in log2 units.  They are rounded to bf16, 2^-8 off at most
+                // each, for the matrix instructions; the sums are of the rounded ones, so
+                // that they still add up to 1.
                 uint32_t pk[kN][kBlocks][2];
                 float sum[kN][2];
                 auto weights = [&](auto is_masked, bool has_ref) -> bool {
