@@ -46,6 +46,11 @@
  *   - The bf16 paths accumulate in fp32 (tensor memory), keep the softmax in
  *     fp32, round the probabilities to bf16 for the P.V product and round
  *     every stored tensor to bf16 (round to nearest even).
+ *     Those accumulators drop what lies below a sum's last places when it is
+ *     added, towards zero.  Attention's sums over many keys are divided so that it
+ *     does not show; the backward calls' dk and dv, sums over the queries, are
+ *     not: where all terms have one sign they are 0.04 % too small over 2^16
+ *     queries, 0.15 % over 2^18, 0.7 % over 2^20.
  */
 #ifndef MHA_H
 #define MHA_H

@@ -49,11 +49,11 @@
 // tensor memory in most others.
 //
 // Measured, 2 x 16 heads x 8,192, causal, without / with the log-sum-exp:
-// 254 / 350 us (1,082 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
-// 410 / 506, slopes 310 / 411, both 468 / 608, 32 buckets 292 / 392, cap 20 under
-// scores of deviation 4 (some in the wide range) 555 / 670, cap 1,000 under scores
-// of deviation 6 (most warps past the polynomials) 722 / 905, 12 documents 97 / 115
-// (capped 130 / 151).  Per item of
+// 254 / 343 us (1,082 TFLOP/s without; attn_bf16.cu's plain forward 254), cap 50
+// 385 / 504, slopes 304 / 399, both 470 / 605, 32 buckets 288 / 380, cap 20 under
+// scores of deviation 4 (some in the wide range) 526 / 663, cap 1,000 under scores
+// of deviation 6 (most warps past the polynomials) 709 / 877, 12 documents 100 / 112
+// (capped 127 / 149).  Per item of
 // 128 rows about 2.5 us (3.5 with the log-sum-exp) and 0.5 to 0.6 (0.7) per key tile;
 // a tile seen in part costs two to three whole ones, which is what documents
 // and short sequences are bound by.

@@ -33,14 +33,16 @@
 // u 2^-133 in bf16.
 //
 // Measured, single tokens, whole calls: 16 sequences of up to 8,192 bf16 rows x 16
-// heads 65.5 us (403 MB, 6.2 TB/s; of up to 32,768 rows 232, 6.9 TB/s); 64 sequences of
-// up to 8,192 int8 rows x 2 heads, 8 query heads each, 29 us (102 MB, 3.5 TB/s; of up to
-// 32,768 rows 84, 4.9 TB/s).  bf16 is bound by DRAM, but for 7 us of launches and
-// joining.  int8 is bound by the ALU pipe: 32 of a lane's 290 instructions a unit there
-// less (V's numbers by 2 and a multiply-add instead of 3 and a subtraction) took 33.2 to
-// 30.9 us, where 40 less on other pipes (first products without cleared accumulators,
-// powers before their shuffles, pairs of scores at a time) and K or V asked for earlier
-// gained nothing.
+// heads 68 us back to back, 65 between a layer's projections (403 MB, 6.2 TB/s; of up to
+// 32,768 rows 238, 6.7 TB/s); 64 sequences of up to 8,192 int8 rows x 2 heads, 8 query
+// heads each, 29 us (102 MB, 3.5 TB/s; of up to 32,768 rows 83, 4.9 TB/s).  bf16 is bound
+// by DRAM, but for 7 us of launches and joining.  int8 fills no pipe (issue 40 %, ALU 35 %,
+// DRAM 46 %; of up to 32,768 rows 45, 41, 61 %): a warp runs 430 instructions a unit, most
+// of which wait for one another, at 16 warps an SM, and with 10 units a warp another
+// quarter outside that loop.  32 less a unit on the ALU pipe (V's numbers by 2 and a
+// multiply-add instead of 3 and a subtraction) took 33.2 to 30.9 us; 40 less on other
+// pipes (first products without cleared accumulators, powers before their shuffles, pairs
+// of scores at a time) and K or V asked for earlier gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
