@@ -86,3 +86,53 @@ def test_decoding_over_a_long_prefix(lib, B, h, T_q):
     want = torch.softmax(s, -1) @ v.double()
     e = 2 * ref.score_error(None, 0.125 * (q.double().abs() @ k.double().abs().transpose(1, 2))).amax(-1, keepdim=True)
     ref.check("o", out, want, (ref.U + e) * 2 * want + ref.U * want, 0)
+
+
+@pytest.mark.parametrize("form", ["plain", "causal", "slopes", "buckets", "documents", "prefix", "padded"])
+def test_masks_and_biases_over_many_keys(lib, form):
+    """300,000 queries and keys: rows on both sides of the ends of documents, prefixes, lengths and runs."""
+    T, dev = 300_000, "cuda"
+    g = gen(74)
+    q, k, v = (torch.randn(1, 1, T, 64, generator=g, device=dev).to(BF) for _ in range(3))
+    i = torch.tensor([0, 127, 128, 9_999, 10_000, 131_071, 131_072, 141_500, 262_143, 262_144, 273_000, T - 129, T - 1], device=dev)
+    j = torch.arange(T, device=dev)
+    kw, vis = {"mask": "causal"}, j[None] <= i[:, None]
+    bias = torch.zeros(len(i), T, dtype=torch.float64, device=dev)
+    if form == "slopes":
+        kw["slopes"] = torch.tensor([2.0 ** -14], device=dev)
+        bias = -(2.0 ** -14) * (j[None] - i[:, None]).abs().double()
+    elif form == "buckets":
+        starts = (0, 1, 300, 20_000)
+        kw["table"], kw["bucket_starts"] = torch.randn(4, 1, generator=g, device=dev).to(BF), starts
+        bias = ref.bias_of(j[None] - i[:, None], 1, None, kw["table"], starts)[0]
+    elif form == "documents":
+        ids = (j >= 10_000).int() + (j >= 273_000).int()
+        kw["doc_ids"] = ids[None].contiguous()
+        vis = vis & (ids[None] == ids[i][:, None])
+    elif form == "prefix":
+        kw["prefix_lens"] = ints(141_500)
+        vis = vis | (j[None] < 141_500)
+    elif form == "padded":
+        kw = {"mask": "key_padding", "key_lens": ints(299_001)}
+        vis = (j[None] < 299_001).expand(len(i), -1)
+    x = q[0, 0, i].double()
+    p, _, lse, s = ref.weights(x @ k[0, 0].double().t() * 0.125, None, bias, vis)
+    mag = 0.125 * (x.abs() @ k[0, 0].double().abs().t()) + bias.abs()
+    e = 2 * torch.where(vis, ref.score_error(None, mag), 0.0).amax(-1, keepdim=True)
+    want = p @ v[0, 0].double()
+    spread = p @ v[0, 0].double().abs() + want.abs()
+    tol = (ref.U + e) * spread + ref.U * want.abs()
+    if form in ("plain", "padded"):
+        o, l = lib.sdpa_forward_lse(q, k, v, **kw)
+        ref.check("o", o[0, 0, i], want, tol, 0)
+        ref.check("lse", l[0, 0, i], lse, ref.U + e[:, 0], 0)
+        ref.check("o", lib.sdpa_forward(q, k, v, **kw)[0, 0, i], want, tol, 0)
+    if form != "plain":
+        ref.check("o", lib.sdpa_scored_forward(q, k, v, **kw)[0, 0, i], want, tol, 0)
+        lo = torch.empty_like(q)
+        o, l = lib.sdpa_scored_forward_lse(q, k, v, out_lo=lo, **kw)
+        ref.check("o", o[0, 0, i], want, tol, 0)
+        ref.check("lse", l[0, 0, i], lse, e[:, 0] + 2.0 ** -22 * lse.abs(), 0)
+        # with what rounding took from it: the weights' second parts, and runs' sums (2^-12)
+        both = o[0, 0, i].double() + lo[0, 0, i].double()
+        ref.check("o + lo", both, want, (ref.U ** 2 + e + 2.0 ** -12) * spread + ref.U ** 2 * want.abs(), 0)

@@ -778,21 +778,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) mbar_arrive(&sm.o_free);
                     }
                     if (row < p.Tq && row_ok) {
-                        float x[32];
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            x[c] = (la > 0.f ? u2f(oa[c]) * fa : 0.f) + (lb > 0.f ? u2f(ob[c]) * fb : 0.f);
-                            if constexpr (kRuns) {
-                                if (!single) {
-                                    if (run > 0) x[c] = fmaf(sum_o[32 * part + c], keep, x[c]);
-                                    if (!last) sum_o[32 * part + c] = x[c];
-                                }
-                            }
-                        }
-                        if (!last) continue;
                         uint32_t packed[16];
+                        if constexpr (kRuns) {
+                            float x[32];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) packed[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+                            for (int c = 0; c < 32; ++c) {
+                                x[c] = (la > 0.f ? u2f(oa[c]) * fa : 0.f) + (lb > 0.f ? u2f(ob[c]) * fb : 0.f);
+                                if (run > 0) x[c] = fmaf(sum_o[32 * part + c], keep, x[c]);
+                                if (!last) sum_o[32 * part + c] = x[c];
+                            }
+                            if (!last) continue;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) packed[c] = pack_bf16x2(x[2 * c], x[2 * c + 1]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                packed[c] = pack_bf16x2((la > 0.f ? u2f(oa[2 * c]) * fa : 0.f) +
+                                                            (lb > 0.f ? u2f(ob[2 * c]) * fb : 0.f),
+                                                        (la > 0.f ? u2f(oa[2 * c + 1]) * fa : 0.f) +
+                                                            (lb > 0.f ? u2f(ob[2 * c + 1]) * fb : 0.f));
+                        }
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             d4[4 * part + c] = make_uint4(packed[4 * c], packed[4 * c + 1],
